@@ -15,6 +15,10 @@ Typical use::
     qw, s_w = fp8_quantize_weight(w, fmt="e5m2")     # the other FP8 format
     y = fp8_linear_ex(a, qw, s_w, fmt_a="e5m2", fmt_w="e5m2")
     y = fp8_linear_weight_only(a, qw, s_w, fmt_w="e5m2")  # bf16 A, FP8 weights up-converted
+    qw, s_w = fp8_block_quantize_weight(w)           # a scale for each 128 x 128 block
+    y = fp8_block_linear(a, qw, s_w, bias)           # activations: a scale per row and 128 columns
+    ids, weights = fp8_moe_route(logits, k, score="sigmoid", renormalize=True)
+    y = fp8_moe_experts(x, ids, weights, qw13, s13, qw2, s2)  # the chosen experts, block-scaled
 """
 
 from __future__ import annotations
@@ -68,6 +72,16 @@ _SIGNATURES = {
     "fp8_gemm_config": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i64, _sz, _vp, _vp, _vp, _vp, _vp]),
     "fp8_gemm_plan_model": (_int, [_i64, _i64, _i64, _int, _int, _sz, _vp, _vp, _vp, _vp, _vp]),
     "fp8_gemv_plan_model": (_int, [_i64, _i64, _i64, _int, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fp8_block_quantize_weight": (_int, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp]),
+    "fp8_block_quantize_act": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "fp8_block_scaled_mm": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "fp8_block_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "fp8_block_linear": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "fp8_moe_route": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _int, _int, _int, _int, ctypes.c_float, _vp,
+                             _vp, _vp]),
+    "fp8_moe_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "fp8_moe_experts": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64,
+                               _vp, _i64, _vp, _sz, _vp]),
     "fp8_last_device_status": (_int, [_vp]),
     "fp8_selftest_timeout": (_int, [_i64, _vp]),
     "fp8_status_string": (ctypes.c_char_p, [_int]),
@@ -350,6 +364,178 @@ def fp8_linear_noalloc(a, qw, s_w, per_channel: bool = False, bias=None, out=Non
     _check(lib().fp8_linear_noalloc(a.data_ptr(), M, K, a.stride(0), qw.data_ptr(), N, qw.stride(0),
                                     s_w.data_ptr(), int(per_channel), _ptr(bias), y.data_ptr(), y.stride(0),
                                     _stream_ptr(a)), "fp8_linear_noalloc")
+    return y
+
+
+# ---------------------------------------------------------------------------
+# block-scaled linear and mixture of experts
+# ---------------------------------------------------------------------------
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _out_bf16(out, M: int, N: int, like):
+    torch = _torch()
+    if out is None:
+        return torch.empty((M, N), dtype=torch.bfloat16, device=like.device)
+    _check_bf16_2d(out, "out")
+    if out.shape != (M, N) or out.device != like.device:
+        raise ValueError(f"out: expected [{M}, {N}] on {like.device}")
+    return out
+
+
+def _check_dense(t, dtype, shape, like, name: str):
+    """A gap-free tensor of this dtype and shape on the device of `like`."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}")
+
+
+def _check_block_weight(qw, s_w, lead: tuple, N: int, K: int, like, name: str):
+    """Codes [*lead, N, ld] and scales [*lead, blocks of N, blocks of K] as fp8_block_quantize_weight returns them."""
+    torch = _torch()
+    if qw.dim() != len(lead) + 2 or qw.shape[-1] < K or qw.shape[-1] % 16:
+        raise ValueError(f"{name}: expected uint8 codes [..., N, ld] with ld a multiple of 16 and at least {K}")
+    _check_dense(qw, torch.uint8, (*lead, N, qw.shape[-1]), like, name)
+    _check_dense(s_w, torch.float32, (*lead, _blocks(N), _blocks(K)), like, name + " scales")
+
+
+def _check_bias(bias, N: int, like):
+    if bias is not None:
+        _check_dense(bias, _torch().bfloat16, (N,), like, "bias")
+
+
+def _scratch(ws, need: int, like):
+    """The caller's workspace, or a fresh one."""
+    torch = _torch()
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != like.device:
+        raise ValueError(f"ws: expected a contiguous uint8 tensor on {like.device}")
+    return ws
+
+
+def fp8_block_quantize_weight(w):
+    """W bf16 [..., N, K] -> (qW uint8 [..., N, min_ld(K)], s_w fp32 [..., ceil(N/128), ceil(K/128)]):
+    one scale for each 128 x 128 block. Leading dimensions are separate matrices (experts)."""
+    torch = _torch()
+    if w.dtype != torch.bfloat16 or w.dim() < 2 or not w.is_cuda or w.stride(-1) != 1:
+        raise ValueError("w: expected CUDA bf16 matrices [..., N, K] with unit column stride")
+    lead, (N, K) = tuple(w.shape[:-2]), w.shape[-2:]
+    if w.dim() > 3:
+        w = w.reshape(-1, N, K)
+    B = w.shape[0] if w.dim() == 3 else 1
+    qw = torch.empty((*lead, N, min_ld(K)), dtype=torch.uint8, device=w.device)
+    s_w = torch.empty((*lead, _blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
+    _check(lib().fp8_block_quantize_weight(w.data_ptr(), B, N, K, max(w.stride(-2), K, 1),
+                                           w.stride(0) if w.dim() == 3 else 0, qw.data_ptr(), min_ld(K),
+                                           s_w.data_ptr(), _stream_ptr(w)), "fp8_block_quantize_weight")
+    return qw, s_w
+
+
+def fp8_block_quantize_act(a):
+    """A bf16 [M, K] -> (qA uint8 [M, min_ld(K)], s_a fp32 [ceil(K/128), M]): one scale per row and 128 columns."""
+    torch = _torch()
+    _check_bf16_2d(a, "a")
+    M, K = a.shape
+    qa = torch.empty((M, min_ld(K)), dtype=torch.uint8, device=a.device)
+    s_a = torch.empty((_blocks(K), M), dtype=torch.float32, device=a.device)
+    _check(lib().fp8_block_quantize_act(a.data_ptr(), M, K, max(a.stride(0), K, 1), qa.data_ptr(), qa.stride(0),
+                                        s_a.data_ptr(), max(M, 1), _stream_ptr(a)), "fp8_block_quantize_act")
+    return qa, s_a
+
+
+def fp8_block_scaled_mm(qa, K: int, s_a, qw, s_w, bias=None, out=None):
+    """The block-scaled product on already-quantized operands (fp8_block_quantize_act / _weight), bf16 out."""
+    torch = _torch()
+    _check_fp8_2d(qa, K, "qa")
+    M, N = qa.shape[0], qw.shape[-2]
+    if s_a.dtype != torch.float32 or s_a.shape != (_blocks(K), M) or s_a.device != qa.device or (
+            s_a.numel() and s_a.stride(1) != 1):
+        raise ValueError(f"s_a: expected fp32 [{_blocks(K)}, {M}] with unit column stride")
+    _check_block_weight(qw, s_w, (), N, K, qa, "qw")
+    _check_bias(bias, N, qa)
+    y = _out_bf16(out, M, N, qa)
+    _check(lib().fp8_block_scaled_mm(qa.data_ptr(), M, K, qa.stride(0), s_a.data_ptr(),
+                                     max(s_a.stride(0), M, 1) if s_a.shape[0] > 1 else max(M, 1), qw.data_ptr(), N,
+                                     qw.stride(0), s_w.data_ptr(), _ptr(bias), y.data_ptr(), max(y.stride(0), N, 1),
+                                     _stream_ptr(qa)), "fp8_block_scaled_mm")
+    return y
+
+
+def fp8_block_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(lib().fp8_block_workspace_bytes(M, K, N))
+
+
+def fp8_block_linear(a, qw, s_w, bias=None, out=None, ws=None):
+    """Block-scaled W8A8 linear, Y = A W^T (+ bias) in bf16: A is quantized with a scale per row and 128 columns,
+    qw, s_w come from fp8_block_quantize_weight."""
+    _check_bf16_2d(a, "a")
+    M, K = a.shape
+    N = qw.shape[-2]
+    _check_block_weight(qw, s_w, (), N, K, a, "qw")
+    _check_bias(bias, N, a)
+    y = _out_bf16(out, M, N, a)
+    ws = _scratch(ws, lib().fp8_block_workspace_bytes(M, K, N), a)
+    _check(lib().fp8_block_linear(a.data_ptr(), M, K, max(a.stride(0), K, 1), qw.data_ptr(), N, qw.stride(0),
+                                  s_w.data_ptr(), _ptr(bias), y.data_ptr(), max(y.stride(0), N, 1), _ptr(ws),
+                                  0 if ws is None else ws.numel(), _stream_ptr(a)), "fp8_block_linear")
+    return y
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def fp8_moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1,
+                  keep_groups: Optional[int] = None, renormalize: bool = False, factor: float = 1.0):
+    """Logits [T, E] (fp32 or bf16) -> (ids int32 [T, k], weights fp32 [T, k]): the k chosen experts of each
+    token in descending order and their routing weights. score 'softmax' or 'sigmoid'; bias fp32 [E] steers the
+    choice only; only the keep_groups best of `groups` groups of experts take part (default: all)."""
+    torch = _torch()
+    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.dim() != 2 or not logits.is_cuda or (
+            logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: expected a CUDA fp32 or bf16 matrix with unit column stride")
+    if score not in _SCORES:
+        raise ValueError(f"unknown score {score!r} (expected 'softmax' or 'sigmoid')")
+    T, E = logits.shape
+    if bias is not None:
+        _check_dense(bias, torch.float32, (E,), logits, "bias")
+    if k < 1:
+        raise ValueError(f"k: expected at least 1, got {k}")
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _check(lib().fp8_moe_route(logits.data_ptr(), int(logits.dtype == torch.bfloat16), T, E, max(logits.stride(0), E),
+                               _SCORES[score], _ptr(bias), groups, groups if keep_groups is None else keep_groups, k,
+                               int(bool(renormalize)), float(factor), ids.data_ptr(), weights.data_ptr(),
+                               _stream_ptr(logits)), "fp8_moe_route")
+    return ids, weights
+
+
+def fp8_moe_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:
+    return int(lib().fp8_moe_workspace_bytes(T, k, E, H, I))
+
+
+def fp8_moe_experts(x, ids, weights, qw13, s13, qw2, s2, out=None, ws=None):
+    """The routed experts' gated networks, summed by routing weight, bf16 [T, H].
+
+    x bf16 [T, H]; ids int32 and weights fp32 [T, k] (fp8_moe_route; ids outside [0, E) contribute nothing);
+    qw13, s13 from fp8_block_quantize_weight of [E, 2, I, H] (gate, up), qw2, s2 of [E, H, I]."""
+    torch = _torch()
+    _check_bf16_2d(x, "x")
+    T, H = x.shape
+    if ids.dim() != 2 or qw13.dim() != 4 or qw13.shape[1] != 2:
+        raise ValueError("expected ids [T, k] and qw13 [E, 2, I, ld]")
+    k, E, I = ids.shape[1], qw13.shape[0], qw13.shape[2]
+    _check_dense(ids, torch.int32, (T, k), x, "ids")
+    _check_dense(weights, torch.float32, (T, k), x, "weights")
+    _check_block_weight(qw13, s13, (E, 2), I, H, x, "qw13")
+    _check_block_weight(qw2, s2, (E,), H, I, x, "qw2")
+    y = _out_bf16(out, T, H, x)
+    ws = _scratch(ws, lib().fp8_moe_workspace_bytes(T, k, E, H, I), x)
+    _check(lib().fp8_moe_experts(x.data_ptr(), T, H, max(x.stride(0), H, 1), ids.data_ptr(), weights.data_ptr(), k,
+                                 qw13.data_ptr(), qw13.shape[3], s13.data_ptr(), qw2.data_ptr(), qw2.shape[2],
+                                 s2.data_ptr(), E, I, y.data_ptr(), max(y.stride(0), H, 1), _ptr(ws),
+                                 0 if ws is None else ws.numel(), _stream_ptr(x)), "fp8_moe_experts")
     return y
 
 

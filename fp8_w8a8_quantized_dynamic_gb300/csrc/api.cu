@@ -16,18 +16,17 @@
 #include <utility>
 
 #include "fp8w8a8.h"
+#include "api_common.h"
+#include "block_gemm.h"
 #include "device_common.cuh"
 #include "gemm_tcgen05.h"
 #include "gemv.h"
 #include "quantize.cuh"
 
-#define FP8_API extern "C" __attribute__((visibility("default")))
-
 namespace {
 
 using namespace fp8k;
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int kGemvMaxK = gemv::kMaxCluster * gemv::kMaxSlice;  // 32768
 // Tokens up to which the GEMV quantizes A itself (two n8 token tiles). With four, the 32-token
 // activation area leaves the ring too shallow to hold A, which every cluster would fetch twice
@@ -41,39 +40,6 @@ int64_t gemv_self_quant_max_m() {
     return e ? std::max<int64_t>(0, std::min<int64_t>(std::atoi(e), gemv::kMaxTokens)) : int64_t(2 * 8);
   }();
   return v;
-}
-
-// ---------------------------------------------------------------------------
-// device properties (cached per device)
-// ---------------------------------------------------------------------------
-
-struct DevInfo {
-  int checked = 0;
-  int supported = 0;
-  int sms = 0;
-};
-
-std::mutex g_dev_mu;
-DevInfo g_dev[64];
-
-fp8_status current_device(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8_ERR_CUDA;
-  std::lock_guard<std::mutex> lock(g_dev_mu);
-  DevInfo& d = g_dev[dev];
-  if (!d.checked) {
-    int major = 0, minor = 0, n = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return FP8_ERR_CUDA;
-    d.supported = (major == 10 && minor == 3);
-    d.sms = n;
-    d.checked = 1;
-  }
-  if (!d.supported) return FP8_ERR_UNSUPPORTED_DEVICE;
-  *sms = d.sms;
-  return FP8_OK;
 }
 
 // Largest M that runs the decode GEMV: FP8W8A8_GEMV_MAX_M at start-up (default
@@ -117,55 +83,9 @@ bool gemv_slice_only() {
   return v;
 }
 
-int64_t round_up16(int64_t k) { return (k + 15) / 16 * 16; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Passes `e` through; with FP8W8A8_DEBUG set, a failure is also described on stderr.
-cudaError_t report_cuda(cudaError_t e, const char* where) {
-  static const bool debug = std::getenv("FP8W8A8_DEBUG") != nullptr;
-  if (e != cudaSuccess && debug) std::fprintf(stderr, "fp8w8a8: %s: %s\n", where, cudaGetErrorString(e));
-  return e;
-}
-
 // ---------------------------------------------------------------------------
 // launch helpers
 // ---------------------------------------------------------------------------
-
-template <typename... KArgs, typename... Args>
-fp8_status launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool pdl,
-                  dim3 cluster, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (pdl) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  if (cluster.x * cluster.y * cluster.z > 1) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = cluster.x;
-    attr[n].val.clusterDim.y = cluster.y;
-    attr[n].val.clusterDim.z = cluster.z;
-    ++n;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return report_cuda(cudaLaunchKernelEx(&cfg, kernel, args...), "kernel launch") == cudaSuccess ? FP8_OK
-                                                                                       : FP8_ERR_CUDA;
-}
-
-struct BF16Mat {
-  const uint16_t* p;
-  int64_t rows, cols, ld;
-  int contiguous() const { return ld == cols && aligned(p, 16); }
-  int vec() const { return aligned(p, 16) && ld % 8 == 0; }
-};
 
 // CTAs of the amax pass: at most the partial slots of a workspace, and a whole number per SM
 // (6 on a 152-SM GB300) so that no SM carries one more CTA than the others at the end.
@@ -445,38 +365,8 @@ fp8_status launch_gemv(gemv::Params p, int mode, int fmt_a, int fmt_w, const uin
 }
 
 // ---------------------------------------------------------------------------
-// validation
+// the linear
 // ---------------------------------------------------------------------------
-
-fp8_status check_bf16_mat(const void* p, int64_t rows, int64_t cols, int64_t ld) {
-  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return FP8_ERR_INVALID_ARG;
-  if (ld < std::max<int64_t>(cols, 1)) return FP8_ERR_INVALID_ARG;
-  if (rows > 0 && cols > 0 && p == nullptr) return FP8_ERR_INVALID_ARG;
-  if (!aligned(p, 2)) return FP8_ERR_MISALIGNED;
-  return FP8_OK;
-}
-
-fp8_status check_fp8_mat(const void* p, int64_t rows, int64_t cols, int64_t ld) {
-  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return FP8_ERR_INVALID_ARG;
-  if (ld < std::max<int64_t>(round_up16(cols), 16)) return FP8_ERR_INVALID_ARG;
-  if (ld % FP8_LD_ALIGN != 0) return FP8_ERR_MISALIGNED;
-  if (rows > 0 && p == nullptr) return FP8_ERR_INVALID_ARG;
-  if (!aligned(p, 16)) return FP8_ERR_MISALIGNED;
-  return FP8_OK;
-}
-
-fp8_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
-  if (need == 0) return FP8_OK;
-  if (ws == nullptr || ws_bytes < need) return FP8_ERR_WORKSPACE;
-  if (!aligned(ws, 256)) return FP8_ERR_WORKSPACE;
-  return FP8_OK;
-}
-
-#define FP8_TRY(expr)                  \
-  do {                                 \
-    const fp8_status _s = (expr);      \
-    if (_s != FP8_OK) return _s;       \
-  } while (0)
 
 // Decode shapes need no workspace (the GEMV quantizes A itself); the GEMM path holds the
 // partial amax values, s_a and qA [M, round_up(K, 16)]: the least a GEMM-path call accepts.
@@ -486,8 +376,6 @@ size_t linear_ws_bytes(int64_t M, int64_t K, int64_t N) {
   if (M <= 0 || K <= 0 || (use_gemv(M, K, N) && M <= gemv_self_quant_max_m())) return 0;
   return FP8_QUANT_WORKSPACE_BYTES + size_t(M) * size_t(round_up16(K));
 }
-
-size_t round_up_256(size_t b) { return (b + 255) / 256 * 256; }
 
 // What fp8_workspace_bytes reports: the above plus, from the next 256-byte boundary, the
 // split-K fp32 partials of the split a 152-SM GB300 (76 CTA pairs) would use.
@@ -875,7 +763,8 @@ FP8_API fp8_status fp8_gemm_plan_model(int64_t M, int64_t N, int64_t K, int num_
 
 FP8_API fp8_status fp8_last_device_status(fp8_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FP8_ERR_CUDA;
-  const unsigned int e = fp8k::gemm_read_and_clear_error() | gemv::read_and_clear_error();
+  const unsigned int e =
+      fp8k::gemm_read_and_clear_error() | gemv::read_and_clear_error() | fp8k::block::gemm_read_and_clear_error();
   if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
   return (e & kErrTimeout) ? FP8_ERR_TIMEOUT : FP8_OK;
 }

@@ -1,0 +1,367 @@
+// C ABI of the block-scaled FP8 linear and the mixture of experts (declared in
+// include/fp8w8a8.h): argument validation, workspace layout, launches.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "api_common.h"
+#include "block_gemm.h"
+#include "block_quant.cuh"
+#include "device_cache.h"
+#include "moe.cuh"
+
+namespace {
+
+using namespace fp8k;
+using block::blocks_of;
+
+// Largest row count: a row tile may reach kRowTile past the last row with 32-bit coordinates.
+constexpr int64_t kMaxRows = kMaxDim - block::kRowTile;
+
+int elementwise_grid(int64_t items, int per_cta, int sms, int ctas_per_sm) {
+  const int64_t g = (items + per_cta - 1) / per_cta;
+  return int(std::max<int64_t>(1, std::min<int64_t>(g, int64_t(sms) * ctas_per_sm)));
+}
+
+// A -> codes and scales; pos / copies: see the kernel.
+fp8_status launch_quantize_rows(const BF16Mat& a, uint8_t* q, int64_t ldq, float* s, int64_t lds, const int* pos,
+                                int copies, int sms, cudaStream_t st) {
+  const int64_t units = a.rows * blocks_of(a.cols) * 8;
+  const int grid = elementwise_grid(units, block::kQThreads, sms, 8);
+  auto go = [&](auto kernel) {
+    return launch(kernel, dim3(grid), dim3(block::kQThreads), 0, st, true, dim3(1, 1, 1), a.p, a.rows, a.cols, a.ld,
+                  a.vec(), q, ldq, s, lds, pos, copies);
+  };
+  // the loop index passes `units` by up to a grid stride
+  return units < (int64_t(1) << 31) ? go(block::quantize_rows_1x128_kernel<uint32_t>)
+                                    : go(block::quantize_rows_1x128_kernel<uint64_t>);
+}
+
+// Scales of rows: fp32 [K blocks][lds], lds >= rows.
+fp8_status check_row_scales(const float* s, int64_t rows, int64_t K, int64_t lds) {
+  if (lds < std::max<int64_t>(rows, 1)) return FP8_ERR_INVALID_ARG;
+  if (rows > 0 && K > 0 && s == nullptr) return FP8_ERR_INVALID_ARG;
+  return aligned(s, 4) ? FP8_OK : FP8_ERR_MISALIGNED;
+}
+
+struct Carver {
+  size_t at = 0;
+  size_t take(size_t bytes) {
+    const size_t p = at;
+    at = round_up_256(at + bytes);
+    return p;
+  }
+};
+
+// Workspace of fp8_block_linear: codes of A, then its scales.
+struct LinearWs {
+  size_t qa, s_a, total;
+};
+LinearWs linear_ws(int64_t M, int64_t K) {
+  Carver c;
+  LinearWs w;
+  w.qa = c.take(size_t(M) * size_t(round_up16(K)));
+  w.s_a = c.take(size_t(blocks_of(K)) * size_t(M) * 4);
+  w.total = c.at;
+  return w;
+}
+
+fp8_status block_mm(const uint8_t* qa, int64_t M, int64_t K, int64_t ldqa, const float* s_a, int64_t lds_a,
+                    const uint8_t* qw, int64_t N, int64_t ldqw, const float* s_w, const void* bias, void* y,
+                    int64_t ldy, int sms, cudaStream_t st) {
+  block::GemmArgs g = {};
+  g.qa = qa;
+  g.rows = M;
+  g.lda = ldqa;
+  g.s_a = s_a;
+  g.lds_a = lds_a;
+  g.qw = qw;
+  g.mats = 1;
+  g.ldw = ldqw;
+  g.s_w = s_w;
+  g.N = N;
+  g.K = K;
+  g.bias = static_cast<const uint16_t*>(bias);
+  g.y = static_cast<uint16_t*>(y);
+  g.ldy = ldy;
+  return block::gemm_launch(g, block::kOutBf16, sms, st) ? FP8_OK : FP8_ERR_CUDA;
+}
+
+// y[m, :] = bias (or 0): the product over no K.
+__global__ void rows_of_bias_kernel(const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t M, int64_t N,
+                                    int64_t ldy) {
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < M * N; i += int64_t(gridDim.x) * blockDim.x) {
+    const int64_t m = i / N, n = i - m * N;
+    y[m * ldy + n] = bias ? bias[n] : uint16_t(0);
+  }
+}
+
+fp8_status launch_rows_of_bias(const void* bias, void* y, int64_t M, int64_t N, int64_t ldy, int sms,
+                               cudaStream_t st) {
+  return launch(rows_of_bias_kernel, dim3(elementwise_grid(M * N, 256, sms, 8)), dim3(256), 0, st, true,
+                dim3(1, 1, 1), static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), M, N, ldy);
+}
+
+fp8_status check_product(int64_t M, int64_t K, const uint8_t* qw, int64_t N, int64_t ldqw, const float* s_w,
+                         const void* bias, const void* y, int64_t ldy) {
+  FP8_TRY(check_fp8_mat(qw, N, K, ldqw));
+  FP8_TRY(check_bf16_mat(y, M, N, ldy));
+  if (M > kMaxRows) return FP8_ERR_INVALID_ARG;
+  if (N > 0 && K > 0 && s_w == nullptr) return FP8_ERR_INVALID_ARG;
+  if (!aligned(bias, 2) || !aligned(s_w, 4)) return FP8_ERR_MISALIGNED;
+  return FP8_OK;
+}
+
+// Workspace of fp8_moe_experts over P = T * k pairs.
+struct MoeWs {
+  size_t n_tiles, tiles, pos, qx, s_x, qh, s_h, y, total;
+  int64_t pairs, max_tiles, ldx, ldh, ldy;
+};
+MoeWs moe_ws(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  Carver c;
+  MoeWs w;
+  w.pairs = T * k;
+  w.max_tiles = w.pairs / block::kRowTile + std::min(E, w.pairs);
+  w.ldx = round_up16(H);
+  w.ldh = round_up16(I);
+  w.ldy = (H + 3) / 4 * 4;
+  w.n_tiles = c.take(4);
+  w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
+  w.pos = c.take(size_t(w.pairs) * 4);
+  w.qx = c.take(size_t(w.pairs) * size_t(w.ldx));
+  w.s_x = c.take(size_t(w.pairs) * size_t(blocks_of(H)) * 4);
+  w.qh = c.take(size_t(w.pairs) * size_t(w.ldh));
+  w.s_h = c.take(size_t(w.pairs) * size_t(blocks_of(I)) * 4);
+  w.y = c.take(size_t(w.pairs) * size_t(w.ldy) * 4);
+  w.total = c.at;
+  return w;
+}
+
+bool moe_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  return T >= 0 && k >= 1 && k <= moe::kMaxChosen && E >= 1 && E <= moe::kMaxExperts && H >= 0 && H <= kMaxDim &&
+         I >= 1 && I <= kMaxDim / 2 && T <= kMaxRows / k;
+}
+
+PerDeviceCache<const void*, int> g_attr_cache;
+
+fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int* pos, block::RowTile* tiles, int* n_tiles,
+                       cudaStream_t st) {
+  const size_t smem = size_t(moe::kPlanWarps + 1) * E * sizeof(int);
+  int dev = 0, set = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
+  if (!g_attr_cache.get(dev, reinterpret_cast<const void*>(moe::plan_kernel), &set, [&](int* v) {
+        *v = 1;
+        return report_cuda(cudaFuncSetAttribute(moe::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                (moe::kPlanWarps + 1) * moe::kMaxExperts * int(sizeof(int))),
+                           "plan smem attribute") == cudaSuccess;
+      }))
+    return FP8_ERR_CUDA;
+  return launch(moe::plan_kernel, dim3(1), dim3(moe::kPlanThreads), smem, st, true, dim3(1, 1, 1), ids, pairs, E, pos,
+                tiles, n_tiles);
+}
+
+template <typename T>
+fp8_status launch_route(const T* logits, const moe::RouteParams& p, int sms, cudaStream_t st) {
+  auto go = [&](auto kernel) {
+    const int grid = elementwise_grid(p.tokens, moe::kRouteThreads / 32, sms, 8);
+    return launch(kernel, dim3(grid), dim3(moe::kRouteThreads), 0, st, true, dim3(1, 1, 1), logits, p);
+  };
+  if (p.experts <= 32) return go(moe::route_kernel<T, 1>);
+  if (p.experts <= 64) return go(moe::route_kernel<T, 2>);
+  if (p.experts <= 128) return go(moe::route_kernel<T, 4>);
+  if (p.experts <= 256) return go(moe::route_kernel<T, 8>);
+  return go(moe::route_kernel<T, 16>);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// block-scaled linear
+// ---------------------------------------------------------------------------
+
+FP8_API fp8_status fp8_block_quantize_weight(const void* w_bf16, int64_t B, int64_t N, int64_t K, int64_t ldw,
+                                             int64_t mat_stride, uint8_t* qw, int64_t ldq, float* s_w,
+                                             fp8_stream_t stream) {
+  FP8_TRY(check_bf16_mat(w_bf16, N, K, ldw));
+  FP8_TRY(check_fp8_mat(qw, N, K, ldq));
+  if (B < 0 || B > kMaxDim || (B > 1 && mat_stride < 0)) return FP8_ERR_INVALID_ARG;
+  if (!aligned(s_w, 4)) return FP8_ERR_MISALIGNED;
+  if (B == 0 || N == 0 || K == 0) return FP8_OK;
+  if (s_w == nullptr) return FP8_ERR_INVALID_ARG;
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  const BF16Mat W{static_cast<const uint16_t*>(w_bf16), N, K, ldw};
+  const int vec = W.vec() && (B == 1 || mat_stride % 8 == 0);
+  const int64_t blocks = B * blocks_of(N) * blocks_of(K);
+  // no early programmatic trigger: a following product may read qW before its own wait
+  return launch(block::quantize_128x128_kernel, dim3(elementwise_grid(blocks, 1, sms, 64)), dim3(block::kQThreads), 0,
+                reinterpret_cast<cudaStream_t>(stream), false, dim3(1, 1, 1), W.p, B, N, K, ldw, mat_stride, vec, qw,
+                ldq, s_w);
+}
+
+FP8_API fp8_status fp8_block_quantize_act(const void* a_bf16, int64_t M, int64_t K, int64_t lda, uint8_t* qa,
+                                          int64_t ldq, float* s_a, int64_t lds, fp8_stream_t stream) {
+  FP8_TRY(check_bf16_mat(a_bf16, M, K, lda));
+  FP8_TRY(check_fp8_mat(qa, M, K, ldq));
+  FP8_TRY(check_row_scales(s_a, M, K, lds));
+  if (M == 0 || K == 0) return FP8_OK;
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  const BF16Mat A{static_cast<const uint16_t*>(a_bf16), M, K, lda};
+  return launch_quantize_rows(A, qa, ldq, s_a, lds, nullptr, 0, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+FP8_API fp8_status fp8_block_scaled_mm(const uint8_t* qa, int64_t M, int64_t K, int64_t ldqa, const float* s_a,
+                                       int64_t lds, const uint8_t* qw, int64_t N, int64_t ldqw, const float* s_w,
+                                       const void* bias_bf16, void* y_bf16, int64_t ldy, fp8_stream_t stream) {
+  FP8_TRY(check_fp8_mat(qa, M, K, ldqa));
+  FP8_TRY(check_row_scales(s_a, M, K, lds));
+  FP8_TRY(check_product(M, K, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy));
+  if (M == 0 || N == 0) return FP8_OK;
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (K == 0) return launch_rows_of_bias(bias_bf16, y_bf16, M, N, ldy, sms, st);
+  return block_mm(qa, M, K, ldqa, s_a, lds, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy, sms, st);
+}
+
+FP8_API size_t fp8_block_workspace_bytes(int64_t M, int64_t K, int64_t N) {
+  if (M <= 0 || K <= 0 || N <= 0) return 0;
+  return linear_ws(M, K).total;
+}
+
+FP8_API fp8_status fp8_block_linear(const void* a_bf16, int64_t M, int64_t K, int64_t lda, const uint8_t* qw,
+                                    int64_t N, int64_t ldqw, const float* s_w, const void* bias_bf16, void* y_bf16,
+                                    int64_t ldy, void* ws, size_t ws_bytes, fp8_stream_t stream) {
+  FP8_TRY(check_bf16_mat(a_bf16, M, K, lda));
+  FP8_TRY(check_product(M, K, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy));
+  if (M == 0 || N == 0) return FP8_OK;
+  FP8_TRY(check_ws(ws, ws_bytes, fp8_block_workspace_bytes(M, K, N)));
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (K == 0) return launch_rows_of_bias(bias_bf16, y_bf16, M, N, ldy, sms, st);
+  const BF16Mat A{static_cast<const uint16_t*>(a_bf16), M, K, lda};
+  const LinearWs w = linear_ws(M, K);
+  uint8_t* qa = static_cast<uint8_t*>(ws) + w.qa;
+  float* s_a = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.s_a);
+  FP8_TRY(launch_quantize_rows(A, qa, round_up16(K), s_a, M, nullptr, 0, sms, st));
+  return block_mm(qa, M, K, round_up16(K), s_a, M, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy, sms, st);
+}
+
+// ---------------------------------------------------------------------------
+// mixture of experts
+// ---------------------------------------------------------------------------
+
+FP8_API fp8_status fp8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int64_t ld, int sigmoid,
+                                 const float* bias, int groups, int keep_groups, int k, int renormalize, float factor,
+                                 int32_t* ids, float* weights, fp8_stream_t stream) {
+  if (T < 0 || T > kMaxDim || E < 1 || E > moe::kMaxExperts || ld < E) return FP8_ERR_INVALID_ARG;
+  if ((logits_bf16 != 0 && logits_bf16 != 1) || (sigmoid != 0 && sigmoid != 1) ||
+      (renormalize != 0 && renormalize != 1))
+    return FP8_ERR_INVALID_ARG;
+  if (groups < 1 || groups > moe::kMaxGroups || E % groups != 0 || keep_groups < 1 || keep_groups > groups)
+    return FP8_ERR_INVALID_ARG;
+  if (k < 1 || k > moe::kMaxChosen || k > keep_groups * (E / groups)) return FP8_ERR_INVALID_ARG;
+  if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return FP8_ERR_MISALIGNED;
+  if (T == 0) return FP8_OK;
+  if (logits == nullptr || ids == nullptr || weights == nullptr) return FP8_ERR_INVALID_ARG;
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  moe::RouteParams p = {};
+  p.tokens = T;
+  p.ld = ld;
+  p.experts = int(E);
+  p.k = k;
+  p.groups = groups;
+  p.keep = keep_groups;
+  p.sigmoid = sigmoid;
+  p.renorm = renormalize;
+  p.factor = factor;
+  p.bias = bias;
+  p.ids = ids;
+  p.weights = weights;
+  return logits_bf16 ? launch_route(static_cast<const uint16_t*>(logits), p, sms, st)
+                     : launch_route(static_cast<const float*>(logits), p, sms, st);
+}
+
+FP8_API size_t fp8_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  if (!moe_sizes_ok(T, k, E, H, I) || T == 0 || H == 0) return 0;
+  return moe_ws(T, k, E, H, I).total;
+}
+
+FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
+                                   const float* weights, int64_t k, const uint8_t* qw13, int64_t ldq13,
+                                   const float* s13, const uint8_t* qw2, int64_t ldq2, const float* s2, int64_t E,
+                                   int64_t I, void* y_bf16, int64_t ldy, void* ws, size_t ws_bytes,
+                                   fp8_stream_t stream) {
+  if (!moe_sizes_ok(T, k, E, H, I)) return FP8_ERR_INVALID_ARG;
+  FP8_TRY(check_bf16_mat(x_bf16, T, H, ldx));
+  FP8_TRY(check_bf16_mat(y_bf16, T, H, ldy));
+  FP8_TRY(check_fp8_mat(qw13, I, H, ldq13));
+  FP8_TRY(check_fp8_mat(qw2, H, I, ldq2));
+  if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(s13, 4) || !aligned(s2, 4)) return FP8_ERR_MISALIGNED;
+  if (T == 0 || H == 0) return FP8_OK;
+  if (ids == nullptr || weights == nullptr || s13 == nullptr || s2 == nullptr) return FP8_ERR_INVALID_ARG;
+  const MoeWs w = moe_ws(T, k, E, H, I);
+  FP8_TRY(check_ws(ws, ws_bytes, w.total));
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  int* n_tiles = reinterpret_cast<int*>(b + w.n_tiles);
+  block::RowTile* tiles = reinterpret_cast<block::RowTile*>(b + w.tiles);
+  int* pos = reinterpret_cast<int*>(b + w.pos);
+  float* s_x = reinterpret_cast<float*>(b + w.s_x);
+  float* s_h = reinterpret_cast<float*>(b + w.s_h);
+  float* y32 = reinterpret_cast<float*>(b + w.y);
+
+  // sort the pairs by expert; quantize each token once into its rows; gate and up products with
+  // SwiGLU and the quantization of h in their epilogue; the product back; the weighted sum
+  FP8_TRY(launch_plan(ids, w.pairs, int(E), pos, tiles, n_tiles, st));
+  const BF16Mat X{static_cast<const uint16_t*>(x_bf16), T, H, ldx};
+  FP8_TRY(launch_quantize_rows(X, b + w.qx, w.ldx, s_x, w.pairs, pos, int(k), sms, st));
+  block::GemmArgs g = {};
+  g.rows = w.pairs;
+  g.tiles = tiles;
+  g.n_tiles = n_tiles;
+  g.max_tiles = w.max_tiles;
+  g.qa = b + w.qx;
+  g.lda = w.ldx;
+  g.s_a = s_x;
+  g.lds_a = w.pairs;
+  g.qw = qw13;
+  g.mats = 2 * E;
+  g.ldw = ldq13;
+  g.s_w = s13;
+  g.N = I;
+  g.K = H;
+  g.qh = b + w.qh;
+  g.ldh = w.ldh;
+  g.s_h = s_h;
+  g.lds_h = w.pairs;
+  if (!block::gemm_launch(g, block::kOutSwiglu, sms, st)) return FP8_ERR_CUDA;
+  g.qa = b + w.qh;
+  g.lda = w.ldh;
+  g.s_a = s_h;
+  g.qw = qw2;
+  g.mats = E;
+  g.ldw = ldq2;
+  g.s_w = s2;
+  g.N = H;
+  g.K = I;
+  g.y32 = y32;
+  g.ldy32 = w.ldy;
+  if (!block::gemm_launch(g, block::kOutF32, sms, st)) return FP8_ERR_CUDA;
+  const int vec = aligned(y_bf16, 8) && ldy % 4 == 0;
+  return launch(moe::weighted_sum_kernel, dim3(elementwise_grid(T * ((H + 3) / 4), moe::kSumThreads, sms, 8)),
+                dim3(moe::kSumThreads), 0, st, true, dim3(1, 1, 1), static_cast<const float*>(y32), w.ldy,
+                static_cast<const int*>(pos), weights, int(k), T, H, static_cast<uint16_t*>(y_bf16), ldy, vec);
+}

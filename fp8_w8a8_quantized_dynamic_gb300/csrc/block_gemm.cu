@@ -1,0 +1,484 @@
+// Block-scaled FP8 GEMM for sm_103a on the 5th-generation tensor cores.
+//
+//   Y[m, n] = sum_b s_a[b, m] * s_w[n / 128, b] * sum_{k in block b} qA[m, k] qW[n, k]
+//
+// over blocks b of 128 values of K. The scale changes every 128 values of K, so the tensor core
+// sums one block at a time (four tcgen05.mma of K = 32 into a fresh tensor-memory accumulator)
+// and the sum over blocks is kept in registers: each thread owns one row of the tile and adds
+// s_a * s_w times the block's partial to its fp32 accumulators, one fma an element. Both sums
+// are fp32.
+//
+// The rows are either those of one matrix, or (grouped) the rows of many experts sorted by
+// expert, with one weight matrix an expert and a table of row tiles in device memory.
+//
+// Structure (persistent, one CTA per SM, output tiles of 128 x BN):
+//   warp 0      TMA producer: activation tile [128 x 128 B] and weight tile [BN x 128 B] of a K
+//               block into a ring of 128B-swizzled shared memory stages.
+//   warp 1      tensor-memory allocator and MMA issuer; the block partials rotate through
+//               512 / BN tensor-memory buffers.
+//   warps 2..9  promotion: two groups of four warps, each with half of the columns; a thread
+//               reads its row of the partial (tcgen05.ld) and adds it, scaled, in registers.
+//               After the last K block the same threads write the tile out.
+// Ragged sizes need no padding: TMA fills out-of-range rows and columns with zeros and the
+// stores are predicated.
+//
+// Every wait is bounded; on expiry the kernel records an error, all roles run to the end of
+// their loops without waiting or storing, copies and MMAs in flight are drained, and the tensor
+// memory is freed.
+
+#include "block_gemm.h"
+
+#include <algorithm>
+
+#include "api_common.h"
+#include "device_cache.h"
+#include "device_common.cuh"
+#include "gemm_tcgen05.h"
+#include "tcgen05.cuh"
+
+namespace fp8k {
+namespace block {
+
+__device__ unsigned int g_block_gemm_error;
+
+constexpr int BM = kRowTile;
+constexpr int BK = kBlock;
+constexpr int kThreads = 320;
+constexpr int kPromoWarps = 8;
+constexpr uint32_t kABytes = BM * BK;
+constexpr uint32_t kRingBytes = 192 * 1024;
+constexpr int kMaxStages = 8;
+constexpr int kMaxBufs = 4;
+
+template <int BN>
+struct Tile {
+  static constexpr uint32_t stage_bytes = kABytes + BN * BK;
+  static constexpr int stages = int(kRingBytes / stage_bytes);  // 4, 6, 8 for BN = 256, 128, 64
+  static constexpr int bufs = 512 / BN < kMaxBufs ? 512 / BN : kMaxBufs;
+  static constexpr int cols = bufs * BN;  // tensor-memory columns (a power of two)
+  static_assert(stages <= kMaxStages, "ring");
+};
+
+struct SharedCtl {
+  uint64_t full[kMaxStages];
+  uint64_t empty[kMaxStages];
+  uint64_t tfull[kMaxBufs];
+  uint64_t tempty[kMaxBufs];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t hmax[2][2][BM];  // SwiGLU: row maxima of the two column halves, by tile parity
+};
+constexpr size_t kSmemBytes = 1024 + kRingBytes + sizeof(SharedCtl);
+static_assert(kSmemBytes <= 232448, "ring and control block must fit the 227 KB per-block limit");
+static_assert(2 * kSmemBytes > 233472, "two GEMM CTAs must never share an SM (tensor memory)");
+
+struct Params {
+  int rows, N, kb;
+  const float* s_a;
+  int64_t lds_a;
+  const float* s_w;
+  int nb;  // scale rows of one weight matrix
+  const RowTile* tiles;
+  const int* n_row_tiles;
+  int m_tiles, n_tiles, group_n;
+  const uint16_t* bias;
+  uint16_t* y;
+  int64_t ldy;
+  int vec;  // rows of the output are 16-byte aligned
+  float* y32;
+  int64_t ldy32;
+  uint8_t* qh;
+  int64_t ldh;
+  float* s_h;
+  int64_t lds_h;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy) : "memory");
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ float lo_of(uint64_t p) { return __uint_as_float(uint32_t(p)); }
+__device__ __forceinline__ float hi_of(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
+
+// silu(g) * u in fp32; exp and the reciprocal by the hardware approximations (a few 2^-23), far
+// below the 2^-4 spacing of the codes h is quantized to.
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+// e4m3 codes of four fp32 values divided by the scale of k (any scale: the division when the
+// exact-quotient form does not cover it).
+__device__ __forceinline__ uint32_t codes4(uint64_t p01, uint64_t p23, const ExactScale& k, float s) {
+  if (k.fast) {
+    const uint64_t a = fma_f32x2(p01, k.r2, mul_f32x2(p01, k.r_lo2));
+    const uint64_t b = fma_f32x2(p23, k.r2, mul_f32x2(p23, k.r_lo2));
+    return cvt_fp8x4<kFmtE4M3>(fma_f32x2(fma_f32x2(k.neg_s2, a, p01), k.r2, a),
+                               fma_f32x2(fma_f32x2(k.neg_s2, b, p23), k.r2, b));
+  }
+  return quant2_divide<kFmtE4M3>(lo_of(p01), hi_of(p01), s) | (quant2_divide<kFmtE4M3>(lo_of(p23), hi_of(p23), s) << 16);
+}
+
+template <int BN, int kOut>
+__global__ void __launch_bounds__(kThreads, 1)
+block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                  const __grid_constant__ Params p) {
+  constexpr int kStages = Tile<BN>::stages;
+  constexpr int kBufs = Tile<BN>::bufs;
+  constexpr int kHalf = BN / 2;                                    // columns of one promotion group
+  constexpr int kTileN = kOut == kOutSwiglu ? BN / 2 : BN;         // output columns of a tile
+  static_assert(kOut != kOutSwiglu || BN == 256, "a SwiGLU tile is one 128-wide block of h");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  SharedCtl* ctl = reinterpret_cast<SharedCtl*>(smem + kRingBytes);
+  const uint32_t smem_base = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &ctl->abort_flag;
+
+  if (threadIdx.x == 0) {
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&tmap_b)) : "memory");
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&ctl->full[s]), 1);
+      mbar_init(smem_u32(&ctl->empty[s]), 1);
+    }
+    for (int b = 0; b < kBufs; ++b) {
+      mbar_init(smem_u32(&ctl->tfull[b]), 1);
+      mbar_init(smem_u32(&ctl->tempty[b]), kPromoWarps);
+    }
+    mbar_init(smem_u32(&ctl->drain), 1);
+    ctl->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(&ctl->tmem_base)), "n"(Tile<BN>::cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+
+  pdl_trigger();
+  pdl_wait();  // qA, s_a and the tile table come from the preceding kernels
+
+  const bool grouped = p.tiles != nullptr;
+  const int m_tiles = grouped ? *p.n_row_tiles : p.m_tiles;
+  const int units = m_tiles * p.n_tiles;
+  // unit -> expert, first row, end of the expert's rows, column tile. Within a group of column
+  // tiles the column runs fastest, so a group's weights stay in L2 while the row tiles pass.
+  auto decode = [&](int u, int& expert, int& row0, int& row_end, int& n_idx) {
+    const int per_group = p.group_n * m_tiles;
+    const int g = u / per_group;
+    const int r = u - g * per_group;
+    const int gn = min(p.group_n, p.n_tiles - g * p.group_n);
+    const int m_idx = r / gn;
+    n_idx = g * p.group_n + (r - m_idx * gn);
+    if (grouped) {
+      const int4 t = *reinterpret_cast<const int4*>(p.tiles + m_idx);
+      expert = t.x, row0 = t.y, row_end = t.z;
+    } else {
+      expert = 0, row0 = m_idx * BM, row_end = p.rows;
+    }
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer ----------------
+      const uint64_t pol = l2_policy(kHintNormal);
+      uint32_t it = 0;
+      for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        int expert, row0, row_end, n_idx;
+        decode(u, expert, row0, row_end, n_idx);
+        const int n0 = n_idx * kTileN;
+        bool ok = true;
+        for (int kb = 0; kb < p.kb; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), ((it / kStages) & 1u) ^ 1u, abort_flag,
+                                 &g_block_gemm_error)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(&ctl->full[s]);
+          const uint32_t dst = smem_base + s * Tile<BN>::stage_bytes;
+          mbar_arrive_expect_tx(fb, Tile<BN>::stage_bytes);
+          tma_load_2d(dst, &tmap_a, fb, kb * BK, row0, pol);
+          if (kOut == kOutSwiglu) {
+            // 64 columns of gate, then the same 64 of up, twice: each promotion group holds both
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              tma_load_3d(dst + kABytes + h * (64 * BK), &tmap_b, fb, kb * BK, n0 + (h >> 1) * 64, 2 * expert + (h & 1),
+                          pol);
+          } else {
+            tma_load_3d(dst + kABytes, &tmap_b, fb, kb * BK, n0, expert, pol);
+          }
+        }
+        if (!ok) break;
+      }
+      // the last fill of every stage must land before the CTA's memory is released
+      for (uint32_t j = it > uint32_t(kStages) ? it - kStages : 0u; j < it; ++j)
+        mbar_wait_bounded(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1u, nullptr, &g_block_gemm_error);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------- MMA issuer ----------------
+      // D fp32, A and B e4m3, both K-major, N = BN, M = 128
+      constexpr uint32_t idesc = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        for (int kb = 0; kb < p.kb; ++kb, ++it) {
+          const int b = it % kBufs, s = it % kStages;
+          if (!mbar_wait_bounded(smem_u32(&ctl->tempty[b]), ((it / kBufs) & 1u) ^ 1u, abort_flag,
+                                 &g_block_gemm_error) ||
+              !mbar_wait_bounded(smem_u32(&ctl->full[s]), (it / kStages) & 1u, abort_flag, &g_block_gemm_error)) {
+            ok = false;
+            break;
+          }
+          tmem_fence_after();
+          const uint64_t adesc = make_sdesc(smem_base + s * Tile<BN>::stage_bytes);
+          const uint64_t bdesc = make_sdesc(smem_base + s * Tile<BN>::stage_bytes + kABytes);
+          const uint32_t d = tmem_base + b * BN;
+#pragma unroll
+          for (int kk = 0; kk < BK / 32; ++kk)
+            mma_f8(d, adesc + uint64_t(kk * 32 >> 4), bdesc + uint64_t(kk * 32 >> 4), idesc, kk != 0);
+          mma_commit<false>(smem_u32(&ctl->empty[s]));
+          mma_commit<false>(smem_u32(&ctl->tfull[b]));
+        }
+      }
+      mma_commit<false>(smem_u32(&ctl->drain));  // all MMAs done before the tensor memory is released
+      mbar_wait_bounded(smem_u32(&ctl->drain), 0, nullptr, &g_block_gemm_error);
+    }
+  } else {
+    // ---------------- promotion and epilogue: warps 2..9 ----------------
+    const int group = (warp - 2) >> 2;   // column half
+    const int quarter = warp & 3;        // tensor-memory lanes this warp may access
+    const int row_in_tile = quarter * 32 + lane;
+    const uint32_t tbase = tmem_base + (uint32_t(quarter * 32) << 16) + group * kHalf;
+    uint32_t it = 0, tile_no = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++tile_no) {
+      int expert, row0, row_end, n_idx;
+      decode(u, expert, row0, row_end, n_idx);
+      const int n0 = n_idx * kTileN;
+      const int row = row0 + row_in_tile;
+      const bool live = row < row_end;
+      const float* sa_ptr = p.s_a + (live ? row : row0);
+      // scale rows: one for all columns of this group, or (SwiGLU) gate and up
+      const float* sw0;
+      const float* sw1 = nullptr;
+      if (kOut == kOutSwiglu) {
+        sw0 = p.s_w + (int64_t(2 * expert) * p.nb + n0 / kBlock) * p.kb;
+        sw1 = sw0 + int64_t(p.nb) * p.kb;
+      } else {
+        sw0 = p.s_w + (int64_t(expert) * p.nb + min((n0 + group * kHalf) / kBlock, p.nb - 1)) * p.kb;
+      }
+      uint64_t acc[kHalf / 2];
+#pragma unroll
+      for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
+      float sa_n = sa_ptr[0], s0_n = sw0[0], s1_n = kOut == kOutSwiglu ? sw1[0] : 0.0f;
+      for (int kb = 0; kb < p.kb; ++kb, ++it) {
+        const float sc0 = sa_n * s0_n, sc1 = sa_n * s1_n;
+        if (kb + 1 < p.kb) {
+          sa_n = sa_ptr[int64_t(kb + 1) * p.lds_a];
+          s0_n = sw0[kb + 1];
+          if (kOut == kOutSwiglu) s1_n = sw1[kb + 1];
+        }
+        const int b = it % kBufs;
+        mbar_wait_bounded(smem_u32(&ctl->tfull[b]), (it / kBufs) & 1u, abort_flag, &g_block_gemm_error);
+        __syncwarp();
+        tmem_fence_after();
+#pragma unroll
+        for (int c = 0; c < kHalf / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tbase + b * BN + c * 32, r);
+          const float sc = kOut == kOutSwiglu && c >= 2 ? sc1 : sc0;
+          const uint64_t s2 = pack_f32x2(sc, sc);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            acc[c * 16 + j] = fma_f32x2(pack_f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2,
+                                        acc[c * 16 + j]);
+        }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[b]));
+      }
+      const bool store = live && *abort_flag == 0;
+      if constexpr (kOut == kOutSwiglu) {
+        // columns [64 group, 64 group + 64) of the tile's 128-wide block of h
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float h0 = swiglu(lo_of(acc[j]), lo_of(acc[32 + j])), h1 = swiglu(hi_of(acc[j]), hi_of(acc[32 + j]));
+          m = max(m, max(__float_as_uint(fabsf(h0)), __float_as_uint(fabsf(h1))));  // keeps a NaN
+          acc[j] = pack_f32x2(h0, h1);
+        }
+        ctl->hmax[tile_no & 1][group][row_in_tile] = m;
+        // the two warps that hold the halves of the same 32 rows meet; two tiles' maxima alternate,
+        // so one meeting a tile is enough
+        asm volatile("bar.sync %0, 64;" :: "r"(1 + quarter) : "memory");
+        m = max(m, ctl->hmax[tile_no & 1][group ^ 1][row_in_tile]);
+        const float s = scale_from_amax<kFmtE4M3>(__uint_as_float(m));
+        const ExactScale k = make_exact_scale(s);
+        if (store) {
+          uint8_t* dst = p.qh + int64_t(row) * p.ldh + n0 + group * 64;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            if (n0 + group * 64 + v * 16 < p.ldh) {  // columns past N hold zeros (zero weight rows)
+              uint4 o;
+              o.x = codes4(acc[v * 8], acc[v * 8 + 1], k, s);
+              o.y = codes4(acc[v * 8 + 2], acc[v * 8 + 3], k, s);
+              o.z = codes4(acc[v * 8 + 4], acc[v * 8 + 5], k, s);
+              o.w = codes4(acc[v * 8 + 6], acc[v * 8 + 7], k, s);
+              *reinterpret_cast<uint4*>(dst + v * 16) = o;
+            }
+          }
+          if (group == 0) p.s_h[int64_t(n_idx) * p.lds_h + row] = s;
+        }
+      } else if constexpr (kOut == kOutF32) {
+        if (store) {
+          float* dst = p.y32 + int64_t(row) * p.ldy32 + n0 + group * kHalf;
+#pragma unroll
+          for (int v = 0; v < kHalf / 4; ++v) {
+            if (n0 + group * kHalf + v * 4 < p.ldy32)  // ldy32: N rounded up to 4
+              *reinterpret_cast<float4*>(dst + v * 4) =
+                  make_float4(lo_of(acc[2 * v]), hi_of(acc[2 * v]), lo_of(acc[2 * v + 1]), hi_of(acc[2 * v + 1]));
+          }
+        }
+      } else {
+        const int c0 = n0 + group * kHalf;
+        uint16_t* dst = p.y + int64_t(row) * p.ldy + c0;
+        if (store) {
+#pragma unroll
+          for (int v = 0; v < kHalf / 8; ++v) {
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[2 * j] = lo_of(acc[4 * v + j]), o[2 * j + 1] = hi_of(acc[4 * v + j]);
+            if (p.bias) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (c0 + v * 8 + j < p.N) o[j] += bf16_bits_to_float(p.bias[c0 + v * 8 + j]);
+            }
+            if (p.vec && c0 + v * 8 + 8 <= p.N) {
+              *reinterpret_cast<uint4*>(dst + v * 8) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                                                                  pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (c0 + v * 8 + j < p.N) dst[v * 8 + j] = __bfloat16_as_ushort(__float2bfloat16_rn(o[j]));
+            }
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem_base), "n"(Tile<BN>::cols)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+namespace {
+
+PerDeviceCache<const void*, int> g_attr_cache;
+
+template <int BN, int kOut>
+bool launch_tile(const GemmArgs& a, int num_sms, cudaStream_t st) {
+  auto kfn = block_gemm_kernel<BN, kOut>;
+  int dev = 0, set = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (!g_attr_cache.get(dev, reinterpret_cast<const void*>(kfn), &set, [&](int* v) {
+        *v = 1;
+        return report_cuda(cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes)),
+                           "block gemm smem attribute") == cudaSuccess;
+      }))
+    return false;
+  Params p = {};
+  p.rows = int(a.rows);
+  p.N = int(a.N);
+  p.kb = int(blocks_of(a.K));
+  p.s_a = a.s_a;
+  p.lds_a = a.lds_a;
+  p.s_w = a.s_w;
+  p.nb = int(blocks_of(a.N));
+  p.tiles = a.tiles;
+  p.n_row_tiles = a.n_tiles;
+  constexpr int kTileN = kOut == kOutSwiglu ? BN / 2 : BN;
+  p.m_tiles = int((a.rows + BM - 1) / BM);
+  p.n_tiles = int((a.N + kTileN - 1) / kTileN);
+  // Weights of a raster group: about 28 MB, which L2 holds beside the activations that stream
+  // past. Grouped: the row tiles of an expert follow one another, so all of its columns.
+  const int64_t tile_bytes = int64_t(BN) * a.ldw;
+  p.group_n = a.tiles ? p.n_tiles : int(std::min<int64_t>(p.n_tiles, std::max<int64_t>(1, (28 << 20) / tile_bytes)));
+  p.bias = a.bias;
+  p.y = a.y;
+  p.ldy = a.ldy;
+  p.vec = aligned(a.y, 16) && a.ldy % 8 == 0;
+  p.y32 = a.y32;
+  p.ldy32 = a.ldy32;
+  p.qh = a.qh;
+  p.ldh = a.ldh;
+  p.s_h = a.s_h;
+  p.lds_h = a.lds_h;
+  const int64_t units = (a.tiles ? a.max_tiles : int64_t(p.m_tiles)) * p.n_tiles;
+  if (units > kMaxDim) return false;
+  CUtensorMap ma, mb;
+  if (!make_fp8_tensor_map(&ma, a.qa, a.rows, a.K, a.lda, BM) ||
+      !make_fp8_tensor_map_3d(&mb, a.qw, a.mats, a.N, a.K, a.ldw, kOut == kOutSwiglu ? 64 : BN))
+    return false;
+  const int grid = int(std::min<int64_t>(units, num_sms));
+  return launch(kfn, dim3(grid), dim3(kThreads), kSmemBytes, st, true, dim3(1, 1, 1), ma, mb, p) == FP8_OK;
+}
+
+template <int kOut>
+bool launch_any(const GemmArgs& a, int num_sms, cudaStream_t st) {
+  // the widest tile that still gives every SM one
+  const int64_t m_tiles = a.tiles ? a.max_tiles : (a.rows + BM - 1) / BM;
+  if (m_tiles * ((a.N + 255) / 256) >= num_sms) return launch_tile<256, kOut>(a, num_sms, st);
+  if (m_tiles * ((a.N + 127) / 128) >= num_sms) return launch_tile<128, kOut>(a, num_sms, st);
+  return launch_tile<64, kOut>(a, num_sms, st);
+}
+
+}  // namespace
+
+bool gemm_launch(const GemmArgs& a, Out out, int num_sms, cudaStream_t stream) {
+  switch (out) {
+    case kOutBf16: return launch_any<kOutBf16>(a, num_sms, stream);
+    case kOutSwiglu: return launch_tile<256, kOutSwiglu>(a, num_sms, stream);
+    case kOutF32: return launch_any<kOutF32>(a, num_sms, stream);
+  }
+  return false;
+}
+
+unsigned int gemm_read_and_clear_error() {
+  unsigned int v = 0;
+  const unsigned int zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_block_gemm_error, sizeof(v)) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_block_gemm_error, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace block
+}  // namespace fp8k

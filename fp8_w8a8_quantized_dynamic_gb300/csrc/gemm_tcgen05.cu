@@ -66,6 +66,7 @@
 #include "device_cache.h"
 #include "device_common.cuh"
 #include "gemm_tcgen05.h"
+#include "tcgen05.cuh"
 
 namespace fp8k {
 namespace gemm {
@@ -129,62 +130,9 @@ constexpr uint32_t make_idesc(int fmt_a, int fmt_w) {
 // kind::f16 with bf16 A and B: the format fields hold BF16 = 1.
 constexpr uint32_t kIdescBf16 = kIdescBase | (1u << 7) | (1u << 10);
 
-// The same descriptor for an MMA of n columns (a multiple of 16, at most BN).
-__host__ __device__ constexpr uint32_t idesc_with_n(uint32_t idesc, int n) {
-  return (idesc & ~(0x3Fu << 17)) | (uint32_t(n >> 3) << 17);
-}
-
 // The two-SM MMA covers both CTAs' rows: M = 256 in the descriptor.
 __host__ __device__ constexpr uint32_t idesc_two_sm(uint32_t idesc) {
   return (idesc & ~(0x1Fu << 24)) | (uint32_t((2 * BM) >> 4) << 24);
-}
-
-// Shared-memory matrix descriptor for a K-major operand tile written by TMA with 128-byte
-// swizzle: rows of 128 bytes, 8-row swizzle atoms of 1024 bytes (stride byte offset), start
-// address >> 4 in bits 0-13, descriptor version 1 at bit 46, swizzle mode 2 (128B) at bits 61-63.
-// The leading byte offset is unused for swizzled K-major layouts (set to 1).
-__device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= uint64_t((saddr & 0x3FFFFu) >> 4);
-  d |= uint64_t(1) << 16;
-  d |= uint64_t(1024 >> 4) << 32;
-  d |= uint64_t(1) << 46;
-  d |= uint64_t(2) << 61;
-  return d;
-}
-
-// L2 eviction priorities for the TMA loads and the output stores (createpolicy): the operand
-// the raster keeps hot in L2 is loaded evict_last, the one streamed once evict_first.
-enum : int { kHintNormal = 0, kHintFirst = 1, kHintLast = 2 };
-
-__device__ __forceinline__ uint64_t l2_policy(int hint) {
-  uint64_t p;
-  if (hint == kHintLast)
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-  else if (hint == kHintFirst)
-    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-  else
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                            uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5;"
-      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy) : "memory");
-}
-
-// Two-SM form: the copy lands in this CTA's shared memory and completes its bytes on an
-// mbarrier that may be the peer's (here always the leader's).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int x,
-                                                 int y, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4}], [%2], %5;"
-      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y), "l"(policy)
-      : "memory");
 }
 
 template <bool kBf16, bool kTwo>
@@ -212,66 +160,6 @@ __device__ __forceinline__ void mma_issue(uint32_t d_tmem, uint64_t adesc, uint6
         :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
 
-// Arrives once on `bar` when every MMA this thread issued before has completed; in two-SM
-// mode it arrives on the barrier at that offset in both CTAs of the pair.
-template <bool kTwo>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  if constexpr (kTwo)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 :: "r"(bar), "h"(uint16_t(0x3)) : "memory");
-  else
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-// A shared-memory address of this CTA, as seen in CTA `rank` of the cluster (shared::cluster).
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t a, uint32_t rank) {
-  uint32_t d;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
-  return d;
-}
-
-__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(cluster_addr), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_bar) : "memory");
-}
-
-// Accounts for `bytes` that will never arrive on this CTA's barrier (abort path only).
-__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
-}
-
-// Every thread of both CTAs: barrier inits visible before the first remote signal, and no CTA
-// leaves while its peer may still write into its shared memory or arrive on its barriers.
-__device__ __forceinline__ void pair_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
 // Named barrier over the 128 epilogue threads that also ORs a flag across them, so every
 // epilogue warp takes the same exit decision.
 __device__ __forceinline__ bool epi_bar_any(bool v) {
@@ -281,16 +169,6 @@ __device__ __forceinline__ bool epi_bar_any(bool v) {
       "bar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r) : "r"(uint32_t(v)), "n"(kEpiThreads) : "memory");
   return r != 0;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  return uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(lo))) |
-         (uint32_t(__bfloat16_as_ushort(__float2bfloat16_rn(hi))) << 16);
-}
-
-__device__ __forceinline__ void st_global_v4(uint4* p, uint4 v, uint64_t policy) {
-  asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;"
-               :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy) : "memory");
 }
 
 // Tile order: groups of `group_n` column tiles; inside a group the column index runs fastest.
@@ -747,6 +625,19 @@ static bool make_tensor_map(CUtensorMap* map, const void* base, bool bf16, int64
 
 bool make_fp8_tensor_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t K, int64_t ld, uint32_t box_rows) {
   return make_tensor_map(map, base, false, rows, K, ld, box_rows);
+}
+
+bool make_fp8_tensor_map_3d(CUtensorMap* map, const uint8_t* base, int64_t mats, int64_t rows, int64_t K, int64_t ld,
+                            uint32_t box_rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(K), cuuint64_t(rows), cuuint64_t(mats)};
+  const cuuint64_t strides[2] = {cuuint64_t(ld), cuuint64_t(ld) * cuuint64_t(rows)};
+  const cuuint32_t box[3] = {uint32_t(fp8k::gemm::BK), box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 namespace {

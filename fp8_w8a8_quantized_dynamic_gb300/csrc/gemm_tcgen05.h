@@ -99,6 +99,10 @@ int gemm_bf16_launch(const uint16_t* a, int64_t lda, const uint16_t* w, int64_t 
 bool make_fp8_tensor_map(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t K, int64_t ld,
                          uint32_t box_rows);
 
+// The same over `mats` matrices [rows, K] that follow one another (3-D map, box of one matrix).
+bool make_fp8_tensor_map_3d(CUtensorMap* map, const uint8_t* base, int64_t mats, int64_t rows, int64_t K, int64_t ld,
+                            uint32_t box_rows);
+
 // Device-side error bits recorded by the GEMM kernel on the current device (read, then cleared).
 unsigned int gemm_read_and_clear_error();
 

@@ -300,6 +300,100 @@ fp8_status fp8_linear_weight_only(const void* a_bf16, int64_t M, int64_t K, int6
                                   fp8_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Block-scaled FP8 linear: one scale per token and 128 values of K for the
+ * activations, one per 128 x 128 block of the weights. With K blocks
+ * b = [128 b, min(K, 128 b + 128)), KB = ceil(K / 128), NB = ceil(N / 128):
+ *
+ *   s_a[b][m] = max_{k in b} |A[m, k]| / 448        qA[m, k] = e4m3(A[m, k] / s_a[b][m])
+ *   s_w[j][b] = max over rows 128 j .. and b |W| / 448   qW[n, k] = e4m3(W[n, k] / s_w[j][b])
+ *   Y[m, n]   = bf16( sum_b s_a[b][m] s_w[n / 128][b] sum_{k in b} qA[m, k] qW[n, k] (+ bias[n]) )
+ *
+ * with the quotient, rounding and zero rules above (a block of zeros has scale
+ * 1). Both formats are e4m3: a scale for every 128 values leaves no use for the
+ * wider range of e5m2. Sums are fp32. A block that holds a NaN has a NaN
+ * scale, so its token's (weights: its 128 rows') results are NaN; an infinity
+ * gives an infinite scale and NaN as well. Other rows are not affected.
+ * FP8 matrices are laid out as above (ld a multiple of 16, zero tails).
+ * ---------------------------------------------------------------------------
+ */
+
+/* Quantizes B matrices W [N, K] (row stride ldw, matrix stride mat_stride, in
+ * elements; ignored when B is 1) to qw u8 [B][N, ldq] and s_w fp32
+ * [B][NB][KB], both without gaps between matrices. */
+fp8_status fp8_block_quantize_weight(const void* w_bf16, int64_t B, int64_t N, int64_t K, int64_t ldw,
+                                     int64_t mat_stride, uint8_t* qw, int64_t ldq, float* s_w,
+                                     fp8_stream_t stream);
+
+/* Quantizes activations A [M, K] to qa u8 [M, ldq] and s_a fp32 [KB][lds],
+ * lds >= M (the scales of one K block are adjacent). */
+fp8_status fp8_block_quantize_act(const void* a_bf16, int64_t M, int64_t K, int64_t lda, uint8_t* qa,
+                                  int64_t ldq, float* s_a, int64_t lds, fp8_stream_t stream);
+
+/* The product on operands quantized by the two calls above. Uses no workspace. */
+fp8_status fp8_block_scaled_mm(const uint8_t* qa, int64_t M, int64_t K, int64_t ldqa, const float* s_a,
+                               int64_t lds, const uint8_t* qw, int64_t N, int64_t ldqw, const float* s_w,
+                               const void* bias_bf16, void* y_bf16, int64_t ldy, fp8_stream_t stream);
+
+/* Workspace fp8_block_linear needs for this shape. Host-only. */
+size_t fp8_block_workspace_bytes(int64_t M, int64_t K, int64_t N);
+
+/* The linear: quantizes A, then the product. ws: >= fp8_block_workspace_bytes,
+ * 256-byte aligned. */
+fp8_status fp8_block_linear(const void* a_bf16, int64_t M, int64_t K, int64_t lda, const uint8_t* qw,
+                            int64_t N, int64_t ldqw, const float* s_w, const void* bias_bf16, void* y_bf16,
+                            int64_t ldy, void* ws, size_t ws_bytes, fp8_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Mixture of experts: the choice of experts, and the chosen experts' networks
+ * on block-scaled FP8 weights.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Chooses k of E experts for each of T tokens from logits x [T, E] (row stride
+ * ld; fp32, or bf16 when logits_bf16 is 1), in fp32:
+ *   sigmoid == 0: p = exp(x - max x) / sum;  sigmoid == 1: p = 1 / (1 + exp(-x))
+ *   choice c = p + bias (bias fp32 [E], a term for load balance that steers the
+ *   choice only; NULL: c = p, for softmax compared as x, the same order).
+ * groups > 1: the experts form `groups` equal consecutive groups; a group's
+ * score is the sum of its two largest c (its largest for softmax without bias)
+ * and only the keep_groups best groups take part.
+ * ids[t, 0..k) (int32): the experts with the largest c in descending order, ties
+ * to the lowest index; weights[t, j] (fp32) = p of ids[t, j], divided by
+ * (their sum + 1e-20) when renormalize is 1, times factor.
+ * A NaN logit counts as -inf. A softmax row of only -inf gives weights 0.
+ * Limits: E <= 512, k <= 32, groups <= 32, E a multiple of groups,
+ * k <= keep_groups * E / groups (else FP8_ERR_INVALID_ARG).
+ */
+fp8_status fp8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int64_t ld, int sigmoid,
+                         const float* bias, int groups, int keep_groups, int k, int renormalize, float factor,
+                         int32_t* ids, float* weights, fp8_stream_t stream);
+
+/* Workspace fp8_moe_experts needs (0 for sizes it refuses). Host-only. */
+size_t fp8_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
+
+/*
+ * The experts' gated networks over tokens x bf16 [T, H], summed by routing
+ * weight. For each pair (t, j) with e = ids[t, j] in [0, E):
+ *   g = x_t W13[e, 0]^T,  u = x_t W13[e, 1]^T        (block-scaled products, fp32)
+ *   h = silu(g) * u, quantized like activations (1 x 128 along I) from fp32
+ *   y[t] = bf16( sum_j weights[t, j] * (h W2[e]^T) )  (fp32, in the order of j)
+ * Pairs with any other id (experts that live elsewhere) contribute nothing; a
+ * token with none gets zeros. ids, weights [T, k] without gaps; an expert may
+ * occur more than once in a row. qw13 u8 [E][2][I, ldq13], s13 fp32
+ * [E][2][ceil(I/128)][ceil(H/128)]; qw2 u8 [E][H, ldq2], s2 fp32
+ * [E][ceil(H/128)][ceil(I/128)], as fp8_block_quantize_weight writes them for
+ * 2 E and E matrices. Results do not depend on timing. y may not overlap x.
+ * ws: >= fp8_moe_workspace_bytes, 256-byte aligned. Limits: E <= 512, k <= 32.
+ */
+fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
+                           const float* weights, int64_t k, const uint8_t* qw13, int64_t ldq13, const float* s13,
+                           const uint8_t* qw2, int64_t ldq2, const float* s2, int64_t E, int64_t I, void* y_bf16,
+                           int64_t ldy, void* ws, size_t ws_bytes, fp8_stream_t stream);
+
+/*
  * Diagnostics (no counterpart on the source pages): the launch the GEMM path of
  * fp8_linear (and fp8_scaled_mm, which never splits K) would use for FP8
  * operands qa [M, ldqa] and qw [N, ldqw] (ld in bytes), K columns, and a
