@@ -130,13 +130,27 @@ def min_ld(K: int) -> int:
 # torch-facing wrappers (torch is imported lazily: host-only users need none of it)
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+_raw_stream = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(t) -> int:
-    return _torch().cuda.current_stream(t.device).cuda_stream
+    """The current stream of t's device. The raw query takes a tenth of a microsecond where building a
+    Stream object takes two, a good part of a small call's time."""
+    global _raw_stream
+    if _raw_stream is None:
+        torch = _torch()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(t.get_device())
 
 
 def _ptr(t) -> Optional[int]:
@@ -376,43 +390,43 @@ def _blocks(n: int) -> int:
 
 
 def _out_bf16(out, M: int, N: int, like):
-    torch = _torch()
     if out is None:
-        return torch.empty((M, N), dtype=torch.bfloat16, device=like.device)
+        return _torch().empty((M, N), dtype=like.dtype, device=like.device)  # `like` is bf16
     _check_bf16_2d(out, "out")
     if out.shape != (M, N) or out.device != like.device:
         raise ValueError(f"out: expected [{M}, {N}] on {like.device}")
     return out
 
 
-def _check_dense(t, dtype, shape, like, name: str):
-    """A gap-free tensor of this dtype and shape on the device of `like`."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}")
+def _check_dense(t, dtype, shape, device, name: str):
+    """A gap-free tensor of this dtype and shape on this device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
-def _check_block_weight(qw, s_w, lead: tuple, N: int, K: int, like, name: str):
-    """Codes [*lead, N, ld] and scales [*lead, blocks of N, blocks of K] as fp8_block_quantize_weight returns them."""
+def _check_block_weight(qw, s_w, lead: tuple, N: int, K: int, device, name: str) -> int:
+    """Codes [*lead, N, ld] and scales [*lead, blocks of N, blocks of K] as fp8_block_quantize_weight returns
+    them; returns ld."""
     torch = _torch()
-    if qw.dim() != len(lead) + 2 or qw.shape[-1] < K or qw.shape[-1] % 16:
+    ld = qw.shape[-1]
+    if ld < K or ld % 16 or ld == 0:
         raise ValueError(f"{name}: expected uint8 codes [..., N, ld] with ld a multiple of 16 and at least {K}")
-    _check_dense(qw, torch.uint8, (*lead, N, qw.shape[-1]), like, name)
-    _check_dense(s_w, torch.float32, (*lead, _blocks(N), _blocks(K)), like, name + " scales")
+    _check_dense(qw, torch.uint8, (*lead, N, ld), device, name)
+    _check_dense(s_w, torch.float32, (*lead, (N + 127) // 128, (K + 127) // 128), device, name + " scales")
+    return ld
 
 
-def _check_bias(bias, N: int, like):
-    if bias is not None:
-        _check_dense(bias, _torch().bfloat16, (N,), like, "bias")
-
-
-def _scratch(ws, need: int, like):
-    """The caller's workspace, or a fresh one."""
+def _scratch(ws, need: int, device):
+    """(address, bytes, tensor) of the caller's workspace, or of a fresh one (none where none is needed)."""
     torch = _torch()
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device) if need else None
-    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != like.device:
-        raise ValueError(f"ws: expected a contiguous uint8 tensor on {like.device}")
-    return ws
+        if not need:
+            return None, 0, None
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws.data_ptr(), need, ws
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
+        raise ValueError(f"ws: expected a contiguous uint8 tensor on {device}")
+    return ws.data_ptr(), ws.numel(), ws
 
 
 def fp8_block_quantize_weight(w):
@@ -449,16 +463,17 @@ def fp8_block_scaled_mm(qa, K: int, s_a, qw, s_w, bias=None, out=None):
     """The block-scaled product on already-quantized operands (fp8_block_quantize_act / _weight), bf16 out."""
     torch = _torch()
     _check_fp8_2d(qa, K, "qa")
-    M, N = qa.shape[0], qw.shape[-2]
-    if s_a.dtype != torch.float32 or s_a.shape != (_blocks(K), M) or s_a.device != qa.device or (
+    M, N, device = qa.shape[0], qw.shape[-2], qa.device
+    if s_a.dtype != torch.float32 or s_a.shape != (_blocks(K), M) or s_a.device != device or (
             s_a.numel() and s_a.stride(1) != 1):
         raise ValueError(f"s_a: expected fp32 [{_blocks(K)}, {M}] with unit column stride")
-    _check_block_weight(qw, s_w, (), N, K, qa, "qw")
-    _check_bias(bias, N, qa)
-    y = _out_bf16(out, M, N, qa)
+    ld = _check_block_weight(qw, s_w, (), N, K, device, "qw")
+    if bias is not None:
+        _check_dense(bias, torch.bfloat16, (N,), device, "bias")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=device) if out is None else _out_bf16(out, M, N, qa)
     _check(lib().fp8_block_scaled_mm(qa.data_ptr(), M, K, qa.stride(0), s_a.data_ptr(),
                                      max(s_a.stride(0), M, 1) if s_a.shape[0] > 1 else max(M, 1), qw.data_ptr(), N,
-                                     qw.stride(0), s_w.data_ptr(), _ptr(bias), y.data_ptr(), max(y.stride(0), N, 1),
+                                     ld, s_w.data_ptr(), _ptr(bias), y.data_ptr(), max(y.stride(0), N, 1),
                                      _stream_ptr(qa)), "fp8_block_scaled_mm")
     return y
 
@@ -472,14 +487,18 @@ def fp8_block_linear(a, qw, s_w, bias=None, out=None, ws=None):
     qw, s_w come from fp8_block_quantize_weight."""
     _check_bf16_2d(a, "a")
     M, K = a.shape
-    N = qw.shape[-2]
-    _check_block_weight(qw, s_w, (), N, K, a, "qw")
-    _check_bias(bias, N, a)
+    N, device = qw.shape[-2], a.device
+    ld = _check_block_weight(qw, s_w, (), N, K, device, "qw")
+    if bias is not None:
+        _check_dense(bias, a.dtype, (N,), device, "bias")
     y = _out_bf16(out, M, N, a)
-    ws = _scratch(ws, lib().fp8_block_workspace_bytes(M, K, N), a)
-    _check(lib().fp8_block_linear(a.data_ptr(), M, K, max(a.stride(0), K, 1), qw.data_ptr(), N, qw.stride(0),
-                                  s_w.data_ptr(), _ptr(bias), y.data_ptr(), max(y.stride(0), N, 1), _ptr(ws),
-                                  0 if ws is None else ws.numel(), _stream_ptr(a)), "fp8_block_linear")
+    L = lib()
+    wp, wn, ws = _scratch(ws, L.fp8_block_workspace_bytes(M, K, N), device)
+    status = L.fp8_block_linear(a.data_ptr(), M, K, max(a.stride(0), K, 1), qw.data_ptr(), N, ld, s_w.data_ptr(),
+                                None if bias is None else bias.data_ptr(), y.data_ptr(), max(y.stride(0), N, 1), wp,
+                                wn, _stream_ptr(a))
+    if status:
+        raise FP8Error(status, "fp8_block_linear")
     return y
 
 
@@ -492,22 +511,26 @@ def fp8_moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int
     token in descending order and their routing weights. score 'softmax' or 'sigmoid'; bias fp32 [E] steers the
     choice only; only the keep_groups best of `groups` groups of experts take part (default: all)."""
     torch = _torch()
-    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.dim() != 2 or not logits.is_cuda or (
+    dtype = logits.dtype
+    if (dtype != torch.float32 and dtype != torch.bfloat16) or logits.dim() != 2 or not logits.is_cuda or (
             logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits: expected a CUDA fp32 or bf16 matrix with unit column stride")
     if score not in _SCORES:
         raise ValueError(f"unknown score {score!r} (expected 'softmax' or 'sigmoid')")
     T, E = logits.shape
+    device = logits.device
     if bias is not None:
-        _check_dense(bias, torch.float32, (E,), logits, "bias")
+        _check_dense(bias, torch.float32, (E,), device, "bias")
     if k < 1:
         raise ValueError(f"k: expected at least 1, got {k}")
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    _check(lib().fp8_moe_route(logits.data_ptr(), int(logits.dtype == torch.bfloat16), T, E, max(logits.stride(0), E),
-                               _SCORES[score], _ptr(bias), groups, groups if keep_groups is None else keep_groups, k,
-                               int(bool(renormalize)), float(factor), ids.data_ptr(), weights.data_ptr(),
-                               _stream_ptr(logits)), "fp8_moe_route")
+    ids = torch.empty((T, k), dtype=torch.int32, device=device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=device)
+    status = lib().fp8_moe_route(logits.data_ptr(), dtype == torch.bfloat16, T, E, max(logits.stride(0), E),
+                                 _SCORES[score], None if bias is None else bias.data_ptr(), groups,
+                                 groups if keep_groups is None else keep_groups, k, bool(renormalize), factor,
+                                 ids.data_ptr(), weights.data_ptr(), _stream_ptr(logits))
+    if status:
+        raise FP8Error(status, "fp8_moe_route")
     return ids, weights
 
 
@@ -523,19 +546,22 @@ def fp8_moe_experts(x, ids, weights, qw13, s13, qw2, s2, out=None, ws=None):
     torch = _torch()
     _check_bf16_2d(x, "x")
     T, H = x.shape
-    if ids.dim() != 2 or qw13.dim() != 4 or qw13.shape[1] != 2:
+    if ids.dim() != 2 or qw13.dim() != 4:
         raise ValueError("expected ids [T, k] and qw13 [E, 2, I, ld]")
-    k, E, I = ids.shape[1], qw13.shape[0], qw13.shape[2]
-    _check_dense(ids, torch.int32, (T, k), x, "ids")
-    _check_dense(weights, torch.float32, (T, k), x, "weights")
-    _check_block_weight(qw13, s13, (E, 2), I, H, x, "qw13")
-    _check_block_weight(qw2, s2, (E,), H, I, x, "qw2")
+    E, _, I, _ = qw13.shape
+    k, device = ids.shape[1], x.device
+    _check_dense(ids, torch.int32, (T, k), device, "ids")
+    _check_dense(weights, torch.float32, (T, k), device, "weights")
+    ld13 = _check_block_weight(qw13, s13, (E, 2), I, H, device, "qw13")
+    ld2 = _check_block_weight(qw2, s2, (E,), H, I, device, "qw2")
     y = _out_bf16(out, T, H, x)
-    ws = _scratch(ws, lib().fp8_moe_workspace_bytes(T, k, E, H, I), x)
-    _check(lib().fp8_moe_experts(x.data_ptr(), T, H, max(x.stride(0), H, 1), ids.data_ptr(), weights.data_ptr(), k,
-                                 qw13.data_ptr(), qw13.shape[3], s13.data_ptr(), qw2.data_ptr(), qw2.shape[2],
-                                 s2.data_ptr(), E, I, y.data_ptr(), max(y.stride(0), H, 1), _ptr(ws),
-                                 0 if ws is None else ws.numel(), _stream_ptr(x)), "fp8_moe_experts")
+    L = lib()
+    wp, wn, ws = _scratch(ws, L.fp8_moe_workspace_bytes(T, k, E, H, I), device)
+    status = L.fp8_moe_experts(x.data_ptr(), T, H, max(x.stride(0), H, 1), ids.data_ptr(), weights.data_ptr(), k,
+                               qw13.data_ptr(), ld13, s13.data_ptr(), qw2.data_ptr(), ld2, s2.data_ptr(), E, I,
+                               y.data_ptr(), max(y.stride(0), H, 1), wp, wn, _stream_ptr(x))
+    if status:
+        raise FP8Error(status, "fp8_moe_experts")
     return y
 
 

@@ -9,6 +9,7 @@
 
 #include "api_common.h"
 #include "block_gemm.h"
+#include "block_gemv.h"
 #include "block_quant.cuh"
 #include "device_cache.h"
 #include "moe.cuh"
@@ -56,15 +57,21 @@ struct Carver {
   }
 };
 
-// Workspace of fp8_block_linear: codes of A, then its scales.
+// Few rows: one kernel quantizes A and streams the weights.
+bool linear_fused(int64_t M, int64_t K) { return block::gemv_fits(M, K, 1) && block::gemv_quantizes(M, K); }
+
+// Workspace of fp8_block_linear: codes of A, then its scales; none when one kernel does both.
 struct LinearWs {
   size_t qa, s_a, total;
+  int64_t lds;  // M rounded up to 4: the GEMM copies whole 16-byte pieces of a block's scales
 };
 LinearWs linear_ws(int64_t M, int64_t K) {
   Carver c;
-  LinearWs w;
+  LinearWs w = {};
+  if (linear_fused(M, K)) return w;
   w.qa = c.take(size_t(M) * size_t(round_up16(K)));
-  w.s_a = c.take(size_t(blocks_of(K)) * size_t(M) * 4);
+  w.lds = (M + 3) / 4 * 4;
+  w.s_a = c.take(size_t(blocks_of(K)) * size_t(w.lds) * 4);
   w.total = c.at;
   return w;
 }
@@ -72,6 +79,24 @@ LinearWs linear_ws(int64_t M, int64_t K) {
 fp8_status block_mm(const uint8_t* qa, int64_t M, int64_t K, int64_t ldqa, const float* s_a, int64_t lds_a,
                     const uint8_t* qw, int64_t N, int64_t ldqw, const float* s_w, const void* bias, void* y,
                     int64_t ldy, int sms, cudaStream_t st) {
+  if (block::gemv_fits(M, K, 1)) {
+    block::GemvArgs v = {};
+    v.src = block::kSrcCodes;
+    v.a = qa;
+    v.lda = ldqa;
+    v.s_a = s_a;
+    v.lds_a = lds_a;
+    v.M = M;
+    v.qw = qw;
+    v.ldw = ldqw;
+    v.s_w = s_w;
+    v.N = N;
+    v.K = K;
+    v.bias = static_cast<const uint16_t*>(bias);
+    v.y = static_cast<uint16_t*>(y);
+    v.ldy = ldy;
+    return block::gemv_launch(v, block::kGemvBf16, sms, st) ? FP8_OK : FP8_ERR_CUDA;
+  }
   block::GemmArgs g = {};
   g.qa = qa;
   g.rows = M;
@@ -117,27 +142,55 @@ fp8_status check_product(int64_t M, int64_t K, const uint8_t* qw, int64_t N, int
   return FP8_OK;
 }
 
-// Workspace of fp8_moe_experts over P = T * k pairs.
-struct MoeWs {
-  size_t n_tiles, tiles, pos, qx, s_x, qh, s_h, y, total;
-  int64_t pairs, max_tiles, ldx, ldh, ldy;
+// How the experts of P = T * k pairs run, by the rows an expert has on average:
+//   one token: a GEMV over the pairs for h, one over all of their h for y (two launches);
+//   few rows:  sort, GEMV for h, GEMV for the pairs' rows, weighted sum;
+//   more:      sort, quantize, two tensor-core products, weighted sum.
+enum class MoePath { kOneToken, kGemv, kGemm };
+
+struct MoePlan {
+  MoePath path;
+  int tile_rows;
 };
-MoeWs moe_ws(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+
+MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  const int64_t pairs = T * k;
+  if (T == 1 && block::gemv_fits(1, H, 2) && block::gemv_fits(1, k * blocks_of(I) * block::kBlock, 1))
+    return {MoePath::kOneToken, 1};
+  const int rows = pairs <= 4 * E ? 8 : 16;
+  if (pairs <= 12 * E && block::gemv_fits(rows, H, 2) && block::gemv_fits(rows, I, 1)) return {MoePath::kGemv, rows};
+  return {MoePath::kGemm, block::kRowTile};
+}
+
+struct MoeWs {
+  size_t n_tiles, tiles, pos, row_src, qx, s_x, h, s_h, y, total;
+  int64_t pairs, max_tiles, ldx, ldh, ldy, lds;
+};
+MoeWs moe_ws(const MoePlan& plan, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   Carver c;
-  MoeWs w;
+  MoeWs w = {};
   w.pairs = T * k;
-  w.max_tiles = w.pairs / block::kRowTile + std::min(E, w.pairs);
+  w.max_tiles = w.pairs / plan.tile_rows + std::min(E, w.pairs);
   w.ldx = round_up16(H);
   w.ldh = round_up16(I);
   w.ldy = (H + 3) / 4 * 4;
-  w.n_tiles = c.take(4);
-  w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
-  w.pos = c.take(size_t(w.pairs) * 4);
-  w.qx = c.take(size_t(w.pairs) * size_t(w.ldx));
-  w.s_x = c.take(size_t(w.pairs) * size_t(blocks_of(H)) * 4);
-  w.qh = c.take(size_t(w.pairs) * size_t(w.ldh));
-  w.s_h = c.take(size_t(w.pairs) * size_t(blocks_of(I)) * 4);
-  w.y = c.take(size_t(w.pairs) * size_t(w.ldy) * 4);
+  w.lds = (w.pairs + 3) / 4 * 4;
+  const size_t pairs = size_t(w.pairs);
+  if (plan.path != MoePath::kOneToken) {
+    w.n_tiles = c.take(4);
+    w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
+    w.pos = c.take(pairs * 4);
+    w.y = c.take(pairs * size_t(w.ldy) * 4);
+  }
+  if (plan.path == MoePath::kGemv) w.row_src = c.take(pairs * 4);
+  if (plan.path == MoePath::kGemm) {
+    w.qx = c.take(pairs * size_t(w.ldx));
+    w.s_x = c.take(size_t(w.lds) * size_t(blocks_of(H)) * 4);
+    w.h = c.take(pairs * size_t(w.ldh));
+    w.s_h = c.take(size_t(w.lds) * size_t(blocks_of(I)) * 4);
+  } else {
+    w.h = c.take(pairs * size_t(w.ldh) * 4);  // fp32; the second GEMV quantizes it
+  }
   w.total = c.at;
   return w;
 }
@@ -149,8 +202,8 @@ bool moe_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
 
 PerDeviceCache<const void*, int> g_attr_cache;
 
-fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int* pos, block::RowTile* tiles, int* n_tiles,
-                       cudaStream_t st) {
+fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int k, int tile_rows, int* pos, int* row_src,
+                       block::RowTile* tiles, int* n_tiles, cudaStream_t st) {
   const size_t smem = size_t(moe::kPlanWarps + 1) * E * sizeof(int);
   int dev = 0, set = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
@@ -161,8 +214,8 @@ fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int* pos, block
                            "plan smem attribute") == cudaSuccess;
       }))
     return FP8_ERR_CUDA;
-  return launch(moe::plan_kernel, dim3(1), dim3(moe::kPlanThreads), smem, st, true, dim3(1, 1, 1), ids, pairs, E, pos,
-                tiles, n_tiles);
+  return launch(moe::plan_kernel, dim3(1), dim3(moe::kPlanThreads), smem, st, true, dim3(1, 1, 1), ids, pairs, E, k,
+                tile_rows, pos, row_src, tiles, n_tiles);
 }
 
 template <typename T>
@@ -247,11 +300,27 @@ FP8_API fp8_status fp8_block_linear(const void* a_bf16, int64_t M, int64_t K, in
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (K == 0) return launch_rows_of_bias(bias_bf16, y_bf16, M, N, ldy, sms, st);
   const BF16Mat A{static_cast<const uint16_t*>(a_bf16), M, K, lda};
+  if (linear_fused(M, K)) {
+    block::GemvArgs v = {};
+    v.src = block::kSrcBf16;
+    v.a = A.p;
+    v.lda = lda;
+    v.M = M;
+    v.qw = qw;
+    v.ldw = ldqw;
+    v.s_w = s_w;
+    v.N = N;
+    v.K = K;
+    v.bias = static_cast<const uint16_t*>(bias_bf16);
+    v.y = static_cast<uint16_t*>(y_bf16);
+    v.ldy = ldy;
+    return block::gemv_launch(v, block::kGemvBf16, sms, st) ? FP8_OK : FP8_ERR_CUDA;
+  }
   const LinearWs w = linear_ws(M, K);
   uint8_t* qa = static_cast<uint8_t*>(ws) + w.qa;
   float* s_a = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.s_a);
-  FP8_TRY(launch_quantize_rows(A, qa, round_up16(K), s_a, M, nullptr, 0, sms, st));
-  return block_mm(qa, M, K, round_up16(K), s_a, M, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy, sms, st);
+  FP8_TRY(launch_quantize_rows(A, qa, round_up16(K), s_a, w.lds, nullptr, 0, sms, st));
+  return block_mm(qa, M, K, round_up16(K), s_a, w.lds, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy, sms, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -294,7 +363,7 @@ FP8_API fp8_status fp8_moe_route(const void* logits, int logits_bf16, int64_t T,
 
 FP8_API size_t fp8_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   if (!moe_sizes_ok(T, k, E, H, I) || T == 0 || H == 0) return 0;
-  return moe_ws(T, k, E, H, I).total;
+  return moe_ws(moe_plan(T, k, E, H, I), T, k, E, H, I).total;
 }
 
 FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
@@ -310,24 +379,86 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(s13, 4) || !aligned(s2, 4)) return FP8_ERR_MISALIGNED;
   if (T == 0 || H == 0) return FP8_OK;
   if (ids == nullptr || weights == nullptr || s13 == nullptr || s2 == nullptr) return FP8_ERR_INVALID_ARG;
-  const MoeWs w = moe_ws(T, k, E, H, I);
+  const MoePlan plan = moe_plan(T, k, E, H, I);
+  const MoeWs w = moe_ws(plan, T, k, E, H, I);
   FP8_TRY(check_ws(ws, ws_bytes, w.total));
   int sms = 0;
   FP8_TRY(current_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* b = static_cast<uint8_t*>(ws);
+  const BF16Mat X{static_cast<const uint16_t*>(x_bf16), T, H, ldx};
+
+  block::GemvArgs v = {};
+  if (plan.path != MoePath::kGemm) {
+    v.src = block::kSrcBf16;
+    v.a = X.p;
+    v.lda = ldx;
+    v.experts = E;
+    v.qw = qw13;
+    v.ldw = ldq13;
+    v.s_w = s13;
+    v.N = I;
+    v.K = H;
+    v.y32 = reinterpret_cast<float*>(b + w.h);
+    v.ldy32 = w.ldh;
+  }
+  if (plan.path == MoePath::kOneToken) {
+    v.ids = ids;
+    v.weights = weights;
+    v.pairs = int(k);
+    if (!block::gemv_launch(v, block::kGemvSwiglu, sms, st)) return FP8_ERR_CUDA;
+    v.src = block::kSrcF32;
+    v.a = b + w.h;
+    v.lda = w.ldh;
+    v.qw = qw2;
+    v.ldw = ldq2;
+    v.s_w = s2;
+    v.N = H;
+    v.K = I;
+    v.y = static_cast<uint16_t*>(y_bf16);
+    v.ldy = ldy;
+    return block::gemv_launch(v, block::kGemvSum, sms, st) ? FP8_OK : FP8_ERR_CUDA;
+  }
+
   int* n_tiles = reinterpret_cast<int*>(b + w.n_tiles);
   block::RowTile* tiles = reinterpret_cast<block::RowTile*>(b + w.tiles);
   int* pos = reinterpret_cast<int*>(b + w.pos);
+  int* row_src = plan.path == MoePath::kGemv ? reinterpret_cast<int*>(b + w.row_src) : nullptr;
+  float* y32 = reinterpret_cast<float*>(b + w.y);
+  FP8_TRY(launch_plan(ids, w.pairs, int(E), int(k), plan.tile_rows, pos, row_src, tiles, n_tiles, st));
+  auto weighted_sum = [&] {
+    const int vec = aligned(y_bf16, 8) && ldy % 4 == 0;
+    return launch(moe::weighted_sum_kernel, dim3(elementwise_grid(T * ((H + 3) / 4), moe::kSumThreads, sms, 8)),
+                  dim3(moe::kSumThreads), 0, st, true, dim3(1, 1, 1), static_cast<const float*>(y32), w.ldy,
+                  static_cast<const int*>(pos), weights, int(k), T, H, static_cast<uint16_t*>(y_bf16), ldy, vec);
+  };
+  if (plan.path == MoePath::kGemv) {
+    v.tiles = tiles;
+    v.n_tiles = n_tiles;
+    v.max_tiles = w.max_tiles;
+    v.tile_rows = plan.tile_rows;
+    v.row_src = row_src;
+    if (!block::gemv_launch(v, block::kGemvSwiglu, sms, st)) return FP8_ERR_CUDA;
+    v.src = block::kSrcF32;
+    v.a = b + w.h;
+    v.lda = w.ldh;
+    v.row_src = nullptr;
+    v.qw = qw2;
+    v.ldw = ldq2;
+    v.s_w = s2;
+    v.N = H;
+    v.K = I;
+    v.y32 = y32;
+    v.ldy32 = w.ldy;
+    if (!block::gemv_launch(v, block::kGemvF32, sms, st)) return FP8_ERR_CUDA;
+    return weighted_sum();
+  }
+
+  // quantize each token once into its rows; gate and up products with SwiGLU and the quantization
+  // of h in their epilogue; the product back; the weighted sum
   float* s_x = reinterpret_cast<float*>(b + w.s_x);
   float* s_h = reinterpret_cast<float*>(b + w.s_h);
-  float* y32 = reinterpret_cast<float*>(b + w.y);
-
-  // sort the pairs by expert; quantize each token once into its rows; gate and up products with
-  // SwiGLU and the quantization of h in their epilogue; the product back; the weighted sum
-  FP8_TRY(launch_plan(ids, w.pairs, int(E), pos, tiles, n_tiles, st));
-  const BF16Mat X{static_cast<const uint16_t*>(x_bf16), T, H, ldx};
-  FP8_TRY(launch_quantize_rows(X, b + w.qx, w.ldx, s_x, w.pairs, pos, int(k), sms, st));
+  FP8_TRY(launch_quantize_rows(X, b + w.qx, w.ldx, s_x, w.lds, pos, int(k), sms, st));
   block::GemmArgs g = {};
   g.rows = w.pairs;
   g.tiles = tiles;
@@ -336,19 +467,19 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   g.qa = b + w.qx;
   g.lda = w.ldx;
   g.s_a = s_x;
-  g.lds_a = w.pairs;
+  g.lds_a = w.lds;
   g.qw = qw13;
   g.mats = 2 * E;
   g.ldw = ldq13;
   g.s_w = s13;
   g.N = I;
   g.K = H;
-  g.qh = b + w.qh;
+  g.qh = b + w.h;
   g.ldh = w.ldh;
   g.s_h = s_h;
-  g.lds_h = w.pairs;
+  g.lds_h = w.lds;
   if (!block::gemm_launch(g, block::kOutSwiglu, sms, st)) return FP8_ERR_CUDA;
-  g.qa = b + w.qh;
+  g.qa = b + w.h;
   g.lda = w.ldh;
   g.s_a = s_h;
   g.qw = qw2;
@@ -360,8 +491,5 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   g.y32 = y32;
   g.ldy32 = w.ldy;
   if (!block::gemm_launch(g, block::kOutF32, sms, st)) return FP8_ERR_CUDA;
-  const int vec = aligned(y_bf16, 8) && ldy % 4 == 0;
-  return launch(moe::weighted_sum_kernel, dim3(elementwise_grid(T * ((H + 3) / 4), moe::kSumThreads, sms, 8)),
-                dim3(moe::kSumThreads), 0, st, true, dim3(1, 1, 1), static_cast<const float*>(y32), w.ldy,
-                static_cast<const int*>(pos), weights, int(k), T, H, static_cast<uint16_t*>(y_bf16), ldy, vec);
+  return weighted_sum();
 }

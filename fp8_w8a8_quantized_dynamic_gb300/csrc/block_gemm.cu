@@ -14,13 +14,27 @@
 // Structure (persistent, one CTA per SM, output tiles of 128 x BN):
 //   warp 0      TMA producer: activation tile [128 x 128 B] and weight tile [BN x 128 B] of a K
 //               block into a ring of 128B-swizzled shared memory stages.
-//   warp 1      tensor-memory allocator and MMA issuer; the block partials rotate through
-//               512 / BN tensor-memory buffers.
-//   warps 2..9  promotion: two groups of four warps, each with half of the columns; a thread
-//               reads its row of the partial (tcgen05.ld) and adds it, scaled, in registers.
-//               After the last K block the same threads write the tile out.
+//   warps 1, 3  MMA issuers, for the K blocks of even and odd number; the block partials rotate
+//               through 512 / BN tensor-memory buffers (at most four). One block's waits, MMAs and
+//               commits take a thread about 650 cycles and the tensor core 512 (BN = 256), so one
+//               issuer would set the pace (measured: 740 cycles a block with one, 556 with two).
+//               Warp 1 also allocates the tensor memory.
+//   warp 2      scale loader: the rows' scales and the weight blocks' scales of kScaleKb K blocks a
+//               slot, by bulk copies and cp.async into a ring of its own (a load from L2 takes longer
+//               than a block, and the ring runs ahead over the ends of tiles).
+//   warps 4..11 promotion: two groups of four warps, each with half of the columns; a thread
+//               reads its row of the partial (tcgen05.ld, 32 columns at a time; a read and its wait
+//               take some 30 cycles, which the other warp of the scheduler fills, and keeping reads
+//               in flight behind the additions costs more in copied registers) and adds it, scaled,
+//               in registers. After the last K block the same threads write the tile out. Their 128
+//               accumulators and the read buffer need more registers than an even share, which the
+//               first warpgroup gives up.
 // Ragged sizes need no padding: TMA fills out-of-range rows and columns with zeros and the
 // stores are predicated.
+//
+// One CTA computes 128 x 256 by itself. The two-SM MMA on 256 x 256 (half the weight traffic from L2)
+// was built and measured slower, 540 against 300 us at 8192 x 4096 x 8192: its commits and the peer's
+// arrivals cross the cluster in every block, and two tensor-memory buffers cannot hide that.
 //
 // Every wait is bounded; on expiry the kernel records an error, all roles run to the end of
 // their loops without waiting or storing, copies and MMAs in flight are drained, and the tensor
@@ -43,8 +57,15 @@ __device__ unsigned int g_block_gemm_error;
 
 constexpr int BM = kRowTile;
 constexpr int BK = kBlock;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kPromoWarps = 8;
+constexpr int kFirstPromoWarp = 4;
+constexpr int kScaleKb = 4;     // K blocks of one slot of the scale ring
+constexpr int kScaleSlots = 4;
+constexpr int kStageBytes = 2048;  // a promotion warp's output staging: 32 rows of 64 bytes
+// 384 threads start with 168 registers each; 56 + 2 * 224 = 3 * 168
+constexpr int kLaunchRegs = 168, kIssueRegs = 56, kPromoRegs = 224;
+static_assert(kIssueRegs + 2 * kPromoRegs <= 3 * kLaunchRegs, "register shares of the three warpgroups");
 constexpr uint32_t kABytes = BM * BK;
 constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 8;
@@ -67,7 +88,12 @@ struct SharedCtl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
+  uint64_t sfull[kScaleSlots];
+  uint64_t sempty[kScaleSlots];
   uint32_t hmax[2][2][BM];  // SwiGLU: row maxima of the two column halves, by tile parity
+  alignas(16) float s_row[kScaleSlots][kScaleKb][BM + 4];  // from the tile's first row rounded down to 4
+  alignas(16) float s_col[kScaleSlots][kScaleKb][4];  // [promotion group][gate, up]
+  alignas(16) uint8_t staging[kPromoWarps][kStageBytes];
 };
 constexpr size_t kSmemBytes = 1024 + kRingBytes + sizeof(SharedCtl);
 static_assert(kSmemBytes <= 232448, "ring and control block must fit the 227 KB per-block limit");
@@ -77,6 +103,7 @@ struct Params {
   int rows, N, kb;
   const float* s_a;
   int64_t lds_a;
+  int bulk_scales;  // s_a's rows start on 16-byte boundaries
   const float* s_w;
   int nb;  // scale rows of one weight matrix
   const RowTile* tiles;
@@ -113,6 +140,40 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
 __device__ __forceinline__ float lo_of(uint64_t p) { return __uint_as_float(uint32_t(p)); }
 __device__ __forceinline__ float hi_of(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
 
+// Copies `bytes` (a multiple of 16, both addresses 16-byte aligned) and completes them on the barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const float* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+
+// A predicated arrival, without a branch.
+__device__ __forceinline__ void arrive_if(uint32_t bar, bool p) {
+  asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}"
+               :: "r"(bar), "r"(uint32_t(p)) : "memory");
+}
+
+// One lane of a converged warp (the compiler keeps the branch uniform).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+// Arrives on the barrier when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+// acc[0..15] += s2 * r (32 columns, in pairs).
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&r)[32], uint64_t s2) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    acc[j] = fma_f32x2(pack_f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2, acc[j]);
+}
+
 // silu(g) * u in fp32; exp and the reciprocal by the hardware approximations (a few 2^-23), far
 // below the 2^-4 spacing of the codes h is quantized to.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
@@ -145,6 +206,9 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
   const uint32_t smem_base = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &ctl->abort_flag;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return mbar_wait_short(smem_u32(bar), parity, abort_flag, &g_block_gemm_error);
+  };
 
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
@@ -157,7 +221,11 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       mbar_init(smem_u32(&ctl->tfull[b]), 1);
       mbar_init(smem_u32(&ctl->tempty[b]), kPromoWarps);
     }
-    mbar_init(smem_u32(&ctl->drain), 1);
+    mbar_init(smem_u32(&ctl->drain), 2);
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(smem_u32(&ctl->sfull[i]), 33);  // each lane's cp.async, and the bulk copies
+      mbar_init(smem_u32(&ctl->sempty[i]), kPromoWarps);
+    }
     ctl->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -195,7 +263,9 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     }
   };
 
-  if (warp == 0) {
+  if (warp < kFirstPromoWarp) {
+   if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssueRegs));
+   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer ----------------
       const uint64_t pol = l2_policy(kHintNormal);
@@ -207,8 +277,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         bool ok = true;
         for (int kb = 0; kb < p.kb; ++kb, ++it) {
           const int s = it % kStages;
-          if (!mbar_wait_bounded(smem_u32(&ctl->empty[s]), ((it / kStages) & 1u) ^ 1u, abort_flag,
-                                 &g_block_gemm_error)) {
+          if (!wait(&ctl->empty[s], ((it / kStages) & 1u) ^ 1u)) {
             ok = false;
             break;
           }
@@ -232,90 +301,158 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       for (uint32_t j = it > uint32_t(kStages) ? it - kStages : 0u; j < it; ++j)
         mbar_wait_bounded(smem_u32(&ctl->full[j % kStages]), (j / kStages) & 1u, nullptr, &g_block_gemm_error);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      // D fp32, A and B e4m3, both K-major, N = BN, M = 128
-      constexpr uint32_t idesc = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-        for (int kb = 0; kb < p.kb; ++kb, ++it) {
-          const int b = it % kBufs, s = it % kStages;
-          if (!mbar_wait_bounded(smem_u32(&ctl->tempty[b]), ((it / kBufs) & 1u) ^ 1u, abort_flag,
-                                 &g_block_gemm_error) ||
-              !mbar_wait_bounded(smem_u32(&ctl->full[s]), (it / kStages) & 1u, abort_flag, &g_block_gemm_error)) {
-            ok = false;
-            break;
-          }
-          tmem_fence_after();
-          const uint64_t adesc = make_sdesc(smem_base + s * Tile<BN>::stage_bytes);
-          const uint64_t bdesc = make_sdesc(smem_base + s * Tile<BN>::stage_bytes + kABytes);
-          const uint32_t d = tmem_base + b * BN;
+   } else if (warp != 2) {
+    // ---------------- MMA issuers: warps 1 and 3, K blocks of even and odd number ----------------
+    // D fp32, A and B e4m3, both K-major, N = BN, M = 128
+    constexpr uint32_t idesc =
+        (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
+    const int mine = units > int(blockIdx.x) ? (units - int(blockIdx.x) + int(gridDim.x) - 1) / int(gridDim.x) : 0;
+    const uint32_t total = uint32_t(mine) * uint32_t(p.kb);  // blocks of all of this CTA's tiles
+    for (uint32_t it = warp >> 1; it < total; it += 2) {
+      const int b = it % kBufs, s = it % kStages;
+      // the operands are there long before the buffer is free: what follows the last wait is
+      // what counts
+      bool ok = wait(&ctl->full[s], (it / kStages) & 1u);
+      ok = wait(&ctl->tempty[b], ((it / kBufs) & 1u) ^ 1u) && ok;
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tmem_fence_after();
+      if (elect_one()) {
+        const uint64_t adesc = make_sdesc(smem_base + s * Tile<BN>::stage_bytes);
+        const uint64_t bdesc = make_sdesc(smem_base + s * Tile<BN>::stage_bytes + kABytes);
+        const uint32_t d = tmem_base + b * BN;
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            mma_f8(d, adesc + uint64_t(kk * 32 >> 4), bdesc + uint64_t(kk * 32 >> 4), idesc, kk != 0);
-          mma_commit<false>(smem_u32(&ctl->empty[s]));
-          mma_commit<false>(smem_u32(&ctl->tfull[b]));
-        }
+        for (int kk = 0; kk < BK / 32; ++kk)
+          mma_f8(d, adesc + uint64_t(kk * 32 >> 4), bdesc + uint64_t(kk * 32 >> 4), idesc, kk != 0);
+        mma_commit<false>(smem_u32(&ctl->tfull[b]));
+        mma_commit<false>(smem_u32(&ctl->empty[s]));
       }
-      mma_commit<false>(smem_u32(&ctl->drain));  // all MMAs done before the tensor memory is released
-      mbar_wait_bounded(smem_u32(&ctl->drain), 0, nullptr, &g_block_gemm_error);
+      __syncwarp();
     }
+    if (elect_one()) mma_commit<false>(smem_u32(&ctl->drain));
+    __syncwarp();
+    // all MMAs done before the tensor memory is released
+    mbar_wait_bounded(smem_u32(&ctl->drain), 0, nullptr, &g_block_gemm_error);
+   } else if (warp == 2) {
+    // ---------------- scale loader ----------------
+    uint32_t slot_no = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      int expert, row0, row_end, n_idx;
+      decode(u, expert, row0, row_end, n_idx);
+      const int n0 = n_idx * kTileN;
+      // lane % 4: the weight scale row of (promotion group, matrix)
+      const int mat = kOut == kOutSwiglu ? 2 * expert + (lane & 1) : expert;
+      const int col = kOut == kOutSwiglu ? n0 : n0 + ((lane >> 1) & 1) * kHalf;
+      const float* sw = p.s_w + (int64_t(mat) * p.nb + min(col / kBlock, p.nb - 1)) * p.kb;
+      for (int kb0 = 0; kb0 < p.kb; kb0 += kScaleKb, ++slot_no) {
+        const int slot = slot_no % kScaleSlots;
+        wait(&ctl->sempty[slot], ((slot_no / kScaleSlots) & 1u) ^ 1u);
+        __syncwarp();
+        const uint32_t bar = smem_u32(&ctl->sfull[slot]);
+        if (p.bulk_scales) {
+          // one bulk copy a block: rows [a0, a0 + n), whole 16-byte pieces inside the block's lds_a
+          const int a0 = row0 & ~3;
+          const uint32_t bytes = uint32_t(min(int64_t(BM + 4), p.lds_a - a0)) * 4u;
+          const int blocks = min(kScaleKb, p.kb - kb0);
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes * blocks);
+          __syncwarp();
+          if (lane < blocks)
+            bulk_load(smem_u32(&ctl->s_row[slot][lane][0]), p.s_a + int64_t(kb0 + lane) * p.lds_a + a0, bytes, bar);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kScaleKb; ++j) {
+            const int kb = min(kb0 + j, p.kb - 1);
+#pragma unroll
+            for (int i = 0; i < BM / 32; ++i) {
+              const int row = row0 + lane + i * 32;  // rows past the tile's repeat its first
+              cp_async4(smem_u32(&ctl->s_row[slot][j][(row0 & 3) + lane + i * 32]),
+                        p.s_a + int64_t(kb) * p.lds_a + (row < row_end ? row : row0));
+            }
+          }
+          if (lane == 0) mbar_arrive(bar);
+        }
+        if (lane < 4 * kScaleKb)
+          cp_async4(smem_u32(&ctl->s_col[slot][lane >> 2][lane & 3]), sw + min(kb0 + (lane >> 2), p.kb - 1));
+        cp_async_arrive(bar);
+      }
+    }
+    // nothing of the last slots may land after the CTA has left
+    for (uint32_t i = slot_no > uint32_t(kScaleSlots) ? slot_no - kScaleSlots : 0u; i < slot_no; ++i)
+      mbar_wait_bounded(smem_u32(&ctl->sfull[i % kScaleSlots]), (i / kScaleSlots) & 1u, nullptr, &g_block_gemm_error);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+   }
   } else {
-    // ---------------- promotion and epilogue: warps 2..9 ----------------
-    const int group = (warp - 2) >> 2;   // column half
+    // ---------------- promotion and epilogue: warps 4..11 ----------------
+    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kPromoRegs));
+    const int group = (warp - kFirstPromoWarp) >> 2;  // column half
     const int quarter = warp & 3;        // tensor-memory lanes this warp may access
     const int row_in_tile = quarter * 32 + lane;
     const uint32_t tbase = tmem_base + (uint32_t(quarter * 32) << 16) + group * kHalf;
-    uint32_t it = 0, tile_no = 0;
+    uint32_t it = 0, tile_no = 0, slot_no = 0;
+    uint8_t* staging = ctl->staging[warp - kFirstPromoWarp];
     for (int u = blockIdx.x; u < units; u += gridDim.x, ++tile_no) {
       int expert, row0, row_end, n_idx;
       decode(u, expert, row0, row_end, n_idx);
       const int n0 = n_idx * kTileN;
       const int row = row0 + row_in_tile;
       const bool live = row < row_end;
-      const float* sa_ptr = p.s_a + (live ? row : row0);
-      // scale rows: one for all columns of this group, or (SwiGLU) gate and up
-      const float* sw0;
-      const float* sw1 = nullptr;
-      if (kOut == kOutSwiglu) {
-        sw0 = p.s_w + (int64_t(2 * expert) * p.nb + n0 / kBlock) * p.kb;
-        sw1 = sw0 + int64_t(p.nb) * p.kb;
-      } else {
-        sw0 = p.s_w + (int64_t(expert) * p.nb + min((n0 + group * kHalf) / kBlock, p.nb - 1)) * p.kb;
-      }
       uint64_t acc[kHalf / 2];
 #pragma unroll
       for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
-      float sa_n = sa_ptr[0], s0_n = sw0[0], s1_n = kOut == kOutSwiglu ? sw1[0] : 0.0f;
-      for (int kb = 0; kb < p.kb; ++kb, ++it) {
-        const float sc0 = sa_n * s0_n, sc1 = sa_n * s1_n;
-        if (kb + 1 < p.kb) {
-          sa_n = sa_ptr[int64_t(kb + 1) * p.lds_a];
-          s0_n = sw0[kb + 1];
-          if (kOut == kOutSwiglu) s1_n = sw1[kb + 1];
+      uint64_t g2 = 0, u2 = 0;  // this block's scales of the group's first and second half of columns
+      // the scales of block kb; the slot is handed back with its last block
+      auto next_scales = [&](int kb) {
+        const int slot = slot_no % kScaleSlots, j = kb % kScaleKb;
+        if (j == 0) {
+          wait(&ctl->sfull[slot], (slot_no / kScaleSlots) & 1u);
+          __syncwarp();
         }
+        const float sa = ctl->s_row[slot][j][(row0 & 3) + row_in_tile];
+        const float2 sw = *reinterpret_cast<const float2*>(&ctl->s_col[slot][j][2 * group]);
+        if (j == kScaleKb - 1 || kb == p.kb - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->sempty[slot]));
+          ++slot_no;
+        }
+        g2 = pack_f32x2(sa * sw.x, sa * sw.x);
+        u2 = kOut == kOutSwiglu ? pack_f32x2(sa * sw.y, sa * sw.y) : g2;
+      };
+      for (int kb = 0; kb < p.kb; ++kb, ++it) {
+        constexpr int kChunks = kHalf / 32;
         const int b = it % kBufs;
-        mbar_wait_bounded(smem_u32(&ctl->tfull[b]), (it / kBufs) & 1u, abort_flag, &g_block_gemm_error);
+        next_scales(kb);
+        wait(&ctl->tfull[b], (it / kBufs) & 1u);
         __syncwarp();
         tmem_fence_after();
+        const uint32_t tempty = smem_u32(&ctl->tempty[b]);
 #pragma unroll
-        for (int c = 0; c < kHalf / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(tbase + b * BN + c * 32, r);
-          const float sc = kOut == kOutSwiglu && c >= 2 ? sc1 : sc0;
-          const uint64_t s2 = pack_f32x2(sc, sc);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            acc[c * 16 + j] = fma_f32x2(pack_f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2,
-                                        acc[c * 16 + j]);
+        for (int c = 0; c < kChunks; ++c) {
+          uint32_t part[32];
+          tmem_ld32(tbase + b * BN + c * 32, part);
+          if (c == kChunks - 1) {  // the last read has landed: the buffer is free before its columns are added
+            tmem_fence_before();
+            arrive_if(tempty, lane == 0);
+          }
+          add_scaled(acc + c * 16, part, 2 * c < kChunks ? g2 : u2);
         }
-        tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[b]));
       }
-      const bool store = live && *abort_flag == 0;
+      const bool store = *abort_flag == 0;
+      // 64 bytes of each of the warp's 32 rows, from one row a lane to eight whole rows a store
+      // instruction: through shared memory, the 16-byte pieces of a row exchanged by (row / 2) % 4
+      // so that neither side has bank conflicts
+      const int warp_row0 = row0 + quarter * 32;
+      auto put_row_piece = [&](int c, uint4 v) {
+        *reinterpret_cast<uint4*>(staging + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) = v;
+      };
+      auto for_pieces = [&](auto&& write) {  // write(row, piece of the 64 bytes, its 16 bytes)
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + (lane >> 2), c = lane & 3;
+          const uint4 v = *reinterpret_cast<const uint4*>(staging + r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
+          if (store && warp_row0 + r < row_end) write(warp_row0 + r, c, v);
+        }
+        __syncwarp();
+      };
       if constexpr (kOut == kOutSwiglu) {
         // columns [64 group, 64 group + 64) of the tile's 128-wide block of h
         uint32_t m = 0;
@@ -332,54 +469,62 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         m = max(m, ctl->hmax[tile_no & 1][group ^ 1][row_in_tile]);
         const float s = scale_from_amax<kFmtE4M3>(__uint_as_float(m));
         const ExactScale k = make_exact_scale(s);
-        if (store) {
-          uint8_t* dst = p.qh + int64_t(row) * p.ldh + n0 + group * 64;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          put_row_piece(v, make_uint4(codes4(acc[v * 8], acc[v * 8 + 1], k, s), codes4(acc[v * 8 + 2], acc[v * 8 + 3], k, s),
+                                      codes4(acc[v * 8 + 4], acc[v * 8 + 5], k, s),
+                                      codes4(acc[v * 8 + 6], acc[v * 8 + 7], k, s)));
+        for_pieces([&](int r, int c, uint4 v) {
+          const int col = n0 + group * 64 + c * 16;  // columns past N hold zeros (zero weight rows)
+          if (col < p.ldh) *reinterpret_cast<uint4*>(p.qh + int64_t(r) * p.ldh + col) = v;
+        });
+        if (store && live && group == 0) p.s_h[int64_t(n_idx) * p.lds_h + row] = s;
+      } else if constexpr (kOut == kOutF32) {
+#pragma unroll
+        for (int q = 0; q < kHalf / 16; ++q) {
+          const int col0 = n0 + group * kHalf + q * 16;
+          if (col0 >= p.ldy32) break;  // ldy32: N rounded up to 4
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            if (n0 + group * 64 + v * 16 < p.ldh) {  // columns past N hold zeros (zero weight rows)
-              uint4 o;
-              o.x = codes4(acc[v * 8], acc[v * 8 + 1], k, s);
-              o.y = codes4(acc[v * 8 + 2], acc[v * 8 + 3], k, s);
-              o.z = codes4(acc[v * 8 + 4], acc[v * 8 + 5], k, s);
-              o.w = codes4(acc[v * 8 + 6], acc[v * 8 + 7], k, s);
-              *reinterpret_cast<uint4*>(dst + v * 16) = o;
-            }
+            const uint64_t a0 = acc[q * 8 + 2 * v], a1 = acc[q * 8 + 2 * v + 1];
+            put_row_piece(v, make_uint4(uint32_t(a0), uint32_t(a0 >> 32), uint32_t(a1), uint32_t(a1 >> 32)));
           }
-          if (group == 0) p.s_h[int64_t(n_idx) * p.lds_h + row] = s;
-        }
-      } else if constexpr (kOut == kOutF32) {
-        if (store) {
-          float* dst = p.y32 + int64_t(row) * p.ldy32 + n0 + group * kHalf;
-#pragma unroll
-          for (int v = 0; v < kHalf / 4; ++v) {
-            if (n0 + group * kHalf + v * 4 < p.ldy32)  // ldy32: N rounded up to 4
-              *reinterpret_cast<float4*>(dst + v * 4) =
-                  make_float4(lo_of(acc[2 * v]), hi_of(acc[2 * v]), lo_of(acc[2 * v + 1]), hi_of(acc[2 * v + 1]));
-          }
+          for_pieces([&](int r, int c, uint4 v) {
+            if (col0 + c * 4 < p.ldy32) *reinterpret_cast<uint4*>(p.y32 + int64_t(r) * p.ldy32 + col0 + c * 4) = v;
+          });
         }
       } else {
-        const int c0 = n0 + group * kHalf;
-        uint16_t* dst = p.y + int64_t(row) * p.ldy + c0;
-        if (store) {
 #pragma unroll
-          for (int v = 0; v < kHalf / 8; ++v) {
+        for (int q = 0; q < kHalf / 32; ++q) {
+          const int col0 = n0 + group * kHalf + q * 32;
+          if (col0 >= p.N) break;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
             float o[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[2 * j] = lo_of(acc[4 * v + j]), o[2 * j + 1] = hi_of(acc[4 * v + j]);
+            for (int j = 0; j < 4; ++j) {
+              const uint64_t a = acc[q * 16 + v * 4 + j];
+              o[2 * j] = lo_of(a), o[2 * j + 1] = hi_of(a);
+            }
             if (p.bias) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (c0 + v * 8 + j < p.N) o[j] += bf16_bits_to_float(p.bias[c0 + v * 8 + j]);
+              for (int j = 0; j < 8; ++j) o[j] += bf16_bits_to_float(__ldg(p.bias + min(col0 + v * 8 + j, p.N - 1)));
             }
-            if (p.vec && c0 + v * 8 + 8 <= p.N) {
-              *reinterpret_cast<uint4*>(dst + v * 8) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                                                                  pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+            put_row_piece(v, make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                        pack_bf16x2(o[6], o[7])));
+          }
+          for_pieces([&](int r, int c, uint4 v) {
+            const int col = col0 + c * 8;
+            uint16_t* dst = p.y + int64_t(r) * p.ldy + col;
+            if (p.vec && col + 8 <= p.N) {
+              *reinterpret_cast<uint4*>(dst) = v;
             } else {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                if (c0 + v * 8 + j < p.N) dst[v * 8 + j] = __bfloat16_as_ushort(__float2bfloat16_rn(o[j]));
+                if (col + j < p.N) dst[j] = uint16_t(w[j >> 1] >> ((j & 1) * 16));
             }
-          }
+          });
         }
       }
     }
@@ -421,6 +566,7 @@ bool launch_tile(const GemmArgs& a, int num_sms, cudaStream_t st) {
   p.kb = int(blocks_of(a.K));
   p.s_a = a.s_a;
   p.lds_a = a.lds_a;
+  p.bulk_scales = aligned(a.s_a, 16) && a.lds_a % 4 == 0;
   p.s_w = a.s_w;
   p.nb = int(blocks_of(a.N));
   p.tiles = a.tiles;
@@ -454,11 +600,15 @@ bool launch_tile(const GemmArgs& a, int num_sms, cudaStream_t st) {
 
 template <int kOut>
 bool launch_any(const GemmArgs& a, int num_sms, cudaStream_t st) {
-  // the widest tile that still gives every SM one
-  const int64_t m_tiles = a.tiles ? a.max_tiles : (a.rows + BM - 1) / BM;
-  if (m_tiles * ((a.N + 255) / 256) >= num_sms) return launch_tile<256, kOut>(a, num_sms, st);
-  if (m_tiles * ((a.N + 127) / 128) >= num_sms) return launch_tile<128, kOut>(a, num_sms, st);
-  return launch_tile<64, kOut>(a, num_sms, st);
+  if constexpr (kOut == kOutSwiglu) {
+    return launch_tile<256, kOut>(a, num_sms, st);
+  } else {
+    // the widest tile that still gives every SM one
+    const int64_t m_tiles = a.tiles ? a.max_tiles : (a.rows + BM - 1) / BM;
+    if (m_tiles * ((a.N + 255) / 256) >= num_sms) return launch_tile<256, kOut>(a, num_sms, st);
+    if (m_tiles * ((a.N + 127) / 128) >= num_sms) return launch_tile<128, kOut>(a, num_sms, st);
+    return launch_tile<64, kOut>(a, num_sms, st);
+  }
 }
 
 }  // namespace
@@ -466,7 +616,7 @@ bool launch_any(const GemmArgs& a, int num_sms, cudaStream_t st) {
 bool gemm_launch(const GemmArgs& a, Out out, int num_sms, cudaStream_t stream) {
   switch (out) {
     case kOutBf16: return launch_any<kOutBf16>(a, num_sms, stream);
-    case kOutSwiglu: return launch_tile<256, kOutSwiglu>(a, num_sms, stream);
+    case kOutSwiglu: return launch_any<kOutSwiglu>(a, num_sms, stream);
     case kOutF32: return launch_any<kOutF32>(a, num_sms, stream);
   }
   return false;

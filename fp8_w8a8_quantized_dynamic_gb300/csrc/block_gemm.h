@@ -23,7 +23,7 @@ enum Out : int {
 };
 
 // A row tile of the grouped product: rows [row0, row_end) of the sorted activations belong to
-// `expert`; a tile covers the first kRowTile of them. Written by the routing plan kernel.
+// `expert`; a tile covers the first of them (kRowTile in the GEMM). Written by the routing plan kernel.
 struct RowTile {
   int expert, row0, row_end, pad;
 };

@@ -173,12 +173,13 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 
 // Order of the routed pairs: pair i (= token * k + j) with expert ids[i] in [0, experts) gets row
 // pos[i], rows sorted by expert and, within one, by pair (stable, so nothing depends on timing);
-// any other id gives -1. Then the row tiles of the grouped product. One CTA: each warp counts its
+// any other id gives -1; row_src (may be null) gets the token of each row. Then the row tiles, of
+// tile_rows rows each. One CTA: each warp counts its
 // contiguous share of the pairs by expert in shared memory (equal ids of a step are found by a
 // warp match), the counts are scanned over warps and experts, and the second walk hands out rows.
 __global__ void __launch_bounds__(kPlanThreads, 1)
-plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, int* __restrict__ pos,
-            block::RowTile* __restrict__ tiles, int* __restrict__ n_tiles) {
+plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, int k, int tile_rows, int* __restrict__ pos,
+            int* __restrict__ row_src, block::RowTile* __restrict__ tiles, int* __restrict__ n_tiles) {
   extern __shared__ int count[];  // [kPlanWarps][experts], then [experts] totals
   int* total = count + kPlanWarps * experts;
   __shared__ int warp_sum[2][kPlanWarps];
@@ -207,7 +208,7 @@ plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, int* __
       tot += v;
     }
   }
-  const int my_tiles = (tot + block::kRowTile - 1) / block::kRowTile;
+  const int my_tiles = (tot + tile_rows - 1) / tile_rows;
   int rows_before = tot, tiles_before = my_tiles;  // inclusive scans over the experts
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -226,7 +227,7 @@ plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, int* __
   if (int(threadIdx.x) < experts) {
     total[threadIdx.x] = rows_before;
     for (int j = 0; j < my_tiles; ++j) {
-      const int r0 = rows_before + j * block::kRowTile;
+      const int r0 = rows_before + j * tile_rows;
       tiles[tiles_before + j] = block::RowTile{int(threadIdx.x), r0, rows_before + tot, 0};
     }
   }
@@ -242,6 +243,7 @@ plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, int* __
     if (in && lane == __ffs(same) - 1) mine[id] += __popc(same);
     __syncwarp();
     if (i + lane < end) pos[i + lane] = d;
+    if (row_src != nullptr && d >= 0) row_src[d] = int((i + lane) / k);
   }
 }
 
