@@ -162,8 +162,14 @@ MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   return {MoePath::kGemm, block::kRowTile};
 }
 
+// CTAs that sort the pairs; more than one need their counts first.
+int plan_ctas(int64_t pairs) {
+  if (pairs <= 4 * moe::kPlanPairs) return 1;  // a second launch costs more than it saves
+  return int(std::min<int64_t>(moe::kPlanMaxCtas, (pairs + moe::kPlanPairs - 1) / moe::kPlanPairs));
+}
+
 struct MoeWs {
-  size_t n_tiles, tiles, pos, row_src, qx, s_x, h, s_h, y, total;
+  size_t n_tiles, tiles, counts, pos, row_src, qx, s_x, h, s_h, y, total;
   int64_t pairs, max_tiles, ldx, ldh, ldy, lds;
 };
 MoeWs moe_ws(const MoePlan& plan, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
@@ -179,6 +185,7 @@ MoeWs moe_ws(const MoePlan& plan, int64_t T, int64_t k, int64_t E, int64_t H, in
   if (plan.path != MoePath::kOneToken) {
     w.n_tiles = c.take(4);
     w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
+    w.counts = c.take(plan_ctas(w.pairs) > 1 ? size_t(plan_ctas(w.pairs)) * size_t(E) * 4 : 0);
     w.pos = c.take(pairs * 4);
     w.y = c.take(pairs * size_t(w.ldy) * 4);
   }
@@ -202,8 +209,8 @@ bool moe_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
 
 PerDeviceCache<const void*, int> g_attr_cache;
 
-fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int k, int tile_rows, int* pos, int* row_src,
-                       block::RowTile* tiles, int* n_tiles, cudaStream_t st) {
+fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int k, int tile_rows, int* counts, int* pos,
+                       int* row_src, block::RowTile* tiles, int* n_tiles, cudaStream_t st) {
   const size_t smem = size_t(moe::kPlanWarps + 1) * E * sizeof(int);
   int dev = 0, set = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
@@ -214,14 +221,18 @@ fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int k, int tile
                            "plan smem attribute") == cudaSuccess;
       }))
     return FP8_ERR_CUDA;
-  return launch(moe::plan_kernel, dim3(1), dim3(moe::kPlanThreads), smem, st, true, dim3(1, 1, 1), ids, pairs, E, k,
-                tile_rows, pos, row_src, tiles, n_tiles);
+  const int ctas = plan_ctas(pairs);
+  if (ctas > 1)
+    FP8_TRY(launch(moe::plan_count_kernel, dim3(ctas), dim3(moe::kPlanThreads), 0, st, true, dim3(1, 1, 1), ids, pairs,
+                   E, counts));
+  return launch(moe::plan_kernel, dim3(ctas), dim3(moe::kPlanThreads), smem, st, true, dim3(1, 1, 1), ids, pairs, E, k,
+                tile_rows, ctas > 1 ? static_cast<const int*>(counts) : nullptr, pos, row_src, tiles, n_tiles);
 }
 
 template <typename T>
 fp8_status launch_route(const T* logits, const moe::RouteParams& p, int sms, cudaStream_t st) {
   auto go = [&](auto kernel) {
-    const int grid = elementwise_grid(p.tokens, moe::kRouteThreads / 32, sms, 8);
+    const int grid = int((p.tokens + moe::kRouteThreads / 32 - 1) / (moe::kRouteThreads / 32));
     return launch(kernel, dim3(grid), dim3(moe::kRouteThreads), 0, st, true, dim3(1, 1, 1), logits, p);
   };
   if (p.experts <= 32) return go(moe::route_kernel<T, 1>);
@@ -347,6 +358,7 @@ FP8_API fp8_status fp8_moe_route(const void* logits, int logits_bf16, int64_t T,
   moe::RouteParams p = {};
   p.tokens = T;
   p.ld = ld;
+  p.vec = aligned(logits, 16) && ld * (logits_bf16 ? 2 : 4) % 16 == 0;
   p.experts = int(E);
   p.k = k;
   p.groups = groups;
@@ -425,7 +437,8 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   int* pos = reinterpret_cast<int*>(b + w.pos);
   int* row_src = plan.path == MoePath::kGemv ? reinterpret_cast<int*>(b + w.row_src) : nullptr;
   float* y32 = reinterpret_cast<float*>(b + w.y);
-  FP8_TRY(launch_plan(ids, w.pairs, int(E), int(k), plan.tile_rows, pos, row_src, tiles, n_tiles, st));
+  FP8_TRY(launch_plan(ids, w.pairs, int(E), int(k), plan.tile_rows, reinterpret_cast<int*>(b + w.counts), pos,
+                      row_src, tiles, n_tiles, st));
   auto weighted_sum = [&] {
     const int vec = aligned(y_bf16, 8) && ldy % 4 == 0;
     return launch(moe::weighted_sum_kernel, dim3(elementwise_grid(T * ((H + 3) / 4), moe::kSumThreads, sms, 8)),

@@ -265,3 +265,15 @@ def test_layer_end_to_end():
     logits = F.fp8_block_linear(x.to(DEV), *F.fp8_block_quantize_weight(gate.to(DEV)))
     ids, w = check_route(logits.cpu(), k, renormalize=True)
     check_experts(T, E, k, H, I, seed=20, x=x, ids=torch.from_numpy(ids), w=torch.from_numpy(w.astype(np.float32)))
+
+
+def test_experts_many_pairs_sorted_by_several_ctas():
+    """Enough pairs that several CTAs sort them: the same result as in two halves, which one CTA sorts each."""
+    T, E, k, H, I = 1500, 24, 4, 64, 128
+    x, (ids, w) = tokens_of(T, H, 30).to(DEV), choices(T, E, k, 31, drop=0.1)
+    ids, w = ids.to(DEV), w.to(DEV)
+    q = weights_of(E, H, I, 32)
+    y = F.fp8_moe_experts(x, ids, w, *q)
+    parts = [F.fp8_moe_experts(x[s], ids[s].contiguous(), w[s].contiguous(), *q)
+             for s in (slice(0, 700), slice(700, 1500))]
+    assert torch.equal(y, torch.cat(parts))
