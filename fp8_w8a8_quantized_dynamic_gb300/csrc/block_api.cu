@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "api_common.h"
@@ -450,6 +451,9 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
     v.n_tiles = n_tiles;
     v.max_tiles = w.max_tiles;
     v.tile_rows = plan.tile_rows;
+    // experts that an even routing of the pairs touches
+    const double untouched = std::pow(1.0 - 1.0 / double(E), double(w.pairs));
+    v.likely_tiles = std::max<int64_t>(1, std::min<int64_t>(w.max_tiles, int64_t(double(E) * (1.0 - untouched) + 0.5)));
     v.row_src = row_src;
     if (!block::gemv_launch(v, block::kGemvSwiglu, sms, st)) return FP8_ERR_CUDA;
     v.src = block::kSrcF32;

@@ -29,6 +29,7 @@ struct GemvArgs {
   const int* n_tiles;
   int64_t max_tiles;
   int tile_rows;          // 8 or 16
+  int64_t likely_tiles;   // how many of max_tiles an even routing fills (0: unknown)
   // one token: the tiles are its pairs, expert ids[j] and row j; with kOutSum K runs over all pairs
   const int32_t* ids;
   const float* weights;
