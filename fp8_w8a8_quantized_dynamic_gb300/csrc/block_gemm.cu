@@ -32,6 +32,9 @@
 // Ragged sizes need no padding: TMA fills out-of-range rows and columns with zeros and the
 // stores are predicated.
 //
+// Few tiles (kSplit): a cluster of 2, 4 or 8 CTAs shares a tile's K; each sends its sums to the CTAs
+// that own their columns (distributed shared memory), which add them in order and write them out.
+//
 // One CTA computes 128 x 256 by itself. The two-SM MMA on 256 x 256 (half the weight traffic from L2)
 // was built and measured slower, 540 against 300 us at 8192 x 4096 x 8192: its commits and the peer's
 // arrivals cross the cluster in every block, and two tensor-memory buffers cannot hide that.
@@ -43,6 +46,7 @@
 #include "block_gemm.h"
 
 #include <algorithm>
+#include <utility>
 
 #include "api_common.h"
 #include "device_cache.h"
@@ -71,10 +75,12 @@ constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 8;
 constexpr int kMaxBufs = 4;
 
-template <int BN>
+// kSplit: a cluster's CTAs share a tile's K; part of the ring holds the sums they exchange.
+template <int BN, bool kSplit>
 struct Tile {
   static constexpr uint32_t stage_bytes = kABytes + BN * BK;
-  static constexpr int stages = int(kRingBytes / stage_bytes);  // 4, 6, 8 for BN = 256, 128, 64
+  static constexpr uint32_t exchange_bytes = kSplit ? BN * BM * 4 : 0;
+  static constexpr int stages = int((kRingBytes - exchange_bytes) / stage_bytes);  // 4, 6, 8 for BN = 256, 128, 64
   static constexpr int bufs = 512 / BN < kMaxBufs ? 512 / BN : kMaxBufs;
   static constexpr int cols = bufs * BN;  // tensor-memory columns (a power of two)
   static_assert(stages <= kMaxStages, "ring");
@@ -109,6 +115,7 @@ struct Params {
   const RowTile* tiles;
   const int* n_row_tiles;
   int m_tiles, n_tiles, group_n;
+  int split_log2, kb_slice;  // kSplit: CTAs of a cluster, K blocks of one
   const uint16_t* bias;
   uint16_t* y;
   int64_t ldy;
@@ -136,6 +143,8 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
       :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
+
+__host__ __device__ constexpr int ilog2(int n) { return n <= 1 ? 0 : 1 + ilog2(n / 2); }
 
 __device__ __forceinline__ float lo_of(uint64_t p) { return __uint_as_float(uint32_t(p)); }
 __device__ __forceinline__ float hi_of(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
@@ -190,20 +199,22 @@ __device__ __forceinline__ uint32_t codes4(uint64_t p01, uint64_t p23, const Exa
   return quant2_divide<kFmtE4M3>(lo_of(p01), hi_of(p01), s) | (quant2_divide<kFmtE4M3>(lo_of(p23), hi_of(p23), s) << 16);
 }
 
-template <int BN, int kOut>
+template <int BN, int kOut, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                   const __grid_constant__ Params p) {
-  constexpr int kStages = Tile<BN>::stages;
-  constexpr int kBufs = Tile<BN>::bufs;
+  constexpr int kStages = Tile<BN, kSplit>::stages;
+  constexpr int kBufs = Tile<BN, kSplit>::bufs;
   constexpr int kHalf = BN / 2;                                    // columns of one promotion group
   constexpr int kTileN = kOut == kOutSwiglu ? BN / 2 : BN;         // output columns of a tile
   static_assert(kOut != kOutSwiglu || BN == 256, "a SwiGLU tile is one 128-wide block of h");
+  static_assert(!kSplit || (kOut != kOutSwiglu && BN <= 128), "sums of K slices are linear outputs of narrow tiles");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   SharedCtl* ctl = reinterpret_cast<SharedCtl*>(smem + kRingBytes);
   const uint32_t smem_base = smem_u32(smem);
+  float* exchange = reinterpret_cast<float*>(smem + kStages * Tile<BN, kSplit>::stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &ctl->abort_flag;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -232,11 +243,12 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-                 :: "r"(smem_u32(&ctl->tmem_base)), "n"(Tile<BN>::cols) : "memory");
+                 :: "r"(smem_u32(&ctl->tmem_base)), "n"(Tile<BN, kSplit>::cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tmem_fence_before();
   __syncthreads();
+  if (kSplit) pair_sync();  // the cluster's other CTAs run: their shared memory may be written
   tmem_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
 
@@ -263,6 +275,14 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     }
   };
 
+  // K slice and work units: all of K and every gridDim.x-th tile, or (kSplit) a cluster a tile and
+  // rank r's share of its K
+  auto rank_of = [&]() { return kSplit ? int(cluster_rank()) : 0; };
+  auto kb_begin = [&]() { return kSplit ? min(p.kb, rank_of() * p.kb_slice) : 0; };
+  auto kb_end = [&]() { return kSplit ? min(p.kb, (rank_of() + 1) * p.kb_slice) : p.kb; };
+  auto first_unit = [&]() { return kSplit ? int(blockIdx.x) >> p.split_log2 : int(blockIdx.x); };
+  auto unit_stride = [&]() { return kSplit ? int(gridDim.x) >> p.split_log2 : int(gridDim.x); };
+
   if (warp < kFirstPromoWarp) {
    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssueRegs));
    if (warp == 0) {
@@ -270,20 +290,20 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       // ---------------- TMA producer ----------------
       const uint64_t pol = l2_policy(kHintNormal);
       uint32_t it = 0;
-      for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      for (int u = first_unit(); u < units; u += unit_stride()) {
         int expert, row0, row_end, n_idx;
         decode(u, expert, row0, row_end, n_idx);
         const int n0 = n_idx * kTileN;
         bool ok = true;
-        for (int kb = 0; kb < p.kb; ++kb, ++it) {
+        for (int kb = kb_begin(); kb < kb_end(); ++kb, ++it) {
           const int s = it % kStages;
           if (!wait(&ctl->empty[s], ((it / kStages) & 1u) ^ 1u)) {
             ok = false;
             break;
           }
           const uint32_t fb = smem_u32(&ctl->full[s]);
-          const uint32_t dst = smem_base + s * Tile<BN>::stage_bytes;
-          mbar_arrive_expect_tx(fb, Tile<BN>::stage_bytes);
+          const uint32_t dst = smem_base + s * Tile<BN, kSplit>::stage_bytes;
+          mbar_arrive_expect_tx(fb, Tile<BN, kSplit>::stage_bytes);
           tma_load_2d(dst, &tmap_a, fb, kb * BK, row0, pol);
           if (kOut == kOutSwiglu) {
             // 64 columns of gate, then the same 64 of up, twice: each promotion group holds both
@@ -306,8 +326,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     // D fp32, A and B e4m3, both K-major, N = BN, M = 128
     constexpr uint32_t idesc =
         (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
-    const int mine = units > int(blockIdx.x) ? (units - int(blockIdx.x) + int(gridDim.x) - 1) / int(gridDim.x) : 0;
-    const uint32_t total = uint32_t(mine) * uint32_t(p.kb);  // blocks of all of this CTA's tiles
+    const int mine = units > first_unit() ? (units - first_unit() + unit_stride() - 1) / unit_stride() : 0;
+    const uint32_t total = uint32_t(mine) * uint32_t(kb_end() - kb_begin());  // blocks of all of this CTA's tiles
     for (uint32_t it = warp >> 1; it < total; it += 2) {
       const int b = it % kBufs, s = it % kStages;
       // the operands are there long before the buffer is free: what follows the last wait is
@@ -317,8 +337,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       if (!__all_sync(0xffffffffu, ok)) break;
       tmem_fence_after();
       if (elect_one()) {
-        const uint64_t adesc = make_sdesc(smem_base + s * Tile<BN>::stage_bytes);
-        const uint64_t bdesc = make_sdesc(smem_base + s * Tile<BN>::stage_bytes + kABytes);
+        const uint64_t adesc = make_sdesc(smem_base + s * Tile<BN, kSplit>::stage_bytes);
+        const uint64_t bdesc = make_sdesc(smem_base + s * Tile<BN, kSplit>::stage_bytes + kABytes);
         const uint32_t d = tmem_base + b * BN;
 #pragma unroll
         for (int kk = 0; kk < BK / 32; ++kk)
@@ -335,7 +355,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
    } else if (warp == 2) {
     // ---------------- scale loader ----------------
     uint32_t slot_no = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    for (int u = first_unit(); u < units; u += unit_stride()) {
       int expert, row0, row_end, n_idx;
       decode(u, expert, row0, row_end, n_idx);
       const int n0 = n_idx * kTileN;
@@ -343,7 +363,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       const int mat = kOut == kOutSwiglu ? 2 * expert + (lane & 1) : expert;
       const int col = kOut == kOutSwiglu ? n0 : n0 + ((lane >> 1) & 1) * kHalf;
       const float* sw = p.s_w + (int64_t(mat) * p.nb + min(col / kBlock, p.nb - 1)) * p.kb;
-      for (int kb0 = 0; kb0 < p.kb; kb0 += kScaleKb, ++slot_no) {
+      for (int kb0 = kb_begin(); kb0 < kb_end(); kb0 += kScaleKb, ++slot_no) {
         const int slot = slot_no % kScaleSlots;
         wait(&ctl->sempty[slot], ((slot_no / kScaleSlots) & 1u) ^ 1u);
         __syncwarp();
@@ -352,7 +372,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           // one bulk copy a block: rows [a0, a0 + n), whole 16-byte pieces inside the block's lds_a
           const int a0 = row0 & ~3;
           const uint32_t bytes = uint32_t(min(int64_t(BM + 4), p.lds_a - a0)) * 4u;
-          const int blocks = min(kScaleKb, p.kb - kb0);
+          const int blocks = min(kScaleKb, kb_end() - kb0);
           if (lane == 0) mbar_arrive_expect_tx(bar, bytes * blocks);
           __syncwarp();
           if (lane < blocks)
@@ -360,7 +380,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         } else {
 #pragma unroll
           for (int j = 0; j < kScaleKb; ++j) {
-            const int kb = min(kb0 + j, p.kb - 1);
+            const int kb = min(kb0 + j, kb_end() - 1);
 #pragma unroll
             for (int i = 0; i < BM / 32; ++i) {
               const int row = row0 + lane + i * 32;  // rows past the tile's repeat its first
@@ -371,7 +391,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           if (lane == 0) mbar_arrive(bar);
         }
         if (lane < 4 * kScaleKb)
-          cp_async4(smem_u32(&ctl->s_col[slot][lane >> 2][lane & 3]), sw + min(kb0 + (lane >> 2), p.kb - 1));
+          cp_async4(smem_u32(&ctl->s_col[slot][lane >> 2][lane & 3]), sw + min(kb0 + (lane >> 2), kb_end() - 1));
         cp_async_arrive(bar);
       }
     }
@@ -389,7 +409,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     const uint32_t tbase = tmem_base + (uint32_t(quarter * 32) << 16) + group * kHalf;
     uint32_t it = 0, tile_no = 0, slot_no = 0;
     uint8_t* staging = ctl->staging[warp - kFirstPromoWarp];
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++tile_no) {
+    for (int u = first_unit(); u < units; u += unit_stride(), ++tile_no) {
       int expert, row0, row_end, n_idx;
       decode(u, expert, row0, row_end, n_idx);
       const int n0 = n_idx * kTileN;
@@ -401,14 +421,14 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       uint64_t g2 = 0, u2 = 0;  // this block's scales of the group's first and second half of columns
       // the scales of block kb; the slot is handed back with its last block
       auto next_scales = [&](int kb) {
-        const int slot = slot_no % kScaleSlots, j = kb % kScaleKb;
+        const int slot = slot_no % kScaleSlots, j = (kb - kb_begin()) % kScaleKb;
         if (j == 0) {
           wait(&ctl->sfull[slot], (slot_no / kScaleSlots) & 1u);
           __syncwarp();
         }
         const float sa = ctl->s_row[slot][j][(row0 & 3) + row_in_tile];
         const float2 sw = *reinterpret_cast<const float2*>(&ctl->s_col[slot][j][2 * group]);
-        if (j == kScaleKb - 1 || kb == p.kb - 1) {
+        if (j == kScaleKb - 1 || kb == kb_end() - 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl->sempty[slot]));
           ++slot_no;
@@ -416,7 +436,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         g2 = pack_f32x2(sa * sw.x, sa * sw.x);
         u2 = kOut == kOutSwiglu ? pack_f32x2(sa * sw.y, sa * sw.y) : g2;
       };
-      for (int kb = 0; kb < p.kb; ++kb, ++it) {
+      for (int kb = kb_begin(); kb < kb_end(); ++kb, ++it) {
         constexpr int kChunks = kHalf / 32;
         const int b = it % kBufs;
         next_scales(kb);
@@ -434,6 +454,21 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           }
           add_scaled(acc + c * 16, part, 2 * c < kChunks ? g2 : u2);
         }
+      }
+      if constexpr (kSplit) {
+        // this slice's sums go to the CTAs that own their columns: [slice][column][row], so that a
+        // warp's stores are whole lines
+        const int own_log2 = ilog2(BN) - p.split_log2;
+        const uint32_t at = smem_u32(exchange) + row_in_tile * 4u;
+#pragma unroll
+        for (int j = 0; j < kHalf / 2; ++j) {
+          const int c = group * kHalf + 2 * j;
+          const uint32_t dst = map_to_rank(at, uint32_t(c) >> own_log2) +
+                               ((uint32_t(rank_of()) << own_log2) + (uint32_t(c) & ((1u << own_log2) - 1u))) * (BM * 4u);
+          st_cluster_u32(dst, uint32_t(acc[j]));
+          st_cluster_u32(dst + BM * 4u, uint32_t(acc[j] >> 32));
+        }
+        continue;
       }
       const bool store = *abort_flag == 0;
       // 64 bytes of each of the warp's 32 rows, from one row a lane to eight whole rows a store
@@ -530,13 +565,50 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     }
   }
 
+  if constexpr (kSplit) {
+    __syncwarp();
+    pair_sync();  // all threads of the cluster: every slice's sums have arrived
+    if (warp >= kFirstPromoWarp && first_unit() < units && *abort_flag == 0) {
+      // the owner adds the slices in order: two threads a row, half of the owned columns each
+      int expert, row0, row_end, n_idx;
+      decode(first_unit(), expert, row0, row_end, n_idx);
+      const int t = threadIdx.x - kFirstPromoWarp * 32, r = t % BM;
+      const int own = BN >> p.split_log2;
+      const int row = row0 + r;
+      if (row < row_end) {
+        for (int c = (t / BM) * (own / 2); c < (t / BM + 1) * (own / 2); c += 4) {
+          const int n = n_idx * kTileN + rank_of() * own + c;
+          if (n >= p.N) break;
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int k = 0; k < (1 << p.split_log2); ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += exchange[(k * own + c + i) * BM + r];
+          if constexpr (kOut == kOutF32) {  // ldy32: N rounded up to 4
+            *reinterpret_cast<float4*>(p.y32 + int64_t(row) * p.ldy32 + n) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (p.bias) v[i] += bf16_bits_to_float(__ldg(p.bias + min(n + i, p.N - 1)));
+            uint16_t* dst = p.y + int64_t(row) * p.ldy + n;
+            if (p.vec && n + 4 <= p.N) {
+              *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (n + i < p.N) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+            }
+          }
+        }
+      }
+    }
+  }
   __syncwarp();
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
   if (warp == 1) {
     __syncwarp();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem_base), "n"(Tile<BN>::cols)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem_base), "n"(Tile<BN, kSplit>::cols)
                  : "memory");
   }
 }
@@ -547,19 +619,46 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
 
 namespace {
 
-PerDeviceCache<const void*, int> g_attr_cache;
+PerDeviceCache<std::pair<const void*, int>, int> g_slot_cache;
 
-template <int BN, int kOut>
-bool launch_tile(const GemmArgs& a, int num_sms, cudaStream_t st) {
-  auto kfn = block_gemm_kernel<BN, kOut>;
-  int dev = 0, set = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  if (!g_attr_cache.get(dev, reinterpret_cast<const void*>(kfn), &set, [&](int* v) {
-        *v = 1;
-        return report_cuda(cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes)),
-                           "block gemm smem attribute") == cudaSuccess;
-      }))
-    return false;
+// CTAs of the kernel that run at once in clusters of `split`, its attributes set; 0: it cannot run.
+int slots_of(const void* kfn, int split, int num_sms) {
+  int dev = 0, slots = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  g_slot_cache.get(dev, std::make_pair(kfn, split), &slots, [&](int* v) {
+    if (report_cuda(cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemBytes)),
+                    "block gemm smem attribute") != cudaSuccess)
+      return false;
+    *v = num_sms;
+    if (split > 1) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kSmemBytes;
+      cfg.gridDim = dim3(split * 64);
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = split;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      if (report_cuda(cudaOccupancyMaxActiveClusters(&clusters, kfn, &cfg), "block gemm clusters") != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+      }
+      *v = clusters * split;
+    }
+    return true;
+  });
+  return slots;
+}
+
+template <int BN, int kOut, bool kSplit = false>
+bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
+  auto kfn = block_gemm_kernel<BN, kOut, kSplit>;
+  const int slots = slots_of(reinterpret_cast<const void*>(kfn), split, num_sms);
+  if (slots <= 0) return false;
   Params p = {};
   p.rows = int(a.rows);
   p.N = int(a.N);
@@ -569,6 +668,8 @@ bool launch_tile(const GemmArgs& a, int num_sms, cudaStream_t st) {
   p.bulk_scales = aligned(a.s_a, 16) && a.lds_a % 4 == 0;
   p.s_w = a.s_w;
   p.nb = int(blocks_of(a.N));
+  p.split_log2 = ilog2(split);
+  p.kb_slice = (p.kb + split - 1) / split;
   p.tiles = a.tiles;
   p.n_row_tiles = a.n_tiles;
   constexpr int kTileN = kOut == kOutSwiglu ? BN / 2 : BN;
@@ -594,20 +695,52 @@ bool launch_tile(const GemmArgs& a, int num_sms, cudaStream_t st) {
   if (!make_fp8_tensor_map(&ma, a.qa, a.rows, a.K, a.lda, BM) ||
       !make_fp8_tensor_map_3d(&mb, a.qw, a.mats, a.N, a.K, a.ldw, kOut == kOutSwiglu ? 64 : BN))
     return false;
-  const int grid = int(std::min<int64_t>(units, num_sms));
-  return launch(kfn, dim3(grid), dim3(kThreads), kSmemBytes, st, true, dim3(1, 1, 1), ma, mb, p) == FP8_OK;
+  // a split tile's cluster comes and goes with it; otherwise the CTAs stay and walk the tiles
+  const int64_t grid = kSplit ? units * split : std::min<int64_t>(units, slots);
+  return launch(kfn, dim3(unsigned(grid)), dim3(kThreads), kSmemBytes, st, true, dim3(split, 1, 1), ma, mb, p) == FP8_OK;
+}
+
+// Tile width and K split, by the time of the busiest CTA in us: waves of CTAs, each the blocks of its
+// K slice and about one for its start and end, and an exchange of sums where K is split. Measured on
+// a GB300: a block of a 128 x 64, 128 x 128 and 128 x 256 tile takes 0.30, 0.36 and 0.50.
+struct TileChoice {
+  int bn, split;
+};
+
+template <int kOut>
+TileChoice choose_tile(int64_t m_tiles, int64_t N, int64_t kb, int num_sms) {
+  TileChoice best = {256, 1};
+  double best_us = -1;
+  auto consider = [&](int bn, int split, int slots, double block_us) {
+    if (slots < split || (split > 1 && (kb + split - 1) / split * (split - 1) >= kb)) return;  // an empty slice
+    const int64_t units = m_tiles * ((N + bn - 1) / bn);
+    const int64_t waves = (units * split + slots - 1) / slots;
+    if (split > 1 && waves > 1) return;
+    const double us = double(waves) * (double((kb + split - 1) / split) * block_us + 1.0) + (split > 1 ? 1.2 : 0.0);
+    if (best_us < 0 || us < best_us) best = {bn, split}, best_us = us;
+  };
+  consider(256, 1, num_sms, 0.50);
+  consider(128, 1, num_sms, 0.36);
+  consider(64, 1, num_sms, 0.30);
+  for (int split = 2; split <= 8; split *= 2) {
+    consider(128, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<128, kOut, true>), split, num_sms), 0.36);
+    consider(64, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<64, kOut, true>), split, num_sms), 0.30);
+  }
+  return best;
 }
 
 template <int kOut>
 bool launch_any(const GemmArgs& a, int num_sms, cudaStream_t st) {
   if constexpr (kOut == kOutSwiglu) {
-    return launch_tile<256, kOut>(a, num_sms, st);
+    return launch_tile<256, kOut>(a, 1, num_sms, st);
   } else {
-    // the widest tile that still gives every SM one
     const int64_t m_tiles = a.tiles ? a.max_tiles : (a.rows + BM - 1) / BM;
-    if (m_tiles * ((a.N + 255) / 256) >= num_sms) return launch_tile<256, kOut>(a, num_sms, st);
-    if (m_tiles * ((a.N + 127) / 128) >= num_sms) return launch_tile<128, kOut>(a, num_sms, st);
-    return launch_tile<64, kOut>(a, num_sms, st);
+    const TileChoice c = choose_tile<kOut>(m_tiles, a.N, blocks_of(a.K), num_sms);
+    if (c.split > 1)
+      return c.bn == 128 ? launch_tile<128, kOut, true>(a, c.split, num_sms, st)
+                         : launch_tile<64, kOut, true>(a, c.split, num_sms, st);
+    if (c.bn == 256) return launch_tile<256, kOut>(a, 1, num_sms, st);
+    return c.bn == 128 ? launch_tile<128, kOut>(a, 1, num_sms, st) : launch_tile<64, kOut>(a, 1, num_sms, st);
   }
 }
 

@@ -101,8 +101,8 @@ __device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
 }
 
-// Every thread of both CTAs: barrier inits visible before the first remote signal, and no CTA
-// leaves while its peer may still write into its shared memory or arrive on its barriers.
+// Every thread of the cluster's CTAs: barrier inits visible before the first remote signal, and no
+// CTA leaves while a peer may still write into its shared memory or arrive on its barriers.
 __device__ __forceinline__ void pair_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -216,3 +216,10 @@ def test_wrapper_refusals():
     with pytest.raises(F.FP8Error) as e:
         F.fp8_block_linear(big, qw, s_w, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
     assert e.value.status == F.FP8_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("M,K,N", [(17, 640, 64), (40, 1152, 130), (100, 2049, 512), (129, 4096, 384), (200, 5632, 320),
+                                   (64, 14336, 256), (250, 1800, 1000)])
+def test_few_tiles_share_k(M, K, N):
+    """Shapes with few output tiles, whose K is divided among the CTAs of a cluster."""
+    run(M, K, N, seed=M, bias=True)
