@@ -22,13 +22,13 @@
 //   warp 2      scale loader: the rows' scales and the weight blocks' scales of kScaleKb K blocks a
 //               slot, by bulk copies and cp.async into a ring of its own (a load from L2 takes longer
 //               than a block, and the ring runs ahead over the ends of tiles).
-//   warps 4..11 promotion: two groups of four warps, each with half of the columns; a thread
-//               reads its row of the partial (tcgen05.ld, 32 columns at a time; a read and its wait
-//               take some 30 cycles, which the other warp of the scheduler fills, and keeping reads
-//               in flight behind the additions costs more in copied registers) and adds it, scaled,
-//               in registers. After the last K block the same threads write the tile out. Their 128
-//               accumulators and the read buffer need more registers than an even share, which the
-//               first warpgroup gives up.
+//   warps 4 on  promotion: warpgroups with 64 columns each (32 at BN = 64); a thread reads its row of
+//               the partial (tcgen05.ld, at most 32 columns at a time; a read and its wait take some
+//               30 cycles, which the scheduler's other warps fill, and keeping reads in flight behind
+//               the additions costs more in copied registers) and adds it, scaled, in registers.
+//               After the last K block the same threads write the tile out, a 32-byte sector a
+//               store. Four warpgroups of 64 columns keep four warps a scheduler busy: 16384 x 4096 x
+//               28672 in 1426 us (2.70 PFLOP/s; two warpgroups of 128 columns 1560).
 // Ragged sizes need no padding: TMA fills out-of-range rows and columns with zeros and the
 // stores are predicated.
 //
@@ -61,15 +61,12 @@ __device__ unsigned int g_block_gemm_error;
 
 constexpr int BM = kRowTile;
 constexpr int BK = kBlock;
-constexpr int kThreads = 384;
-constexpr int kPromoWarps = 8;
 constexpr int kFirstPromoWarp = 4;
 constexpr int kScaleKb = 4;     // K blocks of one slot of the scale ring
 constexpr int kScaleSlots = 4;
-constexpr int kStageBytes = 2048;  // a promotion warp's output staging: 32 rows of 64 bytes
-// 384 threads start with 168 registers each; 56 + 2 * 224 = 3 * 168
-constexpr int kLaunchRegs = 168, kIssueRegs = 56, kPromoRegs = 224;
-static_assert(kIssueRegs + 2 * kPromoRegs <= 3 * kLaunchRegs, "register shares of the three warpgroups");
+// 640 threads (BN = 256) start with 96 registers each; 64 + 4 * 104 = 5 * 96
+constexpr int kLaunchRegs = 96, kIssueRegs = 64, kPromoRegs = 104;
+static_assert(kIssueRegs + 4 * kPromoRegs <= 5 * kLaunchRegs, "register shares of the five warpgroups");
 constexpr uint32_t kABytes = BM * BK;
 constexpr uint32_t kRingBytes = 192 * 1024;
 constexpr int kMaxStages = 8;
@@ -83,6 +80,9 @@ struct Tile {
   static constexpr int stages = int((kRingBytes - exchange_bytes) / stage_bytes);  // 4, 6, 8 for BN = 256, 128, 64
   static constexpr int bufs = 512 / BN < kMaxBufs ? 512 / BN : kMaxBufs;
   static constexpr int cols = bufs * BN;  // tensor-memory columns (a power of two)
+  static constexpr int groups = BN == 256 ? 4 : 2;  // promotion warpgroups, BN / groups columns each
+  static constexpr int promo_warps = 4 * groups;
+  static constexpr int threads = 128 + 128 * groups;
   static_assert(stages <= kMaxStages, "ring");
 };
 
@@ -96,10 +96,9 @@ struct SharedCtl {
   int abort_flag;
   uint64_t sfull[kScaleSlots];
   uint64_t sempty[kScaleSlots];
-  uint32_t hmax[2][2][BM];  // SwiGLU: row maxima of the two column halves, by tile parity
+  uint32_t hmax[2][4][BM];  // SwiGLU: row maxima of the groups' columns, by tile parity
   alignas(16) float s_row[kScaleSlots][kScaleKb][BM + 4];  // from the tile's first row rounded down to 4
-  alignas(16) float s_col[kScaleSlots][kScaleKb][4];  // [promotion group][gate, up]
-  alignas(16) uint8_t staging[kPromoWarps][kStageBytes];
+  alignas(16) float s_col[kScaleSlots][kScaleKb][4];  // [half of the columns][gate, up]
 };
 constexpr size_t kSmemBytes = 1024 + kRingBytes + sizeof(SharedCtl);
 static_assert(kSmemBytes <= 232448, "ring and control block must fit the 227 KB per-block limit");
@@ -119,7 +118,7 @@ struct Params {
   const uint16_t* bias;
   uint16_t* y;
   int64_t ldy;
-  int vec;  // rows of the output are 16-byte aligned
+  int vec;  // alignment of the output's rows: 32, 16 or less bytes
   float* y32;
   int64_t ldy32;
   uint8_t* qh;
@@ -176,11 +175,29 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
 }
 
-// acc[0..15] += s2 * r (32 columns, in pairs).
-__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&r)[32], uint64_t s2) {
+// Reads 32 or 16 columns of this warp's tensor-memory lanes and waits for them.
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// acc += s2 * r (kN columns, in pairs).
+template <int kN>
+__device__ __forceinline__ void add_scaled(uint64_t* acc, const uint32_t (&r)[kN], uint64_t s2) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
+  for (int j = 0; j < kN / 2; ++j)
     acc[j] = fma_f32x2(pack_f32x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2, acc[j]);
+}
+
+__device__ __forceinline__ void st_global_v8(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
+                                             uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
 }
 
 // silu(g) * u in fp32; exp and the reciprocal by the hardware approximations (a few 2^-23), far
@@ -200,12 +217,16 @@ __device__ __forceinline__ uint32_t codes4(uint64_t p01, uint64_t p23, const Exa
 }
 
 template <int BN, int kOut, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Tile<BN, kSplit>::threads, 1)
 block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                   const __grid_constant__ Params p) {
   constexpr int kStages = Tile<BN, kSplit>::stages;
   constexpr int kBufs = Tile<BN, kSplit>::bufs;
-  constexpr int kHalf = BN / 2;                                    // columns of one promotion group
+  constexpr int kGroups = Tile<BN, kSplit>::groups;
+  constexpr int kPromoWarps = Tile<BN, kSplit>::promo_warps;
+  constexpr int kCols = BN / kGroups;                              // columns of one promotion group
+  constexpr int kChunk = kCols < 32 || kOut == kOutSwiglu ? 16 : 32;  // read at a time (SwiGLU: its second scale takes
+                                                                      // the registers of the other 16)
   constexpr int kTileN = kOut == kOutSwiglu ? BN / 2 : BN;         // output columns of a tile
   static_assert(kOut != kOutSwiglu || BN == 256, "a SwiGLU tile is one 128-wide block of h");
   static_assert(!kSplit || (kOut != kOutSwiglu && BN <= 128), "sums of K slices are linear outputs of narrow tiles");
@@ -306,7 +327,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           mbar_arrive_expect_tx(fb, Tile<BN, kSplit>::stage_bytes);
           tma_load_2d(dst, &tmap_a, fb, kb * BK, row0, pol);
           if (kOut == kOutSwiglu) {
-            // 64 columns of gate, then the same 64 of up, twice: each promotion group holds both
+            // 64 columns of gate, then the same 64 of up, twice
 #pragma unroll
             for (int h = 0; h < 4; ++h)
               tma_load_3d(dst + kABytes + h * (64 * BK), &tmap_b, fb, kb * BK, n0 + (h >> 1) * 64, 2 * expert + (h & 1),
@@ -359,9 +380,9 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       int expert, row0, row_end, n_idx;
       decode(u, expert, row0, row_end, n_idx);
       const int n0 = n_idx * kTileN;
-      // lane % 4: the weight scale row of (promotion group, matrix)
+      // lane % 4: the weight scale row of (half of the columns, matrix)
       const int mat = kOut == kOutSwiglu ? 2 * expert + (lane & 1) : expert;
-      const int col = kOut == kOutSwiglu ? n0 : n0 + ((lane >> 1) & 1) * kHalf;
+      const int col = kOut == kOutSwiglu ? n0 : n0 + ((lane >> 1) & 1) * (BN / 2);
       const float* sw = p.s_w + (int64_t(mat) * p.nb + min(col / kBlock, p.nb - 1)) * p.kb;
       for (int kb0 = kb_begin(); kb0 < kb_end(); kb0 += kScaleKb, ++slot_no) {
         const int slot = slot_no % kScaleSlots;
@@ -401,23 +422,25 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     asm volatile("cp.async.wait_all;" ::: "memory");
    }
   } else {
-    // ---------------- promotion and epilogue: warps 4..11 ----------------
+    // ---------------- promotion and epilogue: warps 4 on ----------------
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kPromoRegs));
-    const int group = (warp - kFirstPromoWarp) >> 2;  // column half
+    const int group = (warp - kFirstPromoWarp) >> 2;  // of columns
     const int quarter = warp & 3;        // tensor-memory lanes this warp may access
     const int row_in_tile = quarter * 32 + lane;
-    const uint32_t tbase = tmem_base + (uint32_t(quarter * 32) << 16) + group * kHalf;
+    // first column of the group, and from one 32-column read to the next (SwiGLU: 32 columns of gate
+    // and the same 32 of up, 64 on)
+    const uint32_t tbase = tmem_base + (uint32_t(quarter * 32) << 16) +
+                           (kOut == kOutSwiglu ? (group >> 1) * 128 + (group & 1) * 32 : group * kCols);
     uint32_t it = 0, tile_no = 0, slot_no = 0;
-    uint8_t* staging = ctl->staging[warp - kFirstPromoWarp];
     for (int u = first_unit(); u < units; u += unit_stride(), ++tile_no) {
       int expert, row0, row_end, n_idx;
       decode(u, expert, row0, row_end, n_idx);
       const int n0 = n_idx * kTileN;
       const int row = row0 + row_in_tile;
       const bool live = row < row_end;
-      uint64_t acc[kHalf / 2];
+      uint64_t acc[kCols / 2];
 #pragma unroll
-      for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
       uint64_t g2 = 0, u2 = 0;  // this block's scales of the group's first and second half of columns
       // the scales of block kb; the slot is handed back with its last block
       auto next_scales = [&](int kb) {
@@ -427,7 +450,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           __syncwarp();
         }
         const float sa = ctl->s_row[slot][j][(row0 & 3) + row_in_tile];
-        const float2 sw = *reinterpret_cast<const float2*>(&ctl->s_col[slot][j][2 * group]);
+        const float2 sw = *reinterpret_cast<const float2*>(&ctl->s_col[slot][j][2 * (group / (kGroups / 2))]);
         if (j == kScaleKb - 1 || kb == kb_end() - 1) {
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl->sempty[slot]));
@@ -437,7 +460,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         u2 = kOut == kOutSwiglu ? pack_f32x2(sa * sw.y, sa * sw.y) : g2;
       };
       for (int kb = kb_begin(); kb < kb_end(); ++kb, ++it) {
-        constexpr int kChunks = kHalf / 32;
+        constexpr int kChunks = kCols / kChunk;
         const int b = it % kBufs;
         next_scales(kb);
         wait(&ctl->tfull[b], (it / kBufs) & 1u);
@@ -446,13 +469,13 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         const uint32_t tempty = smem_u32(&ctl->tempty[b]);
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          uint32_t part[32];
-          tmem_ld32(tbase + b * BN + c * 32, part);
+          uint32_t part[kChunk];
+          tmem_read(tbase + b * BN + (kOut == kOutSwiglu ? (c >> 1) * 64 + (c & 1) * 16 : c * kChunk), part);
           if (c == kChunks - 1) {  // the last read has landed: the buffer is free before its columns are added
             tmem_fence_before();
             arrive_if(tempty, lane == 0);
           }
-          add_scaled(acc + c * 16, part, 2 * c < kChunks ? g2 : u2);
+          add_scaled(acc + c * (kChunk / 2), part, 2 * c < kChunks ? g2 : u2);
         }
       }
       if constexpr (kSplit) {
@@ -461,8 +484,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         const int own_log2 = ilog2(BN) - p.split_log2;
         const uint32_t at = smem_u32(exchange) + row_in_tile * 4u;
 #pragma unroll
-        for (int j = 0; j < kHalf / 2; ++j) {
-          const int c = group * kHalf + 2 * j;
+        for (int j = 0; j < kCols / 2; ++j) {
+          const int c = group * kCols + 2 * j;
           const uint32_t dst = map_to_rank(at, uint32_t(c) >> own_log2) +
                                ((uint32_t(rank_of()) << own_log2) + (uint32_t(c) & ((1u << own_log2) - 1u))) * (BM * 4u);
           st_cluster_u32(dst, uint32_t(acc[j]));
@@ -471,95 +494,87 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         continue;
       }
       const bool store = *abort_flag == 0;
-      // 64 bytes of each of the warp's 32 rows, from one row a lane to eight whole rows a store
-      // instruction: through shared memory, the 16-byte pieces of a row exchanged by (row / 2) % 4
-      // so that neither side has bank conflicts
-      const int warp_row0 = row0 + quarter * 32;
-      auto put_row_piece = [&](int c, uint4 v) {
-        *reinterpret_cast<uint4*>(staging + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16)) = v;
-      };
-      auto for_pieces = [&](auto&& write) {  // write(row, piece of the 64 bytes, its 16 bytes)
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i * 8 + (lane >> 2), c = lane & 3;
-          const uint4 v = *reinterpret_cast<const uint4*>(staging + r * 64 + ((c ^ ((r >> 1) & 3)) * 16));
-          if (store && warp_row0 + r < row_end) write(warp_row0 + r, c, v);
-        }
-        __syncwarp();
-      };
+      // each thread writes its row's columns, a 32-byte sector a store
       if constexpr (kOut == kOutSwiglu) {
-        // columns [64 group, 64 group + 64) of the tile's 128-wide block of h
+        // columns [32 group, 32 group + 32) of the tile's 128-wide block of h
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float h0 = swiglu(lo_of(acc[j]), lo_of(acc[32 + j])), h1 = swiglu(hi_of(acc[j]), hi_of(acc[32 + j]));
+        for (int j = 0; j < 16; ++j) {
+          const float h0 = swiglu(lo_of(acc[j]), lo_of(acc[16 + j])), h1 = swiglu(hi_of(acc[j]), hi_of(acc[16 + j]));
           m = max(m, max(__float_as_uint(fabsf(h0)), __float_as_uint(fabsf(h1))));  // keeps a NaN
           acc[j] = pack_f32x2(h0, h1);
         }
         ctl->hmax[tile_no & 1][group][row_in_tile] = m;
-        // the two warps that hold the halves of the same 32 rows meet; two tiles' maxima alternate,
-        // so one meeting a tile is enough
-        asm volatile("bar.sync %0, 64;" :: "r"(1 + quarter) : "memory");
-        m = max(m, ctl->hmax[tile_no & 1][group ^ 1][row_in_tile]);
+        // the warps that hold the same 32 rows meet; two tiles' maxima alternate, so one meeting a
+        // tile is enough
+        asm volatile("bar.sync %0, %1;" :: "r"(1 + quarter), "n"(32 * kGroups) : "memory");
+#pragma unroll
+        for (int o = 0; o < kGroups; ++o) m = max(m, ctl->hmax[tile_no & 1][o][row_in_tile]);
         const float s = scale_from_amax<kFmtE4M3>(__uint_as_float(m));
         const ExactScale k = make_exact_scale(s);
+        if (store && live) {
+          uint32_t w[8];
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          put_row_piece(v, make_uint4(codes4(acc[v * 8], acc[v * 8 + 1], k, s), codes4(acc[v * 8 + 2], acc[v * 8 + 3], k, s),
-                                      codes4(acc[v * 8 + 4], acc[v * 8 + 5], k, s),
-                                      codes4(acc[v * 8 + 6], acc[v * 8 + 7], k, s)));
-        for_pieces([&](int r, int c, uint4 v) {
-          const int col = n0 + group * 64 + c * 16;  // columns past N hold zeros (zero weight rows)
-          if (col < p.ldh) *reinterpret_cast<uint4*>(p.qh + int64_t(r) * p.ldh + col) = v;
-        });
-        if (store && live && group == 0) p.s_h[int64_t(n_idx) * p.lds_h + row] = s;
+          for (int v = 0; v < 8; ++v) w[v] = codes4(acc[v * 2], acc[v * 2 + 1], k, s);
+          const int col = n0 + group * 32;  // columns past N hold zeros (zero weight rows)
+          uint8_t* dst = p.qh + int64_t(row) * p.ldh + col;
+          if (col < p.ldh) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (col + 16 < p.ldh) *reinterpret_cast<uint4*>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+          if (group == 0) p.s_h[int64_t(n_idx) * p.lds_h + row] = s;
+        }
       } else if constexpr (kOut == kOutF32) {
+        const int col0 = n0 + group * kCols;
+        float* dst = p.y32 + int64_t(row) * p.ldy32 + col0;
+        if (store && live) {
 #pragma unroll
-        for (int q = 0; q < kHalf / 16; ++q) {
-          const int col0 = n0 + group * kHalf + q * 16;
-          if (col0 >= p.ldy32) break;  // ldy32: N rounded up to 4
+          for (int q = 0; q < kCols / 8; ++q) {
+            const uint64_t* a = acc + q * 4;
+            if (p.vec >= 32 && col0 + q * 8 + 8 <= p.ldy32) {
+              st_global_v8(dst + q * 8, uint32_t(a[0]), uint32_t(a[0] >> 32), uint32_t(a[1]), uint32_t(a[1] >> 32),
+                           uint32_t(a[2]), uint32_t(a[2] >> 32), uint32_t(a[3]), uint32_t(a[3] >> 32));
+            } else {  // ldy32: N rounded up to 4
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const uint64_t a0 = acc[q * 8 + 2 * v], a1 = acc[q * 8 + 2 * v + 1];
-            put_row_piece(v, make_uint4(uint32_t(a0), uint32_t(a0 >> 32), uint32_t(a1), uint32_t(a1 >> 32)));
+              for (int i = 0; i < 2; ++i)
+                if (col0 + q * 8 + i * 4 < p.ldy32)
+                  *reinterpret_cast<float4*>(dst + q * 8 + i * 4) =
+                      make_float4(lo_of(a[2 * i]), hi_of(a[2 * i]), lo_of(a[2 * i + 1]), hi_of(a[2 * i + 1]));
+            }
           }
-          for_pieces([&](int r, int c, uint4 v) {
-            if (col0 + c * 4 < p.ldy32) *reinterpret_cast<uint4*>(p.y32 + int64_t(r) * p.ldy32 + col0 + c * 4) = v;
-          });
         }
       } else {
+        const int col0 = n0 + group * kCols;
+        uint16_t* dst = p.y + int64_t(row) * p.ldy + col0;
+        if (store && live) {
 #pragma unroll
-        for (int q = 0; q < kHalf / 32; ++q) {
-          const int col0 = n0 + group * kHalf + q * 32;
-          if (col0 >= p.N) break;
+          for (int q = 0; q < kCols / 16; ++q) {
+            const int col = col0 + q * 16;
+            uint32_t w[8];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            float o[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint64_t a = acc[q * 16 + v * 4 + j];
-              o[2 * j] = lo_of(a), o[2 * j + 1] = hi_of(a);
+            for (int j = 0; j < 8; ++j) {
+              const uint64_t a = acc[q * 8 + j];
+              float lo = lo_of(a), hi = hi_of(a);
+              if (p.bias) {
+                lo += bf16_bits_to_float(__ldg(p.bias + min(col + 2 * j, p.N - 1)));
+                hi += bf16_bits_to_float(__ldg(p.bias + min(col + 2 * j + 1, p.N - 1)));
+              }
+              w[j] = pack_bf16x2(lo, hi);
             }
-            if (p.bias) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] += bf16_bits_to_float(__ldg(p.bias + min(col0 + v * 8 + j, p.N - 1)));
-            }
-            put_row_piece(v, make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                        pack_bf16x2(o[6], o[7])));
-          }
-          for_pieces([&](int r, int c, uint4 v) {
-            const int col = col0 + c * 8;
-            uint16_t* dst = p.y + int64_t(r) * p.ldy + col;
-            if (p.vec && col + 8 <= p.N) {
-              *reinterpret_cast<uint4*>(dst) = v;
+            if (p.vec >= 32 && col + 16 <= p.N) {
+              st_global_v8(dst + q * 16, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
             } else {
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (col + j < p.N) dst[j] = uint16_t(w[j >> 1] >> ((j & 1) * 16));
+              for (int h = 0; h < 2; ++h) {
+                if (p.vec >= 16 && col + h * 8 + 8 <= p.N) {
+                  *reinterpret_cast<uint4*>(dst + q * 16 + h * 8) =
+                      make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j)
+                    if (col + h * 8 + j < p.N) dst[q * 16 + h * 8 + j] = uint16_t(w[4 * h + (j >> 1)] >> ((j & 1) * 16));
+                }
+              }
             }
-          });
+          }
         }
       }
     }
@@ -590,7 +605,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
             for (int i = 0; i < 4; ++i)
               if (p.bias) v[i] += bf16_bits_to_float(__ldg(p.bias + min(n + i, p.N - 1)));
             uint16_t* dst = p.y + int64_t(row) * p.ldy + n;
-            if (p.vec && n + 4 <= p.N) {
+            if (p.vec >= 16 && n + 4 <= p.N) {
               *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
             } else {
 #pragma unroll
@@ -622,7 +637,7 @@ namespace {
 PerDeviceCache<std::pair<const void*, int>, int> g_slot_cache;
 
 // CTAs of the kernel that run at once in clusters of `split`, its attributes set; 0: it cannot run.
-int slots_of(const void* kfn, int split, int num_sms) {
+int slots_of(const void* kfn, int threads, int split, int num_sms) {
   int dev = 0, slots = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   g_slot_cache.get(dev, std::make_pair(kfn, split), &slots, [&](int* v) {
@@ -632,7 +647,7 @@ int slots_of(const void* kfn, int split, int num_sms) {
     *v = num_sms;
     if (split > 1) {
       cudaLaunchConfig_t cfg = {};
-      cfg.blockDim = dim3(kThreads);
+      cfg.blockDim = dim3(unsigned(threads));
       cfg.dynamicSmemBytes = kSmemBytes;
       cfg.gridDim = dim3(split * 64);
       cudaLaunchAttribute attr[1];
@@ -657,7 +672,7 @@ int slots_of(const void* kfn, int split, int num_sms) {
 template <int BN, int kOut, bool kSplit = false>
 bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
   auto kfn = block_gemm_kernel<BN, kOut, kSplit>;
-  const int slots = slots_of(reinterpret_cast<const void*>(kfn), split, num_sms);
+  const int slots = slots_of(reinterpret_cast<const void*>(kfn), Tile<BN, kSplit>::threads, split, num_sms);
   if (slots <= 0) return false;
   Params p = {};
   p.rows = int(a.rows);
@@ -682,13 +697,15 @@ bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
   p.bias = a.bias;
   p.y = a.y;
   p.ldy = a.ldy;
-  p.vec = aligned(a.y, 16) && a.ldy % 8 == 0;
   p.y32 = a.y32;
   p.ldy32 = a.ldy32;
   p.qh = a.qh;
   p.ldh = a.ldh;
   p.s_h = a.s_h;
   p.lds_h = a.lds_h;
+  const void* out = kOut == kOutF32 ? static_cast<const void*>(a.y32) : a.y;
+  const int64_t out_ld = kOut == kOutF32 ? a.ldy32 * 4 : a.ldy * 2;
+  p.vec = aligned(out, 32) && out_ld % 32 == 0 ? 32 : aligned(out, 16) && out_ld % 16 == 0 ? 16 : 0;
   const int64_t units = (a.tiles ? a.max_tiles : int64_t(p.m_tiles)) * p.n_tiles;
   if (units > kMaxDim) return false;
   CUtensorMap ma, mb;
@@ -697,7 +714,7 @@ bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
     return false;
   // a split tile's cluster comes and goes with it; otherwise the CTAs stay and walk the tiles
   const int64_t grid = kSplit ? units * split : std::min<int64_t>(units, slots);
-  return launch(kfn, dim3(unsigned(grid)), dim3(kThreads), kSmemBytes, st, true, dim3(split, 1, 1), ma, mb, p) == FP8_OK;
+  return launch(kfn, dim3(unsigned(grid)), dim3(Tile<BN, kSplit>::threads), kSmemBytes, st, true, dim3(split, 1, 1), ma, mb, p) == FP8_OK;
 }
 
 // Tile width and K split, by the time of the busiest CTA in us: waves of CTAs, each the blocks of its
@@ -723,8 +740,8 @@ TileChoice choose_tile(int64_t m_tiles, int64_t N, int64_t kb, int num_sms) {
   consider(128, 1, num_sms, 0.36);
   consider(64, 1, num_sms, 0.30);
   for (int split = 2; split <= 8; split *= 2) {
-    consider(128, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<128, kOut, true>), split, num_sms), 0.36);
-    consider(64, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<64, kOut, true>), split, num_sms), 0.30);
+    consider(128, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<128, kOut, true>), Tile<128, true>::threads, split, num_sms), 0.36);
+    consider(64, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<64, kOut, true>), Tile<64, true>::threads, split, num_sms), 0.30);
   }
   return best;
 }
