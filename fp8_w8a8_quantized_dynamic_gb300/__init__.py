@@ -398,34 +398,34 @@ def _out_bf16(out, M: int, N: int, like):
     return out
 
 
-def _check_dense(t, dtype, shape, device, name: str):
-    """A gap-free tensor of this dtype and shape on this device."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+def _check_dense(t, dtype, shape, index: int, name: str):
+    """A gap-free tensor of this dtype and shape on CUDA device `index`."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
 
 
-def _check_block_weight(qw, s_w, lead: tuple, N: int, K: int, device, name: str) -> int:
+def _check_block_weight(qw, s_w, lead: tuple, N: int, K: int, index: int, name: str) -> int:
     """Codes [*lead, N, ld] and scales [*lead, blocks of N, blocks of K] as fp8_block_quantize_weight returns
     them; returns ld."""
     torch = _torch()
     ld = qw.shape[-1]
     if ld < K or ld % 16 or ld == 0:
         raise ValueError(f"{name}: expected uint8 codes [..., N, ld] with ld a multiple of 16 and at least {K}")
-    _check_dense(qw, torch.uint8, (*lead, N, ld), device, name)
-    _check_dense(s_w, torch.float32, (*lead, (N + 127) // 128, (K + 127) // 128), device, name + " scales")
+    _check_dense(qw, torch.uint8, (*lead, N, ld), index, name)
+    _check_dense(s_w, torch.float32, (*lead, (N + 127) // 128, (K + 127) // 128), index, name + " scales")
     return ld
 
 
-def _scratch(ws, need: int, device):
+def _scratch(ws, need: int, like):
     """(address, bytes, tensor) of the caller's workspace, or of a fresh one (none where none is needed)."""
     torch = _torch()
     if ws is None:
         if not need:
             return None, 0, None
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
         return ws.data_ptr(), need, ws
-    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device:
-        raise ValueError(f"ws: expected a contiguous uint8 tensor on {device}")
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != like.device:
+        raise ValueError(f"ws: expected a contiguous uint8 tensor on {like.device}")
     return ws.data_ptr(), ws.numel(), ws
 
 
@@ -448,14 +448,16 @@ def fp8_block_quantize_weight(w):
 
 
 def fp8_block_quantize_act(a):
-    """A bf16 [M, K] -> (qA uint8 [M, min_ld(K)], s_a fp32 [ceil(K/128), M]): one scale per row and 128 columns."""
+    """A bf16 [M, K] -> (qA uint8 [M, min_ld(K)], s_a fp32 [ceil(K/128), M]): one scale per row and 128 columns.
+    The rows of s_a start on 16-byte boundaries (the product copies them in whole pieces)."""
     torch = _torch()
     _check_bf16_2d(a, "a")
     M, K = a.shape
     qa = torch.empty((M, min_ld(K)), dtype=torch.uint8, device=a.device)
-    s_a = torch.empty((_blocks(K), M), dtype=torch.float32, device=a.device)
+    s_a = torch.empty((_blocks(K), (M + 3) // 4 * 4), dtype=torch.float32, device=a.device)[:, :M]
     _check(lib().fp8_block_quantize_act(a.data_ptr(), M, K, max(a.stride(0), K, 1), qa.data_ptr(), qa.stride(0),
-                                        s_a.data_ptr(), max(M, 1), _stream_ptr(a)), "fp8_block_quantize_act")
+                                        s_a.data_ptr(), max(s_a.stride(0), 1), _stream_ptr(a)),
+           "fp8_block_quantize_act")
     return qa, s_a
 
 
@@ -463,14 +465,14 @@ def fp8_block_scaled_mm(qa, K: int, s_a, qw, s_w, bias=None, out=None):
     """The block-scaled product on already-quantized operands (fp8_block_quantize_act / _weight), bf16 out."""
     torch = _torch()
     _check_fp8_2d(qa, K, "qa")
-    M, N, device = qa.shape[0], qw.shape[-2], qa.device
-    if s_a.dtype != torch.float32 or s_a.shape != (_blocks(K), M) or s_a.device != device or (
+    M, N, index = qa.shape[0], qw.shape[-2], qa.get_device()
+    if s_a.dtype != torch.float32 or s_a.shape != (_blocks(K), M) or s_a.get_device() != index or (
             s_a.numel() and s_a.stride(1) != 1):
         raise ValueError(f"s_a: expected fp32 [{_blocks(K)}, {M}] with unit column stride")
-    ld = _check_block_weight(qw, s_w, (), N, K, device, "qw")
+    ld = _check_block_weight(qw, s_w, (), N, K, index, "qw")
     if bias is not None:
-        _check_dense(bias, torch.bfloat16, (N,), device, "bias")
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=device) if out is None else _out_bf16(out, M, N, qa)
+        _check_dense(bias, torch.bfloat16, (N,), index, "bias")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device) if out is None else _out_bf16(out, M, N, qa)
     _check(lib().fp8_block_scaled_mm(qa.data_ptr(), M, K, qa.stride(0), s_a.data_ptr(),
                                      max(s_a.stride(0), M, 1) if s_a.shape[0] > 1 else max(M, 1), qw.data_ptr(), N,
                                      ld, s_w.data_ptr(), _ptr(bias), y.data_ptr(), max(y.stride(0), N, 1),
@@ -485,18 +487,30 @@ def fp8_block_workspace_bytes(M: int, K: int, N: int) -> int:
 def fp8_block_linear(a, qw, s_w, bias=None, out=None, ws=None):
     """Block-scaled W8A8 linear, Y = A W^T (+ bias) in bf16: A is quantized with a scale per row and 128 columns,
     qw, s_w come from fp8_block_quantize_weight."""
-    _check_bf16_2d(a, "a")
+    # a decode step's calls are as short as the checks around them: each tensor is asked once
+    torch = _torch_module or _torch()
+    if a.dtype is not torch.bfloat16 or a.dim() != 2 or not a.is_cuda:
+        raise ValueError("a: expected a CUDA bf16 matrix with unit column stride")
     M, K = a.shape
-    N, device = qw.shape[-2], a.device
-    ld = _check_block_weight(qw, s_w, (), N, K, device, "qw")
+    lda, unit = a.stride()
+    if unit != 1:
+        raise ValueError("a: expected a CUDA bf16 matrix with unit column stride")
+    index = a.get_device()
+    N = qw.shape[-2]
+    ld = _check_block_weight(qw, s_w, (), N, K, index, "qw")
     if bias is not None:
-        _check_dense(bias, a.dtype, (N,), device, "bias")
-    y = _out_bf16(out, M, N, a)
-    L = lib()
-    wp, wn, ws = _scratch(ws, L.fp8_block_workspace_bytes(M, K, N), device)
-    status = L.fp8_block_linear(a.data_ptr(), M, K, max(a.stride(0), K, 1), qw.data_ptr(), N, ld, s_w.data_ptr(),
-                                None if bias is None else bias.data_ptr(), y.data_ptr(), max(y.stride(0), N, 1), wp,
-                                wn, _stream_ptr(a))
+        _check_dense(bias, torch.bfloat16, (N,), index, "bias")
+    L = _lib or lib()
+    need = L.fp8_block_workspace_bytes(M, K, N)
+    wp, wn, ws = _scratch(ws, need, a) if need or ws is not None else (None, 0, None)
+    if out is None:
+        y, ldy = torch.empty((M, N), dtype=torch.bfloat16, device=a.device), N
+    else:
+        y = _out_bf16(out, M, N, a)
+        ldy = y.stride(0)
+    status = L.fp8_block_linear(a.data_ptr(), M, K, lda if lda > K else K or 1, qw.data_ptr(), N, ld, s_w.data_ptr(),
+                                None if bias is None else bias.data_ptr(), y.data_ptr(), ldy if ldy > N else N or 1,
+                                wp, wn, _stream_ptr(a))
     if status:
         raise FP8Error(status, "fp8_block_linear")
     return y
@@ -510,25 +524,28 @@ def fp8_moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int
     """Logits [T, E] (fp32 or bf16) -> (ids int32 [T, k], weights fp32 [T, k]): the k chosen experts of each
     token in descending order and their routing weights. score 'softmax' or 'sigmoid'; bias fp32 [E] steers the
     choice only; only the keep_groups best of `groups` groups of experts take part (default: all)."""
-    torch = _torch()
-    dtype = logits.dtype
-    if (dtype != torch.float32 and dtype != torch.bfloat16) or logits.dim() != 2 or not logits.is_cuda or (
-            logits.shape[1] > 1 and logits.stride(1) != 1):
+    torch = _torch_module or _torch()
+    bf16 = logits.dtype is torch.bfloat16
+    if not (bf16 or logits.dtype is torch.float32) or logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits: expected a CUDA fp32 or bf16 matrix with unit column stride")
-    if score not in _SCORES:
-        raise ValueError(f"unknown score {score!r} (expected 'softmax' or 'sigmoid')")
     T, E = logits.shape
-    device = logits.device
+    ld, unit = logits.stride()
+    if unit != 1 and E > 1:
+        raise ValueError("logits: expected a CUDA fp32 or bf16 matrix with unit column stride")
+    kind = _SCORES.get(score)
+    if kind is None:
+        raise ValueError(f"unknown score {score!r} (expected 'softmax' or 'sigmoid')")
     if bias is not None:
-        _check_dense(bias, torch.float32, (E,), device, "bias")
+        _check_dense(bias, torch.float32, (E,), logits.get_device(), "bias")
     if k < 1:
         raise ValueError(f"k: expected at least 1, got {k}")
+    device = logits.device
     ids = torch.empty((T, k), dtype=torch.int32, device=device)
     weights = torch.empty((T, k), dtype=torch.float32, device=device)
-    status = lib().fp8_moe_route(logits.data_ptr(), dtype == torch.bfloat16, T, E, max(logits.stride(0), E),
-                                 _SCORES[score], None if bias is None else bias.data_ptr(), groups,
-                                 groups if keep_groups is None else keep_groups, k, bool(renormalize), factor,
-                                 ids.data_ptr(), weights.data_ptr(), _stream_ptr(logits))
+    status = (_lib or lib()).fp8_moe_route(
+        logits.data_ptr(), bf16, T, E, ld if ld > E else E, kind, None if bias is None else bias.data_ptr(), groups,
+        groups if keep_groups is None else keep_groups, k, 1 if renormalize else 0, factor, ids.data_ptr(),
+        weights.data_ptr(), _stream_ptr(logits))
     if status:
         raise FP8Error(status, "fp8_moe_route")
     return ids, weights
@@ -543,20 +560,20 @@ def fp8_moe_experts(x, ids, weights, qw13, s13, qw2, s2, out=None, ws=None):
 
     x bf16 [T, H]; ids int32 and weights fp32 [T, k] (fp8_moe_route; ids outside [0, E) contribute nothing);
     qw13, s13 from fp8_block_quantize_weight of [E, 2, I, H] (gate, up), qw2, s2 of [E, H, I]."""
-    torch = _torch()
+    torch = _torch_module or _torch()
     _check_bf16_2d(x, "x")
     T, H = x.shape
     if ids.dim() != 2 or qw13.dim() != 4:
         raise ValueError("expected ids [T, k] and qw13 [E, 2, I, ld]")
     E, _, I, _ = qw13.shape
-    k, device = ids.shape[1], x.device
-    _check_dense(ids, torch.int32, (T, k), device, "ids")
-    _check_dense(weights, torch.float32, (T, k), device, "weights")
-    ld13 = _check_block_weight(qw13, s13, (E, 2), I, H, device, "qw13")
-    ld2 = _check_block_weight(qw2, s2, (E,), H, I, device, "qw2")
+    k, index = ids.shape[1], x.get_device()
+    _check_dense(ids, torch.int32, (T, k), index, "ids")
+    _check_dense(weights, torch.float32, (T, k), index, "weights")
+    ld13 = _check_block_weight(qw13, s13, (E, 2), I, H, index, "qw13")
+    ld2 = _check_block_weight(qw2, s2, (E,), H, I, index, "qw2")
+    L = _lib or lib()
+    wp, wn, ws = _scratch(ws, L.fp8_moe_workspace_bytes(T, k, E, H, I), x)
     y = _out_bf16(out, T, H, x)
-    L = lib()
-    wp, wn, ws = _scratch(ws, L.fp8_moe_workspace_bytes(T, k, E, H, I), device)
     status = L.fp8_moe_experts(x.data_ptr(), T, H, max(x.stride(0), H, 1), ids.data_ptr(), weights.data_ptr(), k,
                                qw13.data_ptr(), ld13, s13.data_ptr(), qw2.data_ptr(), ld2, s2.data_ptr(), E, I,
                                y.data_ptr(), max(y.stride(0), H, 1), wp, wn, _stream_ptr(x))
