@@ -5,7 +5,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 #include <cstdint>
 
 #include "api_common.h"
@@ -58,8 +57,15 @@ struct Carver {
   }
 };
 
-// Few rows: one kernel quantizes A and streams the weights.
-bool linear_fused(int64_t M, int64_t K) { return block::gemv_fits(M, K, 1) && block::gemv_quantizes(M, K); }
+// Whether the GEMV takes a dense product. Its CTAs each bring in their K slices of A, so its time grows
+// with M * K and the GEMM's does not; graph replays, in us, GEMV and GEMM: M 8 K 4096 N 6144 11.4 and
+// 13.7, M 12 15.5 and 13.9; M 8 K 5632 N 2048 10.6 and 10.8, M 12 15.1 and 10.8; M 4 K 14336 N 4096 18.0
+// and 21.1, M 8 24.5 and 21.5; M 16 K 2048 N 2048 7.8 and 7.9, K 1000 N 1027 6.0 and 9.7.
+bool uses_gemv(int64_t M, int64_t K) {
+  return block::gemv_fits(M, K, 1) && (M <= 4 || M * K <= 40 * 1024);
+}
+// One kernel quantizes A and streams the weights.
+bool linear_fused(int64_t M, int64_t K) { return uses_gemv(M, K) && block::gemv_quantizes(M, K); }
 
 // Workspace of fp8_block_linear: codes of A, then its scales; none when one kernel does both.
 struct LinearWs {
@@ -80,7 +86,7 @@ LinearWs linear_ws(int64_t M, int64_t K) {
 fp8_status block_mm(const uint8_t* qa, int64_t M, int64_t K, int64_t ldqa, const float* s_a, int64_t lds_a,
                     const uint8_t* qw, int64_t N, int64_t ldqw, const float* s_w, const void* bias, void* y,
                     int64_t ldy, int sms, cudaStream_t st) {
-  if (block::gemv_fits(M, K, 1)) {
+  if (uses_gemv(M, K)) {
     block::GemvArgs v = {};
     v.src = block::kSrcCodes;
     v.a = qa;
@@ -143,75 +149,61 @@ fp8_status check_product(int64_t M, int64_t K, const uint8_t* qw, int64_t N, int
   return FP8_OK;
 }
 
-// How the experts of P = T * k pairs run, by the rows an expert has on average:
-//   one token: a GEMV over the pairs for h, one over all of their h for y (two launches);
-//   few rows:  sort, GEMV for h, GEMV for the pairs' rows, weighted sum;
-//   more:      sort, quantize, two tensor-core products, weighted sum.
-enum class MoePath { kOneToken, kGemv, kGemm };
-
-struct MoePlan {
-  MoePath path;
-  int tile_rows;
-};
-
-MoePlan moe_plan(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
-  const int64_t pairs = T * k;
-  if (T == 1 && block::gemv_fits(1, H, 2) && block::gemv_fits(1, k * blocks_of(I) * block::kBlock, 1))
-    return {MoePath::kOneToken, 1};
-  const int rows = pairs <= 4 * E ? 8 : 16;
-  if (pairs <= 12 * E && block::gemv_fits(rows, H, 2) && block::gemv_fits(rows, I, 1)) return {MoePath::kGemv, rows};
-  return {MoePath::kGemm, block::kRowTile};
+// How the experts run. One token: a GEMV over its pairs for h, one over all of their h for y (two
+// launches). More: sort the pairs, quantize, two tensor-core products, weighted sum (five). Experts of
+// 2048 x 1408, 8 of 64 a token: one token 29 us (36 as sorted pairs), 16 tokens 97 us (104 as GEMVs
+// over sorted pairs, which are not kept).
+bool one_token(int64_t T, int64_t k, int64_t H, int64_t I) {
+  return T == 1 && block::gemv_fits(1, H, 2) && block::gemv_fits(1, k * blocks_of(I) * block::kBlock, 1);
 }
 
 // CTAs that sort the pairs; more than one need their counts first.
 int plan_ctas(int64_t pairs) {
-  if (pairs <= 4 * moe::kPlanPairs) return 1;  // a second launch costs more than it saves
+  if (pairs <= 2 * moe::kPlanPairs) return 1;  // a second launch costs more than it saves
   return int(std::min<int64_t>(moe::kPlanMaxCtas, (pairs + moe::kPlanPairs - 1) / moe::kPlanPairs));
 }
 
 struct MoeWs {
-  size_t n_tiles, tiles, counts, pos, row_src, qx, s_x, h, s_h, y, total;
+  size_t n_tiles, tiles, counts, pos, qx, s_x, h, s_h, y, total;
   int64_t pairs, max_tiles, ldx, ldh, ldy, lds;
 };
-MoeWs moe_ws(const MoePlan& plan, int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+MoeWs moe_ws(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   Carver c;
   MoeWs w = {};
   w.pairs = T * k;
-  w.max_tiles = w.pairs / plan.tile_rows + std::min(E, w.pairs);
-  w.ldx = round_up16(H);
   w.ldh = round_up16(I);
-  w.ldy = (H + 3) / 4 * 4;
-  w.lds = (w.pairs + 3) / 4 * 4;
   const size_t pairs = size_t(w.pairs);
-  if (plan.path != MoePath::kOneToken) {
+  if (one_token(T, k, H, I)) {
+    w.h = c.take(pairs * size_t(w.ldh) * 4);  // fp32; the second GEMV quantizes it
+  } else {
+    w.max_tiles = w.pairs / block::kRowTile + std::min(E, w.pairs);
+    w.ldx = round_up16(H);
+    w.ldy = (H + 7) / 8 * 8;
+    w.lds = (w.pairs + 3) / 4 * 4;
     w.n_tiles = c.take(4);
     w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
     w.counts = c.take(plan_ctas(w.pairs) > 1 ? size_t(plan_ctas(w.pairs)) * size_t(E) * 4 : 0);
     w.pos = c.take(pairs * 4);
     w.y = c.take(pairs * size_t(w.ldy) * 4);
-  }
-  if (plan.path == MoePath::kGemv) w.row_src = c.take(pairs * 4);
-  if (plan.path == MoePath::kGemm) {
     w.qx = c.take(pairs * size_t(w.ldx));
     w.s_x = c.take(size_t(w.lds) * size_t(blocks_of(H)) * 4);
     w.h = c.take(pairs * size_t(w.ldh));
     w.s_h = c.take(size_t(w.lds) * size_t(blocks_of(I)) * 4);
-  } else {
-    w.h = c.take(pairs * size_t(w.ldh) * 4);  // fp32; the second GEMV quantizes it
   }
   w.total = c.at;
   return w;
 }
 
+// (the last: sizes of the workspace stay far below 2^64)
 bool moe_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   return T >= 0 && k >= 1 && k <= moe::kMaxChosen && E >= 1 && E <= moe::kMaxExperts && H >= 0 && H <= kMaxDim &&
-         I >= 1 && I <= kMaxDim / 2 && T <= kMaxRows / k;
+         I >= 1 && I <= kMaxDim / 2 && T <= kMaxRows / k && T * k <= (int64_t(1) << 56) / (H + I);
 }
 
 PerDeviceCache<const void*, int> g_attr_cache;
 
-fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int k, int tile_rows, int* counts, int* pos,
-                       int* row_src, block::RowTile* tiles, int* n_tiles, cudaStream_t st) {
+fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int* counts, int* pos, block::RowTile* tiles,
+                       int* n_tiles, cudaStream_t st) {
   const size_t smem = size_t(moe::kPlanWarps + 1) * E * sizeof(int);
   int dev = 0, set = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
@@ -226,8 +218,8 @@ fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int k, int tile
   if (ctas > 1)
     FP8_TRY(launch(moe::plan_count_kernel, dim3(ctas), dim3(moe::kPlanThreads), 0, st, true, dim3(1, 1, 1), ids, pairs,
                    E, counts));
-  return launch(moe::plan_kernel, dim3(ctas), dim3(moe::kPlanThreads), smem, st, true, dim3(1, 1, 1), ids, pairs, E, k,
-                tile_rows, ctas > 1 ? static_cast<const int*>(counts) : nullptr, pos, row_src, tiles, n_tiles);
+  return launch(moe::plan_kernel, dim3(ctas), dim3(moe::kPlanThreads), smem, st, true, dim3(1, 1, 1), ids, pairs, E,
+                ctas > 1 ? static_cast<const int*>(counts) : nullptr, pos, tiles, n_tiles);
 }
 
 template <typename T>
@@ -376,7 +368,7 @@ FP8_API fp8_status fp8_moe_route(const void* logits, int logits_bf16, int64_t T,
 
 FP8_API size_t fp8_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   if (!moe_sizes_ok(T, k, E, H, I) || T == 0 || H == 0) return 0;
-  return moe_ws(moe_plan(T, k, E, H, I), T, k, E, H, I).total;
+  return moe_ws(T, k, E, H, I).total;
 }
 
 FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
@@ -392,8 +384,7 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(s13, 4) || !aligned(s2, 4)) return FP8_ERR_MISALIGNED;
   if (T == 0 || H == 0) return FP8_OK;
   if (ids == nullptr || weights == nullptr || s13 == nullptr || s2 == nullptr) return FP8_ERR_INVALID_ARG;
-  const MoePlan plan = moe_plan(T, k, E, H, I);
-  const MoeWs w = moe_ws(plan, T, k, E, H, I);
+  const MoeWs w = moe_ws(T, k, E, H, I);
   FP8_TRY(check_ws(ws, ws_bytes, w.total));
   int sms = 0;
   FP8_TRY(current_device(&sms));
@@ -401,11 +392,14 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   uint8_t* b = static_cast<uint8_t*>(ws);
   const BF16Mat X{static_cast<const uint16_t*>(x_bf16), T, H, ldx};
 
-  block::GemvArgs v = {};
-  if (plan.path != MoePath::kGemm) {
+  if (one_token(T, k, H, I)) {
+    block::GemvArgs v = {};
     v.src = block::kSrcBf16;
     v.a = X.p;
     v.lda = ldx;
+    v.ids = ids;
+    v.weights = weights;
+    v.pairs = int(k);
     v.experts = E;
     v.qw = qw13;
     v.ldw = ldq13;
@@ -414,11 +408,6 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
     v.K = H;
     v.y32 = reinterpret_cast<float*>(b + w.h);
     v.ldy32 = w.ldh;
-  }
-  if (plan.path == MoePath::kOneToken) {
-    v.ids = ids;
-    v.weights = weights;
-    v.pairs = int(k);
     if (!block::gemv_launch(v, block::kGemvSwiglu, sms, st)) return FP8_ERR_CUDA;
     v.src = block::kSrcF32;
     v.a = b + w.h;
@@ -436,41 +425,8 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   int* n_tiles = reinterpret_cast<int*>(b + w.n_tiles);
   block::RowTile* tiles = reinterpret_cast<block::RowTile*>(b + w.tiles);
   int* pos = reinterpret_cast<int*>(b + w.pos);
-  int* row_src = plan.path == MoePath::kGemv ? reinterpret_cast<int*>(b + w.row_src) : nullptr;
   float* y32 = reinterpret_cast<float*>(b + w.y);
-  FP8_TRY(launch_plan(ids, w.pairs, int(E), int(k), plan.tile_rows, reinterpret_cast<int*>(b + w.counts), pos,
-                      row_src, tiles, n_tiles, st));
-  auto weighted_sum = [&] {
-    const int vec = aligned(y_bf16, 8) && ldy % 4 == 0;
-    return launch(moe::weighted_sum_kernel, dim3(elementwise_grid(T * ((H + 3) / 4), moe::kSumThreads, sms, 8)),
-                  dim3(moe::kSumThreads), 0, st, true, dim3(1, 1, 1), static_cast<const float*>(y32), w.ldy,
-                  static_cast<const int*>(pos), weights, int(k), T, H, static_cast<uint16_t*>(y_bf16), ldy, vec);
-  };
-  if (plan.path == MoePath::kGemv) {
-    v.tiles = tiles;
-    v.n_tiles = n_tiles;
-    v.max_tiles = w.max_tiles;
-    v.tile_rows = plan.tile_rows;
-    // experts that an even routing of the pairs touches
-    const double untouched = std::pow(1.0 - 1.0 / double(E), double(w.pairs));
-    v.likely_tiles = std::max<int64_t>(1, std::min<int64_t>(w.max_tiles, int64_t(double(E) * (1.0 - untouched) + 0.5)));
-    v.row_src = row_src;
-    if (!block::gemv_launch(v, block::kGemvSwiglu, sms, st)) return FP8_ERR_CUDA;
-    v.src = block::kSrcF32;
-    v.a = b + w.h;
-    v.lda = w.ldh;
-    v.row_src = nullptr;
-    v.qw = qw2;
-    v.ldw = ldq2;
-    v.s_w = s2;
-    v.N = H;
-    v.K = I;
-    v.y32 = y32;
-    v.ldy32 = w.ldy;
-    if (!block::gemv_launch(v, block::kGemvF32, sms, st)) return FP8_ERR_CUDA;
-    return weighted_sum();
-  }
-
+  FP8_TRY(launch_plan(ids, w.pairs, int(E), reinterpret_cast<int*>(b + w.counts), pos, tiles, n_tiles, st));
   // quantize each token once into its rows; gate and up products with SwiGLU and the quantization
   // of h in their epilogue; the product back; the weighted sum
   float* s_x = reinterpret_cast<float*>(b + w.s_x);
@@ -508,5 +464,8 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   g.y32 = y32;
   g.ldy32 = w.ldy;
   if (!block::gemm_launch(g, block::kOutF32, sms, st)) return FP8_ERR_CUDA;
-  return weighted_sum();
+  const int vec = aligned(y_bf16, 8) && ldy % 4 == 0;
+  return launch(moe::weighted_sum_kernel, dim3(elementwise_grid(T * ((H + 3) / 4), moe::kSumThreads, sms, 8)),
+                dim3(moe::kSumThreads), 0, st, true, dim3(1, 1, 1), static_cast<const float*>(y32), w.ldy,
+                static_cast<const int*>(pos), weights, int(k), T, H, static_cast<uint16_t*>(y_bf16), ldy, vec);
 }

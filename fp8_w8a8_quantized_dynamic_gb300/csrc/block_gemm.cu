@@ -46,6 +46,7 @@
 #include "block_gemm.h"
 
 #include <algorithm>
+#include <type_traits>
 #include <utility>
 
 #include "api_common.h"
@@ -68,7 +69,7 @@ constexpr int kScaleSlots = 4;
 constexpr int kLaunchRegs = 96, kIssueRegs = 64, kPromoRegs = 104;
 static_assert(kIssueRegs + 4 * kPromoRegs <= 5 * kLaunchRegs, "register shares of the five warpgroups");
 constexpr uint32_t kABytes = BM * BK;
-constexpr uint32_t kRingBytes = 192 * 1024;
+constexpr uint32_t kRingBytes = 194 * 1024;  // four stages of 48 KB; or of 32 KB beside 66 KB of exchanged sums
 constexpr int kMaxStages = 8;
 constexpr int kMaxBufs = 4;
 
@@ -76,14 +77,14 @@ constexpr int kMaxBufs = 4;
 template <int BN, bool kSplit>
 struct Tile {
   static constexpr uint32_t stage_bytes = kABytes + BN * BK;
-  static constexpr uint32_t exchange_bytes = kSplit ? BN * BM * 4 : 0;
+  static constexpr uint32_t exchange_bytes = kSplit ? BN * (BM + 4) * 4 : 0;
   static constexpr int stages = int((kRingBytes - exchange_bytes) / stage_bytes);  // 4, 6, 8 for BN = 256, 128, 64
   static constexpr int bufs = 512 / BN < kMaxBufs ? 512 / BN : kMaxBufs;
   static constexpr int cols = bufs * BN;  // tensor-memory columns (a power of two)
   static constexpr int groups = BN == 256 ? 4 : 2;  // promotion warpgroups, BN / groups columns each
   static constexpr int promo_warps = 4 * groups;
   static constexpr int threads = 128 + 128 * groups;
-  static_assert(stages <= kMaxStages, "ring");
+  static_assert(stages <= kMaxStages && stages * stage_bytes + exchange_bytes <= kRingBytes, "ring");
 };
 
 struct SharedCtl {
@@ -97,6 +98,7 @@ struct SharedCtl {
   uint64_t sfull[kScaleSlots];
   uint64_t sempty[kScaleSlots];
   uint32_t hmax[2][4][BM];  // SwiGLU: row maxima of the groups' columns, by tile parity
+  uint32_t staged[16][32][9];  // a promotion warp's 32 rows of 16 bf16 (+ 2: its lanes' writes on 32 banks)
   alignas(16) float s_row[kScaleSlots][kScaleKb][BM + 4];  // from the tile's first row rounded down to 4
   alignas(16) float s_col[kScaleSlots][kScaleKb][4];  // [half of the columns][gate, up]
 };
@@ -118,7 +120,7 @@ struct Params {
   const uint16_t* bias;
   uint16_t* y;
   int64_t ldy;
-  int vec;  // alignment of the output's rows: 32, 16 or less bytes
+  int vec;  // kOutBf16: alignment of the output's rows, 32 or 16 bytes
   float* y32;
   int64_t ldy32;
   uint8_t* qh;
@@ -215,6 +217,8 @@ __device__ __forceinline__ uint32_t codes4(uint64_t p01, uint64_t p23, const Exa
   }
   return quant2_divide<kFmtE4M3>(lo_of(p01), hi_of(p01), s) | (quant2_divide<kFmtE4M3>(lo_of(p23), hi_of(p23), s) << 16);
 }
+
+constexpr int kOutBf16Any = 3;  // kOutBf16 with rows of any alignment and width
 
 template <int BN, int kOut, bool kSplit>
 __global__ void __launch_bounds__(Tile<BN, kSplit>::threads, 1)
@@ -325,7 +329,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           const uint32_t fb = smem_u32(&ctl->full[s]);
           const uint32_t dst = smem_base + s * Tile<BN, kSplit>::stage_bytes;
           mbar_arrive_expect_tx(fb, Tile<BN, kSplit>::stage_bytes);
-          tma_load_2d(dst, &tmap_a, fb, kb * BK, row0, pol);
+          tma_load_3d(dst, &tmap_a, fb, kb * BK, row0, 0, pol);
           if (kOut == kOutSwiglu) {
             // 64 columns of gate, then the same 64 of up, twice
 #pragma unroll
@@ -390,9 +394,10 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         __syncwarp();
         const uint32_t bar = smem_u32(&ctl->sfull[slot]);
         if (p.bulk_scales) {
-          // one bulk copy a block: rows [a0, a0 + n), whole 16-byte pieces inside the block's lds_a
+          // one bulk copy a block: rows [a0, a0 + n), whole 16-byte pieces that each hold one of the
+          // rows (so nothing past the buffer of a view is read)
           const int a0 = row0 & ~3;
-          const uint32_t bytes = uint32_t(min(int64_t(BM + 4), p.lds_a - a0)) * 4u;
+          const uint32_t bytes = uint32_t(min(BM + 4, ((p.rows + 3) & ~3) - a0)) * 4u;
           const int blocks = min(kScaleKb, kb_end() - kb0);
           if (lane == 0) mbar_arrive_expect_tx(bar, bytes * blocks);
           __syncwarp();
@@ -479,17 +484,21 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         }
       }
       if constexpr (kSplit) {
-        // this slice's sums go to the CTAs that own their columns: [slice][column][row], so that a
-        // warp's stores are whole lines
+        // this slice's sums go to the CTAs that own their columns: [slice][column][row], columns far enough
+        // apart that a warp's loads of whole rows below fall on 32 banks, as its stores here do
         const int own_log2 = ilog2(BN) - p.split_log2;
-        const uint32_t at = smem_u32(exchange) + row_in_tile * 4u;
+        const uint32_t column_bytes = (BM + (1u << max(0, 5 - own_log2))) * 4u;
+        const uint32_t at = smem_u32(exchange) + (uint32_t(rank_of()) << own_log2) * column_bytes + row_in_tile * 4u;
 #pragma unroll
-        for (int j = 0; j < kCols / 2; ++j) {
-          const int c = group * kCols + 2 * j;
-          const uint32_t dst = map_to_rank(at, uint32_t(c) >> own_log2) +
-                               ((uint32_t(rank_of()) << own_log2) + (uint32_t(c) & ((1u << own_log2) - 1u))) * (BM * 4u);
-          st_cluster_u32(dst, uint32_t(acc[j]));
-          st_cluster_u32(dst + BM * 4u, uint32_t(acc[j] >> 32));
+        for (int q = 0; q < kCols / 8; ++q) {  // eight columns have one owner
+          const uint32_t c = group * kCols + 8 * q;
+          uint32_t dst = map_to_rank(at, c >> own_log2) + (c & ((1u << own_log2) - 1u)) * column_bytes;
+#pragma unroll
+          for (int j = 4 * q; j < 4 * q + 4; ++j) {
+            st_cluster_u32(dst, uint32_t(acc[j]));
+            st_cluster_u32(dst + column_bytes, uint32_t(acc[j] >> 32));
+            dst += 2 * column_bytes;
+          }
         }
         continue;
       }
@@ -529,51 +538,64 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
 #pragma unroll
           for (int q = 0; q < kCols / 8; ++q) {
             const uint64_t* a = acc + q * 4;
-            if (p.vec >= 32 && col0 + q * 8 + 8 <= p.ldy32) {
+            if (col0 + q * 8 < p.ldy32)  // ldy32: N rounded up to 8
               st_global_v8(dst + q * 8, uint32_t(a[0]), uint32_t(a[0] >> 32), uint32_t(a[1]), uint32_t(a[1] >> 32),
                            uint32_t(a[2]), uint32_t(a[2] >> 32), uint32_t(a[3]), uint32_t(a[3] >> 32));
-            } else {  // ldy32: N rounded up to 4
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (col0 + q * 8 + i * 4 < p.ldy32)
-                  *reinterpret_cast<float4*>(dst + q * 8 + i * 4) =
-                      make_float4(lo_of(a[2 * i]), hi_of(a[2 * i]), lo_of(a[2 * i + 1]), hi_of(a[2 * i + 1]));
-            }
           }
         }
       } else {
         const int col0 = n0 + group * kCols;
-        uint16_t* dst = p.y + int64_t(row) * p.ldy + col0;
-        if (store && live) {
+        // sixteen columns as bf16 pairs
+        auto packed = [&](int q, uint32_t (&w)[8]) {
+          const int col = col0 + q * 16;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint64_t a = acc[q * 8 + j];
+            float lo = lo_of(a), hi = hi_of(a);
+            if (p.bias) {
+              lo += bf16_bits_to_float(__ldg(p.bias + min(col + 2 * j, p.N - 1)));
+              hi += bf16_bits_to_float(__ldg(p.bias + min(col + 2 * j + 1, p.N - 1)));
+            }
+            w[j] = pack_bf16x2(lo, hi);
+          }
+        };
+        if constexpr (kOut == kOutBf16) {
+          uint16_t* dst = p.y + int64_t(row) * p.ldy + col0;
+          if (store && live) {
+#pragma unroll
+            for (int q = 0; q < kCols / 16; ++q) {
+              if (col0 + q * 16 >= p.N) break;  // N: whole eights
+              uint32_t w[8];
+              packed(q, w);
+              const bool both = col0 + q * 16 + 16 <= p.N;
+              if (p.vec >= 32 && both) {
+                st_global_v8(dst + q * 16, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+              } else {
+                *reinterpret_cast<uint4*>(dst + q * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (both) *reinterpret_cast<uint4*>(dst + q * 16 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+          }
+        } else if (store) {
+          // rows that start and end anywhere: through shared memory, two rows' 16 columns a store (8192 x 4096 x
+          // 8191: 285 us; two bytes of 32 rows a store: 768)
+          uint32_t(&mine)[32][9] = ctl->staged[warp - kFirstPromoWarp];
+          const int c = lane & 15;
 #pragma unroll
           for (int q = 0; q < kCols / 16; ++q) {
-            const int col = col0 + q * 16;
             uint32_t w[8];
+            packed(q, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint64_t a = acc[q * 8 + j];
-              float lo = lo_of(a), hi = hi_of(a);
-              if (p.bias) {
-                lo += bf16_bits_to_float(__ldg(p.bias + min(col + 2 * j, p.N - 1)));
-                hi += bf16_bits_to_float(__ldg(p.bias + min(col + 2 * j + 1, p.N - 1)));
-              }
-              w[j] = pack_bf16x2(lo, hi);
+            for (int j = 0; j < 8; ++j) mine[lane][j] = w[j];
+            __syncwarp();
+            const int col = col0 + q * 16 + c;
+#pragma unroll 1
+            for (int r = lane >> 4; r < 32; r += 2) {
+              const int to = row0 + quarter * 32 + r;
+              if (to < row_end && col < p.N)
+                p.y[int64_t(to) * p.ldy + col] = reinterpret_cast<const uint16_t*>(mine[r])[c];
             }
-            if (p.vec >= 32 && col + 16 <= p.N) {
-              st_global_v8(dst + q * 16, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-            } else {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (p.vec >= 16 && col + h * 8 + 8 <= p.N) {
-                  *reinterpret_cast<uint4*>(dst + q * 16 + h * 8) =
-                      make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 8; ++j)
-                    if (col + h * 8 + j < p.N) dst[q * 16 + h * 8 + j] = uint16_t(w[4 * h + (j >> 1)] >> ((j & 1) * 16));
-                }
-              }
-            }
+            __syncwarp();
           }
         }
       }
@@ -584,35 +606,35 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     __syncwarp();
     pair_sync();  // all threads of the cluster: every slice's sums have arrived
     if (warp >= kFirstPromoWarp && first_unit() < units && *abort_flag == 0) {
-      // the owner adds the slices in order: two threads a row, half of the owned columns each
+      // the owner adds the slices in order: a thread a column of every `step`-th row, neighbouring
+      // threads neighbouring columns
       int expert, row0, row_end, n_idx;
       decode(first_unit(), expert, row0, row_end, n_idx);
-      const int t = threadIdx.x - kFirstPromoWarp * 32, r = t % BM;
-      const int own = BN >> p.split_log2;
-      const int row = row0 + r;
-      if (row < row_end) {
-        for (int c = (t / BM) * (own / 2); c < (t / BM + 1) * (own / 2); c += 4) {
-          const int n = n_idx * kTileN + rank_of() * own + c;
-          if (n >= p.N) break;
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int k = 0; k < (1 << p.split_log2); ++k)
+      constexpr int kAtOnce = 4;  // rows in flight; BM is a multiple of kAtOnce * step
+      const int own_log2 = ilog2(BN) - p.split_log2;
+      const int column = BM + (1 << max(0, 5 - own_log2));
+      const int t = threadIdx.x - kFirstPromoWarp * 32, c = t & ((1 << own_log2) - 1);
+      const int step = kPromoWarps * 32 >> own_log2;
+      const int n = n_idx * kTileN + (rank_of() << own_log2) + c;
+      const int rows = n < p.N ? min(BM, row_end - row0) : 0;
+      float bias = 0.0f;
+      if (kOut != kOutF32 && p.bias && n < p.N) bias = bf16_bits_to_float(__ldg(p.bias + n));
+      for (int r = t >> own_log2; r < rows; r += kAtOnce * step) {
+        float v[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += exchange[(k * own + c + i) * BM + r];
-          if constexpr (kOut == kOutF32) {  // ldy32: N rounded up to 4
-            *reinterpret_cast<float4*>(p.y32 + int64_t(row) * p.ldy32 + n) = make_float4(v[0], v[1], v[2], v[3]);
-          } else {
+        for (int j = 0; j < kAtOnce; ++j) v[j] = 0.0f;
+        const float* from = exchange + c * column + r;
+        for (int k = 0; k < (1 << p.split_log2); ++k, from += column << own_log2)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (p.bias) v[i] += bf16_bits_to_float(__ldg(p.bias + min(n + i, p.N - 1)));
-            uint16_t* dst = p.y + int64_t(row) * p.ldy + n;
-            if (p.vec >= 16 && n + 4 <= p.N) {
-              *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-            } else {
+          for (int j = 0; j < kAtOnce; ++j) v[j] += from[j * step];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (n + i < p.N) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
-            }
-          }
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int64_t row = row0 + r + j * step;
+          if (r + j * step >= rows) continue;
+          if constexpr (kOut == kOutF32)
+            p.y32[row * p.ldy32 + n] = v[j];
+          else
+            p.y[row * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j] + bias));
         }
       }
     }
@@ -669,6 +691,13 @@ int slots_of(const void* kfn, int threads, int split, int num_sms) {
   return slots;
 }
 
+// Loads through the map of a tensor of less than 128 KB take about twice as long (31 rows x 4096 x 6144:
+// 28.7 us, 32 rows 13.0), so the map of a small one counts matrices that no load names.
+bool make_map(CUtensorMap* map, const uint8_t* base, int64_t mats, int64_t rows, int64_t K, int64_t ld, uint32_t box) {
+  constexpr int64_t kSmall = 128 * 1024;
+  return make_fp8_tensor_map_3d(map, base, std::max(mats, (kSmall + rows * ld - 1) / (rows * ld)), rows, K, ld, box);
+}
+
 template <int BN, int kOut, bool kSplit = false>
 bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
   auto kfn = block_gemm_kernel<BN, kOut, kSplit>;
@@ -703,14 +732,12 @@ bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
   p.ldh = a.ldh;
   p.s_h = a.s_h;
   p.lds_h = a.lds_h;
-  const void* out = kOut == kOutF32 ? static_cast<const void*>(a.y32) : a.y;
-  const int64_t out_ld = kOut == kOutF32 ? a.ldy32 * 4 : a.ldy * 2;
-  p.vec = aligned(out, 32) && out_ld % 32 == 0 ? 32 : aligned(out, 16) && out_ld % 16 == 0 ? 16 : 0;
+  p.vec = aligned(a.y, 32) && a.ldy % 16 == 0 ? 32 : 16;
   const int64_t units = (a.tiles ? a.max_tiles : int64_t(p.m_tiles)) * p.n_tiles;
   if (units > kMaxDim) return false;
   CUtensorMap ma, mb;
-  if (!make_fp8_tensor_map(&ma, a.qa, a.rows, a.K, a.lda, BM) ||
-      !make_fp8_tensor_map_3d(&mb, a.qw, a.mats, a.N, a.K, a.ldw, kOut == kOutSwiglu ? 64 : BN))
+  if (!make_map(&ma, a.qa, 1, a.rows, a.K, a.lda, BM) ||
+      !make_map(&mb, a.qw, a.mats, a.N, a.K, a.ldw, kOut == kOutSwiglu ? 64 : BN))
     return false;
   // a split tile's cluster comes and goes with it; otherwise the CTAs stay and walk the tiles
   const int64_t grid = kSplit ? units * split : std::min<int64_t>(units, slots);
@@ -756,8 +783,15 @@ bool launch_any(const GemmArgs& a, int num_sms, cudaStream_t st) {
     if (c.split > 1)
       return c.bn == 128 ? launch_tile<128, kOut, true>(a, c.split, num_sms, st)
                          : launch_tile<64, kOut, true>(a, c.split, num_sms, st);
-    if (c.bn == 256) return launch_tile<256, kOut>(a, 1, num_sms, st);
-    return c.bn == 128 ? launch_tile<128, kOut>(a, 1, num_sms, st) : launch_tile<64, kOut>(a, 1, num_sms, st);
+    auto whole = [&](auto out) {
+      constexpr int kHow = decltype(out)::value;
+      if (c.bn == 256) return launch_tile<256, kHow>(a, 1, num_sms, st);
+      return c.bn == 128 ? launch_tile<128, kHow>(a, 1, num_sms, st) : launch_tile<64, kHow>(a, 1, num_sms, st);
+    };
+    // whole sectors are stored at once where the rows allow it
+    if (kOut == kOutBf16 && !(aligned(a.y, 16) && a.ldy % 8 == 0 && a.N % 8 == 0))
+      return whole(std::integral_constant<int, kOutBf16Any>{});
+    return whole(std::integral_constant<int, kOut>{});
   }
 }
 

@@ -35,10 +35,7 @@ struct GvParams {
   int64_t lda;
   const float* s_a;
   int64_t lds_a;
-  const int* row_src;
   int M;
-  const RowTile* tiles;
-  const int* n_tiles;
   const int32_t* ids;
   const float* weights;
   int pairs, experts;
@@ -121,11 +118,11 @@ block_gemv_kernel(const __grid_constant__ GvParams p) {
   const int split = warp & (splits - 1), sub = warp >> p.split_log2;  // K slice, and row group of the unit
   const int kb0 = split * kbw;                        // this warp's blocks [kb0, kb0 + kbw)
   const int total_kb = kSum ? p.kb * p.pairs : p.kb;  // kSum: the pairs' K one after the other
-  const bool one_token = kGated && p.ids != nullptr;
+  constexpr bool kPairs = kGated;  // the tiles are the pairs of one token
 
   // shared memory of a K slice: rows of codes, then scales [kbw][8 kNT]
   const int stride = kbw * kBlock + 16;
-  const int rows_held = kSum || one_token ? 1 : kNT * 8;
+  const int rows_held = kSum || kPairs ? 1 : kNT * 8;
   const int rows_max = min(rows_held, p.M);
   const int slice_bytes = (rows_max * stride + kbw * kNT * 8 * 4 + 15) / 16 * 16;
   uint8_t* my_act = act + split * slice_bytes;
@@ -139,11 +136,8 @@ block_gemv_kernel(const __grid_constant__ GvParams p) {
   auto tile_of = [&](int ti, int& expert, int& row0, int& rows) {
     if (kSum) {
       expert = 0, row0 = 0, rows = 1;
-    } else if (one_token) {
+    } else if (kPairs) {
       expert = expert_of_pair(ti), row0 = ti, rows = 1;
-    } else if (p.tiles != nullptr) {
-      const int4 v = *reinterpret_cast<const int4*>(p.tiles + ti);
-      expert = v.x, row0 = v.y, rows = min(v.z - v.y, kNT * 8);
     } else {
       expert = 0, row0 = 0, rows = p.M;
     }
@@ -151,14 +145,10 @@ block_gemv_kernel(const __grid_constant__ GvParams p) {
 
   // dense weights do not depend on the kernel before; kSum's ids are older than it too (the
   // kernel before starts its dependents after its own wait)
-  bool waited = false;
-  if (!kSum && (p.tiles != nullptr || one_token)) {
-    pdl_wait();
-    waited = true;
-  }
+  if (kPairs) pdl_wait();
   pdl_trigger();
 
-  const int n_tiles = kSum ? 1 : one_token ? p.pairs : p.tiles != nullptr ? *p.n_tiles : 1;
+  const int n_tiles = kPairs ? p.pairs : 1;
   const int units = n_tiles * p.units;
   // contiguous units, so a CTA sees few tiles
   const int first = int(int64_t(units) * blockIdx.x / gridDim.x);
@@ -240,7 +230,7 @@ block_gemv_kernel(const __grid_constant__ GvParams p) {
   seek();
 #pragma unroll
   for (int d = 0; d < kDepth; ++d) issue(d);
-  if (!waited) pdl_wait();
+  if (!kPairs) pdl_wait();
 
   int tile = -1, expert = 0, row0 = 0, rows = 0;
   // codes and scales of the K slices for the rows of the current tile; the warps that share a slice
@@ -278,8 +268,7 @@ block_gemv_kernel(const __grid_constant__ GvParams p) {
           if (use) wt = __ldg(p.weights + src_row);
           kb -= int(src_row) * p.kb;
         }
-        if (one_token) src_row = 0;
-        if (p.row_src != nullptr && in) src_row = __ldg(p.row_src + row0 + r);
+        if (kPairs) src_row = 0;
         const int c = kb * kBlock + l8 * 16;
         uint4 codes = make_uint4(0, 0, 0, 0);
         float s;
@@ -415,8 +404,6 @@ block_gemv_kernel(const __grid_constant__ GvParams p) {
             // rows of h are whole sixteens: columns past N come from clamped rows and are zero
             const float h = n < p.N ? __fdividef(v[0], 1.0f + __expf(-v[0])) * v[1] : 0.0f;
             if (n < p.ldy32) p.y32[int64_t(row0 + r) * p.ldy32 + n] = h;
-          } else if constexpr (kOut == kGemvF32) {
-            if (n < p.N) p.y32[int64_t(row0 + r) * p.ldy32 + n] = v[0];
           } else if (n < p.N) {
             if (p.bias != nullptr) v[0] += bf16_bits_to_float(p.bias[n]);
             p.y[int64_t(row0 + r) * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
@@ -476,14 +463,11 @@ bool launch_as(const GemvArgs& a, int num_sms, cudaStream_t st) {
   p.lda = a.lda;
   p.s_a = a.s_a;
   p.lds_a = a.lds_a;
-  p.row_src = a.row_src;
-  p.tiles = a.tiles;
-  p.n_tiles = a.n_tiles;
   p.ids = a.ids;
   p.weights = a.weights;
   p.pairs = a.pairs;
   p.experts = int(a.experts);
-  p.M = int(a.tiles ? a.tile_rows : a.ids ? 1 : a.M);
+  p.M = int(a.ids ? 1 : a.M);
   p.qw = a.qw;
   p.ldw = a.ldw;
   p.mat_bytes = a.N * a.ldw;
@@ -495,8 +479,8 @@ bool launch_as(const GemvArgs& a, int num_sms, cudaStream_t st) {
   // (SwiGLU: the rows of h are whole sixteens)
   const int64_t groups = (std::min<int64_t>(kOut == kGemvSwiglu ? a.ldy32 : a.N, round_up16(a.N)) + kGvRows - 1) / kGvRows;
   const int64_t total_kb = kOut == kGemvSum ? int64_t(p.kb) * a.pairs : p.kb;
-  const int64_t tiles = kOut == kGemvSum ? 1 : a.tiles ? a.max_tiles : a.ids ? a.pairs : 1;
-  const int splits = splits_of(total_kb, a.tiles && a.likely_tiles > 0 ? a.likely_tiles : tiles, groups, num_sms);
+  const int64_t tiles = kOut == kGemvSwiglu ? a.pairs : 1;
+  const int splits = splits_of(total_kb, tiles, groups, num_sms);
   while ((1 << p.split_log2) < splits) ++p.split_log2;
   p.units = int((groups * splits + kGvWarps - 1) / kGvWarps);
   p.kbw = int((total_kb + splits - 1) / splits);
@@ -531,18 +515,14 @@ bool gemv_fits(int64_t rows, int64_t K, int mats) {
 bool gemv_quantizes(int64_t M, int64_t K) { return M * ((blocks_of(K) + kGvWarps - 1) / kGvWarps) <= 16; }
 
 bool gemv_launch(const GemvArgs& a, GemvOut out, int num_sms, cudaStream_t st) {
-  const int64_t rows = a.tiles ? a.tile_rows : a.ids ? 1 : a.M;
-  const bool two = rows > 8;
+  const bool two = a.M > 8;  // dense rows
   switch (out) {
     case kGemvBf16:
       if (a.src == kSrcBf16)
         return two ? launch_gv<2, kSrcBf16, kGemvBf16>(a, num_sms, st) : launch_gv<1, kSrcBf16, kGemvBf16>(a, num_sms, st);
       return two ? launch_gv<2, kSrcCodes, kGemvBf16>(a, num_sms, st) : launch_gv<1, kSrcCodes, kGemvBf16>(a, num_sms, st);
     case kGemvSwiglu:
-      return two ? launch_gv<2, kSrcBf16, kGemvSwiglu>(a, num_sms, st)
-                 : launch_gv<1, kSrcBf16, kGemvSwiglu>(a, num_sms, st);
-    case kGemvF32:
-      return two ? launch_gv<2, kSrcF32, kGemvF32>(a, num_sms, st) : launch_gv<1, kSrcF32, kGemvF32>(a, num_sms, st);
+      return launch_gv<1, kSrcBf16, kGemvSwiglu>(a, num_sms, st);
     case kGemvSum:
       return launch_gv<1, kSrcF32, kGemvSum>(a, num_sms, st);
   }

@@ -1,5 +1,5 @@
 // Internal interface of the block-scaled FP8 GEMV: products of at most 16 rows with streamed
-// weights, dense or for the experts of a few tokens.
+// weights, or of one token with its experts.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -23,13 +23,7 @@ struct GemvArgs {
   int64_t lda;            // elements (bytes for codes)
   const float* s_a;       // kSrcCodes: [K blocks][lds_a]
   int64_t lds_a;
-  const int* row_src;     // sorted row -> row of a; null: the same row
   int64_t M;              // dense: rows
-  const RowTile* tiles;   // grouped: row tiles of at most tile_rows rows, else null
-  const int* n_tiles;
-  int64_t max_tiles;
-  int tile_rows;          // 8 or 16
-  int64_t likely_tiles;   // how many of max_tiles an even routing fills (0: unknown)
   // one token: the tiles are its pairs, expert ids[j] and row j; with kOutSum K runs over all pairs
   const int32_t* ids;
   const float* weights;
@@ -42,15 +36,14 @@ struct GemvArgs {
   const uint16_t* bias;
   uint16_t* y;            // bf16 output
   int64_t ldy;
-  float* y32;             // fp32 output
+  float* y32;             // fp32 output, rows of ldy32 (whole sixteens)
   int64_t ldy32;
 };
 
 enum GemvOut : int {
   kGemvBf16 = 0,    // y = bf16(acc (+ bias))
-  kGemvSwiglu = 1,  // gate and up matrices: y32 = silu(gate) * up
-  kGemvF32 = 2,     // y32 = acc
-  kGemvSum = 3      // one token: y = bf16(sum over pairs of weight * acc)
+  kGemvSwiglu = 1,  // one token: gate and up matrices of its pairs' experts: y32 = silu(gate) * up
+  kGemvSum = 2      // one token: y = bf16(sum over pairs of weight * acc)
 };
 
 // Whether the GEMV holds `rows` rows of K columns beside the sums of `mats` matrices in one SM's

@@ -8,6 +8,7 @@
 #include <cstddef>
 #include <map>
 #include <mutex>
+#include <new>
 #include <utility>
 
 namespace fp8k {
@@ -27,7 +28,10 @@ class PerDeviceCache {
     }
     Value v{};
     if (!compute(&v)) return false;
-    map_.emplace(k, v);
+    try {
+      map_.emplace(k, v);
+    } catch (const std::bad_alloc&) {  // not remembered; nothing is thrown through a C entry point
+    }
     *out = v;
     return true;
   }

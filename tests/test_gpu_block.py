@@ -162,6 +162,19 @@ def test_scaled_mm_equals_linear(M):
     assert torch.equal(y, F.fp8_block_scaled_mm(qa, K, s_a, qw, s_w, b))
 
 
+@pytest.mark.parametrize("M,first,after", [(30, 4, 2), (130, 8, 2), (131, 4, 5), (200, 1, 3), (260, 16, 0)])
+def test_scaled_mm_scales_from_inside_a_buffer(M, first, after):
+    """Scales that are columns [first, first + M) of a wider buffer, filled with NaN around them."""
+    K, N = 700, 330
+    a = rand((M, K), 24).to(DEV)
+    qw, s_w = F.fp8_block_quantize_weight(rand((N, K), 25, std=0.02).to(DEV))
+    qa, s_a = F.fp8_block_quantize_act(a)
+    wide = torch.full((s_a.shape[0], first + M + after), float("nan"), device=DEV)
+    wide[:, first:first + M] = s_a
+    assert torch.equal(F.fp8_block_scaled_mm(qa, K, wide[:, first:first + M], qw, s_w),
+                       F.fp8_block_scaled_mm(qa, K, s_a, qw, s_w))
+
+
 @pytest.mark.parametrize("M", [4, 24, 160])
 def test_repeatable_on_another_stream(M):
     """The same bits on every call and on a side stream, with a workspace full of garbage."""
