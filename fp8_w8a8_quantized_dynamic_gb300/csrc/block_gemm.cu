@@ -120,7 +120,7 @@ struct Params {
   const uint16_t* bias;
   uint16_t* y;
   int64_t ldy;
-  int vec;  // kOutBf16: alignment of the output's rows, 32 or 16 bytes
+  int vec;  // alignment of the bf16 output's rows: 32 bytes or less
   float* y32;
   int64_t ldy32;
   uint8_t* qh;
@@ -606,35 +606,42 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     __syncwarp();
     pair_sync();  // all threads of the cluster: every slice's sums have arrived
     if (warp >= kFirstPromoWarp && first_unit() < units && *abort_flag == 0) {
-      // the owner adds the slices in order: a thread a column of every `step`-th row, neighbouring
+      // the owner adds the slices in order: a thread four columns of every `step`-th row, neighbouring
       // threads neighbouring columns
       int expert, row0, row_end, n_idx;
       decode(first_unit(), expert, row0, row_end, n_idx);
-      constexpr int kAtOnce = 4;  // rows in flight; BM is a multiple of kAtOnce * step
       const int own_log2 = ilog2(BN) - p.split_log2;
       const int column = BM + (1 << max(0, 5 - own_log2));
-      const int t = threadIdx.x - kFirstPromoWarp * 32, c = t & ((1 << own_log2) - 1);
-      const int step = kPromoWarps * 32 >> own_log2;
+      const int t = threadIdx.x - kFirstPromoWarp * 32, c = (t & ((1 << (own_log2 - 2)) - 1)) * 4;
+      const int step = kPromoWarps * 32 >> (own_log2 - 2);
       const int n = n_idx * kTileN + (rank_of() << own_log2) + c;
       const int rows = n < p.N ? min(BM, row_end - row0) : 0;
-      float bias = 0.0f;
-      if (kOut != kOutF32 && p.bias && n < p.N) bias = bf16_bits_to_float(__ldg(p.bias + n));
-      for (int r = t >> own_log2; r < rows; r += kAtOnce * step) {
-        float v[kAtOnce];
+      float bias[4] = {0.f, 0.f, 0.f, 0.f};
+      if (kOut != kOutF32 && p.bias && n < p.N)
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) v[j] = 0.0f;
+        for (int i = 0; i < 4; ++i) bias[i] = bf16_bits_to_float(__ldg(p.bias + min(n + i, p.N - 1)));
+      for (int r = t >> (own_log2 - 2); r < rows; r += step) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
         const float* from = exchange + c * column + r;
+#pragma unroll 2
         for (int k = 0; k < (1 << p.split_log2); ++k, from += column << own_log2)
 #pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) v[j] += from[j * step];
-#pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) {
-          const int64_t row = row0 + r + j * step;
-          if (r + j * step >= rows) continue;
-          if constexpr (kOut == kOutF32)
-            p.y32[row * p.ldy32 + n] = v[j];
-          else
-            p.y[row * p.ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j] + bias));
+          for (int i = 0; i < 4; ++i) v[i] += from[i * column];
+        const int64_t row = row0 + r;
+        if constexpr (kOut == kOutF32) {  // ldy32: N rounded up to 8
+          *reinterpret_cast<float4*>(p.y32 + row * p.ldy32 + n) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+          uint16_t* dst = p.y + row * p.ldy + n;
+          const uint32_t lo = pack_bf16x2(v[0] + bias[0], v[1] + bias[1]);
+          const uint32_t hi = pack_bf16x2(v[2] + bias[2], v[3] + bias[3]);
+          if (p.vec >= 8 && n + 4 <= p.N) {
+            *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+          } else {
+            dst[0] = uint16_t(lo);
+            if (n + 1 < p.N) dst[1] = uint16_t(lo >> 16);
+            if (n + 2 < p.N) dst[2] = uint16_t(hi);
+            if (n + 3 < p.N) dst[3] = uint16_t(hi >> 16);
+          }
         }
       }
     }
@@ -732,7 +739,8 @@ bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
   p.ldh = a.ldh;
   p.s_h = a.s_h;
   p.lds_h = a.lds_h;
-  p.vec = aligned(a.y, 32) && a.ldy % 16 == 0 ? 32 : 16;
+  p.vec = 32;
+  while (p.vec > 2 && !(aligned(a.y, p.vec) && a.ldy * 2 % p.vec == 0)) p.vec /= 2;
   const int64_t units = (a.tiles ? a.max_tiles : int64_t(p.m_tiles)) * p.n_tiles;
   if (units > kMaxDim) return false;
   CUtensorMap ma, mb;
