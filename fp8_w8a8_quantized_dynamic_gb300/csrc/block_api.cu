@@ -157,7 +157,8 @@ bool one_token(int64_t T, int64_t k, int64_t H, int64_t I) {
   return T == 1 && block::gemv_fits(1, H, 2) && block::gemv_fits(1, k * blocks_of(I) * block::kBlock, 1);
 }
 
-// CTAs that sort the pairs; more than one need their counts first.
+// CTAs that sort the pairs; more than one need their counts first (the whole layer, experts of 2048 x
+// 1408, in us: 4096 pairs 131.7, by one CTA 134.5; 8192 pairs 161.1 and 170.8).
 int plan_ctas(int64_t pairs) {
   if (pairs <= 2 * moe::kPlanPairs) return 1;  // a second launch costs more than it saves
   return int(std::min<int64_t>(moe::kPlanMaxCtas, (pairs + moe::kPlanPairs - 1) / moe::kPlanPairs));

@@ -1,4 +1,7 @@
-// Block-scaled FP8 GEMV for sm_103a: the product for few rows, bound by streaming the weights.
+// Block-scaled FP8 GEMV for sm_103a: the product for few rows, bound by streaming the weights (one row,
+// 4096 x 6144, 25 MB: 8.0 us in a graph, 3.1 TB/s; 4096 x 28672, 117 MB: 20.0 us, 5.9 TB/s; the start of
+// a launch, its first loads and the last sums take 4 us). One token's experts, 8 of 2048 x 1408: 26.5 us
+// for 69 MB in two launches.
 //
 // A warp takes 16 weight rows at a time (kGemvSwiglu: 16 of gate and the same 16 of up) over a slice
 // of K in whole 128-wide blocks; 1, 2, 4 or all 8 warps of a CTA share one row group's K. A lane loads
@@ -100,7 +103,9 @@ __device__ __forceinline__ uint4 codes_of_f32(const float (&x)[16], float s) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// kNT: eight-row activation tiles (1 or 2). kFull: weight rows are whole blocks, 32-byte aligned.
+// kNT: eight-row activation tiles (1 or 2). kFull: weight rows are whole blocks, 32-byte aligned, and
+// loaded 32 bytes at a time (16 x 4096 x 6144 in 17.4 us, 19.4 in predicated 16-byte loads; 4 x 5632 x
+// 2048 8.8 and 9.5; equal within 3 percent for one row).
 template <int kNT, int kSrc, int kOut, bool kFull>
 __global__ void __launch_bounds__(kGvThreads, 2)
 block_gemv_kernel(const __grid_constant__ GvParams p) {
@@ -430,9 +435,9 @@ size_t act_bytes(int64_t rows, int64_t kbw, int splits, int nt) {
 }
 size_t red_bytes(int nt, int mats) { return size_t(2) * kGvWarps * mats * nt * 8 * (kGvRows + 4) * 4; }
 // Warps that share a row group's K (1, 2, 4 or 8): the split with the fewest steps of the busiest
-// warp, a unit counting kbw blocks and one more for its barrier and output. Few row groups take all
-// eight (and so the whole GPU), many take fewer, longer slices with fewer slots empty (11 blocks:
-// 2 x 6 and not 8 x 2: 50 -> 40 us for the second product of 16 tokens' experts, 2048 x 1408).
+// warp, a unit counting its blocks and one more for its barrier and output; of equals the smaller, which
+// takes fewer CTAs. Few row groups take all eight and so the whole GPU (one row, K 4096, N 1024: 3.9 us,
+// 5.2 with four, 12.3 with one), many take fewer and longer slices (K 512, N 28672: 6.3 us, 8.8 with eight).
 int splits_of(int64_t kb, int64_t tiles, int64_t groups, int num_sms) {
   int best = kGvWarps;
   int64_t best_cost = -1;
@@ -440,7 +445,7 @@ int splits_of(int64_t kb, int64_t tiles, int64_t groups, int num_sms) {
     const int64_t units = tiles * ((groups * s + kGvWarps - 1) / kGvWarps);
     const int64_t per_cta = (units + 2 * num_sms - 1) / (2 * num_sms);
     const int64_t cost = per_cta * ((kb + s - 1) / s + 1);
-    if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
+    if (best_cost < 0 || cost <= best_cost) best = s, best_cost = cost;
   }
   return best;
 }
@@ -512,6 +517,10 @@ bool gemv_fits(int64_t rows, int64_t K, int mats) {
   return act_bytes(rows, (blocks_of(K) + kGvWarps - 1) / kGvWarps, kGvWarps, nt) + red_bytes(nt, mats) + 1024 <= size_t(kSmemCap);
 }
 
+// The fill of a K slice by every CTA against a second launch and codes through L2 (graph replays, us,
+// in the kernel / before it): M 1 K 4096 N 6144 9.2 / 10.6, M 4 11.9 / 11.1, M 8 16.0 / 11.3; M 4 K 5632
+// N 2048 10.7 / 8.7; K 1000 N 1027 M 8 3.9 / 4.5, M 16 6.0 / 5.8. Where the two are level the one launch is
+// less work for the host.
 bool gemv_quantizes(int64_t M, int64_t K) { return M * ((blocks_of(K) + kGvWarps - 1) / kGvWarps) <= 16; }
 
 bool gemv_launch(const GemvArgs& a, GemvOut out, int num_sms, cudaStream_t st) {

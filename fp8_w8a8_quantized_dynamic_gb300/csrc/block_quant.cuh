@@ -89,7 +89,8 @@ quantize_rows_1x128_kernel(const uint16_t* __restrict__ a, int64_t rows, int64_t
 }
 
 // W [mats][N, K] -> q [mats][N, ldq], s [mats][N blocks][K blocks]. One CTA a 128 x 128 block: a
-// thread holds half a row of it (64 columns) in registers between the maximum and the codes.
+// thread holds half a row of it (64 columns) in registers between the maximum and the codes. Runs once,
+// when weights are loaded.
 __global__ void __launch_bounds__(kQThreads)
 quantize_128x128_kernel(const uint16_t* __restrict__ w, int64_t mats, int64_t N, int64_t K, int64_t ld,
                         int64_t mat_stride, int vec, uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s) {
