@@ -76,7 +76,8 @@ LinearWs linear_ws(int64_t M, int64_t K) {
   Carver c;
   LinearWs w = {};
   if (linear_fused(M, K)) return w;
-  w.qa = c.take(size_t(M) * size_t(round_up16(K)));
+  const int64_t rows = uses_gemv(M, K) ? M : block::gemm_held_rows(M, round_up16(K));
+  w.qa = c.take(size_t(rows) * size_t(round_up16(K)));
   w.lds = (M + 3) / 4 * 4;
   w.s_a = c.take(size_t(blocks_of(K)) * size_t(w.lds) * 4);
   w.total = c.at;
@@ -85,7 +86,7 @@ LinearWs linear_ws(int64_t M, int64_t K) {
 
 fp8_status block_mm(const uint8_t* qa, int64_t M, int64_t K, int64_t ldqa, const float* s_a, int64_t lds_a,
                     const uint8_t* qw, int64_t N, int64_t ldqw, const float* s_w, const void* bias, void* y,
-                    int64_t ldy, int sms, cudaStream_t st) {
+                    int64_t ldy, int64_t held_rows, int sms, cudaStream_t st) {
   if (uses_gemv(M, K)) {
     block::GemvArgs v = {};
     v.src = block::kSrcCodes;
@@ -107,6 +108,7 @@ fp8_status block_mm(const uint8_t* qa, int64_t M, int64_t K, int64_t ldqa, const
   block::GemmArgs g = {};
   g.qa = qa;
   g.rows = M;
+  g.held_rows = held_rows;
   g.lda = ldqa;
   g.s_a = s_a;
   g.lds_a = lds_a;
@@ -186,9 +188,9 @@ MoeWs moe_ws(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     w.counts = c.take(plan_ctas(w.pairs) > 1 ? size_t(plan_ctas(w.pairs)) * size_t(E) * 4 : 0);
     w.pos = c.take(pairs * 4);
     w.y = c.take(pairs * size_t(w.ldy) * 4);
-    w.qx = c.take(pairs * size_t(w.ldx));
+    w.qx = c.take(size_t(block::gemm_held_rows(w.pairs, w.ldx)) * size_t(w.ldx));
     w.s_x = c.take(size_t(w.lds) * size_t(blocks_of(H)) * 4);
-    w.h = c.take(pairs * size_t(w.ldh));
+    w.h = c.take(size_t(block::gemm_held_rows(w.pairs, w.ldh)) * size_t(w.ldh));
     w.s_h = c.take(size_t(w.lds) * size_t(blocks_of(I)) * 4);
   }
   w.total = c.at;
@@ -285,7 +287,7 @@ FP8_API fp8_status fp8_block_scaled_mm(const uint8_t* qa, int64_t M, int64_t K, 
   FP8_TRY(current_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (K == 0) return launch_rows_of_bias(bias_bf16, y_bf16, M, N, ldy, sms, st);
-  return block_mm(qa, M, K, ldqa, s_a, lds, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy, sms, st);
+  return block_mm(qa, M, K, ldqa, s_a, lds, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy, M, sms, st);
 }
 
 FP8_API size_t fp8_block_workspace_bytes(int64_t M, int64_t K, int64_t N) {
@@ -325,7 +327,8 @@ FP8_API fp8_status fp8_block_linear(const void* a_bf16, int64_t M, int64_t K, in
   uint8_t* qa = static_cast<uint8_t*>(ws) + w.qa;
   float* s_a = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.s_a);
   FP8_TRY(launch_quantize_rows(A, qa, round_up16(K), s_a, w.lds, nullptr, 0, sms, st));
-  return block_mm(qa, M, K, round_up16(K), s_a, w.lds, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy, sms, st);
+  return block_mm(qa, M, K, round_up16(K), s_a, w.lds, qw, N, ldqw, s_w, bias_bf16, y_bf16, ldy,
+                  block::gemm_held_rows(M, round_up16(K)), sms, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -440,6 +443,7 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   g.max_tiles = w.max_tiles;
   g.qa = b + w.qx;
   g.lda = w.ldx;
+  g.held_rows = block::gemm_held_rows(w.pairs, w.ldx);
   g.s_a = s_x;
   g.lds_a = w.lds;
   g.qw = qw13;
@@ -455,6 +459,7 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   if (!block::gemm_launch(g, block::kOutSwiglu, sms, st)) return FP8_ERR_CUDA;
   g.qa = b + w.h;
   g.lda = w.ldh;
+  g.held_rows = block::gemm_held_rows(w.pairs, w.ldh);
   g.s_a = s_h;
   g.qw = qw2;
   g.mats = E;

@@ -330,7 +330,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           const uint32_t fb = smem_u32(&ctl->full[s]);
           const uint32_t dst = smem_base + s * Tile<BN, kSplit>::stage_bytes;
           mbar_arrive_expect_tx(fb, Tile<BN, kSplit>::stage_bytes);
-          tma_load_3d(dst, &tmap_a, fb, kb * BK, row0, 0, pol);
+          tma_load_2d(dst, &tmap_a, fb, kb * BK, row0, pol);
           if (kOut == kOutSwiglu) {
             // 64 columns of gate, then the same 64 of up, twice
 #pragma unroll
@@ -699,13 +699,6 @@ int slots_of(const void* kfn, int threads, int split, int num_sms) {
   return slots;
 }
 
-// Loads through the map of a tensor of less than 128 KB take about twice as long (rows x 4096 x 6144: 17
-// rows 27.2 us, 32 rows 12.9), so the map of a small one counts matrices that no load names (17 rows 11.4).
-bool make_map(CUtensorMap* map, const uint8_t* base, int64_t mats, int64_t rows, int64_t K, int64_t ld, uint32_t box) {
-  constexpr int64_t kSmall = 128 * 1024;
-  return make_fp8_tensor_map_3d(map, base, std::max(mats, (kSmall + rows * ld - 1) / (rows * ld)), rows, K, ld, box);
-}
-
 template <int BN, int kOut, bool kSplit = false>
 bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
   auto kfn = block_gemm_kernel<BN, kOut, kSplit>;
@@ -745,8 +738,8 @@ bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
   const int64_t units = (a.tiles ? a.max_tiles : int64_t(p.m_tiles)) * p.n_tiles;
   if (units > kMaxDim) return false;
   CUtensorMap ma, mb;
-  if (!make_map(&ma, a.qa, 1, a.rows, a.K, a.lda, BM) ||
-      !make_map(&mb, a.qw, a.mats, a.N, a.K, a.ldw, kOut == kOutSwiglu ? 64 : BN))
+  if (!make_fp8_tensor_map(&ma, a.qa, std::max(a.rows, a.held_rows), a.K, a.lda, BM) ||
+      !make_fp8_tensor_map_3d(&mb, a.qw, a.mats, a.N, a.K, a.ldw, kOut == kOutSwiglu ? 64 : BN))
     return false;
   // a split tile's cluster comes and goes with it; otherwise the CTAs stay and walk the tiles
   const int64_t grid = kSplit ? units * split : std::min<int64_t>(units, slots);
@@ -805,6 +798,8 @@ bool launch_any(const GemmArgs& a, int num_sms, cudaStream_t st) {
 }
 
 }  // namespace
+
+int64_t gemm_held_rows(int64_t rows, int64_t ld) { return std::max(rows, (128 * 1024 + ld - 1) / ld); }
 
 bool gemm_launch(const GemmArgs& a, Out out, int num_sms, cudaStream_t stream) {
   switch (out) {

@@ -236,3 +236,23 @@ def test_wrapper_refusals():
 def test_few_tiles_share_k(M, K, N):
     """Shapes with few output tiles, whose K is divided among the CTAs of a cluster."""
     run(M, K, N, seed=M, bias=True)
+
+
+@pytest.mark.parametrize("M,K,N", [(5, 256, 72), (40, 1152, 136), (300, 2048, 264), (1300, 128, 704), (2000, 384, 1032),
+                                   (4100, 256, 2056)])
+@pytest.mark.parametrize("first,after", [(0, 3), (1, 0), (2, 2), (4, 4), (8, 8), (5, 11)])
+def test_output_rows_of_any_alignment(M, K, N, first, after):
+    """Columns [first, first + N) of a wider output: the same bits as a gap-free one, nothing beside them touched."""
+    a = rand((M, K), 41).to(DEV)
+    b = rand((N,), 42).to(DEV)
+    qw, s_w = F.fp8_block_quantize_weight(rand((N, K), 43, std=0.02).to(DEV))
+    y = F.fp8_block_linear(a, qw, s_w, b)
+    wide = torch.full((M, first + N + after), 7.0, dtype=torch.bfloat16, device=DEV)
+    F.fp8_block_linear(a, qw, s_w, b, out=wide[:, first:first + N])
+    assert torch.equal(wide[:, first:first + N], y)
+    assert bool((wide[:, :first] == 7).all()) and bool((wide[:, first + N:] == 7).all())
+
+
+@pytest.mark.parametrize("M,K,N", [(1500, 130, 1031), (3000, 257, 1153), (700, 100, 67)])
+def test_odd_outputs_of_many_tiles(M, K, N):
+    run(M, K, N, seed=N, bias=True)
