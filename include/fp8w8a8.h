@@ -40,9 +40,10 @@
  *  - Launch ordering: kernels use programmatic dependent launch. The weight
  *    operands (qW, s_w, bias) of a linear call may be read before the kernel
  *    enqueued just before it has finished, so they must not be written by the
- *    immediately preceding kernel unless that kernel is fp8_quantize_weight or
- *    a kernel that does not trigger programmatic launch early (any ordinary
- *    CUDA or PyTorch kernel). Activations, workspace and Y are always ordered.
+ *    immediately preceding kernel unless that kernel is fp8_quantize_weight,
+ *    fp8_block_quantize_weight or one that does not trigger programmatic
+ *    launch early (any ordinary CUDA or PyTorch kernel). Activations,
+ *    workspace and Y are always ordered.
  */
 #ifndef FP8W8A8_H
 #define FP8W8A8_H
