@@ -104,8 +104,8 @@ __device__ __forceinline__ uint4 codes_of_f32(const float (&x)[16], float s) {
 }
 
 // kNT: eight-row activation tiles (1 or 2). kFull: weight rows are whole blocks, 32-byte aligned, and
-// loaded 32 bytes at a time (16 x 4096 x 6144 in 17.4 us, 19.4 in predicated 16-byte loads; 4 x 5632 x
-// 2048 8.8 and 9.5; equal within 3 percent for one row).
+// loaded 32 bytes at a time (1 x 5632 x 2048 in 6.9 us, 7.9 in predicated 16-byte loads; 4 rows 8.8 and
+// 9.5; 1 x 4096 x 6144 9.2 and 8.9).
 template <int kNT, int kSrc, int kOut, bool kFull>
 __global__ void __launch_bounds__(kGvThreads, 2)
 block_gemv_kernel(const __grid_constant__ GvParams p) {

@@ -24,7 +24,7 @@ struct GemvArgs {
   const float* s_a;       // kSrcCodes: [K blocks][lds_a]
   int64_t lds_a;
   int64_t M;              // dense: rows
-  // one token: the tiles are its pairs, expert ids[j] and row j; with kOutSum K runs over all pairs
+  // one token: the tiles are its pairs, expert ids[j] and row j; with kGemvSum K runs over all pairs
   const int32_t* ids;
   const float* weights;
   int pairs;
