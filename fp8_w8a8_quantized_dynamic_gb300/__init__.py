@@ -389,6 +389,12 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _row_stride(t, rows: int, width: int) -> int:
+    """Leading dimension handed to C: the true stride between rows, so that C refuses rows that overlap
+    (broadcast ones have stride 0). A single row's stride means nothing: the width stands for it."""
+    return t.stride(-2) if rows > 1 else width or 1
+
+
 def _out_bf16(out, M: int, N: int, like):
     if out is None:
         return _torch().empty((M, N), dtype=like.dtype, device=like.device)  # `like` is bf16
@@ -441,7 +447,7 @@ def fp8_block_quantize_weight(w):
     B = w.shape[0] if w.dim() == 3 else 1
     qw = torch.empty((*lead, N, min_ld(K)), dtype=torch.uint8, device=w.device)
     s_w = torch.empty((*lead, _blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
-    _check(lib().fp8_block_quantize_weight(w.data_ptr(), B, N, K, max(w.stride(-2), K, 1),
+    _check(lib().fp8_block_quantize_weight(w.data_ptr(), B, N, K, _row_stride(w, N, K),
                                            w.stride(0) if w.dim() == 3 else 0, qw.data_ptr(), min_ld(K),
                                            s_w.data_ptr(), _stream_ptr(w)), "fp8_block_quantize_weight")
     return qw, s_w
@@ -455,7 +461,7 @@ def fp8_block_quantize_act(a):
     M, K = a.shape
     qa = torch.empty((M, min_ld(K)), dtype=torch.uint8, device=a.device)
     s_a = torch.empty((_blocks(K), (M + 3) // 4 * 4), dtype=torch.float32, device=a.device)[:, :M]
-    _check(lib().fp8_block_quantize_act(a.data_ptr(), M, K, max(a.stride(0), K, 1), qa.data_ptr(), qa.stride(0),
+    _check(lib().fp8_block_quantize_act(a.data_ptr(), M, K, _row_stride(a, M, K), qa.data_ptr(), qa.stride(0),
                                         s_a.data_ptr(), max(s_a.stride(0), 1), _stream_ptr(a)),
            "fp8_block_quantize_act")
     return qa, s_a
@@ -474,9 +480,9 @@ def fp8_block_scaled_mm(qa, K: int, s_a, qw, s_w, bias=None, out=None):
         _check_dense(bias, torch.bfloat16, (N,), index, "bias")
     y = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device) if out is None else _out_bf16(out, M, N, qa)
     _check(lib().fp8_block_scaled_mm(qa.data_ptr(), M, K, qa.stride(0), s_a.data_ptr(),
-                                     max(s_a.stride(0), M, 1) if s_a.shape[0] > 1 else max(M, 1), qw.data_ptr(), N,
-                                     ld, s_w.data_ptr(), _ptr(bias), y.data_ptr(), max(y.stride(0), N, 1),
-                                     _stream_ptr(qa)), "fp8_block_scaled_mm")
+                                     _row_stride(s_a, s_a.shape[0], M), qw.data_ptr(), N, ld, s_w.data_ptr(),
+                                     _ptr(bias), y.data_ptr(), _row_stride(y, M, N), _stream_ptr(qa)),
+           "fp8_block_scaled_mm")
     return y
 
 
@@ -504,13 +510,12 @@ def fp8_block_linear(a, qw, s_w, bias=None, out=None, ws=None):
     need = L.fp8_block_workspace_bytes(M, K, N)
     wp, wn, ws = _scratch(ws, need, a) if need or ws is not None else (None, 0, None)
     if out is None:
-        y, ldy = torch.empty((M, N), dtype=torch.bfloat16, device=a.device), N
+        y, ldy = torch.empty((M, N), dtype=torch.bfloat16, device=a.device), N or 1
     else:
         y = _out_bf16(out, M, N, a)
-        ldy = y.stride(0)
-    status = L.fp8_block_linear(a.data_ptr(), M, K, lda if lda > K else K or 1, qw.data_ptr(), N, ld, s_w.data_ptr(),
-                                None if bias is None else bias.data_ptr(), y.data_ptr(), ldy if ldy > N else N or 1,
-                                wp, wn, _stream_ptr(a))
+        ldy = _row_stride(y, M, N)
+    status = L.fp8_block_linear(a.data_ptr(), M, K, lda if M > 1 else K or 1, qw.data_ptr(), N, ld, s_w.data_ptr(),
+                                None if bias is None else bias.data_ptr(), y.data_ptr(), ldy, wp, wn, _stream_ptr(a))
     if status:
         raise FP8Error(status, "fp8_block_linear")
     return y
@@ -543,7 +548,7 @@ def fp8_moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int
     ids = torch.empty((T, k), dtype=torch.int32, device=device)
     weights = torch.empty((T, k), dtype=torch.float32, device=device)
     status = (_lib or lib()).fp8_moe_route(
-        logits.data_ptr(), bf16, T, E, ld if ld > E else E, kind, None if bias is None else bias.data_ptr(), groups,
+        logits.data_ptr(), bf16, T, E, ld if T > 1 else E, kind, None if bias is None else bias.data_ptr(), groups,
         groups if keep_groups is None else keep_groups, k, 1 if renormalize else 0, factor, ids.data_ptr(),
         weights.data_ptr(), _stream_ptr(logits))
     if status:
@@ -574,9 +579,9 @@ def fp8_moe_experts(x, ids, weights, qw13, s13, qw2, s2, out=None, ws=None):
     L = _lib or lib()
     wp, wn, ws = _scratch(ws, L.fp8_moe_workspace_bytes(T, k, E, H, I), x)
     y = _out_bf16(out, T, H, x)
-    status = L.fp8_moe_experts(x.data_ptr(), T, H, max(x.stride(0), H, 1), ids.data_ptr(), weights.data_ptr(), k,
+    status = L.fp8_moe_experts(x.data_ptr(), T, H, _row_stride(x, T, H), ids.data_ptr(), weights.data_ptr(), k,
                                qw13.data_ptr(), ld13, s13.data_ptr(), qw2.data_ptr(), ld2, s2.data_ptr(), E, I,
-                               y.data_ptr(), max(y.stride(0), H, 1), wp, wn, _stream_ptr(x))
+                               y.data_ptr(), _row_stride(y, T, H), wp, wn, _stream_ptr(x))
     if status:
         raise FP8Error(status, "fp8_moe_experts")
     return y
