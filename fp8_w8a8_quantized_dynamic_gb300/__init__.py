@@ -84,6 +84,8 @@ _SIGNATURES = {
                                _vp, _i64, _vp, _sz, _vp]),
     "fp8_last_device_status": (_int, [_vp]),
     "fp8_selftest_timeout": (_int, [_i64, _vp]),
+    "fp8_block_selftest_timeout": (_int, [_int, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
+                                          _i64, _vp]),
     "fp8_status_string": (ctypes.c_char_p, [_int]),
 }
 
@@ -592,6 +594,17 @@ def fp8_selftest_timeout(limit_ns: int = 20_000_000, stream=None) -> int:
     torch = _torch()
     s = stream if stream is not None else torch.cuda.current_stream().cuda_stream
     return int(lib().fp8_selftest_timeout(int(limit_ns), s))
+
+
+def fp8_block_selftest_timeout(form: int, qa, K: int, s_a, qw, s_w, out, s_out=None, stream=None) -> int:
+    """Enqueue the block-scaled product with one load withheld from its waits (forms: see the C header); returns
+    the status."""
+    if stream is None:
+        stream = _torch().cuda.current_stream().cuda_stream
+    return int(lib().fp8_block_selftest_timeout(
+        form, qa.data_ptr(), qa.shape[0], K, qa.stride(0), s_a.data_ptr(), s_a.stride(0), qw.data_ptr(), qw.shape[-2],
+        qw.shape[-1], s_w.data_ptr(), out.data_ptr(), out.stride(0), _ptr(s_out),
+        0 if s_out is None else s_out.stride(0), stream))
 
 
 def fp8_last_device_status(stream=None) -> int:

@@ -331,6 +331,51 @@ FP8_API fp8_status fp8_block_linear(const void* a_bf16, int64_t M, int64_t K, in
                   block::gemm_held_rows(M, round_up16(K)), sms, st);
 }
 
+FP8_API fp8_status fp8_block_selftest_timeout(int form, const uint8_t* qa, int64_t M, int64_t K, int64_t ldqa,
+                                              const float* s_a, int64_t lds, const uint8_t* qw, int64_t N,
+                                              int64_t ldqw, const float* s_w, void* y, int64_t ldy, float* s_y,
+                                              int64_t lds_y, fp8_stream_t stream) {
+  if (form < 0 || form > 2 || M < 1 || N < 1 || K < 1) return FP8_ERR_INVALID_ARG;
+  FP8_TRY(check_fp8_mat(qa, M, K, ldqa));
+  FP8_TRY(check_row_scales(s_a, M, K, lds));
+  if (form == 2) {
+    FP8_TRY(check_fp8_mat(qw, N, K, ldqw));
+    FP8_TRY(check_fp8_mat(y, M, N, ldy));
+    FP8_TRY(check_row_scales(s_y, M, N, lds_y));
+    if (M > kMaxRows || s_w == nullptr) return FP8_ERR_INVALID_ARG;
+    if (!aligned(s_w, 4)) return FP8_ERR_MISALIGNED;
+  } else {
+    FP8_TRY(check_product(M, K, qw, N, ldqw, s_w, nullptr, y, ldy));
+    if (N % 8 != 0 || ldy % 8 != 0) return FP8_ERR_INVALID_ARG;
+    if (!aligned(y, 16)) return FP8_ERR_MISALIGNED;
+    if (form == 1 && K <= block::kBlock) return FP8_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  block::GemmArgs g = {};
+  g.qa = qa;
+  g.rows = g.held_rows = M;
+  g.lda = ldqa;
+  g.s_a = s_a;
+  g.lds_a = lds;
+  g.qw = qw;
+  g.mats = form == 2 ? 2 : 1;
+  g.ldw = ldqw;
+  g.s_w = s_w;
+  g.N = N;
+  g.K = K;
+  g.y = static_cast<uint16_t*>(y);
+  g.ldy = ldy;
+  g.qh = static_cast<uint8_t*>(y);
+  g.ldh = ldy;
+  g.s_h = s_y;
+  g.lds_h = lds_y;
+  return block::gemm_launch_withheld(g, form == 2 ? block::kOutSwiglu : block::kOutBf16, form == 1 ? 2 : 1, sms,
+                                     reinterpret_cast<cudaStream_t>(stream))
+             ? FP8_OK
+             : FP8_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------------------
 // mixture of experts
 // ---------------------------------------------------------------------------

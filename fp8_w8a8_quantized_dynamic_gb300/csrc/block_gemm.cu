@@ -40,9 +40,11 @@
 // was built and measured slower, 540 against 300 us at 8192 x 4096 x 8192: its commits and the peer's
 // arrivals cross the cluster in every block, and two tensor-memory buffers cannot hide that.
 //
-// Every wait is bounded; on expiry the kernel records an error, all roles run to the end of
-// their loops without waiting or storing, copies and MMAs in flight are drained, and the tensor
-// memory is freed.
+// Every wait is bounded; on expiry the kernel records an error and each role leaves its loops at the
+// first wait of its own that gives up: nothing is issued for a slot that was not handed back, and a
+// warp whose waits did not all succeed stores nothing of its tile (with SwiGLU none of the warps that
+// meet for its rows does, in a split tile none of the cluster's CTAs). Copies and MMAs in flight are
+// drained, and the tensor memory is freed.
 
 #include "block_gemm.h"
 
@@ -221,7 +223,11 @@ __device__ __forceinline__ uint32_t codes4(uint64_t p01, uint64_t p23, const Exa
 
 constexpr int kOutBf16Any = 3;  // kOutBf16 with rows of any alignment and width
 
-template <int BN, int kOut, bool kSplit>
+// kWithhold (the failure-path self-test): CTA 0 does not load the last K block of its first tile, so the
+// waits for it run out, after kWithheldNs.
+constexpr unsigned long long kWithheldNs = 20000000ull;
+
+template <int BN, int kOut, bool kSplit, bool kWithhold>
 __global__ void __launch_bounds__(Tile<BN, kSplit>::threads, 1)
 block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                   const __grid_constant__ Params p) {
@@ -244,8 +250,11 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &ctl->abort_flag;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return mbar_wait_short(smem_u32(bar), parity, abort_flag, &g_block_gemm_error);
+    return mbar_wait_short(smem_u32(bar), parity, abort_flag, &g_block_gemm_error,
+                           kWithhold ? kWithheldNs : kWaitLimitNs);
   };
+  // for a whole warp: whether all of its lanes' waits succeeded
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
   if (threadIdx.x == 0) {
     asm volatile("prefetch.tensormap [%0];" :: "l"(reinterpret_cast<uint64_t>(&tmap_a)) : "memory");
@@ -323,7 +332,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         bool ok = true;
         for (int kb = kb_begin(); kb < kb_end(); ++kb, ++it) {
           const int s = it % kStages;
-          if (!wait(&ctl->empty[s], ((it / kStages) & 1u) ^ 1u)) {
+          if (!wait(&ctl->empty[s], ((it / kStages) & 1u) ^ 1u) ||
+              (kWithhold && blockIdx.x == 0 && kb == kb_end() - 1)) {
             ok = false;
             break;
           }
@@ -381,7 +391,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
    } else if (warp == 2) {
     // ---------------- scale loader ----------------
     uint32_t slot_no = 0;
-    for (int u = first_unit(); u < units; u += unit_stride()) {
+    bool ok = true;
+    for (int u = first_unit(); ok && u < units; u += unit_stride()) {
       int expert, row0, row_end, n_idx;
       decode(u, expert, row0, row_end, n_idx);
       const int n0 = n_idx * kTileN;
@@ -391,8 +402,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       const float* sw = p.s_w + (int64_t(mat) * p.nb + min(col / kBlock, p.nb - 1)) * p.kb;
       for (int kb0 = kb_begin(); kb0 < kb_end(); kb0 += kScaleKb, ++slot_no) {
         const int slot = slot_no % kScaleSlots;
-        wait(&ctl->sempty[slot], ((slot_no / kScaleSlots) & 1u) ^ 1u);
-        __syncwarp();
+        // (a slot that was not handed back may still expect bytes of its last fill: never filled again)
+        if (!(ok = wait_all(&ctl->sempty[slot], ((slot_no / kScaleSlots) & 1u) ^ 1u))) break;
         const uint32_t bar = smem_u32(&ctl->sfull[slot]);
         if (p.bulk_scales) {
           // one bulk copy a block: rows [a0, a0 + n), whole 16-byte pieces that each hold one of the
@@ -438,7 +449,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     const uint32_t tbase = tmem_base + (uint32_t(quarter * 32) << 16) +
                            (kOut == kOutSwiglu ? (group >> 1) * 128 + (group & 1) * 32 : group * kCols);
     uint32_t it = 0, tile_no = 0, slot_no = 0;
-    for (int u = first_unit(); u < units; u += unit_stride(), ++tile_no) {
+    int u = first_unit();
+    for (; u < units; u += unit_stride(), ++tile_no) {
       int expert, row0, row_end, n_idx;
       decode(u, expert, row0, row_end, n_idx);
       const int n0 = n_idx * kTileN;
@@ -448,13 +460,10 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
       uint64_t g2 = 0, u2 = 0;  // this block's scales of the group's first and second half of columns
-      // the scales of block kb; the slot is handed back with its last block
+      // the scales of block kb; the slot is handed back with its last block. False: they did not come.
       auto next_scales = [&](int kb) {
         const int slot = slot_no % kScaleSlots, j = (kb - kb_begin()) % kScaleKb;
-        if (j == 0) {
-          wait(&ctl->sfull[slot], (slot_no / kScaleSlots) & 1u);
-          __syncwarp();
-        }
+        if (j == 0 && !wait_all(&ctl->sfull[slot], (slot_no / kScaleSlots) & 1u)) return false;
         const float sa = ctl->s_row[slot][j][(row0 & 3) + row_in_tile];
         const float2 sw = *reinterpret_cast<const float2*>(&ctl->s_col[slot][j][2 * (group / (kGroups / 2))]);
         if (j == kScaleKb - 1 || kb == kb_end() - 1) {
@@ -464,13 +473,13 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         }
         g2 = pack_f32x2(sa * sw.x, sa * sw.x);
         u2 = kOut == kOutSwiglu ? pack_f32x2(sa * sw.y, sa * sw.y) : g2;
+        return true;
       };
+      bool ok = true;
       for (int kb = kb_begin(); kb < kb_end(); ++kb, ++it) {
         constexpr int kChunks = kCols / kChunk;
         const int b = it % kBufs;
-        next_scales(kb);
-        wait(&ctl->tfull[b], (it / kBufs) & 1u);
-        __syncwarp();
+        if (!(ok = next_scales(kb) && wait_all(&ctl->tfull[b], (it / kBufs) & 1u))) break;
         tmem_fence_after();
         const uint32_t tempty = smem_u32(&ctl->tempty[b]);
 #pragma unroll
@@ -484,6 +493,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           add_scaled(acc + c * (kChunk / 2), part, 2 * c < kChunks ? g2 : u2);
         }
       }
+      if (!ok) break;
       if constexpr (kSplit) {
         // this slice's sums go to the CTAs that own their columns: [slice][column][row], columns far enough
         // apart that a warp's loads of whole rows below fall on 32 banks, as its stores here do
@@ -503,7 +513,6 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         }
         continue;
       }
-      const bool store = *abort_flag == 0;
       // each thread writes its row's columns, a 32-byte sector a store
       if constexpr (kOut == kOutSwiglu) {
         // columns [32 group, 32 group + 32) of the tile's 128-wide block of h
@@ -522,7 +531,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         for (int o = 0; o < kGroups; ++o) m = max(m, ctl->hmax[tile_no & 1][o][row_in_tile]);
         const float s = scale_from_amax<kFmtE4M3>(__uint_as_float(m));
         const ExactScale k = make_exact_scale(s);
-        if (store && live) {
+        // a warp whose waits gave up comes to the meeting without a maximum, after it raised (saw) the flag
+        if (*abort_flag == 0 && live) {
           uint32_t w[8];
 #pragma unroll
           for (int v = 0; v < 8; ++v) w[v] = codes4(acc[v * 2], acc[v * 2 + 1], k, s);
@@ -535,7 +545,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       } else if constexpr (kOut == kOutF32) {
         const int col0 = n0 + group * kCols;
         float* dst = p.y32 + int64_t(row) * p.ldy32 + col0;
-        if (store && live) {
+        if (live) {
 #pragma unroll
           for (int q = 0; q < kCols / 8; ++q) {
             const uint64_t* a = acc + q * 4;
@@ -562,7 +572,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         };
         if constexpr (kOut == kOutBf16) {
           uint16_t* dst = p.y + int64_t(row) * p.ldy + col0;
-          if (store && live) {
+          if (live) {
 #pragma unroll
             for (int q = 0; q < kCols / 16; ++q) {
               if (col0 + q * 16 >= p.N) break;  // N: whole eights
@@ -577,7 +587,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
               }
             }
           }
-        } else if (store) {
+        } else {
           // rows that start and end anywhere: through shared memory, two rows' 16 columns a store (8192 x 4096 x
           // 8191: 285 us; two bytes of 32 rows a store: 768)
           uint32_t(&mine)[32][9] = ctl->staged[warp - kFirstPromoWarp];
@@ -601,11 +611,18 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         }
       }
     }
+    // a warp that left early still comes to the meetings of its remaining tiles, where the others wait
+    if constexpr (kOut == kOutSwiglu)
+      for (; u < units; u += unit_stride())
+        asm volatile("bar.sync %0, %1;" :: "r"(1 + quarter), "n"(32 * kGroups) : "memory");
   }
 
   if constexpr (kSplit) {
+    // a slice that is not whole is nobody's to add: the threads that know raise every CTA's flag
+    if (*abort_flag != 0)
+      for (int r = 0; r < (1 << p.split_log2); ++r) st_cluster_u32(map_to_rank(smem_u32(&ctl->abort_flag), r), 1u);
     __syncwarp();
-    pair_sync();  // all threads of the cluster: every slice's sums have arrived
+    pair_sync();  // all threads of the cluster: every slice's sums (or flags) have arrived
     if (warp >= kFirstPromoWarp && first_unit() < units && *abort_flag == 0) {
       // the owner adds the slices in order: a thread four columns of every `step`-th row, neighbouring
       // threads neighbouring columns
@@ -699,9 +716,9 @@ int slots_of(const void* kfn, int threads, int split, int num_sms) {
   return slots;
 }
 
-template <int BN, int kOut, bool kSplit = false>
+template <int BN, int kOut, bool kSplit = false, bool kWithhold = false>
 bool launch_tile(const GemmArgs& a, int split, int num_sms, cudaStream_t st) {
-  auto kfn = block_gemm_kernel<BN, kOut, kSplit>;
+  auto kfn = block_gemm_kernel<BN, kOut, kSplit, kWithhold>;
   const int slots = slots_of(reinterpret_cast<const void*>(kfn), Tile<BN, kSplit>::threads, split, num_sms);
   if (slots <= 0) return false;
   Params p = {};
@@ -769,8 +786,8 @@ TileChoice choose_tile(int64_t m_tiles, int64_t N, int64_t kb, int num_sms) {
   consider(128, 1, num_sms, 0.36);
   consider(64, 1, num_sms, 0.30);
   for (int split = 2; split <= 8; split *= 2) {
-    consider(128, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<128, kOut, true>), Tile<128, true>::threads, split, num_sms), 0.36);
-    consider(64, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<64, kOut, true>), Tile<64, true>::threads, split, num_sms), 0.30);
+    consider(128, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<128, kOut, true, false>), Tile<128, true>::threads, split, num_sms), 0.36);
+    consider(64, split, slots_of(reinterpret_cast<const void*>(block_gemm_kernel<64, kOut, true, false>), Tile<64, true>::threads, split, num_sms), 0.30);
   }
   return best;
 }
@@ -806,6 +823,17 @@ bool gemm_launch(const GemmArgs& a, Out out, int num_sms, cudaStream_t stream) {
     case kOutBf16: return launch_any<kOutBf16>(a, num_sms, stream);
     case kOutSwiglu: return launch_any<kOutSwiglu>(a, num_sms, stream);
     case kOutF32: return launch_any<kOutF32>(a, num_sms, stream);
+  }
+  return false;
+}
+
+bool gemm_launch_withheld(const GemmArgs& a, Out out, int split, int num_sms, cudaStream_t stream) {
+  switch (out) {
+    case kOutBf16:
+      return split > 1 ? launch_tile<64, kOutBf16, true, true>(a, split, num_sms, stream)
+                       : launch_tile<256, kOutBf16, false, true>(a, 1, num_sms, stream);
+    case kOutSwiglu: return launch_tile<256, kOutSwiglu, false, true>(a, 1, num_sms, stream);
+    case kOutF32: break;
   }
   return false;
 }

@@ -65,6 +65,10 @@ int64_t gemm_held_rows(int64_t rows, int64_t ld);
 // Enqueues the product. False when a tensor map could not be encoded or the launch failed.
 bool gemm_launch(const GemmArgs& a, Out out, int num_sms, cudaStream_t stream);
 
+// The product with one load withheld from its waits, for the failure-path self-test: whole tiles of 256
+// columns, 64 with K shared by `split` CTAs, or SwiGLU.
+bool gemm_launch_withheld(const GemmArgs& a, Out out, int split, int num_sms, cudaStream_t stream);
+
 // Device-side error bits recorded by this file's kernels on the current device (read, then cleared).
 unsigned int gemm_read_and_clear_error();
 

@@ -459,11 +459,11 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
 // The same for waits in a tight hand-over: the barrier is tried some tens of times (each try
 // suspends the thread for a while) before the first, slow read of the timer.
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                                unsigned int* err) {
+                                                unsigned int* err, unsigned long long limit_ns = kWaitLimitNs) {
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
     if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_bounded(bar, parity, abort_flag, err);
+  return mbar_wait_bounded(bar, parity, abort_flag, err, limit_ns);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {

@@ -460,6 +460,22 @@ fp8_status fp8_last_device_status(fp8_stream_t stream);
  */
 fp8_status fp8_selftest_timeout(int64_t limit_ns, fp8_stream_t stream);
 
+/*
+ * The same for the block-scaled product: enqueues it with one load withheld
+ * from its waits (the last K block of the first tile of its first CTA), so that
+ * they run out after 20 ms, the CTA leaves its work and the next
+ * fp8_last_device_status reports FP8_ERR_TIMEOUT once. That tile, and what the
+ * CTA had still to do, keeps what Y held; all else is the product. form 0:
+ * tiles of 256 columns, Y bf16 [M, N] (N and ldy multiples of 8, Y 16-byte
+ * aligned); 1: tiles of 64, each shared by two CTAs (K > 128); 2: the gate and
+ * up matrices qw [2][N, ldqw], s_w [2][NB][KB] with SwiGLU, Y the codes
+ * [M, ldy] and s_y [NB][lds_y] of h (s_y, lds_y unused otherwise). M, N, K >= 1.
+ */
+fp8_status fp8_block_selftest_timeout(int form, const uint8_t* qa, int64_t M, int64_t K, int64_t ldqa,
+                                      const float* s_a, int64_t lds, const uint8_t* qw, int64_t N, int64_t ldqw,
+                                      const float* s_w, void* y, int64_t ldy, float* s_y, int64_t lds_y,
+                                      fp8_stream_t stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 const char* fp8_status_string(fp8_status status);
 
