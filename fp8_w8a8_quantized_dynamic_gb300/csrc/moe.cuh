@@ -180,7 +180,7 @@ route_kernel(const T* __restrict__ logits, const __grid_constant__ RouteParams p
         // x == max covers max = +inf, whose difference is NaN
         const float e = c[i] == mx ? 1.0f : expf(c[i] - mx);
         sum += e0 + i < E ? e : 0.0f;
-        if (p.bias) c[i] = e;
+        if (p.bias) c[i] = mx == -INFINITY ? 0.0f : e;  // a row of only -inf: p = 0, the bias alone chooses
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

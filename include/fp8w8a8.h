@@ -364,7 +364,8 @@ fp8_status fp8_block_linear(const void* a_bf16, int64_t M, int64_t K, int64_t ld
  * ids[t, 0..k) (int32): the experts with the largest c in descending order, ties
  * to the lowest index; weights[t, j] (fp32) = p of ids[t, j], divided by
  * (their sum + 1e-20) when renormalize is 1, times factor.
- * A NaN logit counts as -inf. A softmax row of only -inf gives weights 0.
+ * A NaN logit counts as -inf. A softmax row of only -inf has p = 0 (weights 0;
+ * the bias, if any, alone orders its experts).
  * Limits: E <= 512, k <= 32, groups <= 32, E a multiple of groups,
  * k <= keep_groups * E / groups (else FP8_ERR_INVALID_ARG).
  */
