@@ -205,10 +205,6 @@ __device__ __forceinline__ void st_global_v8(void* p, uint32_t a, uint32_t b, ui
                :: "l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
 }
 
-// silu(g) * u in fp32; exp and the reciprocal by the hardware approximations (a few 2^-23), far
-// below the 2^-4 spacing of the codes h is quantized to.
-__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-
 // e4m3 codes of four fp32 values divided by the scale of k (any scale: the division when the
 // exact-quotient form does not cover it).
 __device__ __forceinline__ uint32_t codes4(uint64_t p01, uint64_t p23, const ExactScale& k, float s) {

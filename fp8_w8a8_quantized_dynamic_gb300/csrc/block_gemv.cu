@@ -407,7 +407,7 @@ block_gemv_kernel(const __grid_constant__ GvParams p) {
           }
           if constexpr (kGated) {
             // rows of h are whole sixteens: columns past N come from clamped rows and are zero
-            const float h = n < p.N ? __fdividef(v[0], 1.0f + __expf(-v[0])) * v[1] : 0.0f;
+            const float h = n < p.N ? swiglu(v[0], v[1]) : 0.0f;
             if (n < p.ldy32) p.y32[int64_t(row0 + r) * p.ldy32 + n] = h;
           } else if (n < p.N) {
             if (p.bias != nullptr) v[0] += bf16_bits_to_float(p.bias[n]);

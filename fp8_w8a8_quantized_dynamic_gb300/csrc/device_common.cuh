@@ -210,6 +210,17 @@ __device__ __forceinline__ uint2 quant8_bf16(uint4 v, const Quantizer& q) {
   return bad == 0 ? r : quant8_bf16_fix<F>(v, r, bad, q.s, q.r);
 }
 
+// silu(g) * u in fp32, as g / (1 + e^-g) for g >= 0 and g e^g / (1 + e^g) below: the exponential lies in
+// [0, 1], so the denominator stays in [1, 2] and the numerator keeps its range down to the subnormal numbers
+// (1 + e^-g passes 2^126, where the fast division gives 0, from g = -87.4 on). The hardware exp and division
+// are off by a few 2^-23 relative and the exp by another |g| * 2^-23 (it rounds g log2 e): against the
+// 2^-4 spacing of the codes h is quantized to, a code differs from the accurate functions' only within
+// that much of a rounding boundary.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  const float t = __expf(-fabsf(g));
+  return __fdividef(g < 0.0f ? g * t : g, 1.0f + t) * u;
+}
+
 __device__ __forceinline__ float bf16_bits_to_float(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
 
 // ---------------------------------------------------------------------------

@@ -1,4 +1,5 @@
-"""Wider GPU tests of the choice of experts and of the experts' networks: rows with nothing to choose from."""
+"""Wider GPU tests of the choice of experts and of the experts' networks: rows with nothing to choose from,
+gates far below zero."""
 
 import numpy as np
 import pytest
@@ -32,3 +33,25 @@ def test_softmax_row_of_only_masks_follows_the_bias(groups, keep, dtype):
     assert ref[1].tolist() == [63, 62, 61, 60, 59]
     assert ids.cpu().numpy().tolist() == ref.tolist()
     assert not w[1].any() and np.allclose(w.cpu().numpy(), w_ref, rtol=(8 + E + k) * 2.0 ** -23, atol=1e-37)
+
+
+@pytest.mark.parametrize("T", [1, 5, 300])
+@pytest.mark.parametrize("gate", [-80.0, -88.0, 88.0])
+def test_experts_far_gates(T, gate):
+    """silu(g) stays itself where exp(-g) is near the largest fp32 number: -88 e^-88 = -5.3e-37 is a normal
+    one. With |g| = 88 a fp32 exp of g, itself off by 2**-23 of 88, is off by about 1e-5: far below 0.01."""
+    H, I, u = 128, 128, 2.0 ** 40
+    x = torch.zeros((T, H))
+    x[:, 0] = 1.0
+    x = x.to(torch.bfloat16)
+    w13 = torch.zeros((1, 2, I, H))
+    w13[0, 0, :, 0], w13[0, 1, :, 0] = gate, u
+    w2 = torch.randn((1, H, I), generator=torch.Generator().manual_seed(2))
+    q13, s13 = F.fp8_block_quantize_weight(w13.to(torch.bfloat16).to(DEV))
+    q2, s2 = F.fp8_block_quantize_weight(w2.to(torch.bfloat16).to(DEV))
+    ids, w = torch.zeros((T, 1), dtype=torch.int32), torch.ones((T, 1))
+    y = f32(F.fp8_moe_experts(x.to(DEV), ids.to(DEV), w.to(DEV), q13, s13, q2, s2)).astype(np.float64)
+    ref, _ = B.experts(f32(x), ids.numpy(), w.numpy(), q13.cpu().numpy(), s13.cpu().numpy(), q2.cpu().numpy(),
+                       s2.cpu().numpy())
+    assert np.linalg.norm(ref) > 1e-24
+    assert np.linalg.norm(y - ref) <= 0.01 * np.linalg.norm(ref)
