@@ -30,7 +30,7 @@ int elementwise_grid(int64_t items, int per_cta, int sms, int ctas_per_sm) {
 // A -> codes and scales; pos / copies: see the kernel.
 fp8_status launch_quantize_rows(const BF16Mat& a, uint8_t* q, int64_t ldq, float* s, int64_t lds, const int* pos,
                                 int copies, int sms, cudaStream_t st) {
-  const int64_t units = a.rows * blocks_of(a.cols) * 8;
+  const int64_t units = a.rows * blocks_of(ldq) * 8;
   const int grid = elementwise_grid(units, block::kQThreads, sms, 8);
   auto go = [&](auto kernel) {
     return launch(kernel, dim3(grid), dim3(block::kQThreads), 0, st, true, dim3(1, 1, 1), a.p, a.rows, a.cols, a.ld,
@@ -251,13 +251,13 @@ FP8_API fp8_status fp8_block_quantize_weight(const void* w_bf16, int64_t B, int6
   FP8_TRY(check_fp8_mat(qw, N, K, ldq));
   if (B < 0 || B > kMaxDim || (B > 1 && mat_stride < 0)) return FP8_ERR_INVALID_ARG;
   if (!aligned(s_w, 4)) return FP8_ERR_MISALIGNED;
-  if (B == 0 || N == 0 || K == 0) return FP8_OK;
-  if (s_w == nullptr) return FP8_ERR_INVALID_ARG;
+  if (B == 0 || N == 0) return FP8_OK;
+  if (K > 0 && s_w == nullptr) return FP8_ERR_INVALID_ARG;
   int sms = 0;
   FP8_TRY(current_device(&sms));
   const BF16Mat W{static_cast<const uint16_t*>(w_bf16), N, K, ldw};
   const int vec = W.vec() && (B == 1 || mat_stride % 8 == 0);
-  const int64_t blocks = B * blocks_of(N) * blocks_of(K);
+  const int64_t blocks = B * blocks_of(N) * blocks_of(ldq);
   // no early programmatic trigger: a following product may read qW before its own wait
   return launch(block::quantize_128x128_kernel, dim3(elementwise_grid(blocks, 1, sms, 64)), dim3(block::kQThreads), 0,
                 reinterpret_cast<cudaStream_t>(stream), false, dim3(1, 1, 1), W.p, B, N, K, ldw, mat_stride, vec, qw,
@@ -269,7 +269,7 @@ FP8_API fp8_status fp8_block_quantize_act(const void* a_bf16, int64_t M, int64_t
   FP8_TRY(check_bf16_mat(a_bf16, M, K, lda));
   FP8_TRY(check_fp8_mat(qa, M, K, ldq));
   FP8_TRY(check_row_scales(s_a, M, K, lds));
-  if (M == 0 || K == 0) return FP8_OK;
+  if (M == 0) return FP8_OK;
   int sms = 0;
   FP8_TRY(current_device(&sms));
   const BF16Mat A{static_cast<const uint16_t*>(a_bf16), M, K, lda};

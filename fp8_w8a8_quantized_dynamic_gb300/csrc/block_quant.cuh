@@ -47,8 +47,8 @@ __device__ __forceinline__ uint32_t max_of_eight(uint32_t m2) {
   return m2;
 }
 
-// A [rows, cols] -> q [rows or sorted rows, ldq], s [K blocks][lds]. Eight lanes hold a block of
-// a row, sixteen columns each. copies == 0: row r of A goes to row r. copies > 0: it goes to the
+// A [rows, cols] -> q [rows or sorted rows, ldq], zero from cols on, s [K blocks][lds]. Eight lanes hold a
+// block of a row, sixteen columns each. copies == 0: row r of A goes to row r. copies > 0: it goes to the
 // rows pos[r * copies + j], j < copies (a negative one is skipped): the rows of many experts,
 // each token quantized once. Bound by HBM: 32 registers a thread let eight CTAs on an SM, whose loads
 // cover its latency: 16384 x 4096 in 36.0 us (201 MB, 5.6 TB/s; 42.4 with five CTAs). Rows of 4095, which
@@ -60,7 +60,7 @@ quantize_rows_1x128_kernel(const uint16_t* __restrict__ a, int64_t rows, int64_t
                            const int* __restrict__ pos, int copies) {
   pdl_trigger();
   pdl_wait();
-  const Idx upr = static_cast<Idx>((cols + kBlock - 1) / kBlock) * 8;  // sixteen-column units of a row, whole blocks
+  const Idx upr = static_cast<Idx>((ldq + kBlock - 1) / kBlock) * 8;  // sixteen-column units of a row, whole blocks
   const Idx units = static_cast<Idx>(rows) * upr;
   const Idx stride = static_cast<Idx>(gridDim.x) * kQThreads;
   const Idx rounded = (units + 31) / 32 * 32;  // whole warps take part in the shuffles
@@ -69,37 +69,38 @@ quantize_rows_1x128_kernel(const uint16_t* __restrict__ a, int64_t rows, int64_t
     const int64_t i = u - static_cast<Idx>(r) * upr;
     const int64_t c = i * 16;
     Sixteen v = {};
-    if (u < units && c < cols) v = load16(a + r * ld, c, cols, vec);
+    const bool in = u < units && c < cols;
+    if (in) v = load16(a + r * ld, c, cols, vec);
     const float sc = scale_from_amax<kFmtE4M3>(u16x2_max_to_float(max_of_eight(amax16(v))));
     const ExactScale k = make_exact_scale(sc);
     const uint4 o = codes16(v, k, sc);
     if (u >= units) continue;
     if (copies == 0) {
       if (c < ldq) *reinterpret_cast<uint4*>(q + r * ldq + c) = o;
-      if ((i & 7) == 0) s[(i >> 3) * lds + r] = sc;
+      if ((i & 7) == 0 && in) s[(i >> 3) * lds + r] = sc;
     } else {
       for (int j = 0; j < copies; ++j) {
         const int d = pos[r * copies + j];
         if (d < 0) continue;
         if (c < ldq) *reinterpret_cast<uint4*>(q + int64_t(d) * ldq + c) = o;
-        if ((i & 7) == 0) s[(i >> 3) * lds + d] = sc;
+        if ((i & 7) == 0 && in) s[(i >> 3) * lds + d] = sc;
       }
     }
   }
 }
 
-// W [mats][N, K] -> q [mats][N, ldq], s [mats][N blocks][K blocks]. One CTA a 128 x 128 block: a
-// thread holds half a row of it (64 columns) in registers between the maximum and the codes. Runs once,
-// when weights are loaded.
+// W [mats][N, K] -> q [mats][N, ldq], zero from K on, s [mats][N blocks][K blocks]. One CTA a 128 x 128
+// block (past the last of K, to ldq: of zeros, without a scale): a thread holds half a row of it (64 columns)
+// in registers between the maximum and the codes. Runs once, when weights are loaded.
 __global__ void __launch_bounds__(kQThreads)
 quantize_128x128_kernel(const uint16_t* __restrict__ w, int64_t mats, int64_t N, int64_t K, int64_t ld,
                         int64_t mat_stride, int vec, uint8_t* __restrict__ q, int64_t ldq, float* __restrict__ s) {
   __shared__ uint32_t red[kQThreads / 32];
   pdl_wait();
-  const int64_t nb = (N + kBlock - 1) / kBlock, kb = (K + kBlock - 1) / kBlock;
-  for (int64_t blk = blockIdx.x; blk < mats * nb * kb; blk += gridDim.x) {
-    const int64_t m = blk / (nb * kb), in = blk - m * nb * kb;
-    const int64_t j = in / kb, b = in - j * kb;
+  const int64_t nb = (N + kBlock - 1) / kBlock, kb = (K + kBlock - 1) / kBlock, ldb = (ldq + kBlock - 1) / kBlock;
+  for (int64_t blk = blockIdx.x; blk < mats * nb * ldb; blk += gridDim.x) {
+    const int64_t m = blk / (nb * ldb), in = blk - m * nb * ldb;
+    const int64_t j = in / ldb, b = in - j * ldb;
     const int64_t r = j * kBlock + (threadIdx.x >> 1);
     const int64_t c0 = b * kBlock + (threadIdx.x & 1) * 64;
     Sixteen v[4] = {};
@@ -120,7 +121,7 @@ quantize_128x128_kernel(const uint16_t* __restrict__ w, int64_t mats, int64_t N,
     for (int i = 0; i < kQThreads / 32; ++i) mx = max(mx, red[i]);
     const float sc = scale_from_amax<kFmtE4M3>(__uint_as_float(mx << 16));
     const ExactScale k = make_exact_scale(sc);
-    if (threadIdx.x == 0) s[blk] = sc;
+    if (threadIdx.x == 0 && b < kb) s[(m * nb + j) * kb + b] = sc;
     if (r < N) {
       uint8_t* dst = q + (m * N + r) * ldq;
 #pragma unroll

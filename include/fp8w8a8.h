@@ -315,7 +315,8 @@ fp8_status fp8_linear_weight_only(const void* a_bf16, int64_t M, int64_t K, int6
  * wider range of e5m2. Sums are fp32. A block that holds a NaN has a NaN
  * scale, so its token's (weights: its 128 rows') results are NaN; an infinity
  * gives an infinite scale and NaN as well. Other rows are not affected.
- * FP8 matrices are laid out as above (ld a multiple of 16, zero tails).
+ * FP8 matrices are laid out as above (ld a multiple of 16; the quantizers write bytes
+ * [K, ld) of each row as zero).
  * ---------------------------------------------------------------------------
  */
 
