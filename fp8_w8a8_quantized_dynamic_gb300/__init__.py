@@ -19,6 +19,9 @@ Typical use::
     y = fp8_block_linear(a, qw, s_w, bias)           # activations: a scale per row and 128 columns
     ids, weights = fp8_moe_route(logits, k, score="sigmoid", renormalize=True)
     y = fp8_moe_experts(x, ids, weights, qw13, s13, qw2, s2)  # the chosen experts, block-scaled
+
+Kernels are launched on the current CUDA device and its current stream; tensors of another device are refused
+(ValueError).
 """
 
 from __future__ import annotations
@@ -144,14 +147,27 @@ def _torch():
     return _torch_module
 
 
+def _stream_query(torch):
+    """index -> the current stream of CUDA device `index`, which has to be the current device: kernels are
+    launched there, and another device's stream would put them in no order with that device's work. The raw
+    query takes a tenth of a microsecond where building a Stream object takes two, a good part of a small
+    call's time."""
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+    def query(index):
+        if index != current():
+            raise ValueError(f"tensors are on cuda:{index} and the current device is cuda:{current()} "
+                             f"(call within torch.cuda.device({index}))")
+        return stream(index)
+    return query
+
+
 def _stream_ptr(t) -> int:
-    """The current stream of t's device. The raw query takes a tenth of a microsecond where building a
-    Stream object takes two, a good part of a small call's time."""
     global _raw_stream
     if _raw_stream is None:
-        torch = _torch()
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _raw_stream = _stream_query(_torch())
     return _raw_stream(t.get_device())
 
 

@@ -149,3 +149,44 @@ def test_wider_rows_keep_their_stride(rec):
     assert rec.calls["fp8_block_linear"][3] == 300 and rec.calls["fp8_block_linear"][10] == 100
     F.fp8_block_quantize_weight(Fake(zeros(3, 2, 20, 64)[:, 1, :, :50]))
     assert rec.calls["fp8_block_quantize_weight"][1:6] == (3, 20, 50, 64, 2 * 20 * 64)
+
+
+# ---------------------------------------------------------------------------
+# tensors of a device that is not the current one
+# ---------------------------------------------------------------------------
+
+def test_the_stream_is_the_current_devices():
+    from types import SimpleNamespace as NS
+    raw = NS(_C=NS(_cuda_getCurrentRawStream=lambda i: 100 + i, _cuda_getDevice=lambda: 1))
+    older = NS(_C=NS(), cuda=NS(current_device=lambda: 1, current_stream=lambda i: NS(cuda_stream=100 + i)))
+    for torch_like in (raw, older):
+        stream = F._stream_query(torch_like)
+        assert stream(1) == 101
+        with pytest.raises(ValueError, match="cuda:0.*current device is cuda:1"):
+            stream(0)
+
+
+def test_tensors_of_another_device_are_refused_by_every_wrapper(rec, monkeypatch):
+    from types import SimpleNamespace as NS
+    monkeypatch.setattr(F, "_raw_stream", F._stream_query(NS(_C=NS(_cuda_getCurrentRawStream=lambda i: 0,
+                                                                   _cuda_getDevice=lambda: 0))))
+
+    def on1(t):
+        return Fake(t, 1)
+    a, x = on1(zeros(4, 256)), on1(zeros(4, 16))
+    qw, s_w, one = on1(zeros(64, 256, dtype=torch.uint8)), on1(torch.ones(1, 2)), on1(torch.ones(1))
+    qa, s_a = on1(zeros(4, 256, dtype=torch.uint8)), on1(torch.ones(2, 4))
+    experts = [on1(t._t) for t in expert_operands()]
+    for call in (lambda: F.fp8_quantize_weight(a), lambda: F.fp8_quantize_act(a),
+                 lambda: F.fp8_scaled_mm(qa, 256, one, qw, one), lambda: F.fp8_linear(a, qw, one, ws=zeros(1)),
+                 lambda: F.fp8_linear_static(a, one, qw, one, ws=zeros(1)),
+                 lambda: F.fp8_linear_ex(a, qw, one, ws=zeros(1)),
+                 lambda: F.fp8_linear_weight_only(a, qw, one, ws=zeros(1)),
+                 lambda: F.fp8_linear_noalloc(a, qw, one), lambda: F.fp8_block_quantize_weight(a),
+                 lambda: F.fp8_block_quantize_act(a), lambda: F.fp8_block_scaled_mm(qa, 256, s_a, qw, s_w),
+                 lambda: F.fp8_block_linear(a, qw, s_w), lambda: F.fp8_moe_route(x, 2),
+                 lambda: F.fp8_moe_experts(a, *experts)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    enqueued = {name for name in rec.calls if not name.endswith("_bytes")}
+    assert not enqueued
