@@ -82,6 +82,8 @@ _SIGNATURES = {
     "fp8_block_linear": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
     "fp8_moe_route": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _int, _int, _int, _int, ctypes.c_float, _vp,
                              _vp, _vp]),
+    "fp8_moe_route_ex": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _int, _int, _int, _int, _int, ctypes.c_float,
+                                _vp, _vp, _vp]),
     "fp8_moe_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "fp8_moe_experts": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64,
                                _vp, _i64, _vp, _sz, _vp]),
@@ -540,13 +542,17 @@ def fp8_block_linear(a, qw, s_w, bias=None, out=None, ws=None):
 
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"auto": 0, "max": 1}
 
 
 def fp8_moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int = 1,
-                  keep_groups: Optional[int] = None, renormalize: bool = False, factor: float = 1.0):
+                  keep_groups: Optional[int] = None, renormalize: bool = False, factor: float = 1.0,
+                  group_score: str = "auto"):
     """Logits [T, E] (fp32 or bf16) -> (ids int32 [T, k], weights fp32 [T, k]): the k chosen experts of each
     token in descending order and their routing weights. score 'softmax' or 'sigmoid'; bias fp32 [E] steers the
-    choice only; only the keep_groups best of `groups` groups of experts take part (default: all)."""
+    choice only; only the keep_groups best of `groups` groups of experts take part (default: all).
+    group_score 'auto': a group's score is the sum of its two best choices (softmax without bias: its best one);
+    'max': its best choice in every case, as published gates without a bias have it, for sigmoid too."""
     torch = _torch_module or _torch()
     bf16 = logits.dtype is torch.bfloat16
     if not (bf16 or logits.dtype is torch.float32) or logits.dim() != 2 or not logits.is_cuda:
@@ -558,6 +564,9 @@ def fp8_moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int
     kind = _SCORES.get(score)
     if kind is None:
         raise ValueError(f"unknown score {score!r} (expected 'softmax' or 'sigmoid')")
+    group_max = _GROUP_SCORES.get(group_score)
+    if group_max is None:
+        raise ValueError(f"unknown group_score {group_score!r} (expected 'auto' or 'max')")
     if bias is not None:
         _check_dense(bias, torch.float32, (E,), logits.get_device(), "bias")
     if k < 1:
@@ -565,13 +574,20 @@ def fp8_moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int
     device = logits.device
     ids = torch.empty((T, k), dtype=torch.int32, device=device)
     weights = torch.empty((T, k), dtype=torch.float32, device=device)
-    status = (_lib or lib()).fp8_moe_route(
-        logits.data_ptr(), bf16, T, E, ld if T > 1 else E, kind, None if bias is None else bias.data_ptr(), groups,
-        groups if keep_groups is None else keep_groups, k, 1 if renormalize else 0, factor, ids.data_ptr(),
-        weights.data_ptr(), _stream_ptr(logits))
+    L = _lib or lib()
+    head = (logits.data_ptr(), bf16, T, E, ld if T > 1 else E, kind, None if bias is None else bias.data_ptr(), groups,
+            groups if keep_groups is None else keep_groups)
+    tail = (k, 1 if renormalize else 0, factor, ids.data_ptr(), weights.data_ptr(), _stream_ptr(logits))
+    status = L.fp8_moe_route_ex(*head, 1, *tail) if group_max else L.fp8_moe_route(*head, *tail)
     if status:
         raise FP8Error(status, "fp8_moe_route")
     return ids, weights
+
+
+def fp8_moe_route_ex(logits, k: int, group_score: str, score: str = "softmax", bias=None, groups: int = 1,
+                     keep_groups: Optional[int] = None, renormalize: bool = False, factor: float = 1.0):
+    """fp8_moe_route with an explicit rule of a group's score."""
+    return fp8_moe_route(logits, k, score, bias, groups, keep_groups, renormalize, factor, group_score)
 
 
 def fp8_moe_workspace_bytes(T: int, k: int, E: int, H: int, I: int) -> int:

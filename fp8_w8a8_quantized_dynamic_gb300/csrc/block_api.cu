@@ -383,9 +383,17 @@ FP8_API fp8_status fp8_block_selftest_timeout(int form, const uint8_t* qa, int64
 FP8_API fp8_status fp8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int64_t ld, int sigmoid,
                                  const float* bias, int groups, int keep_groups, int k, int renormalize, float factor,
                                  int32_t* ids, float* weights, fp8_stream_t stream) {
+  return fp8_moe_route_ex(logits, logits_bf16, T, E, ld, sigmoid, bias, groups, keep_groups, 0, k, renormalize, factor,
+                          ids, weights, stream);
+}
+
+FP8_API fp8_status fp8_moe_route_ex(const void* logits, int logits_bf16, int64_t T, int64_t E, int64_t ld, int sigmoid,
+                                    const float* bias, int groups, int keep_groups, int group_max, int k,
+                                    int renormalize, float factor, int32_t* ids, float* weights,
+                                    fp8_stream_t stream) {
   if (T < 0 || T > kMaxDim || E < 1 || E > moe::kMaxExperts || ld < E) return FP8_ERR_INVALID_ARG;
   if ((logits_bf16 != 0 && logits_bf16 != 1) || (sigmoid != 0 && sigmoid != 1) ||
-      (renormalize != 0 && renormalize != 1))
+      (renormalize != 0 && renormalize != 1) || (group_max != 0 && group_max != 1))
     return FP8_ERR_INVALID_ARG;
   if (groups < 1 || groups > moe::kMaxGroups || E % groups != 0 || keep_groups < 1 || keep_groups > groups)
     return FP8_ERR_INVALID_ARG;
@@ -407,6 +415,7 @@ FP8_API fp8_status fp8_moe_route(const void* logits, int logits_bf16, int64_t T,
   p.keep = keep_groups;
   p.sigmoid = sigmoid;
   p.renorm = renormalize;
+  p.pair_score = !group_max && (sigmoid || bias != nullptr);
   p.factor = factor;
   p.bias = bias;
   p.ids = ids;

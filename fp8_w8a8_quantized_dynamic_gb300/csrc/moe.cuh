@@ -40,6 +40,7 @@ struct RouteParams {
   int64_t tokens, ld;
   int experts, k, groups, keep;
   int sigmoid, renorm;
+  int pair_score;  // a group's score is the sum of its two best choices, else the best one
   int vec;  // rows start on 16-byte boundaries
   float factor;
   const float* bias;
@@ -230,7 +231,7 @@ route_kernel(const T* __restrict__ logits, const __grid_constant__ RouteParams p
         b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
         b1 = fmaxf(b1, o1);
       }
-      const uint32_t mine = order_key(((p.sigmoid || p.bias) && size > 1) ? b1 + b2 : b1);
+      const uint32_t mine = order_key(p.pair_score && size > 1 ? b1 + b2 : b1);
       // a group stays when fewer than `keep` groups beat it (ties: the lower index first)
       int beaten_by = 0;
       for (int g = 0; g < p.groups; ++g) {

@@ -374,6 +374,13 @@ fp8_status fp8_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t
                          const float* bias, int groups, int keep_groups, int k, int renormalize, float factor,
                          int32_t* ids, float* weights, fp8_stream_t stream);
 
+/* The same with group_max: 1 scores a group by its largest c in every case, 0 as above. Gates that are
+ * published with groups take the largest where they have no bias, for sigmoid too: such a sigmoid gate
+ * without a bias is called with 1. */
+fp8_status fp8_moe_route_ex(const void* logits, int logits_bf16, int64_t T, int64_t E, int64_t ld, int sigmoid,
+                            const float* bias, int groups, int keep_groups, int group_max, int k, int renormalize,
+                            float factor, int32_t* ids, float* weights, fp8_stream_t stream);
+
 /* Workspace fp8_moe_experts needs (0 for sizes it refuses). Host-only. */
 size_t fp8_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
 

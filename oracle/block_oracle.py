@@ -75,7 +75,7 @@ def linear(a: np.ndarray, qw, s_w, bias: Optional[np.ndarray] = None) -> Tuple[n
 
 
 def route(x: np.ndarray, k: int, sigmoid: bool, bias: Optional[np.ndarray] = None, groups: int = 1, keep: int = 1,
-          renorm: bool = False, factor: float = 1.0):
+          renorm: bool = False, factor: float = 1.0, group_max: bool = False):
     """(ids [T, k], weights float64 [T, k], margin [T]): margin is the smallest gap between choices that
     the order of the k chosen, or the kept groups, hangs on (0: an exact tie, settled by the index)."""
     x = x.astype(np.float64)
@@ -93,7 +93,7 @@ def route(x: np.ndarray, k: int, sigmoid: bool, bias: Optional[np.ndarray] = Non
     if groups > 1:
         per = choice.reshape(T, groups, E // groups)
         ordered = -np.sort(-per, axis=2)
-        pair = (sigmoid or bias is not None) and E // groups > 1
+        pair = not group_max and (sigmoid or bias is not None) and E // groups > 1
         score = ordered[:, :, 0] + ordered[:, :, 1] if pair else ordered[:, :, 0]
         order = np.argsort(-score, axis=1, kind="stable")
         if keep < groups:

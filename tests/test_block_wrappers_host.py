@@ -190,3 +190,13 @@ def test_tensors_of_another_device_are_refused_by_every_wrapper(rec, monkeypatch
             call()
     enqueued = {name for name in rec.calls if not name.endswith("_bytes")}
     assert not enqueued
+
+
+def test_route_ex_refusals(real):
+    P = 0x7F0000000000  # aligned fake address, never read
+    d = dict(x=P, bf16=0, T=4, E=64, ld=64, sigmoid=1, bias=None, groups=8, keep=2, group_max=1, k=8, renorm=0,
+             factor=1.0, ids=P, w=P, stream=None)
+    for kw in (dict(group_max=2), dict(group_max=-1), dict(groups=3), dict(keep=9), dict(k=17), dict(ld=63),
+               dict(renorm=2), dict(x=None)):
+        assert F.lib().fp8_moe_route_ex(*{**d, **kw}.values()) == F.FP8_ERR_INVALID_ARG, kw
+    assert F.lib().fp8_moe_route_ex(*{**d, "T": 0}.values()) == F.FP8_OK

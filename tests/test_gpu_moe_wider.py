@@ -1,5 +1,5 @@
 """Wider GPU tests of the choice of experts and of the experts' networks: rows with nothing to choose from,
-gates far below zero."""
+the rules of a group's score, gates far below zero."""
 
 import numpy as np
 import pytest
@@ -33,6 +33,37 @@ def test_softmax_row_of_only_masks_follows_the_bias(groups, keep, dtype):
     assert ref[1].tolist() == [63, 62, 61, 60, 59]
     assert ids.cpu().numpy().tolist() == ref.tolist()
     assert not w[1].any() and np.allclose(w.cpu().numpy(), w_ref, rtol=(8 + E + k) * 2.0 ** -23, atol=1e-37)
+
+
+@pytest.mark.parametrize("T,E,k,groups,keep", [(1, 256, 8, 8, 4), (200, 256, 8, 8, 4), (33, 12, 3, 3, 2),
+                                               (20, 96, 3, 32, 2), (11, 8, 2, 8, 2), (300, 512, 16, 16, 4)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_groups_scored_by_their_best_choice(T, E, k, groups, keep, score, with_bias):
+    g = torch.Generator().manual_seed(T + E)
+    x = torch.randn((T, E), generator=g) * 1.5
+    bias = torch.randn(E, generator=g) * 0.1 if with_bias else None
+    kw = dict(score=score, bias=None if bias is None else bias.to(DEV), groups=groups, keep_groups=keep,
+              renormalize=True, factor=2.5)
+    ids, w = F.fp8_moe_route(x.to(DEV), k, group_score="max", **kw)
+    ex = F.fp8_moe_route_ex(x.to(DEV), k, "max", **kw)
+    assert torch.equal(ids, ex[0]) and torch.equal(w, ex[1])
+    b = None if bias is None else bias.numpy()
+    ref, w_ref, margin = B.route(x.numpy(), k, score == "sigmoid", b, groups, keep, True, 2.5, group_max=True)
+    rows = margin > 2.0 ** -19  # scores are a few fp32 operations from the exact ones, all below 4
+    assert rows.mean() > 0.9 and np.array_equal(ids.cpu().numpy()[rows], ref[rows])
+    tol = (8 + E + k) * 2.0 ** -23 * np.abs(w_ref) + 1e-37
+    assert np.all(np.abs(w.cpu().numpy() - w_ref)[rows] <= tol[rows])
+
+
+def test_group_score_rules_differ():
+    """Group 0 holds the best expert, group 1 the best two: sigmoid without a bias, one group kept."""
+    x = torch.tensor([[2.0, -4.0, 1.5, 1.5]], device=DEV)
+    kw = dict(score="sigmoid", groups=2, keep_groups=1)
+    assert F.fp8_moe_route(x, 2, **kw)[0].tolist() == [[2, 3]]
+    assert F.fp8_moe_route(x, 2, group_score="max", **kw)[0].tolist() == [[0, 1]]
+    with pytest.raises(ValueError):
+        F.fp8_moe_route(x, 2, group_score="sum", **kw)
 
 
 @pytest.mark.parametrize("T", [1, 5, 300])
