@@ -150,9 +150,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
 
 __host__ __device__ constexpr int ilog2(int n) { return n <= 1 ? 0 : 1 + ilog2(n / 2); }
 
-__device__ __forceinline__ float lo_of(uint64_t p) { return __uint_as_float(uint32_t(p)); }
-__device__ __forceinline__ float hi_of(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
-
 // Copies `bytes` (a multiple of 16, both addresses 16-byte aligned) and completes them on the barrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const float* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -203,18 +200,6 @@ __device__ __forceinline__ void st_global_v8(void* p, uint32_t a, uint32_t b, ui
                                              uint32_t f, uint32_t g, uint32_t h) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                :: "l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
-}
-
-// e4m3 codes of four fp32 values divided by the scale of k (any scale: the division when the
-// exact-quotient form does not cover it).
-__device__ __forceinline__ uint32_t codes4(uint64_t p01, uint64_t p23, const ExactScale& k, float s) {
-  if (k.fast) {
-    const uint64_t a = fma_f32x2(p01, k.r2, mul_f32x2(p01, k.r_lo2));
-    const uint64_t b = fma_f32x2(p23, k.r2, mul_f32x2(p23, k.r_lo2));
-    return cvt_fp8x4<kFmtE4M3>(fma_f32x2(fma_f32x2(k.neg_s2, a, p01), k.r2, a),
-                               fma_f32x2(fma_f32x2(k.neg_s2, b, p23), k.r2, b));
-  }
-  return quant2_divide<kFmtE4M3>(lo_of(p01), hi_of(p01), s) | (quant2_divide<kFmtE4M3>(lo_of(p23), hi_of(p23), s) << 16);
 }
 
 constexpr int kOutBf16Any = 3;  // kOutBf16 with rows of any alignment and width
@@ -531,7 +516,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         if (*abort_flag == 0 && live) {
           uint32_t w[8];
 #pragma unroll
-          for (int v = 0; v < 8; ++v) w[v] = codes4(acc[v * 2], acc[v * 2 + 1], k, s);
+          for (int v = 0; v < 8; ++v) w[v] = quant4_exact_f32<kFmtE4M3>(acc[v * 2], acc[v * 2 + 1], k, s);
           const int col = n0 + group * 32;  // columns past N hold zeros (zero weight rows)
           uint8_t* dst = p.qh + int64_t(row) * p.ldh + col;
           if (col < p.ldh) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);

@@ -89,17 +89,8 @@ __device__ __forceinline__ uint4 codes_of_f32(const float (&x)[16], float s) {
   const ExactScale k = make_exact_scale(s);
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (k.fast) {
-      const uint64_t p = pack_f32x2(x[4 * i], x[4 * i + 1]), q = pack_f32x2(x[4 * i + 2], x[4 * i + 3]);
-      const uint64_t a = fma_f32x2(p, k.r2, mul_f32x2(p, k.r_lo2)), b = fma_f32x2(q, k.r2, mul_f32x2(q, k.r_lo2));
-      w[i] = cvt_fp8x4<kFmtE4M3>(fma_f32x2(fma_f32x2(k.neg_s2, a, p), k.r2, a),
-                                 fma_f32x2(fma_f32x2(k.neg_s2, b, q), k.r2, b));
-    } else {
-      w[i] = quant2_divide<kFmtE4M3>(x[4 * i], x[4 * i + 1], s) |
-             (quant2_divide<kFmtE4M3>(x[4 * i + 2], x[4 * i + 3], s) << 16);
-    }
-  }
+  for (int i = 0; i < 4; ++i)
+    w[i] = quant4_exact_f32<kFmtE4M3>(pack_f32x2(x[4 * i], x[4 * i + 1]), pack_f32x2(x[4 * i + 2], x[4 * i + 3]), k, s);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -336,6 +336,21 @@ __device__ __forceinline__ uint2 quant8_exact(uint4 v, const ExactScale& k, floa
   return quant8_bf16_slow<F>(v, s);
 }
 
+__device__ __forceinline__ float lo_of(uint64_t p) { return __uint_as_float(uint32_t(p)); }
+__device__ __forceinline__ float hi_of(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
+
+// Four fp32 values (two packed pairs) -> four FP8 codes of fl32(x / s) for any s: the exact quotient, whose
+// argument holds for any fp32 x, when s is in its range, else the division.
+template <int F>
+__device__ __forceinline__ uint32_t quant4_exact_f32(uint64_t p01, uint64_t p23, const ExactScale& k, float s) {
+  if (k.fast) {
+    const uint64_t a = fma_f32x2(p01, k.r2, mul_f32x2(p01, k.r_lo2));
+    const uint64_t b = fma_f32x2(p23, k.r2, mul_f32x2(p23, k.r_lo2));
+    return cvt_fp8x4<F>(fma_f32x2(fma_f32x2(k.neg_s2, a, p01), k.r2, a), fma_f32x2(fma_f32x2(k.neg_s2, b, p23), k.r2, b));
+  }
+  return quant2_divide<F>(lo_of(p01), hi_of(p01), s) | (quant2_divide<F>(lo_of(p23), hi_of(p23), s) << 16);
+}
+
 // scale = amax / 448 (57344 for e5m2) by IEEE fp32 division; 1 when amax is 0 (or the
 // quotient underflows).
 template <int F>
