@@ -575,10 +575,16 @@ def fp8_moe_route(logits, k: int, score: str = "softmax", bias=None, groups: int
     ids = torch.empty((T, k), dtype=torch.int32, device=device)
     weights = torch.empty((T, k), dtype=torch.float32, device=device)
     L = _lib or lib()
-    head = (logits.data_ptr(), bf16, T, E, ld if T > 1 else E, kind, None if bias is None else bias.data_ptr(), groups,
-            groups if keep_groups is None else keep_groups)
-    tail = (k, 1 if renormalize else 0, factor, ids.data_ptr(), weights.data_ptr(), _stream_ptr(logits))
-    status = L.fp8_moe_route_ex(*head, 1, *tail) if group_max else L.fp8_moe_route(*head, *tail)
+    keep = groups if keep_groups is None else keep_groups
+    bias_ptr = None if bias is None else bias.data_ptr()
+    if group_max:
+        status = L.fp8_moe_route_ex(logits.data_ptr(), bf16, T, E, ld if T > 1 else E, kind, bias_ptr, groups, keep, 1, k,
+                                    1 if renormalize else 0, factor, ids.data_ptr(), weights.data_ptr(),
+                                    _stream_ptr(logits))
+    else:
+        status = L.fp8_moe_route(logits.data_ptr(), bf16, T, E, ld if T > 1 else E, kind, bias_ptr, groups, keep, k,
+                                 1 if renormalize else 0, factor, ids.data_ptr(), weights.data_ptr(),
+                                 _stream_ptr(logits))
     if status:
         raise FP8Error(status, "fp8_moe_route")
     return ids, weights
