@@ -58,9 +58,13 @@ struct Carver {
 };
 
 // Whether the GEMV takes a dense product. Its CTAs each bring in their K slices of A, so its time grows
-// with M * K and the GEMM's does not; graph replays, in us, GEMV and GEMM: M 8 K 4096 N 6144 11.4 and
-// 13.7, M 12 15.5 and 13.9; M 8 K 5632 N 2048 10.6 and 10.8, M 12 15.1 and 10.8; M 4 K 14336 N 4096 18.0
-// and 21.1, M 8 24.5 and 21.5; M 16 K 2048 N 2048 7.8 and 7.9, K 1000 N 1027 6.0 and 9.7.
+// with M * K and the GEMM's does not (both stream the weights, so N decides nothing). Graphs over weights
+// that together pass L2, in us, GEMV and GEMM: K 4096 N 6144 M 8 11.0 and 13.0, M 12 14.5 and 13.0; K 4096
+// N 28672 M 8 24.3 and 26.6, M 12 29.1 and 26.6; K 2048 N 14336 M 12 12.4 and 12.7, M 16 13.2 and 12.7; K
+// 14336 N 4096 M 4 17.3 and 20.6, M 8 24.1 and 19.8; K 1000 N 1027 M 16 6.0 and 9.7. Of 64 shapes with K
+// from 1024 to 14336, N from 4096 to 28672 and up to 16 rows, the side not taken is 5 percent or more faster in
+// four: K 8192 N 8192 M 6 (GEMV 18.2, GEMM 21.1) and M 8 (19.3, 21.1), K 8192 N 28672 M 6 (43.1, 45.3), K 1024
+// N 28672 M 16 (13.4, 11.6).
 bool uses_gemv(int64_t M, int64_t K) {
   return block::gemv_fits(M, K, 1) && (M <= 4 || M * K <= 40 * 1024);
 }

@@ -1,7 +1,8 @@
-// Block-scaled FP8 GEMV for sm_103a: the product for few rows, bound by streaming the weights (one row,
-// 4096 x 6144, 25 MB: 8.0 us in a graph, 3.1 TB/s; 4096 x 28672, 117 MB: 20.0 us, 5.9 TB/s; the start of
-// a launch, its first loads and the last sums take 4 us). One token's experts, 8 of 2048 x 1408: 26.5 us
-// for 69 MB in two launches.
+// Block-scaled FP8 GEMV for sm_103a: the product for few rows, bound by streaming the weights (times here
+// and below: graphs that cycle through weights which together pass L2. One row, 4096 x 6144, 25 MB: 7.7 to
+// 8.9 us over several GPUs, 2.8 to 3.3 TB/s; 4096 x 28672, 117 MB: 20.2 us, 5.8 TB/s; the start of a launch,
+// its first loads and the last sums take 4 us). One token's experts, 8 of 2048 x 1408: 23.3 us for 69 MB in
+// two launches.
 //
 // A warp takes 16 weight rows at a time (kGemvSwiglu: 16 of gate and the same 16 of up) over a slice
 // of K in whole 128-wide blocks; 1, 2, 4 or all 8 warps of a CTA share one row group's K. A lane loads
@@ -95,8 +96,8 @@ __device__ __forceinline__ uint4 codes_of_f32(const float (&x)[16], float s) {
 }
 
 // kNT: eight-row activation tiles (1 or 2). kFull: weight rows are whole blocks, 32-byte aligned, and
-// loaded 32 bytes at a time (1 x 5632 x 2048 in 6.9 us, 7.9 in predicated 16-byte loads; 4 rows 8.8 and
-// 9.5; 1 x 4096 x 6144 9.2 and 8.9).
+// loaded 32 bytes at a time (1 x 4096 x 28672 in 20.2 us, 21.7 in predicated 16-byte loads; 1 x 5632 x 2048
+// 6.7 and 7.3; 1 x 4096 x 6144 7.7 and 7.9, 8 rows 11.0 and 10.7; 1 x 512 x 28672 6.3 and 5.4).
 template <int kNT, int kSrc, int kOut, bool kFull>
 __global__ void __launch_bounds__(kGvThreads, 2)
 block_gemv_kernel(const __grid_constant__ GvParams p) {
@@ -508,10 +509,10 @@ bool gemv_fits(int64_t rows, int64_t K, int mats) {
   return act_bytes(rows, (blocks_of(K) + kGvWarps - 1) / kGvWarps, kGvWarps, nt) + red_bytes(nt, mats) + 1024 <= size_t(kSmemCap);
 }
 
-// The fill of a K slice by every CTA against a second launch and codes through L2 (graph replays, us,
-// in the kernel / before it): M 1 K 4096 N 6144 9.2 / 10.6, M 4 11.9 / 11.1, M 8 16.0 / 11.3; M 4 K 5632
-// N 2048 10.7 / 8.7; K 1000 N 1027 M 8 3.9 / 4.5, M 16 6.0 / 5.8. Where the two are level the one launch is
-// less work for the host.
+// The fill of a K slice by every CTA against a second launch and codes through L2 (us, in the kernel /
+// before it): M 1 K 4096 N 6144 8.2 / 9.8, M 2 9.0 / 9.9, M 4 10.9 / 10.6, M 8 15.3 / 11.0; M 4 K 5632 N 2048
+// 10.2 / 8.6; K 1000 N 1027 M 8 3.5 / 4.6, M 16 5.6 / 5.8. Where the two are level the one launch is less
+// work for the host.
 bool gemv_quantizes(int64_t M, int64_t K) { return M * ((blocks_of(K) + kGvWarps - 1) / kGvWarps) <= 16; }
 
 bool gemv_launch(const GemvArgs& a, GemvOut out, int num_sms, cudaStream_t st) {

@@ -147,9 +147,11 @@ __device__ __forceinline__ void load_logits(const uint16_t* row, int lane, int E
 // each in fp32 with the accurate exp and division: equal scores are equal bits and the lowest
 // index wins them. With groups, 32 / groups lanes (rounded down to a power of two) find a group's
 // two best each in its share, and only the experts of the groups that stay are looked at again, in
-// their order (without that, and with the keys of a lane unsorted, 24.7 and 22.5 us below). Bound: issue
-// slots (63 percent of them used; the logits are read once): 16384 tokens of 256 experts in 8 groups, k =
-// 8, take 19.6 us.
+// their order (without that, and with the keys of a lane unsorted, 24.7 and 22.5 us below). 16384 tokens of
+// 256 experts in 8 groups, k = 8, take 19.6 us. Not memory (the logits, read once, are 2.5 us) but
+// instructions set that: 1123 a token, 14.7 us if every scheduler issued one a cycle. While they have warps
+// the schedulers issue in 76 percent of the cycles; 64 registers a thread allow half of the warps an SM
+// holds, and 2048 CTAs are 3.4 waves of them, so that the last one runs part empty.
 template <typename T, int kPerLane>
 __global__ void __launch_bounds__(kRouteThreads)
 route_kernel(const T* __restrict__ logits, const __grid_constant__ RouteParams p) {
@@ -322,7 +324,7 @@ plan_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, i
 // any other id gives -1. Then the row tiles. A CTA's warps count their contiguous shares of the CTA's pairs by expert in
 // shared memory (equal ids of a step are found by a warp match), the counts are scanned over warps,
 // CTAs (from plan_count_kernel; one CTA needs none) and experts, and a second walk hands out rows.
-// One CTA sorts 65536 pairs in 109 us, 64 of them in 11 us.
+// One CTA sorts 65536 pairs in 109 us, 64 CTAs in 11 us.
 __global__ void __launch_bounds__(kPlanThreads, 1)
 plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, const int* __restrict__ counts,
             int* __restrict__ pos, block::RowTile* __restrict__ tiles, int* __restrict__ n_tiles) {

@@ -396,7 +396,9 @@ size_t fp8_moe_workspace_bytes(int64_t T, int64_t k, int64_t E, int64_t H, int64
  * [E][2][ceil(I/128)][ceil(H/128)]; qw2 u8 [E][H, ldq2], s2 fp32
  * [E][ceil(H/128)][ceil(I/128)], as fp8_block_quantize_weight writes them for
  * 2 E and E matrices. Results do not depend on timing. y may not overlap x.
- * ws: >= fp8_moe_workspace_bytes, 256-byte aligned. Limits: E <= 512, k <= 32.
+ * ws: >= fp8_moe_workspace_bytes, 256-byte aligned: from two tokens on about
+ * T * k * (5 H + I) bytes, most of it the pairs' fp32 rows of H (8192 tokens, 8
+ * experts each, H 4096, I 2048: 1.5 GB). Limits: E <= 512, k <= 32.
  */
 fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
                            const float* weights, int64_t k, const uint8_t* qw13, int64_t ldq13, const float* s13,
