@@ -447,13 +447,19 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         if (j == 0 && !wait_all(&ctl->sfull[slot], (slot_no / kScaleSlots) & 1u)) return false;
         const float sa = ctl->s_row[slot][j][(row0 & 3) + row_in_tile];
         const float2 sw = *reinterpret_cast<const float2*>(&ctl->s_col[slot][j][2 * (group / (kGroups / 2))]);
+        const float g = sa * sw.x, u = kOut == kOutSwiglu ? sa * sw.y : g;
         if (j == kScaleKb - 1 || kb == kb_end() - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl->sempty[slot]));
+          // The slot goes back only when the loads of every lane have delivered: the arriving lane depends on
+          // their values. The barrier alone does not order them before the bulk copy that fills the slot again
+          // (another proxy): behind the stores of other warps a load waits for microseconds, and an arrival
+          // that was merely issued after it gave wrong scales at K of one to three blocks, where the tiles
+          // before this one are still being stored.
+          const float all = kOut == kOutSwiglu ? g + u : g;
+          if (lane == (__any_sync(0xffffffffu, all == all) ? 0 : 1)) mbar_arrive(smem_u32(&ctl->sempty[slot]));
           ++slot_no;
         }
-        g2 = pack_f32x2(sa * sw.x, sa * sw.x);
-        u2 = kOut == kOutSwiglu ? pack_f32x2(sa * sw.y, sa * sw.y) : g2;
+        g2 = pack_f32x2(g, g);
+        u2 = kOut == kOutSwiglu ? pack_f32x2(u, u) : g2;
         return true;
       };
       bool ok = true;

@@ -115,3 +115,18 @@ def test_rows_that_overlap_are_refused():
         assert e.value.status == F.FP8_ERR_INVALID_ARG
     assert torch.equal(F.fp8_block_linear(row.expand(40, 256).contiguous(), qw, s_w)[7:8],
                        F.fp8_block_linear(row.expand(40, 256).contiguous(), qw, s_w)[:1])
+
+
+@pytest.mark.parametrize("M,K,N", [(16000, 128, 4096), (16000, 256, 4096), (16000, 384, 4099), (30000, 128, 120),
+                                   (40000, 200, 40)])
+def test_short_k_repeats(M, K, N):
+    """Tiles of one to three K blocks, bound by their stores: the same bits on every run, the oracle's values."""
+    a, w = rand((M, K), 1).to(DEV), rand((N, K), 2, 0.05).to(DEV)
+    qw, s_w = F.fp8_block_quantize_weight(w)
+    y = F.fp8_block_linear(a, qw, s_w)
+    for _ in range(10):
+        assert torch.equal(F.fp8_block_linear(a, qw, s_w), y)
+    rows = np.unique(np.r_[0, M - 1, np.random.default_rng(M).integers(0, M, 60)])
+    at = torch.from_numpy(rows).to(DEV)
+    ref, tol = B.linear(f32(a[at]), qw.cpu().numpy()[:, :K], s_w.cpu().numpy())
+    assert np.all(np.abs(f32(y[at]).astype(np.float64) - ref) <= tol)

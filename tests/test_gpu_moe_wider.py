@@ -225,3 +225,19 @@ def test_experts_of_a_prompt_batch():
     ids = torch.randn((T, E), generator=g).topk(k, dim=1).indices.to(torch.int32)
     w = torch.rand((T, k), generator=g)
     check_experts(tokens_of(T, H, 10), ids, w, weights_of(E, H, I, 11), rows=[0, 77, 2048, 4095])
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(2000, 6, 8, 4096, 128), (2000, 6, 8, 4096, 200), (3000, 6, 8, 4096, 384),
+                                       (20000, 5, 4, 2048, 128), (4000, 6, 8, 128, 2048), (4000, 6, 8, 300, 2048)])
+def test_short_k_behind_many_stores(T, E, k, H, I):
+    """Tiles of one to three K blocks, whose scales are read while the memory pipe is full of the stores of tiles
+    before: the slots of the scale ring may go back only when every lane has its scales. Every run gives the
+    same bits, and the oracle's values on sampled tokens."""
+    g = torch.Generator().manual_seed(T)
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    w, x, q = torch.rand((T, k), generator=g), tokens_of(T, H, 1), weights_of(E, H, I, 2)
+    rows = np.unique(np.r_[0, 1, T - 1, torch.randint(0, T, (60,), generator=g).numpy()])
+    y = check_experts(x, ids, w, q, rows)
+    xd, idd, wd = x.to(DEV), ids.to(DEV), w.to(DEV)
+    for _ in range(10):
+        assert torch.equal(F.fp8_moe_experts(xd, idd, wd, *q), y)
