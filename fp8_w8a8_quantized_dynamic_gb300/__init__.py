@@ -87,6 +87,15 @@ _SIGNATURES = {
     "fp8_moe_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "fp8_moe_experts": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64,
                                _vp, _i64, _vp, _sz, _vp]),
+    "fp8_moe_dispatch_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "fp8_moe_dispatch": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "fp8_moe_combine": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "fp8_moe_combine_grad": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "fp8_moe_dispatch_grad": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "fp8_residual_norm": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.c_float, _vp, _i64, _vp, ctypes.c_float,
+                                 _int, _vp, _i64, _vp, _i64, _vp]),
+    "fp8_residual_norm_quantize": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.c_float, _vp, _i64, _vp,
+                                          ctypes.c_float, _int, _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
     "fp8_last_device_status": (_int, [_vp]),
     "fp8_selftest_timeout": (_int, [_i64, _vp]),
     "fp8_block_selftest_timeout": (_int, [_int, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
@@ -430,6 +439,12 @@ def _check_dense(t, dtype, shape, index: int, name: str):
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
 
 
+def _check_rows(t, dtype, rows: int, cols: int, index: int, name: str):
+    """A matrix of this dtype and shape with unit column stride on CUDA device `index`."""
+    if t.dtype != dtype or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1) or t.get_device() != index:
+        raise ValueError(f"{name}: expected a {dtype} matrix [{rows}, {cols}] with unit column stride on cuda:{index}")
+
+
 def _check_block_weight(qw, s_w, lead: tuple, N: int, K: int, index: int, name: str) -> int:
     """Codes [*lead, N, ld] and scales [*lead, blocks of N, blocks of K] as fp8_block_quantize_weight returns
     them; returns ld."""
@@ -625,6 +640,200 @@ def fp8_moe_experts(x, ids, weights, qw13, s13, qw2, s2, out=None, ws=None):
     if status:
         raise FP8Error(status, "fp8_moe_experts")
     return y
+
+
+# ---------------------------------------------------------------------------
+# tokens sorted by expert and back
+# ---------------------------------------------------------------------------
+
+def _check_rows_in(t, name: str):
+    """A CUDA matrix of bf16 or fp32 with unit column stride; (1 for fp32, rows, columns, row stride)."""
+    torch = _torch_module or _torch()
+    f32 = t.dtype is torch.float32
+    if not (f32 or t.dtype is torch.bfloat16) or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a CUDA bf16 or fp32 matrix with unit column stride")
+    rows, cols = t.shape
+    return int(f32), rows, cols, t.stride(0) if rows > 1 else cols or 1
+
+
+def _rows_out(out, rows: int, cols: int, like, name: str = "out"):
+    """(tensor, row stride) of an output of `like`'s type."""
+    if out is None:
+        return _torch().empty((rows, cols), dtype=like.dtype, device=like.device), cols or 1
+    _check_rows(out, like.dtype, rows, cols, like.get_device(), name)
+    return out, _row_stride(out, rows, cols)
+
+
+def _check_pairs(pos, weights, index: int):
+    """(T, k) of pos int32 [T, k] and weights fp32 of the same shape, or None."""
+    torch = _torch_module or _torch()
+    if pos.dim() != 2:
+        raise ValueError("pos: expected an int32 matrix [T, k]")
+    T, k = pos.shape
+    _check_dense(pos, torch.int32, (T, k), index, "pos")
+    if weights is not None:
+        _check_dense(weights, torch.float32, (T, k), index, "weights")
+    return T, k
+
+
+def fp8_moe_dispatch_workspace_bytes(T: int, k: int, E: int) -> int:
+    return int(lib().fp8_moe_dispatch_workspace_bytes(T, k, E))
+
+
+def fp8_moe_dispatch(x, ids, E: int, out=None, ws=None):
+    """Tokens copied to rows sorted by expert: x [T, H] (bf16 or fp32), ids int32 [T, k] -> (xs [T * k, H],
+    pos int32 [T, k], offsets int32 [E + 1]). xs[pos[t, j]] = x[t]; rows offsets[e] to offsets[e + 1] are expert e's, in
+    the tokens' order. Ids outside [0, E) have pos -1 and no row; rows from offsets[E] on are not written."""
+    torch = _torch_module or _torch()
+    f32, T, H, ldx = _check_rows_in(x, "x")
+    if ids.dim() != 2:
+        raise ValueError("ids: expected an int32 matrix [T, k]")
+    k = ids.shape[1]
+    _check_dense(ids, torch.int32, (T, k), x.get_device(), "ids")
+    if E < 1:
+        raise ValueError(f"E: expected at least 1, got {E}")
+    L = _lib or lib()
+    need = L.fp8_moe_dispatch_workspace_bytes(T, k, E)
+    wp, wn, ws = _scratch(ws, need, x) if need or ws is not None else (None, 0, None)
+    xs, ldxs = _rows_out(out, T * k, H, x)
+    pos = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=x.device)
+    status = L.fp8_moe_dispatch(x.data_ptr(), f32, T, H, ldx, ids.data_ptr(), k, E, xs.data_ptr(), ldxs, pos.data_ptr(),
+                                offsets.data_ptr(), wp, wn, _stream_ptr(x))
+    if status:
+        raise FP8Error(status, "fp8_moe_dispatch")
+    return xs, pos, offsets
+
+
+def fp8_moe_combine(ys, pos, weights=None, out=None):
+    """The experts' rows back at their tokens: y[t] = sum_j weights[t, j] ys[pos[t, j]] in fp32 (weights None: ones),
+    of ys' type (bf16 or fp32). Pairs with pos outside ys' rows contribute nothing."""
+    f32, R, H, ldys = _check_rows_in(ys, "ys")
+    T, k = _check_pairs(pos, weights, ys.get_device())
+    y, ldy = _rows_out(out, T, H, ys)
+    status = (_lib or lib()).fp8_moe_combine(ys.data_ptr(), f32, R, H, ldys, pos.data_ptr(), _ptr(weights), T, k,
+                                             y.data_ptr(), ldy, _stream_ptr(ys))
+    if status:
+        raise FP8Error(status, "fp8_moe_combine")
+    return y
+
+
+def fp8_moe_combine_grad(dy, ys, pos, weights, out=None):
+    """The gradient of fp8_moe_combine: (dys [R, H] with dys[pos[t, j]] = weights[t, j] dy[t], dw fp32 [T, k] with
+    <dy[t], ys[pos[t, j]]>). Rows of dys that no pair has are not written; out may be ys."""
+    torch = _torch_module or _torch()
+    f32, T, H, lddy = _check_rows_in(dy, "dy")
+    index = dy.get_device()
+    _, R, _, ldys = _check_rows_in(ys, "ys")
+    _check_rows(ys, dy.dtype, R, H, index, "ys")
+    if weights is None or _check_pairs(pos, weights, index)[0] != T:
+        raise ValueError("expected pos [T, k] and weights [T, k] for dy [T, H]")
+    k = pos.shape[1]
+    dys, lddys = _rows_out(out, R, H, ys)
+    dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    status = (_lib or lib()).fp8_moe_combine_grad(dy.data_ptr(), f32, T, H, lddy, ys.data_ptr(), R, ldys,
+                                                  pos.data_ptr(), weights.data_ptr(), k, dys.data_ptr(), lddys,
+                                                  dw.data_ptr(), _stream_ptr(dy))
+    if status:
+        raise FP8Error(status, "fp8_moe_combine_grad")
+    return dys, dw
+
+
+def fp8_moe_dispatch_grad(dxs, pos, out=None):
+    """The gradient of fp8_moe_dispatch: dx[t] = sum_j dxs[pos[t, j]]."""
+    f32, R, H, lddxs = _check_rows_in(dxs, "dxs")
+    T, k = _check_pairs(pos, None, dxs.get_device())
+    dx, lddx = _rows_out(out, T, H, dxs)
+    status = (_lib or lib()).fp8_moe_dispatch_grad(dxs.data_ptr(), f32, R, H, lddxs, pos.data_ptr(), T, k,
+                                                   dx.data_ptr(), lddx, _stream_ptr(dxs))
+    if status:
+        raise FP8Error(status, "fp8_moe_dispatch_grad")
+    return dx
+
+
+# ---------------------------------------------------------------------------
+# norms around a block
+# ---------------------------------------------------------------------------
+
+def _norm_operands(torch, y, weight, residual, post_weight, gate, scale, residual_out):
+    """Checks what both norms share; (M, H, ldy, index, gate's row stride, residual's, r, r's row stride). r is None
+    where nothing changes y."""
+    if y.dtype is not torch.bfloat16 or y.dim() != 2 or not y.is_cuda:
+        raise ValueError("y: expected a CUDA bf16 matrix with unit column stride")
+    M, H = y.shape
+    ldy, unit = y.stride()
+    if unit != 1 and H > 1:
+        raise ValueError("y: expected a CUDA bf16 matrix with unit column stride")
+    index = y.get_device()
+    if weight is not None:
+        _check_dense(weight, torch.bfloat16, (H,), index, "weight")
+    if post_weight is not None:
+        _check_dense(post_weight, torch.bfloat16, (H,), index, "post_weight")
+    ldg = 0
+    if gate is not None:
+        if gate.dim() == 1:
+            _check_dense(gate, torch.bfloat16, (H,), index, "gate")
+        else:
+            _check_rows(gate, torch.bfloat16, M, H, index, "gate")
+            ldg = _row_stride(gate, M, H)
+    ldr = 0
+    if residual is not None:
+        _check_rows(residual, torch.bfloat16, M, H, index, "residual")
+        ldr = _row_stride(residual, M, H)
+    if residual_out is not None:
+        r = _out_bf16(residual_out, M, H, y)
+        ldro = _row_stride(r, M, H)
+    elif residual is None and post_weight is None and gate is None and scale == 1.0:
+        r, ldro = None, 0
+    else:
+        r, ldro = torch.empty((M, H), dtype=torch.bfloat16, device=y.device), H or 1
+    return M, H, ldy if M > 1 else H or 1, index, ldg, ldr, r, ldro
+
+
+def fp8_residual_norm(y, weight=None, residual=None, post_weight=None, gate=None, scale: float = 1.0,
+                      eps: float = 1e-6, plus_one: bool = False, out=None, residual_out=None):
+    """The end of a block and the norm before the next: (n, r) bf16 [M, H] of y bf16 [M, H], with
+    t = y (with post_weight: y / sqrt(mean y^2 + eps) * post_weight), r = residual + scale * gate * t and
+    n = r / sqrt(mean r^2 + eps) * weight, in fp32 with one rounding of r and of n. Weights bf16 [H] (plus_one: they
+    stand for 1 + weight), gate bf16 [H] or [M, H]. Without a weight n is None; where nothing changes y, r is y.
+    residual_out may be y or residual itself."""
+    torch = _torch_module or _torch()
+    M, H, ldy, index, ldg, ldr, r, ldro = _norm_operands(torch, y, weight, residual, post_weight, gate, scale,
+                                                         residual_out)
+    n = None
+    if weight is not None:
+        n = torch.empty((M, H), dtype=torch.bfloat16, device=y.device) if out is None else _out_bf16(out, M, H, y)
+    elif out is not None:
+        raise ValueError("out: there is no n without a weight")
+    if n is None and r is None:
+        return None, y
+    status = (_lib or lib()).fp8_residual_norm(
+        y.data_ptr(), M, H, ldy, _ptr(post_weight), _ptr(gate), ldg, scale, _ptr(residual), ldr, _ptr(weight), eps,
+        1 if plus_one else 0, _ptr(r), ldro, _ptr(n), 0 if n is None else _row_stride(n, M, H), _stream_ptr(y))
+    if status:
+        raise FP8Error(status, "fp8_residual_norm")
+    return n, y if r is None else r
+
+
+def fp8_residual_norm_quantize(y, weight, residual=None, post_weight=None, gate=None, scale: float = 1.0,
+                               eps: float = 1e-6, plus_one: bool = False, residual_out=None):
+    """fp8_residual_norm with n quantized for fp8_block_scaled_mm: (qn uint8 [M, min_ld(H)], s_n fp32
+    [ceil(H/128), M], r), one scale per row and 128 columns, as fp8_block_quantize_act returns them."""
+    torch = _torch_module or _torch()
+    M, H, ldy, index, ldg, ldr, r, ldro = _norm_operands(torch, y, weight, residual, post_weight, gate, scale,
+                                                         residual_out)
+    if weight is None:
+        raise ValueError("weight: expected a bf16 vector")
+    ldq, device = min_ld(H), y.device
+    lds = (M + 3) // 4 * 4 or 1
+    qn = torch.empty((M, ldq), dtype=torch.uint8, device=device)
+    s_n = torch.empty((_blocks(H), lds), dtype=torch.float32, device=device)
+    status = (_lib or lib()).fp8_residual_norm_quantize(
+        y.data_ptr(), M, H, ldy, _ptr(post_weight), _ptr(gate), ldg, scale, _ptr(residual), ldr, weight.data_ptr(), eps,
+        1 if plus_one else 0, _ptr(r), ldro, qn.data_ptr(), ldq, s_n.data_ptr(), lds, _stream_ptr(y))
+    if status:
+        raise FP8Error(status, "fp8_residual_norm_quantize")
+    return qn, s_n[:, :M], y if r is None else r
 
 
 def fp8_selftest_timeout(limit_ns: int = 20_000_000, stream=None) -> int:

@@ -128,6 +128,13 @@ inline fp8_status check_fp8_mat(const void* p, int64_t rows, int64_t cols, int64
   return FP8_OK;
 }
 
+// Scales of rows: fp32 [K blocks][lds], lds >= rows.
+inline fp8_status check_row_scales(const float* s, int64_t rows, int64_t K, int64_t lds) {
+  if (lds < std::max<int64_t>(rows, 1)) return FP8_ERR_INVALID_ARG;
+  if (rows > 0 && K > 0 && s == nullptr) return FP8_ERR_INVALID_ARG;
+  return aligned(s, 4) ? FP8_OK : FP8_ERR_MISALIGNED;
+}
+
 inline fp8_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
   if (need == 0) return FP8_OK;
   if (ws == nullptr || ws_bytes < need) return FP8_ERR_WORKSPACE;

@@ -41,13 +41,6 @@ fp8_status launch_quantize_rows(const BF16Mat& a, uint8_t* q, int64_t ldq, float
                                     : go(block::quantize_rows_1x128_kernel<uint64_t>);
 }
 
-// Scales of rows: fp32 [K blocks][lds], lds >= rows.
-fp8_status check_row_scales(const float* s, int64_t rows, int64_t K, int64_t lds) {
-  if (lds < std::max<int64_t>(rows, 1)) return FP8_ERR_INVALID_ARG;
-  if (rows > 0 && K > 0 && s == nullptr) return FP8_ERR_INVALID_ARG;
-  return aligned(s, 4) ? FP8_OK : FP8_ERR_MISALIGNED;
-}
-
 struct Carver {
   size_t at = 0;
   size_t take(size_t bytes) {
@@ -210,7 +203,7 @@ bool moe_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
 PerDeviceCache<const void*, int> g_attr_cache;
 
 fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int* counts, int* pos, block::RowTile* tiles,
-                       int* n_tiles, cudaStream_t st) {
+                       int* n_tiles, int* offsets, cudaStream_t st) {
   const size_t smem = size_t(moe::kPlanWarps + 1) * E * sizeof(int);
   int dev = 0, set = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
@@ -226,7 +219,7 @@ fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int* counts, in
     FP8_TRY(launch(moe::plan_count_kernel, dim3(ctas), dim3(moe::kPlanThreads), 0, st, true, dim3(1, 1, 1), ids, pairs,
                    E, counts));
   return launch(moe::plan_kernel, dim3(ctas), dim3(moe::kPlanThreads), smem, st, true, dim3(1, 1, 1), ids, pairs, E,
-                ctas > 1 ? static_cast<const int*>(counts) : nullptr, pos, tiles, n_tiles);
+                ctas > 1 ? static_cast<const int*>(counts) : nullptr, pos, tiles, n_tiles, offsets);
 }
 
 template <typename T>
@@ -240,6 +233,52 @@ fp8_status launch_route(const T* logits, const moe::RouteParams& p, int sms, cud
   if (p.experts <= 128) return go(moe::route_kernel<T, 4>);
   if (p.experts <= 256) return go(moe::route_kernel<T, 8>);
   return go(moe::route_kernel<T, 16>);
+}
+
+// ---- tokens sorted by expert and back ----
+
+bool pair_sizes_ok(int64_t T, int64_t k) { return T >= 0 && k >= 1 && k <= moe::kMaxChosen && T <= kMaxRows / k; }
+
+// Rows of fp32 or bf16 (f32 1 or 0).
+fp8_status check_rows(const void* p, int f32, int64_t rows, int64_t cols, int64_t ld) {
+  if (f32 != 0 && f32 != 1) return FP8_ERR_INVALID_ARG;
+  FP8_TRY(check_bf16_mat(p, rows, cols, ld));
+  return aligned(p, f32 ? 4 : 2) ? FP8_OK : FP8_ERR_MISALIGNED;
+}
+
+// Whether all rows start and end on 16-byte boundaries.
+bool whole_pieces(const void* p, int64_t rows, int64_t ld, int64_t cols, int size) {
+  return aligned(p, 16) && (rows <= 1 || ld * size % 16 == 0) && cols * size % 16 == 0;
+}
+
+template <typename U>
+fp8_status launch_rows_out(const void* x, int64_t row_bytes, int64_t ldx_bytes, int64_t T, const int* pos, int64_t k,
+                           int64_t rows, void* xs, int64_t ldxs_bytes, int sms, cudaStream_t st) {
+  const int64_t pieces = row_bytes / int64_t(sizeof(U));
+  return launch(moe::rows_out_kernel<U>, dim3(elementwise_grid(T * pieces, moe::kRowThreads, sms, 8)),
+                dim3(moe::kRowThreads), 0, st, true, dim3(1, 1, 1), static_cast<const U*>(x),
+                ldx_bytes / int64_t(sizeof(U)), T, pieces, pos, int(k), rows, static_cast<U*>(xs),
+                ldxs_bytes / int64_t(sizeof(U)));
+}
+
+template <typename T, int kN>
+fp8_status launch_rows_back(const void* ys, int64_t ldys, int64_t R, const int* pos, const float* weights, int64_t k,
+                            int64_t tokens, int64_t H, void* y, int64_t ldy, int sms, cudaStream_t st) {
+  return launch(moe::rows_back_kernel<T, kN>, dim3(elementwise_grid(tokens * (H / kN), moe::kRowThreads, sms, 8)),
+                dim3(moe::kRowThreads), 0, st, true, dim3(1, 1, 1), static_cast<const T*>(ys), ldys, R, pos, weights,
+                int(k), tokens, H, static_cast<T*>(y), ldy);
+}
+
+template <typename T, int kN>
+fp8_status launch_rows_back_grad(const void* dy, int64_t lddy, const void* ys, int64_t ldys, int64_t R, const int* pos,
+                                 const float* weights, int64_t k, int64_t tokens, int64_t H, void* dys, int64_t lddys,
+                                 float* dw, int sms, cudaStream_t st) {
+  int per_token = 32;
+  while (per_token < moe::kRowThreads && per_token * kN < H) per_token *= 2;
+  const int per_cta = moe::kRowThreads / per_token;
+  return launch(moe::rows_back_grad_kernel<T, kN>, dim3(elementwise_grid(tokens, per_cta, sms, 64)),
+                dim3(per_token, per_cta), 0, st, true, dim3(1, 1, 1), static_cast<const T*>(dy), lddy,
+                static_cast<const T*>(ys), ldys, R, pos, weights, int(k), tokens, H, static_cast<T*>(dys), lddys, dw);
 }
 
 }  // namespace
@@ -488,7 +527,8 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   block::RowTile* tiles = reinterpret_cast<block::RowTile*>(b + w.tiles);
   int* pos = reinterpret_cast<int*>(b + w.pos);
   float* y32 = reinterpret_cast<float*>(b + w.y);
-  FP8_TRY(launch_plan(ids, w.pairs, int(E), reinterpret_cast<int*>(b + w.counts), pos, tiles, n_tiles, st));
+  FP8_TRY(launch_plan(ids, w.pairs, int(E), reinterpret_cast<int*>(b + w.counts), pos, tiles, n_tiles,
+                      nullptr, st));
   // quantize each token once into its rows; gate and up products with SwiGLU and the quantization
   // of h in their epilogue; the product back; the weighted sum
   float* s_x = reinterpret_cast<float*>(b + w.s_x);
@@ -532,4 +572,91 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   return launch(moe::weighted_sum_kernel, dim3(elementwise_grid(T * ((H + 3) / 4), moe::kSumThreads, sms, 8)),
                 dim3(moe::kSumThreads), 0, st, true, dim3(1, 1, 1), static_cast<const float*>(y32), w.ldy,
                 static_cast<const int*>(pos), weights, int(k), T, H, static_cast<uint16_t*>(y_bf16), ldy, vec);
+}
+
+// ---------------------------------------------------------------------------
+// tokens sorted by expert and back
+// ---------------------------------------------------------------------------
+
+FP8_API size_t fp8_moe_dispatch_workspace_bytes(int64_t T, int64_t k, int64_t E) {
+  if (!pair_sizes_ok(T, k) || E < 1 || E > moe::kMaxExperts) return 0;
+  const int ctas = plan_ctas(T * k);
+  return ctas > 1 ? round_up_256(size_t(ctas) * size_t(E) * 4) : 0;
+}
+
+FP8_API fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
+                                    int64_t k, int64_t E, void* xs, int64_t ldxs, int32_t* pos, int32_t* offsets,
+                                    void* ws, size_t ws_bytes, fp8_stream_t stream) {
+  if (!pair_sizes_ok(T, k) || E < 1 || E > moe::kMaxExperts) return FP8_ERR_INVALID_ARG;
+  FP8_TRY(check_rows(x, f32, T, H, ldx));
+  FP8_TRY(check_rows(xs, f32, T * k, H, ldxs));
+  if (!aligned(ids, 4) || !aligned(pos, 4) || !aligned(offsets, 4)) return FP8_ERR_MISALIGNED;
+  if (offsets == nullptr || (T > 0 && (ids == nullptr || pos == nullptr))) return FP8_ERR_INVALID_ARG;
+  FP8_TRY(check_ws(ws, ws_bytes, fp8_moe_dispatch_workspace_bytes(T, k, E)));
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  FP8_TRY(launch_plan(ids, T * k, int(E), static_cast<int*>(ws), pos, nullptr, nullptr, offsets, st));
+  if (T == 0 || H == 0) return FP8_OK;
+  const int size = f32 ? 4 : 2;
+  // the widest pieces that every row of both consists of
+  const int64_t any = int64_t(reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(xs)) | H * size |
+                      (T > 1 ? ldx * size : 0) | (T * k > 1 ? ldxs * size : 0);
+  auto go = [&](auto piece) {
+    return launch_rows_out<decltype(piece)>(x, H * size, ldx * size, T, pos, k, T * k, xs, ldxs * size, sms, st);
+  };
+  if (any % 16 == 0) return go(uint4{});
+  if (any % 8 == 0) return go(uint2{});
+  return any % 4 == 0 ? go(uint32_t{}) : go(uint16_t{});
+}
+
+FP8_API fp8_status fp8_moe_combine(const void* ys, int f32, int64_t R, int64_t H, int64_t ldys, const int32_t* pos,
+                                   const float* weights, int64_t T, int64_t k, void* y, int64_t ldy,
+                                   fp8_stream_t stream) {
+  if (!pair_sizes_ok(T, k)) return FP8_ERR_INVALID_ARG;
+  FP8_TRY(check_rows(ys, f32, R, H, ldys));
+  FP8_TRY(check_rows(y, f32, T, H, ldy));
+  if (!aligned(pos, 4) || !aligned(weights, 4)) return FP8_ERR_MISALIGNED;
+  if (T == 0 || H == 0) return FP8_OK;
+  if (pos == nullptr) return FP8_ERR_INVALID_ARG;
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int size = f32 ? 4 : 2;
+  const bool whole = whole_pieces(ys, R, ldys, H, size) && whole_pieces(y, T, ldy, H, size);
+  if (f32)
+    return whole ? launch_rows_back<float, 4>(ys, ldys, R, pos, weights, k, T, H, y, ldy, sms, st)
+                 : launch_rows_back<float, 1>(ys, ldys, R, pos, weights, k, T, H, y, ldy, sms, st);
+  return whole ? launch_rows_back<uint16_t, 8>(ys, ldys, R, pos, weights, k, T, H, y, ldy, sms, st)
+               : launch_rows_back<uint16_t, 1>(ys, ldys, R, pos, weights, k, T, H, y, ldy, sms, st);
+}
+
+FP8_API fp8_status fp8_moe_dispatch_grad(const void* dxs, int f32, int64_t R, int64_t H, int64_t lddxs,
+                                         const int32_t* pos, int64_t T, int64_t k, void* dx, int64_t lddx,
+                                         fp8_stream_t stream) {
+  return fp8_moe_combine(dxs, f32, R, H, lddxs, pos, nullptr, T, k, dx, lddx, stream);
+}
+
+FP8_API fp8_status fp8_moe_combine_grad(const void* dy, int f32, int64_t T, int64_t H, int64_t lddy, const void* ys,
+                                        int64_t R, int64_t ldys, const int32_t* pos, const float* weights, int64_t k,
+                                        void* dys, int64_t lddys, float* dw, fp8_stream_t stream) {
+  if (!pair_sizes_ok(T, k)) return FP8_ERR_INVALID_ARG;
+  FP8_TRY(check_rows(dy, f32, T, H, lddy));
+  FP8_TRY(check_rows(ys, f32, R, H, ldys));
+  FP8_TRY(check_rows(dys, f32, R, H, lddys));
+  if (!aligned(pos, 4) || !aligned(weights, 4) || !aligned(dw, 4)) return FP8_ERR_MISALIGNED;
+  if (T == 0) return FP8_OK;
+  if (pos == nullptr || weights == nullptr || dw == nullptr) return FP8_ERR_INVALID_ARG;
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int size = f32 ? 4 : 2;
+  const bool whole = whole_pieces(dy, T, lddy, H, size) && whole_pieces(ys, R, ldys, H, size) &&
+                     whole_pieces(dys, R, lddys, H, size);
+  if (f32)
+    return whole ? launch_rows_back_grad<float, 4>(dy, lddy, ys, ldys, R, pos, weights, k, T, H, dys, lddys, dw, sms, st)
+                 : launch_rows_back_grad<float, 1>(dy, lddy, ys, ldys, R, pos, weights, k, T, H, dys, lddys, dw, sms, st);
+  return whole
+             ? launch_rows_back_grad<uint16_t, 8>(dy, lddy, ys, ldys, R, pos, weights, k, T, H, dys, lddys, dw, sms, st)
+             : launch_rows_back_grad<uint16_t, 1>(dy, lddy, ys, ldys, R, pos, weights, k, T, H, dys, lddys, dw, sms, st);
 }

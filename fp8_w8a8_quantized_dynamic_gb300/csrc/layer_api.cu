@@ -1,0 +1,120 @@
+// C ABI of the norms around a block (declared in include/fp8w8a8.h): argument validation, launches.
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "api_common.h"
+#include "norm.cuh"
+
+namespace {
+
+using namespace fp8k;
+
+fp8_status check_row_vector(const void* p) { return aligned(p, 2) ? FP8_OK : FP8_ERR_MISALIGNED; }
+
+int rows_vec(const void* p, int64_t rows, int64_t ld) { return aligned(p, 16) && (rows <= 1 || ld % 8 == 0); }
+
+template <int kThreads, int kUnits>
+fp8_status launch_norm(const norm::Params& p, int sms, cudaStream_t st) {
+  const int per_sm = 2048 / kThreads;
+  const int64_t grid = std::min<int64_t>(p.rows, int64_t(sms) * per_sm);
+  return launch(norm::residual_norm_kernel<kThreads, kUnits>, dim3(unsigned(grid)), dim3(kThreads), 0, st, true,
+                dim3(1, 1, 1), p);
+}
+
+// Threads of a row.
+fp8_status launch_norm_any(const norm::Params& p, int sms, cudaStream_t st) {
+  const int units = (p.cols + 15) / 16 * 2;  // of eight columns; the codes' rows are whole sixteens
+  if (units <= 128) return launch_norm<128, 1>(p, sms, st);
+  if (units <= 256) return launch_norm<256, 1>(p, sms, st);
+  if (units <= 512) return p.rows <= sms ? launch_norm<512, 1>(p, sms, st) : launch_norm<256, 2>(p, sms, st);
+  if (units <= 1024) return p.rows <= sms ? launch_norm<1024, 1>(p, sms, st) : launch_norm<256, 4>(p, sms, st);
+  if (units <= 2048) return p.rows <= sms ? launch_norm<1024, 2>(p, sms, st) : launch_norm<512, 4>(p, sms, st);
+  return launch_norm<1024, 4>(p, sms, st);
+}
+
+// What both calls share, up to r.
+fp8_status fill_norm(norm::Params& p, const void* y, int64_t M, int64_t H, int64_t ldy, const void* post_w,
+                     const void* gate, int64_t ldg, float scale, const void* residual, int64_t ldr, const void* w,
+                     float eps, int plus_one, void* r, int64_t ldro) {
+  FP8_TRY(check_bf16_mat(y, M, H, ldy));
+  if (H > norm::kMaxCols) return FP8_ERR_INVALID_ARG;
+  if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(scale)) return FP8_ERR_INVALID_ARG;
+  if (plus_one != 0 && plus_one != 1) return FP8_ERR_INVALID_ARG;
+  if (gate != nullptr && ldg != 0) FP8_TRY(check_bf16_mat(gate, M, H, ldg));
+  if (residual != nullptr) FP8_TRY(check_bf16_mat(residual, M, H, ldr));
+  if (r != nullptr) FP8_TRY(check_bf16_mat(r, M, H, ldro));
+  FP8_TRY(check_row_vector(post_w));
+  FP8_TRY(check_row_vector(gate));
+  FP8_TRY(check_row_vector(w));
+  p.rows = M;
+  p.cols = int(H);
+  p.y = static_cast<const uint16_t*>(y);
+  p.ldy = ldy;
+  p.vec_y = rows_vec(y, M, ldy);
+  p.post_w = static_cast<const uint16_t*>(post_w);
+  p.vec_post = aligned(post_w, 16);
+  p.gate = static_cast<const uint16_t*>(gate);
+  p.ldg = ldg;
+  p.vec_gate = rows_vec(gate, M, ldg);
+  p.residual = static_cast<const uint16_t*>(residual);
+  p.ldr = ldr;
+  p.vec_res = rows_vec(residual, M, ldr);
+  p.w = static_cast<const uint16_t*>(w);
+  p.vec_w = aligned(w, 16);
+  p.scale = scale;
+  p.eps = eps;
+  p.w_offset = plus_one ? 1.0f : 0.0f;
+  p.r = static_cast<uint16_t*>(r);
+  p.ldro = ldro;
+  p.vec_r = rows_vec(r, M, ldro);
+  return FP8_OK;
+}
+
+}  // namespace
+
+FP8_API fp8_status fp8_residual_norm(const void* y_bf16, int64_t M, int64_t H, int64_t ldy, const void* post_w_bf16,
+                                     const void* gate_bf16, int64_t ldg, float scale, const void* residual_bf16,
+                                     int64_t ldr, const void* w_bf16, float eps, int plus_one, void* r_bf16,
+                                     int64_t ldro, void* n_bf16, int64_t ldn, fp8_stream_t stream) {
+  norm::Params p = {};
+  FP8_TRY(fill_norm(p, y_bf16, M, H, ldy, post_w_bf16, gate_bf16, ldg, scale, residual_bf16, ldr, w_bf16, eps,
+                    plus_one, r_bf16, ldro));
+  if (n_bf16 != nullptr) FP8_TRY(check_bf16_mat(n_bf16, M, H, ldn));
+  if (M == 0 || H == 0) return FP8_OK;
+  if ((w_bf16 == nullptr) != (n_bf16 == nullptr)) return FP8_ERR_INVALID_ARG;
+  if (n_bf16 == nullptr && r_bf16 == nullptr) return FP8_ERR_INVALID_ARG;
+  p.pre = n_bf16 != nullptr;
+  p.n = static_cast<uint16_t*>(n_bf16);
+  p.ldn = ldn;
+  p.vec_n = rows_vec(n_bf16, M, ldn);
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  return launch_norm_any(p, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+FP8_API fp8_status fp8_residual_norm_quantize(const void* y_bf16, int64_t M, int64_t H, int64_t ldy,
+                                              const void* post_w_bf16, const void* gate_bf16, int64_t ldg,
+                                              float scale, const void* residual_bf16, int64_t ldr,
+                                              const void* w_bf16, float eps, int plus_one, void* r_bf16,
+                                              int64_t ldro, uint8_t* qn, int64_t ldq, float* s_n, int64_t lds,
+                                              fp8_stream_t stream) {
+  norm::Params p = {};
+  FP8_TRY(fill_norm(p, y_bf16, M, H, ldy, post_w_bf16, gate_bf16, ldg, scale, residual_bf16, ldr, w_bf16, eps,
+                    plus_one, r_bf16, ldro));
+  FP8_TRY(check_fp8_mat(qn, M, H, ldq));
+  FP8_TRY(check_row_scales(s_n, M, H, lds));
+  if (M == 0) return FP8_OK;
+  if (H > 0 && w_bf16 == nullptr) return FP8_ERR_INVALID_ARG;
+  p.pre = 1;
+  p.q = qn;
+  p.ldq = ldq;
+  p.s = s_n;
+  p.lds = lds;
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  return launch_norm_any(p, sms, reinterpret_cast<cudaStream_t>(stream));
+}

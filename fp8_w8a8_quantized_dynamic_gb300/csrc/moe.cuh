@@ -321,13 +321,14 @@ plan_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, i
 
 // Order of the routed pairs: pair i (= token * k + j) with expert ids[i] in [0, experts) gets row
 // pos[i], rows sorted by expert and, within one, by pair (stable, so nothing depends on timing);
-// any other id gives -1. Then the row tiles. A CTA's warps count their contiguous shares of the CTA's pairs by expert in
+// any other id gives -1. Then the row tiles and the experts' first rows (each where its pointer is not null). A CTA's warps count their contiguous shares of the CTA's pairs by expert in
 // shared memory (equal ids of a step are found by a warp match), the counts are scanned over warps,
 // CTAs (from plan_count_kernel; one CTA needs none) and experts, and a second walk hands out rows.
 // One CTA sorts 65536 pairs in 109 us, 64 CTAs in 11 us.
 __global__ void __launch_bounds__(kPlanThreads, 1)
 plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, const int* __restrict__ counts,
-            int* __restrict__ pos, block::RowTile* __restrict__ tiles, int* __restrict__ n_tiles) {
+            int* __restrict__ pos, block::RowTile* __restrict__ tiles, int* __restrict__ n_tiles,
+            int* __restrict__ offsets) {
   extern __shared__ int count[];  // [kPlanWarps][experts], then [experts] first rows
   int* total = count + kPlanWarps * experts;
   __shared__ int warp_sum[2][kPlanWarps];
@@ -387,12 +388,16 @@ plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, const i
   if (int(threadIdx.x) < experts) {
     total[threadIdx.x] = rows_before;
     // the CTAs share out an expert's tiles
-    for (int j = blockIdx.x; j < my_tiles; j += gridDim.x) {
+    for (int j = blockIdx.x; tiles != nullptr && j < my_tiles; j += gridDim.x) {
       const int r0 = rows_before + j * block::kRowTile;
       tiles[tiles_before + j] = block::RowTile{int(threadIdx.x), r0, rows_before + tot, 0};
     }
+    if (offsets != nullptr && blockIdx.x == 0) {
+      offsets[threadIdx.x] = rows_before;
+      if (int(threadIdx.x) == experts - 1) offsets[experts] = rows_before + tot;
+    }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *n_tiles = all_t;
+  if (n_tiles != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *n_tiles = all_t;
   __syncthreads();
   for (int64_t i = begin; i < end; i += 32) {
     const int id = i + lane < end ? ids[i + lane] : -1;
@@ -449,6 +454,154 @@ weighted_sum_kernel(const float* __restrict__ y, int64_t ldy32, const int* __res
       const float a[4] = {acc.x, acc.y, acc.z, acc.w};
       for (int e = 0; e < 4; ++e)
         if (c + e < cols) dst[e] = __bfloat16_as_ushort(__float2bfloat16_rn(a[e]));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// tokens sorted by expert and back
+// ---------------------------------------------------------------------------
+
+constexpr int kRowThreads = 256;
+
+// Row t of x to the rows pos[t, j] of xs (those in [0, rows)), as U-sized pieces: `pieces` of a row, row strides in pieces.
+template <typename U>
+__global__ void __launch_bounds__(kRowThreads)
+rows_out_kernel(const U* __restrict__ x, int64_t ldx, int64_t tokens, int64_t pieces, const int* __restrict__ pos, int k,
+                int64_t rows, U* __restrict__ xs, int64_t ldxs) {
+  pdl_trigger();
+  pdl_wait();
+  for (int64_t u = int64_t(blockIdx.x) * kRowThreads + threadIdx.x; u < tokens * pieces;
+       u += int64_t(gridDim.x) * kRowThreads) {
+    const int64_t t = u / pieces, c = u - t * pieces;
+    const U v = x[t * ldx + c];
+    for (int j = 0; j < k; ++j) {
+      const int d = pos[t * k + j];
+      if (d >= 0 && d < rows) xs[int64_t(d) * ldxs + c] = v;
+    }
+  }
+}
+
+// kN columns of a row as fp32.
+template <int kN>
+__device__ __forceinline__ void load_cols(const float* p, float (&f)[kN]) {
+  if constexpr (kN == 4) {
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(p));
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+  } else {
+    f[0] = __ldcs(p);
+  }
+}
+template <int kN>
+__device__ __forceinline__ void load_cols(const uint16_t* p, float (&f)[kN]) {
+  if constexpr (kN == 8) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
+  } else {
+    f[0] = bf16_bits_to_float(__ldcs(p));
+  }
+}
+template <int kN>
+__device__ __forceinline__ void store_cols(float* p, const float (&f)[kN]) {
+  if constexpr (kN == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  else
+    *p = f[0];
+}
+template <int kN>
+__device__ __forceinline__ void store_cols(uint16_t* p, const float (&f)[kN]) {
+  if constexpr (kN == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                              pack_bf16x2(f[6], f[7]));
+  else
+    *p = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+}
+
+// y[t] = sum_j w[t, j] ys[pos[t, j]] (weights null: 1) over the pairs that have a row, in the order of j, in fp32, kN columns
+// a thread (1 or 16 bytes' worth; the row's columns are a multiple of it).
+template <typename T, int kN>
+__global__ void __launch_bounds__(kRowThreads)
+rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int* __restrict__ pos,
+                 const float* __restrict__ weights, int k, int64_t tokens, int64_t cols, T* __restrict__ y, int64_t ldy) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t upr = cols / kN;
+  for (int64_t u = int64_t(blockIdx.x) * kRowThreads + threadIdx.x; u < tokens * upr;
+       u += int64_t(gridDim.x) * kRowThreads) {
+    const int64_t t = u / upr, c = (u - t * upr) * kN;
+    float acc[kN] = {};
+    for (int j = 0; j < k; ++j) {
+      const int d = pos[t * k + j];
+      if (d < 0 || d >= rows) continue;
+      const float w = weights ? weights[t * k + j] : 1.0f;
+      float f[kN];
+      load_cols<kN>(ys + int64_t(d) * ldys + c, f);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+    }
+    store_cols<kN>(y + t * ldy + c, acc);
+  }
+}
+
+constexpr int kGradPairs = 8;  // pairs of a token whose dot products a thread holds at once
+
+// The gradient of rows_back: dys[pos[t, j]] = w[t, j] dy[t], dw[t, j] = <dy[t], ys[pos[t, j]]> (0 for a pair without a
+// row), fp32 sums in a fixed order. dys may be ys. blockDim.x threads a token (a power of two from 32), blockDim.y tokens a CTA.
+template <typename T, int kN>
+__global__ void __launch_bounds__(kRowThreads)
+rows_back_grad_kernel(const T* __restrict__ dy, int64_t lddy, const T* ys, int64_t ldys, int64_t rows,
+                      const int* __restrict__ pos, const float* __restrict__ weights, int k, int64_t tokens, int64_t cols,
+                      T* dys, int64_t lddys, float* __restrict__ dw) {
+  __shared__ float part[kRowThreads / 32][kGradPairs];
+  pdl_trigger();
+  pdl_wait();
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t step = int64_t(gridDim.x) * blockDim.y;
+  for (int64_t t0 = int64_t(blockIdx.x) * blockDim.y; t0 < tokens; t0 += step) {
+    const int64_t t = t0 + threadIdx.y;
+    for (int j0 = 0; j0 < k; j0 += kGradPairs) {
+      float sum[kGradPairs] = {};
+      if (t < tokens) {
+        int d[kGradPairs];
+        float w[kGradPairs];
+#pragma unroll
+        for (int j = 0; j < kGradPairs; ++j) {
+          d[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
+          if (d[j] >= rows) d[j] = -1;
+          w[j] = d[j] >= 0 ? weights[t * k + j0 + j] : 0.0f;
+        }
+        for (int64_t c = int64_t(threadIdx.x) * kN; c < cols; c += int64_t(blockDim.x) * kN) {
+          float g[kN];
+          load_cols<kN>(dy + t * lddy + c, g);
+#pragma unroll
+          for (int j = 0; j < kGradPairs; ++j) {
+            if (d[j] < 0) continue;
+            float f[kN], o[kN];
+            load_cols<kN>(ys + int64_t(d[j]) * ldys + c, f);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              sum[j] = fmaf(g[i], f[i], sum[j]);
+              o[i] = w[j] * g[i];
+            }
+            store_cols<kN>(dys + int64_t(d[j]) * lddys + c, o);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kGradPairs; ++j) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+        if (lane == 0) part[threadIdx.y * warps + warp][j] = sum[j];
+      }
+      __syncthreads();
+      if (t < tokens && threadIdx.x < kGradPairs && j0 + int(threadIdx.x) < k) {
+        float v = 0.0f;
+        for (int i = 0; i < warps; ++i) v += part[threadIdx.y * warps + i][threadIdx.x];
+        dw[t * k + j0 + threadIdx.x] = v;
+      }
+      __syncthreads();
     }
   }
 }

@@ -406,6 +406,70 @@ fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int64_t ldx
                            int64_t ldy, void* ws, size_t ws_bytes, fp8_stream_t stream);
 
 /*
+ * Tokens to rows sorted by expert, and back: for experts' networks other than the one above (a per-tensor
+ * fp8_linear of each, or ones that are trained). Rows are bf16, or fp32 when f32 is 1.
+ *
+ * fp8_moe_dispatch: pair (t, j) with ids[t, j] in [0, E) gets row pos[t, j] of xs, rows sorted by expert and, within one,
+ * by t and j; any other id gets pos -1 and no row. offsets[e] is expert e's first row, offsets[E] the number
+ * of rows; xs[pos[t, j]] = x[t]. xs has T * k rows; those from offsets[E] on are left as they were. ids and pos int32
+ * [T, k], offsets int32 [E + 1], in device memory. ws: >= fp8_moe_dispatch_workspace_bytes, 256-byte aligned.
+ */
+size_t fp8_moe_dispatch_workspace_bytes(int64_t T, int64_t k, int64_t E);
+fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H, int64_t ldx, const int32_t* ids, int64_t k,
+                            int64_t E, void* xs, int64_t ldxs, int32_t* pos, int32_t* offsets, void* ws,
+                            size_t ws_bytes, fp8_stream_t stream);
+
+/* y[t] = sum_j weights[t, j] ys[pos[t, j]] over the pairs with pos in [0, R), in the order of j, in fp32 with one
+ * rounding; a token with none gets zeros. weights fp32 [T, k], or NULL for ones. */
+fp8_status fp8_moe_combine(const void* ys, int f32, int64_t R, int64_t H, int64_t ldys, const int32_t* pos,
+                           const float* weights, int64_t T, int64_t k, void* y, int64_t ldy, fp8_stream_t stream);
+
+/* The gradient of fp8_moe_combine: dys[pos[t, j]] = weights[t, j] dy[t] (rows of no pair are left as they were) and
+ * dw[t, j] = <dy[t], ys[pos[t, j]]>, fp32 [T, k], 0 for a pair without a row. dys may be ys. */
+fp8_status fp8_moe_combine_grad(const void* dy, int f32, int64_t T, int64_t H, int64_t lddy, const void* ys, int64_t R,
+                                int64_t ldys, const int32_t* pos, const float* weights, int64_t k, void* dys,
+                                int64_t lddys, float* dw, fp8_stream_t stream);
+
+/* The gradient of fp8_moe_dispatch: dx[t] = sum_j dxs[pos[t, j]], as fp8_moe_combine without weights. */
+fp8_status fp8_moe_dispatch_grad(const void* dxs, int f32, int64_t R, int64_t H, int64_t lddxs, const int32_t* pos,
+                                 int64_t T, int64_t k, void* dx, int64_t lddx, fp8_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Norms before and after a block, with its gate and residual.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * The end of one block and the norm before the next, row by row, in fp32:
+ *   t = y                                                  (post_w NULL)
+ *   t = y / sqrt(mean y^2 + eps) * post_w                  (else)
+ *   r = residual + scale * gate * t                        (NULL: 0 and 1)
+ *   n = r / sqrt(mean r^2 + eps) * w                       (of r before its rounding)
+ * y, residual bf16 [M, H]; post_w, w bf16 [H], with plus_one 1 both stand for
+ * 1 + their values; gate bf16 [M, H] with row stride ldg, or [H] with ldg 0.
+ * Writes r and n as bf16 [M, H]; either may be NULL (w NULL with n). r may be y
+ * or residual itself, and so may n where r is not. The mean is over H columns;
+ * rows whose squares pass fp32's range are normalised as the formula has it. A
+ * NaN or an infinity in a row makes NaN of what it multiplies in that row and
+ * of no other row. eps > 0, scale finite, H <= 32768
+ * (FP8_ERR_INVALID_ARG). post_w and w are weights to the launch ordering above,
+ * gate is an activation.
+ */
+fp8_status fp8_residual_norm(const void* y_bf16, int64_t M, int64_t H, int64_t ldy, const void* post_w_bf16,
+                             const void* gate_bf16, int64_t ldg, float scale, const void* residual_bf16,
+                             int64_t ldr, const void* w_bf16, float eps, int plus_one, void* r_bf16, int64_t ldro,
+                             void* n_bf16, int64_t ldn, fp8_stream_t stream);
+
+/* The same with n quantized as fp8_block_quantize_act quantizes, from fp32: qn u8 [M, ldq] (bytes [H, ldq) of
+ * each row zero) and s_n fp32 [ceil(H/128)][lds], lds >= M: operands of fp8_block_scaled_mm. r may be NULL. */
+fp8_status fp8_residual_norm_quantize(const void* y_bf16, int64_t M, int64_t H, int64_t ldy, const void* post_w_bf16,
+                                      const void* gate_bf16, int64_t ldg, float scale, const void* residual_bf16,
+                                      int64_t ldr, const void* w_bf16, float eps, int plus_one, void* r_bf16,
+                                      int64_t ldro, uint8_t* qn, int64_t ldq, float* s_n, int64_t lds,
+                                      fp8_stream_t stream);
+
+/*
  * Diagnostics (no counterpart on the source pages): the launch the GEMM path of
  * fp8_linear (and fp8_scaled_mm, which never splits K) would use for FP8
  * operands qa [M, ldqa] and qw [N, ldqw] (ld in bytes), K columns, and a
