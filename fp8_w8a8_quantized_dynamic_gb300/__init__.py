@@ -19,6 +19,10 @@ Typical use::
     y = fp8_block_linear(a, qw, s_w, bias)           # activations: a scale per row and 128 columns
     ids, weights = fp8_moe_route(logits, k, score="sigmoid", renormalize=True)
     y = fp8_moe_experts(x, ids, weights, qw13, s13, qw2, s2)  # the chosen experts, block-scaled
+    xs, pos, offsets = fp8_moe_dispatch(x, ids, E)   # or rows sorted by expert for other networks, and back
+    y = fp8_moe_combine(ys, pos, weights)
+    y = fp8_lora_add(y, x, a, b, request_adapters)   # adapters of many requests beside a projection
+    qa, s_a, r = fp8_residual_norm_quantize(y, w_norm, residual=r)  # the next block's norm, quantized for it
 
 Kernels are launched on the current CUDA device and its current stream; tensors of another device are refused
 (ValueError).
@@ -92,6 +96,9 @@ _SIGNATURES = {
     "fp8_moe_combine": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp]),
     "fp8_moe_combine_grad": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp]),
     "fp8_moe_dispatch_grad": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "fp8_lora_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "fp8_lora_add": (_int, [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _sz,
+                            _vp]),
     "fp8_residual_norm": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.c_float, _vp, _i64, _vp, ctypes.c_float,
                                  _int, _vp, _i64, _vp, _i64, _vp]),
     "fp8_residual_norm_quantize": (_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, ctypes.c_float, _vp, _i64, _vp,
@@ -640,6 +647,56 @@ def fp8_moe_experts(x, ids, weights, qw13, s13, qw2, s2, out=None, ws=None):
     if status:
         raise FP8Error(status, "fp8_moe_experts")
     return y
+
+
+# ---------------------------------------------------------------------------
+# adapters beside a projection
+# ---------------------------------------------------------------------------
+
+def fp8_lora_workspace_bytes(M: int, K: int, N: int, L: int, r: int) -> int:
+    return int(lib().fp8_lora_workspace_bytes(M, K, N, L, r))
+
+
+def fp8_lora_add(y, x, a, b, ids, scales=None, out=None, ws=None):
+    """The low-rank adapters of many requests beside a projection they share: y[m] + scales[e] * B[e] (A[e] x[m]) with
+    e = ids[m], bf16 [M, N]. y [M, N] is the projection's output of x [M, K] (both bf16), a bf16 [L, r, K],
+    b bf16 [L, N, r], ids int32 [M] (outside [0, L): no adapter, the row is y's), scales fp32 [L] or None (ones). out may
+    be y."""
+    torch = _torch_module or _torch()
+    bf16 = torch.bfloat16
+    if y.dtype is not bf16 or x.dtype is not bf16 or y.dim() != 2 or x.dim() != 2 or not y.is_cuda:
+        raise ValueError("y, x: expected CUDA bf16 matrices with unit column stride")
+    M, N = y.shape
+    K = x.shape[1]
+    ldy, unit_y = y.stride()
+    ldx, unit_x = x.stride()
+    if (unit_y != 1 and N > 1) or (unit_x != 1 and K > 1):
+        raise ValueError("y, x: expected CUDA bf16 matrices with unit column stride")
+    index = y.get_device()
+    if x.shape[0] != M or x.get_device() != index:
+        raise ValueError(f"x: expected [{M}, K] on cuda:{index}")
+    if a.dim() != 3:
+        raise ValueError("a: expected bf16 [L, r, K]")
+    L, r, _ = a.shape
+    _check_dense(a, bf16, (L, r, K), index, "a")
+    _check_dense(b, bf16, (L, N, r), index, "b")
+    _check_dense(ids, torch.int32, (M,), index, "ids")
+    if scales is not None:
+        _check_dense(scales, torch.float32, (L,), index, "scales")
+    lb = _lib or lib()
+    need = lb.fp8_lora_workspace_bytes(M, K, N, L, r)
+    wp, wn, ws = _scratch(ws, need, y) if need or ws is not None else (None, 0, None)
+    if out is None:
+        o, ldo = torch.empty((M, N), dtype=bf16, device=y.device), N or 1
+    else:
+        o = _out_bf16(out, M, N, y)
+        ldo = _row_stride(o, M, N)
+    status = lb.fp8_lora_add(y.data_ptr(), M, N, ldy if M > 1 else N or 1, x.data_ptr(), K, ldx if M > 1 else K or 1,
+                             a.data_ptr(), b.data_ptr(), L, r, ids.data_ptr(), None if scales is None else scales.data_ptr(),
+                             o.data_ptr(), ldo, wp, wn, _stream_ptr(y))
+    if status:
+        raise FP8Error(status, "fp8_lora_add")
+    return o
 
 
 # ---------------------------------------------------------------------------

@@ -18,6 +18,7 @@
 #include "fp8w8a8.h"
 #include "api_common.h"
 #include "block_gemm.h"
+#include "lora.h"
 #include "device_common.cuh"
 #include "gemm_tcgen05.h"
 #include "gemv.h"
@@ -764,7 +765,8 @@ FP8_API fp8_status fp8_gemm_plan_model(int64_t M, int64_t N, int64_t K, int num_
 FP8_API fp8_status fp8_last_device_status(fp8_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FP8_ERR_CUDA;
   const unsigned int e =
-      fp8k::gemm_read_and_clear_error() | gemv::read_and_clear_error() | fp8k::block::gemm_read_and_clear_error();
+      fp8k::gemm_read_and_clear_error() | gemv::read_and_clear_error() | fp8k::block::gemm_read_and_clear_error() |
+      fp8k::lora::read_and_clear_error();
   if (cudaGetLastError() != cudaSuccess) return FP8_ERR_CUDA;
   return (e & kErrTimeout) ? FP8_ERR_TIMEOUT : FP8_OK;
 }

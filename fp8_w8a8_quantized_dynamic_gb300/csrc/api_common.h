@@ -144,4 +144,14 @@ inline fp8_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
 
 inline size_t round_up_256(size_t b) { return (b + 255) / 256 * 256; }
 
+// Hands out the parts of a workspace.
+struct Carver {
+  size_t at = 0;
+  size_t take(size_t bytes) {
+    const size_t p = at;
+    at = round_up_256(at + bytes);
+    return p;
+  }
+};
+
 }  // namespace fp8k

@@ -14,6 +14,40 @@
 #include "device_cache.h"
 #include "moe.cuh"
 
+namespace fp8k {
+namespace moe {
+
+// CTAs that sort the pairs; more than one need their counts first (the whole layer, experts of 2048 x
+// 1408, in us: 4096 pairs 131.7, by one CTA 134.5; 8192 pairs 161.1 and 170.8).
+int plan_ctas(int64_t pairs) {
+  if (pairs <= 2 * kPlanPairs) return 1;  // a second launch costs more than it saves
+  return int(std::min<int64_t>(kPlanMaxCtas, (pairs + kPlanPairs - 1) / kPlanPairs));
+}
+
+namespace {
+PerDeviceCache<const void*, int> g_attr_cache;
+}
+
+fp8_status launch_plan(const Plan& p, cudaStream_t st) {
+  const size_t smem = size_t(kPlanWarps + 1) * p.experts * sizeof(int);
+  int dev = 0, set = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
+  if (!g_attr_cache.get(dev, reinterpret_cast<const void*>(plan_kernel), &set, [&](int* v) {
+        *v = 1;
+        return report_cuda(cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                (kPlanWarps + 1) * kMaxExperts * int(sizeof(int))),
+                           "plan smem attribute") == cudaSuccess;
+      }))
+    return FP8_ERR_CUDA;
+  const int ctas = plan_ctas(p.pairs);
+  if (ctas > 1)
+    FP8_TRY(launch(plan_count_kernel, dim3(ctas), dim3(kPlanThreads), 0, st, true, dim3(1, 1, 1), p));
+  return launch(plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, st, true, dim3(1, 1, 1), p, int(ctas > 1));
+}
+
+}  // namespace moe
+}  // namespace fp8k
+
 namespace {
 
 using namespace fp8k;
@@ -40,15 +74,6 @@ fp8_status launch_quantize_rows(const BF16Mat& a, uint8_t* q, int64_t ldq, float
   return units < (int64_t(1) << 31) ? go(block::quantize_rows_1x128_kernel<uint32_t>)
                                     : go(block::quantize_rows_1x128_kernel<uint64_t>);
 }
-
-struct Carver {
-  size_t at = 0;
-  size_t take(size_t bytes) {
-    const size_t p = at;
-    at = round_up_256(at + bytes);
-    return p;
-  }
-};
 
 // Whether the GEMV takes a dense product. Its CTAs each bring in their K slices of A, so its time grows
 // with M * K and the GEMM's does not (both stream the weights, so N decides nothing). Graphs over weights
@@ -156,13 +181,6 @@ bool one_token(int64_t T, int64_t k, int64_t H, int64_t I) {
   return T == 1 && block::gemv_fits(1, H, 2) && block::gemv_fits(1, k * blocks_of(I) * block::kBlock, 1);
 }
 
-// CTAs that sort the pairs; more than one need their counts first (the whole layer, experts of 2048 x
-// 1408, in us: 4096 pairs 131.7, by one CTA 134.5; 8192 pairs 161.1 and 170.8).
-int plan_ctas(int64_t pairs) {
-  if (pairs <= 2 * moe::kPlanPairs) return 1;  // a second launch costs more than it saves
-  return int(std::min<int64_t>(moe::kPlanMaxCtas, (pairs + moe::kPlanPairs - 1) / moe::kPlanPairs));
-}
-
 struct MoeWs {
   size_t n_tiles, tiles, counts, pos, qx, s_x, h, s_h, y, total;
   int64_t pairs, max_tiles, ldx, ldh, ldy, lds;
@@ -182,7 +200,7 @@ MoeWs moe_ws(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     w.lds = (w.pairs + 3) / 4 * 4;
     w.n_tiles = c.take(4);
     w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
-    w.counts = c.take(plan_ctas(w.pairs) > 1 ? size_t(plan_ctas(w.pairs)) * size_t(E) * 4 : 0);
+    w.counts = c.take(moe::plan_ctas(w.pairs) > 1 ? size_t(moe::plan_ctas(w.pairs)) * size_t(E) * 4 : 0);
     w.pos = c.take(pairs * 4);
     w.y = c.take(pairs * size_t(w.ldy) * 4);
     w.qx = c.take(size_t(block::gemm_held_rows(w.pairs, w.ldx)) * size_t(w.ldx));
@@ -198,28 +216,6 @@ MoeWs moe_ws(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
 bool moe_sizes_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   return T >= 0 && k >= 1 && k <= moe::kMaxChosen && E >= 1 && E <= moe::kMaxExperts && H >= 0 && H <= kMaxDim &&
          I >= 1 && I <= kMaxDim / 2 && T <= kMaxRows / k && T * k <= (int64_t(1) << 56) / (H + I);
-}
-
-PerDeviceCache<const void*, int> g_attr_cache;
-
-fp8_status launch_plan(const int32_t* ids, int64_t pairs, int E, int* counts, int* pos, block::RowTile* tiles,
-                       int* n_tiles, int* offsets, cudaStream_t st) {
-  const size_t smem = size_t(moe::kPlanWarps + 1) * E * sizeof(int);
-  int dev = 0, set = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
-  if (!g_attr_cache.get(dev, reinterpret_cast<const void*>(moe::plan_kernel), &set, [&](int* v) {
-        *v = 1;
-        return report_cuda(cudaFuncSetAttribute(moe::plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                (moe::kPlanWarps + 1) * moe::kMaxExperts * int(sizeof(int))),
-                           "plan smem attribute") == cudaSuccess;
-      }))
-    return FP8_ERR_CUDA;
-  const int ctas = plan_ctas(pairs);
-  if (ctas > 1)
-    FP8_TRY(launch(moe::plan_count_kernel, dim3(ctas), dim3(moe::kPlanThreads), 0, st, true, dim3(1, 1, 1), ids, pairs,
-                   E, counts));
-  return launch(moe::plan_kernel, dim3(ctas), dim3(moe::kPlanThreads), smem, st, true, dim3(1, 1, 1), ids, pairs, E,
-                ctas > 1 ? static_cast<const int*>(counts) : nullptr, pos, tiles, n_tiles, offsets);
 }
 
 template <typename T>
@@ -527,8 +523,8 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
   block::RowTile* tiles = reinterpret_cast<block::RowTile*>(b + w.tiles);
   int* pos = reinterpret_cast<int*>(b + w.pos);
   float* y32 = reinterpret_cast<float*>(b + w.y);
-  FP8_TRY(launch_plan(ids, w.pairs, int(E), reinterpret_cast<int*>(b + w.counts), pos, tiles, n_tiles,
-                      nullptr, st));
+  moe::Plan plan = {ids, w.pairs, int(E), -1, reinterpret_cast<int*>(b + w.counts), pos, nullptr, tiles, n_tiles, nullptr};
+  FP8_TRY(moe::launch_plan(plan, st));
   // quantize each token once into its rows; gate and up products with SwiGLU and the quantization
   // of h in their epilogue; the product back; the weighted sum
   float* s_x = reinterpret_cast<float*>(b + w.s_x);
@@ -580,7 +576,7 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
 
 FP8_API size_t fp8_moe_dispatch_workspace_bytes(int64_t T, int64_t k, int64_t E) {
   if (!pair_sizes_ok(T, k) || E < 1 || E > moe::kMaxExperts) return 0;
-  const int ctas = plan_ctas(T * k);
+  const int ctas = moe::plan_ctas(T * k);
   return ctas > 1 ? round_up_256(size_t(ctas) * size_t(E) * 4) : 0;
 }
 
@@ -596,7 +592,7 @@ FP8_API fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H
   int sms = 0;
   FP8_TRY(current_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  FP8_TRY(launch_plan(ids, T * k, int(E), static_cast<int*>(ws), pos, nullptr, nullptr, offsets, st));
+  FP8_TRY(moe::launch_plan({ids, T * k, int(E), -1, static_cast<int*>(ws), pos, nullptr, nullptr, nullptr, offsets}, st));
   if (T == 0 || H == 0) return FP8_OK;
   const int size = f32 ? 4 : 2;
   // the widest pieces that every row of both consists of

@@ -1,4 +1,4 @@
-// C ABI of the norms around a block (declared in include/fp8w8a8.h): argument validation, launches.
+// C ABI of the norms around a block and of the adapters beside a projection (declared in include/fp8w8a8.h): argument validation, launches.
 
 #include <cuda_runtime.h>
 
@@ -7,6 +7,8 @@
 #include <cstdint>
 
 #include "api_common.h"
+#include "lora.h"
+#include "moe_plan.h"
 #include "norm.cuh"
 
 namespace {
@@ -74,6 +76,40 @@ fp8_status fill_norm(norm::Params& p, const void* y, int64_t M, int64_t H, int64
   return FP8_OK;
 }
 
+// ---- adapters ----
+
+constexpr int kMaxAdapters = 511;                // one more class of the sort stands for none
+constexpr int64_t kMaxLoraDim = int64_t(1) << 30;  // columns past a tile's last keep 32-bit indexes
+
+bool lora_sizes_ok(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
+  return M >= 0 && M <= kMaxDim - block::kRowTile && K >= 0 && K <= kMaxLoraDim && N >= 0 && N <= kMaxLoraDim && L >= 0 &&
+         L <= kMaxAdapters && r >= 1 && r <= lora::kMaxRank;
+}
+
+// Few tokens: one launch, a cluster a token.
+bool lora_by_token(int64_t M) { return M <= 64; }
+
+struct LoraWs {
+  size_t n_tiles, tiles, counts, pos, order, v, total;
+  int64_t max_tiles;
+  int splits;
+};
+LoraWs lora_ws(int64_t M, int64_t K, int64_t L, int64_t r) {
+  Carver c;
+  LoraWs w = {};
+  if (lora_by_token(M)) return w;
+  w.max_tiles = M / block::kRowTile + std::min(L + 1, M);
+  w.splits = lora::splits_of(M, K, L);
+  w.n_tiles = c.take(4);
+  w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
+  w.counts = c.take(moe::plan_ctas(M) > 1 ? size_t(moe::plan_ctas(M)) * size_t(L + 1) * 4 : 0);
+  w.pos = c.take(size_t(M) * 4);
+  w.order = c.take(size_t(M) * 4);
+  w.v = c.take(size_t(w.splits) * size_t(M) * size_t(lora::padded_rank(r)) * 4);
+  w.total = c.at;
+  return w;
+}
+
 }  // namespace
 
 FP8_API fp8_status fp8_residual_norm(const void* y_bf16, int64_t M, int64_t H, int64_t ldy, const void* post_w_bf16,
@@ -117,4 +153,70 @@ FP8_API fp8_status fp8_residual_norm_quantize(const void* y_bf16, int64_t M, int
   int sms = 0;
   FP8_TRY(current_device(&sms));
   return launch_norm_any(p, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+FP8_API size_t fp8_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
+  if (!lora_sizes_ok(M, K, N, L, r) || M == 0 || K == 0 || N == 0 || L == 0) return 0;
+  return lora_ws(M, K, L, r).total;
+}
+
+FP8_API fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_t ldy, const void* x_bf16, int64_t K,
+                                int64_t ldx, const void* a_bf16, const void* b_bf16, int64_t L, int64_t r,
+                                const int32_t* ids, const float* scales, void* out_bf16, int64_t ldo, void* ws,
+                                size_t ws_bytes, fp8_stream_t stream) {
+  if (!lora_sizes_ok(M, K, N, L, r)) return FP8_ERR_INVALID_ARG;
+  FP8_TRY(check_bf16_mat(y_bf16, M, N, ldy));
+  FP8_TRY(check_bf16_mat(x_bf16, M, K, ldx));
+  FP8_TRY(check_bf16_mat(out_bf16, M, N, ldo));
+  if (!aligned(a_bf16, 2) || !aligned(b_bf16, 2) || !aligned(ids, 4) || !aligned(scales, 4)) return FP8_ERR_MISALIGNED;
+  if (M == 0 || N == 0) return FP8_OK;
+  if (out_bf16 == y_bf16 && M > 1 && ldo != ldy) return FP8_ERR_INVALID_ARG;
+  const bool none = K == 0 || L == 0;
+  if (!none && (a_bf16 == nullptr || b_bf16 == nullptr || ids == nullptr)) return FP8_ERR_INVALID_ARG;
+  FP8_TRY(check_ws(ws, ws_bytes, fp8_lora_workspace_bytes(M, K, N, L, r)));
+  int sms = 0;
+  FP8_TRY(current_device(&sms));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (none) {  // every product is empty
+    if (out_bf16 == y_bf16) return FP8_OK;
+    return report_cuda(cudaMemcpy2DAsync(out_bf16, size_t(ldo) * 2, y_bf16, size_t(ldy) * 2, size_t(N) * 2, size_t(M),
+                                         cudaMemcpyDeviceToDevice, st),
+                       "lora copy") == cudaSuccess
+               ? FP8_OK
+               : FP8_ERR_CUDA;
+  }
+  lora::Args p = {};
+  p.y = static_cast<const uint16_t*>(y_bf16);
+  p.M = M;
+  p.N = N;
+  p.ldy = ldy;
+  p.x = static_cast<const uint16_t*>(x_bf16);
+  p.K = K;
+  p.ldx = ldx;
+  p.a = static_cast<const uint16_t*>(a_bf16);
+  p.b = static_cast<const uint16_t*>(b_bf16);
+  p.adapters = int(L);
+  p.rank = int(r);
+  p.ids = ids;
+  p.scales = scales;
+  p.out = static_cast<uint16_t*>(out_bf16);
+  p.ldo = ldo;
+  if (lora_by_token(M)) return lora::launch_tokens(p, sms, st) ? FP8_OK : FP8_ERR_CUDA;
+  const LoraWs w = lora_ws(M, K, L, r);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  lora::Sorted s = {};
+  block::RowTile* tiles = reinterpret_cast<block::RowTile*>(base + w.tiles);
+  int* n_tiles = reinterpret_cast<int*>(base + w.n_tiles);
+  int* order = reinterpret_cast<int*>(base + w.order);
+  // rows sorted by adapter, those without one last, as adapter L
+  FP8_TRY(moe::launch_plan({ids, M, int(L) + 1, int(L), reinterpret_cast<int*>(base + w.counts),
+                            reinterpret_cast<int*>(base + w.pos), order, tiles, n_tiles, nullptr},
+                           st));
+  s.tiles = tiles;
+  s.n_tiles = n_tiles;
+  s.max_tiles = w.max_tiles;
+  s.order = order;
+  s.v = reinterpret_cast<float*>(base + w.v);
+  s.splits = w.splits;
+  return lora::launch_sorted(p, s, sms, st) ? FP8_OK : FP8_ERR_CUDA;
 }

@@ -1,0 +1,601 @@
+// Low-rank adapters of many requests beside a projection they share, for sm_103a:
+//
+//   out[m] = bf16( y[m] + s[e] * B[e] (A[e] x[m]) ),  e = ids[m]; rows without an adapter are copied.
+//
+// Two forms. Few tokens (tokens_kernel): a cluster of CTAs a token, one launch; the adapter's
+// matrices are read once a token, by wide loads. Many tokens (shrink_kernel, expand_kernel): rows are
+// sorted by adapter and tiles of up to 128 of them pass the tensor cores, first v = A x over all of K, then
+// y + s B v, whose time is the stream of y. v is fp32 between the two; the tensor core takes it as the sum of two bf16
+// numbers (16 bits of its fraction), against B's exact bf16 values.
+//
+// Every wait is bounded; on expiry the kernel records an error, leaves its loop and stores nothing more.
+
+#include "lora.h"
+
+#include <algorithm>
+
+#include "api_common.h"
+#include "device_cache.h"
+#include "device_common.cuh"
+#include "tcgen05.cuh"
+
+namespace fp8k {
+namespace lora {
+
+__device__ unsigned int g_lora_error;
+
+// ---------------------------------------------------------------------------
+// few tokens: a cluster a token
+// ---------------------------------------------------------------------------
+
+constexpr int kCluster = 8;
+constexpr int kTokenThreads = 256;
+constexpr int kTokenWarps = kTokenThreads / 32;
+
+struct TokenParams {
+  Args a;
+  int vec_x, vec_a, vec_b;  // rows start on 16-byte boundaries
+  int k_slice;              // of a CTA of the cluster, a multiple of 8
+  int n_slice;              // columns of a CTA
+};
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
+}
+
+__device__ __forceinline__ float dot8(uint4 v, const float (&f)[8], float sum) {
+  float g[8];
+  unpack8(v, g);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum = fmaf(g[i], f[i], sum);
+  return sum;
+}
+
+// Sums of kValues values over the kLanes lanes (a power of two) that share them: each halving step exchanges half of the
+// values, so that a lane ends with one of them, whose index is returned; past that all lanes add.
+template <int kLanes, int kValues>
+__device__ __forceinline__ int sum_halving(float (&p)[kValues], int lane) {
+  int mine = 0;
+  int left = kValues;
+#pragma unroll
+  for (int m = kLanes / 2; m > 0; m >>= 1) {
+    if (left > 1) {
+      left >>= 1;
+      const bool upper = (lane & m) != 0;
+#pragma unroll
+      for (int i = 0; i < kValues / 2; ++i) {
+        if (i < left) {
+          const float send = upper ? p[i] : p[i + left];
+          const float keep = upper ? p[i + left] : p[i];
+          p[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+        }
+      }
+      if (upper) mine += left;
+    } else {
+      p[0] += __shfl_xor_sync(0xffffffffu, p[0], m);
+    }
+  }
+  return mine;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// kLpr lanes share a row of B (eight values of the rank each). Cluster rank c sums K slice c of v = A x
+// and sends it to all of the cluster; then every CTA adds the slices in order and computes its columns.
+template <int kLpr>
+__global__ void __launch_bounds__(kTokenThreads)
+tokens_kernel(const __grid_constant__ TokenParams p) {
+  constexpr int kU = kLpr < 8 ? kLpr : 8;      // loads of a batch; a lane ends with one column of it
+  constexpr int kBatches = 8 / kU;             // batches in flight: eight loads a lane
+  constexpr int kRowsPerLoad = 32 / kLpr;
+  constexpr int kBatchCols = kU * kRowsPerLoad;
+  constexpr int kStepCols = kBatches * kBatchCols;  // of a warp
+  __shared__ float part[kCluster][kMaxRank];
+  __shared__ float v[kMaxRank];
+  pdl_trigger();
+  pdl_wait();
+  cluster_arrive();  // waited for before the first store into another CTA: by then it runs
+  const Args& g = p.a;
+  const int64_t m = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(cluster_rank());
+  const int N = int(g.N), K = int(g.K), r = g.rank;
+  const int n0 = min(N, int(blockIdx.x) * p.n_slice), n1 = min(N, n0 + p.n_slice);
+  const int e = g.ids[m];
+  const uint16_t* y = g.y + m * g.ldy;
+  uint16_t* out = g.out + m * g.ldo;
+  if (e < 0 || e >= g.adapters) {  // (the whole cluster)
+    if (out != y)
+      for (int n = n0 + threadIdx.x; n < n1; n += kTokenThreads) out[n] = y[n];
+    cluster_wait();
+    return;
+  }
+  const uint16_t* A = g.a + int64_t(e) * r * K;
+  const uint16_t* B = g.b + int64_t(e) * N * r;
+  const int sub = lane % kLpr, row_in_load = lane / kLpr;
+  // the first loads of B are under way while v is summed
+  uint4 bv[8];
+  auto load_b = [&](int base) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int n = base + (q / kU) * kBatchCols + (q % kU) * kRowsPerLoad + row_in_load;
+      bv[q] = make_uint4(0, 0, 0, 0);
+      if (n < n1 && sub * 8 < r) bv[q] = load8_bf16(B + int64_t(n) * r, sub * 8, r, p.vec_b);
+    }
+  };
+  load_b(n0 + warp * kStepCols);
+
+  const int k0 = min(K, rank * p.k_slice), k1 = min(K, k0 + p.k_slice);
+  const uint16_t* x = g.x + m * g.ldx;
+  cluster_wait();
+  for (int i0 = warp * 8; i0 < r; i0 += kTokenWarps * 8) {
+    float acc[8] = {};
+    for (int k = k0 + lane * 8; k < k1; k += 256) {
+      float f[8];
+      unpack8(load8_bf16(x, k, k1, p.vec_x), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i0 + i < r) acc[i] = dot8(load8_bf16(A + int64_t(i0 + i) * K, k, k1, p.vec_a), f, acc[i]);
+    }
+    const int i = i0 + sum_halving<32, 8>(acc, lane);
+    // four lanes hold the sum: each sends it to two of the cluster's CTAs
+    const uint32_t at = smem_u32(&part[rank][i]);
+#pragma unroll
+    for (int c = 0; c < kCluster; c += 4) st_cluster_u32(map_to_rank(at, c + (lane & 3)), __float_as_uint(acc[0]));
+  }
+  pair_sync();
+  for (int i = threadIdx.x; i < kMaxRank; i += kTokenThreads) {
+    float s = 0.0f;
+    if (i < r)
+      for (int c = 0; c < kCluster; ++c) s += part[c][i];
+    v[i] = s;
+  }
+  __syncthreads();
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = v[sub * 8 + j];
+  const float scale = g.scales ? g.scales[e] : 1.0f;
+  for (int base = n0 + warp * kStepCols; base < n1; base += kTokenWarps * kStepCols) {
+    float sum[kBatches][kU];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum[q / kU][q % kU] = dot8(bv[q], f, 0.0f);
+    if (base + kTokenWarps * kStepCols < n1) load_b(base + kTokenWarps * kStepCols);
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b) {
+      const int u = sum_halving<kLpr, kU>(sum[b], lane);
+      const int n = base + b * kBatchCols + u * kRowsPerLoad + row_in_load;
+      if (n < n1 && (sub & (kLpr / kU - 1)) == 0)
+        out[n] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(scale, sum[b][0], bf16_bits_to_float(y[n]))));
+    }
+  }
+}
+
+template <int kLpr>
+bool launch_tokens_of(const TokenParams& p, int groups, cudaStream_t st) {
+  return launch(tokens_kernel<kLpr>, dim3(unsigned(kCluster * groups), unsigned(p.a.M)), dim3(kTokenThreads), 0, st,
+                true, dim3(kCluster, 1, 1), p) == FP8_OK;
+}
+
+bool launch_tokens(const Args& a, int num_sms, cudaStream_t st) {
+  TokenParams p = {};
+  p.a = a;
+  p.vec_x = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0);
+  p.vec_a = aligned(a.a, 16) && a.K % 8 == 0;
+  p.vec_b = aligned(a.b, 16) && a.rank % 8 == 0;
+  p.k_slice = int(((a.K + 7) / 8 + kCluster - 1) / kCluster * 8);
+  const int groups = 1;
+  p.n_slice = int((a.N + kCluster * groups - 1) / (kCluster * groups));
+  if (a.rank <= 8) return launch_tokens_of<1>(p, groups, st);
+  if (a.rank <= 16) return launch_tokens_of<2>(p, groups, st);
+  if (a.rank <= 32) return launch_tokens_of<4>(p, groups, st);
+  if (a.rank <= 64) return launch_tokens_of<8>(p, groups, st);
+  return a.rank <= 128 ? launch_tokens_of<16>(p, groups, st) : launch_tokens_of<32>(p, groups, st);
+}
+
+// ---------------------------------------------------------------------------
+// many tokens: tiles of rows sorted by adapter, on tensor cores
+// ---------------------------------------------------------------------------
+
+constexpr int kTileRows = block::kRowTile;  // 128, the MMA's M
+constexpr int kTileThreads = 256;
+constexpr int kBk = 64;                     // bf16 values of K in a 128-byte swizzled row
+constexpr uint32_t kXBytes = kTileRows * 128;
+constexpr int kShrinkMaxStages = 6;
+
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// D fp32, A and B bf16, both K-major, M = 128.
+__host__ __device__ constexpr uint32_t idesc_of(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(kTileRows >> 4) << 24);
+}
+
+// Byte offset of 16-byte piece c of row r in a tile of 128-byte rows with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(int r, int c) { return uint32_t(r) * 128u + uint32_t((c ^ (r & 7)) << 4); }
+
+// Eight values k .. k + 7 of a row (zeros from K on, and all of them where the row is not live) into shared memory: an
+// asynchronous 16-byte copy where the rows allow it (then K is whole eights).
+__device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* row, bool live, int k, int K, int vec) {
+  live = live && k < K;
+  if (vec) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(dst), "l"(live ? row + k : row), "r"(live ? 16u : 0u) : "memory");
+  } else {
+    const uint4 v = live ? load8_bf16(row, k, K, 0) : make_uint4(0, 0, 0, 0);
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+  }
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kLeft) : "memory"); }
+// What this thread wrote to shared memory becomes visible to the tensor core (after the barrier that follows).
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+struct TileParams {
+  Args a;
+  Sorted s;
+  int rp;                   // rank rounded up to 16
+  int kb, kb_slice;         // blocks of 64 of K, and of one split
+  int stages;
+  int cols_per_cta;         // expand: a multiple of kBn
+  int vec_x, vec_a, vec_b, vec_y;
+  uint32_t tmem_cols;
+};
+
+struct TileCtl {
+  uint64_t done[8];
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__device__ __forceinline__ uint32_t align1024(uint32_t a) { return (a + 1023u) & ~1023u; }
+
+// The start and end that both kernels share: barriers and tensor memory. The trigger for the next kernel comes after the
+// tensor memory is held, so that no CTA of a later kernel can hold it while one of this kernel waits for it.
+__device__ __forceinline__ void tile_begin(TileCtl* ctl, uint32_t cols) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&ctl->done[i]), 1);
+    ctl->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async();
+  }
+  if (threadIdx.x < 32) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(&ctl->tmem_base)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  pdl_trigger();
+  pdl_wait();
+}
+__device__ __forceinline__ void tile_end(TileCtl* ctl, uint32_t cols) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (threadIdx.x < 32)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(ctl->tmem_base), "r"(cols) : "memory");
+}
+
+// v[split][row] = A[e] x[row's token] over the split's K, for a tile's rows.
+__global__ void __launch_bounds__(kTileThreads)
+shrink_kernel(const __grid_constant__ TileParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TileCtl ctl;
+  const uint32_t base = align1024(smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tile_begin(&ctl, p.tmem_cols);
+  const int tile = blockIdx.x;
+  const Args& g = p.a;
+  const int K = int(g.K), r = g.rank;
+  if (tile < *p.s.n_tiles) {
+    const block::RowTile t = p.s.tiles[tile];
+    const int kb0 = int(blockIdx.y) * p.kb_slice, steps = min(p.kb, kb0 + p.kb_slice) - kb0;
+    if (t.expert < g.adapters && steps > 0) {
+      const int rows = min(kTileRows, t.row_end - t.row0);
+      const uint32_t stage_bytes = kXBytes + uint32_t(p.rp) * 128u;
+      // eight threads a row; this thread's rows of x
+      const int piece = threadIdx.x & 7, first = threadIdx.x >> 3;
+      const uint16_t* x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = first + 32 * i;
+        x[i] = row < rows ? g.x + int64_t(p.s.order[t.row0 + row]) * g.ldx : g.x;
+      }
+      const uint16_t* A = g.a + int64_t(t.expert) * r * K;
+      auto fill = [&](int step) {
+        const uint32_t st = base + uint32_t(step % p.stages) * stage_bytes;
+        const int k = (kb0 + step) * kBk + piece * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          copy8(st + swizzled(first + 32 * i, piece), x[i], first + 32 * i < rows, k, K, p.vec_x);
+        for (int row = first; row < p.rp; row += 32)
+          copy8(st + kXBytes + swizzled(row, piece), A + int64_t(min(row, r - 1)) * K, row < r, k, K, p.vec_a);
+      };
+      auto wait = [&](int step) {
+        return mbar_wait_short(smem_u32(&ctl.done[step % p.stages]), uint32_t(step / p.stages) & 1u, &ctl.abort_flag,
+                               &g_lora_error);
+      };
+      // stages - 2 steps ahead, so that the MMA whose stage is filled again is not the one just issued
+      const int ahead = p.stages - 2;
+      for (int i = 0; i < ahead; ++i) {
+        if (i < steps) fill(i);
+        cp_commit();
+      }
+      bool ok = true;
+      for (int i = 0; i < steps; ++i) {
+        if (i >= 2) ok = wait(i - 2);
+        if (ok && i + ahead < steps) fill(i + ahead);
+        cp_commit();
+        // the copies of step i have landed
+        if (ahead == 1) cp_wait<1>();
+        else if (ahead == 2) cp_wait<2>();
+        else if (ahead == 3) cp_wait<3>();
+        else cp_wait<4>();
+        fence_async();
+        if (!__syncthreads_and(ok)) break;
+        if (threadIdx.x == 0) {
+          const uint32_t st = base + uint32_t(i % p.stages) * stage_bytes;
+          const uint64_t ad = make_sdesc(st), bd = make_sdesc(st + kXBytes);
+#pragma unroll
+          for (int kk = 0; kk < kBk / 16; ++kk)
+            mma_bf16(ctl.tmem_base, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc_of(p.rp), i != 0 || kk != 0);
+          mma_commit<false>(smem_u32(&ctl.done[i % p.stages]));
+        }
+      }
+      if (ok) ok = wait(steps - 1);
+      if (__syncthreads_and(ok)) {
+        tmem_fence_after();
+        // four warps hold the tile's rows, the other four the second half of the columns
+        const int row = (warp & 3) * 32 + lane;
+        float* dst = p.s.v + (int64_t(blockIdx.y) * g.M + t.row0 + row) * p.rp;
+        const uint32_t from = ctl.tmem_base + (uint32_t((warp & 3) * 32) << 16);
+        for (int c = (warp >> 2) * 32; c < p.rp; c += 64) {
+          uint32_t f[32];
+          tmem_ld32(from + c, f);
+          if (row < rows) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (c + 4 * q < p.rp)
+                *reinterpret_cast<uint4*>(dst + c + 4 * q) = make_uint4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+          }
+        }
+      }
+    }
+  }
+  tile_end(&ctl, p.tmem_cols);
+}
+
+constexpr int kStagePitch = 33;  // floats of a staged row: a warp's writes by row and reads by column both take 32 banks
+
+// out = y + s B[e] v for a tile's rows and the CTA's columns, kBn a step (64 where the rank's
+// operands leave no room for 128): while a step's sums are read, joined with
+// y and stored, the next one's MMAs run and B of the one after that is copied.
+template <int kBn>
+__global__ void __launch_bounds__(kTileThreads)
+expand_kernel(const __grid_constant__ TileParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TileCtl ctl;
+  __shared__ int order[kTileRows];
+  __shared__ float staged[kTileThreads / 32][32 * kStagePitch];
+  const uint32_t base = align1024(smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tile_begin(&ctl, p.tmem_cols);
+  const Args& g = p.a;
+  const int N = int(g.N), r = g.rank;
+  const int tile = blockIdx.x;
+  const int n0 = int(blockIdx.y) * p.cols_per_cta, n1 = min(N, n0 + p.cols_per_cta);
+  const bool mine = tile < *p.s.n_tiles;
+  const block::RowTile t = mine ? p.s.tiles[tile] : block::RowTile{g.adapters, 0, 0, 0};
+  const int rows = min(kTileRows, t.row_end - t.row0);
+  if (mine && threadIdx.x < kTileRows) order[threadIdx.x] = int(threadIdx.x) < rows ? p.s.order[t.row0 + threadIdx.x] : -1;
+  __syncthreads();
+  if (mine && t.expert >= g.adapters) {
+    if (g.out != g.y)
+      for (int row = warp; row < rows; row += kTileThreads / 32)
+        for (int n = n0 + lane; n < n1; n += 32)
+          g.out[int64_t(order[row]) * g.ldo + n] = g.y[int64_t(order[row]) * g.ldy + n];
+  } else if (mine) {
+    const int rk = (p.rp + kBk - 1) / kBk;  // 128-byte rows that the rank fills
+    const uint32_t v_hi = base, v_lo = base + uint32_t(rk) * kXBytes, b_at = v_lo + uint32_t(rk) * kXBytes;
+    const uint32_t b_bytes = uint32_t(rk) * (kBn * 128u);
+    const int steps = (n1 - n0 + kBn - 1) / kBn;
+    const uint16_t* B = g.b + int64_t(t.expert) * N * r;
+    const int pieces = p.rp / 8;
+    auto fill = [&](int step) {
+      const uint32_t to = b_at + uint32_t(step & 1) * b_bytes;
+      for (int i = threadIdx.x; i < kBn * pieces; i += kTileThreads) {
+        const int row = i / pieces, c = i - row * pieces;
+        const int n = n0 + step * kBn + row;
+        copy8(to + uint32_t(c >> 3) * (kBn * 128u) + swizzled(row, c & 7), B + int64_t(min(n, N - 1)) * r, n < N, c * 8, r,
+              p.vec_b);
+      }
+    };
+    fill(0);
+    cp_commit();
+    // v, the sum of the splits in order, as two bf16 numbers
+    for (int i = threadIdx.x; i < kTileRows * pieces; i += kTileThreads) {
+      const int row = i / pieces, c = i - row * pieces;
+      float f[8] = {};
+      if (row < rows) {
+        const float* from = p.s.v + int64_t(t.row0 + row) * p.rp + c * 8;
+        for (int s = 0; s < p.s.splits; ++s, from += g.M * p.rp) {
+          const float4 lo = *reinterpret_cast<const float4*>(from), hi = *reinterpret_cast<const float4*>(from + 4);
+          f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
+          f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
+        }
+      }
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+        const float h0 = bf16_lo(h[j]), h1 = bf16_hi(h[j]);
+        // (an infinity has no second part)
+        l[j] = pack_bf16x2(fabsf(h0) <= 3.39e38f ? f[2 * j] - h0 : 0.0f, fabsf(h1) <= 3.39e38f ? f[2 * j + 1] - h1 : 0.0f);
+      }
+      const uint32_t at = uint32_t(c >> 3) * kXBytes + swizzled(row, c & 7);
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v_hi + at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v_lo + at), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3]) : "memory");
+    }
+    auto multiply = [&](int step) {
+      const uint32_t b = b_at + uint32_t(step & 1) * b_bytes, d = ctl.tmem_base + uint32_t(step & 1) * kBn;
+      for (int part = 0; part < 2; ++part)
+        for (int k16 = 0; k16 < p.rp / 16; ++k16) {
+          const uint64_t ad = make_sdesc((part ? v_lo : v_hi) + uint32_t(k16 >> 2) * kXBytes) + uint64_t((k16 & 3) * 2);
+          const uint64_t bd = make_sdesc(b + uint32_t(k16 >> 2) * (kBn * 128u)) + uint64_t((k16 & 3) * 2);
+          mma_bf16(d, ad, bd, idesc_of(kBn), part != 0 || k16 != 0);
+        }
+      mma_commit<false>(smem_u32(&ctl.done[step & 1]));
+    };
+    cp_wait<0>();
+    fence_async();
+    __syncthreads();
+    if (threadIdx.x == 0) multiply(0);
+    if (steps > 1) fill(1);
+    cp_commit();
+    const float scale = g.scales ? g.scales[t.expert] : 1.0f;
+    const int quarter = warp & 3, half = warp >> 2;
+    float* mine32 = staged[warp];
+    // lane: row lane / 4 of each eight, columns (lane % 4) * 8 of each 32
+    const int c8 = (lane & 3) * 8, r8 = lane >> 2;
+    for (int step = 0; step < steps; ++step) {
+      const int col = n0 + step * kBn + half * (kBn / 2);
+      uint4 yv[kBn / 64][4];
+#pragma unroll
+      for (int h = 0; h < kBn / 64; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int token = order[quarter * 32 + i * 8 + r8], n = col + h * 32 + c8;
+          yv[h][i] = make_uint4(0, 0, 0, 0);
+          if (token >= 0 && n < N) yv[h][i] = load8_bf16(g.y + int64_t(token) * g.ldy, n, N, p.vec_y);
+        }
+      bool ok = mbar_wait_short(smem_u32(&ctl.done[step & 1]), uint32_t(step >> 1) & 1u, &ctl.abort_flag, &g_lora_error);
+      // B of the next step has landed; the sums of the step before this one have been read by all warps
+      cp_wait<0>();
+      fence_async();
+      tmem_fence_before();
+      if (!__syncthreads_and(ok)) break;
+      tmem_fence_after();
+      if (threadIdx.x == 0 && step + 1 < steps) multiply(step + 1);
+      if (step + 2 < steps) fill(step + 2);
+      cp_commit();
+#pragma unroll
+      for (int h = 0; h < kBn / 64; ++h) {
+        uint32_t f[32];
+        tmem_ld32(ctl.tmem_base + uint32_t(step & 1) * kBn + (uint32_t(quarter * 32) << 16) + half * (kBn / 2) + h * 32, f);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mine32[lane * kStagePitch + j] = __uint_as_float(f[j]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = i * 8 + r8, token = order[quarter * 32 + row], n = col + h * 32 + c8;
+          float o[8];
+          unpack8(yv[h][i], o);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = fmaf(scale, mine32[row * kStagePitch + c8 + j], o[j]);
+          if (token >= 0 && n < N) {
+            uint16_t* dst = g.out + int64_t(token) * g.ldo + n;
+            if (p.vec_y && n + 8 <= N) {
+              *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                                                          pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (n + j < N) dst[j] = __bfloat16_as_ushort(__float2bfloat16_rn(o[j]));
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tile_end(&ctl, p.tmem_cols);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+namespace {
+PerDeviceCache<const void*, int> g_smem_cache;
+
+bool allow_smem(const void* kfn) {
+  int dev = 0, set = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  return g_smem_cache.get(dev, kfn, &set, [&](int* v) {
+    *v = 1;
+    cudaFuncAttributes at = {};
+    return report_cuda(cudaFuncGetAttributes(&at, kfn), "lora attributes") == cudaSuccess &&
+           report_cuda(cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            232448 - int(at.sharedSizeBytes)),
+                       "lora smem attribute") == cudaSuccess;
+  });
+}
+}  // namespace
+
+// K splits of the shrink: CTAs enough for the SMs, each with at least four blocks of K.
+int splits_of(int64_t M, int64_t K, int64_t adapters) {
+  const int64_t tiles = (M + kTileRows - 1) / kTileRows + std::min(M, adapters) / 2;
+  const int64_t kb = (K + kBk - 1) / kBk;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kb / 4, (2 * 152 + tiles - 1) / tiles));
+  const int64_t slice = (kb + want - 1) / want;
+  return int(std::max<int64_t>(1, (kb + slice - 1) / std::max<int64_t>(slice, 1)));
+}
+
+template <int kBn>
+bool launch_expand(TileParams p, int num_sms, cudaStream_t st) {
+  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn>))) return false;
+  const int rk = (p.rp + kBk - 1) / kBk;
+  const size_t smem = 1024 + size_t(rk) * (2 * kXBytes + 2 * kBn * 128);
+  // columns of a CTA: CTAs for two on every SM, as far as there are columns
+  const int64_t steps = (p.a.N + kBn - 1) / kBn;
+  const int64_t tiles = (p.a.M + kTileRows - 1) / kTileRows + std::min<int64_t>(p.a.M, p.a.adapters) / 2;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(steps, (4 * num_sms + tiles - 1) / tiles));
+  p.cols_per_cta = int((steps + want - 1) / want) * kBn;
+  p.tmem_cols = 2 * kBn;
+  return launch(expand_kernel<kBn>, dim3(unsigned(p.s.max_tiles), unsigned((p.a.N + p.cols_per_cta - 1) / p.cols_per_cta)),
+                dim3(kTileThreads), smem, st, true, dim3(1, 1, 1), p) == FP8_OK;
+}
+
+bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st) {
+  TileParams p = {};
+  p.a = a;
+  p.s = s;
+  p.rp = padded_rank(a.rank);
+  p.kb = int((a.K + kBk - 1) / kBk);
+  p.kb_slice = (p.kb + s.splits - 1) / s.splits;
+  p.vec_x = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0) && a.K % 8 == 0;
+  p.vec_a = aligned(a.a, 16) && a.K % 8 == 0;
+  p.vec_b = aligned(a.b, 16) && a.rank % 8 == 0;
+  p.vec_y = aligned(a.y, 16) && aligned(a.out, 16) && (a.M <= 1 || (a.ldy % 8 == 0 && a.ldo % 8 == 0));
+  if (!allow_smem(reinterpret_cast<const void*>(shrink_kernel))) return false;
+  const int stage_bytes = int(kXBytes) + p.rp * 128;
+  p.stages = std::max(3, std::min(kShrinkMaxStages, 108 * 1024 / stage_bytes));
+  p.tmem_cols = 32;
+  while (int(p.tmem_cols) < p.rp) p.tmem_cols *= 2;
+  if (launch(shrink_kernel, dim3(unsigned(s.max_tiles), unsigned(s.splits)), dim3(kTileThreads),
+             size_t(p.stages) * stage_bytes + 1024, st, true, dim3(1, 1, 1), p) != FP8_OK)
+    return false;
+  return p.rp <= 2 * kBk ? launch_expand<128>(p, num_sms, st) : launch_expand<64>(p, num_sms, st);
+}
+
+unsigned int read_and_clear_error() {
+  unsigned int v = 0;
+  const unsigned int zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_lora_error, sizeof(v)) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_lora_error, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace lora
+}  // namespace fp8k

@@ -6,6 +6,7 @@
 
 #include "block_gemm.h"
 #include "device_common.cuh"
+#include "moe_plan.h"
 #include "tcgen05.cuh"
 
 namespace fp8k {
@@ -301,34 +302,38 @@ __device__ __forceinline__ void plan_range(int64_t pairs, int part, int parts, i
   end = min(pairs, begin + share);
 }
 
+// The expert that an id stands for, -1 for none.
+__device__ __forceinline__ int expert_of(int id, const Plan& p) { return id >= 0 && id < p.experts ? id : p.spare; }
+
 // counts[cta][expert] of the CTA's pairs, for a plan of several CTAs.
 __global__ void __launch_bounds__(kPlanThreads, 1)
-plan_count_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, int* __restrict__ counts) {
+plan_count_kernel(const __grid_constant__ Plan p) {
+  const int experts = p.experts;
   __shared__ int count[kMaxExperts];
   pdl_trigger();
   pdl_wait();
   for (int i = threadIdx.x; i < experts; i += kPlanThreads) count[i] = 0;
   __syncthreads();
   int64_t begin, end;
-  plan_range(pairs, blockIdx.x, gridDim.x, begin, end);
+  plan_range(p.pairs, blockIdx.x, gridDim.x, begin, end);
   for (int64_t i = begin + threadIdx.x; i < end; i += kPlanThreads) {
-    const int id = ids[i];
-    if (id >= 0 && id < experts) atomicAdd(&count[id], 1);  // sums of ones: any order
+    const int id = expert_of(p.ids[i], p);
+    if (id >= 0) atomicAdd(&count[id], 1);  // sums of ones: any order
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < experts; i += kPlanThreads) counts[blockIdx.x * experts + i] = count[i];
+  for (int i = threadIdx.x; i < experts; i += kPlanThreads) p.counts[blockIdx.x * experts + i] = count[i];
 }
 
 // Order of the routed pairs: pair i (= token * k + j) with expert ids[i] in [0, experts) gets row
 // pos[i], rows sorted by expert and, within one, by pair (stable, so nothing depends on timing);
-// any other id gives -1. Then the row tiles and the experts' first rows (each where its pointer is not null). A CTA's warps count their contiguous shares of the CTA's pairs by expert in
+// any other id gives -1, or counts as expert `spare`. Then the row tiles and the experts' first rows (where wanted). A CTA's warps count their contiguous shares of the CTA's pairs by expert in
 // shared memory (equal ids of a step are found by a warp match), the counts are scanned over warps,
 // CTAs (from plan_count_kernel; one CTA needs none) and experts, and a second walk hands out rows.
 // One CTA sorts 65536 pairs in 109 us, 64 CTAs in 11 us.
 __global__ void __launch_bounds__(kPlanThreads, 1)
-plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, const int* __restrict__ counts,
-            int* __restrict__ pos, block::RowTile* __restrict__ tiles, int* __restrict__ n_tiles,
-            int* __restrict__ offsets) {
+plan_kernel(const __grid_constant__ Plan p, int has_counts) {
+  const int experts = p.experts;
+  const int* counts = has_counts ? p.counts : nullptr;
   extern __shared__ int count[];  // [kPlanWarps][experts], then [experts] first rows
   int* total = count + kPlanWarps * experts;
   __shared__ int warp_sum[2][kPlanWarps];
@@ -338,14 +343,14 @@ plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, const i
   for (int i = threadIdx.x; i < kPlanWarps * experts; i += kPlanThreads) count[i] = 0;
   __syncthreads();
   int64_t cta_begin, cta_end, begin, end;
-  plan_range(pairs, blockIdx.x, gridDim.x, cta_begin, cta_end);
+  plan_range(p.pairs, blockIdx.x, gridDim.x, cta_begin, cta_end);
   plan_range(cta_end - cta_begin, warp, kPlanWarps, begin, end);
   begin += cta_begin, end += cta_begin;
   int* mine = count + warp * experts;
   for (int64_t i = begin; i < end; i += 32) {
-    const int id = i + lane < end ? ids[i + lane] : -1;
-    const bool in = id >= 0 && id < experts;
-    const uint32_t same = __match_any_sync(0xffffffffu, in ? id : -1);
+    const int id = i + lane < end ? expert_of(p.ids[i + lane], p) : -1;
+    const bool in = id >= 0;
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
     if (in && lane == __ffs(same) - 1) mine[id] += __popc(same);
     __syncwarp();
   }
@@ -388,27 +393,28 @@ plan_kernel(const int32_t* __restrict__ ids, int64_t pairs, int experts, const i
   if (int(threadIdx.x) < experts) {
     total[threadIdx.x] = rows_before;
     // the CTAs share out an expert's tiles
-    for (int j = blockIdx.x; tiles != nullptr && j < my_tiles; j += gridDim.x) {
+    for (int j = blockIdx.x; p.tiles != nullptr && j < my_tiles; j += gridDim.x) {
       const int r0 = rows_before + j * block::kRowTile;
-      tiles[tiles_before + j] = block::RowTile{int(threadIdx.x), r0, rows_before + tot, 0};
+      p.tiles[tiles_before + j] = block::RowTile{int(threadIdx.x), r0, rows_before + tot, 0};
     }
-    if (offsets != nullptr && blockIdx.x == 0) {
-      offsets[threadIdx.x] = rows_before;
-      if (int(threadIdx.x) == experts - 1) offsets[experts] = rows_before + tot;
+    if (p.offsets != nullptr && blockIdx.x == 0) {
+      p.offsets[threadIdx.x] = rows_before;
+      if (int(threadIdx.x) == experts - 1) p.offsets[experts] = rows_before + tot;
     }
   }
-  if (n_tiles != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *n_tiles = all_t;
+  if (p.n_tiles != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.n_tiles = all_t;
   __syncthreads();
   for (int64_t i = begin; i < end; i += 32) {
-    const int id = i + lane < end ? ids[i + lane] : -1;
-    const bool in = id >= 0 && id < experts;
-    const uint32_t same = __match_any_sync(0xffffffffu, in ? id : -1);
+    const int id = i + lane < end ? expert_of(p.ids[i + lane], p) : -1;
+    const bool in = id >= 0;
+    const uint32_t same = __match_any_sync(0xffffffffu, id);
     int d = -1;
     if (in) d = total[id] + mine[id] + __popc(same & ((1u << lane) - 1));
     __syncwarp();
     if (in && lane == __ffs(same) - 1) mine[id] += __popc(same);
     __syncwarp();
-    if (i + lane < end) pos[i + lane] = d;
+    if (i + lane < end) p.pos[i + lane] = d;
+    if (d >= 0 && p.order != nullptr) p.order[d] = int(i) + lane;
   }
 }
 

@@ -436,6 +436,29 @@ fp8_status fp8_moe_dispatch_grad(const void* dxs, int f32, int64_t R, int64_t H,
 
 /*
  * ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a projection they share. For each
+ * token m with e = ids[m] in [0, L):
+ *   out[m] = bf16( y[m] + scales[e] * B[e] (A[e] x[m]) )
+ * and out[m] = y[m] for any other id. y bf16 [M, N] is the output of a linear
+ * of x bf16 [M, K] (any of the linears here), A bf16 [L][r, K], B bf16
+ * [L][N, r], without gaps; ids int32 [M], scales fp32 [L] (NULL: ones). Sums and
+ * A x are fp32 (for B's product A x is the sum of two bf16 numbers, off by 2^-16);
+ * the only rounding to bf16 is that of out. Results do not depend
+ * on timing. A NaN or an infinity stays with the tokens of its row or
+ * adapter. out may be y (with the same stride), else may not overlap it. A
+ * and B are weights to the launch ordering above. ws: >=
+ * fp8_lora_workspace_bytes, 256-byte aligned. Limits: r 1 to 256, L <= 511, K
+ * and N <= 2^30 (FP8_ERR_INVALID_ARG).
+ * ---------------------------------------------------------------------------
+ */
+size_t fp8_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r);
+fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_t ldy, const void* x_bf16, int64_t K,
+                        int64_t ldx, const void* a_bf16, const void* b_bf16, int64_t L, int64_t r, const int32_t* ids,
+                        const float* scales, void* out_bf16, int64_t ldo, void* ws, size_t ws_bytes,
+                        fp8_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
  * Norms before and after a block, with its gate and residual.
  * ---------------------------------------------------------------------------
  */

@@ -98,3 +98,26 @@ def combine_grad(dy: np.ndarray, ys: np.ndarray, pos: np.ndarray, weights: np.nd
                 terms = dy[t].astype(np.float64) * ys[d].astype(np.float64)
                 dw[t, j], mag[t, j] = terms.sum(), np.abs(terms).sum()
     return dys, dw, (-(-H // 32) + 14) * U * mag + TINY
+
+
+def lora(y, x, a, b, ids, scales=None) -> Tuple[np.ndarray, np.ndarray]:
+    """(out, bound) before the rounding to bf16. Sums of K and of 2 r products in fp32 in any order, 2**-23 a step (a
+    tensor core may cut instead of round); v as two bf16 numbers is off by 2**-8 of what 2**-8 of it left; one fma."""
+    M, K = x.shape
+    L, r, _ = a.shape
+    out = y.astype(np.float64)
+    err = np.zeros_like(out)
+    for e in range(L):
+        t = np.nonzero(ids == e)[0]
+        if not t.size:
+            continue
+        A, Bm, X = (v.astype(np.float64) for v in (a[e], b[e], x[t]))
+        s = 1.0 if scales is None else float(scales[e])
+        v = X @ A.T
+        dv = (K + 16) * 2 * U * (np.abs(X) @ np.abs(A).T) + TINY
+        d = v @ Bm.T
+        dd = (dv + np.abs(v) * HALF_BF16 ** 2) @ np.abs(Bm).T + (2 * r + 8) * 2 * U * ((np.abs(v) + dv) @ np.abs(Bm).T)
+        out[t] += s * d
+        err[t] = abs(s) * dd
+        err[t] += (np.abs(out[t]) + err[t]) * U + TINY
+    return out, err
