@@ -257,6 +257,21 @@ fp8_status launch_rows_out(const void* x, int64_t row_bytes, int64_t ldx_bytes, 
                 ldxs_bytes / int64_t(sizeof(U)));
 }
 
+bool few_pairs(int64_t T, int64_t k) { return T * k <= moe::kFewPairs; }
+
+template <typename U>
+fp8_status launch_few_rows_out(const void* x, int64_t row_bytes, int64_t ldx_bytes, int64_t T, const int32_t* ids,
+                               int64_t k, int64_t E, int* pos, int* offsets, void* xs, int64_t ldxs_bytes,
+                               cudaStream_t st) {
+  const int64_t pieces = row_bytes / int64_t(sizeof(U));
+  // (at least one CTA: the experts' first rows)
+  const dim3 grid(unsigned(std::max<int64_t>(T, 1)),
+                  unsigned(std::max<int64_t>(1, (pieces + moe::kRowThreads - 1) / moe::kRowThreads)));
+  return launch(moe::few_rows_out_kernel<U>, grid, dim3(moe::kRowThreads), 0, st, true, dim3(1, 1, 1),
+                static_cast<const U*>(x), ldx_bytes / int64_t(sizeof(U)), pieces, ids, int(T * k), int(k), int(E), pos,
+                offsets, static_cast<U*>(xs), ldxs_bytes / int64_t(sizeof(U)));
+}
+
 template <typename T, int kN>
 fp8_status launch_rows_back(const void* ys, int64_t ldys, int64_t R, const int* pos, const float* weights, int64_t k,
                             int64_t tokens, int64_t H, void* y, int64_t ldy, int sms, cudaStream_t st) {
@@ -577,7 +592,7 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
 FP8_API size_t fp8_moe_dispatch_workspace_bytes(int64_t T, int64_t k, int64_t E) {
   if (!pair_sizes_ok(T, k) || E < 1 || E > moe::kMaxExperts) return 0;
   const int ctas = moe::plan_ctas(T * k);
-  return ctas > 1 ? round_up_256(size_t(ctas) * size_t(E) * 4) : 0;
+  return ctas > 1 && !few_pairs(T, k) ? round_up_256(size_t(ctas) * size_t(E) * 4) : 0;
 }
 
 FP8_API fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,
@@ -592,12 +607,21 @@ FP8_API fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H
   int sms = 0;
   FP8_TRY(current_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  FP8_TRY(moe::launch_plan({ids, T * k, int(E), -1, static_cast<int*>(ws), pos, nullptr, nullptr, nullptr, offsets}, st));
-  if (T == 0 || H == 0) return FP8_OK;
   const int size = f32 ? 4 : 2;
   // the widest pieces that every row of both consists of
   const int64_t any = int64_t(reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(xs)) | H * size |
                       (T > 1 ? ldx * size : 0) | (T * k > 1 ? ldxs * size : 0);
+  if (few_pairs(T, k)) {
+    auto go = [&](auto piece) {
+      return launch_few_rows_out<decltype(piece)>(x, H * size, ldx * size, T, ids, k, E, pos, offsets, xs, ldxs * size,
+                                                  st);
+    };
+    if (any % 16 == 0) return go(uint4{});
+    if (any % 8 == 0) return go(uint2{});
+    return any % 4 == 0 ? go(uint32_t{}) : go(uint16_t{});
+  }
+  FP8_TRY(moe::launch_plan({ids, T * k, int(E), -1, static_cast<int*>(ws), pos, nullptr, nullptr, nullptr, offsets}, st));
+  if (H == 0) return FP8_OK;
   auto go = [&](auto piece) {
     return launch_rows_out<decltype(piece)>(x, H * size, ldx * size, T, pos, k, T * k, xs, ldxs * size, sms, st);
   };

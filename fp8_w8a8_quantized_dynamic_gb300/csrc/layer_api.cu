@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "api_common.h"
+#include "device_cache.h"
 #include "lora.h"
 #include "moe_plan.h"
 #include "norm.cuh"
@@ -19,12 +20,30 @@ fp8_status check_row_vector(const void* p) { return aligned(p, 2) ? FP8_OK : FP8
 
 int rows_vec(const void* p, int64_t rows, int64_t ld) { return aligned(p, 16) && (rows <= 1 || ld % 8 == 0); }
 
+PerDeviceCache<const void*, int> g_norm_ctas;
+
+template <int kThreads, int kUnits, bool kPost, bool kGate>
+fp8_status launch_norm_of(const norm::Params& p, int sms, cudaStream_t st) {
+  auto kernel = norm::residual_norm_kernel<kThreads, kUnits, kPost, kGate>;
+  int dev = 0, per_sm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
+  if (p.rows > sms &&  // (fewer: one CTA each)
+      !g_norm_ctas.get(dev, reinterpret_cast<const void*>(kernel), &per_sm, [&](int* v) {
+        return report_cuda(cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kernel, kThreads, 0), "norm occupancy") ==
+                   cudaSuccess &&
+               *v > 0;
+      }))
+    return FP8_ERR_CUDA;
+  const int64_t grid = std::min<int64_t>(p.rows, int64_t(sms) * std::max(per_sm, 1));
+  return launch(kernel, dim3(unsigned(grid)), dim3(kThreads), 0, st, true, dim3(1, 1, 1), p);
+}
 template <int kThreads, int kUnits>
 fp8_status launch_norm(const norm::Params& p, int sms, cudaStream_t st) {
-  const int per_sm = 2048 / kThreads;
-  const int64_t grid = std::min<int64_t>(p.rows, int64_t(sms) * per_sm);
-  return launch(norm::residual_norm_kernel<kThreads, kUnits>, dim3(unsigned(grid)), dim3(kThreads), 0, st, true,
-                dim3(1, 1, 1), p);
+  if (p.post_w)
+    return p.gate ? launch_norm_of<kThreads, kUnits, true, true>(p, sms, st)
+                  : launch_norm_of<kThreads, kUnits, true, false>(p, sms, st);
+  return p.gate ? launch_norm_of<kThreads, kUnits, false, true>(p, sms, st)
+                : launch_norm_of<kThreads, kUnits, false, false>(p, sms, st);
 }
 
 // Threads of a row.

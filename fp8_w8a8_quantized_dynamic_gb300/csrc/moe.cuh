@@ -488,27 +488,87 @@ rows_out_kernel(const U* __restrict__ x, int64_t ldx, int64_t tokens, int64_t pi
   }
 }
 
-// kN columns of a row as fp32.
-template <int kN>
-__device__ __forceinline__ void load_cols(const float* p, float (&f)[kN]) {
-  if constexpr (kN == 4) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p));
-    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-  } else {
-    f[0] = __ldcs(p);
+constexpr int kFewPairs = 1024;  // that every CTA of few_rows_out_kernel looks at by itself
+
+// The same with the sort, for few pairs: a CTA a token and kRowThreads pieces of its row. The row of a pair is the number of
+// pairs that come before it, which a warp counts over all of them; an expert's first row likewise.
+template <typename U>
+__global__ void __launch_bounds__(kRowThreads)
+few_rows_out_kernel(const U* __restrict__ x, int64_t ldx, int64_t pieces, const int32_t* __restrict__ ids, int pairs, int k,
+                    int experts, int* __restrict__ pos, int* __restrict__ offsets, U* __restrict__ xs, int64_t ldxs) {
+  __shared__ int row_of[kMaxChosen];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = blockIdx.x, c = int64_t(blockIdx.y) * kRowThreads + threadIdx.x;
+  const bool live = pairs > 0 && c < pieces;
+  U v = {};
+  if (live) v = x[t * ldx + c];  // under way while the rows are counted
+  // kept pairs of experts before e, and those of e before pair p
+  auto before = [&](int e, int p) {
+    int n = 0;
+    for (int i = lane; i < pairs; i += 32) {
+      const int id = ids[i];
+      n += (id >= 0 && id < e) || (id == e && i < p);
+    }
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  for (int j = warp; pairs > 0 && j < k; j += kRowThreads / 32) {
+    const int p = int(t) * k + j, e = ids[p];
+    const int n = e >= 0 && e < experts ? before(e, p) : -1;
+    if (lane == 0) {
+      row_of[j] = n;
+      if (blockIdx.y == 0) pos[p] = n;
+    }
+  }
+  const int ctas = int(gridDim.x * gridDim.y), cta = int(blockIdx.y * gridDim.x + blockIdx.x);
+  for (int e = cta * (kRowThreads / 32) + warp; e <= experts; e += ctas * (kRowThreads / 32)) {
+    const int n = before(e, 0);
+    if (lane == 0) offsets[e] = n;
+  }
+  __syncthreads();
+  if (!live) return;
+  for (int j = 0; j < k; ++j) {
+    const int d = row_of[j];
+    if (d >= 0) xs[int64_t(d) * ldxs + c] = v;
   }
 }
-template <int kN>
-__device__ __forceinline__ void load_cols(const uint16_t* p, float (&f)[kN]) {
-  if constexpr (kN == 8) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+
+// kN columns of a row as they are held, 16 bytes or one value, and as fp32.
+template <typename T, int kN>
+struct Cols;
+template <>
+struct Cols<float, 4> {
+  using Held = float4;
+  static __device__ __forceinline__ Held zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+  static __device__ __forceinline__ Held load(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
+  static __device__ __forceinline__ void values(Held v, float (&f)[4]) { f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w; }
+};
+template <>
+struct Cols<float, 1> {
+  using Held = float;
+  static __device__ __forceinline__ Held zero() { return 0.0f; }
+  static __device__ __forceinline__ Held load(const float* p) { return __ldcs(p); }
+  static __device__ __forceinline__ void values(Held v, float (&f)[1]) { f[0] = v; }
+};
+template <>
+struct Cols<uint16_t, 8> {
+  using Held = uint4;
+  static __device__ __forceinline__ Held zero() { return make_uint4(0, 0, 0, 0); }
+  static __device__ __forceinline__ Held load(const uint16_t* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
+  static __device__ __forceinline__ void values(Held v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
-  } else {
-    f[0] = bf16_bits_to_float(__ldcs(p));
   }
-}
+};
+template <>
+struct Cols<uint16_t, 1> {
+  using Held = uint16_t;
+  static __device__ __forceinline__ Held zero() { return 0; }
+  static __device__ __forceinline__ Held load(const uint16_t* p) { return __ldcs(p); }
+  static __device__ __forceinline__ void values(Held v, float (&f)[1]) { f[0] = bf16_bits_to_float(v); }
+};
 template <int kN>
 __device__ __forceinline__ void store_cols(float* p, const float (&f)[kN]) {
   if constexpr (kN == 4)
@@ -525,6 +585,8 @@ __device__ __forceinline__ void store_cols(uint16_t* p, const float (&f)[kN]) {
     *p = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
 }
 
+constexpr int kRowBatch = 8;  // rows of a token whose loads a thread has under way
+
 // y[t] = sum_j w[t, j] ys[pos[t, j]] (weights null: 1) over the pairs that have a row, in the order of j, in fp32, kN columns
 // a thread (1 or 16 bytes' worth; the row's columns are a multiple of it).
 template <typename T, int kN>
@@ -533,25 +595,33 @@ rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int
                  const float* __restrict__ weights, int k, int64_t tokens, int64_t cols, T* __restrict__ y, int64_t ldy) {
   pdl_trigger();
   pdl_wait();
+  using C = Cols<T, kN>;
   const int64_t upr = cols / kN;
   for (int64_t u = int64_t(blockIdx.x) * kRowThreads + threadIdx.x; u < tokens * upr;
        u += int64_t(gridDim.x) * kRowThreads) {
     const int64_t t = u / upr, c = (u - t * upr) * kN;
     float acc[kN] = {};
-    for (int j = 0; j < k; ++j) {
-      const int d = pos[t * k + j];
-      if (d < 0 || d >= rows) continue;
-      const float w = weights ? weights[t * k + j] : 1.0f;
-      float f[kN];
-      load_cols<kN>(ys + int64_t(d) * ldys + c, f);
+    for (int j0 = 0; j0 < k; j0 += kRowBatch) {
+      typename C::Held v[kRowBatch];
+      float w[kRowBatch];
 #pragma unroll
-      for (int i = 0; i < kN; ++i) acc[i] = fmaf(w, f[i], acc[i]);
+      for (int j = 0; j < kRowBatch; ++j) {
+        const int d = j0 + j < k ? pos[t * k + j0 + j] : -1;
+        const bool in = d >= 0 && d < rows;
+        w[j] = in ? (weights ? weights[t * k + j0 + j] : 1.0f) : 0.0f;
+        v[j] = in ? C::load(ys + int64_t(d) * ldys + c) : C::zero();
+      }
+#pragma unroll
+      for (int j = 0; j < kRowBatch; ++j) {
+        float f[kN];
+        C::values(v[j], f);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+      }
     }
     store_cols<kN>(y + t * ldy + c, acc);
   }
 }
-
-constexpr int kGradPairs = 8;  // pairs of a token whose dot products a thread holds at once
 
 // The gradient of rows_back: dys[pos[t, j]] = w[t, j] dy[t], dw[t, j] = <dy[t], ys[pos[t, j]]> (0 for a pair without a
 // row), fp32 sums in a fixed order. dys may be ys. blockDim.x threads a token (a power of two from 32), blockDim.y tokens a CTA.
@@ -560,32 +630,36 @@ __global__ void __launch_bounds__(kRowThreads)
 rows_back_grad_kernel(const T* __restrict__ dy, int64_t lddy, const T* ys, int64_t ldys, int64_t rows,
                       const int* __restrict__ pos, const float* __restrict__ weights, int k, int64_t tokens, int64_t cols,
                       T* dys, int64_t lddys, float* __restrict__ dw) {
-  __shared__ float part[kRowThreads / 32][kGradPairs];
+  using C = Cols<T, kN>;
+  __shared__ float part[kRowThreads / 32][kRowBatch];
   pdl_trigger();
   pdl_wait();
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t step = int64_t(gridDim.x) * blockDim.y;
   for (int64_t t0 = int64_t(blockIdx.x) * blockDim.y; t0 < tokens; t0 += step) {
     const int64_t t = t0 + threadIdx.y;
-    for (int j0 = 0; j0 < k; j0 += kGradPairs) {
-      float sum[kGradPairs] = {};
+    for (int j0 = 0; j0 < k; j0 += kRowBatch) {
+      float sum[kRowBatch] = {};
       if (t < tokens) {
-        int d[kGradPairs];
-        float w[kGradPairs];
+        int d[kRowBatch];
+        float w[kRowBatch];
 #pragma unroll
-        for (int j = 0; j < kGradPairs; ++j) {
+        for (int j = 0; j < kRowBatch; ++j) {
           d[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
           if (d[j] >= rows) d[j] = -1;
           w[j] = d[j] >= 0 ? weights[t * k + j0 + j] : 0.0f;
         }
         for (int64_t c = int64_t(threadIdx.x) * kN; c < cols; c += int64_t(blockDim.x) * kN) {
           float g[kN];
-          load_cols<kN>(dy + t * lddy + c, g);
+          C::values(C::load(dy + t * lddy + c), g);
+          typename C::Held v[kRowBatch];
 #pragma unroll
-          for (int j = 0; j < kGradPairs; ++j) {
+          for (int j = 0; j < kRowBatch; ++j) v[j] = d[j] >= 0 ? C::load(ys + int64_t(d[j]) * ldys + c) : C::zero();
+#pragma unroll
+          for (int j = 0; j < kRowBatch; ++j) {
             if (d[j] < 0) continue;
             float f[kN], o[kN];
-            load_cols<kN>(ys + int64_t(d[j]) * ldys + c, f);
+            C::values(v[j], f);
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
               sum[j] = fmaf(g[i], f[i], sum[j]);
@@ -596,13 +670,13 @@ rows_back_grad_kernel(const T* __restrict__ dy, int64_t lddy, const T* ys, int64
         }
       }
 #pragma unroll
-      for (int j = 0; j < kGradPairs; ++j) {
+      for (int j = 0; j < kRowBatch; ++j) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
         if (lane == 0) part[threadIdx.y * warps + warp][j] = sum[j];
       }
       __syncthreads();
-      if (t < tokens && threadIdx.x < kGradPairs && j0 + int(threadIdx.x) < k) {
+      if (t < tokens && threadIdx.x < kRowBatch && j0 + int(threadIdx.x) < k) {
         float v = 0.0f;
         for (int i = 0; i < warps; ++i) v += part[threadIdx.y * warps + i][threadIdx.x];
         dw[t * k + j0 + threadIdx.x] = v;

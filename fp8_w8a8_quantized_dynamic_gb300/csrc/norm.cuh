@@ -8,6 +8,8 @@
 // One pass: a CTA holds a row in fp32 registers between the loads, the two sums and the stores.
 #pragma once
 
+#include <algorithm>
+
 #include "block_gemm.h"
 #include "device_common.cuh"
 #include "tcgen05.cuh"
@@ -99,72 +101,96 @@ __device__ __forceinline__ float inverse_rms(const float (&v)[kUnits][8], const 
   return __frcp_rn(__fsqrt_rn(__fdiv_rn(ss, float(p.cols)))) * 0x1p-80f;
 }
 
+// A thread's raw values of one row.
+template <int kUnits, bool kGate>
+struct Raw {
+  uint4 y[kUnits], res[kUnits], gate[kGate ? kUnits : 1];
+};
+
+template <int kThreads, int kUnits, bool kGate>
+__device__ __forceinline__ void load_row(Raw<kUnits, kGate>& in, const Params& p, int64_t row) {
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int c = (i * kThreads + threadIdx.x) * 8;
+    in.y[i] = in.res[i] = make_uint4(0, 0, 0, 0);
+    if constexpr (kGate) in.gate[i] = make_uint4(0, 0, 0, 0);
+    if (c < p.cols) {
+      in.y[i] = load8_bf16(p.y + row * p.ldy, c, p.cols, p.vec_y);
+      if (p.residual) in.res[i] = load8_bf16(p.residual + row * p.ldr, c, p.cols, p.vec_res);
+      if constexpr (kGate) in.gate[i] = load8_bf16(p.gate + row * p.ldg, c, p.cols, p.vec_gate);
+    }
+  }
+}
+
 template <int kThreads, int kUnits>
-__global__ void __launch_bounds__(kThreads)
+constexpr bool kAhead = kThreads * kUnits < 4096;  // else a row in fp32 alone takes the registers
+// CTAs of an SM, by the registers that a row takes.
+constexpr int ctas_of(int threads, int units) {
+  return units == 1 ? 1536 / threads : std::max(1, 2048 / (threads * units));
+}
+
+// A CTA takes every gridDim.x-th row. The loads of its next row are under way while it sums, joins and stores the one
+// in its registers.
+template <int kThreads, int kUnits, bool kPost, bool kGate>
+__global__ void __launch_bounds__(kThreads, ctas_of(kThreads, kUnits))
 residual_norm_kernel(const __grid_constant__ Params p) {
   __shared__ float red[2][kThreads / 32];
   pdl_trigger();
   const int cols = p.cols;
-  // the weights stay in registers over the CTA's rows
-  uint4 w[kUnits], pw[kUnits];
+  auto col_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) * 8; };
+  auto weights = [&](const uint16_t* w, int vec, int i, float (&f)[8]) {
+    const int c = col_of(i);
+    unpack8(c < cols ? load8_bf16(w, c, cols, vec) : make_uint4(0, 0, 0, 0), f);
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int c = (i * kThreads + threadIdx.x) * 8;
-    w[i] = pw[i] = make_uint4(0, 0, 0, 0);
-    if (p.pre && c < cols) w[i] = load8_bf16(p.w, c, cols, p.vec_w);
-    if (p.post_w && c < cols) pw[i] = load8_bf16(p.post_w, c, cols, p.vec_post);
-  }
+    for (int j = 0; j < 8; ++j) f[j] += p.w_offset;
+  };
   pdl_wait();
   int turn = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+  Raw<kUnits, kGate> in;
+  int64_t row = blockIdx.x;
+  if (kAhead<kThreads, kUnits> && row < p.rows) load_row<kThreads>(in, p, row);
+  for (; row < p.rows; row += gridDim.x) {
+    if (!kAhead<kThreads, kUnits>) load_row<kThreads>(in, p, row);
     float v[kUnits][8];
-    uint4 in[kUnits], res[kUnits], gate[kUnits];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int c = (i * kThreads + threadIdx.x) * 8;
-      in[i] = res[i] = gate[i] = make_uint4(0, 0, 0, 0);
-      if (c < cols) {
-        in[i] = load8_bf16(p.y + row * p.ldy, c, cols, p.vec_y);
-        if (p.residual) res[i] = load8_bf16(p.residual + row * p.ldr, c, cols, p.vec_res);
-        if (p.gate) gate[i] = load8_bf16(p.gate + row * p.ldg, c, cols, p.vec_gate);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) unpack8(in[i], v[i]);
-    if (p.post_w) {
+    for (int i = 0; i < kUnits; ++i) unpack8(in.y[i], v[i]);
+    if constexpr (kPost) {
       const float inv = inverse_rms<kThreads, kUnits>(v, p, red, turn);
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         float f[8];
-        unpack8(pw[i], f);
+        weights(p.post_w, p.vec_post, i, f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * (f[j] + p.w_offset);
+        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * f[j];
       }
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      if (p.gate) {
-        float f[8];
-        unpack8(gate[i], f);
+      float f[8];
+      if constexpr (kGate) {
+        unpack8(in.gate[i], f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] *= f[j];
       }
-      float f[8];
-      unpack8(res[i], f);
+      unpack8(in.res[i], f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = fmaf(p.scale, v[i][j], f[j]);
-      const int c = (i * kThreads + threadIdx.x) * 8;
-      if (p.r && c < cols) store8_bf16(p.r + row * p.ldro, c, cols, p.vec_r, v[i]);
+    }
+    if (kAhead<kThreads, kUnits> && row + gridDim.x < p.rows) load_row<kThreads>(in, p, row + gridDim.x);
+    if (p.r) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+        if (col_of(i) < cols) store8_bf16(p.r + row * p.ldro, col_of(i), cols, p.vec_r, v[i]);
     }
     if (!p.pre) continue;
     const float inv = inverse_rms<kThreads, kUnits>(v, p, red, turn);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int c = (i * kThreads + threadIdx.x) * 8;
+      const int c = col_of(i);
       float f[8];
-      unpack8(w[i], f);
+      weights(p.w, p.vec_w, i, f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = c + j < cols ? v[i][j] * inv * (f[j] + p.w_offset) : 0.0f;
+      for (int j = 0; j < 8; ++j) v[i][j] = c + j < cols ? v[i][j] * inv * f[j] : 0.0f;
       if (p.n && c < cols) store8_bf16(p.n + row * p.ldn, c, cols, p.vec_n, v[i]);
       if (p.q) {
         // sixteen lanes hold a block of 128 columns; magnitudes compare as integers, which keeps a NaN
