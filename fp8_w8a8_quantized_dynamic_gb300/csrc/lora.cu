@@ -17,6 +17,7 @@
 #include "api_common.h"
 #include "device_cache.h"
 #include "device_common.cuh"
+#include "gemm_tcgen05.h"
 #include "tcgen05.cuh"
 
 namespace fp8k {
@@ -218,6 +219,49 @@ __host__ __device__ constexpr uint32_t idesc_of(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(kTileRows >> 4) << 24);
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+// Sixteen bf16 of a row, in one or two loads and stores.
+struct Sixteen {
+  uint32_t w[8];
+};
+template <int kAlign>
+__device__ __forceinline__ Sixteen load16(const uint16_t* p) {
+  Sixteen v;
+  if constexpr (kAlign == 32)
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+                   "=r"(v.w[7]) : "l"(p) : "memory");
+  else
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(v.w[4 * i]), "=r"(v.w[4 * i + 1]), "=r"(v.w[4 * i + 2]), "=r"(v.w[4 * i + 3]) : "l"(p + 8 * i)
+                   : "memory");
+  return v;
+}
+template <int kAlign>
+__device__ __forceinline__ void store16(uint16_t* p, const Sixteen& v) {
+  if constexpr (kAlign == 32)
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(p), "r"(v.w[0]), "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
+                    "r"(v.w[7]) : "memory");
+  else
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint4*>(p + 8 * i) = make_uint4(v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]);
+}
+// Two fp32 to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 // Byte offset of 16-byte piece c of row r in a tile of 128-byte rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int r, int c) { return uint32_t(r) * 128u + uint32_t((c ^ (r & 7)) << 4); }
 
@@ -239,6 +283,9 @@ __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0
 // What this thread wrote to shared memory becomes visible to the tensor core (after the barrier that follows).
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// n / d for 0 <= n < 4096, d <= 32 and inv = 1 / d: the half keeps the product clear of whole numbers.
+__device__ __forceinline__ int quotient(int n, float inv) { return int((float(n) + 0.5f) * inv); }
+
 struct TileParams {
   Args a;
   Sorted s;
@@ -251,7 +298,9 @@ struct TileParams {
 };
 
 struct TileCtl {
-  uint64_t done[8];
+  uint64_t done[8];    // MMAs of a stage (shrink), of a step (expand)
+  uint64_t loaded[8];  // A of a stage, B of a step
+  uint64_t read[2];    // expand: the warps that have read a step's sums
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -262,7 +311,11 @@ __device__ __forceinline__ uint32_t align1024(uint32_t a) { return (a + 1023u) &
 // tensor memory is held, so that no CTA of a later kernel can hold it while one of this kernel waits for it.
 __device__ __forceinline__ void tile_begin(TileCtl* ctl, uint32_t cols) {
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&ctl->done[i]), 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(smem_u32(&ctl->done[i]), 1);
+      mbar_init(smem_u32(&ctl->loaded[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl->read[i]), kTileThreads / 32);
     ctl->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
@@ -289,7 +342,7 @@ __device__ __forceinline__ void tile_end(TileCtl* ctl, uint32_t cols) {
 
 // v[split][row] = A[e] x[row's token] over the split's K, for a tile's rows.
 __global__ void __launch_bounds__(kTileThreads)
-shrink_kernel(const __grid_constant__ TileParams p) {
+shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ TileParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ TileCtl ctl;
   const uint32_t base = align1024(smem_u32(smem_raw));
@@ -319,32 +372,42 @@ shrink_kernel(const __grid_constant__ TileParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           copy8(st + swizzled(first + 32 * i, piece), x[i], first + 32 * i < rows, k, K, p.vec_x);
+        if (p.vec_a) {
+          if (threadIdx.x == 0) {
+            const uint32_t bar = smem_u32(&ctl.loaded[step % p.stages]);
+            mbar_arrive_expect_tx(bar, uint32_t(p.rp) * 128u);
+            tma_load_3d(st + kXBytes, &tmap_a, bar, (kb0 + step) * 128, 0, t.expert);
+          }
+          return;
+        }
         for (int row = first; row < p.rp; row += 32)
-          copy8(st + kXBytes + swizzled(row, piece), A + int64_t(min(row, r - 1)) * K, row < r, k, K, p.vec_a);
+          copy8(st + kXBytes + swizzled(row, piece), A + int64_t(min(row, r - 1)) * K, row < r, k, K, 0);
       };
       auto wait = [&](int step) {
         return mbar_wait_short(smem_u32(&ctl.done[step % p.stages]), uint32_t(step / p.stages) & 1u, &ctl.abort_flag,
                                &g_lora_error);
       };
-      // stages - 2 steps ahead, so that the MMA whose stage is filled again is not the one just issued
-      const int ahead = p.stages - 2;
+      const int ahead = p.stages - 1;
       for (int i = 0; i < ahead; ++i) {
         if (i < steps) fill(i);
         cp_commit();
       }
       bool ok = true;
       for (int i = 0; i < steps; ++i) {
-        if (i >= 2) ok = wait(i - 2);
+        if (i >= 1) ok = wait(i - 1);  // its stage is filled again
         if (ok && i + ahead < steps) fill(i + ahead);
         cp_commit();
         // the copies of step i have landed
-        if (ahead == 1) cp_wait<1>();
-        else if (ahead == 2) cp_wait<2>();
+        if (ahead == 2) cp_wait<2>();
         else if (ahead == 3) cp_wait<3>();
-        else cp_wait<4>();
+        else if (ahead == 4) cp_wait<4>();
+        else cp_wait<5>();
         fence_async();
         if (!__syncthreads_and(ok)) break;
         if (threadIdx.x == 0) {
+          if (p.vec_a && !mbar_wait_short(smem_u32(&ctl.loaded[i % p.stages]), uint32_t(i / p.stages) & 1u, &ctl.abort_flag,
+                                          &g_lora_error))
+            continue;  // the wait for this step's MMAs gives up as well
           const uint32_t st = base + uint32_t(i % p.stages) * stage_bytes;
           const uint64_t ad = make_sdesc(st), bd = make_sdesc(st + kXBytes);
 #pragma unroll
@@ -376,18 +439,54 @@ shrink_kernel(const __grid_constant__ TileParams p) {
   tile_end(&ctl, p.tmem_cols);
 }
 
-constexpr int kStagePitch = 33;  // floats of a staged row: a warp's writes by row and reads by column both take 32 banks
+// Columns that a warp passes through shared memory at a time, and floats between rows there: eight lanes' 16-byte accesses,
+// down the rows or along them, take 32 banks (pitch 36; along rows of pitch 20 two a bank). 16 columns where a large
+// rank leaves no room for 32.
+__host__ __device__ constexpr int stage_cols(int bn) { return bn == 128 ? 32 : 16; }
 
 // out = y + s B[e] v for a tile's rows and the CTA's columns, kBn a step (64 where the rank's
 // operands leave no room for 128): while a step's sums are read, joined with
 // y and stored, the next one's MMAs run and B of the one after that is copied.
+// v of a tile's rows, the sum of the splits in order, as two bf16 numbers in two swizzled tiles: all kTileThreads threads.
+__device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile& t, int rows, uint32_t v_hi, uint32_t v_lo) {
+  const Args& g = p.a;
+  const int pieces = p.rp / 8;
+  const float inv_pieces = 1.0f / float(pieces);
+  for (int i = threadIdx.x; i < kTileRows * pieces; i += kTileThreads) {
+    const int row = quotient(i, inv_pieces), c = i - row * pieces;
+    float f[8] = {};
+    if (row < rows) {
+      const float* from = p.s.v + int64_t(t.row0 + row) * p.rp + c * 8;
+      for (int s = 0; s < p.s.splits; ++s, from += g.M * p.rp) {
+        const float4 lo = *reinterpret_cast<const float4*>(from), hi = *reinterpret_cast<const float4*>(from + 4);
+        f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
+        f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
+      }
+    }
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+      const float h0 = bf16_lo(h[j]), h1 = bf16_hi(h[j]);
+      // (an infinity has no second part)
+      l[j] = pack_bf16x2(fabsf(h0) <= 3.39e38f ? f[2 * j] - h0 : 0.0f, fabsf(h1) <= 3.39e38f ? f[2 * j + 1] - h1 : 0.0f);
+    }
+    const uint32_t at = uint32_t(c >> 3) * kXBytes + swizzled(row, c & 7);
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v_hi + at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v_lo + at), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3]) : "memory");
+  }
+}
+
 template <int kBn>
-__global__ void __launch_bounds__(kTileThreads)
-expand_kernel(const __grid_constant__ TileParams p) {
+__global__ void __launch_bounds__(kTileThreads, kBn == 128 ? 2 : 1)
+expand_any_kernel(const __grid_constant__ TileParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ TileCtl ctl;
   __shared__ int order[kTileRows];
-  __shared__ float staged[kTileThreads / 32][32 * kStagePitch];
+  constexpr int kSc = stage_cols(kBn), kStagePitch = kSc + 4;
+  constexpr int kLanes = kSc / 8, kRowsAt = 32 / kLanes, kI = 32 / kRowsAt;  // lanes of a row, rows at a time, times
+  constexpr int kParts = kBn / 2 / kSc;
+  __shared__ __align__(16) float staged[kTileThreads / 32][32 * kStagePitch];
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   tile_begin(&ctl, p.tmem_cols);
@@ -412,10 +511,11 @@ expand_kernel(const __grid_constant__ TileParams p) {
     const int steps = (n1 - n0 + kBn - 1) / kBn;
     const uint16_t* B = g.b + int64_t(t.expert) * N * r;
     const int pieces = p.rp / 8;
+    const float inv_pieces = 1.0f / float(pieces);
     auto fill = [&](int step) {
       const uint32_t to = b_at + uint32_t(step & 1) * b_bytes;
       for (int i = threadIdx.x; i < kBn * pieces; i += kTileThreads) {
-        const int row = i / pieces, c = i - row * pieces;
+        const int row = quotient(i, inv_pieces), c = i - row * pieces;
         const int n = n0 + step * kBn + row;
         copy8(to + uint32_t(c >> 3) * (kBn * 128u) + swizzled(row, c & 7), B + int64_t(min(n, N - 1)) * r, n < N, c * 8, r,
               p.vec_b);
@@ -423,30 +523,7 @@ expand_kernel(const __grid_constant__ TileParams p) {
     };
     fill(0);
     cp_commit();
-    // v, the sum of the splits in order, as two bf16 numbers
-    for (int i = threadIdx.x; i < kTileRows * pieces; i += kTileThreads) {
-      const int row = i / pieces, c = i - row * pieces;
-      float f[8] = {};
-      if (row < rows) {
-        const float* from = p.s.v + int64_t(t.row0 + row) * p.rp + c * 8;
-        for (int s = 0; s < p.s.splits; ++s, from += g.M * p.rp) {
-          const float4 lo = *reinterpret_cast<const float4*>(from), hi = *reinterpret_cast<const float4*>(from + 4);
-          f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
-          f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
-        }
-      }
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-        const float h0 = bf16_lo(h[j]), h1 = bf16_hi(h[j]);
-        // (an infinity has no second part)
-        l[j] = pack_bf16x2(fabsf(h0) <= 3.39e38f ? f[2 * j] - h0 : 0.0f, fabsf(h1) <= 3.39e38f ? f[2 * j + 1] - h1 : 0.0f);
-      }
-      const uint32_t at = uint32_t(c >> 3) * kXBytes + swizzled(row, c & 7);
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v_hi + at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v_lo + at), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3]) : "memory");
-    }
+    put_v(p, t, rows, v_hi, v_lo);
     auto multiply = [&](int step) {
       const uint32_t b = b_at + uint32_t(step & 1) * b_bytes, d = ctl.tmem_base + uint32_t(step & 1) * kBn;
       for (int part = 0; part < 2; ++part)
@@ -466,19 +543,26 @@ expand_kernel(const __grid_constant__ TileParams p) {
     const float scale = g.scales ? g.scales[t.expert] : 1.0f;
     const int quarter = warp & 3, half = warp >> 2;
     float* mine32 = staged[warp];
-    // lane: row lane / 4 of each eight, columns (lane % 4) * 8 of each 32
-    const int c8 = (lane & 3) * 8, r8 = lane >> 2;
+    const int c8 = (lane % kLanes) * 8, r8 = lane / kLanes;
+    int64_t row_y[kI], row_o[kI];       // the first element of a row, -1 for none
+#pragma unroll
+    for (int i = 0; i < kI; ++i) {
+      const int token = order[quarter * 32 + i * kRowsAt + r8];
+      row_y[i] = token >= 0 ? token * g.ldy : -1;
+      row_o[i] = token * g.ldo;
+    }
+    auto col_of = [&](int step, int h) { return n0 + step * kBn + half * (kBn / 2) + h * kSc + c8; };
+    auto load_y = [&](int step, int h, int i) {
+      const int n = col_of(step, h);
+      if (row_y[i] < 0 || n >= N) return make_uint4(0, 0, 0, 0);
+      return load8_bf16(g.y + row_y[i], n, N, p.vec_y);
+    };
+    uint4 yv[kParts][kI];
+#pragma unroll
+    for (int h = 0; h < kParts; ++h)
+#pragma unroll
+      for (int i = 0; i < kI; ++i) yv[h][i] = load_y(0, h, i);
     for (int step = 0; step < steps; ++step) {
-      const int col = n0 + step * kBn + half * (kBn / 2);
-      uint4 yv[kBn / 64][4];
-#pragma unroll
-      for (int h = 0; h < kBn / 64; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int token = order[quarter * 32 + i * 8 + r8], n = col + h * 32 + c8;
-          yv[h][i] = make_uint4(0, 0, 0, 0);
-          if (token >= 0 && n < N) yv[h][i] = load8_bf16(g.y + int64_t(token) * g.ldy, n, N, p.vec_y);
-        }
       bool ok = mbar_wait_short(smem_u32(&ctl.done[step & 1]), uint32_t(step >> 1) & 1u, &ctl.abort_flag, &g_lora_error);
       // B of the next step has landed; the sums of the step before this one have been read by all warps
       cp_wait<0>();
@@ -489,35 +573,173 @@ expand_kernel(const __grid_constant__ TileParams p) {
       if (threadIdx.x == 0 && step + 1 < steps) multiply(step + 1);
       if (step + 2 < steps) fill(step + 2);
       cp_commit();
+      uint32_t f[32];
 #pragma unroll
-      for (int h = 0; h < kBn / 64; ++h) {
-        uint32_t f[32];
-        tmem_ld32(ctl.tmem_base + uint32_t(step & 1) * kBn + (uint32_t(quarter * 32) << 16) + half * (kBn / 2) + h * 32, f);
+      for (int h = 0; h < kParts; ++h) {
+        if (h * kSc % 32 == 0)
+          tmem_ld32(ctl.tmem_base + uint32_t(step & 1) * kBn + (uint32_t(quarter * 32) << 16) + half * (kBn / 2) + h * kSc, f);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mine32[lane * kStagePitch + j] = __uint_as_float(f[j]);
+        for (int j = 0; j < kSc; j += 4) {
+          const uint32_t* from = f + h * kSc % 32 + j;
+          *reinterpret_cast<uint4*>(mine32 + lane * kStagePitch + j) = make_uint4(from[0], from[1], from[2], from[3]);
+        }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = i * 8 + r8, token = order[quarter * 32 + row], n = col + h * 32 + c8;
+        for (int i = 0; i < kI; ++i) {
+          const int n = col_of(step, h);
           float o[8];
           unpack8(yv[h][i], o);
+          // y of the next step is under way from here on
+          if (step + 1 < steps) yv[h][i] = load_y(step + 1, h, i);
+          const float4 lo = *reinterpret_cast<const float4*>(mine32 + (i * kRowsAt + r8) * kStagePitch + c8);
+          const float4 hi = *reinterpret_cast<const float4*>(mine32 + (i * kRowsAt + r8) * kStagePitch + c8 + 4);
+          const float d[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = fmaf(scale, mine32[row * kStagePitch + c8 + j], o[j]);
-          if (token >= 0 && n < N) {
-            uint16_t* dst = g.out + int64_t(token) * g.ldo + n;
-            if (p.vec_y && n + 8 <= N) {
-              *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                                                          pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-            } else {
+          for (int j = 0; j < 8; ++j) o[j] = fmaf(scale, d[j], o[j]);
+          if (row_y[i] >= 0 && n < N) {
+            uint16_t* dst = g.out + row_o[i] + n;
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (n + j < N) dst[j] = __bfloat16_as_ushort(__float2bfloat16_rn(o[j]));
-            }
+            for (int j = 0; j < 8; ++j)
+              if (n + j < N) dst[j] = __bfloat16_as_ushort(__float2bfloat16_rn(o[j]));
           }
         }
         __syncwarp();
       }
     }
+  }
+  tile_end(&ctl, p.tmem_cols);
+}
+
+// out = y + s B[e] v where the rows of y, out and B start on 16-byte boundaries and N is whole sixteens. The CTAs share out
+// (tile, kBn columns) steps in equal runs, so that a CTA passes along the columns of one tile and perhaps on to the next
+// one. Warps 0 to 7 hold 32 rows and half of the columns each: a thread reads its row of the sums, joins 16 columns at a
+// time with y, which it loaded a step ahead, and stores them. Warp 8 loads B by TMA and issues the MMAs, a step ahead.
+constexpr int kExpandThreads = kTileThreads + 32;
+
+template <int kBn, int kAlign>
+__global__ void __launch_bounds__(kExpandThreads, kBn == 128 ? 2 : 1)
+expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ TileParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TileCtl ctl;
+  __shared__ int order[2][kTileRows];
+  const uint32_t base = align1024(smem_u32(smem_raw));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tile_begin(&ctl, p.tmem_cols);
+  const Args& g = p.a;
+  const int N = int(g.N);
+  const int steps = (N + kBn - 1) / kBn;
+  const int64_t total = int64_t(*p.s.n_tiles) * steps, run = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t end = min(total, run * (blockIdx.x + 1));
+  const int rk = (p.rp + kBk - 1) / kBk;  // 128-byte rows that the rank fills
+  const uint32_t v_hi = base, v_lo = base + uint32_t(rk) * kXBytes, b_at = v_lo + uint32_t(rk) * kXBytes;
+  const uint32_t b_bytes = uint32_t(rk) * (kBn * 128u);
+  auto wait = [&](uint64_t* bar, uint32_t it) {  // the it-th step's phase of a pair of barriers
+    return mbar_wait_short(smem_u32(bar + (it & 1u)), (it >> 1) & 1u, &ctl.abort_flag, &g_lora_error);
+  };
+  uint32_t it = 0;  // steps so far
+  bool ok = true;
+  int turn = 0;
+  for (int64_t u = run * blockIdx.x; u < end;) {
+    const int tile = int(u / steps), s0 = int(u - int64_t(tile) * steps), s1 = int(min(int64_t(steps), s0 + (end - u)));
+    u += s1 - s0;
+    const block::RowTile t = p.s.tiles[tile];
+    const int rows = min(kTileRows, t.row_end - t.row0);
+    if (t.expert >= g.adapters) {
+      if (g.out != g.y)
+        for (int row = warp; row < rows; row += kExpandThreads / 32) {
+          const int64_t token = p.s.order[t.row0 + row];
+          for (int n = s0 * kBn + lane * 8; n < min(N, s1 * kBn); n += 256)
+            *reinterpret_cast<uint4*>(g.out + token * g.ldo + n) = *reinterpret_cast<const uint4*>(g.y + token * g.ldy + n);
+        }
+      continue;
+    }
+    int* token_of = order[turn++ & 1];
+    auto fill = [&](int step, uint32_t at) {
+      const uint32_t bar = smem_u32(&ctl.loaded[at & 1u]);
+      mbar_arrive_expect_tx(bar, b_bytes);
+      for (int i = 0; i < rk; ++i)
+        tma_load_3d(b_at + (at & 1u) * b_bytes + uint32_t(i) * (kBn * 128u), &tmap_b, bar, i * 128, step * kBn, t.expert);
+    };
+    if (warp == kTileThreads / 32) {
+      if (lane == 0 && ok) {  // the buffer's last MMAs are those of step it - 2
+        if (it >= 2) ok = wait(ctl.done, it - 2);
+        if (ok) fill(s0, it);
+      }
+    } else {
+      // all of the last tile's MMAs are done: each warp waited for its last step
+      if (threadIdx.x < kTileRows) token_of[threadIdx.x] = int(threadIdx.x) < rows ? p.s.order[t.row0 + threadIdx.x] : -1;
+      put_v(p, t, rows, v_hi, v_lo);
+      fence_async();
+    }
+    if (!__syncthreads_and(ok)) break;
+    if (warp == kTileThreads / 32) {
+      if (lane == 0) {
+        for (int s = s0; s < s1 && ok; ++s, ++it) {
+          ok = wait(ctl.loaded, it) && (it < 2 || wait(ctl.read, it - 2));
+          if (!ok) break;
+          tmem_fence_after();
+          const uint32_t b = b_at + (it & 1u) * b_bytes, d = ctl.tmem_base + (it & 1u) * kBn;
+          for (int part = 0; part < 2; ++part)
+            for (int k16 = 0; k16 < p.rp / 16; ++k16) {
+              const uint64_t ad = make_sdesc((part ? v_lo : v_hi) + uint32_t(k16 >> 2) * kXBytes) + uint64_t((k16 & 3) * 2);
+              const uint64_t bd = make_sdesc(b + uint32_t(k16 >> 2) * (kBn * 128u)) + uint64_t((k16 & 3) * 2);
+              mma_bf16(d, ad, bd, idesc_of(kBn), part != 0 || k16 != 0);
+            }
+          mma_commit<false>(smem_u32(&ctl.done[it & 1u]));
+          if (s + 1 < s1) {
+            if (it >= 1) ok = wait(ctl.done, it - 1);
+            if (ok) fill(s + 1, it + 1);
+          }
+        }
+      }
+      it = __shfl_sync(0xffffffffu, it, 0);
+      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+      continue;
+    }
+    const int quarter = warp & 3, half = warp >> 2;
+    constexpr int kPieces = kBn / 2 / 16;  // of sixteen columns, of a warp
+    const int token = token_of[quarter * 32 + lane];
+    const uint16_t* y = g.y + (token >= 0 ? token * g.ldy : 0);
+    uint16_t* out = g.out + (token >= 0 ? token * g.ldo : 0);
+    const float scale = g.scales ? g.scales[t.expert] : 1.0f;
+    Sixteen yv[kPieces];
+    int col = s0 * kBn + half * (kBn / 2);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (token >= 0 && col + i * 16 < N) yv[i] = load16<kAlign>(y + col + i * 16);
+    for (int s = s0; s < s1; ++s, ++it, col += kBn) {
+      ok = __all_sync(0xffffffffu, ok && wait(ctl.done, it));
+      if (!ok) break;
+      tmem_fence_after();
+      const uint32_t from = ctl.tmem_base + (it & 1u) * kBn + (uint32_t(quarter * 32) << 16) + half * (kBn / 2);
+#pragma unroll
+      for (int h = 0; h < kPieces / 2; ++h) {
+        uint32_t f[32];
+        tmem_ld32(from + h * 32, f);
+        if (h == kPieces / 2 - 1) {  // the sums have been read: the buffer is free before they are joined
+          tmem_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.read[it & 1u]));
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int i = 2 * h + q;
+          Sixteen o;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o.w[j] = cvt_bf16x2(fmaf(scale, __uint_as_float(f[q * 16 + 2 * j]), bf16_lo(yv[i].w[j])),
+                                fmaf(scale, __uint_as_float(f[q * 16 + 2 * j + 1]), bf16_hi(yv[i].w[j])));
+          const int n = col + i * 16;
+          // y of the next step is under way from here on
+          if (token >= 0 && s + 1 < s1 && n + kBn < N) yv[i] = load16<kAlign>(y + n + kBn);
+          if (token >= 0 && n < N) store16<kAlign>(out + n, o);
+        }
+      }
+    }
+  }
+  if (!ok) {  // nothing of a load may land after the CTA has left
+    if (threadIdx.x == kTileThreads)
+      for (int i = 0; i < 2; ++i) mbar_wait_bounded(smem_u32(&ctl.loaded[(it + i) & 1u]), ((it + i) >> 1) & 1u, nullptr, &g_lora_error);
   }
   tile_end(&ctl, p.tmem_cols);
 }
@@ -547,14 +769,14 @@ bool allow_smem(const void* kfn) {
 int splits_of(int64_t M, int64_t K, int64_t adapters) {
   const int64_t tiles = (M + kTileRows - 1) / kTileRows + std::min(M, adapters) / 2;
   const int64_t kb = (K + kBk - 1) / kBk;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kb / 4, (2 * 152 + tiles - 1) / tiles));
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kb / 4, 2 * 152 / tiles));
   const int64_t slice = (kb + want - 1) / want;
   return int(std::max<int64_t>(1, (kb + slice - 1) / std::max<int64_t>(slice, 1)));
 }
 
 template <int kBn>
-bool launch_expand(TileParams p, int num_sms, cudaStream_t st) {
-  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn>))) return false;
+bool launch_expand_any(TileParams p, int num_sms, cudaStream_t st) {
+  if (!allow_smem(reinterpret_cast<const void*>(expand_any_kernel<kBn>))) return false;
   const int rk = (p.rp + kBk - 1) / kBk;
   const size_t smem = 1024 + size_t(rk) * (2 * kXBytes + 2 * kBn * 128);
   // columns of a CTA: CTAs for two on every SM, as far as there are columns
@@ -563,8 +785,21 @@ bool launch_expand(TileParams p, int num_sms, cudaStream_t st) {
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(steps, (4 * num_sms + tiles - 1) / tiles));
   p.cols_per_cta = int((steps + want - 1) / want) * kBn;
   p.tmem_cols = 2 * kBn;
-  return launch(expand_kernel<kBn>, dim3(unsigned(p.s.max_tiles), unsigned((p.a.N + p.cols_per_cta - 1) / p.cols_per_cta)),
+  return launch(expand_any_kernel<kBn>,
+                dim3(unsigned(p.s.max_tiles), unsigned((p.a.N + p.cols_per_cta - 1) / p.cols_per_cta)),
                 dim3(kTileThreads), smem, st, true, dim3(1, 1, 1), p) == FP8_OK;
+}
+
+template <int kBn, int kAlign>
+bool launch_expand(TileParams p, const CUtensorMap& map_b, int num_sms, cudaStream_t st) {
+  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn, kAlign>))) return false;
+  const int rk = (p.rp + kBk - 1) / kBk;
+  const size_t smem = 1024 + size_t(rk) * (2 * kXBytes + 2 * kBn * 128);
+  const int per_sm = smem <= 112 * 1024 ? 2 : 1;
+  const int64_t units = p.s.max_tiles * ((p.a.N + kBn - 1) / kBn);
+  p.tmem_cols = 2 * kBn;
+  return launch(expand_kernel<kBn, kAlign>, dim3(unsigned(std::min<int64_t>(units, int64_t(per_sm) * num_sms))),
+                dim3(kExpandThreads), smem, st, true, dim3(1, 1, 1), map_b, p) == FP8_OK;
 }
 
 bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st) {
@@ -583,10 +818,27 @@ bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st)
   p.stages = std::max(3, std::min(kShrinkMaxStages, 108 * 1024 / stage_bytes));
   p.tmem_cols = 32;
   while (int(p.tmem_cols) < p.rp) p.tmem_cols *= 2;
-  if (launch(shrink_kernel, dim3(unsigned(s.max_tiles), unsigned(s.splits)), dim3(kTileThreads),
-             size_t(p.stages) * stage_bytes + 1024, st, true, dim3(1, 1, 1), p) != FP8_OK)
+  CUtensorMap map_a = {}, map_b = {};
+  // (rows of 128 bytes; what lies past the rank or past K reads as zeros)
+  if ((p.vec_a && !make_fp8_tensor_map_3d(&map_a, reinterpret_cast<const uint8_t*>(a.a), a.adapters, a.rank, a.K * 2,
+                                          a.K * 2, uint32_t(p.rp))) ||
+      (p.vec_b && !make_fp8_tensor_map_3d(&map_b, reinterpret_cast<const uint8_t*>(a.b), a.adapters, a.N,
+                                          int64_t(a.rank) * 2, int64_t(a.rank) * 2, p.rp <= 2 * kBk ? 128 : 64)))
     return false;
-  return p.rp <= 2 * kBk ? launch_expand<128>(p, num_sms, st) : launch_expand<64>(p, num_sms, st);
+  if (launch(shrink_kernel, dim3(unsigned(s.max_tiles), unsigned(s.splits)), dim3(kTileThreads),
+             size_t(p.stages) * stage_bytes + 1024, st, true, dim3(1, 1, 1), map_a, p) != FP8_OK)
+    return false;
+  auto rows_on = [&](int bytes) {
+    return aligned(a.y, bytes) && aligned(a.out, bytes) && (a.M <= 1 || (a.ldy * 2 % bytes == 0 && a.ldo * 2 % bytes == 0));
+  };
+  const int on = p.vec_b && a.N % 16 == 0 ? (rows_on(32) ? 32 : rows_on(16) ? 16 : 0) : 0;
+  if (p.rp <= 2 * kBk)
+    return on == 32   ? launch_expand<128, 32>(p, map_b, num_sms, st)
+           : on == 16 ? launch_expand<128, 16>(p, map_b, num_sms, st)
+                      : launch_expand_any<128>(p, num_sms, st);
+  return on == 32   ? launch_expand<64, 32>(p, map_b, num_sms, st)
+         : on == 16 ? launch_expand<64, 16>(p, map_b, num_sms, st)
+                    : launch_expand_any<64>(p, num_sms, st);
 }
 
 unsigned int read_and_clear_error() {
