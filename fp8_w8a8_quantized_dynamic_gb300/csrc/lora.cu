@@ -225,36 +225,23 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
-// Sixteen bf16 of a row, in one or two loads and stores.
-struct Sixteen {
-  uint32_t w[8];
-};
-template <int kAlign>
-__device__ __forceinline__ Sixteen load16(const uint16_t* p) {
-  Sixteen v;
-  if constexpr (kAlign == 32)
-    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
-                   "=r"(v.w[7]) : "l"(p) : "memory");
-  else
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(v.w[4 * i]), "=r"(v.w[4 * i + 1]), "=r"(v.w[4 * i + 2]), "=r"(v.w[4 * i + 3]) : "l"(p + 8 * i)
-                   : "memory");
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
-template <int kAlign>
-__device__ __forceinline__ void store16(uint16_t* p, const Sixteen& v) {
-  if constexpr (kAlign == 32)
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                 :: "l"(p), "r"(v.w[0]), "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
-                    "r"(v.w[7]) : "memory");
-  else
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint4*>(p + 8 * i) = make_uint4(v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]);
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+
+// A barrier of `threads` of the block's threads; whether ok holds for all of them.
+__device__ __forceinline__ bool barrier_all(int id, int threads, bool ok) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"(uint32_t(ok)), "r"(id), "r"(threads) : "memory");
+  return r != 0;
+}
+
 // Two fp32 to bf16, the first in the low half.
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   uint32_t d;
@@ -291,16 +278,20 @@ struct TileParams {
   Sorted s;
   int rp;                   // rank rounded up to 16
   int kb, kb_slice;         // blocks of 64 of K, and of one split
-  int stages;
+  int stages;               // shrink
+  int slots, b_bufs;        // expand: of y, of B
   int cols_per_cta;         // expand: a multiple of kBn
   int vec_x, vec_a, vec_b, vec_y;
   uint32_t tmem_cols;
 };
 
+constexpr int kCopyThreads = 128;  // expand: those that copy y and out
+
 struct TileCtl {
   uint64_t done[8];    // MMAs of a stage (shrink), of a step (expand)
   uint64_t loaded[8];  // A of a stage, B of a step
   uint64_t read[2];    // expand: the warps that have read a step's sums
+  uint64_t y_in[4], y_out[4];  // expand: a slot holds y, holds out
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -309,13 +300,18 @@ __device__ __forceinline__ uint32_t align1024(uint32_t a) { return (a + 1023u) &
 
 // The start and end that both kernels share: barriers and tensor memory. The trigger for the next kernel comes after the
 // tensor memory is held, so that no CTA of a later kernel can hold it while one of this kernel waits for it.
-__device__ __forceinline__ void tile_begin(TileCtl* ctl, uint32_t cols) {
+// (warps: those that join sums with y)
+__device__ __forceinline__ void tile_begin(TileCtl* ctl, uint32_t cols, int warps) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&ctl->done[i]), 1);
       mbar_init(smem_u32(&ctl->loaded[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl->read[i]), kTileThreads / 32);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl->read[i]), uint32_t(warps));
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&ctl->y_in[i]), kCopyThreads);
+      mbar_init(smem_u32(&ctl->y_out[i]), uint32_t(warps));
+    }
     ctl->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async();
@@ -347,7 +343,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
   __shared__ TileCtl ctl;
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tile_begin(&ctl, p.tmem_cols);
+  tile_begin(&ctl, p.tmem_cols, kTileThreads / 32);
   const int tile = blockIdx.x;
   const Args& g = p.a;
   const int K = int(g.K), r = g.rank;
@@ -447,12 +443,14 @@ __host__ __device__ constexpr int stage_cols(int bn) { return bn == 128 ? 32 : 1
 // out = y + s B[e] v for a tile's rows and the CTA's columns, kBn a step (64 where the rank's
 // operands leave no room for 128): while a step's sums are read, joined with
 // y and stored, the next one's MMAs run and B of the one after that is copied.
-// v of a tile's rows, the sum of the splits in order, as two bf16 numbers in two swizzled tiles: all kTileThreads threads.
-__device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile& t, int rows, uint32_t v_hi, uint32_t v_lo) {
+// v of a tile's rows, the sum of the splits in order, as two bf16 numbers in two swizzled tiles, by the block's first
+// `threads` threads.
+__device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile& t, int rows, uint32_t v_hi, uint32_t v_lo,
+                                      int threads) {
   const Args& g = p.a;
   const int pieces = p.rp / 8;
   const float inv_pieces = 1.0f / float(pieces);
-  for (int i = threadIdx.x; i < kTileRows * pieces; i += kTileThreads) {
+  for (int i = threadIdx.x; i < kTileRows * pieces; i += threads) {
     const int row = quotient(i, inv_pieces), c = i - row * pieces;
     float f[8] = {};
     if (row < rows) {
@@ -489,7 +487,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
   __shared__ __align__(16) float staged[kTileThreads / 32][32 * kStagePitch];
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tile_begin(&ctl, p.tmem_cols);
+  tile_begin(&ctl, p.tmem_cols, kTileThreads / 32);
   const Args& g = p.a;
   const int N = int(g.N), r = g.rank;
   const int tile = blockIdx.x;
@@ -523,7 +521,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
     };
     fill(0);
     cp_commit();
-    put_v(p, t, rows, v_hi, v_lo);
+    put_v(p, t, rows, v_hi, v_lo, kTileThreads);
     auto multiply = [&](int step) {
       const uint32_t b = b_at + uint32_t(step & 1) * b_bytes, d = ctl.tmem_base + uint32_t(step & 1) * kBn;
       for (int part = 0; part < 2; ++part)
@@ -610,137 +608,200 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
   tile_end(&ctl, p.tmem_cols);
 }
 
-// out = y + s B[e] v where the rows of y, out and B start on 16-byte boundaries and N is whole sixteens. The CTAs share out
-// (tile, kBn columns) steps in equal runs, so that a CTA passes along the columns of one tile and perhaps on to the next
-// one. Warps 0 to 7 hold 32 rows and half of the columns each: a thread reads its row of the sums, joins 16 columns at a
-// time with y, which it loaded a step ahead, and stores them. Warp 8 loads B by TMA and issues the MMAs, a step ahead.
-constexpr int kExpandThreads = kTileThreads + 32;
+// out = y + s B[e] v where the rows of y, out and B start on 16-byte boundaries and N is whole eights. The CTAs share out
+// (tile, kBn columns) steps in equal runs, so that a CTA passes along the columns of one tile and perhaps on to the next.
+//   joining warps  32 rows and 32 columns each: a thread reads its row of a step's sums from tensor memory, joins it with y in
+//                  a slot of shared memory and writes the result over y there.
+//   issuing warp   loads B by TMA, two or three steps ahead, and issues the MMAs.
+//   copying warps  y into the slots, by asynchronous 16-byte copies as far ahead as there are slots, and out from them: 32
+//                  rows each, whole lines at a time (the rows of a tile may be any tokens).
+// What was measured for 8192 x 14336: rows loaded and stored by the joining threads, 32 bytes of a row at a time, 111 us
+// (each asks the L2 for a single sector); a bulk copy of 256 bytes a row each way 470 us (some 60 cycles a copy).
+// Slot rows lie 16 bytes further apart than they are long, so that eight lanes' accesses down the rows take all banks.
+constexpr int join_threads(int bn) { return bn * 4; }
+constexpr int expand_threads(int bn) { return join_threads(bn) + 32 + kCopyThreads; }
 
-template <int kBn, int kAlign>
-__global__ void __launch_bounds__(kExpandThreads, kBn == 128 ? 2 : 1)
+template <int kBn>
+__global__ void __launch_bounds__(kBn * 4 + 32 + kCopyThreads, 1)
 expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ TileParams p) {
+  constexpr int kJoin = kBn * 4, kJoinWarps = kJoin / 32;
+  constexpr uint32_t kPitch = kBn * 2 + 16, kSlotBytes = kTileRows * kPitch;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TileCtl ctl;
-  __shared__ int order[2][kTileRows];
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tile_begin(&ctl, p.tmem_cols);
+  tile_begin(&ctl, p.tmem_cols, kJoinWarps);
   const Args& g = p.a;
   const int N = int(g.N);
   const int steps = (N + kBn - 1) / kBn;
   const int64_t total = int64_t(*p.s.n_tiles) * steps, run = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t end = min(total, run * (blockIdx.x + 1));
+  const int64_t begin = run * blockIdx.x, end = min(total, run * (blockIdx.x + 1));
   const int rk = (p.rp + kBk - 1) / kBk;  // 128-byte rows that the rank fills
   const uint32_t v_hi = base, v_lo = base + uint32_t(rk) * kXBytes, b_at = v_lo + uint32_t(rk) * kXBytes;
   const uint32_t b_bytes = uint32_t(rk) * (kBn * 128u);
+  const uint32_t slots_at = b_at + uint32_t(p.b_bufs) * b_bytes;
   auto wait = [&](uint64_t* bar, uint32_t it) {  // the it-th step's phase of a pair of barriers
     return mbar_wait_short(smem_u32(bar + (it & 1u)), (it >> 1) & 1u, &ctl.abort_flag, &g_lora_error);
   };
-  uint32_t it = 0;  // steps so far
-  bool ok = true;
-  int turn = 0;
-  for (int64_t u = run * blockIdx.x; u < end;) {
-    const int tile = int(u / steps), s0 = int(u - int64_t(tile) * steps), s1 = int(min(int64_t(steps), s0 + (end - u)));
-    u += s1 - s0;
-    const block::RowTile t = p.s.tiles[tile];
-    const int rows = min(kTileRows, t.row_end - t.row0);
-    if (t.expert >= g.adapters) {
-      if (g.out != g.y)
-        for (int row = warp; row < rows; row += kExpandThreads / 32) {
-          const int64_t token = p.s.order[t.row0 + row];
-          for (int n = s0 * kBn + lane * 8; n < min(N, s1 * kBn); n += 256)
-            *reinterpret_cast<uint4*>(g.out + token * g.ldo + n) = *reinterpret_cast<const uint4*>(g.y + token * g.ldy + n);
-        }
-      continue;
-    }
-    int* token_of = order[turn++ & 1];
-    auto fill = [&](int step, uint32_t at) {
-      const uint32_t bar = smem_u32(&ctl.loaded[at & 1u]);
-      mbar_arrive_expect_tx(bar, b_bytes);
-      for (int i = 0; i < rk; ++i)
-        tma_load_3d(b_at + (at & 1u) * b_bytes + uint32_t(i) * (kBn * 128u), &tmap_b, bar, i * 128, step * kBn, t.expert);
+  auto wait_ring = [&](uint64_t* bars, uint32_t it, int n) {  // of a ring of n
+    return mbar_wait_short(smem_u32(bars + it % uint32_t(n)), (it / uint32_t(n)) & 1u, &ctl.abort_flag, &g_lora_error);
+  };
+
+  if (warp > kJoinWarps) {
+    // ---------------- copies of y and out: 32 rows a warp, lane l knows the token of the l-th ----------------
+    constexpr int kLanes = kBn / 8, kRowsAt = 32 / kLanes;  // lanes of a row, rows at a time
+    const int first = (warp - kJoinWarps - 1) * 32, at_row = lane / kLanes, at_col = (lane % kLanes) * 8;
+    struct Walk {
+      int64_t u;      // the step after this part of a tile
+      int s, s1;      // columns of the next step, and where the part ends
+      int token;
     };
-    if (warp == kTileThreads / 32) {
-      if (lane == 0 && ok) {  // the buffer's last MMAs are those of step it - 2
-        if (it >= 2) ok = wait(ctl.done, it - 2);
-        if (ok) fill(s0, it);
+    auto enter = [&](Walk& w) {  // the next part of a tile with an adapter; false behind the last
+      while (w.u < end) {
+        const int tile = int(w.u / steps);
+        w.s = int(w.u - int64_t(tile) * steps);
+        w.s1 = int(min(int64_t(steps), w.s + (end - w.u)));
+        w.u += w.s1 - w.s;
+        const block::RowTile t = p.s.tiles[tile];
+        if (t.expert >= g.adapters) continue;
+        w.token = first + lane < min(kTileRows, t.row_end - t.row0) ? p.s.order[t.row0 + first + lane] : -1;
+        return true;
       }
-    } else {
-      // all of the last tile's MMAs are done: each warp waited for its last step
-      if (threadIdx.x < kTileRows) token_of[threadIdx.x] = int(threadIdx.x) < rows ? p.s.order[t.row0 + threadIdx.x] : -1;
-      put_v(p, t, rows, v_hi, v_lo);
-      fence_async();
+      return false;
+    };
+    const uint32_t mine = slots_at + uint32_t(first + at_row) * kPitch + at_col * 2u;
+    Walk in = {begin}, out = {begin};
+    bool more = enter(in), left = enter(out);
+    uint32_t n_in = 0, n_out = 0;
+    while (left) {
+      while (more && n_in < n_out + uint32_t(p.slots)) {
+        const uint32_t slot = n_in % uint32_t(p.slots), to = mine + slot * kSlotBytes;
+        const int col = in.s * kBn + at_col;
+#pragma unroll
+        for (int i = 0; i < kLanes; ++i) {
+          const int token = __shfl_sync(0xffffffffu, in.token, i * kRowsAt + at_row);
+          if (token >= 0 && col < N)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                         :: "r"(to + uint32_t(i * kRowsAt) * kPitch), "l"(g.y + token * g.ldy + col) : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(smem_u32(&ctl.y_in[slot])) : "memory");
+        ++n_in;
+        if (++in.s == in.s1) more = enter(in);
+      }
+      if (!__all_sync(0xffffffffu, wait_ring(ctl.y_out, n_out, p.slots))) break;
+      const uint32_t from = mine + (n_out % uint32_t(p.slots)) * kSlotBytes;
+      const int col = out.s * kBn + at_col;
+#pragma unroll
+      for (int i0 = 0; i0 < kLanes; i0 += 4) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lds128(from + uint32_t((i0 + i) * kRowsAt) * kPitch);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int token = __shfl_sync(0xffffffffu, out.token, (i0 + i) * kRowsAt + at_row);
+          if (token >= 0 && col < N) *reinterpret_cast<uint4*>(g.out + token * g.ldo + col) = v[i];
+        }
+      }
+      ++n_out;
+      if (++out.s == out.s1) left = enter(out);
     }
-    if (!__syncthreads_and(ok)) break;
-    if (warp == kTileThreads / 32) {
-      if (lane == 0) {
-        for (int s = s0; s < s1 && ok; ++s, ++it) {
-          ok = wait(ctl.loaded, it) && (it < 2 || wait(ctl.read, it - 2));
-          if (!ok) break;
-          tmem_fence_after();
-          const uint32_t b = b_at + (it & 1u) * b_bytes, d = ctl.tmem_base + (it & 1u) * kBn;
-          for (int part = 0; part < 2; ++part)
-            for (int k16 = 0; k16 < p.rp / 16; ++k16) {
-              const uint64_t ad = make_sdesc((part ? v_lo : v_hi) + uint32_t(k16 >> 2) * kXBytes) + uint64_t((k16 & 3) * 2);
-              const uint64_t bd = make_sdesc(b + uint32_t(k16 >> 2) * (kBn * 128u)) + uint64_t((k16 & 3) * 2);
-              mma_bf16(d, ad, bd, idesc_of(kBn), part != 0 || k16 != 0);
+  } else {
+    uint32_t it = 0;  // steps so far
+    bool ok = true;
+    for (int64_t u = begin; u < end;) {
+      const int tile = int(u / steps), s0 = int(u - int64_t(tile) * steps), s1 = int(min(int64_t(steps), s0 + (end - u)));
+      u += s1 - s0;
+      const block::RowTile t = p.s.tiles[tile];
+      const int rows = min(kTileRows, t.row_end - t.row0);
+      if (t.expert >= g.adapters) {
+        if (g.out != g.y)
+          for (int row = warp; row < rows; row += kJoinWarps + 1) {
+            const int64_t token = p.s.order[t.row0 + row];
+            for (int n = s0 * kBn + lane * 8; n < min(N, s1 * kBn); n += 256)
+              *reinterpret_cast<uint4*>(g.out + token * g.ldo + n) = *reinterpret_cast<const uint4*>(g.y + token * g.ldy + n);
+          }
+        continue;
+      }
+      auto fill = [&](int step, uint32_t at) {
+        const uint32_t buf = at % uint32_t(p.b_bufs), bar = smem_u32(&ctl.loaded[buf]);
+        mbar_arrive_expect_tx(bar, b_bytes);
+        for (int i = 0; i < rk; ++i)
+          tma_load_3d(b_at + buf * b_bytes + uint32_t(i) * (kBn * 128u), &tmap_b, bar, i * 128, step * kBn, t.expert);
+      };
+      if (warp == kJoinWarps) {
+        if (lane == 0 && ok) {  // the buffers are free behind the last tile's last MMAs
+          if (it >= 1) ok = wait(ctl.done, it - 1);
+          for (int i = 0; ok && i < p.b_bufs - 1 && s0 + i < s1; ++i) fill(s0 + i, it + i);
+        }
+      } else {
+        // all of the last tile's MMAs are done: each warp waited for its last step
+        put_v(p, t, rows, v_hi, v_lo, kJoin);
+        fence_async();
+      }
+      if (!barrier_all(1, kJoin + 32, ok)) {
+        ok = false;
+        break;
+      }
+      if (warp == kJoinWarps) {
+        if (lane == 0) {
+          for (int s = s0; s < s1 && ok; ++s, ++it) {
+            ok = wait_ring(ctl.loaded, it, p.b_bufs) && (it < 2 || wait(ctl.read, it - 2));
+            if (!ok) break;
+            tmem_fence_after();
+            const uint32_t b = b_at + it % uint32_t(p.b_bufs) * b_bytes, d = ctl.tmem_base + (it & 1u) * kBn;
+            for (int part = 0; part < 2; ++part)
+              for (int k16 = 0; k16 < p.rp / 16; ++k16) {
+                const uint64_t ad = make_sdesc((part ? v_lo : v_hi) + uint32_t(k16 >> 2) * kXBytes) + uint64_t((k16 & 3) * 2);
+                const uint64_t bd = make_sdesc(b + uint32_t(k16 >> 2) * (kBn * 128u)) + uint64_t((k16 & 3) * 2);
+                mma_bf16(d, ad, bd, idesc_of(kBn), part != 0 || k16 != 0);
+              }
+            mma_commit<false>(smem_u32(&ctl.done[it & 1u]));
+            // B as far ahead as there are buffers: the next to fill is that of the step before this one
+            const int ahead = s + p.b_bufs - 1;
+            if (ahead < s1) {
+              if (s > s0) ok = wait(ctl.done, it - 1);
+              if (ok) fill(ahead, it + p.b_bufs - 1);
             }
-          mma_commit<false>(smem_u32(&ctl.done[it & 1u]));
-          if (s + 1 < s1) {
-            if (it >= 1) ok = wait(ctl.done, it - 1);
-            if (ok) fill(s + 1, it + 1);
           }
         }
+        it = __shfl_sync(0xffffffffu, it, 0);
+        ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+        continue;
       }
-      it = __shfl_sync(0xffffffffu, it, 0);
-      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
-      continue;
-    }
-    const int quarter = warp & 3, half = warp >> 2;
-    constexpr int kPieces = kBn / 2 / 16;  // of sixteen columns, of a warp
-    const int token = token_of[quarter * 32 + lane];
-    const uint16_t* y = g.y + (token >= 0 ? token * g.ldy : 0);
-    uint16_t* out = g.out + (token >= 0 ? token * g.ldo : 0);
-    const float scale = g.scales ? g.scales[t.expert] : 1.0f;
-    Sixteen yv[kPieces];
-    int col = s0 * kBn + half * (kBn / 2);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (token >= 0 && col + i * 16 < N) yv[i] = load16<kAlign>(y + col + i * 16);
-    for (int s = s0; s < s1; ++s, ++it, col += kBn) {
-      ok = __all_sync(0xffffffffu, ok && wait(ctl.done, it));
-      if (!ok) break;
-      tmem_fence_after();
-      const uint32_t from = ctl.tmem_base + (it & 1u) * kBn + (uint32_t(quarter * 32) << 16) + half * (kBn / 2);
-#pragma unroll
-      for (int h = 0; h < kPieces / 2; ++h) {
+      const int row = (warp & 3) * 32 + lane, group = warp >> 2;  // columns [32 group, 32 group + 32)
+      const float scale = g.scales ? g.scales[t.expert] : 1.0f;
+      for (int s = s0; s < s1; ++s, ++it) {
+        ok = ok && wait(ctl.done, it);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        tmem_fence_after();
         uint32_t f[32];
-        tmem_ld32(from + h * 32, f);
-        if (h == kPieces / 2 - 1) {  // the sums have been read: the buffer is free before they are joined
-          tmem_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl.read[it & 1u]));
-        }
+        tmem_ld32(ctl.tmem_base + (it & 1u) * kBn + (uint32_t((warp & 3) * 32) << 16) + group * 32, f);
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.read[it & 1u]));
+        if (!(ok = __all_sync(0xffffffffu, wait_ring(ctl.y_in, it, p.slots)))) break;
+        const uint32_t slot = it % uint32_t(p.slots);
+        const uint32_t at = slots_at + slot * kSlotBytes + uint32_t(row) * kPitch + uint32_t(group) * 64u;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int i = 2 * h + q;
-          Sixteen o;
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = lds128(at + i * 16);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            o.w[j] = cvt_bf16x2(fmaf(scale, __uint_as_float(f[q * 16 + 2 * j]), bf16_lo(yv[i].w[j])),
-                                fmaf(scale, __uint_as_float(f[q * 16 + 2 * j + 1]), bf16_hi(yv[i].w[j])));
-          const int n = col + i * 16;
-          // y of the next step is under way from here on
-          if (token >= 0 && s + 1 < s1 && n + kBn < N) yv[i] = load16<kAlign>(y + n + kBn);
-          if (token >= 0 && n < N) store16<kAlign>(out + n, o);
+          for (int j = 0; j < 4; ++j)
+            o[j] = cvt_bf16x2(fmaf(scale, __uint_as_float(f[8 * i + 2 * j]), bf16_lo(w[j])),
+                              fmaf(scale, __uint_as_float(f[8 * i + 2 * j + 1]), bf16_hi(w[j])));
+          sts128(at + i * 16, make_uint4(o[0], o[1], o[2], o[3]));
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.y_out[slot]));
       }
     }
+    if (!ok && threadIdx.x == kJoin)  // nothing of a load may land after the CTA has left
+      for (uint32_t i = it; i < it + uint32_t(p.b_bufs); ++i)
+        mbar_wait_bounded(smem_u32(&ctl.loaded[i % uint32_t(p.b_bufs)]), (i / uint32_t(p.b_bufs)) & 1u, nullptr, &g_lora_error);
   }
-  if (!ok) {  // nothing of a load may land after the CTA has left
-    if (threadIdx.x == kTileThreads)
-      for (int i = 0; i < 2; ++i) mbar_wait_bounded(smem_u32(&ctl.loaded[(it + i) & 1u]), ((it + i) >> 1) & 1u, nullptr, &g_lora_error);
-  }
+  __syncwarp();
   tile_end(&ctl, p.tmem_cols);
 }
 
@@ -790,16 +851,18 @@ bool launch_expand_any(TileParams p, int num_sms, cudaStream_t st) {
                 dim3(kTileThreads), smem, st, true, dim3(1, 1, 1), p) == FP8_OK;
 }
 
-template <int kBn, int kAlign>
+template <int kBn>
 bool launch_expand(TileParams p, const CUtensorMap& map_b, int num_sms, cudaStream_t st) {
-  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn, kAlign>))) return false;
+  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn>))) return false;
   const int rk = (p.rp + kBk - 1) / kBk;
-  const size_t smem = 1024 + size_t(rk) * (2 * kXBytes + 2 * kBn * 128);
-  const int per_sm = smem <= 112 * 1024 ? 2 : 1;
+  const size_t v = size_t(rk) * 2 * kXBytes, buf = size_t(rk) * kBn * 128, slot = size_t(kTileRows) * (kBn * 2 + 16);
+  const size_t room = 232448 - 1024 - 1024 - v;  // (the control block and the alignment)
+  p.b_bufs = room >= 4 * (buf + slot) ? 4 : 3;
+  p.slots = int(std::min<size_t>(4, (room - p.b_bufs * buf) / slot));
   const int64_t units = p.s.max_tiles * ((p.a.N + kBn - 1) / kBn);
   p.tmem_cols = 2 * kBn;
-  return launch(expand_kernel<kBn, kAlign>, dim3(unsigned(std::min<int64_t>(units, int64_t(per_sm) * num_sms))),
-                dim3(kExpandThreads), smem, st, true, dim3(1, 1, 1), map_b, p) == FP8_OK;
+  return launch(expand_kernel<kBn>, dim3(unsigned(std::min<int64_t>(units, num_sms))), dim3(expand_threads(kBn)),
+                1024 + v + size_t(p.b_bufs) * buf + size_t(p.slots) * slot, st, true, dim3(1, 1, 1), map_b, p) == FP8_OK;
 }
 
 bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st) {
@@ -823,22 +886,16 @@ bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st)
   if ((p.vec_a && !make_fp8_tensor_map_3d(&map_a, reinterpret_cast<const uint8_t*>(a.a), a.adapters, a.rank, a.K * 2,
                                           a.K * 2, uint32_t(p.rp))) ||
       (p.vec_b && !make_fp8_tensor_map_3d(&map_b, reinterpret_cast<const uint8_t*>(a.b), a.adapters, a.N,
-                                          int64_t(a.rank) * 2, int64_t(a.rank) * 2, p.rp <= 2 * kBk ? 128 : 64)))
+                                          int64_t(a.rank) * 2, int64_t(a.rank) * 2, p.rp <= kBk ? 128 : p.rp <= 3 * kBk ? 64 : 32)))
     return false;
   if (launch(shrink_kernel, dim3(unsigned(s.max_tiles), unsigned(s.splits)), dim3(kTileThreads),
              size_t(p.stages) * stage_bytes + 1024, st, true, dim3(1, 1, 1), map_a, p) != FP8_OK)
     return false;
-  auto rows_on = [&](int bytes) {
-    return aligned(a.y, bytes) && aligned(a.out, bytes) && (a.M <= 1 || (a.ldy * 2 % bytes == 0 && a.ldo * 2 % bytes == 0));
-  };
-  const int on = p.vec_b && a.N % 16 == 0 ? (rows_on(32) ? 32 : rows_on(16) ? 16 : 0) : 0;
-  if (p.rp <= 2 * kBk)
-    return on == 32   ? launch_expand<128, 32>(p, map_b, num_sms, st)
-           : on == 16 ? launch_expand<128, 16>(p, map_b, num_sms, st)
-                      : launch_expand_any<128>(p, num_sms, st);
-  return on == 32   ? launch_expand<64, 32>(p, map_b, num_sms, st)
-         : on == 16 ? launch_expand<64, 16>(p, map_b, num_sms, st)
-                    : launch_expand_any<64>(p, num_sms, st);
+  if (p.vec_y && p.vec_b && a.N % 8 == 0) {
+    if (p.rp <= kBk) return launch_expand<128>(p, map_b, num_sms, st);
+    return p.rp <= 3 * kBk ? launch_expand<64>(p, map_b, num_sms, st) : launch_expand<32>(p, map_b, num_sms, st);
+  }
+  return p.rp <= 2 * kBk ? launch_expand_any<128>(p, num_sms, st) : launch_expand_any<64>(p, num_sms, st);
 }
 
 unsigned int read_and_clear_error() {
