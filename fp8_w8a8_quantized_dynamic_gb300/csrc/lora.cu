@@ -205,6 +205,7 @@ constexpr int kTileThreads = 256;
 constexpr int kBk = 64;                     // bf16 values of K in a 128-byte swizzled row
 constexpr uint32_t kXBytes = kTileRows * 128;
 constexpr int kShrinkMaxStages = 6;
+constexpr int kShrinkThreads = kTileThreads + 32;
 
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
@@ -285,7 +286,8 @@ struct TileParams {
   uint32_t tmem_cols;
 };
 
-constexpr int kCopyThreads = 128;  // expand: those that copy y and out
+constexpr int kCopyThreads = 256;  // expand: those that copy y and out
+constexpr int kCopyRows = kTileRows / (kCopyThreads / 32);  // of a warp
 
 struct TileCtl {
   uint64_t done[8];    // MMAs of a stage (shrink), of a step (expand)
@@ -300,12 +302,12 @@ __device__ __forceinline__ uint32_t align1024(uint32_t a) { return (a + 1023u) &
 
 // The start and end that both kernels share: barriers and tensor memory. The trigger for the next kernel comes after the
 // tensor memory is held, so that no CTA of a later kernel can hold it while one of this kernel waits for it.
-// (warps: those that join sums with y)
-__device__ __forceinline__ void tile_begin(TileCtl* ctl, uint32_t cols, int warps) {
+// (loads: arrivals on a load's barrier; warps: those that join sums with y)
+__device__ __forceinline__ void tile_begin(TileCtl* ctl, uint32_t cols, int loads, int warps) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_u32(&ctl->done[i]), 1);
-      mbar_init(smem_u32(&ctl->loaded[i]), 1);
+      mbar_init(smem_u32(&ctl->loaded[i]), uint32_t(loads));
     }
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctl->read[i]), uint32_t(warps));
     for (int i = 0; i < 4; ++i) {
@@ -336,14 +338,17 @@ __device__ __forceinline__ void tile_end(TileCtl* ctl, uint32_t cols) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(ctl->tmem_base), "r"(cols) : "memory");
 }
 
-// v[split][row] = A[e] x[row's token] over the split's K, for a tile's rows.
-__global__ void __launch_bounds__(kTileThreads)
+// v[split][row] = A[e] x[row's token] over the split's K, for a tile's rows. Warps 0 to 7 copy the tile's rows of x (any
+// tokens: eight threads a 128-byte piece of a row, asynchronous 16-byte copies) and, by TMA, A's into a ring of stages, whose
+// barrier counts the copies' completion; warp 8 issues the MMAs. (With a fence for the tensor core in the copying
+// threads, which waits for their copies in flight, a step took a load's latency: 27 us for 8192 x 4096 at rank 64.)
+__global__ void __launch_bounds__(kShrinkThreads)
 shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ TileParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ TileCtl ctl;
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tile_begin(&ctl, p.tmem_cols, kTileThreads / 32);
+  tile_begin(&ctl, p.tmem_cols, kTileThreads + 1, 1);
   const int tile = blockIdx.x;
   const Args& g = p.a;
   const int K = int(g.K), r = g.rank;
@@ -353,73 +358,74 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
     if (t.expert < g.adapters && steps > 0) {
       const int rows = min(kTileRows, t.row_end - t.row0);
       const uint32_t stage_bytes = kXBytes + uint32_t(p.rp) * 128u;
-      // eight threads a row; this thread's rows of x
-      const int piece = threadIdx.x & 7, first = threadIdx.x >> 3;
-      const uint16_t* x[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = first + 32 * i;
-        x[i] = row < rows ? g.x + int64_t(p.s.order[t.row0 + row]) * g.ldx : g.x;
-      }
-      const uint16_t* A = g.a + int64_t(t.expert) * r * K;
-      auto fill = [&](int step) {
-        const uint32_t st = base + uint32_t(step % p.stages) * stage_bytes;
-        const int k = (kb0 + step) * kBk + piece * 8;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          copy8(st + swizzled(first + 32 * i, piece), x[i], first + 32 * i < rows, k, K, p.vec_x);
-        if (p.vec_a) {
-          if (threadIdx.x == 0) {
-            const uint32_t bar = smem_u32(&ctl.loaded[step % p.stages]);
-            mbar_arrive_expect_tx(bar, uint32_t(p.rp) * 128u);
-            tma_load_3d(st + kXBytes, &tmap_a, bar, (kb0 + step) * 128, 0, t.expert);
-          }
-          return;
-        }
-        for (int row = first; row < p.rp; row += 32)
-          copy8(st + kXBytes + swizzled(row, piece), A + int64_t(min(row, r - 1)) * K, row < r, k, K, 0);
-      };
-      auto wait = [&](int step) {
-        return mbar_wait_short(smem_u32(&ctl.done[step % p.stages]), uint32_t(step / p.stages) & 1u, &ctl.abort_flag,
+      auto wait = [&](uint64_t* bars, int step) {
+        return mbar_wait_short(smem_u32(bars + step % p.stages), uint32_t(step / p.stages) & 1u, &ctl.abort_flag,
                                &g_lora_error);
       };
-      const int ahead = p.stages - 1;
-      for (int i = 0; i < ahead; ++i) {
-        if (i < steps) fill(i);
-        cp_commit();
-      }
       bool ok = true;
-      for (int i = 0; i < steps; ++i) {
-        if (i >= 1) ok = wait(i - 1);  // its stage is filled again
-        if (ok && i + ahead < steps) fill(i + ahead);
-        cp_commit();
-        // the copies of step i have landed
-        if (ahead == 2) cp_wait<2>();
-        else if (ahead == 3) cp_wait<3>();
-        else if (ahead == 4) cp_wait<4>();
-        else cp_wait<5>();
-        fence_async();
-        if (!__syncthreads_and(ok)) break;
-        if (threadIdx.x == 0) {
-          if (p.vec_a && !mbar_wait_short(smem_u32(&ctl.loaded[i % p.stages]), uint32_t(i / p.stages) & 1u, &ctl.abort_flag,
-                                          &g_lora_error))
-            continue;  // the wait for this step's MMAs gives up as well
-          const uint32_t st = base + uint32_t(i % p.stages) * stage_bytes;
-          const uint64_t ad = make_sdesc(st), bd = make_sdesc(st + kXBytes);
+      int filled = 0;
+      if (warp == kTileThreads / 32) {
+        if (lane == 0) {
+          for (int i = 0; i < steps; ++i) {
+            if (!(ok = wait(ctl.loaded, i))) break;
+            fence_async();  // what the copying threads wrote becomes visible to the tensor core
+            tmem_fence_after();
+            const uint32_t st = base + uint32_t(i % p.stages) * stage_bytes;
+            const uint64_t ad = make_sdesc(st), bd = make_sdesc(st + kXBytes);
 #pragma unroll
-          for (int kk = 0; kk < kBk / 16; ++kk)
-            mma_bf16(ctl.tmem_base, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc_of(p.rp), i != 0 || kk != 0);
-          mma_commit<false>(smem_u32(&ctl.done[i % p.stages]));
+            for (int kk = 0; kk < kBk / 16; ++kk)
+              mma_bf16(ctl.tmem_base, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc_of(p.rp), i != 0 || kk != 0);
+            mma_commit<false>(smem_u32(&ctl.done[i % p.stages]));
+          }
+        }
+        __syncwarp();
+      } else {
+        // eight threads a row; this thread's rows of x
+        const int piece = threadIdx.x & 7, first = threadIdx.x >> 3;
+        const bool whole = p.vec_x && p.vec_a;
+        const uint16_t* x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = first + 32 * i;
+          x[i] = row < rows ? g.x + int64_t(p.s.order[t.row0 + row]) * g.ldx : g.x;
+        }
+        const uint16_t* A = g.a + int64_t(t.expert) * r * K;
+        for (; filled < steps; ++filled) {
+          if (filled >= p.stages && !(ok = wait(ctl.done, filled - p.stages))) break;
+          const uint32_t st = base + uint32_t(filled % p.stages) * stage_bytes;
+          const uint32_t bar = smem_u32(&ctl.loaded[filled % p.stages]);
+          if (threadIdx.x == 0) {
+            if (p.vec_a) {
+              mbar_arrive_expect_tx(bar, uint32_t(p.rp) * 128u);
+              tma_load_3d(st + kXBytes, &tmap_a, bar, (kb0 + filled) * 128, 0, t.expert);
+            } else {
+              mbar_arrive(bar);
+            }
+          }
+          const int k = (kb0 + filled) * kBk + piece * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            copy8(st + swizzled(first + 32 * i, piece), x[i], first + 32 * i < rows, k, K, p.vec_x);
+          if (whole) {
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
+          } else {
+            if (!p.vec_a)
+              for (int row = first; row < p.rp; row += 32)
+                copy8(st + kXBytes + swizzled(row, piece), A + int64_t(min(row, r - 1)) * K, row < r, k, K, 0);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async();
+            mbar_arrive(bar);
+          }
         }
       }
-      if (ok) ok = wait(steps - 1);
+      if (ok) ok = wait(ctl.done, steps - 1);
       if (__syncthreads_and(ok)) {
         tmem_fence_after();
         // four warps hold the tile's rows, the other four the second half of the columns
         const int row = (warp & 3) * 32 + lane;
         float* dst = p.s.v + (int64_t(blockIdx.y) * g.M + t.row0 + row) * p.rp;
         const uint32_t from = ctl.tmem_base + (uint32_t((warp & 3) * 32) << 16);
-        for (int c = (warp >> 2) * 32; c < p.rp; c += 64) {
+        for (int c = (warp >> 2) * 32; warp < kTileThreads / 32 && c < p.rp; c += 64) {
           uint32_t f[32];
           tmem_ld32(from + c, f);
           if (row < rows) {
@@ -429,6 +435,9 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
                 *reinterpret_cast<uint4*>(dst + c + 4 * q) = make_uint4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
           }
         }
+      } else if (threadIdx.x == 0) {  // nothing of a load may land after the CTA has left
+        for (int i = max(0, filled - p.stages); i < filled; ++i)
+          mbar_wait_bounded(smem_u32(&ctl.loaded[i % p.stages]), uint32_t(i / p.stages) & 1u, nullptr, &g_lora_error);
       }
     }
   }
@@ -487,7 +496,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
   __shared__ __align__(16) float staged[kTileThreads / 32][32 * kStagePitch];
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tile_begin(&ctl, p.tmem_cols, kTileThreads / 32);
+  tile_begin(&ctl, p.tmem_cols, 1, kTileThreads / 32);
   const Args& g = p.a;
   const int N = int(g.N), r = g.rank;
   const int tile = blockIdx.x;
@@ -613,7 +622,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
 //   joining warps  32 rows and 32 columns each: a thread reads its row of a step's sums from tensor memory, joins it with y in
 //                  a slot of shared memory and writes the result over y there.
 //   issuing warp   loads B by TMA, two or three steps ahead, and issues the MMAs.
-//   copying warps  y into the slots, by asynchronous 16-byte copies as far ahead as there are slots, and out from them: 32
+//   copying warps  y into the slots, by asynchronous 16-byte copies as far ahead as there are slots, and out from them: 16
 //                  rows each, whole lines at a time (the rows of a tile may be any tokens).
 // What was measured for 8192 x 14336: rows loaded and stored by the joining threads, 32 bytes of a row at a time, 111 us
 // (each asks the L2 for a single sector); a bulk copy of 256 bytes a row each way 470 us (some 60 cycles a copy).
@@ -630,7 +639,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
   __shared__ TileCtl ctl;
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tile_begin(&ctl, p.tmem_cols, kJoinWarps);
+  tile_begin(&ctl, p.tmem_cols, 1, kJoinWarps);
   const Args& g = p.a;
   const int N = int(g.N);
   const int steps = (N + kBn - 1) / kBn;
@@ -648,9 +657,10 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
   };
 
   if (warp > kJoinWarps) {
-    // ---------------- copies of y and out: 32 rows a warp, lane l knows the token of the l-th ----------------
+    // ---------------- copies of y and out: kCopyRows rows a warp, lane l knows the token of the l-th ----------------
     constexpr int kLanes = kBn / 8, kRowsAt = 32 / kLanes;  // lanes of a row, rows at a time
-    const int first = (warp - kJoinWarps - 1) * 32, at_row = lane / kLanes, at_col = (lane % kLanes) * 8;
+    constexpr int kTimes = kCopyRows / kRowsAt, kBatch = kTimes < 4 ? kTimes : 4;
+    const int first = (warp - kJoinWarps - 1) * kCopyRows, at_row = lane / kLanes, at_col = (lane % kLanes) * 8;
     struct Walk {
       int64_t u;      // the step after this part of a tile
       int s, s1;      // columns of the next step, and where the part ends
@@ -664,7 +674,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         w.u += w.s1 - w.s;
         const block::RowTile t = p.s.tiles[tile];
         if (t.expert >= g.adapters) continue;
-        w.token = first + lane < min(kTileRows, t.row_end - t.row0) ? p.s.order[t.row0 + first + lane] : -1;
+        w.token = lane < kCopyRows && first + lane < min(kTileRows, t.row_end - t.row0) ? p.s.order[t.row0 + first + lane] : -1;
         return true;
       }
       return false;
@@ -678,7 +688,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         const uint32_t slot = n_in % uint32_t(p.slots), to = mine + slot * kSlotBytes;
         const int col = in.s * kBn + at_col;
 #pragma unroll
-        for (int i = 0; i < kLanes; ++i) {
+        for (int i = 0; i < kTimes; ++i) {
           const int token = __shfl_sync(0xffffffffu, in.token, i * kRowsAt + at_row);
           if (token >= 0 && col < N)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
@@ -692,12 +702,12 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       const uint32_t from = mine + (n_out % uint32_t(p.slots)) * kSlotBytes;
       const int col = out.s * kBn + at_col;
 #pragma unroll
-      for (int i0 = 0; i0 < kLanes; i0 += 4) {
-        uint4 v[4];
+      for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
+        uint4 v[kBatch];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = lds128(from + uint32_t((i0 + i) * kRowsAt) * kPitch);
+        for (int i = 0; i < kBatch; ++i) v[i] = lds128(from + uint32_t((i0 + i) * kRowsAt) * kPitch);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kBatch; ++i) {
           const int token = __shfl_sync(0xffffffffu, out.token, (i0 + i) * kRowsAt + at_row);
           if (token >= 0 && col < N) *reinterpret_cast<uint4*>(g.out + token * g.ldo + col) = v[i];
         }
@@ -888,7 +898,7 @@ bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st)
       (p.vec_b && !make_fp8_tensor_map_3d(&map_b, reinterpret_cast<const uint8_t*>(a.b), a.adapters, a.N,
                                           int64_t(a.rank) * 2, int64_t(a.rank) * 2, p.rp <= kBk ? 128 : p.rp <= 3 * kBk ? 64 : 32)))
     return false;
-  if (launch(shrink_kernel, dim3(unsigned(s.max_tiles), unsigned(s.splits)), dim3(kTileThreads),
+  if (launch(shrink_kernel, dim3(unsigned(s.max_tiles), unsigned(s.splits)), dim3(kShrinkThreads),
              size_t(p.stages) * stage_bytes + 1024, st, true, dim3(1, 1, 1), map_a, p) != FP8_OK)
     return false;
   if (p.vec_y && p.vec_b && a.N % 8 == 0) {
