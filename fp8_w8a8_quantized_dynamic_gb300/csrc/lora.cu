@@ -55,10 +55,9 @@ __device__ __forceinline__ float dot8(uint4 v, const float (&f)[8], float sum) {
 }
 
 // Sums of kValues values over the kLanes lanes (a power of two) that share them: each halving step exchanges half of the
-// values, so that a lane ends with one of them, whose index is returned; past that all lanes add.
+// values, so that a lane ends with one of them in p[0], that of halving_index; past that all lanes add.
 template <int kLanes, int kValues>
-__device__ __forceinline__ int sum_halving(float (&p)[kValues], int lane) {
-  int mine = 0;
+__device__ __forceinline__ void sum_halving(float (&p)[kValues], int lane) {
   int left = kValues;
 #pragma unroll
   for (int m = kLanes / 2; m > 0; m >>= 1) {
@@ -73,9 +72,19 @@ __device__ __forceinline__ int sum_halving(float (&p)[kValues], int lane) {
           p[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
         }
       }
-      if (upper) mine += left;
     } else {
       p[0] += __shfl_xor_sync(0xffffffffu, p[0], m);
+    }
+  }
+}
+template <int kLanes, int kValues>
+__device__ __forceinline__ int halving_index(int lane) {
+  int mine = 0, left = kValues;
+#pragma unroll
+  for (int m = kLanes / 2; m > 0; m >>= 1) {
+    if (left > 1) {
+      left >>= 1;
+      mine += (lane & m) != 0 ? left : 0;
     }
   }
   return mine;
@@ -87,7 +96,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // kLpr lanes share a row of B (eight values of the rank each). Cluster rank c sums K slice c of v = A x
 // and sends it to all of the cluster; then every CTA adds the slices in order and computes its columns.
 template <int kLpr>
-__global__ void __launch_bounds__(kTokenThreads)
+__global__ void __launch_bounds__(kTokenThreads, 2)
 tokens_kernel(const __grid_constant__ TokenParams p) {
   constexpr int kU = kLpr < 8 ? kLpr : 8;      // loads of a batch; a lane ends with one column of it
   constexpr int kBatches = 8 / kU;             // batches in flight: eight loads a lane
@@ -117,8 +126,11 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   const uint16_t* A = g.a + int64_t(e) * r * K;
   const uint16_t* B = g.b + int64_t(e) * N * r;
   const int sub = lane % kLpr, row_in_load = lane / kLpr;
-  // the first loads of B are under way while v is summed
+  // the first loads of B and y are under way while v is summed
   uint4 bv[8];
+  uint16_t yv[kBatches];
+  const int my_u = halving_index<kLpr, kU>(lane);
+  auto col_of = [&](int base, int b) { return base + b * kBatchCols + my_u * kRowsPerLoad + row_in_load; };
   auto load_b = [&](int base) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
@@ -126,26 +138,40 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
       bv[q] = make_uint4(0, 0, 0, 0);
       if (n < n1 && sub * 8 < r) bv[q] = load8_bf16(B + int64_t(n) * r, sub * 8, r, p.vec_b);
     }
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b) yv[b] = col_of(base, b) < n1 ? y[col_of(base, b)] : uint16_t(0);
   };
   load_b(n0 + warp * kStepCols);
+  const float scale = g.scales ? g.scales[e] : 1.0f;
 
   const int k0 = min(K, rank * p.k_slice), k1 = min(K, k0 + p.k_slice);
   const uint16_t* x = g.x + m * g.ldx;
   cluster_wait();
-  for (int i0 = warp * 8; i0 < r; i0 += kTokenWarps * 8) {
-    float acc[8] = {};
-    for (int k = k0 + lane * 8; k < k1; k += 256) {
-      float f[8];
-      unpack8(load8_bf16(x, k, k1, p.vec_x), f);
+  const int per_warp = (r + kTokenWarps - 1) / kTokenWarps, i_end = min(r, (warp + 1) * per_warp);
+  for (int i0 = warp * per_warp; i0 < i_end; i0 += 4) {
+    float acc[4] = {};
+    for (int k = k0 + lane * 8; k < k1; k += 512) {  // two pieces of four rows at a time
+      uint4 xv[2], av[2][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i0 + i < r) acc[i] = dot8(load8_bf16(A + int64_t(i0 + i) * K, k, k1, p.vec_a), f, acc[i]);
+      for (int h = 0; h < 2; ++h) {
+        const int kh = k + 256 * h;
+        xv[h] = kh < k1 ? load8_bf16(x, kh, k1, p.vec_x) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          av[h][i] = kh < k1 && i0 + i < i_end ? load8_bf16(A + int64_t(i0 + i) * K, kh, k1, p.vec_a) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float f[8];
+        unpack8(xv[h], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = dot8(av[h][i], f, acc[i]);
+      }
     }
-    const int i = i0 + sum_halving<32, 8>(acc, lane);
-    // four lanes hold the sum: each sends it to two of the cluster's CTAs
-    const uint32_t at = smem_u32(&part[rank][i]);
-#pragma unroll
-    for (int c = 0; c < kCluster; c += 4) st_cluster_u32(map_to_rank(at, c + (lane & 3)), __float_as_uint(acc[0]));
+    // eight lanes end with the sum of a row: each sends it to one of the cluster's CTAs
+    const int i = i0 + halving_index<32, 4>(lane);
+    sum_halving<32, 4>(acc, lane);
+    if (i < i_end) st_cluster_u32(map_to_rank(smem_u32(&part[rank][i]), lane & 7), __float_as_uint(acc[0]));
   }
   pair_sync();
   for (int i = threadIdx.x; i < kMaxRank; i += kTokenThreads) {
@@ -158,18 +184,19 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   float f[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = v[sub * 8 + j];
-  const float scale = g.scales ? g.scales[e] : 1.0f;
   for (int base = n0 + warp * kStepCols; base < n1; base += kTokenWarps * kStepCols) {
-    float sum[kBatches][kU];
+    float sum[kBatches][kU], was[kBatches];
 #pragma unroll
     for (int q = 0; q < 8; ++q) sum[q / kU][q % kU] = dot8(bv[q], f, 0.0f);
+#pragma unroll
+    for (int b = 0; b < kBatches; ++b) was[b] = bf16_bits_to_float(yv[b]);
     if (base + kTokenWarps * kStepCols < n1) load_b(base + kTokenWarps * kStepCols);
 #pragma unroll
     for (int b = 0; b < kBatches; ++b) {
-      const int u = sum_halving<kLpr, kU>(sum[b], lane);
-      const int n = base + b * kBatchCols + u * kRowsPerLoad + row_in_load;
+      sum_halving<kLpr, kU>(sum[b], lane);
+      const int n = col_of(base, b);
       if (n < n1 && (sub & (kLpr / kU - 1)) == 0)
-        out[n] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(scale, sum[b][0], bf16_bits_to_float(y[n]))));
+        out[n] = __bfloat16_as_ushort(__float2bfloat16_rn(fmaf(scale, sum[b][0], was[b])));
     }
   }
 }
