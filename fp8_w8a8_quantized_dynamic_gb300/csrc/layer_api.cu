@@ -22,9 +22,9 @@ int rows_vec(const void* p, int64_t rows, int64_t ld) { return aligned(p, 16) &&
 
 PerDeviceCache<const void*, int> g_norm_ctas;
 
-template <int kThreads, int kUnits, bool kPost, bool kGate>
+template <int kThreads, int kUnits, bool kPost, bool kGate, bool kVec>
 fp8_status launch_norm_of(const norm::Params& p, int sms, cudaStream_t st) {
-  auto kernel = norm::residual_norm_kernel<kThreads, kUnits, kPost, kGate>;
+  auto kernel = norm::residual_norm_kernel<kThreads, kUnits, kPost, kGate, kVec>;
   int dev = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FP8_ERR_CUDA;
   if (p.rows > sms &&  // (fewer: one CTA each)
@@ -37,24 +37,30 @@ fp8_status launch_norm_of(const norm::Params& p, int sms, cudaStream_t st) {
   const int64_t grid = std::min<int64_t>(p.rows, int64_t(sms) * std::max(per_sm, 1));
   return launch(kernel, dim3(unsigned(grid)), dim3(kThreads), 0, st, true, dim3(1, 1, 1), p);
 }
-template <int kThreads, int kUnits>
+template <int kThreads, int kUnits, bool kVec>
 fp8_status launch_norm(const norm::Params& p, int sms, cudaStream_t st) {
   if (p.post_w)
-    return p.gate ? launch_norm_of<kThreads, kUnits, true, true>(p, sms, st)
-                  : launch_norm_of<kThreads, kUnits, true, false>(p, sms, st);
-  return p.gate ? launch_norm_of<kThreads, kUnits, false, true>(p, sms, st)
-                : launch_norm_of<kThreads, kUnits, false, false>(p, sms, st);
+    return p.gate ? launch_norm_of<kThreads, kUnits, true, true, kVec>(p, sms, st)
+                  : launch_norm_of<kThreads, kUnits, true, false, kVec>(p, sms, st);
+  return p.gate ? launch_norm_of<kThreads, kUnits, false, true, kVec>(p, sms, st)
+                : launch_norm_of<kThreads, kUnits, false, false, kVec>(p, sms, st);
 }
 
-// Threads of a row.
+// Threads of a row: few rows take as many as there are, many as few as hold one.
 fp8_status launch_norm_any(const norm::Params& p, int sms, cudaStream_t st) {
   const int units = (p.cols + 15) / 16 * 2;  // of eight columns; the codes' rows are whole sixteens
-  if (units <= 128) return launch_norm<128, 1>(p, sms, st);
-  if (units <= 256) return launch_norm<256, 1>(p, sms, st);
-  if (units <= 512) return p.rows <= sms ? launch_norm<512, 1>(p, sms, st) : launch_norm<256, 2>(p, sms, st);
-  if (units <= 1024) return p.rows <= sms ? launch_norm<1024, 1>(p, sms, st) : launch_norm<256, 4>(p, sms, st);
-  if (units <= 2048) return p.rows <= sms ? launch_norm<1024, 2>(p, sms, st) : launch_norm<512, 4>(p, sms, st);
-  return launch_norm<1024, 4>(p, sms, st);
+  const bool few = p.rows <= sms;
+  if (!p.vec) {
+    if (units <= 256) return launch_norm<256, 1, false>(p, sms, st);
+    if (units <= 1024) return launch_norm<512, 2, false>(p, sms, st);
+    return launch_norm<1024, 4, false>(p, sms, st);
+  }
+  if (units <= 128) return launch_norm<128, 1, true>(p, sms, st);
+  if (units <= 256) return launch_norm<256, 1, true>(p, sms, st);
+  if (units <= 512) return few ? launch_norm<512, 1, true>(p, sms, st) : launch_norm<256, 2, true>(p, sms, st);
+  if (units <= 1024) return few ? launch_norm<1024, 1, true>(p, sms, st) : launch_norm<256, 4, true>(p, sms, st);
+  if (units <= 2048) return few ? launch_norm<1024, 2, true>(p, sms, st) : launch_norm<512, 4, true>(p, sms, st);
+  return launch_norm<1024, 4, true>(p, sms, st);
 }
 
 // What both calls share, up to r.
@@ -75,23 +81,19 @@ fp8_status fill_norm(norm::Params& p, const void* y, int64_t M, int64_t H, int64
   p.cols = int(H);
   p.y = static_cast<const uint16_t*>(y);
   p.ldy = ldy;
-  p.vec_y = rows_vec(y, M, ldy);
   p.post_w = static_cast<const uint16_t*>(post_w);
-  p.vec_post = aligned(post_w, 16);
   p.gate = static_cast<const uint16_t*>(gate);
   p.ldg = ldg;
-  p.vec_gate = rows_vec(gate, M, ldg);
   p.residual = static_cast<const uint16_t*>(residual);
   p.ldr = ldr;
-  p.vec_res = rows_vec(residual, M, ldr);
   p.w = static_cast<const uint16_t*>(w);
-  p.vec_w = aligned(w, 16);
   p.scale = scale;
   p.eps = eps;
   p.w_offset = plus_one ? 1.0f : 0.0f;
   p.r = static_cast<uint16_t*>(r);
   p.ldro = ldro;
-  p.vec_r = rows_vec(r, M, ldro);
+  p.vec = H % 8 == 0 && aligned(post_w, 16) && aligned(w, 16) && rows_vec(y, M, ldy) && rows_vec(gate, M, ldg) &&
+          rows_vec(residual, M, ldr) && rows_vec(r, M, ldro);
   return FP8_OK;
 }
 
@@ -105,18 +107,25 @@ bool lora_sizes_ok(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
          L <= kMaxAdapters && r >= 1 && r <= lora::kMaxRank;
 }
 
-// Few tokens: one launch, a cluster a token.
-bool lora_by_token(int64_t M) { return M <= 64; }
+// A cluster a token, or rows sorted by adapter: by the estimated time in us. A token takes 0.06 and its adapter's w MB at
+// 8.5 MB/us; the sorted form 16 and its adapters (between one and min(L, M): half) at 2.2. Measured, by token and sorted
+// (tokens of 32 adapters drawn at random; of one): K 4096 N 4096 r 64, 64 tokens 11 and 32; 18, 128 tokens 20 and 33; 23, 256
+// tokens 37 and 32; 23. r 16: 128 tokens 10 and 29; 17, 256 tokens 18 and 30; 17. N 14336 r 64: 64 tokens 22 and 49; 18, 128
+// tokens 41 and 58; 23. K 8192 N 8192 r 128: 64 tokens 39 and 71; 26, 128 tokens 71 and 76; 34.
+bool lora_by_token(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
+  const double w = 2e-6 * double(r) * double(K + N);
+  return M <= 512 && double(M) * (0.058 + w / 8.5) <= 16.0 + double(std::min(L, M)) * w / 4.4;
+}
 
 struct LoraWs {
   size_t n_tiles, tiles, counts, pos, order, v, total;
   int64_t max_tiles;
   int splits;
 };
-LoraWs lora_ws(int64_t M, int64_t K, int64_t L, int64_t r) {
+LoraWs lora_ws(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
   Carver c;
   LoraWs w = {};
-  if (lora_by_token(M)) return w;
+  if (lora_by_token(M, K, N, L, r)) return w;
   w.max_tiles = M / block::kRowTile + std::min(L + 1, M);
   w.splits = lora::splits_of(M, K, L);
   w.n_tiles = c.take(4);
@@ -145,7 +154,7 @@ FP8_API fp8_status fp8_residual_norm(const void* y_bf16, int64_t M, int64_t H, i
   p.pre = n_bf16 != nullptr;
   p.n = static_cast<uint16_t*>(n_bf16);
   p.ldn = ldn;
-  p.vec_n = rows_vec(n_bf16, M, ldn);
+  p.vec = p.vec && rows_vec(n_bf16, M, ldn);
   int sms = 0;
   FP8_TRY(current_device(&sms));
   return launch_norm_any(p, sms, reinterpret_cast<cudaStream_t>(stream));
@@ -176,7 +185,7 @@ FP8_API fp8_status fp8_residual_norm_quantize(const void* y_bf16, int64_t M, int
 
 FP8_API size_t fp8_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
   if (!lora_sizes_ok(M, K, N, L, r) || M == 0 || K == 0 || N == 0 || L == 0) return 0;
-  return lora_ws(M, K, L, r).total;
+  return lora_ws(M, K, N, L, r).total;
 }
 
 FP8_API fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_t ldy, const void* x_bf16, int64_t K,
@@ -220,8 +229,8 @@ FP8_API fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_
   p.scales = scales;
   p.out = static_cast<uint16_t*>(out_bf16);
   p.ldo = ldo;
-  if (lora_by_token(M)) return lora::launch_tokens(p, sms, st) ? FP8_OK : FP8_ERR_CUDA;
-  const LoraWs w = lora_ws(M, K, L, r);
+  if (lora_by_token(M, K, N, L, r)) return lora::launch_tokens(p, sms, st) ? FP8_OK : FP8_ERR_CUDA;
+  const LoraWs w = lora_ws(M, K, N, L, r);
   uint8_t* base = static_cast<uint8_t*>(ws);
   lora::Sorted s = {};
   block::RowTile* tiles = reinterpret_cast<block::RowTile*>(base + w.tiles);

@@ -95,11 +95,12 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // kLpr lanes share a row of B (eight values of the rank each). Cluster rank c sums K slice c of v = A x
 // and sends it to all of the cluster; then every CTA adds the slices in order and computes its columns.
-template <int kLpr>
-__global__ void __launch_bounds__(kTokenThreads, 2)
+template <int kLpr, int kLoads>
+__global__ void __launch_bounds__(kTokenThreads, kLoads == 8 ? 2 : 4)
 tokens_kernel(const __grid_constant__ TokenParams p) {
-  constexpr int kU = kLpr < 8 ? kLpr : 8;      // loads of a batch; a lane ends with one column of it
-  constexpr int kBatches = 8 / kU;             // batches in flight: eight loads a lane
+  constexpr int kU = kLpr < kLoads ? kLpr : kLoads;  // loads of a batch; a lane ends with one column of it
+  constexpr int kBatches = kLoads / kU;              // batches in flight
+  constexpr int kHalves = kLoads / 4;                // pieces of A's rows in flight
   constexpr int kRowsPerLoad = 32 / kLpr;
   constexpr int kBatchCols = kU * kRowsPerLoad;
   constexpr int kStepCols = kBatches * kBatchCols;  // of a warp
@@ -127,13 +128,13 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   const uint16_t* B = g.b + int64_t(e) * N * r;
   const int sub = lane % kLpr, row_in_load = lane / kLpr;
   // the first loads of B and y are under way while v is summed
-  uint4 bv[8];
+  uint4 bv[kLoads];
   uint16_t yv[kBatches];
   const int my_u = halving_index<kLpr, kU>(lane);
   auto col_of = [&](int base, int b) { return base + b * kBatchCols + my_u * kRowsPerLoad + row_in_load; };
   auto load_b = [&](int base) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kLoads; ++q) {
       const int n = base + (q / kU) * kBatchCols + (q % kU) * kRowsPerLoad + row_in_load;
       bv[q] = make_uint4(0, 0, 0, 0);
       if (n < n1 && sub * 8 < r) bv[q] = load8_bf16(B + int64_t(n) * r, sub * 8, r, p.vec_b);
@@ -150,10 +151,10 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   const int per_warp = (r + kTokenWarps - 1) / kTokenWarps, i_end = min(r, (warp + 1) * per_warp);
   for (int i0 = warp * per_warp; i0 < i_end; i0 += 4) {
     float acc[4] = {};
-    for (int k = k0 + lane * 8; k < k1; k += 512) {  // two pieces of four rows at a time
-      uint4 xv[2], av[2][4];
+    for (int k = k0 + lane * 8; k < k1; k += 256 * kHalves) {  // four rows at a time
+      uint4 xv[kHalves], av[kHalves][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kHalves; ++h) {
         const int kh = k + 256 * h;
         xv[h] = kh < k1 ? load8_bf16(x, kh, k1, p.vec_x) : make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -161,7 +162,7 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
           av[h][i] = kh < k1 && i0 + i < i_end ? load8_bf16(A + int64_t(i0 + i) * K, kh, k1, p.vec_a) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kHalves; ++h) {
         float f[8];
         unpack8(xv[h], f);
 #pragma unroll
@@ -187,7 +188,7 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   for (int base = n0 + warp * kStepCols; base < n1; base += kTokenWarps * kStepCols) {
     float sum[kBatches][kU], was[kBatches];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sum[q / kU][q % kU] = dot8(bv[q], f, 0.0f);
+    for (int q = 0; q < kLoads; ++q) sum[q / kU][q % kU] = dot8(bv[q], f, 0.0f);
 #pragma unroll
     for (int b = 0; b < kBatches; ++b) was[b] = bf16_bits_to_float(yv[b]);
     if (base + kTokenWarps * kStepCols < n1) load_b(base + kTokenWarps * kStepCols);
@@ -201,10 +202,18 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   }
 }
 
-template <int kLpr>
+template <int kLpr, int kLoads>
 bool launch_tokens_of(const TokenParams& p, int groups, cudaStream_t st) {
-  return launch(tokens_kernel<kLpr>, dim3(unsigned(kCluster * groups), unsigned(p.a.M)), dim3(kTokenThreads), 0, st,
+  return launch(tokens_kernel<kLpr, kLoads>, dim3(unsigned(kCluster * groups), unsigned(p.a.M)), dim3(kTokenThreads), 0, st,
                 true, dim3(kCluster, 1, 1), p) == FP8_OK;
+}
+template <int kLoads>
+bool launch_tokens_by_rank(const TokenParams& p, int groups, cudaStream_t st) {
+  if (p.a.rank <= 8) return launch_tokens_of<1, kLoads>(p, groups, st);
+  if (p.a.rank <= 16) return launch_tokens_of<2, kLoads>(p, groups, st);
+  if (p.a.rank <= 32) return launch_tokens_of<4, kLoads>(p, groups, st);
+  if (p.a.rank <= 64) return launch_tokens_of<8, kLoads>(p, groups, st);
+  return p.a.rank <= 128 ? launch_tokens_of<16, kLoads>(p, groups, st) : launch_tokens_of<32, kLoads>(p, groups, st);
 }
 
 bool launch_tokens(const Args& a, int num_sms, cudaStream_t st) {
@@ -216,11 +225,8 @@ bool launch_tokens(const Args& a, int num_sms, cudaStream_t st) {
   p.k_slice = int(((a.K + 7) / 8 + kCluster - 1) / kCluster * 8);
   const int groups = 1;
   p.n_slice = int((a.N + kCluster * groups - 1) / (kCluster * groups));
-  if (a.rank <= 8) return launch_tokens_of<1>(p, groups, st);
-  if (a.rank <= 16) return launch_tokens_of<2>(p, groups, st);
-  if (a.rank <= 32) return launch_tokens_of<4>(p, groups, st);
-  if (a.rank <= 64) return launch_tokens_of<8>(p, groups, st);
-  return a.rank <= 128 ? launch_tokens_of<16>(p, groups, st) : launch_tokens_of<32>(p, groups, st);
+  // two CTAs of the deep form fit an SM, four of the other
+  return a.M * kCluster <= 2 * num_sms ? launch_tokens_by_rank<8>(p, groups, st) : launch_tokens_by_rank<4>(p, groups, st);
 }
 
 // ---------------------------------------------------------------------------
