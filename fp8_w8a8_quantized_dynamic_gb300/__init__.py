@@ -707,16 +707,19 @@ def _check_rows_in(t, name: str):
     """A CUDA matrix of bf16 or fp32 with unit column stride; (1 for fp32, rows, columns, row stride)."""
     torch = _torch_module or _torch()
     f32 = t.dtype is torch.float32
-    if not (f32 or t.dtype is torch.bfloat16) or t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+    if not (f32 or t.dtype is torch.bfloat16) or t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA bf16 or fp32 matrix with unit column stride")
     rows, cols = t.shape
-    return int(f32), rows, cols, t.stride(0) if rows > 1 else cols or 1
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name}: expected a CUDA bf16 or fp32 matrix with unit column stride")
+    return 1 if f32 else 0, rows, cols, ld if rows > 1 else cols or 1
 
 
 def _rows_out(out, rows: int, cols: int, like, name: str = "out"):
     """(tensor, row stride) of an output of `like`'s type."""
     if out is None:
-        return _torch().empty((rows, cols), dtype=like.dtype, device=like.device), cols or 1
+        return (_torch_module or _torch()).empty((rows, cols), dtype=like.dtype, device=like.device), cols or 1
     _check_rows(out, like.dtype, rows, cols, like.get_device(), name)
     return out, _row_stride(out, rows, cols)
 
@@ -726,11 +729,11 @@ def _check_pairs(pos, weights, index: int):
     torch = _torch_module or _torch()
     if pos.dim() != 2:
         raise ValueError("pos: expected an int32 matrix [T, k]")
-    T, k = pos.shape
-    _check_dense(pos, torch.int32, (T, k), index, "pos")
+    shape = pos.shape
+    _check_dense(pos, torch.int32, shape, index, "pos")
     if weights is not None:
-        _check_dense(weights, torch.float32, (T, k), index, "weights")
-    return T, k
+        _check_dense(weights, torch.float32, shape, index, "weights")
+    return shape
 
 
 def fp8_moe_dispatch_workspace_bytes(T: int, k: int, E: int) -> int:
@@ -884,13 +887,14 @@ def fp8_residual_norm_quantize(y, weight, residual=None, post_weight=None, gate=
     ldq, device = min_ld(H), y.device
     lds = (M + 3) // 4 * 4 or 1
     qn = torch.empty((M, ldq), dtype=torch.uint8, device=device)
-    s_n = torch.empty((_blocks(H), lds), dtype=torch.float32, device=device)
+    # the last row ends with its last scale, within the 16 bytes that a copy of whole pieces reads
+    s_n = torch.empty_strided((_blocks(H), M), (lds, 1), dtype=torch.float32, device=device)
     status = (_lib or lib()).fp8_residual_norm_quantize(
         y.data_ptr(), M, H, ldy, _ptr(post_weight), _ptr(gate), ldg, scale, _ptr(residual), ldr, weight.data_ptr(), eps,
         1 if plus_one else 0, _ptr(r), ldro, qn.data_ptr(), ldq, s_n.data_ptr(), lds, _stream_ptr(y))
     if status:
         raise FP8Error(status, "fp8_residual_norm_quantize")
-    return qn, s_n[:, :M], y if r is None else r
+    return qn, s_n, y if r is None else r
 
 
 def fp8_selftest_timeout(limit_ns: int = 20_000_000, stream=None) -> int:

@@ -251,7 +251,7 @@ template <typename U>
 fp8_status launch_rows_out(const void* x, int64_t row_bytes, int64_t ldx_bytes, int64_t T, const int* pos, int64_t k,
                            int64_t rows, void* xs, int64_t ldxs_bytes, int sms, cudaStream_t st) {
   const int64_t pieces = row_bytes / int64_t(sizeof(U));
-  return launch(moe::rows_out_kernel<U>, dim3(elementwise_grid(T * pieces, moe::kRowThreads, sms, 8)),
+  return launch(moe::rows_out_kernel<U>, dim3(elementwise_grid(T * pieces, moe::kRowThreads, sms, 64)),
                 dim3(moe::kRowThreads), 0, st, true, dim3(1, 1, 1), static_cast<const U*>(x),
                 ldx_bytes / int64_t(sizeof(U)), T, pieces, pos, int(k), rows, static_cast<U*>(xs),
                 ldxs_bytes / int64_t(sizeof(U)));
@@ -275,7 +275,7 @@ fp8_status launch_few_rows_out(const void* x, int64_t row_bytes, int64_t ldx_byt
 template <typename T, int kN>
 fp8_status launch_rows_back(const void* ys, int64_t ldys, int64_t R, const int* pos, const float* weights, int64_t k,
                             int64_t tokens, int64_t H, void* y, int64_t ldy, int sms, cudaStream_t st) {
-  return launch(moe::rows_back_kernel<T, kN>, dim3(elementwise_grid(tokens * (H / kN), moe::kRowThreads, sms, 8)),
+  return launch(moe::rows_back_kernel<T, kN>, dim3(elementwise_grid(tokens * (H / kN), moe::kRowThreads, sms, 1024)),
                 dim3(moe::kRowThreads), 0, st, true, dim3(1, 1, 1), static_cast<const T*>(ys), ldys, R, pos, weights,
                 int(k), tokens, H, static_cast<T*>(y), ldy);
 }

@@ -482,9 +482,6 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
 // rank leaves no room for 32.
 __host__ __device__ constexpr int stage_cols(int bn) { return bn == 128 ? 32 : 16; }
 
-// out = y + s B[e] v for a tile's rows and the CTA's columns, kBn a step (64 where the rank's
-// operands leave no room for 128): while a step's sums are read, joined with
-// y and stored, the next one's MMAs run and B of the one after that is copied.
 // v of a tile's rows, the sum of the splits in order, as two bf16 numbers in two swizzled tiles, by the block's first
 // `threads` threads.
 __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile& t, int rows, uint32_t v_hi, uint32_t v_lo,
@@ -517,6 +514,9 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
   }
 }
 
+// out = y + s B[e] v for rows and sizes of any alignment: a tile's rows and the CTA's columns, kBn a step (64 where the
+// rank's operands leave no room for 128). While a step's sums are read, joined with y and stored, the next one's MMAs run and
+// B of the one after that is copied.
 template <int kBn>
 __global__ void __launch_bounds__(kTileThreads, kBn == 128 ? 2 : 1)
 expand_any_kernel(const __grid_constant__ TileParams p) {
@@ -524,8 +524,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
   __shared__ TileCtl ctl;
   __shared__ int order[kTileRows];
   constexpr int kSc = stage_cols(kBn), kStagePitch = kSc + 4;
-  constexpr int kLanes = kSc / 8, kRowsAt = 32 / kLanes, kI = 32 / kRowsAt;  // lanes of a row, rows at a time, times
-  constexpr int kParts = kBn / 2 / kSc;
+  constexpr int kRowsAt = 32 / kSc, kParts = kBn / 2 / kSc;
   __shared__ __align__(16) float staged[kTileThreads / 32][32 * kStagePitch];
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -541,9 +540,15 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
   __syncthreads();
   if (mine && t.expert >= g.adapters) {
     if (g.out != g.y)
-      for (int row = warp; row < rows; row += kTileThreads / 32)
-        for (int n = n0 + lane; n < n1; n += 32)
-          g.out[int64_t(order[row]) * g.ldo + n] = g.y[int64_t(order[row]) * g.ldy + n];
+      for (int n = n0 + lane; n < n1; n += 32)
+        for (int row0 = warp * 8; row0 < rows; row0 += kTileThreads / 32 * 8) {
+          uint16_t v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = row0 + i < rows ? g.y[int64_t(order[row0 + i]) * g.ldy + n] : uint16_t(0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (row0 + i < rows) g.out[int64_t(order[row0 + i]) * g.ldo + n] = v[i];
+        }
   } else if (mine) {
     const int rk = (p.rp + kBk - 1) / kBk;  // 128-byte rows that the rank fills
     const uint32_t v_hi = base, v_lo = base + uint32_t(rk) * kXBytes, b_at = v_lo + uint32_t(rk) * kXBytes;
@@ -583,25 +588,20 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
     const float scale = g.scales ? g.scales[t.expert] : 1.0f;
     const int quarter = warp & 3, half = warp >> 2;
     float* mine32 = staged[warp];
-    const int c8 = (lane % kLanes) * 8, r8 = lane / kLanes;
-    int64_t row_y[kI], row_o[kI];       // the first element of a row, -1 for none
-#pragma unroll
-    for (int i = 0; i < kI; ++i) {
-      const int token = order[quarter * 32 + i * kRowsAt + r8];
-      row_y[i] = token >= 0 ? token * g.ldy : -1;
-      row_o[i] = token * g.ldo;
-    }
-    auto col_of = [&](int step, int h) { return n0 + step * kBn + half * (kBn / 2) + h * kSc + c8; };
-    auto load_y = [&](int step, int h, int i) {
+    // 32 rows of kSc columns at a time, a column a lane: whole sectors wherever the rows start
+    const int c1 = lane % kSc, r1 = lane / kSc;
+    uint16_t yv[kSc];
+    auto col_of = [&](int step, int h) { return n0 + step * kBn + half * (kBn / 2) + h * kSc + c1; };
+    auto token_of = [&](int i) { return order[quarter * 32 + i * kRowsAt + r1]; };
+    auto load_y = [&](int step, int h) {
       const int n = col_of(step, h);
-      if (row_y[i] < 0 || n >= N) return make_uint4(0, 0, 0, 0);
-      return load8_bf16(g.y + row_y[i], n, N, p.vec_y);
+#pragma unroll
+      for (int i = 0; i < kSc; ++i) {
+        const int token = token_of(i);
+        yv[i] = token >= 0 && n < N ? g.y[token * g.ldy + n] : uint16_t(0);
+      }
     };
-    uint4 yv[kParts][kI];
-#pragma unroll
-    for (int h = 0; h < kParts; ++h)
-#pragma unroll
-      for (int i = 0; i < kI; ++i) yv[h][i] = load_y(0, h, i);
+    load_y(0, 0);
     for (int step = 0; step < steps; ++step) {
       bool ok = mbar_wait_short(smem_u32(&ctl.done[step & 1]), uint32_t(step >> 1) & 1u, &ctl.abort_flag, &g_lora_error);
       // B of the next step has landed; the sums of the step before this one have been read by all warps
@@ -624,26 +624,15 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
           *reinterpret_cast<uint4*>(mine32 + lane * kStagePitch + j) = make_uint4(from[0], from[1], from[2], from[3]);
         }
         __syncwarp();
+        const int n = col_of(step, h);
 #pragma unroll
-        for (int i = 0; i < kI; ++i) {
-          const int n = col_of(step, h);
-          float o[8];
-          unpack8(yv[h][i], o);
-          // y of the next step is under way from here on
-          if (step + 1 < steps) yv[h][i] = load_y(step + 1, h, i);
-          const float4 lo = *reinterpret_cast<const float4*>(mine32 + (i * kRowsAt + r8) * kStagePitch + c8);
-          const float4 hi = *reinterpret_cast<const float4*>(mine32 + (i * kRowsAt + r8) * kStagePitch + c8 + 4);
-          const float d[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = fmaf(scale, d[j], o[j]);
-          if (row_y[i] >= 0 && n < N) {
-            uint16_t* dst = g.out + row_o[i] + n;
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (n + j < N) dst[j] = __bfloat16_as_ushort(__float2bfloat16_rn(o[j]));
-          }
+        for (int i = 0; i < kSc; ++i) {
+          const int token = token_of(i);
+          const float o = fmaf(scale, mine32[(i * kRowsAt + r1) * kStagePitch + c1], bf16_bits_to_float(yv[i]));
+          if (token >= 0 && n < N) g.out[token * g.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
         }
         __syncwarp();
+        if (h + 1 < kParts || step + 1 < steps) load_y(h + 1 < kParts ? step : step + 1, (h + 1) % kParts);
       }
     }
   }
@@ -699,14 +688,14 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       int s, s1;      // columns of the next step, and where the part ends
       int token;
     };
-    auto enter = [&](Walk& w) {  // the next part of a tile with an adapter; false behind the last
+    auto enter = [&](Walk& w) {  // the next part of a tile with something to do; false behind the last
       while (w.u < end) {
         const int tile = int(w.u / steps);
         w.s = int(w.u - int64_t(tile) * steps);
         w.s1 = int(min(int64_t(steps), w.s + (end - w.u)));
         w.u += w.s1 - w.s;
         const block::RowTile t = p.s.tiles[tile];
-        if (t.expert >= g.adapters) continue;
+        if (t.expert >= g.adapters && g.out == g.y) continue;
         w.token = lane < kCopyRows && first + lane < min(kTileRows, t.row_end - t.row0) ? p.s.order[t.row0 + first + lane] : -1;
         return true;
       }
@@ -749,19 +738,18 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       if (++out.s == out.s1) left = enter(out);
     }
   } else {
-    uint32_t it = 0;  // steps so far
+    uint32_t it = 0, slot_it = 0;  // steps with an adapter, and all that pass the slots, so far
     bool ok = true;
     for (int64_t u = begin; u < end;) {
       const int tile = int(u / steps), s0 = int(u - int64_t(tile) * steps), s1 = int(min(int64_t(steps), s0 + (end - u)));
       u += s1 - s0;
       const block::RowTile t = p.s.tiles[tile];
       const int rows = min(kTileRows, t.row_end - t.row0);
-      if (t.expert >= g.adapters) {
-        if (g.out != g.y)
-          for (int row = warp; row < rows; row += kJoinWarps + 1) {
-            const int64_t token = p.s.order[t.row0 + row];
-            for (int n = s0 * kBn + lane * 8; n < min(N, s1 * kBn); n += 256)
-              *reinterpret_cast<uint4*>(g.out + token * g.ldo + n) = *reinterpret_cast<const uint4*>(g.y + token * g.ldy + n);
+      if (t.expert >= g.adapters) {  // no adapter: y passes the slots as it is
+        if (g.out != g.y && warp < kJoinWarps)
+          for (int s = s0; ok && s < s1; ++s, ++slot_it) {
+            if (!(ok = __all_sync(0xffffffffu, wait_ring(ctl.y_in, slot_it, p.slots)))) break;
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.y_out[slot_it % uint32_t(p.slots)]));
           }
         continue;
       }
@@ -813,7 +801,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       }
       const int row = (warp & 3) * 32 + lane, group = warp >> 2;  // columns [32 group, 32 group + 32)
       const float scale = g.scales ? g.scales[t.expert] : 1.0f;
-      for (int s = s0; s < s1; ++s, ++it) {
+      for (int s = s0; s < s1; ++s, ++it, ++slot_it) {
         ok = ok && wait(ctl.done, it);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tmem_fence_after();
@@ -822,8 +810,8 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl.read[it & 1u]));
-        if (!(ok = __all_sync(0xffffffffu, wait_ring(ctl.y_in, it, p.slots)))) break;
-        const uint32_t slot = it % uint32_t(p.slots);
+        if (!(ok = __all_sync(0xffffffffu, wait_ring(ctl.y_in, slot_it, p.slots)))) break;
+        const uint32_t slot = slot_it % uint32_t(p.slots);
         const uint32_t at = slots_at + slot * kSlotBytes + uint32_t(row) * kPitch + uint32_t(group) * 64u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

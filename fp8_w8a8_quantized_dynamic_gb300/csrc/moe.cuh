@@ -337,10 +337,12 @@ plan_kernel(const __grid_constant__ Plan p, int has_counts) {
   extern __shared__ int count[];  // [kPlanWarps][experts], then [experts] first rows
   int* total = count + kPlanWarps * experts;
   __shared__ int warp_sum[2][kPlanWarps];
+  __shared__ int elsewhere[2][kMaxExperts];  // pairs of each expert in the CTAs before this one, and in all
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < kPlanWarps * experts; i += kPlanThreads) count[i] = 0;
+  if (threadIdx.x < kMaxExperts) elsewhere[0][threadIdx.x] = elsewhere[1][threadIdx.x] = 0;
   __syncthreads();
   int64_t cta_begin, cta_end, begin, end;
   plan_range(p.pairs, blockIdx.x, gridDim.x, cta_begin, cta_end);
@@ -355,24 +357,37 @@ plan_kernel(const __grid_constant__ Plan p, int has_counts) {
     __syncwarp();
   }
   __syncthreads();
+  // this CTA's place: every expert's pairs in the CTAs before it, and in all of them, by as many threads as there are
+  if (counts != nullptr) {
+    const int wide = experts <= 32 ? 32 : 1 << (32 - __clz(experts - 1)), e = threadIdx.x & (wide - 1);
+    if (e < experts) {
+      int before = 0, all = 0;
+#pragma unroll 4
+      for (int c = threadIdx.x / wide; c < int(gridDim.x); c += kPlanThreads / wide) {
+        const int v = counts[c * experts + e];
+        before += c < int(blockIdx.x) ? v : 0;
+        all += v;
+      }
+      atomicAdd(&elsewhere[0][e], before);  // sums of whole numbers: any order
+      atomicAdd(&elsewhere[1][e], all);
+    }
+    __syncthreads();
+  }
   // experts are scanned in order: thread e < experts sums its column over the warps
   int tot = 0;
   if (int(threadIdx.x) < experts) {
-    int before = 0;  // this expert's pairs in the CTAs before this one
-    if (counts != nullptr) {
-#pragma unroll 8
-      for (int c = 0; c < int(gridDim.x); ++c) {
-        const int v = counts[c * experts + threadIdx.x];
-        before += c < int(blockIdx.x) ? v : 0;
-        tot += v;
+    int before = elsewhere[0][threadIdx.x];
+    for (int w0 = 0; w0 < kPlanWarps; w0 += 8) {
+      int v[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v[w] = count[(w0 + w) * experts + threadIdx.x];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        count[(w0 + w) * experts + threadIdx.x] = before;
+        before += v[w];
       }
     }
-    for (int w = 0; w < kPlanWarps; ++w) {
-      const int v = count[w * experts + threadIdx.x];
-      count[w * experts + threadIdx.x] = before;
-      before += v;
-    }
-    if (counts == nullptr) tot = before;
+    tot = counts == nullptr ? before : elsewhere[1][threadIdx.x];
   }
   const int my_tiles = (tot + block::kRowTile - 1) / block::kRowTile;
   int rows_before = tot, tiles_before = my_tiles;  // inclusive scans over the experts
@@ -491,12 +506,14 @@ rows_out_kernel(const U* __restrict__ x, int64_t ldx, int64_t tokens, int64_t pi
 constexpr int kFewPairs = 1024;  // that every CTA of few_rows_out_kernel looks at by itself
 
 // The same with the sort, for few pairs: a CTA a token and kRowThreads pieces of its row. The row of a pair is the number of
-// pairs that come before it, which a warp counts over all of them; an expert's first row likewise.
+// pairs that come before it, which a warp counts over all of them; an expert's first row likewise. (Any id >= experts
+// is in no count: e is at most experts.)
 template <typename U>
 __global__ void __launch_bounds__(kRowThreads)
 few_rows_out_kernel(const U* __restrict__ x, int64_t ldx, int64_t pieces, const int32_t* __restrict__ ids, int pairs, int k,
                     int experts, int* __restrict__ pos, int* __restrict__ offsets, U* __restrict__ xs, int64_t ldxs) {
   __shared__ int row_of[kMaxChosen];
+  __shared__ int id_of[kFewPairs];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -504,17 +521,19 @@ few_rows_out_kernel(const U* __restrict__ x, int64_t ldx, int64_t pieces, const 
   const bool live = pairs > 0 && c < pieces;
   U v = {};
   if (live) v = x[t * ldx + c];  // under way while the rows are counted
-  // kept pairs of experts before e, and those of e before pair p
+  for (int i = threadIdx.x; i < pairs; i += kRowThreads) id_of[i] = ids[i];
+  __syncthreads();
+  // kept pairs of experts before e, and those of e before pair p, by a warp
   auto before = [&](int e, int p) {
     int n = 0;
     for (int i = lane; i < pairs; i += 32) {
-      const int id = ids[i];
+      const int id = id_of[i];
       n += (id >= 0 && id < e) || (id == e && i < p);
     }
     return __reduce_add_sync(0xffffffffu, n);
   };
   for (int j = warp; pairs > 0 && j < k; j += kRowThreads / 32) {
-    const int p = int(t) * k + j, e = ids[p];
+    const int p = int(t) * k + j, e = id_of[p];
     const int n = e >= 0 && e < experts ? before(e, p) : -1;
     if (lane == 0) {
       row_of[j] = n;
@@ -522,9 +541,17 @@ few_rows_out_kernel(const U* __restrict__ x, int64_t ldx, int64_t pieces, const 
     }
   }
   const int ctas = int(gridDim.x * gridDim.y), cta = int(blockIdx.y * gridDim.x + blockIdx.x);
-  for (int e = cta * (kRowThreads / 32) + warp; e <= experts; e += ctas * (kRowThreads / 32)) {
-    const int n = before(e, 0);
-    if (lane == 0) offsets[e] = n;
+  if (pairs <= 64) {  // a thread an expert, the last CTAs first: the first ones' warps count rows
+    for (int e = (ctas - 1 - cta) * kRowThreads + int(threadIdx.x); e <= experts; e += ctas * kRowThreads) {
+      int n = 0;
+      for (int i = 0; i < pairs; ++i) n += id_of[i] >= 0 && id_of[i] < e;
+      offsets[e] = n;
+    }
+  } else {
+    for (int e = cta * (kRowThreads / 32) + warp; e <= experts; e += ctas * (kRowThreads / 32)) {
+      const int n = before(e, 0);
+      if (lane == 0) offsets[e] = n;
+    }
   }
   __syncthreads();
   if (!live) return;
@@ -572,15 +599,15 @@ struct Cols<uint16_t, 1> {
 template <int kN>
 __device__ __forceinline__ void store_cols(float* p, const float (&f)[kN]) {
   if constexpr (kN == 4)
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
   else
     *p = f[0];
 }
 template <int kN>
 __device__ __forceinline__ void store_cols(uint16_t* p, const float (&f)[kN]) {
   if constexpr (kN == 8)
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                              pack_bf16x2(f[6], f[7]));
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                                   pack_bf16x2(f[6], f[7])));
   else
     *p = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
 }
@@ -590,7 +617,7 @@ constexpr int kRowBatch = 8;  // rows of a token whose loads a thread has under 
 // y[t] = sum_j w[t, j] ys[pos[t, j]] (weights null: 1) over the pairs that have a row, in the order of j, in fp32, kN columns
 // a thread (1 or 16 bytes' worth; the row's columns are a multiple of it).
 template <typename T, int kN>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 4)
 rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int* __restrict__ pos,
                  const float* __restrict__ weights, int k, int64_t tokens, int64_t cols, T* __restrict__ y, int64_t ldy) {
   pdl_trigger();
@@ -626,7 +653,7 @@ rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int
 // The gradient of rows_back: dys[pos[t, j]] = w[t, j] dy[t], dw[t, j] = <dy[t], ys[pos[t, j]]> (0 for a pair without a
 // row), fp32 sums in a fixed order. dys may be ys. blockDim.x threads a token (a power of two from 32), blockDim.y tokens a CTA.
 template <typename T, int kN>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 4)
 rows_back_grad_kernel(const T* __restrict__ dy, int64_t lddy, const T* ys, int64_t ldys, int64_t rows,
                       const int* __restrict__ pos, const float* __restrict__ weights, int k, int64_t tokens, int64_t cols,
                       T* dys, int64_t lddys, float* __restrict__ dw) {
