@@ -18,7 +18,10 @@ using namespace fp8k;
 
 fp8_status check_row_vector(const void* p) { return aligned(p, 2) ? FP8_OK : FP8_ERR_MISALIGNED; }
 
-int rows_vec(const void* p, int64_t rows, int64_t ld) { return aligned(p, 16) && (rows <= 1 || ld % 8 == 0); }
+// Whether all rows of bf16 start on boundaries of `bytes`.
+bool rows_start_on(int bytes, const void* p, int64_t rows, int64_t ld) {
+  return aligned(p, uintptr_t(bytes)) && (rows <= 1 || ld * 2 % bytes == 0);
+}
 
 PerDeviceCache<const void*, int> g_norm_ctas;
 
@@ -48,19 +51,19 @@ fp8_status launch_norm(const norm::Params& p, int sms, cudaStream_t st) {
 
 // Threads of a row: few rows take as many as there are, many as few as hold one.
 fp8_status launch_norm_any(const norm::Params& p, int sms, cudaStream_t st) {
-  const int units = (p.cols + 15) / 16 * 2;  // of eight columns; the codes' rows are whole sixteens
+  const int units = (p.cols + norm::kUnit - 1) / norm::kUnit;
   const bool few = p.rows <= sms;
   if (!p.vec) {
-    if (units <= 256) return launch_norm<256, 1, false>(p, sms, st);
-    if (units <= 1024) return launch_norm<512, 2, false>(p, sms, st);
-    return launch_norm<1024, 4, false>(p, sms, st);
+    if (units <= 128) return launch_norm<128, 1, false>(p, sms, st);
+    if (units <= 512) return launch_norm<512, 1, false>(p, sms, st);
+    return launch_norm<1024, 2, false>(p, sms, st);
   }
+  if (units <= 64) return launch_norm<64, 1, true>(p, sms, st);
   if (units <= 128) return launch_norm<128, 1, true>(p, sms, st);
   if (units <= 256) return launch_norm<256, 1, true>(p, sms, st);
   if (units <= 512) return few ? launch_norm<512, 1, true>(p, sms, st) : launch_norm<256, 2, true>(p, sms, st);
-  if (units <= 1024) return few ? launch_norm<1024, 1, true>(p, sms, st) : launch_norm<256, 4, true>(p, sms, st);
-  if (units <= 2048) return few ? launch_norm<1024, 2, true>(p, sms, st) : launch_norm<512, 4, true>(p, sms, st);
-  return launch_norm<1024, 4, true>(p, sms, st);
+  if (units <= 1024) return few ? launch_norm<1024, 1, true>(p, sms, st) : launch_norm<512, 2, true>(p, sms, st);
+  return launch_norm<1024, 2, true>(p, sms, st);
 }
 
 // What both calls share, up to r.
@@ -90,10 +93,15 @@ fp8_status fill_norm(norm::Params& p, const void* y, int64_t M, int64_t H, int64
   p.scale = scale;
   p.eps = eps;
   p.w_offset = plus_one ? 1.0f : 0.0f;
+  p.inv_cols = H > 0 ? 1.0f / float(H) : 0.0f;
   p.r = static_cast<uint16_t*>(r);
   p.ldro = ldro;
-  p.vec = H % 8 == 0 && aligned(post_w, 16) && aligned(w, 16) && rows_vec(y, M, ldy) && rows_vec(gate, M, ldg) &&
-          rows_vec(residual, M, ldr) && rows_vec(r, M, ldro);
+  auto rows_on = [&](int bytes) {
+    return H * 2 % bytes == 0 && rows_start_on(bytes, y, M, ldy) && rows_start_on(bytes, gate, M, ldg) &&
+           rows_start_on(bytes, residual, M, ldr) && rows_start_on(bytes, r, M, ldro);
+  };
+  p.vec = rows_on(16) && aligned(post_w, 16) && aligned(w, 16);
+  p.wide = p.vec && rows_on(32);
   return FP8_OK;
 }
 
@@ -154,7 +162,8 @@ FP8_API fp8_status fp8_residual_norm(const void* y_bf16, int64_t M, int64_t H, i
   p.pre = n_bf16 != nullptr;
   p.n = static_cast<uint16_t*>(n_bf16);
   p.ldn = ldn;
-  p.vec = p.vec && rows_vec(n_bf16, M, ldn);
+  p.vec = p.vec && rows_start_on(16, n_bf16, M, ldn);
+  p.wide = p.wide && rows_start_on(32, n_bf16, M, ldn);
   int sms = 0;
   FP8_TRY(current_device(&sms));
   return launch_norm_any(p, sms, reinterpret_cast<cudaStream_t>(stream));

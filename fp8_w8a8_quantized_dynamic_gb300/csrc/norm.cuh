@@ -17,9 +17,10 @@
 namespace fp8k {
 namespace norm {
 
+constexpr int kUnit = 16;       // adjacent columns of a thread: eight lanes hold a block of 128
 constexpr int kMaxThreads = 1024;
-constexpr int kMaxUnits = 4;                          // eight columns each
-constexpr int kMaxCols = kMaxThreads * kMaxUnits * 8;
+constexpr int kMaxUnits = 2;
+constexpr int kMaxCols = kMaxThreads * kMaxUnits * kUnit;
 
 struct Params {
   int64_t rows;
@@ -33,7 +34,7 @@ struct Params {
   int64_t ldr;
   const uint16_t* w;
   int pre;                   // n or the codes are wanted, else r alone
-  float scale, eps, w_offset;
+  float scale, eps, w_offset, inv_cols;
   uint16_t* r;               // may be null
   int64_t ldro;
   uint16_t* n;               // may be null
@@ -42,19 +43,22 @@ struct Params {
   int64_t ldq;
   float* s;
   int64_t lds;
-  int vec;  // all rows start on 16-byte boundaries and are whole eights
+  int vec;   // all rows start on 16-byte boundaries and are whole eights
+  int wide;  // .. on 32-byte boundaries and are whole sixteens
 };
 
-// Eight fp32 values in four packed pairs: the arithmetic below takes two at a time.
-struct Eight {
-  uint64_t p[4];
+// A unit as it is held, and as fp32 in packed pairs: the arithmetic below takes two values at a time.
+struct Held {
+  uint32_t w[8];
 };
-__device__ __forceinline__ Eight unpack8(uint4 v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  Eight e;
+struct Values {
+  uint64_t p[8];
+};
+__device__ __forceinline__ Values values_of(const Held& h) {
+  Values v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) e.p[i] = pack_f32x2(bf16_lo(w[i]), bf16_hi(w[i]));
-  return e;
+  for (int i = 0; i < 8; ++i) v.p[i] = pack_f32x2(bf16_lo(h.w[i]), bf16_hi(h.w[i]));
+  return v;
 }
 __device__ __forceinline__ uint64_t both(float x) { return pack_f32x2(x, x); }
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
@@ -67,23 +71,60 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(uint64_t p) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi_of(p)), "f"(lo_of(p)));
   return d;
 }
+__device__ __forceinline__ Held zeros() {
+  Held h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h.w[i] = 0;
+  return h;
+}
+__device__ __forceinline__ void put8(Held& h, int at, uint4 v) {
+  h.w[at] = v.x, h.w[at + 1] = v.y, h.w[at + 2] = v.z, h.w[at + 3] = v.w;
+}
 
-// kVec: rows start on 16-byte boundaries and are whole eights. Else single values, zeros from cols on.
+// A unit of a row from column c < cols on, zeros from cols on. kVec: see Params::vec.
 template <bool kVec>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int cols) {
-  return kVec ? ld_nc_v4(row + c) : load8_bf16(row, c, cols, 0);
+__device__ __forceinline__ Held load_unit(const uint16_t* row, int c, int cols, int wide) {
+  Held h;
+  if (kVec && wide) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(h.w[0]), "=r"(h.w[1]), "=r"(h.w[2]), "=r"(h.w[3]), "=r"(h.w[4]), "=r"(h.w[5]), "=r"(h.w[6]),
+                   "=r"(h.w[7]) : "l"(row + c));
+  } else {
+    put8(h, 0, kVec ? ld_nc_v4(row + c) : load8_bf16(row, c, cols, 0));
+    put8(h, 4, kVec ? (c + 8 < cols ? ld_nc_v4(row + c + 8) : make_uint4(0, 0, 0, 0)) : load8_bf16(row, c + 8, cols, 0));
+  }
+  return h;
+}
+// The same of a weight, which stays in L1 for the CTA's next rows.
+template <bool kVec>
+__device__ __forceinline__ Held load_weights(const uint16_t* w, int c, int cols) {
+  Held h;
+  if constexpr (kVec) {
+    put8(h, 0, __ldg(reinterpret_cast<const uint4*>(w + c)));
+    put8(h, 4, c + 8 < cols ? __ldg(reinterpret_cast<const uint4*>(w + c + 8)) : make_uint4(0, 0, 0, 0));
+  } else {
+    put8(h, 0, load8_bf16(w, c, cols, 0));
+    put8(h, 4, load8_bf16(w, c + 8, cols, 0));
+  }
+  return h;
 }
 template <bool kVec>
-__device__ __forceinline__ void store8(uint16_t* row, int c, int cols, const Eight& e) {
-  if constexpr (kVec) {
-    *reinterpret_cast<uint4*>(row + c) =
-        make_uint4(cvt_bf16x2(e.p[0]), cvt_bf16x2(e.p[1]), cvt_bf16x2(e.p[2]), cvt_bf16x2(e.p[3]));
+__device__ __forceinline__ void store_unit(uint16_t* row, int c, int cols, int wide, const Values& v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = cvt_bf16x2(v.p[i]);
+  if (kVec && wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(row + c), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else if constexpr (kVec) {
+    *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (c + 8 < cols) *reinterpret_cast<uint4*>(row + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = cvt_bf16x2(e.p[i]);
-      if (c + 2 * i < cols) row[c + 2 * i] = uint16_t(w);
-      if (c + 2 * i + 1 < cols) row[c + 2 * i + 1] = uint16_t(w >> 16);
+    for (int i = 0; i < 8; ++i) {
+      if (c + 2 * i < cols) row[c + 2 * i] = uint16_t(w[i]);
+      if (c + 2 * i + 1 < cols) row[c + 2 * i + 1] = uint16_t(w[i] >> 16);
     }
   }
 }
@@ -98,20 +139,28 @@ __device__ __forceinline__ float block_sum(float v, float (&red)[2][kThreads / 3
   if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0.0f;
+  if constexpr (kThreads >= 128) {
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) v += mine[i];
+    for (int i = 0; i < kThreads / 128; ++i) {
+      const float4 f = reinterpret_cast<const float4*>(mine)[i];
+      v += (f.x + f.y) + (f.z + f.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) v += mine[i];
+  }
   return v;
 }
 
 // Sum of the squares of factor * v over the CTA's row.
 template <int kThreads, int kUnits>
-__device__ __forceinline__ float squares(const Eight (&v)[kUnits], float factor, float (&red)[2][kThreads / 32], int& turn) {
+__device__ __forceinline__ float squares(const Values (&v)[kUnits], float factor, float (&red)[2][kThreads / 32], int& turn) {
   uint64_t ss[2] = {0, 0};
   const uint64_t f = both(factor);
 #pragma unroll
   for (int i = 0; i < kUnits; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const uint64_t x = factor == 1.0f ? v[i].p[j] : mul_f32x2(v[i].p[j], f);
       ss[j & 1] = fma_f32x2(x, x, ss[j & 1]);
     }
@@ -119,103 +168,72 @@ __device__ __forceinline__ float squares(const Eight (&v)[kUnits], float factor,
   return block_sum<kThreads>(lo_of(s) + hi_of(s), red, turn);
 }
 
-// 1 / sqrt(mean v^2 + eps) of the CTA's row. Squares of bf16's range may pass fp32's: then once more of v 2^-80.
+// 1 / sqrt(mean v^2 + eps) of the CTA's row; the hardware root is off by two units in the last place. Squares of bf16's range
+// may pass fp32's: then once more of v 2^-80.
 template <int kThreads, int kUnits>
-__device__ __forceinline__ float inverse_rms(const Eight (&v)[kUnits], const Params& p, float (&red)[2][kThreads / 32],
+__device__ __forceinline__ float inverse_rms(const Values (&v)[kUnits], const Params& p, float (&red)[2][kThreads / 32],
                                              int& turn) {
-  float ss = squares<kThreads, kUnits>(v, 1.0f, red, turn);
-  if (ss <= 0x1.fffffep127f) return __frcp_rn(__fsqrt_rn(__fdiv_rn(ss, float(p.cols)) + p.eps));
-  ss = squares<kThreads, kUnits>(v, 0x1p-80f, red, turn);
-  return __frcp_rn(__fsqrt_rn(__fdiv_rn(ss, float(p.cols)))) * 0x1p-80f;
+  const float ss = squares<kThreads, kUnits>(v, 1.0f, red, turn);
+  if (ss <= 0x1.fffffep127f) return rsqrtf(fmaf(ss, p.inv_cols, p.eps));
+  return rsqrtf(squares<kThreads, kUnits>(v, 0x1p-80f, red, turn) * p.inv_cols) * 0x1p-80f;
 }
 
 // A thread's raw values of one row.
 template <int kUnits, bool kGate>
 struct Raw {
-  uint4 y[kUnits], res[kUnits], gate[kGate ? kUnits : 1];
+  Held y[kUnits], res[kUnits], gate[kGate ? kUnits : 1];
 };
 
 template <int kThreads, int kUnits, bool kGate, bool kVec>
 __device__ __forceinline__ void load_row(Raw<kUnits, kGate>& in, const Params& p, int64_t row) {
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    const int c = (i * kThreads + threadIdx.x) * 8;
-    in.y[i] = in.res[i] = make_uint4(0, 0, 0, 0);
-    if constexpr (kGate) in.gate[i] = make_uint4(0, 0, 0, 0);
+    const int c = (i * kThreads + threadIdx.x) * kUnit;
+    in.y[i] = in.res[i] = zeros();
+    if constexpr (kGate) in.gate[i] = zeros();
     if (c < p.cols) {
-      in.y[i] = load8<kVec>(p.y + row * p.ldy, c, p.cols);
-      if (p.residual) in.res[i] = load8<kVec>(p.residual + row * p.ldr, c, p.cols);
-      if constexpr (kGate) in.gate[i] = load8<kVec>(p.gate + row * p.ldg, c, p.cols);
+      in.y[i] = load_unit<kVec>(p.y + row * p.ldy, c, p.cols, p.wide);
+      if (p.residual) in.res[i] = load_unit<kVec>(p.residual + row * p.ldr, c, p.cols, p.wide);
+      if constexpr (kGate) in.gate[i] = load_unit<kVec>(p.gate + row * p.ldg, c, p.cols, p.wide);
     }
   }
 }
 
 template <int kThreads, int kUnits>
-constexpr bool kAhead = kThreads * kUnits < 4096;  // else a row in fp32 alone takes the registers
+constexpr bool kAhead = kThreads * kUnits < 2048;  // else a row in fp32 alone takes the registers
 // CTAs of an SM, by the registers that a row takes.
-constexpr int ctas_of(int threads, int units) {
-  return units == 1 ? 1536 / threads : std::max(1, 2048 / (threads * units));
+constexpr int ctas_of(int threads, int units) { return std::max(1, 1024 / (threads * units)); }
+
+// The larger magnitude; a NaN stays one.
+__device__ __forceinline__ float larger(float a, float b) {
+  float d;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
-// Scales and reciprocals of a thread's units, each shared by the sixteen lanes that hold its 128 columns. Magnitudes
-// compare as integers, which keeps a NaN. Units are shared out over the lanes as far as they go: in each exchange a lane
-// keeps the maxima of half of them, computes the scale of the one it ends with, and all fetch theirs from it.
-template <int kUnits>
-__device__ __forceinline__ void block_scales(const Eight (&v)[kUnits], float (&s)[kUnits], float (&r)[kUnits]) {
-  uint32_t m[kUnits];
+// The scale of the 128 columns that eight lanes hold.
+__device__ __forceinline__ float block_scale(const Values& v) {
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    m[i] = 0;
+  for (int j = 0; j < 8; ++j) m = larger(m, larger(lo_of(v.p[j]), hi_of(v.p[j])));
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      m[i] = max(m[i], max(uint32_t(v[i].p[j]) & 0x7FFFFFFFu, uint32_t(v[i].p[j] >> 32) & 0x7FFFFFFFu));
-  }
-  const int lane = threadIdx.x & 31;
-  int left = kUnits;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    if (left > 1) {
-      left >>= 1;
-      const bool upper = (lane & o) != 0;
-#pragma unroll
-      for (int i = 0; i < kUnits / 2; ++i)
-        if (i < left) {
-          const uint32_t send = upper ? m[i] : m[i + left], keep = upper ? m[i + left] : m[i];
-          m[i] = max(keep, __shfl_xor_sync(0xffffffffu, send, o));
-        }
-    } else {
-      m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
-    }
-  }
-  const float sc = scale_from_amax<kFmtE4M3>(__uint_as_float(m[0]));
-  const float rc = __frcp_rn(sc);
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    // unit i's lanes: bit 3 of the lane is its highest index bit, bit 2 the next
-    const int from = kUnits == 1 ? lane : (lane & 16) | (kUnits == 2 ? i << 3 : i << 2);
-    s[i] = kUnits == 1 ? sc : __shfl_sync(0xffffffffu, sc, from);
-    r[i] = kUnits == 1 ? rc : __shfl_sync(0xffffffffu, rc, from);
-  }
+  for (int o = 4; o > 0; o >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return scale_from_amax<kFmtE4M3>(fabsf(m));
 }
 
-// Codes of eight values under scale s with r = fl32(1 / s); the sign of zero is kept.
-__device__ __forceinline__ uint2 codes8(const Eight& e, float s, float r) {
-  ExactScale k;
-  const float r_lo = fmaf(-s, r, 1.0f) * r;
-  k.r2 = both(r);
-  k.r_lo2 = both(r_lo);
-  k.neg_s2 = both(-s);
-  k.fast = s >= 0x1p-80f && s <= 0x1p100f;
-  uint32_t code[2];
+// Codes of a unit under scale s; the sign of zero is kept.
+__device__ __forceinline__ uint4 codes_of(const Values& v, float s) {
+  const ExactScale k = make_exact_scale(s);
+  uint32_t code[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint64_t a = e.p[2 * h], b = e.p[2 * h + 1];
+  for (int h = 0; h < 4; ++h) {
+    const uint64_t a = v.p[2 * h], b = v.p[2 * h + 1];
     code[h] = quant4_exact_f32<kFmtE4M3>(a, b, k, s);
     const uint32_t lo = __byte_perm(uint32_t(a), uint32_t(a >> 32), 0x0073);
     const uint32_t hi = __byte_perm(uint32_t(b), uint32_t(b >> 32), 0x0073);
     code[h] = (code[h] & 0x7F7F7F7Fu) | (__byte_perm(lo, hi, 0x5410) & 0x80808080u);
   }
-  return make_uint2(code[0], code[1]);
+  return make_uint4(code[0], code[1], code[2], code[3]);
 }
 
 // A CTA takes every gridDim.x-th row. The loads of its next row are under way while it sums, joins and stores the one
@@ -223,20 +241,19 @@ __device__ __forceinline__ uint2 codes8(const Eight& e, float s, float r) {
 template <int kThreads, int kUnits, bool kPost, bool kGate, bool kVec>
 __global__ void __launch_bounds__(kThreads, ctas_of(kThreads, kUnits))
 residual_norm_kernel(const __grid_constant__ Params p) {
-  __shared__ float red[2][kThreads / 32];
+  __shared__ __align__(16) float red[2][kThreads / 32];
   pdl_trigger();
   const int cols = p.cols;
-  auto col_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) * 8; };
+  auto col_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) * kUnit; };
   // v * inv * (w_offset + w)
-  auto scaled = [&](const uint16_t* w, int i, Eight& v, float inv) {
-    const int c = col_of(i);
-    Eight f = unpack8(c < cols ? load8<kVec>(w, c, cols) : make_uint4(0, 0, 0, 0));
+  auto scaled = [&](const uint16_t* w, int i, Values& v, float inv) {
+    Values f = values_of(col_of(i) < cols ? load_weights<kVec>(w, col_of(i), cols) : zeros());
     if (p.w_offset != 0.0f) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f.p[j] = add_f32x2(f.p[j], both(p.w_offset));
+      for (int j = 0; j < 8; ++j) f.p[j] = add_f32x2(f.p[j], both(p.w_offset));
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v.p[j] = mul_f32x2(mul_f32x2(v.p[j], both(inv)), f.p[j]);
+    for (int j = 0; j < 8; ++j) v.p[j] = mul_f32x2(mul_f32x2(v.p[j], both(inv)), f.p[j]);
   };
   pdl_wait();
   int turn = 0;
@@ -245,9 +262,9 @@ residual_norm_kernel(const __grid_constant__ Params p) {
   if (kAhead<kThreads, kUnits> && row < p.rows) load_row<kThreads, kUnits, kGate, kVec>(in, p, row);
   for (; row < p.rows; row += gridDim.x) {
     if (!kAhead<kThreads, kUnits>) load_row<kThreads, kUnits, kGate, kVec>(in, p, row);
-    Eight v[kUnits];
+    Values v[kUnits];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) v[i] = unpack8(in.y[i]);
+    for (int i = 0; i < kUnits; ++i) v[i] = values_of(in.y[i]);
     if constexpr (kPost) {
       const float inv = inverse_rms<kThreads, kUnits>(v, p, red, turn);
 #pragma unroll
@@ -256,20 +273,20 @@ residual_norm_kernel(const __grid_constant__ Params p) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       if constexpr (kGate) {
-        const Eight f = unpack8(in.gate[i]);
+        const Values f = values_of(in.gate[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[i].p[j] = mul_f32x2(v[i].p[j], f.p[j]);
+        for (int j = 0; j < 8; ++j) v[i].p[j] = mul_f32x2(v[i].p[j], f.p[j]);
       }
-      const Eight f = unpack8(in.res[i]);
+      const Values f = values_of(in.res[i]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i].p[j] = fma_f32x2(both(p.scale), v[i].p[j], f.p[j]);
+      for (int j = 0; j < 8; ++j) v[i].p[j] = fma_f32x2(both(p.scale), v[i].p[j], f.p[j]);
     }
     if (kAhead<kThreads, kUnits> && row + gridDim.x < p.rows)
       load_row<kThreads, kUnits, kGate, kVec>(in, p, row + gridDim.x);
     if (p.r) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i)
-        if (col_of(i) < cols) store8<kVec>(p.r + row * p.ldro, col_of(i), cols, v[i]);
+        if (col_of(i) < cols) store_unit<kVec>(p.r + row * p.ldro, col_of(i), cols, p.wide, v[i]);
     }
     if (!p.pre) continue;
     const float inv = inverse_rms<kThreads, kUnits>(v, p, red, turn);
@@ -277,26 +294,22 @@ residual_norm_kernel(const __grid_constant__ Params p) {
     for (int i = 0; i < kUnits; ++i) {
       const int c = col_of(i);
       scaled(p.w, i, v[i], inv);
-      if (c + 8 > cols) {  // nothing past the last column counts
+      if (c + kUnit > cols) {  // nothing past the last column counts
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 8; ++j)
           v[i].p[j] = pack_f32x2(c + 2 * j < cols ? lo_of(v[i].p[j]) : 0.0f, c + 2 * j + 1 < cols ? hi_of(v[i].p[j]) : 0.0f);
       }
-      if (p.n && c < cols) store8<kVec>(p.n + row * p.ldn, c, cols, v[i]);
-    }
-    if (p.q) {
-      float s[kUnits], r[kUnits];
-      block_scales<kUnits>(v, s, r);
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int c = col_of(i);
-        if (c < p.ldq) *reinterpret_cast<uint2*>(p.q + row * p.ldq + c) = codes8(v[i], s[i], r[i]);
-        if ((threadIdx.x & 15) == 0 && c < cols) p.s[int64_t(c / block::kBlock) * p.lds + row] = s[i];
+      if (p.n && c < cols) store_unit<kVec>(p.n + row * p.ldn, c, cols, p.wide, v[i]);
+      if (p.q) {
+        const float s = block_scale(v[i]);
+        const uint4 q = codes_of(v[i], s);
+        if (c < p.ldq) *reinterpret_cast<uint4*>(p.q + row * p.ldq + c) = q;
+        if ((threadIdx.x & 7) == 0 && c < cols) p.s[int64_t(c / block::kBlock) * p.lds + row] = s;
       }
-      // zeros to the end of a longer row
-      for (int64_t c = (int64_t(kUnits) * kThreads + threadIdx.x) * 8; c < p.ldq; c += kThreads * 8)
-        *reinterpret_cast<uint2*>(p.q + row * p.ldq + c) = make_uint2(0, 0);
     }
+    if (p.q)  // zeros to the end of a longer row
+      for (int64_t c = (int64_t(kUnits) * kThreads + threadIdx.x) * kUnit; c < p.ldq; c += kThreads * kUnit)
+        *reinterpret_cast<uint4*>(p.q + row * p.ldq + c) = make_uint4(0, 0, 0, 0);
   }
 }
 
