@@ -81,51 +81,92 @@ __device__ __forceinline__ void put8(Held& h, int at, uint4 v) {
   h.w[at] = v.x, h.w[at + 1] = v.y, h.w[at + 2] = v.z, h.w[at + 3] = v.w;
 }
 
+// (not through the read-only path: r may be written over y or the residual)
+__device__ __forceinline__ uint4 load_16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// A unit from column c < cols of a row that starts and ends anywhere, zeros from cols on: the two or three whole 16-byte
+// pieces that hold its values (each holds one of the row's, so that all of it may be read), shifted into place. The shift is
+// one for the row.
+__device__ __forceinline__ Held load_unit_any(const uint16_t* row, int c, int cols) {
+  const uint16_t* first = row + c;
+  const int shift = int(reinterpret_cast<uintptr_t>(first) >> 1) & 7;
+  const uint4* piece = reinterpret_cast<const uint4*>(first - shift);
+  const int n = min(kUnit, cols - c);
+  uint32_t w[12];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint4 v = 8 * i - shift < n ? load_16(piece + i) : make_uint4(0, 0, 0, 0);
+    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 10; ++i) w[i] = shift & 4 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 9; ++i) w[i] = shift & 2 ? w[i + 1] : w[i];
+  Held h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    h.w[i] = __funnelshift_r(w[i], w[i + 1], shift & 1 ? 16 : 0);
+    if (n < kUnit) h.w[i] = 2 * i + 1 < n ? h.w[i] : 2 * i < n ? h.w[i] & 0xFFFFu : 0u;
+  }
+  return h;
+}
+
 // A unit of a row from column c < cols on, zeros from cols on. kVec: see Params::vec.
 template <bool kVec>
 __device__ __forceinline__ Held load_unit(const uint16_t* row, int c, int cols, int wide) {
+  if constexpr (!kVec) return load_unit_any(row, c, cols);
   Held h;
-  if (kVec && wide) {
+  if (wide) {
     asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(h.w[0]), "=r"(h.w[1]), "=r"(h.w[2]), "=r"(h.w[3]), "=r"(h.w[4]), "=r"(h.w[5]), "=r"(h.w[6]),
                    "=r"(h.w[7]) : "l"(row + c));
   } else {
-    put8(h, 0, kVec ? ld_nc_v4(row + c) : load8_bf16(row, c, cols, 0));
-    put8(h, 4, kVec ? (c + 8 < cols ? ld_nc_v4(row + c + 8) : make_uint4(0, 0, 0, 0)) : load8_bf16(row, c + 8, cols, 0));
+    put8(h, 0, load_16(row + c));
+    put8(h, 4, c + 8 < cols ? load_16(row + c + 8) : make_uint4(0, 0, 0, 0));
   }
   return h;
 }
 // The same of a weight, which stays in L1 for the CTA's next rows.
 template <bool kVec>
 __device__ __forceinline__ Held load_weights(const uint16_t* w, int c, int cols) {
+  if constexpr (!kVec) return load_unit_any(w, c, cols);
   Held h;
-  if constexpr (kVec) {
-    put8(h, 0, __ldg(reinterpret_cast<const uint4*>(w + c)));
-    put8(h, 4, c + 8 < cols ? __ldg(reinterpret_cast<const uint4*>(w + c + 8)) : make_uint4(0, 0, 0, 0));
-  } else {
-    put8(h, 0, load8_bf16(w, c, cols, 0));
-    put8(h, 4, load8_bf16(w, c + 8, cols, 0));
-  }
+  put8(h, 0, __ldg(reinterpret_cast<const uint4*>(w + c)));
+  put8(h, 4, c + 8 < cols ? __ldg(reinterpret_cast<const uint4*>(w + c + 8)) : make_uint4(0, 0, 0, 0));
   return h;
 }
+// The units of a warp's lanes, from column c on, as bf16. Rows that start and end anywhere pass through the warp's kilobyte of
+// shared memory, so that its lanes store neighbouring columns (777 x 1001: 6.4 us; a unit a lane at a time 15.7).
 template <bool kVec>
-__device__ __forceinline__ void store_unit(uint16_t* row, int c, int cols, int wide, const Values& v) {
+__device__ __forceinline__ void store_unit(uint16_t* row, int c, int cols, int wide, const Values& v, uint32_t* stage) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = cvt_bf16x2(v.p[i]);
-  if (kVec && wide) {
+  if constexpr (!kVec) {
+    const int lane = threadIdx.x & 31, c0 = c - lane * kUnit;
+    if (c0 >= cols) return;  // (the whole warp)
+    *reinterpret_cast<uint4*>(stage + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(stage + lane * 8 + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+    __syncwarp();
+    const uint16_t* from = reinterpret_cast<const uint16_t*>(stage);
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i)
+      if (c0 + i * 32 + lane < cols) row[c0 + i * 32 + lane] = from[i * 32 + lane];
+    __syncwarp();
+  } else if (c >= cols) {
+    return;
+  } else if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                  :: "l"(row + c), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-  } else if constexpr (kVec) {
+  } else {
     *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
     if (c + 8 < cols) *reinterpret_cast<uint4*>(row + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (c + 2 * i < cols) row[c + 2 * i] = uint16_t(w[i]);
-      if (c + 2 * i + 1 < cols) row[c + 2 * i + 1] = uint16_t(w[i] >> 16);
-    }
   }
 }
 
@@ -242,6 +283,7 @@ template <int kThreads, int kUnits, bool kPost, bool kGate, bool kVec>
 __global__ void __launch_bounds__(kThreads, ctas_of(kThreads, kUnits))
 residual_norm_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) float red[2][kThreads / 32];
+  __shared__ __align__(16) uint32_t stage[kVec ? 1 : kThreads / 32][kVec ? 4 : 32 * kUnit / 2];
   pdl_trigger();
   const int cols = p.cols;
   auto col_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) * kUnit; };
@@ -286,7 +328,7 @@ residual_norm_kernel(const __grid_constant__ Params p) {
     if (p.r) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i)
-        if (col_of(i) < cols) store_unit<kVec>(p.r + row * p.ldro, col_of(i), cols, p.wide, v[i]);
+        store_unit<kVec>(p.r + row * p.ldro, col_of(i), cols, p.wide, v[i], stage[kVec ? 0 : threadIdx.x >> 5]);
     }
     if (!p.pre) continue;
     const float inv = inverse_rms<kThreads, kUnits>(v, p, red, turn);
@@ -299,7 +341,7 @@ residual_norm_kernel(const __grid_constant__ Params p) {
         for (int j = 0; j < 8; ++j)
           v[i].p[j] = pack_f32x2(c + 2 * j < cols ? lo_of(v[i].p[j]) : 0.0f, c + 2 * j + 1 < cols ? hi_of(v[i].p[j]) : 0.0f);
       }
-      if (p.n && c < cols) store_unit<kVec>(p.n + row * p.ldn, c, cols, p.wide, v[i]);
+      if (p.n) store_unit<kVec>(p.n + row * p.ldn, c, cols, p.wide, v[i], stage[kVec ? 0 : threadIdx.x >> 5]);
       if (p.q) {
         const float s = block_scale(v[i]);
         const uint4 q = codes_of(v[i], s);
