@@ -162,13 +162,6 @@ __device__ __forceinline__ void arrive_if(uint32_t bar, bool p) {
                :: "r"(bar), "r"(uint32_t(p)) : "memory");
 }
 
-// One lane of a converged warp (the compiler keeps the branch uniform).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
 }

@@ -307,6 +307,15 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 // n / d for 0 <= n < 4096, d <= 32 and inv = 1 / d: the half keeps the product clear of whole numbers.
 __device__ __forceinline__ int quotient(int n, float inv) { return int((float(n) + 0.5f) * inv); }
 
+// A place in a ring of barriers, and the parity of its turn.
+struct Place {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) i = 0, parity ^= 1u;
+  }
+};
+
 struct TileParams {
   Args a;
   Sorted s;
@@ -319,7 +328,7 @@ struct TileParams {
   uint32_t tmem_cols;
 };
 
-constexpr int kCopyThreads = 256;  // expand: those that copy y and out
+constexpr int kCopyThreads = 128;  // expand: those that copy y and out
 constexpr int kCopyRows = kTileRows / (kCopyThreads / 32);  // of a warp
 
 struct TileCtl {
@@ -398,11 +407,11 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
       bool ok = true;
       int filled = 0;
       if (warp == kTileThreads / 32) {
-        if (lane == 0) {
-          for (int i = 0; i < steps; ++i) {
-            if (!(ok = wait(ctl.loaded, i))) break;
-            fence_async();  // what the copying threads wrote becomes visible to the tensor core
-            tmem_fence_after();
+        for (int i = 0; i < steps; ++i) {
+          if (!(ok = __all_sync(0xffffffffu, wait(ctl.loaded, i)))) break;
+          fence_async();  // what the copying threads wrote becomes visible to the tensor core
+          tmem_fence_after();
+          if (elect_one()) {
             const uint32_t st = base + uint32_t(i % p.stages) * stage_bytes;
             const uint64_t ad = make_sdesc(st), bd = make_sdesc(st + kXBytes);
 #pragma unroll
@@ -410,8 +419,8 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
               mma_bf16(ctl.tmem_base, ad + uint64_t(kk * 2), bd + uint64_t(kk * 2), idesc_of(p.rp), i != 0 || kk != 0);
             mma_commit<false>(smem_u32(&ctl.done[i % p.stages]));
           }
+          __syncwarp();
         }
-        __syncwarp();
       } else {
         // eight threads a row; this thread's rows of x
         const int piece = threadIdx.x & 7, first = threadIdx.x >> 3;
@@ -569,20 +578,23 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
     fill(0);
     cp_commit();
     put_v(p, t, rows, v_hi, v_lo, kTileThreads);
-    auto multiply = [&](int step) {
-      const uint32_t b = b_at + uint32_t(step & 1) * b_bytes, d = ctl.tmem_base + uint32_t(step & 1) * kBn;
-      for (int part = 0; part < 2; ++part)
-        for (int k16 = 0; k16 < p.rp / 16; ++k16) {
-          const uint64_t ad = make_sdesc((part ? v_lo : v_hi) + uint32_t(k16 >> 2) * kXBytes) + uint64_t((k16 & 3) * 2);
-          const uint64_t bd = make_sdesc(b + uint32_t(k16 >> 2) * (kBn * 128u)) + uint64_t((k16 & 3) * 2);
-          mma_bf16(d, ad, bd, idesc_of(kBn), part != 0 || k16 != 0);
-        }
-      mma_commit<false>(smem_u32(&ctl.done[step & 1]));
+    auto multiply = [&](int step) {  // by a whole warp
+      if (elect_one()) {
+        const uint32_t b = b_at + uint32_t(step & 1) * b_bytes, d = ctl.tmem_base + uint32_t(step & 1) * kBn;
+        for (int part = 0; part < 2; ++part)
+          for (int k16 = 0; k16 < p.rp / 16; ++k16) {
+            const uint64_t ad = make_sdesc((part ? v_lo : v_hi) + uint32_t(k16 >> 2) * kXBytes) + uint64_t((k16 & 3) * 2);
+            const uint64_t bd = make_sdesc(b + uint32_t(k16 >> 2) * (kBn * 128u)) + uint64_t((k16 & 3) * 2);
+            mma_bf16(d, ad, bd, idesc_of(kBn), part != 0 || k16 != 0);
+          }
+        mma_commit<false>(smem_u32(&ctl.done[step & 1]));
+      }
+      __syncwarp();
     };
     cp_wait<0>();
     fence_async();
     __syncthreads();
-    if (threadIdx.x == 0) multiply(0);
+    if (warp == 0) multiply(0);
     if (steps > 1) fill(1);
     cp_commit();
     const float scale = g.scales ? g.scales[t.expert] : 1.0f;
@@ -610,7 +622,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
       tmem_fence_before();
       if (!__syncthreads_and(ok)) break;
       tmem_fence_after();
-      if (threadIdx.x == 0 && step + 1 < steps) multiply(step + 1);
+      if (warp == 0 && step + 1 < steps) multiply(step + 1);
       if (step + 2 < steps) fill(step + 2);
       cp_commit();
       uint32_t f[32];
@@ -644,7 +656,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
 //   joining warps  32 rows and 32 columns each: a thread reads its row of a step's sums from tensor memory, joins it with y in
 //                  a slot of shared memory and writes the result over y there.
 //   issuing warp   loads B by TMA, two or three steps ahead, and issues the MMAs.
-//   copying warps  y into the slots, by asynchronous 16-byte copies as far ahead as there are slots, and out from them: 16
+//   copying warps  y into the slots, by asynchronous 16-byte copies as far ahead as there are slots, and out from them: 32
 //                  rows each, whole lines at a time (the rows of a tile may be any tokens).
 // What was measured for 8192 x 14336: rows loaded and stored by the joining threads, 32 bytes of a row at a time, 111 us
 // (each asks the L2 for a single sector); a bulk copy of 256 bytes a row each way 470 us (some 60 cycles a copy).
@@ -656,6 +668,7 @@ template <int kBn>
 __global__ void __launch_bounds__(kBn * 4 + 32 + kCopyThreads, 1)
 expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ TileParams p) {
   constexpr int kJoin = kBn * 4, kJoinWarps = kJoin / 32;
+  constexpr int kMostK = kBn == 128 ? 4 : kBn == 64 ? 12 : 16;  // K steps of the ranks that take this width (launch_sorted)
   constexpr uint32_t kPitch = kBn * 2 + 16, kSlotBytes = kTileRows * kPitch;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TileCtl ctl;
@@ -674,8 +687,8 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
   auto wait = [&](uint64_t* bar, uint32_t it) {  // the it-th step's phase of a pair of barriers
     return mbar_wait_short(smem_u32(bar + (it & 1u)), (it >> 1) & 1u, &ctl.abort_flag, &g_lora_error);
   };
-  auto wait_ring = [&](uint64_t* bars, uint32_t it, int n) {  // of a ring of n
-    return mbar_wait_short(smem_u32(bars + it % uint32_t(n)), (it / uint32_t(n)) & 1u, &ctl.abort_flag, &g_lora_error);
+  auto wait_at = [&](uint64_t* bars, const Place& a) {
+    return mbar_wait_short(smem_u32(bars + a.i), a.parity, &ctl.abort_flag, &g_lora_error);
   };
 
   if (warp > kJoinWarps) {
@@ -704,10 +717,11 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
     const uint32_t mine = slots_at + uint32_t(first + at_row) * kPitch + at_col * 2u;
     Walk in = {begin}, out = {begin};
     bool more = enter(in), left = enter(out);
-    uint32_t n_in = 0, n_out = 0;
+    Place in_at, out_at;
+    int held = 0;  // slots that were loaded and not yet stored
     while (left) {
-      while (more && n_in < n_out + uint32_t(p.slots)) {
-        const uint32_t slot = n_in % uint32_t(p.slots), to = mine + slot * kSlotBytes;
+      for (; more && held < p.slots; ++held, in_at.next(p.slots)) {
+        const uint32_t to = mine + uint32_t(in_at.i) * kSlotBytes;
         const int col = in.s * kBn + at_col;
 #pragma unroll
         for (int i = 0; i < kTimes; ++i) {
@@ -716,12 +730,11 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
                          :: "r"(to + uint32_t(i * kRowsAt) * kPitch), "l"(g.y + token * g.ldy + col) : "memory");
         }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(smem_u32(&ctl.y_in[slot])) : "memory");
-        ++n_in;
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(smem_u32(&ctl.y_in[in_at.i])) : "memory");
         if (++in.s == in.s1) more = enter(in);
       }
-      if (!__all_sync(0xffffffffu, wait_ring(ctl.y_out, n_out, p.slots))) break;
-      const uint32_t from = mine + (n_out % uint32_t(p.slots)) * kSlotBytes;
+      if (!__all_sync(0xffffffffu, wait_at(ctl.y_out, out_at))) break;
+      const uint32_t from = mine + uint32_t(out_at.i) * kSlotBytes;
       const int col = out.s * kBn + at_col;
 #pragma unroll
       for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
@@ -734,11 +747,16 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
           if (token >= 0 && col < N) *reinterpret_cast<uint4*>(g.out + token * g.ldo + col) = v[i];
         }
       }
-      ++n_out;
+      --held;
+      out_at.next(p.slots);
       if (++out.s == out.s1) left = enter(out);
     }
   } else {
-    uint32_t it = 0, slot_it = 0;  // steps with an adapter, and all that pass the slots, so far
+    uint32_t it = 0;        // steps with an adapter so far
+    Place slot, filled, used;  // of all steps that pass the slots; of B, filled and multiplied
+    // descriptors of v and of B; K steps of 16 and tiles of 64 lie at fixed distances (in 16-byte units)
+    const uint64_t v_desc = make_sdesc(v_hi), b_desc = make_sdesc(b_at);
+    const uint32_t lo_part = uint32_t(rk) * (kXBytes >> 4);
     bool ok = true;
     for (int64_t u = begin; u < end;) {
       const int tile = int(u / steps), s0 = int(u - int64_t(tile) * steps), s1 = int(min(int64_t(steps), s0 + (end - u)));
@@ -747,23 +765,27 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       const int rows = min(kTileRows, t.row_end - t.row0);
       if (t.expert >= g.adapters) {  // no adapter: y passes the slots as it is
         if (g.out != g.y && warp < kJoinWarps)
-          for (int s = s0; ok && s < s1; ++s, ++slot_it) {
-            if (!(ok = __all_sync(0xffffffffu, wait_ring(ctl.y_in, slot_it, p.slots)))) break;
-            if (lane == 0) mbar_arrive(smem_u32(&ctl.y_out[slot_it % uint32_t(p.slots)]));
+          for (int s = s0; ok && s < s1; ++s, slot.next(p.slots)) {
+            if (!(ok = __all_sync(0xffffffffu, wait_at(ctl.y_in, slot)))) break;
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.y_out[slot.i]));
           }
         continue;
       }
-      auto fill = [&](int step, uint32_t at) {
-        const uint32_t buf = at % uint32_t(p.b_bufs), bar = smem_u32(&ctl.loaded[buf]);
-        mbar_arrive_expect_tx(bar, b_bytes);
-        for (int i = 0; i < rk; ++i)
-          tma_load_3d(b_at + buf * b_bytes + uint32_t(i) * (kBn * 128u), &tmap_b, bar, i * 128, step * kBn, t.expert);
+      auto fill = [&](int step) {  // by the issuing warp
+        if (elect_one()) {
+          const uint32_t bar = smem_u32(&ctl.loaded[filled.i]);
+          mbar_arrive_expect_tx(bar, b_bytes);
+          for (int i = 0; i < rk; ++i)
+            tma_load_3d(b_at + uint32_t(filled.i) * b_bytes + uint32_t(i) * (kBn * 128u), &tmap_b, bar, i * 128, step * kBn,
+                        t.expert);
+        }
+        __syncwarp();
+        filled.next(p.b_bufs);
       };
       if (warp == kJoinWarps) {
-        if (lane == 0 && ok) {  // the buffers are free behind the last tile's last MMAs
-          if (it >= 1) ok = wait(ctl.done, it - 1);
-          for (int i = 0; ok && i < p.b_bufs - 1 && s0 + i < s1; ++i) fill(s0 + i, it + i);
-        }
+        // the buffers are free behind the last tile's last MMAs
+        ok = __all_sync(0xffffffffu, ok && (it == 0 || wait(ctl.done, it - 1)));
+        for (int i = 0; ok && i < p.b_bufs - 1 && s0 + i < s1; ++i) fill(s0 + i);
       } else {
         // all of the last tile's MMAs are done: each warp waited for its last step
         put_v(p, t, rows, v_hi, v_lo, kJoin);
@@ -774,34 +796,41 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         break;
       }
       if (warp == kJoinWarps) {
-        if (lane == 0) {
-          for (int s = s0; s < s1 && ok; ++s, ++it) {
-            ok = wait_ring(ctl.loaded, it, p.b_bufs) && (it < 2 || wait(ctl.read, it - 2));
-            if (!ok) break;
-            tmem_fence_after();
-            const uint32_t b = b_at + it % uint32_t(p.b_bufs) * b_bytes, d = ctl.tmem_base + (it & 1u) * kBn;
-            for (int part = 0; part < 2; ++part)
-              for (int k16 = 0; k16 < p.rp / 16; ++k16) {
-                const uint64_t ad = make_sdesc((part ? v_lo : v_hi) + uint32_t(k16 >> 2) * kXBytes) + uint64_t((k16 & 3) * 2);
-                const uint64_t bd = make_sdesc(b + uint32_t(k16 >> 2) * (kBn * 128u)) + uint64_t((k16 & 3) * 2);
-                mma_bf16(d, ad, bd, idesc_of(kBn), part != 0 || k16 != 0);
+        // (the warp stays together around the one lane that issues)
+        for (int s = s0; s < s1; ++s, ++it) {
+          ok = __all_sync(0xffffffffu, wait_at(ctl.loaded, used) && (it < 2 || wait(ctl.read, it - 2)));
+          if (!ok) break;
+          tmem_fence_after();
+          if (elect_one()) {
+            // (straight code: a thread's chain of address arithmetic around eight MMAs took 2000 cycles a step)
+            const uint64_t b = b_desc + uint32_t(used.i) * (b_bytes >> 4);
+            const uint32_t d = ctl.tmem_base + (it & 1u) * kBn;
+#pragma unroll
+            for (int i = 0; i < kMostK; ++i) {
+              if (i < p.rp / 16) {
+                const uint64_t a = v_desc + uint32_t((i >> 2) * (kXBytes >> 4) + (i & 3) * 2);
+                const uint64_t bi = b + uint32_t((i >> 2) * (kBn * 128 >> 4) + (i & 3) * 2);
+                mma_bf16(d, a, bi, idesc_of(kBn), i != 0);
+                mma_bf16(d, a + lo_part, bi, idesc_of(kBn), 1);
               }
-            mma_commit<false>(smem_u32(&ctl.done[it & 1u]));
-            // B as far ahead as there are buffers: the next to fill is that of the step before this one
-            const int ahead = s + p.b_bufs - 1;
-            if (ahead < s1) {
-              if (s > s0) ok = wait(ctl.done, it - 1);
-              if (ok) fill(ahead, it + p.b_bufs - 1);
             }
+            mma_commit<false>(smem_u32(&ctl.done[it & 1u]));
+          }
+          __syncwarp();
+          used.next(p.b_bufs);
+          // B as far ahead as there are buffers: the next to fill is that of the step before this one
+          const int ahead = s + p.b_bufs - 1;
+          if (ahead < s1) {
+            if (s > s0) ok = __all_sync(0xffffffffu, wait(ctl.done, it - 1));
+            if (!ok) break;
+            fill(ahead);
           }
         }
-        it = __shfl_sync(0xffffffffu, it, 0);
-        ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
         continue;
       }
       const int row = (warp & 3) * 32 + lane, group = warp >> 2;  // columns [32 group, 32 group + 32)
       const float scale = g.scales ? g.scales[t.expert] : 1.0f;
-      for (int s = s0; s < s1; ++s, ++it, ++slot_it) {
+      for (int s = s0; s < s1; ++s, ++it, slot.next(p.slots)) {
         ok = ok && wait(ctl.done, it);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         tmem_fence_after();
@@ -810,9 +839,8 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         tmem_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl.read[it & 1u]));
-        if (!(ok = __all_sync(0xffffffffu, wait_ring(ctl.y_in, slot_it, p.slots)))) break;
-        const uint32_t slot = slot_it % uint32_t(p.slots);
-        const uint32_t at = slots_at + slot * kSlotBytes + uint32_t(row) * kPitch + uint32_t(group) * 64u;
+        if (!(ok = __all_sync(0xffffffffu, wait_at(ctl.y_in, slot)))) break;
+        const uint32_t at = slots_at + uint32_t(slot.i) * kSlotBytes + uint32_t(row) * kPitch + uint32_t(group) * 64u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint4 v = lds128(at + i * 16);
@@ -825,12 +853,12 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
           sts128(at + i * 16, make_uint4(o[0], o[1], o[2], o[3]));
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.y_out[slot]));
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.y_out[slot.i]));
       }
     }
     if (!ok && threadIdx.x == kJoin)  // nothing of a load may land after the CTA has left
-      for (uint32_t i = it; i < it + uint32_t(p.b_bufs); ++i)
-        mbar_wait_bounded(smem_u32(&ctl.loaded[i % uint32_t(p.b_bufs)]), (i / uint32_t(p.b_bufs)) & 1u, nullptr, &g_lora_error);
+      for (; used.i != filled.i || used.parity != filled.parity; used.next(p.b_bufs))
+        mbar_wait_bounded(smem_u32(&ctl.loaded[used.i]), used.parity, nullptr, &g_lora_error);
   }
   __syncwarp();
   tile_end(&ctl, p.tmem_cols);
