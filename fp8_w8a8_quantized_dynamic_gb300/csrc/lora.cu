@@ -8,6 +8,9 @@
 // y + s B v, whose time is the stream of y. v is fp32 between the two; the tensor core takes it as the sum of two bf16
 // numbers (16 bits of its fraction), against B's exact bf16 values.
 //
+// MMAs are issued by one lane of a warp that stays together (elect.sync), never by a lane that runs a loop of its own: that
+// form, with the MMAs of a step in straight code, ended in an illegal instruction.
+//
 // Every wait is bounded; on expiry the kernel records an error, leaves its loop and stores nothing more.
 
 #include "lora.h"
@@ -328,7 +331,7 @@ struct TileParams {
   uint32_t tmem_cols;
 };
 
-constexpr int kCopyThreads = 128;  // expand: those that copy y and out
+constexpr int kCopyThreads = 256;  // expand: those that copy y and out
 constexpr int kCopyRows = kTileRows / (kCopyThreads / 32);  // of a warp
 
 struct TileCtl {
@@ -361,6 +364,7 @@ __device__ __forceinline__ void tile_begin(TileCtl* ctl, uint32_t cols, int load
     fence_async();
   }
   if (threadIdx.x < 32) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(&ctl->tmem_base)), "r"(cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -469,6 +473,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
         const uint32_t from = ctl.tmem_base + (uint32_t((warp & 3) * 32) << 16);
         for (int c = (warp >> 2) * 32; warp < kTileThreads / 32 && c < p.rp; c += 64) {
           uint32_t f[32];
+          __syncwarp();
           tmem_ld32(from + c, f);
           if (row < rows) {
 #pragma unroll
@@ -628,6 +633,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
       uint32_t f[32];
 #pragma unroll
       for (int h = 0; h < kParts; ++h) {
+        __syncwarp();
         if (h * kSc % 32 == 0)
           tmem_ld32(ctl.tmem_base + uint32_t(step & 1) * kBn + (uint32_t(quarter * 32) << 16) + half * (kBn / 2) + h * kSc, f);
 #pragma unroll
@@ -656,7 +662,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
 //   joining warps  32 rows and 32 columns each: a thread reads its row of a step's sums from tensor memory, joins it with y in
 //                  a slot of shared memory and writes the result over y there.
 //   issuing warp   loads B by TMA, two or three steps ahead, and issues the MMAs.
-//   copying warps  y into the slots, by asynchronous 16-byte copies as far ahead as there are slots, and out from them: 32
+//   copying warps  y into the slots, by asynchronous 16-byte copies as far ahead as there are slots, and out from them: 16
 //                  rows each, whole lines at a time (the rows of a tile may be any tokens).
 // What was measured for 8192 x 14336: rows loaded and stored by the joining threads, 32 bytes of a row at a time, 111 us
 // (each asks the L2 for a single sector); a bulk copy of 256 bytes a row each way 470 us (some 60 cycles a copy).

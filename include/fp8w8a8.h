@@ -411,7 +411,7 @@ fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int64_t ldx
  *
  * fp8_moe_dispatch: pair (t, j) with ids[t, j] in [0, E) gets row pos[t, j] of xs, rows sorted by expert and, within one,
  * by t and j; any other id gets pos -1 and no row. offsets[e] is expert e's first row, offsets[E] the number
- * of rows; xs[pos[t, j]] = x[t]. xs has T * k rows; those from offsets[E] on are left as they were. ids and pos int32
+ * of rows; xs[pos[t, j]] = x[t]. xs has T * k rows and may not overlap x; those from offsets[E] on are left as they were. ids and pos int32
  * [T, k], offsets int32 [E + 1], in device memory. ws: >= fp8_moe_dispatch_workspace_bytes, 256-byte aligned.
  */
 size_t fp8_moe_dispatch_workspace_bytes(int64_t T, int64_t k, int64_t E);
@@ -420,7 +420,7 @@ fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H, int64_
                             size_t ws_bytes, fp8_stream_t stream);
 
 /* y[t] = sum_j weights[t, j] ys[pos[t, j]] over the pairs with pos in [0, R), in the order of j, in fp32 with one
- * rounding; a token with none gets zeros. weights fp32 [T, k], or NULL for ones. */
+ * rounding; a token with none gets zeros. weights fp32 [T, k], or NULL for ones. y may not overlap ys. */
 fp8_status fp8_moe_combine(const void* ys, int f32, int64_t R, int64_t H, int64_t ldys, const int32_t* pos,
                            const float* weights, int64_t T, int64_t k, void* y, int64_t ldy, fp8_stream_t stream);
 
@@ -445,9 +445,8 @@ fp8_status fp8_moe_dispatch_grad(const void* dxs, int f32, int64_t R, int64_t H,
  * A x are fp32 (for B's product A x is the sum of two bf16 numbers, off by 2^-16);
  * the only rounding to bf16 is that of out. Results do not depend
  * on timing. A NaN or an infinity stays with the tokens of its row or
- * adapter. out may be y (with the same stride), else may not overlap it. A
- * and B are weights to the launch ordering above. ws: >=
- * fp8_lora_workspace_bytes, 256-byte aligned. Limits: r 1 to 256, L <= 511, K
+ * adapter. out may be y (with the same stride), else may not overlap it, nor
+ * anything else that is read. ws: >= fp8_lora_workspace_bytes, 256-byte aligned. Limits: r 1 to 256, L <= 511, K
  * and N <= 2^30 (FP8_ERR_INVALID_ARG).
  * ---------------------------------------------------------------------------
  */
@@ -476,8 +475,7 @@ fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_t ldy, c
  * rows whose squares pass fp32's range are normalised as the formula has it. A
  * NaN or an infinity in a row makes NaN of what it multiplies in that row and
  * of no other row. eps > 0, scale finite, H <= 32768
- * (FP8_ERR_INVALID_ARG). post_w and w are weights to the launch ordering above,
- * gate is an activation.
+ * (FP8_ERR_INVALID_ARG).
  */
 fp8_status fp8_residual_norm(const void* y_bf16, int64_t M, int64_t H, int64_t ldy, const void* post_w_bf16,
                              const void* gate_bf16, int64_t ldg, float scale, const void* residual_bf16,

@@ -20,13 +20,14 @@ def rounded_bf16(y: np.ndarray, err: np.ndarray) -> np.ndarray:
 def _inverse_rms(x: np.ndarray, err: np.ndarray, eps: float):
     """(1 / sqrt(mean x^2 + eps), its relative bound) per row, for x off by at most err.
 
-    The kernel's sum of squares: at most 32 fmas of one thread, five halvings over its warp's lanes and at most 32 warps:
-    69 roundings of positive sums; then the division by the count, the addition of eps, the root and the reciprocal, one
-    each. The root halves what came before it.
+    The kernel's sum of squares: two chains of at most eight fmas of packed pairs in a thread, their sum and the pair's, five
+    halvings over its warp's lanes, and at most 32 warps' by fours (two and eight): 25 roundings of positive sums; then the
+    rounded 1 / count, and one fma with it and eps: 27. The root halves what came before it, and is itself off by at most two
+    units in the last place (two halves each).
     """
     mean = np.mean(x * x, axis=1, keepdims=True) + eps
     inv = 1.0 / np.sqrt(mean)
-    rel = (71 / 2 + 2) * U + np.mean(np.abs(x) * err + err * err, axis=1, keepdims=True) * inv * inv
+    rel = (27 / 2 + 4) * U + np.mean(np.abs(x) * err + err * err, axis=1, keepdims=True) * inv * inv
     return inv, rel
 
 
