@@ -17,11 +17,18 @@
 namespace fp8k {
 namespace moe {
 
-// CTAs that sort the pairs; more than one need their counts first (the whole layer, experts of 2048 x
-// 1408, in us: 4096 pairs 131.7, by one CTA 134.5; 8192 pairs 161.1 and 170.8).
+// One CTA, a cluster, or as many as their pairs fill after a launch that counts them. The sort and the copy of narrow rows, 64
+// experts, in us, by a cluster (one CTA; counts): 1032 pairs 7.0 (7.5; 8.6), 2048 7.9 (9.9; 10.1), 8192 9.5 (-; 10.6), 16384
+// 11.3 (-; 10.4), 65536 21.7 (-; 11.9).
+PlanBy plan_by(int64_t pairs) {
+  return pairs <= kPlanPairs ? PlanBy::kAlone : pairs <= kPlanClusterPairs ? PlanBy::kCluster : PlanBy::kCounts;
+}
 int plan_ctas(int64_t pairs) {
-  if (pairs <= 2 * kPlanPairs) return 1;  // a second launch costs more than it saves
   return int(std::min<int64_t>(kPlanMaxCtas, (pairs + kPlanPairs - 1) / kPlanPairs));
+}
+
+size_t plan_counts_bytes(int64_t pairs, int64_t experts) {
+  return plan_by(pairs) == PlanBy::kCounts ? size_t(plan_ctas(pairs)) * size_t(experts) * sizeof(int) : 0;
 }
 
 namespace {
@@ -39,10 +46,12 @@ fp8_status launch_plan(const Plan& p, cudaStream_t st) {
                            "plan smem attribute") == cudaSuccess;
       }))
     return FP8_ERR_CUDA;
-  const int ctas = plan_ctas(p.pairs);
-  if (ctas > 1)
+  const PlanBy by = plan_by(p.pairs);
+  const int ctas = by == PlanBy::kAlone ? 1 : by == PlanBy::kCluster ? kPlanCluster : plan_ctas(p.pairs);
+  if (by == PlanBy::kCounts)
     FP8_TRY(launch(plan_count_kernel, dim3(ctas), dim3(kPlanThreads), 0, st, true, dim3(1, 1, 1), p));
-  return launch(plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, st, true, dim3(1, 1, 1), p, int(ctas > 1));
+  return launch(plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, st, true,
+                dim3(by == PlanBy::kCluster ? kPlanCluster : 1, 1, 1), p, by);
 }
 
 }  // namespace moe
@@ -200,7 +209,7 @@ MoeWs moe_ws(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
     w.lds = (w.pairs + 3) / 4 * 4;
     w.n_tiles = c.take(4);
     w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
-    w.counts = c.take(moe::plan_ctas(w.pairs) > 1 ? size_t(moe::plan_ctas(w.pairs)) * size_t(E) * 4 : 0);
+    w.counts = c.take(moe::plan_counts_bytes(w.pairs, E));
     w.pos = c.take(pairs * 4);
     w.y = c.take(pairs * size_t(w.ldy) * 4);
     w.qx = c.take(size_t(block::gemm_held_rows(w.pairs, w.ldx)) * size_t(w.ldx));
@@ -591,8 +600,7 @@ FP8_API fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int
 
 FP8_API size_t fp8_moe_dispatch_workspace_bytes(int64_t T, int64_t k, int64_t E) {
   if (!pair_sizes_ok(T, k) || E < 1 || E > moe::kMaxExperts) return 0;
-  const int ctas = moe::plan_ctas(T * k);
-  return ctas > 1 && !few_pairs(T, k) ? round_up_256(size_t(ctas) * size_t(E) * 4) : 0;
+  return few_pairs(T, k) ? 0 : round_up_256(moe::plan_counts_bytes(T * k, E));
 }
 
 FP8_API fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H, int64_t ldx, const int32_t* ids,

@@ -138,7 +138,7 @@ LoraWs lora_ws(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
   w.splits = lora::splits_of(M, K, L);
   w.n_tiles = c.take(4);
   w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
-  w.counts = c.take(moe::plan_ctas(M) > 1 ? size_t(moe::plan_ctas(M)) * size_t(L + 1) * 4 : 0);
+  w.counts = c.take(moe::plan_counts_bytes(M, L + 1));
   w.pos = c.take(size_t(M) * 4);
   w.order = c.take(size_t(M) * 4);
   w.v = c.take(size_t(w.splits) * size_t(M) * size_t(lora::padded_rank(r)) * 4);

@@ -294,6 +294,11 @@ constexpr int kPlanWarps = kPlanThreads / 32;
 
 constexpr int kPlanPairs = 1024;  // pairs of one CTA, about (a step of every warp)
 constexpr int kPlanMaxCtas = 128;
+constexpr int kPlanCluster = 8;  // CTAs that exchange their counts through distributed shared memory
+constexpr int kPlanClusterPairs = 8192;  // that they sort, at most
+
+// Where a CTA learns of the other CTAs' pairs: there are none, from its cluster, from plan_count_kernel.
+enum class PlanBy : int { kAlone, kCluster, kCounts };
 
 // The pairs [begin, end) of CTA `part` of `parts`, whole warp steps.
 __device__ __forceinline__ void plan_range(int64_t pairs, int part, int parts, int64_t& begin, int64_t& end) {
@@ -326,18 +331,18 @@ plan_count_kernel(const __grid_constant__ Plan p) {
 
 // Order of the routed pairs: pair i (= token * k + j) with expert ids[i] in [0, experts) gets row
 // pos[i], rows sorted by expert and, within one, by pair (stable, so nothing depends on timing);
-// any other id gives -1, or counts as expert `spare`. Then the row tiles and the experts' first rows (where wanted). A CTA's warps count their contiguous shares of the CTA's pairs by expert in
-// shared memory (equal ids of a step are found by a warp match), the counts are scanned over warps,
-// CTAs (from plan_count_kernel; one CTA needs none) and experts, and a second walk hands out rows.
-// One CTA sorts 65536 pairs in 109 us, 64 CTAs in 11 us.
+// any other id gives -1, or counts as expert `spare`. Then the row tiles and the experts' first rows (where wanted). A
+// CTA's warps count their contiguous shares of the CTA's pairs by expert in shared memory (equal ids of a step are found by a
+// warp match), the counts are scanned over warps, CTAs (PlanBy) and experts, and a second walk hands out rows.
+// One CTA sorts 65536 pairs in 109 us, 64 CTAs in 8.4 us after counting in 3.6.
 __global__ void __launch_bounds__(kPlanThreads, 1)
-plan_kernel(const __grid_constant__ Plan p, int has_counts) {
+plan_kernel(const __grid_constant__ Plan p, PlanBy by) {
   const int experts = p.experts;
-  const int* counts = has_counts ? p.counts : nullptr;
   extern __shared__ int count[];  // [kPlanWarps][experts], then [experts] first rows
   int* total = count + kPlanWarps * experts;
   __shared__ int warp_sum[2][kPlanWarps];
-  __shared__ int elsewhere[2][kMaxExperts];  // pairs of each expert in the CTAs before this one, and in all
+  __shared__ int in_cta[kMaxExperts];        // pairs of each expert in this CTA
+  __shared__ int elsewhere[2][kMaxExperts];  // in the CTAs before this one, and in all
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -357,37 +362,48 @@ plan_kernel(const __grid_constant__ Plan p, int has_counts) {
     __syncwarp();
   }
   __syncthreads();
-  // this CTA's place: every expert's pairs in the CTAs before it, and in all of them, by as many threads as there are
-  if (counts != nullptr) {
-    const int wide = experts <= 32 ? 32 : 1 << (32 - __clz(experts - 1)), e = threadIdx.x & (wide - 1);
-    if (e < experts) {
-      int before = 0, all = 0;
-#pragma unroll 4
-      for (int c = threadIdx.x / wide; c < int(gridDim.x); c += kPlanThreads / wide) {
-        const int v = counts[c * experts + e];
-        before += c < int(blockIdx.x) ? v : 0;
-        all += v;
-      }
-      atomicAdd(&elsewhere[0][e], before);  // sums of whole numbers: any order
-      atomicAdd(&elsewhere[1][e], all);
-    }
-    __syncthreads();
-  }
-  // experts are scanned in order: thread e < experts sums its column over the warps
-  int tot = 0;
+  // thread e < experts sums its column over the warps
+  int mine_in_cta = 0;
   if (int(threadIdx.x) < experts) {
-    int before = elsewhere[0][threadIdx.x];
     for (int w0 = 0; w0 < kPlanWarps; w0 += 8) {
       int v[8];
 #pragma unroll
       for (int w = 0; w < 8; ++w) v[w] = count[(w0 + w) * experts + threadIdx.x];
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
-        count[(w0 + w) * experts + threadIdx.x] = before;
-        before += v[w];
+        count[(w0 + w) * experts + threadIdx.x] = mine_in_cta;
+        mine_in_cta += v[w];
       }
     }
-    tot = counts == nullptr ? before : elsewhere[1][threadIdx.x];
+    in_cta[threadIdx.x] = mine_in_cta;
+  }
+  // this CTA's place: every expert's pairs in the CTAs before it, and in all of them
+  int before = 0, tot = mine_in_cta;
+  if (by == PlanBy::kCluster) {
+    pair_sync();  // the whole cluster
+    tot = 0;
+    if (int(threadIdx.x) < experts)
+      for (int c = 0; c < int(gridDim.x); ++c) {
+        const int v = int(ld_cluster_u32(map_to_rank(smem_u32(&in_cta[threadIdx.x]), c)));
+        before += c < int(blockIdx.x) ? v : 0;
+        tot += v;
+      }
+  } else if (by == PlanBy::kCounts) {  // (by as many threads as there are)
+    const int wide = experts <= 32 ? 32 : 1 << (32 - __clz(experts - 1)), e = threadIdx.x & (wide - 1);
+    if (e < experts) {
+      int b = 0, all = 0;
+#pragma unroll 4
+      for (int c = threadIdx.x / wide; c < int(gridDim.x); c += kPlanThreads / wide) {
+        const int v = p.counts[c * experts + e];
+        b += c < int(blockIdx.x) ? v : 0;
+        all += v;
+      }
+      atomicAdd(&elsewhere[0][e], b);  // sums of whole numbers: any order
+      atomicAdd(&elsewhere[1][e], all);
+    }
+    __syncthreads();
+    before = threadIdx.x < kMaxExperts ? elsewhere[0][threadIdx.x] : 0;
+    tot = int(threadIdx.x) < experts ? elsewhere[1][threadIdx.x] : 0;
   }
   const int my_tiles = (tot + block::kRowTile - 1) / block::kRowTile;
   int rows_before = tot, tiles_before = my_tiles;  // inclusive scans over the experts
@@ -406,7 +422,7 @@ plan_kernel(const __grid_constant__ Plan p, int has_counts) {
   rows_before += base_r - tot;
   tiles_before += base_t - my_tiles;
   if (int(threadIdx.x) < experts) {
-    total[threadIdx.x] = rows_before;
+    total[threadIdx.x] = rows_before + before;
     // the CTAs share out an expert's tiles
     for (int j = blockIdx.x; p.tiles != nullptr && j < my_tiles; j += gridDim.x) {
       const int r0 = rows_before + j * block::kRowTile;
@@ -431,6 +447,7 @@ plan_kernel(const __grid_constant__ Plan p, int has_counts) {
     if (i + lane < end) p.pos[i + lane] = d;
     if (d >= 0 && p.order != nullptr) p.order[d] = int(i) + lane;
   }
+  if (by == PlanBy::kCluster) pair_sync();  // no CTA leaves while another reads its sums
 }
 
 constexpr int kSumThreads = 256;

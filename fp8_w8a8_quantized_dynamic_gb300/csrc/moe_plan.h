@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 
 #include "api_common.h"
@@ -12,15 +13,15 @@
 namespace fp8k {
 namespace moe {
 
-// CTAs that sort the pairs; more than one need their counts first.
-int plan_ctas(int64_t pairs);
+// Workspace for the counts of many pairs' CTAs (0 for few pairs, which need none).
+size_t plan_counts_bytes(int64_t pairs, int64_t experts);
 
 struct Plan {
   const int32_t* ids;
   int64_t pairs;
   int experts;
   int spare;               // the expert that any id outside [0, experts) counts as; -1: such pairs have no row
-  int* counts;             // [plan_ctas(pairs)][experts] where that is more than one
+  int* counts;             // plan_counts_bytes(pairs, experts)
   int* pos;                // row of each pair
   // what else is wanted; null where not
   int* order;              // pair of each row
