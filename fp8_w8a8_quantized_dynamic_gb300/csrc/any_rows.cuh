@@ -1,0 +1,85 @@
+// Rows of 16-bit values that start and end anywhere, eight values at a time in whole 16-byte pieces.
+#pragma once
+
+#include "device_common.cuh"
+
+namespace fp8k {
+
+// (not through the read-only path: rows may be written over)
+__device__ __forceinline__ uint4 load_piece(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// Sixteen values a (low), b: the eight from the at-th on, at < 8.
+__device__ __forceinline__ uint4 eight_from(uint4 a, uint4 b, int at) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = at & 4 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = at & 2 ? w[i + 1] : w[i];
+  const int bits = at & 1 ? 16 : 0;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// The first n values of v, zeros behind them.
+__device__ __forceinline__ uint4 first_of(uint4 v, int n) {
+  auto keep = [&](uint32_t w, int i) { return i + 1 < n ? w : i < n ? w & 0xFFFFu : 0u; };
+  return make_uint4(keep(v.x, 0), keep(v.y, 2), keep(v.z, 4), keep(v.w, 6));
+}
+
+// Values c .. c + 7 of a row, c < cols, zeros from cols on: from the one or two whole pieces that hold them. Each of those
+// holds one of the row's values, so that all of it may be read.
+__device__ __forceinline__ uint4 load8_any(const uint16_t* row, int64_t c, int64_t cols) {
+  const uint16_t* first = row + c;
+  const int at = int(reinterpret_cast<uintptr_t>(first) >> 1) & 7;
+  const uint4* piece = reinterpret_cast<const uint4*>(first - at);
+  const int n = int(cols - c < 8 ? cols - c : 8);
+  const uint4 a = load_piece(piece);
+  if (at == 0) return n < 8 ? first_of(a, n) : a;
+  const uint4 b = at + n > 8 ? load_piece(piece + 1) : make_uint4(0, 0, 0, 0);
+  const uint4 v = eight_from(a, b, at);
+  return n < 8 ? first_of(v, n) : v;
+}
+
+__device__ __forceinline__ void store_some(uint16_t* p, uint4 v, int from, int to) {  // values [from, to) of eight
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i >= from && i < to) p[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+}
+
+// Stores values c .. c + 7 of a row (those before cols), a multiple of eight a lane: all lanes of the warp come here, lane
+// i + 1 with the eight after lane i's wherever both are of one row (`live`: this lane has any). A lane stores the whole piece
+// that ends with its own values and takes the rest of it from the lane before; the ends of the warp's run of a row are
+// stored by values.
+__device__ __forceinline__ void store8_any(uint16_t* row, int64_t c, int64_t cols, uint4 v, bool live) {
+  const int lane = threadIdx.x & 31;
+  uint4 before;
+  before.x = __shfl_up_sync(0xffffffffu, v.x, 1);
+  before.y = __shfl_up_sync(0xffffffffu, v.y, 1);
+  before.z = __shfl_up_sync(0xffffffffu, v.z, 1);
+  before.w = __shfl_up_sync(0xffffffffu, v.w, 1);
+  if (!live) return;
+  uint16_t* first = row + c;
+  const int at = int(reinterpret_cast<uintptr_t>(first) >> 1) & 7;  // values of the piece that lie before c
+  const int n = int(cols - c < 8 ? cols - c : 8);
+  if (at == 0) {
+    if (n == 8)
+      *reinterpret_cast<uint4*>(first) = v;
+    else
+      store_some(first, v, 0, n);
+    return;
+  }
+  const bool joined = lane > 0 && c > 0, handed_on = lane < 31 && c + 8 < cols;
+  const uint4 piece = eight_from(before, v, 8 - at);
+  if (joined && at + n >= 8)
+    *reinterpret_cast<uint4*>(first - at) = piece;
+  else
+    store_some(first - at, piece, joined ? 0 : at, at + n < 8 ? at + n : 8);
+  if (!handed_on) store_some(first, v, 8 - at, n);
+}
+
+}  // namespace fp8k

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "api_common.h"
 #include "block_gemm.h"
@@ -251,9 +252,9 @@ fp8_status check_rows(const void* p, int f32, int64_t rows, int64_t cols, int64_
   return aligned(p, f32 ? 4 : 2) ? FP8_OK : FP8_ERR_MISALIGNED;
 }
 
-// Whether all rows start and end on 16-byte boundaries.
-bool whole_pieces(const void* p, int64_t rows, int64_t ld, int64_t cols, int size) {
-  return aligned(p, 16) && (rows <= 1 || ld * size % 16 == 0) && cols * size % 16 == 0;
+// Whether all rows start and end on boundaries of `bytes`.
+bool rows_of_pieces(int bytes, const void* p, int64_t rows, int64_t ld, int64_t cols, int size) {
+  return aligned(p, uintptr_t(bytes)) && (rows <= 1 || ld * size % bytes == 0) && cols * size % bytes == 0;
 }
 
 template <typename U>
@@ -264,6 +265,14 @@ fp8_status launch_rows_out(const void* x, int64_t row_bytes, int64_t ldx_bytes, 
                 dim3(moe::kRowThreads), 0, st, true, dim3(1, 1, 1), static_cast<const U*>(x),
                 ldx_bytes / int64_t(sizeof(U)), T, pieces, pos, int(k), rows, static_cast<U*>(xs),
                 ldxs_bytes / int64_t(sizeof(U)));
+}
+
+// (columns and row strides in 16-bit values)
+fp8_status launch_rows_out_any(const void* x, int64_t cols, int64_t ldx, int64_t T, const int* pos, int64_t k, int64_t rows,
+                               void* xs, int64_t ldxs, int sms, cudaStream_t st) {
+  return launch(moe::rows_out_any_kernel, dim3(elementwise_grid(T * ((cols + 7) / 8), moe::kRowThreads, sms, 64)),
+                dim3(moe::kRowThreads), 0, st, true, dim3(1, 1, 1), static_cast<const uint16_t*>(x), ldx, T, cols, pos,
+                int(k), rows, static_cast<uint16_t*>(xs), ldxs);
 }
 
 bool few_pairs(int64_t T, int64_t k) { return T * k <= moe::kFewPairs; }
@@ -281,24 +290,44 @@ fp8_status launch_few_rows_out(const void* x, int64_t row_bytes, int64_t ldx_byt
                 offsets, static_cast<U*>(xs), ldxs_bytes / int64_t(sizeof(U)));
 }
 
-template <typename T, int kN>
-fp8_status launch_rows_back(const void* ys, int64_t ldys, int64_t R, const int* pos, const float* weights, int64_t k,
-                            int64_t tokens, int64_t H, void* y, int64_t ldy, int sms, cudaStream_t st) {
-  return launch(moe::rows_back_kernel<T, kN>, dim3(elementwise_grid(tokens * (H / kN), moe::kRowThreads, sms, 1024)),
-                dim3(moe::kRowThreads), 0, st, true, dim3(1, 1, 1), static_cast<const T*>(ys), ldys, R, pos, weights,
-                int(k), tokens, H, static_cast<T*>(y), ldy);
+template <typename T, int kPiece, int kB>
+fp8_status launch_rows_back_of(const void* ys, int64_t ldys, int64_t R, const int* pos, const float* weights, int64_t k,
+                               int64_t tokens, int64_t H, void* y, int64_t ldy, int sms, cudaStream_t st) {
+  constexpr int kCols = moe::kColsOf<T, kPiece>;
+  const int64_t units = tokens * ((H + kCols - 1) / kCols);
+  return launch(moe::rows_back_kernel<T, kPiece, kB>,
+                dim3(elementwise_grid(units, moe::kRowThreads * moe::kRowBatch / kB, sms, 1024)), dim3(moe::kRowThreads), 0,
+                st, true, dim3(1, 1, 1), static_cast<const T*>(ys), ldys, R, pos, weights, int(k), tokens, H,
+                static_cast<T*>(y), ldy);
+}
+// Few columns in all are not shared out further: a thread each.
+template <typename T, int kPiece, typename... Args>
+fp8_status launch_rows_back(int64_t k, int64_t tokens, int64_t H, int sms, Args... args) {
+  const bool many = tokens * (H / moe::kColsOf<T, kPiece>) >= int64_t(sms) * 2048;
+  if (k == 1 && many) return launch_rows_back_of<T, kPiece, 1>(args...);
+  if (k == 2 && many) return launch_rows_back_of<T, kPiece, 2>(args...);
+  if (k <= 4) return launch_rows_back_of<T, kPiece, 4>(args...);
+  return launch_rows_back_of<T, kPiece, 8>(args...);
 }
 
-template <typename T, int kN>
-fp8_status launch_rows_back_grad(const void* dy, int64_t lddy, const void* ys, int64_t ldys, int64_t R, const int* pos,
-                                 const float* weights, int64_t k, int64_t tokens, int64_t H, void* dys, int64_t lddys,
-                                 float* dw, int sms, cudaStream_t st) {
+template <typename T, int kPiece, int kB>
+fp8_status launch_rows_back_grad_of(const void* dy, int64_t lddy, const void* ys, int64_t ldys, int64_t R, const int* pos,
+                                    const float* weights, int64_t k, int64_t tokens, int64_t H, void* dys, int64_t lddys,
+                                    float* dw, int sms, cudaStream_t st) {
+  constexpr int kCols = moe::kColsOf<T, kPiece> * (kB < 4 ? 4 / kB : 1);  // of a thread
   int per_token = 32;
-  while (per_token < moe::kRowThreads && per_token * kN < H) per_token *= 2;
+  while (per_token < moe::kRowThreads && per_token * kCols < H) per_token *= 2;
   const int per_cta = moe::kRowThreads / per_token;
-  return launch(moe::rows_back_grad_kernel<T, kN>, dim3(elementwise_grid(tokens, per_cta, sms, 64)),
+  return launch(moe::rows_back_grad_kernel<T, kPiece, kB>, dim3(elementwise_grid(tokens, per_cta, sms, 64)),
                 dim3(per_token, per_cta), 0, st, true, dim3(1, 1, 1), static_cast<const T*>(dy), lddy,
                 static_cast<const T*>(ys), ldys, R, pos, weights, int(k), tokens, H, static_cast<T*>(dys), lddys, dw);
+}
+template <typename T, int kPiece, typename... Args>
+fp8_status launch_rows_back_grad(int64_t k, Args... args) {
+  if (k == 1) return launch_rows_back_grad_of<T, kPiece, 1>(args...);
+  if (k == 2) return launch_rows_back_grad_of<T, kPiece, 2>(args...);
+  if (k <= 4) return launch_rows_back_grad_of<T, kPiece, 4>(args...);
+  return launch_rows_back_grad_of<T, kPiece, 8>(args...);
 }
 
 }  // namespace
@@ -630,12 +659,8 @@ FP8_API fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H
   }
   FP8_TRY(moe::launch_plan({ids, T * k, int(E), -1, static_cast<int*>(ws), pos, nullptr, nullptr, nullptr, offsets}, st));
   if (H == 0) return FP8_OK;
-  auto go = [&](auto piece) {
-    return launch_rows_out<decltype(piece)>(x, H * size, ldx * size, T, pos, k, T * k, xs, ldxs * size, sms, st);
-  };
-  if (any % 16 == 0) return go(uint4{});
-  if (any % 8 == 0) return go(uint2{});
-  return any % 4 == 0 ? go(uint32_t{}) : go(uint16_t{});
+  if (any % 16 == 0) return launch_rows_out<uint4>(x, H * size, ldx * size, T, pos, k, T * k, xs, ldxs * size, sms, st);
+  return launch_rows_out_any(x, H * size / 2, ldx * size / 2, T, pos, k, T * k, xs, ldxs * size / 2, sms, st);
 }
 
 FP8_API fp8_status fp8_moe_combine(const void* ys, int f32, int64_t R, int64_t H, int64_t ldys, const int32_t* pos,
@@ -651,12 +676,19 @@ FP8_API fp8_status fp8_moe_combine(const void* ys, int f32, int64_t R, int64_t H
   FP8_TRY(current_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int size = f32 ? 4 : 2;
-  const bool whole = whole_pieces(ys, R, ldys, H, size) && whole_pieces(y, T, ldy, H, size);
-  if (f32)
-    return whole ? launch_rows_back<float, 4>(ys, ldys, R, pos, weights, k, T, H, y, ldy, sms, st)
-                 : launch_rows_back<float, 1>(ys, ldys, R, pos, weights, k, T, H, y, ldy, sms, st);
-  return whole ? launch_rows_back<uint16_t, 8>(ys, ldys, R, pos, weights, k, T, H, y, ldy, sms, st)
-               : launch_rows_back<uint16_t, 1>(ys, ldys, R, pos, weights, k, T, H, y, ldy, sms, st);
+  auto on = [&](int bytes) { return rows_of_pieces(bytes, ys, R, ldys, H, size) && rows_of_pieces(bytes, y, T, ldy, H, size); };
+  const int piece = on(16) ? 16 : on(4) ? 4 : 2;
+  auto go = [&](auto launch_of) { return launch_of(k, T, H, sms, ys, ldys, R, pos, weights, k, T, H, y, ldy, sms, st); };
+  auto with = [&](auto value, auto by) {
+    return go([](int64_t k, int64_t T, int64_t H, int sms, auto... args) {
+      return launch_rows_back<decltype(value), decltype(by)::value>(k, T, H, sms, args...);
+    });
+  };
+  using std::integral_constant;
+  if (f32) return piece == 16 ? with(float(), integral_constant<int, 16>()) : with(float(), integral_constant<int, 4>());
+  return piece == 16  ? with(uint16_t(), integral_constant<int, 16>())
+         : piece == 4 ? with(uint16_t(), integral_constant<int, 4>())
+                      : with(uint16_t(), integral_constant<int, 2>());
 }
 
 FP8_API fp8_status fp8_moe_dispatch_grad(const void* dxs, int f32, int64_t R, int64_t H, int64_t lddxs,
@@ -679,12 +711,18 @@ FP8_API fp8_status fp8_moe_combine_grad(const void* dy, int f32, int64_t T, int6
   FP8_TRY(current_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int size = f32 ? 4 : 2;
-  const bool whole = whole_pieces(dy, T, lddy, H, size) && whole_pieces(ys, R, ldys, H, size) &&
-                     whole_pieces(dys, R, lddys, H, size);
-  if (f32)
-    return whole ? launch_rows_back_grad<float, 4>(dy, lddy, ys, ldys, R, pos, weights, k, T, H, dys, lddys, dw, sms, st)
-                 : launch_rows_back_grad<float, 1>(dy, lddy, ys, ldys, R, pos, weights, k, T, H, dys, lddys, dw, sms, st);
-  return whole
-             ? launch_rows_back_grad<uint16_t, 8>(dy, lddy, ys, ldys, R, pos, weights, k, T, H, dys, lddys, dw, sms, st)
-             : launch_rows_back_grad<uint16_t, 1>(dy, lddy, ys, ldys, R, pos, weights, k, T, H, dys, lddys, dw, sms, st);
+  auto on = [&](int bytes) {
+    return rows_of_pieces(bytes, dy, T, lddy, H, size) && rows_of_pieces(bytes, ys, R, ldys, H, size) &&
+           rows_of_pieces(bytes, dys, R, lddys, H, size);
+  };
+  const int piece = on(16) ? 16 : on(4) ? 4 : 2;
+  auto with = [&](auto value, auto by) {
+    return launch_rows_back_grad<decltype(value), decltype(by)::value>(k, dy, lddy, ys, ldys, R, pos, weights, k, T, H, dys,
+                                                                        lddys, dw, sms, st);
+  };
+  using std::integral_constant;
+  if (f32) return piece == 16 ? with(float(), integral_constant<int, 16>()) : with(float(), integral_constant<int, 4>());
+  return piece == 16  ? with(uint16_t(), integral_constant<int, 16>())
+         : piece == 4 ? with(uint16_t(), integral_constant<int, 4>())
+                      : with(uint16_t(), integral_constant<int, 2>());
 }

@@ -54,10 +54,13 @@ fp8_status launch_norm(const norm::Params& p, int sms, cudaStream_t st) {
 fp8_status launch_norm_any(const norm::Params& p, int sms, cudaStream_t st) {
   const int units = (p.cols + norm::kUnit - 1) / norm::kUnit;
   if (!p.vec) {
+    if (units <= 32) return launch_norm<32, 1, false>(p, sms, st);
     if (units <= 128) return launch_norm<128, 1, false>(p, sms, st);
     if (units <= 512) return launch_norm<512, 1, false>(p, sms, st);
+    if (units <= 1024) return launch_norm<1024, 1, false>(p, sms, st);
     return launch_norm<1024, 2, false>(p, sms, st);
   }
+  if (units <= 32) return launch_norm<32, 1, true>(p, sms, st);
   if (units <= 64) return launch_norm<64, 1, true>(p, sms, st);
   if (units <= 128) return launch_norm<128, 1, true>(p, sms, st);
   if (units <= 256) return launch_norm<256, 1, true>(p, sms, st);
@@ -135,7 +138,7 @@ LoraWs lora_ws(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
   LoraWs w = {};
   if (lora_by_token(M, K, N, L, r)) return w;
   w.max_tiles = M / block::kRowTile + std::min(L + 1, M);
-  w.splits = lora::splits_of(M, K, L);
+  w.splits = lora::splits_of(M, K, L, r);
   w.n_tiles = c.take(4);
   w.tiles = c.take(size_t(w.max_tiles) * sizeof(block::RowTile));
   w.counts = c.take(moe::plan_counts_bytes(M, L + 1));

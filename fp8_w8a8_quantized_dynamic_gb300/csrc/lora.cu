@@ -17,6 +17,7 @@
 
 #include <algorithm>
 
+#include "any_rows.cuh"
 #include "api_common.h"
 #include "device_cache.h"
 #include "device_common.cuh"
@@ -38,7 +39,6 @@ constexpr int kTokenWarps = kTokenThreads / 32;
 
 struct TokenParams {
   Args a;
-  int vec_x, vec_a, vec_b;  // rows start on 16-byte boundaries
   int k_slice;              // of a CTA of the cluster, a multiple of 8
   int n_slice;              // columns of a CTA
 };
@@ -98,8 +98,14 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // kLpr lanes share a row of B (eight values of the rank each). Cluster rank c sums K slice c of v = A x
 // and sends it to all of the cluster; then every CTA adds the slices in order and computes its columns.
-template <int kLpr, int kLoads>
-__global__ void __launch_bounds__(kTokenThreads, kLoads == 8 ? 2 : 4)
+// kVec: all rows start on 16-byte boundaries and are whole eights. Values beyond `end` are zeros.
+template <bool kVec>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int end) {
+  return kVec ? ld_nc_v4(row + c) : load8_any(row, c, end);
+}
+
+template <int kLpr, int kLoads, bool kVec>
+__global__ void __launch_bounds__(kTokenThreads, kLoads == 8 ? 2 : kVec ? 4 : 3)
 tokens_kernel(const __grid_constant__ TokenParams p) {
   constexpr int kU = kLpr < kLoads ? kLpr : kLoads;  // loads of a batch; a lane ends with one column of it
   constexpr int kBatches = kLoads / kU;              // batches in flight
@@ -140,7 +146,7 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
     for (int q = 0; q < kLoads; ++q) {
       const int n = base + (q / kU) * kBatchCols + (q % kU) * kRowsPerLoad + row_in_load;
       bv[q] = make_uint4(0, 0, 0, 0);
-      if (n < n1 && sub * 8 < r) bv[q] = load8_bf16(B + int64_t(n) * r, sub * 8, r, p.vec_b);
+      if (n < n1 && sub * 8 < r) bv[q] = load8<kVec>(B + int64_t(n) * r, sub * 8, r);
     }
 #pragma unroll
     for (int b = 0; b < kBatches; ++b) yv[b] = col_of(base, b) < n1 ? y[col_of(base, b)] : uint16_t(0);
@@ -159,10 +165,10 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         const int kh = k + 256 * h;
-        xv[h] = kh < k1 ? load8_bf16(x, kh, k1, p.vec_x) : make_uint4(0, 0, 0, 0);
+        xv[h] = kh < k1 ? load8<kVec>(x, kh, k1) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          av[h][i] = kh < k1 && i0 + i < i_end ? load8_bf16(A + int64_t(i0 + i) * K, kh, k1, p.vec_a) : make_uint4(0, 0, 0, 0);
+          av[h][i] = kh < k1 && i0 + i < i_end ? load8<kVec>(A + int64_t(i0 + i) * K, kh, k1) : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
@@ -205,31 +211,32 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   }
 }
 
-template <int kLpr, int kLoads>
-bool launch_tokens_of(const TokenParams& p, int groups, cudaStream_t st) {
-  return launch(tokens_kernel<kLpr, kLoads>, dim3(unsigned(kCluster * groups), unsigned(p.a.M)), dim3(kTokenThreads), 0, st,
-                true, dim3(kCluster, 1, 1), p) == FP8_OK;
+template <int kLpr, int kLoads, bool kVec>
+bool launch_tokens_of(const TokenParams& p, int64_t groups, cudaStream_t st) {
+  return launch(tokens_kernel<kLpr, kLoads, kVec>, dim3(unsigned(kCluster * groups), unsigned(p.a.M)), dim3(kTokenThreads), 0, st, true,
+                dim3(kCluster, 1, 1), p) == FP8_OK;
 }
-template <int kLoads>
-bool launch_tokens_by_rank(const TokenParams& p, int groups, cudaStream_t st) {
-  if (p.a.rank <= 8) return launch_tokens_of<1, kLoads>(p, groups, st);
-  if (p.a.rank <= 16) return launch_tokens_of<2, kLoads>(p, groups, st);
-  if (p.a.rank <= 32) return launch_tokens_of<4, kLoads>(p, groups, st);
-  if (p.a.rank <= 64) return launch_tokens_of<8, kLoads>(p, groups, st);
-  return p.a.rank <= 128 ? launch_tokens_of<16, kLoads>(p, groups, st) : launch_tokens_of<32, kLoads>(p, groups, st);
+template <int kLoads, bool kVec>
+bool launch_tokens_by_rank(const TokenParams& p, int64_t groups, cudaStream_t st) {
+  if (p.a.rank <= 8) return launch_tokens_of<1, kLoads, kVec>(p, groups, st);
+  if (p.a.rank <= 16) return launch_tokens_of<2, kLoads, kVec>(p, groups, st);
+  if (p.a.rank <= 32) return launch_tokens_of<4, kLoads, kVec>(p, groups, st);
+  if (p.a.rank <= 64) return launch_tokens_of<8, kLoads, kVec>(p, groups, st);
+  return p.a.rank <= 128 ? launch_tokens_of<16, kLoads, kVec>(p, groups, st) : launch_tokens_of<32, kLoads, kVec>(p, groups, st);
 }
 
 bool launch_tokens(const Args& a, int num_sms, cudaStream_t st) {
   TokenParams p = {};
   p.a = a;
-  p.vec_x = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0);
-  p.vec_a = aligned(a.a, 16) && a.K % 8 == 0;
-  p.vec_b = aligned(a.b, 16) && a.rank % 8 == 0;
   p.k_slice = int(((a.K + 7) / 8 + kCluster - 1) / kCluster * 8);
-  const int groups = 1;
+  // few tokens: several clusters a token, each with all of v and a share of the columns
+  const int64_t groups = std::max<int64_t>(1, std::min<int64_t>({4, 2 * num_sms / (kCluster * a.M), a.N / (kCluster * 128)}));
   p.n_slice = int((a.N + kCluster * groups - 1) / (kCluster * groups));
+  const bool vec = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0) && aligned(a.a, 16) && a.K % 8 == 0 &&
+                   aligned(a.b, 16) && a.rank % 8 == 0;
+  if (!vec) return launch_tokens_by_rank<4, false>(p, groups, st);
   // two CTAs of the deep form fit an SM, four of the other
-  return a.M * kCluster <= 2 * num_sms ? launch_tokens_by_rank<8>(p, groups, st) : launch_tokens_by_rank<4>(p, groups, st);
+  return a.M * kCluster <= 2 * num_sms ? launch_tokens_by_rank<8, true>(p, groups, st) : launch_tokens_by_rank<4, true>(p, groups, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -271,6 +278,39 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// Pieces of 16, 4 or 2 bytes, as rows start and end.
+template <int kBytes>
+struct PieceOf;
+template <>
+struct PieceOf<16> {
+  using type = uint4;
+};
+template <>
+struct PieceOf<4> {
+  using type = uint32_t;
+};
+template <>
+struct PieceOf<2> {
+  using type = uint16_t;
+};
+__device__ __forceinline__ void ld_shared_piece(uint4& v, uint32_t a) { v = lds128(a); }
+__device__ __forceinline__ void ld_shared_piece(uint32_t& v, uint32_t a) {
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ld_shared_piece(uint16_t& v, uint32_t a) {
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void st_shared_piece(uint32_t a, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" :: "r"(a), "h"(v) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint16_t* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(kBytes) : "memory");
+}
+
 // A barrier of `threads` of the block's threads; whether ok holds for all of them.
 __device__ __forceinline__ bool barrier_all(int id, int threads, bool ok) {
   uint32_t r;
@@ -297,7 +337,7 @@ __device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* row, bool li
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                  :: "r"(dst), "l"(live ? row + k : row), "r"(live ? 16u : 0u) : "memory");
   } else {
-    const uint4 v = live ? load8_bf16(row, k, K, 0) : make_uint4(0, 0, 0, 0);
+    const uint4 v = live ? load8_any(row, k, K) : make_uint4(0, 0, 0, 0);
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
   }
 }
@@ -327,7 +367,7 @@ struct TileParams {
   int stages;               // shrink
   int slots, b_bufs;        // expand: of y, of B
   int cols_per_cta;         // expand: a multiple of kBn
-  int vec_x, vec_a, vec_b, vec_y;
+  int vec_x, vec_a, vec_b;
   uint32_t tmem_cols;
 };
 
@@ -508,10 +548,21 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
     float f[8] = {};
     if (row < rows) {
       const float* from = p.s.v + int64_t(t.row0 + row) * p.rp + c * 8;
-      for (int s = 0; s < p.s.splits; ++s, from += g.M * p.rp) {
-        const float4 lo = *reinterpret_cast<const float4*>(from), hi = *reinterpret_cast<const float4*>(from + 4);
-        f[0] += lo.x, f[1] += lo.y, f[2] += lo.z, f[3] += lo.w;
-        f[4] += hi.x, f[5] += hi.y, f[6] += hi.z, f[7] += hi.w;
+      const int64_t step = g.M * p.rp;
+      for (int s0 = 0; s0 < p.s.splits; s0 += 4) {  // four splits' loads at once, added in order
+        float4 in[4][2];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const float4* at = reinterpret_cast<const float4*>(from + (s0 + s) * step);
+          const bool have = s0 + s < p.s.splits;
+          in[s][0] = have ? at[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+          in[s][1] = have ? at[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          f[0] += in[s][0].x, f[1] += in[s][0].y, f[2] += in[s][0].z, f[3] += in[s][0].w;
+          f[4] += in[s][1].x, f[5] += in[s][1].y, f[6] += in[s][1].z, f[7] += in[s][1].w;
+        }
       }
     }
     uint32_t h[4], l[4];
@@ -528,7 +579,7 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
   }
 }
 
-// out = y + s B[e] v for rows and sizes of any alignment: a tile's rows and the CTA's columns, kBn a step (64 where the
+// out = y + s B[e] v for ranks that are no multiple of eight: a tile's rows and the CTA's columns, kBn a step (64 where the
 // rank's operands leave no room for 128). While a step's sums are read, joined with y and stored, the next one's MMAs run and
 // B of the one after that is copied.
 template <int kBn>
@@ -657,12 +708,12 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
   tile_end(&ctl, p.tmem_cols);
 }
 
-// out = y + s B[e] v where the rows of y, out and B start on 16-byte boundaries and N is whole eights. The CTAs share out
+// out = y + s B[e] v where the rows of B start on 16-byte boundaries (rank a multiple of eight). The CTAs share out
 // (tile, kBn columns) steps in equal runs, so that a CTA passes along the columns of one tile and perhaps on to the next.
 //   joining warps  32 rows and 32 columns each: a thread reads its row of a step's sums from tensor memory, joins it with y in
 //                  a slot of shared memory and writes the result over y there.
 //   issuing warp   loads B by TMA, two or three steps ahead, and issues the MMAs.
-//   copying warps  y into the slots, by asynchronous 16-byte copies as far ahead as there are slots, and out from them: 16
+//   copying warps  y into the slots, by asynchronous copies of kPiece bytes (of 2: by loads) as far ahead as there are slots, and out from them: 16
 //                  rows each, whole lines at a time (the rows of a tile may be any tokens).
 // What was measured for 8192 x 14336: rows loaded and stored by the joining threads, 32 bytes of a row at a time, 111 us
 // (each asks the L2 for a single sector); a bulk copy of 256 bytes a row each way 470 us (some 60 cycles a copy).
@@ -670,7 +721,7 @@ expand_any_kernel(const __grid_constant__ TileParams p) {
 constexpr int join_threads(int bn) { return bn * 4; }
 constexpr int expand_threads(int bn) { return join_threads(bn) + 32 + kCopyThreads; }
 
-template <int kBn>
+template <int kBn, int kPiece>
 __global__ void __launch_bounds__(kBn * 4 + 32 + kCopyThreads, 1)
 expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ TileParams p) {
   constexpr int kJoin = kBn * 4, kJoinWarps = kJoin / 32;
@@ -699,9 +750,12 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
 
   if (warp > kJoinWarps) {
     // ---------------- copies of y and out: kCopyRows rows a warp, lane l knows the token of the l-th ----------------
-    constexpr int kLanes = kBn / 8, kRowsAt = 32 / kLanes;  // lanes of a row, rows at a time
-    constexpr int kTimes = kCopyRows / kRowsAt, kBatch = kTimes < 4 ? kTimes : 4;
-    const int first = (warp - kJoinWarps - 1) * kCopyRows, at_row = lane / kLanes, at_col = (lane % kLanes) * 8;
+    constexpr int kCols = kPiece / 2;                                       // of a lane
+    constexpr int kLanes = kBn / kCols < 32 ? kBn / kCols : 32;             // of a row
+    constexpr int kRowsAt = 32 / kLanes, kParts = kBn / kCols / kLanes;     // rows at a time, parts of a row
+    constexpr int kTimes = kCopyRows / kRowsAt * kParts;
+    constexpr int kBatch = kTimes < 64 / kPiece ? kTimes : kPiece == 16 ? 4 : 16;
+    const int first = (warp - kJoinWarps - 1) * kCopyRows, at_row = lane / kLanes, at_col = (lane % kLanes) * kCols;
     struct Walk {
       int64_t u;      // the step after this part of a tile
       int s, s1;      // columns of the next step, and where the part ends
@@ -721,36 +775,55 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       return false;
     };
     const uint32_t mine = slots_at + uint32_t(first + at_row) * kPitch + at_col * 2u;
+    // the i-th access of a lane: a row of the warp's, a part of it
+    auto row_of = [&](int i) { return i / kParts * kRowsAt; };
+    auto part_of = [&](int i) { return i % kParts * kLanes * kCols; };
     Walk in = {begin}, out = {begin};
     bool more = enter(in), left = enter(out);
     Place in_at, out_at;
     int held = 0;  // slots that were loaded and not yet stored
     while (left) {
       for (; more && held < p.slots; ++held, in_at.next(p.slots)) {
-        const uint32_t to = mine + uint32_t(in_at.i) * kSlotBytes;
+        const uint32_t to = mine + uint32_t(in_at.i) * kSlotBytes, bar = smem_u32(&ctl.y_in[in_at.i]);
         const int col = in.s * kBn + at_col;
+        if constexpr (kPiece >= 4) {
 #pragma unroll
-        for (int i = 0; i < kTimes; ++i) {
-          const int token = __shfl_sync(0xffffffffu, in.token, i * kRowsAt + at_row);
-          if (token >= 0 && col < N)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
-                         :: "r"(to + uint32_t(i * kRowsAt) * kPitch), "l"(g.y + token * g.ldy + col) : "memory");
+          for (int i = 0; i < kTimes; ++i) {
+            const int token = __shfl_sync(0xffffffffu, in.token, row_of(i) + at_row), n = col + part_of(i);
+            if (token >= 0 && n < N) copy_async<kPiece>(to + uint32_t(row_of(i)) * kPitch + part_of(i) * 2u, g.y + token * g.ldy + n);
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
+        } else {
+#pragma unroll 1
+          for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
+            uint16_t v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int token = __shfl_sync(0xffffffffu, in.token, row_of(i0 + i) + at_row), n = col + part_of(i0 + i);
+              v[i] = token >= 0 && n < N ? g.y[token * g.ldy + n] : uint16_t(0);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              st_shared_piece(to + uint32_t(row_of(i0 + i)) * kPitch + part_of(i0 + i) * 2u, v[i]);
+          }
+          mbar_arrive(bar);
         }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(smem_u32(&ctl.y_in[in_at.i])) : "memory");
         if (++in.s == in.s1) more = enter(in);
       }
       if (!__all_sync(0xffffffffu, wait_at(ctl.y_out, out_at))) break;
       const uint32_t from = mine + uint32_t(out_at.i) * kSlotBytes;
       const int col = out.s * kBn + at_col;
-#pragma unroll
+      using Piece = typename PieceOf<kPiece>::type;
+#pragma unroll 1
       for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
-        uint4 v[kBatch];
+        Piece v[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) v[i] = lds128(from + uint32_t((i0 + i) * kRowsAt) * kPitch);
+        for (int i = 0; i < kBatch; ++i)
+          ld_shared_piece(v[i], from + uint32_t(row_of(i0 + i)) * kPitch + part_of(i0 + i) * 2u);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-          const int token = __shfl_sync(0xffffffffu, out.token, (i0 + i) * kRowsAt + at_row);
-          if (token >= 0 && col < N) *reinterpret_cast<uint4*>(g.out + token * g.ldo + col) = v[i];
+          const int token = __shfl_sync(0xffffffffu, out.token, row_of(i0 + i) + at_row), n = col + part_of(i0 + i);
+          if (token >= 0 && n < N) *reinterpret_cast<Piece*>(g.out + token * g.ldo + n) = v[i];
         }
       }
       --held;
@@ -891,11 +964,13 @@ bool allow_smem(const void* kfn) {
 }
 }  // namespace
 
-// K splits of the shrink: CTAs enough for the SMs, each with at least four blocks of K.
-int splits_of(int64_t M, int64_t K, int64_t adapters) {
+// K splits of the first product: CTAs for the SMs, each with at least four blocks of K, and no more than pay for themselves:
+// a block takes 0.65 us, and each split of a tile's sums about 0.01 us a rank to read in the second product.
+int splits_of(int64_t M, int64_t K, int64_t adapters, int64_t rank) {
   const int64_t tiles = (M + kTileRows - 1) / kTileRows + std::min(M, adapters) / 2;
   const int64_t kb = (K + kBk - 1) / kBk;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kb / 4, 2 * 152 / tiles));
+  int64_t want = std::max<int64_t>(1, std::min<int64_t>(kb / 4, 2 * 152 / tiles));
+  while (want > 1 && want * want * padded_rank(rank) > 65 * kb) --want;
   const int64_t slice = (kb + want - 1) / want;
   return int(std::max<int64_t>(1, (kb + slice - 1) / std::max<int64_t>(slice, 1)));
 }
@@ -916,9 +991,9 @@ bool launch_expand_any(TileParams p, int num_sms, cudaStream_t st) {
                 dim3(kTileThreads), smem, st, true, dim3(1, 1, 1), p) == FP8_OK;
 }
 
-template <int kBn>
-bool launch_expand(TileParams p, const CUtensorMap& map_b, int num_sms, cudaStream_t st) {
-  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn>))) return false;
+template <int kBn, int kPiece>
+bool launch_expand_of(TileParams p, const CUtensorMap& map_b, int num_sms, cudaStream_t st) {
+  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn, kPiece>))) return false;
   const int rk = (p.rp + kBk - 1) / kBk;
   const size_t v = size_t(rk) * 2 * kXBytes, buf = size_t(rk) * kBn * 128, slot = size_t(kTileRows) * (kBn * 2 + 16);
   const size_t room = 232448 - 1024 - 1024 - v;  // (the control block and the alignment)
@@ -926,8 +1001,15 @@ bool launch_expand(TileParams p, const CUtensorMap& map_b, int num_sms, cudaStre
   p.slots = int(std::min<size_t>(4, (room - p.b_bufs * buf) / slot));
   const int64_t units = p.s.max_tiles * ((p.a.N + kBn - 1) / kBn);
   p.tmem_cols = 2 * kBn;
-  return launch(expand_kernel<kBn>, dim3(unsigned(std::min<int64_t>(units, num_sms))), dim3(expand_threads(kBn)),
+  return launch(expand_kernel<kBn, kPiece>, dim3(unsigned(std::min<int64_t>(units, num_sms))), dim3(expand_threads(kBn)),
                 1024 + v + size_t(p.b_bufs) * buf + size_t(p.slots) * slot, st, true, dim3(1, 1, 1), map_b, p) == FP8_OK;
+}
+
+template <int kBn>
+bool launch_expand(const TileParams& p, int piece, const CUtensorMap& map_b, int num_sms, cudaStream_t st) {
+  return piece == 16  ? launch_expand_of<kBn, 16>(p, map_b, num_sms, st)
+         : piece == 4 ? launch_expand_of<kBn, 4>(p, map_b, num_sms, st)
+                      : launch_expand_of<kBn, 2>(p, map_b, num_sms, st);
 }
 
 bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st) {
@@ -940,7 +1022,6 @@ bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st)
   p.vec_x = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0) && a.K % 8 == 0;
   p.vec_a = aligned(a.a, 16) && a.K % 8 == 0;
   p.vec_b = aligned(a.b, 16) && a.rank % 8 == 0;
-  p.vec_y = aligned(a.y, 16) && aligned(a.out, 16) && (a.M <= 1 || (a.ldy % 8 == 0 && a.ldo % 8 == 0));
   if (!allow_smem(reinterpret_cast<const void*>(shrink_kernel))) return false;
   const int stage_bytes = int(kXBytes) + p.rp * 128;
   p.stages = std::max(3, std::min(kShrinkMaxStages, 108 * 1024 / stage_bytes));
@@ -956,9 +1037,14 @@ bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st)
   if (launch(shrink_kernel, dim3(unsigned(s.max_tiles), unsigned(s.splits)), dim3(kShrinkThreads),
              size_t(p.stages) * stage_bytes + 1024, st, true, dim3(1, 1, 1), map_a, p) != FP8_OK)
     return false;
-  if (p.vec_y && p.vec_b && a.N % 8 == 0) {
-    if (p.rp <= kBk) return launch_expand<128>(p, map_b, num_sms, st);
-    return p.rp <= 3 * kBk ? launch_expand<64>(p, map_b, num_sms, st) : launch_expand<32>(p, map_b, num_sms, st);
+  if (p.vec_b) {
+    auto on = [&](int bytes) {
+      return aligned(a.y, bytes) && aligned(a.out, bytes) && a.N * 2 % bytes == 0 &&
+             (a.M <= 1 || (a.ldy * 2 % bytes == 0 && a.ldo * 2 % bytes == 0));
+    };
+    const int piece = on(16) ? 16 : on(4) ? 4 : 2;
+    if (p.rp <= kBk) return launch_expand<128>(p, piece, map_b, num_sms, st);
+    return p.rp <= 3 * kBk ? launch_expand<64>(p, piece, map_b, num_sms, st) : launch_expand<32>(p, piece, map_b, num_sms, st);
   }
   return p.rp <= 2 * kBk ? launch_expand_any<128>(p, num_sms, st) : launch_expand_any<64>(p, num_sms, st);
 }

@@ -41,7 +41,7 @@ struct Sorted {
   float* v;
   int splits;
 };
-int splits_of(int64_t M, int64_t K, int64_t adapters);
+int splits_of(int64_t M, int64_t K, int64_t adapters, int64_t rank);
 inline int padded_rank(int64_t rank) { return int((rank + 15) / 16 * 16); }
 bool launch_sorted(const Args& p, const Sorted& s, int num_sms, cudaStream_t st);
 

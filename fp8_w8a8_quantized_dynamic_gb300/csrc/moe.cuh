@@ -4,6 +4,7 @@
 #include <cfloat>
 #include <cmath>
 
+#include "any_rows.cuh"
 #include "block_gemm.h"
 #include "device_common.cuh"
 #include "moe_plan.h"
@@ -502,6 +503,11 @@ weighted_sum_kernel(const float* __restrict__ y, int64_t ldy32, const int* __res
 
 constexpr int kRowThreads = 256;
 
+// u / d; by 32 bits where both allow it, a fraction of the 64-bit division's instructions.
+__device__ __forceinline__ int64_t quotient_of_unit(int64_t u, int64_t d) {
+  return ((u | d) >> 32) == 0 ? int64_t(uint32_t(u) / uint32_t(d)) : u / d;
+}
+
 // Row t of x to the rows pos[t, j] of xs (those in [0, rows)), as U-sized pieces: `pieces` of a row, row strides in pieces.
 template <typename U>
 __global__ void __launch_bounds__(kRowThreads)
@@ -511,11 +517,31 @@ rows_out_kernel(const U* __restrict__ x, int64_t ldx, int64_t tokens, int64_t pi
   pdl_wait();
   for (int64_t u = int64_t(blockIdx.x) * kRowThreads + threadIdx.x; u < tokens * pieces;
        u += int64_t(gridDim.x) * kRowThreads) {
-    const int64_t t = u / pieces, c = u - t * pieces;
+    const int64_t t = quotient_of_unit(u, pieces), c = u - t * pieces;
     const U v = x[t * ldx + c];
     for (int j = 0; j < k; ++j) {
       const int d = pos[t * k + j];
       if (d >= 0 && d < rows) xs[int64_t(d) * ldxs + c] = v;
+    }
+  }
+}
+
+// The same where rows start or end off 16-byte boundaries: eight 16-bit values a thread (cols and row strides in them).
+__global__ void __launch_bounds__(kRowThreads)
+rows_out_any_kernel(const uint16_t* __restrict__ x, int64_t ldx, int64_t tokens, int64_t cols, const int* __restrict__ pos,
+                    int k, int64_t rows, uint16_t* __restrict__ xs, int64_t ldxs) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t upr = (cols + 7) / 8, units = tokens * upr;
+  for (int64_t u = int64_t(blockIdx.x) * kRowThreads + threadIdx.x; u - (threadIdx.x & 31) < units;
+       u += int64_t(gridDim.x) * kRowThreads) {  // (whole warps)
+    const bool live = u < units;
+    const int64_t t = live ? quotient_of_unit(u, upr) : 0, c = live ? (u - t * upr) * 8 : 0;
+    const uint4 v = live ? load8_any(x + t * ldx, c, cols) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < k; ++j) {
+      const int d = live ? pos[t * k + j] : -1;
+      // (lanes of two tokens may meet: one has a row where the other has none)
+      store8_any(xs + int64_t(d) * ldxs, c, cols, v, d >= 0 && d < rows);
     }
   }
 }
@@ -578,149 +604,181 @@ few_rows_out_kernel(const U* __restrict__ x, int64_t ldx, int64_t pieces, const 
   }
 }
 
-// kN columns of a row as they are held, 16 bytes or one value, and as fp32.
-template <typename T, int kN>
-struct Cols;
-template <>
-struct Cols<float, 4> {
-  using Held = float4;
-  static __device__ __forceinline__ Held zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
-  static __device__ __forceinline__ Held load(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
-  static __device__ __forceinline__ void values(Held v, float (&f)[4]) { f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w; }
-};
-template <>
-struct Cols<float, 1> {
-  using Held = float;
-  static __device__ __forceinline__ Held zero() { return 0.0f; }
-  static __device__ __forceinline__ Held load(const float* p) { return __ldcs(p); }
-  static __device__ __forceinline__ void values(Held v, float (&f)[1]) { f[0] = v; }
-};
-template <>
-struct Cols<uint16_t, 8> {
-  using Held = uint4;
-  static __device__ __forceinline__ Held zero() { return make_uint4(0, 0, 0, 0); }
-  static __device__ __forceinline__ Held load(const uint16_t* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
-  static __device__ __forceinline__ void values(Held v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// Rows pass in pieces of kPiece bytes on boundaries of as many: 16, or 4 where the rows do not allow it. bf16 rows that start
+// off 4-byte boundaries (kPiece 2) pass in whole 16-byte pieces that are shifted into place, stores by whole warps (store8_any).
+template <typename T, int kPiece>
+constexpr int kColsOf = (kPiece == 4 ? 4 : 16) / int(sizeof(T));
+
+// The columns of a piece as they are held, as fp32 and back.
+__device__ __forceinline__ void values_of(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
-  }
+  for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(w[i]), f[2 * i + 1] = bf16_hi(w[i]);
+}
+__device__ __forceinline__ void values_of(uint4 v, float (&f)[4]) {
+  f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void values_of(uint32_t v, float (&f)[2]) { f[0] = bf16_lo(v), f[1] = bf16_hi(v); }
+__device__ __forceinline__ void values_of(uint32_t v, float (&f)[1]) { f[0] = __uint_as_float(v); }
+__device__ __forceinline__ uint4 held(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+__device__ __forceinline__ uint4 held(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint32_t held(const float (&f)[2]) { return pack_bf16x2(f[0], f[1]); }
+__device__ __forceinline__ uint32_t held(const float (&f)[1]) { return __float_as_uint(f[0]); }
+
+template <int kPiece>
+struct HeldAs {
+  using type = uint4;
+  static __device__ __forceinline__ uint4 zero() { return make_uint4(0, 0, 0, 0); }
 };
 template <>
-struct Cols<uint16_t, 1> {
-  using Held = uint16_t;
-  static __device__ __forceinline__ Held zero() { return 0; }
-  static __device__ __forceinline__ Held load(const uint16_t* p) { return __ldcs(p); }
-  static __device__ __forceinline__ void values(Held v, float (&f)[1]) { f[0] = bf16_bits_to_float(v); }
+struct HeldAs<4> {
+  using type = uint32_t;
+  static __device__ __forceinline__ uint32_t zero() { return 0u; }
 };
-template <int kN>
-__device__ __forceinline__ void store_cols(float* p, const float (&f)[kN]) {
-  if constexpr (kN == 4)
-    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+template <int kPiece, typename T>
+__device__ __forceinline__ typename HeldAs<kPiece>::type load_cols(const T* row, int64_t c, int64_t cols) {
+  if constexpr (kPiece == 2)
+    return load8_any(reinterpret_cast<const uint16_t*>(row), c, cols);
   else
-    *p = f[0];
+    return __ldcs(reinterpret_cast<const typename HeldAs<kPiece>::type*>(row + c));
 }
-template <int kN>
-__device__ __forceinline__ void store_cols(uint16_t* p, const float (&f)[kN]) {
-  if constexpr (kN == 8)
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                                   pack_bf16x2(f[6], f[7])));
-  else
-    *p = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+template <int kPiece, typename T>
+__device__ __forceinline__ void store_cols(T* row, int64_t c, int64_t cols, typename HeldAs<kPiece>::type v, bool live) {
+  if constexpr (kPiece == 2)
+    store8_any(reinterpret_cast<uint16_t*>(row), c, cols, v, live);
+  else if (live)
+    __stcs(reinterpret_cast<typename HeldAs<kPiece>::type*>(row + c), v);
 }
 
-constexpr int kRowBatch = 8;  // rows of a token whose loads a thread has under way
+constexpr int kRowBatch = 8;  // loads that a thread has under way
 
-// y[t] = sum_j w[t, j] ys[pos[t, j]] (weights null: 1) over the pairs that have a row, in the order of j, in fp32, kN columns
-// a thread (1 or 16 bytes' worth; the row's columns are a multiple of it).
-template <typename T, int kN>
+// y[t] = sum_j w[t, j] ys[pos[t, j]] (weights null: 1) over the pairs that have a row, in the order of j, in fp32, the columns
+// of a piece a thread. kB: rows at a time, one to eight; where k <= kB < 8, as many columns more.
+template <typename T, int kPiece, int kB>
 __global__ void __launch_bounds__(kRowThreads, 4)
 rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int* __restrict__ pos,
                  const float* __restrict__ weights, int k, int64_t tokens, int64_t cols, T* __restrict__ y, int64_t ldy) {
+  constexpr int kN = kColsOf<T, kPiece>, kP = kRowBatch / kB;
+  using Held = typename HeldAs<kPiece>::type;
   pdl_trigger();
   pdl_wait();
-  using C = Cols<T, kN>;
-  const int64_t upr = cols / kN;
-  for (int64_t u = int64_t(blockIdx.x) * kRowThreads + threadIdx.x; u < tokens * upr;
-       u += int64_t(gridDim.x) * kRowThreads) {
-    const int64_t t = u / upr, c = (u - t * upr) * kN;
-    float acc[kN] = {};
-    for (int j0 = 0; j0 < k; j0 += kRowBatch) {
-      typename C::Held v[kRowBatch];
-      float w[kRowBatch];
+  const int64_t upr = (cols + kN - 1) / kN, units = tokens * upr;
+  for (int64_t u0 = int64_t(blockIdx.x) * kRowThreads * kP + threadIdx.x; u0 - (threadIdx.x & 31) < units;
+       u0 += int64_t(gridDim.x) * kRowThreads * kP) {  // (whole warps)
+    int64_t t[kP], c[kP];
+    bool live[kP];
+    Held v[kP][kB];
+    float w[kP][kB], acc[kN];
+    auto load = [&](int p, int j0) {
 #pragma unroll
-      for (int j = 0; j < kRowBatch; ++j) {
-        const int d = j0 + j < k ? pos[t * k + j0 + j] : -1;
+      for (int j = 0; j < kB; ++j) {
+        const int d = live[p] && j0 + j < k ? pos[t[p] * k + j0 + j] : -1;
         const bool in = d >= 0 && d < rows;
-        w[j] = in ? (weights ? weights[t * k + j0 + j] : 1.0f) : 0.0f;
-        v[j] = in ? C::load(ys + int64_t(d) * ldys + c) : C::zero();
+        w[p][j] = in ? (weights ? weights[t[p] * k + j0 + j] : 1.0f) : 0.0f;
+        v[p][j] = in ? load_cols<kPiece>(ys + int64_t(d) * ldys, c[p], cols) : HeldAs<kPiece>::zero();
       }
+    };
+    auto add = [&](int p) {
 #pragma unroll
-      for (int j = 0; j < kRowBatch; ++j) {
+      for (int j = 0; j < kB; ++j) {
         float f[kN];
-        C::values(v[j], f);
+        values_of(v[p][j], f);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+        for (int i = 0; i < kN; ++i) acc[i] = fmaf(w[p][j], f[i], acc[i]);
       }
+    };
+#pragma unroll
+    for (int p = 0; p < kP; ++p) {
+      const int64_t u = u0 + p * kRowThreads;
+      live[p] = u < units;
+      t[p] = live[p] ? quotient_of_unit(u, upr) : 0;
+      c[p] = live[p] ? (u - t[p] * upr) * kN : 0;
+      load(p, 0);
     }
-    store_cols<kN>(y + t * ldy + c, acc);
+#pragma unroll
+    for (int p = 0; p < kP; ++p) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) acc[i] = 0.0f;
+      add(p);
+      if constexpr (kP == 1)
+        for (int j0 = kB; j0 < k; j0 += kB) {
+          load(p, j0);
+          add(p);
+        }
+      store_cols<kPiece>(y + t[p] * ldy, c[p], cols, held(acc), live[p]);
+    }
   }
 }
 
 // The gradient of rows_back: dys[pos[t, j]] = w[t, j] dy[t], dw[t, j] = <dy[t], ys[pos[t, j]]> (0 for a pair without a
-// row), fp32 sums in a fixed order. dys may be ys. blockDim.x threads a token (a power of two from 32), blockDim.y tokens a CTA.
-template <typename T, int kN>
+// row), fp32 sums in a fixed order. dys may be ys. blockDim.x threads a token (a power of two from 32), blockDim.y tokens a
+// CTA. kB: pairs at a time; where there are few, as many columns more.
+template <typename T, int kPiece, int kB>
 __global__ void __launch_bounds__(kRowThreads, 4)
 rows_back_grad_kernel(const T* __restrict__ dy, int64_t lddy, const T* ys, int64_t ldys, int64_t rows,
                       const int* __restrict__ pos, const float* __restrict__ weights, int k, int64_t tokens, int64_t cols,
                       T* dys, int64_t lddys, float* __restrict__ dw) {
-  using C = Cols<T, kN>;
-  __shared__ float part[kRowThreads / 32][kRowBatch];
+  constexpr int kN = kColsOf<T, kPiece>, kP = kB < 4 ? 4 / kB : 1;
+  using Held = typename HeldAs<kPiece>::type;
+  __shared__ float part[kRowThreads / 32][kB];
   pdl_trigger();
   pdl_wait();
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t step = int64_t(gridDim.x) * blockDim.y;
+  const int64_t step = int64_t(gridDim.x) * blockDim.y, wide = int64_t(blockDim.x) * kN;
   for (int64_t t0 = int64_t(blockIdx.x) * blockDim.y; t0 < tokens; t0 += step) {
     const int64_t t = t0 + threadIdx.y;
-    for (int j0 = 0; j0 < k; j0 += kRowBatch) {
-      float sum[kRowBatch] = {};
+    for (int j0 = 0; j0 < k; j0 += kB) {
+      float sum[kB] = {};
       if (t < tokens) {
-        int d[kRowBatch];
-        float w[kRowBatch];
+        int d[kB];
+        float w[kB];
 #pragma unroll
-        for (int j = 0; j < kRowBatch; ++j) {
+        for (int j = 0; j < kB; ++j) {
           d[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
           if (d[j] >= rows) d[j] = -1;
           w[j] = d[j] >= 0 ? weights[t * k + j0 + j] : 0.0f;
         }
-        for (int64_t c = int64_t(threadIdx.x) * kN; c < cols; c += int64_t(blockDim.x) * kN) {
-          float g[kN];
-          C::values(C::load(dy + t * lddy + c), g);
-          typename C::Held v[kRowBatch];
+        for (int64_t c0 = int64_t(threadIdx.x) * kN; c0 - int64_t(lane) * kN < cols; c0 += wide * kP) {  // (whole warps)
+          Held g[kP], v[kP][kB];
 #pragma unroll
-          for (int j = 0; j < kRowBatch; ++j) v[j] = d[j] >= 0 ? C::load(ys + int64_t(d[j]) * ldys + c) : C::zero();
+          for (int p = 0; p < kP; ++p) {
+            const int64_t c = c0 + p * wide;
+            g[p] = c < cols ? load_cols<kPiece>(dy + t * lddy, c, cols) : HeldAs<kPiece>::zero();
 #pragma unroll
-          for (int j = 0; j < kRowBatch; ++j) {
-            if (d[j] < 0) continue;
-            float f[kN], o[kN];
-            C::values(v[j], f);
+            for (int j = 0; j < kB; ++j)
+              v[p][j] = c < cols && d[j] >= 0 ? load_cols<kPiece>(ys + int64_t(d[j]) * ldys, c, cols) : HeldAs<kPiece>::zero();
+          }
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-              sum[j] = fmaf(g[i], f[i], sum[j]);
-              o[i] = w[j] * g[i];
+          for (int p = 0; p < kP; ++p) {
+            float h[kN];
+            values_of(g[p], h);
+#pragma unroll
+            for (int j = 0; j < kB; ++j) {
+              if (d[j] < 0) continue;  // (of the token: the whole warp)
+              float f[kN], o[kN];
+              values_of(v[p][j], f);
+#pragma unroll
+              for (int i = 0; i < kN; ++i) {
+                sum[j] = fmaf(h[i], f[i], sum[j]);
+                o[i] = w[j] * h[i];
+              }
+              store_cols<kPiece>(dys + int64_t(d[j]) * lddys, c0 + p * wide, cols, held(o), c0 + p * wide < cols);
             }
-            store_cols<kN>(dys + int64_t(d[j]) * lddys + c, o);
           }
         }
       }
 #pragma unroll
-      for (int j = 0; j < kRowBatch; ++j) {
+      for (int j = 0; j < kB; ++j) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
         if (lane == 0) part[threadIdx.y * warps + warp][j] = sum[j];
       }
       __syncthreads();
-      if (t < tokens && threadIdx.x < kRowBatch && j0 + int(threadIdx.x) < k) {
+      if (t < tokens && threadIdx.x < kB && j0 + int(threadIdx.x) < k) {
         float v = 0.0f;
         for (int i = 0; i < warps; ++i) v += part[threadIdx.y * warps + i][threadIdx.x];
         dw[t * k + j0 + threadIdx.x] = v;
