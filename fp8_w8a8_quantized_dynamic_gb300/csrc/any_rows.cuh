@@ -44,6 +44,24 @@ __device__ __forceinline__ uint4 load8_any(const uint16_t* row, int64_t c, int64
   return n < 8 ? first_of(v, n) : v;
 }
 
+// load8_any in two halves, for loads that run ahead of their use: the pieces, and the values in them. `at` = off_piece(row + c).
+struct Raw8 {
+  uint4 a, b;
+};
+__device__ __forceinline__ int off_piece(const uint16_t* p) { return int(reinterpret_cast<uintptr_t>(p) >> 1) & 7; }
+__device__ __forceinline__ Raw8 load8_raw(const uint16_t* row, int at, int c, int cols) {
+  Raw8 v;
+  v.a = v.b = make_uint4(0, 0, 0, 0);
+  const uint4* piece = reinterpret_cast<const uint4*>(row + c - at);
+  if (c < cols) v.a = load_piece(piece);
+  if (at != 0 && c - at + 8 < cols) v.b = load_piece(piece + 1);
+  return v;
+}
+__device__ __forceinline__ uint4 values8(const Raw8& v, int at, int c, int cols) {
+  const uint4 e = at == 0 ? v.a : eight_from(v.a, v.b, at);
+  return c + 8 <= cols ? e : first_of(e, cols > c ? cols - c : 0);
+}
+
 __device__ __forceinline__ void store_some(uint16_t* p, uint4 v, int from, int to) {  // values [from, to) of eight
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -329,21 +329,11 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
 // Byte offset of 16-byte piece c of row r in a tile of 128-byte rows with the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swizzled(int r, int c) { return uint32_t(r) * 128u + uint32_t((c ^ (r & 7)) << 4); }
 
-// Eight values k .. k + 7 of a row (zeros from K on, and all of them where the row is not live) into shared memory: an
-// asynchronous 16-byte copy where the rows allow it (then K is whole eights).
-__device__ __forceinline__ void copy8(uint32_t dst, const uint16_t* row, bool live, int k, int K, int vec) {
-  live = live && k < K;
-  if (vec) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                 :: "r"(dst), "l"(live ? row + k : row), "r"(live ? 16u : 0u) : "memory");
-  } else {
-    const uint4 v = live ? load8_any(row, k, K) : make_uint4(0, 0, 0, 0);
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-  }
+// Eight values of a row from k on into shared memory, zeros where they are not live, by an asynchronous copy.
+__device__ __forceinline__ void copy8_async(uint32_t dst, const uint16_t* row, bool live, int k) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(dst), "l"(live ? row + k : row), "r"(live ? 16u : 0u) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(kLeft) : "memory"); }
 // What this thread wrote to shared memory becomes visible to the tensor core (after the barrier that follows).
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -366,8 +356,7 @@ struct TileParams {
   int kb, kb_slice;         // blocks of 64 of K, and of one split
   int stages;               // shrink
   int slots, b_bufs;        // expand: of y, of B
-  int cols_per_cta;         // expand: a multiple of kBn
-  int vec_x, vec_a, vec_b;
+  int vec, vec_b;           // rows of x and A, of B, on 16-byte boundaries
   uint32_t tmem_cols;
 };
 
@@ -379,6 +368,7 @@ struct TileCtl {
   uint64_t loaded[8];  // A of a stage, B of a step
   uint64_t read[2];    // expand: the warps that have read a step's sums
   uint64_t y_in[4], y_out[4];  // expand: a slot holds y, holds out
+  uint64_t freed[4];           // expand: B's buffer has been multiplied
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -398,6 +388,7 @@ __device__ __forceinline__ void tile_begin(TileCtl* ctl, uint32_t cols, int load
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&ctl->y_in[i]), kCopyThreads);
       mbar_init(smem_u32(&ctl->y_out[i]), uint32_t(warps));
+      mbar_init(smem_u32(&ctl->freed[i]), 1);
     }
     ctl->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -428,7 +419,9 @@ __device__ __forceinline__ void tile_end(TileCtl* ctl, uint32_t cols) {
 // tokens: eight threads a 128-byte piece of a row, asynchronous 16-byte copies) and, by TMA, A's into a ring of stages, whose
 // barrier counts the copies' completion; warp 8 issues the MMAs. (With a fence for the tensor core in the copying
 // threads, which waits for their copies in flight, a step took a load's latency: 27 us for 8192 x 4096 at rank 64.)
-__global__ void __launch_bounds__(kShrinkThreads)
+// kVec: the rows of x and A start on 16-byte boundaries and K is whole eights.
+template <bool kVec>
+__global__ void __launch_bounds__(kShrinkThreads, 2)
 shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ TileParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ TileCtl ctl;
@@ -468,7 +461,6 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
       } else {
         // eight threads a row; this thread's rows of x
         const int piece = threadIdx.x & 7, first = threadIdx.x >> 3;
-        const bool whole = p.vec_x && p.vec_a;
         const uint16_t* x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -476,30 +468,56 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
           x[i] = row < rows ? g.x + int64_t(p.s.order[t.row0 + row]) * g.ldx : g.x;
         }
         const uint16_t* A = g.a + int64_t(t.expert) * r * K;
-        for (; filled < steps; ++filled) {
-          if (filled >= p.stages && !(ok = wait(ctl.done, filled - p.stages))) break;
-          const uint32_t st = base + uint32_t(filled % p.stages) * stage_bytes;
-          const uint32_t bar = smem_u32(&ctl.loaded[filled % p.stages]);
-          if (threadIdx.x == 0) {
-            if (p.vec_a) {
+        auto a_row = [&](int i) { return A + int64_t(min(first + 32 * i, r - 1)) * K; };
+        if constexpr (kVec) {
+          for (; filled < steps; ++filled) {
+            if (filled >= p.stages && !(ok = wait(ctl.done, filled - p.stages))) break;
+            const uint32_t st = base + uint32_t(filled % p.stages) * stage_bytes;
+            const uint32_t bar = smem_u32(&ctl.loaded[filled % p.stages]);
+            if (threadIdx.x == 0) {
               mbar_arrive_expect_tx(bar, uint32_t(p.rp) * 128u);
               tma_load_3d(st + kXBytes, &tmap_a, bar, (kb0 + filled) * 128, 0, t.expert);
-            } else {
-              mbar_arrive(bar);
             }
-          }
-          const int k = (kb0 + filled) * kBk + piece * 8;
+            const int k = (kb0 + filled) * kBk + piece * 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            copy8(st + swizzled(first + 32 * i, piece), x[i], first + 32 * i < rows, k, K, p.vec_x);
-          if (whole) {
+            for (int i = 0; i < 4; ++i)
+              copy8_async(st + swizzled(first + 32 * i, piece), x[i], first + 32 * i < rows && k < K, k);
             asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
-          } else {
-            if (!p.vec_a)
-              for (int row = first; row < p.rp; row += 32)
-                copy8(st + kXBytes + swizzled(row, piece), A + int64_t(min(row, r - 1)) * K, row < r, k, K, 0);
-            asm volatile("cp.async.wait_all;" ::: "memory");
+          }
+        } else {
+          // rows that start or end anywhere: whole pieces, loaded a step ahead and shifted into place. (The distance from a piece
+          // is one for a row: K steps are whole pieces.)
+          constexpr int kAhead = 4;  // rows of A whose loads run ahead; the others', of ranks over 128, do not
+          int x_at[4], a_at[kAhead];
+          Raw8 xr[4], ar[kAhead];
+          auto load = [&](int step) {
+            const int k = (kb0 + step) * kBk + piece * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xr[i] = load8_raw(x[i], x_at[i], k, first + 32 * i < rows ? K : 0);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) ar[i] = load8_raw(a_row(i), a_at[i], k, first + 32 * i < r ? K : 0);
+          };
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x_at[i] = off_piece(x[i]), a_at[i] = off_piece(a_row(i));
+          load(0);
+          for (; filled < steps; ++filled) {
+            if (filled >= p.stages && !(ok = wait(ctl.done, filled - p.stages))) break;
+            const uint32_t st = base + uint32_t(filled % p.stages) * stage_bytes;
+            const uint32_t bar = smem_u32(&ctl.loaded[filled % p.stages]);
+            const int k = (kb0 + filled) * kBk + piece * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sts128(st + swizzled(first + 32 * i, piece), values8(xr[i], x_at[i], k, first + 32 * i < rows ? K : 0));
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+              if (first + 32 * i < p.rp)
+                sts128(st + kXBytes + swizzled(first + 32 * i, piece), values8(ar[i], a_at[i], k, first + 32 * i < r ? K : 0));
+            for (int row = first + 32 * kAhead; row < p.rp; row += 32)
+              sts128(st + kXBytes + swizzled(row, piece),
+                     row < r && k < K ? load8_any(A + int64_t(row) * K, k, K) : make_uint4(0, 0, 0, 0));
+            if (filled + 1 < steps) load(filled + 1);
             fence_async();
+            if (threadIdx.x == 0) mbar_arrive(bar);  // (in place of the arrival that announces A's bytes)
             mbar_arrive(bar);
           }
         }
@@ -530,11 +548,6 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
   }
   tile_end(&ctl, p.tmem_cols);
 }
-
-// Columns that a warp passes through shared memory at a time, and floats between rows there: eight lanes' 16-byte accesses,
-// down the rows or along them, take 32 banks (pitch 36; along rows of pitch 20 two a bank). 16 columns where a large
-// rank leaves no room for 32.
-__host__ __device__ constexpr int stage_cols(int bn) { return bn == 128 ? 32 : 16; }
 
 // v of a tile's rows, the sum of the splits in order, as two bf16 numbers in two swizzled tiles, by the block's first
 // `threads` threads.
@@ -579,150 +592,23 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
   }
 }
 
-// out = y + s B[e] v for ranks that are no multiple of eight: a tile's rows and the CTA's columns, kBn a step (64 where the
-// rank's operands leave no room for 128). While a step's sums are read, joined with y and stored, the next one's MMAs run and
-// B of the one after that is copied.
-template <int kBn>
-__global__ void __launch_bounds__(kTileThreads, kBn == 128 ? 2 : 1)
-expand_any_kernel(const __grid_constant__ TileParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ TileCtl ctl;
-  __shared__ int order[kTileRows];
-  constexpr int kSc = stage_cols(kBn), kStagePitch = kSc + 4;
-  constexpr int kRowsAt = 32 / kSc, kParts = kBn / 2 / kSc;
-  __shared__ __align__(16) float staged[kTileThreads / 32][32 * kStagePitch];
-  const uint32_t base = align1024(smem_u32(smem_raw));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tile_begin(&ctl, p.tmem_cols, 1, kTileThreads / 32);
-  const Args& g = p.a;
-  const int N = int(g.N), r = g.rank;
-  const int tile = blockIdx.x;
-  const int n0 = int(blockIdx.y) * p.cols_per_cta, n1 = min(N, n0 + p.cols_per_cta);
-  const bool mine = tile < *p.s.n_tiles;
-  const block::RowTile t = mine ? p.s.tiles[tile] : block::RowTile{g.adapters, 0, 0, 0};
-  const int rows = min(kTileRows, t.row_end - t.row0);
-  if (mine && threadIdx.x < kTileRows) order[threadIdx.x] = int(threadIdx.x) < rows ? p.s.order[t.row0 + threadIdx.x] : -1;
-  __syncthreads();
-  if (mine && t.expert >= g.adapters) {
-    if (g.out != g.y)
-      for (int n = n0 + lane; n < n1; n += 32)
-        for (int row0 = warp * 8; row0 < rows; row0 += kTileThreads / 32 * 8) {
-          uint16_t v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = row0 + i < rows ? g.y[int64_t(order[row0 + i]) * g.ldy + n] : uint16_t(0);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (row0 + i < rows) g.out[int64_t(order[row0 + i]) * g.ldo + n] = v[i];
-        }
-  } else if (mine) {
-    const int rk = (p.rp + kBk - 1) / kBk;  // 128-byte rows that the rank fills
-    const uint32_t v_hi = base, v_lo = base + uint32_t(rk) * kXBytes, b_at = v_lo + uint32_t(rk) * kXBytes;
-    const uint32_t b_bytes = uint32_t(rk) * (kBn * 128u);
-    const int steps = (n1 - n0 + kBn - 1) / kBn;
-    const uint16_t* B = g.b + int64_t(t.expert) * N * r;
-    const int pieces = p.rp / 8;
-    const float inv_pieces = 1.0f / float(pieces);
-    auto fill = [&](int step) {
-      const uint32_t to = b_at + uint32_t(step & 1) * b_bytes;
-      for (int i = threadIdx.x; i < kBn * pieces; i += kTileThreads) {
-        const int row = quotient(i, inv_pieces), c = i - row * pieces;
-        const int n = n0 + step * kBn + row;
-        copy8(to + uint32_t(c >> 3) * (kBn * 128u) + swizzled(row, c & 7), B + int64_t(min(n, N - 1)) * r, n < N, c * 8, r,
-              p.vec_b);
-      }
-    };
-    fill(0);
-    cp_commit();
-    put_v(p, t, rows, v_hi, v_lo, kTileThreads);
-    auto multiply = [&](int step) {  // by a whole warp
-      if (elect_one()) {
-        const uint32_t b = b_at + uint32_t(step & 1) * b_bytes, d = ctl.tmem_base + uint32_t(step & 1) * kBn;
-        for (int part = 0; part < 2; ++part)
-          for (int k16 = 0; k16 < p.rp / 16; ++k16) {
-            const uint64_t ad = make_sdesc((part ? v_lo : v_hi) + uint32_t(k16 >> 2) * kXBytes) + uint64_t((k16 & 3) * 2);
-            const uint64_t bd = make_sdesc(b + uint32_t(k16 >> 2) * (kBn * 128u)) + uint64_t((k16 & 3) * 2);
-            mma_bf16(d, ad, bd, idesc_of(kBn), part != 0 || k16 != 0);
-          }
-        mma_commit<false>(smem_u32(&ctl.done[step & 1]));
-      }
-      __syncwarp();
-    };
-    cp_wait<0>();
-    fence_async();
-    __syncthreads();
-    if (warp == 0) multiply(0);
-    if (steps > 1) fill(1);
-    cp_commit();
-    const float scale = g.scales ? g.scales[t.expert] : 1.0f;
-    const int quarter = warp & 3, half = warp >> 2;
-    float* mine32 = staged[warp];
-    // 32 rows of kSc columns at a time, a column a lane: whole sectors wherever the rows start
-    const int c1 = lane % kSc, r1 = lane / kSc;
-    uint16_t yv[kSc];
-    auto col_of = [&](int step, int h) { return n0 + step * kBn + half * (kBn / 2) + h * kSc + c1; };
-    auto token_of = [&](int i) { return order[quarter * 32 + i * kRowsAt + r1]; };
-    auto load_y = [&](int step, int h) {
-      const int n = col_of(step, h);
-#pragma unroll
-      for (int i = 0; i < kSc; ++i) {
-        const int token = token_of(i);
-        yv[i] = token >= 0 && n < N ? g.y[token * g.ldy + n] : uint16_t(0);
-      }
-    };
-    load_y(0, 0);
-    for (int step = 0; step < steps; ++step) {
-      bool ok = mbar_wait_short(smem_u32(&ctl.done[step & 1]), uint32_t(step >> 1) & 1u, &ctl.abort_flag, &g_lora_error);
-      // B of the next step has landed; the sums of the step before this one have been read by all warps
-      cp_wait<0>();
-      fence_async();
-      tmem_fence_before();
-      if (!__syncthreads_and(ok)) break;
-      tmem_fence_after();
-      if (warp == 0 && step + 1 < steps) multiply(step + 1);
-      if (step + 2 < steps) fill(step + 2);
-      cp_commit();
-      uint32_t f[32];
-#pragma unroll
-      for (int h = 0; h < kParts; ++h) {
-        __syncwarp();
-        if (h * kSc % 32 == 0)
-          tmem_ld32(ctl.tmem_base + uint32_t(step & 1) * kBn + (uint32_t(quarter * 32) << 16) + half * (kBn / 2) + h * kSc, f);
-#pragma unroll
-        for (int j = 0; j < kSc; j += 4) {
-          const uint32_t* from = f + h * kSc % 32 + j;
-          *reinterpret_cast<uint4*>(mine32 + lane * kStagePitch + j) = make_uint4(from[0], from[1], from[2], from[3]);
-        }
-        __syncwarp();
-        const int n = col_of(step, h);
-#pragma unroll
-        for (int i = 0; i < kSc; ++i) {
-          const int token = token_of(i);
-          const float o = fmaf(scale, mine32[(i * kRowsAt + r1) * kStagePitch + c1], bf16_bits_to_float(yv[i]));
-          if (token >= 0 && n < N) g.out[token * g.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-        }
-        __syncwarp();
-        if (h + 1 < kParts || step + 1 < steps) load_y(h + 1 < kParts ? step : step + 1, (h + 1) % kParts);
-      }
-    }
-  }
-  tile_end(&ctl, p.tmem_cols);
-}
-
-// out = y + s B[e] v where the rows of B start on 16-byte boundaries (rank a multiple of eight). The CTAs share out
+// out = y + s B[e] v. The CTAs share out
 // (tile, kBn columns) steps in equal runs, so that a CTA passes along the columns of one tile and perhaps on to the next.
 //   joining warps  32 rows and 32 columns each: a thread reads its row of a step's sums from tensor memory, joins it with y in
 //                  a slot of shared memory and writes the result over y there.
-//   issuing warp   loads B by TMA, two or three steps ahead, and issues the MMAs.
+//   issuing warp   loads B by TMA, two or three steps ahead, and issues the MMAs. Where the rows of B do not start on 16-byte
+//                  boundaries (a rank that is no multiple of eight), four warps more load it in whole pieces.
 //   copying warps  y into the slots, by asynchronous copies of kPiece bytes (of 2: by loads) as far ahead as there are slots, and out from them: 16
 //                  rows each, whole lines at a time (the rows of a tile may be any tokens).
 // What was measured for 8192 x 14336: rows loaded and stored by the joining threads, 32 bytes of a row at a time, 111 us
 // (each asks the L2 for a single sector); a bulk copy of 256 bytes a row each way 470 us (some 60 cycles a copy).
 // Slot rows lie 16 bytes further apart than they are long, so that eight lanes' accesses down the rows take all banks.
 constexpr int join_threads(int bn) { return bn * 4; }
-constexpr int expand_threads(int bn) { return join_threads(bn) + 32 + kCopyThreads; }
+constexpr int kBThreads = 128;
+constexpr int expand_threads(int bn, bool tma) { return join_threads(bn) + 32 + kCopyThreads + (tma ? 0 : kBThreads); }
 
-template <int kBn, int kPiece>
-__global__ void __launch_bounds__(kBn * 4 + 32 + kCopyThreads, 1)
+template <int kBn, int kPiece, bool kTma>
+__global__ void __launch_bounds__(kBn * 4 + 32 + kCopyThreads + (kTma ? 0 : kBThreads), 1)
 expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ TileParams p) {
   constexpr int kJoin = kBn * 4, kJoinWarps = kJoin / 32;
   constexpr int kMostK = kBn == 128 ? 4 : kBn == 64 ? 12 : 16;  // K steps of the ranks that take this width (launch_sorted)
@@ -731,7 +617,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
   __shared__ TileCtl ctl;
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  tile_begin(&ctl, p.tmem_cols, 1, kJoinWarps);
+  tile_begin(&ctl, p.tmem_cols, kTma ? 1 : kBThreads, kJoinWarps);
   const Args& g = p.a;
   const int N = int(g.N);
   const int steps = (N + kBn - 1) / kBn;
@@ -748,7 +634,51 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
     return mbar_wait_short(smem_u32(bars + a.i), a.parity, &ctl.abort_flag, &g_lora_error);
   };
 
-  if (warp > kJoinWarps) {
+  constexpr int kCopyWarps = kCopyThreads / 32;
+  if (!kTma && warp > kJoinWarps + kCopyWarps) {
+    // ---------------- B where TMA cannot load it ----------------
+    const int pieces = p.rp / 8, n_pieces = kBn * pieces;
+    const float inv_pieces = 1.0f / float(pieces);
+    const int me = threadIdx.x - (kJoinWarps + 1 + kCopyWarps) * 32;
+    Place at;
+    int free_bufs = p.b_bufs;
+    bool ok = true;
+    for (int64_t u = begin; ok && u < end;) {
+      const int tile = int(u / steps), s0 = int(u - int64_t(tile) * steps), s1 = int(min(int64_t(steps), s0 + (end - u)));
+      u += s1 - s0;
+      const block::RowTile t = p.s.tiles[tile];
+      if (t.expert >= g.adapters) continue;
+      const uint16_t* B = g.b + int64_t(t.expert) * N * g.rank;
+      for (int s = s0; s < s1; ++s, at.next(p.b_bufs)) {
+        if (free_bufs > 0)
+          --free_bufs;
+        else if (!(ok = wait_at(ctl.freed, at)))
+          break;
+        const uint32_t to = b_at + uint32_t(at.i) * b_bytes;
+        for (int i0 = me; i0 < n_pieces; i0 += 4 * kBThreads) {  // four loads at once
+          Raw8 v[4];
+          int where[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = min(i0 + j * kBThreads, n_pieces - 1), row = quotient(i, inv_pieces), c = i - row * pieces;
+            const int n = min(s * kBn + row, N - 1);
+            const uint16_t* from = B + int64_t(n) * g.rank;
+            where[j] = row * 32 + c;
+            v[j] = load8_raw(from, off_piece(from), c * 8, s * kBn + row < N ? g.rank : 0);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = where[j] / 32, c = where[j] % 32;
+            const uint16_t* from = B + int64_t(min(s * kBn + row, N - 1)) * g.rank;
+            sts128(to + uint32_t(c >> 3) * (kBn * 128u) + swizzled(row, c & 7),
+                   values8(v[j], off_piece(from), c * 8, s * kBn + row < N ? g.rank : 0));
+          }
+        }
+        fence_async();
+        mbar_arrive(smem_u32(&ctl.loaded[at.i]));
+      }
+    }
+  } else if (warp > kJoinWarps) {
     // ---------------- copies of y and out: kCopyRows rows a warp, lane l knows the token of the l-th ----------------
     constexpr int kCols = kPiece / 2;                                       // of a lane
     constexpr int kLanes = kBn / kCols < 32 ? kBn / kCols : 32;             // of a row
@@ -851,7 +781,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         continue;
       }
       auto fill = [&](int step) {  // by the issuing warp
-        if (elect_one()) {
+        if (kTma && elect_one()) {
           const uint32_t bar = smem_u32(&ctl.loaded[filled.i]);
           mbar_arrive_expect_tx(bar, b_bytes);
           for (int i = 0; i < rk; ++i)
@@ -894,6 +824,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
               }
             }
             mma_commit<false>(smem_u32(&ctl.done[it & 1u]));
+            if (!kTma) mma_commit<false>(smem_u32(&ctl.freed[used.i]));
           }
           __syncwarp();
           used.next(p.b_bufs);
@@ -935,7 +866,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         if (lane == 0) mbar_arrive(smem_u32(&ctl.y_out[slot.i]));
       }
     }
-    if (!ok && threadIdx.x == kJoin)  // nothing of a load may land after the CTA has left
+    if (kTma && !ok && threadIdx.x == kJoin)  // nothing of a load may land after the CTA has left
       for (; used.i != filled.i || used.parity != filled.parity; used.next(p.b_bufs))
         mbar_wait_bounded(smem_u32(&ctl.loaded[used.i]), used.parity, nullptr, &g_lora_error);
   }
@@ -975,25 +906,9 @@ int splits_of(int64_t M, int64_t K, int64_t adapters, int64_t rank) {
   return int(std::max<int64_t>(1, (kb + slice - 1) / std::max<int64_t>(slice, 1)));
 }
 
-template <int kBn>
-bool launch_expand_any(TileParams p, int num_sms, cudaStream_t st) {
-  if (!allow_smem(reinterpret_cast<const void*>(expand_any_kernel<kBn>))) return false;
-  const int rk = (p.rp + kBk - 1) / kBk;
-  const size_t smem = 1024 + size_t(rk) * (2 * kXBytes + 2 * kBn * 128);
-  // columns of a CTA: CTAs for two on every SM, as far as there are columns
-  const int64_t steps = (p.a.N + kBn - 1) / kBn;
-  const int64_t tiles = (p.a.M + kTileRows - 1) / kTileRows + std::min<int64_t>(p.a.M, p.a.adapters) / 2;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(steps, (4 * num_sms + tiles - 1) / tiles));
-  p.cols_per_cta = int((steps + want - 1) / want) * kBn;
-  p.tmem_cols = 2 * kBn;
-  return launch(expand_any_kernel<kBn>,
-                dim3(unsigned(p.s.max_tiles), unsigned((p.a.N + p.cols_per_cta - 1) / p.cols_per_cta)),
-                dim3(kTileThreads), smem, st, true, dim3(1, 1, 1), p) == FP8_OK;
-}
-
-template <int kBn, int kPiece>
+template <int kBn, int kPiece, bool kTma>
 bool launch_expand_of(TileParams p, const CUtensorMap& map_b, int num_sms, cudaStream_t st) {
-  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn, kPiece>))) return false;
+  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn, kPiece, kTma>))) return false;
   const int rk = (p.rp + kBk - 1) / kBk;
   const size_t v = size_t(rk) * 2 * kXBytes, buf = size_t(rk) * kBn * 128, slot = size_t(kTileRows) * (kBn * 2 + 16);
   const size_t room = 232448 - 1024 - 1024 - v;  // (the control block and the alignment)
@@ -1001,15 +916,15 @@ bool launch_expand_of(TileParams p, const CUtensorMap& map_b, int num_sms, cudaS
   p.slots = int(std::min<size_t>(4, (room - p.b_bufs * buf) / slot));
   const int64_t units = p.s.max_tiles * ((p.a.N + kBn - 1) / kBn);
   p.tmem_cols = 2 * kBn;
-  return launch(expand_kernel<kBn, kPiece>, dim3(unsigned(std::min<int64_t>(units, num_sms))), dim3(expand_threads(kBn)),
+  return launch(expand_kernel<kBn, kPiece, kTma>, dim3(unsigned(std::min<int64_t>(units, num_sms))), dim3(expand_threads(kBn, kTma)),
                 1024 + v + size_t(p.b_bufs) * buf + size_t(p.slots) * slot, st, true, dim3(1, 1, 1), map_b, p) == FP8_OK;
 }
 
-template <int kBn>
+template <int kBn, bool kTma>
 bool launch_expand(const TileParams& p, int piece, const CUtensorMap& map_b, int num_sms, cudaStream_t st) {
-  return piece == 16  ? launch_expand_of<kBn, 16>(p, map_b, num_sms, st)
-         : piece == 4 ? launch_expand_of<kBn, 4>(p, map_b, num_sms, st)
-                      : launch_expand_of<kBn, 2>(p, map_b, num_sms, st);
+  return piece == 16  ? launch_expand_of<kBn, 16, kTma>(p, map_b, num_sms, st)
+         : piece == 4 ? launch_expand_of<kBn, 4, kTma>(p, map_b, num_sms, st)
+                      : launch_expand_of<kBn, 2, kTma>(p, map_b, num_sms, st);
 }
 
 bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st) {
@@ -1019,34 +934,36 @@ bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st)
   p.rp = padded_rank(a.rank);
   p.kb = int((a.K + kBk - 1) / kBk);
   p.kb_slice = (p.kb + s.splits - 1) / s.splits;
-  p.vec_x = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0) && a.K % 8 == 0;
-  p.vec_a = aligned(a.a, 16) && a.K % 8 == 0;
+  p.vec = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0) && aligned(a.a, 16) && a.K % 8 == 0;
   p.vec_b = aligned(a.b, 16) && a.rank % 8 == 0;
-  if (!allow_smem(reinterpret_cast<const void*>(shrink_kernel))) return false;
+  auto shrink = p.vec ? shrink_kernel<true> : shrink_kernel<false>;
+  if (!allow_smem(reinterpret_cast<const void*>(shrink))) return false;
   const int stage_bytes = int(kXBytes) + p.rp * 128;
   p.stages = std::max(3, std::min(kShrinkMaxStages, 108 * 1024 / stage_bytes));
   p.tmem_cols = 32;
   while (int(p.tmem_cols) < p.rp) p.tmem_cols *= 2;
   CUtensorMap map_a = {}, map_b = {};
   // (rows of 128 bytes; what lies past the rank or past K reads as zeros)
-  if ((p.vec_a && !make_fp8_tensor_map_3d(&map_a, reinterpret_cast<const uint8_t*>(a.a), a.adapters, a.rank, a.K * 2,
+  if ((p.vec && !make_fp8_tensor_map_3d(&map_a, reinterpret_cast<const uint8_t*>(a.a), a.adapters, a.rank, a.K * 2,
                                           a.K * 2, uint32_t(p.rp))) ||
       (p.vec_b && !make_fp8_tensor_map_3d(&map_b, reinterpret_cast<const uint8_t*>(a.b), a.adapters, a.N,
                                           int64_t(a.rank) * 2, int64_t(a.rank) * 2, p.rp <= kBk ? 128 : p.rp <= 3 * kBk ? 64 : 32)))
     return false;
-  if (launch(shrink_kernel, dim3(unsigned(s.max_tiles), unsigned(s.splits)), dim3(kShrinkThreads),
+  if (launch(shrink, dim3(unsigned(s.max_tiles), unsigned(s.splits)), dim3(kShrinkThreads),
              size_t(p.stages) * stage_bytes + 1024, st, true, dim3(1, 1, 1), map_a, p) != FP8_OK)
     return false;
+  auto on = [&](int bytes) {
+    return aligned(a.y, bytes) && aligned(a.out, bytes) && a.N * 2 % bytes == 0 &&
+           (a.M <= 1 || (a.ldy * 2 % bytes == 0 && a.ldo * 2 % bytes == 0));
+  };
+  const int piece = on(16) ? 16 : on(4) ? 4 : 2;
   if (p.vec_b) {
-    auto on = [&](int bytes) {
-      return aligned(a.y, bytes) && aligned(a.out, bytes) && a.N * 2 % bytes == 0 &&
-             (a.M <= 1 || (a.ldy * 2 % bytes == 0 && a.ldo * 2 % bytes == 0));
-    };
-    const int piece = on(16) ? 16 : on(4) ? 4 : 2;
-    if (p.rp <= kBk) return launch_expand<128>(p, piece, map_b, num_sms, st);
-    return p.rp <= 3 * kBk ? launch_expand<64>(p, piece, map_b, num_sms, st) : launch_expand<32>(p, piece, map_b, num_sms, st);
+    if (p.rp <= kBk) return launch_expand<128, true>(p, piece, map_b, num_sms, st);
+    return p.rp <= 3 * kBk ? launch_expand<64, true>(p, piece, map_b, num_sms, st)
+                           : launch_expand<32, true>(p, piece, map_b, num_sms, st);
   }
-  return p.rp <= 2 * kBk ? launch_expand_any<128>(p, num_sms, st) : launch_expand_any<64>(p, num_sms, st);
+  return p.rp <= 3 * kBk ? launch_expand<64, false>(p, piece, map_b, num_sms, st)
+                         : launch_expand<32, false>(p, piece, map_b, num_sms, st);
 }
 
 unsigned int read_and_clear_error() {
