@@ -58,8 +58,10 @@ __device__ __forceinline__ Raw8 load8_raw(const uint16_t* row, int at, int c, in
   return v;
 }
 __device__ __forceinline__ uint4 values8(const Raw8& v, int at, int c, int cols) {
-  const uint4 e = at == 0 ? v.a : eight_from(v.a, v.b, at);
-  return c + 8 <= cols ? e : first_of(e, cols > c ? cols - c : 0);
+  uint4 e = v.a;
+  if (at != 0) e = eight_from(v.a, v.b, at);
+  if (c + 8 > cols) e = first_of(e, cols > c ? cols - c : 0);
+  return e;
 }
 
 __device__ __forceinline__ void store_some(uint16_t* p, uint4 v, int from, int to) {  // values [from, to) of eight
@@ -69,12 +71,12 @@ __device__ __forceinline__ void store_some(uint16_t* p, uint4 v, int from, int t
     if (i >= from && i < to) p[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
 }
 
-// Stores values c .. c + 7 of a row (those before cols), a multiple of eight a lane: all lanes of the warp come here, lane
-// i + 1 with the eight after lane i's wherever both are of one row (`live`: this lane has any). A lane stores the whole piece
-// that ends with its own values and takes the rest of it from the lane before; the ends of the warp's run of a row are
-// stored by values.
-__device__ __forceinline__ void store8_any(uint16_t* row, int64_t c, int64_t cols, uint4 v, bool live) {
-  const int lane = threadIdx.x & 31;
+// Stores values c .. c + 7 of a row (those before cols): all lanes of the warp come here, `live` ones have some. Where a lane is
+// joined, the lane before it has the eight before its own; where it hands on, the lane after it is joined. A lane stores the
+// whole piece that ends with its own values, with what it takes from the lane before; the ends of a run of lanes are stored by
+// values.
+__device__ __forceinline__ void store8_run(uint16_t* row, int64_t c, int64_t cols, uint4 v, bool live, bool joined,
+                                           bool handed_on) {
   uint4 before;
   before.x = __shfl_up_sync(0xffffffffu, v.x, 1);
   before.y = __shfl_up_sync(0xffffffffu, v.y, 1);
@@ -82,7 +84,7 @@ __device__ __forceinline__ void store8_any(uint16_t* row, int64_t c, int64_t col
   before.w = __shfl_up_sync(0xffffffffu, v.w, 1);
   if (!live) return;
   uint16_t* first = row + c;
-  const int at = int(reinterpret_cast<uintptr_t>(first) >> 1) & 7;  // values of the piece that lie before c
+  const int at = off_piece(first);  // values of the piece that lie before c
   const int n = int(cols - c < 8 ? cols - c : 8);
   if (at == 0) {
     if (n == 8)
@@ -91,13 +93,17 @@ __device__ __forceinline__ void store8_any(uint16_t* row, int64_t c, int64_t col
       store_some(first, v, 0, n);
     return;
   }
-  const bool joined = lane > 0 && c > 0, handed_on = lane < 31 && c + 8 < cols;
   const uint4 piece = eight_from(before, v, 8 - at);
   if (joined && at + n >= 8)
     *reinterpret_cast<uint4*>(first - at) = piece;
   else
     store_some(first - at, piece, joined ? 0 : at, at + n < 8 ? at + n : 8);
   if (!handed_on) store_some(first, v, 8 - at, n);
+}
+// Lanes with consecutive eights of rows, one row after the other.
+__device__ __forceinline__ void store8_any(uint16_t* row, int64_t c, int64_t cols, uint4 v, bool live) {
+  const int lane = threadIdx.x & 31;
+  store8_run(row, c, cols, v, live, lane > 0 && c > 0, lane < 31 && c + 8 < cols);
 }
 
 }  // namespace fp8k

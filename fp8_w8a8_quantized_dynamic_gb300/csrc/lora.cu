@@ -278,7 +278,7 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Pieces of 16, 4 or 2 bytes, as rows start and end.
+// Pieces of 16 or 4 bytes.
 template <int kBytes>
 struct PieceOf;
 template <>
@@ -289,19 +289,9 @@ template <>
 struct PieceOf<4> {
   using type = uint32_t;
 };
-template <>
-struct PieceOf<2> {
-  using type = uint16_t;
-};
 __device__ __forceinline__ void ld_shared_piece(uint4& v, uint32_t a) { v = lds128(a); }
 __device__ __forceinline__ void ld_shared_piece(uint32_t& v, uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void ld_shared_piece(uint16_t& v, uint32_t a) {
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void st_shared_piece(uint32_t a, uint16_t v) {
-  asm volatile("st.shared.u16 [%0], %1;" :: "r"(a), "h"(v) : "memory");
 }
 template <int kBytes>
 __device__ __forceinline__ void copy_async(uint32_t dst, const uint16_t* src) {
@@ -515,10 +505,10 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
             for (int row = first + 32 * kAhead; row < p.rp; row += 32)
               sts128(st + kXBytes + swizzled(row, piece),
                      row < r && k < K ? load8_any(A + int64_t(row) * K, k, K) : make_uint4(0, 0, 0, 0));
-            if (filled + 1 < steps) load(filled + 1);
-            fence_async();
+            fence_async();  // (before the next loads: it waits for what is in flight)
             if (threadIdx.x == 0) mbar_arrive(bar);  // (in place of the arrival that announces A's bytes)
             mbar_arrive(bar);
+            if (filled + 1 < steps) load(filled + 1);
           }
         }
       }
@@ -598,7 +588,7 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
 //                  a slot of shared memory and writes the result over y there.
 //   issuing warp   loads B by TMA, two or three steps ahead, and issues the MMAs. Where the rows of B do not start on 16-byte
 //                  boundaries (a rank that is no multiple of eight), four warps more load it in whole pieces.
-//   copying warps  y into the slots, by asynchronous copies of kPiece bytes (of 2: by loads) as far ahead as there are slots, and out from them: 16
+//   copying warps  y into the slots, by asynchronous copies of kPiece bytes (2: any rows, by loads) as far ahead as there are slots, and out from them: 16
 //                  rows each, whole lines at a time (the rows of a tile may be any tokens).
 // What was measured for 8192 x 14336: rows loaded and stored by the joining threads, 32 bytes of a row at a time, 111 us
 // (each asks the L2 for a single sector); a bulk copy of 256 bytes a row each way 470 us (some 60 cycles a copy).
@@ -640,8 +630,8 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
     const int pieces = p.rp / 8, n_pieces = kBn * pieces;
     const float inv_pieces = 1.0f / float(pieces);
     const int me = threadIdx.x - (kJoinWarps + 1 + kCopyWarps) * 32;
-    Place at;
-    int free_bufs = p.b_bufs;
+    Place at, last;  // a buffer is free once its last turn's MMAs are done
+    int untouched = p.b_bufs;
     bool ok = true;
     for (int64_t u = begin; ok && u < end;) {
       const int tile = int(u / steps), s0 = int(u - int64_t(tile) * steps), s1 = int(min(int64_t(steps), s0 + (end - u)));
@@ -650,10 +640,12 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       if (t.expert >= g.adapters) continue;
       const uint16_t* B = g.b + int64_t(t.expert) * N * g.rank;
       for (int s = s0; s < s1; ++s, at.next(p.b_bufs)) {
-        if (free_bufs > 0)
-          --free_bufs;
-        else if (!(ok = wait_at(ctl.freed, at)))
-          break;
+        if (untouched > 0) {
+          --untouched;
+        } else {
+          if (!(ok = wait_at(ctl.freed, last))) break;
+          last.next(p.b_bufs);
+        }
         const uint32_t to = b_at + uint32_t(at.i) * b_bytes;
         for (int i0 = me; i0 < n_pieces; i0 += 4 * kBThreads) {  // four loads at once
           Raw8 v[4];
@@ -680,11 +672,11 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
     }
   } else if (warp > kJoinWarps) {
     // ---------------- copies of y and out: kCopyRows rows a warp, lane l knows the token of the l-th ----------------
-    constexpr int kCols = kPiece / 2;                                       // of a lane
+    constexpr int kCols = kPiece == 2 ? 8 : kPiece / 2;                     // of a lane
     constexpr int kLanes = kBn / kCols < 32 ? kBn / kCols : 32;             // of a row
     constexpr int kRowsAt = 32 / kLanes, kParts = kBn / kCols / kLanes;     // rows at a time, parts of a row
     constexpr int kTimes = kCopyRows / kRowsAt * kParts;
-    constexpr int kBatch = kTimes < 64 / kPiece ? kTimes : kPiece == 16 ? 4 : 16;
+    constexpr int kBatch = kPiece == 4 ? (kTimes < 16 ? kTimes : 16) : (kTimes < 4 ? kTimes : 4);
     const int first = (warp - kJoinWarps - 1) * kCopyRows, at_row = lane / kLanes, at_col = (lane % kLanes) * kCols;
     struct Walk {
       int64_t u;      // the step after this part of a tile
@@ -724,17 +716,22 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
         } else {
+          // rows that start off 4-byte boundaries: whole pieces, shifted into place
 #pragma unroll 1
           for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
-            uint16_t v[kBatch];
+            Raw8 v[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-              const int token = __shfl_sync(0xffffffffu, in.token, row_of(i0 + i) + at_row), n = col + part_of(i0 + i);
-              v[i] = token >= 0 && n < N ? g.y[token * g.ldy + n] : uint16_t(0);
+              const int token = __shfl_sync(0xffffffffu, in.token, row_of(i0 + i) + at_row);
+              const uint16_t* row = g.y + (token >= 0 ? token * g.ldy : 0);
+              v[i] = load8_raw(row, off_piece(row), col, token >= 0 ? N : 0);  // (col is whole eights)
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-              st_shared_piece(to + uint32_t(row_of(i0 + i)) * kPitch + part_of(i0 + i) * 2u, v[i]);
+            for (int i = 0; i < kBatch; ++i) {
+              const int token = __shfl_sync(0xffffffffu, in.token, row_of(i0 + i) + at_row);
+              const uint16_t* row = g.y + (token >= 0 ? token * g.ldy : 0);
+              sts128(to + uint32_t(row_of(i0 + i)) * kPitch, values8(v[i], off_piece(row), col, token >= 0 ? N : 0));
+            }
           }
           mbar_arrive(bar);
         }
@@ -743,7 +740,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       if (!__all_sync(0xffffffffu, wait_at(ctl.y_out, out_at))) break;
       const uint32_t from = mine + uint32_t(out_at.i) * kSlotBytes;
       const int col = out.s * kBn + at_col;
-      using Piece = typename PieceOf<kPiece>::type;
+      using Piece = typename PieceOf<kPiece == 2 ? 16 : kPiece>::type;
 #pragma unroll 1
       for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
         Piece v[kBatch];
@@ -753,7 +750,11 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           const int token = __shfl_sync(0xffffffffu, out.token, row_of(i0 + i) + at_row), n = col + part_of(i0 + i);
-          if (token >= 0 && n < N) *reinterpret_cast<Piece*>(g.out + token * g.ldo + n) = v[i];
+          if constexpr (kPiece == 2)
+            store8_run(g.out + (token >= 0 ? token * g.ldo : 0), n, N, v[i], token >= 0 && n < N, lane % kLanes > 0,
+                       lane % kLanes < kLanes - 1 && n + 8 < N);
+          else if (token >= 0 && n < N)
+            *reinterpret_cast<Piece*>(g.out + token * g.ldo + n) = v[i];
         }
       }
       --held;
@@ -895,13 +896,14 @@ bool allow_smem(const void* kfn) {
 }
 }  // namespace
 
-// K splits of the first product: CTAs for the SMs, each with at least four blocks of K, and no more than pay for themselves:
-// a block takes 0.65 us, and each split of a tile's sums about 0.01 us a rank to read in the second product.
+// K splits of the first product: CTAs for the SMs, each with at least four blocks of K (two where rows are shifted into place),
+// and no more than pay for themselves: a block takes 0.65 us (1.5 to 2.2 so), and each split of a tile's sums about 0.01 us a
+// rank to read in the second product.
 int splits_of(int64_t M, int64_t K, int64_t adapters, int64_t rank) {
   const int64_t tiles = (M + kTileRows - 1) / kTileRows + std::min(M, adapters) / 2;
   const int64_t kb = (K + kBk - 1) / kBk;
-  int64_t want = std::max<int64_t>(1, std::min<int64_t>(kb / 4, 2 * 152 / tiles));
-  while (want > 1 && want * want * padded_rank(rank) > 65 * kb) --want;
+  int64_t want = std::max<int64_t>(1, std::min<int64_t>(K % 8 == 0 ? kb / 4 : kb / 2, 2 * 152 / tiles));
+  while (want > 1 && want * want * padded_rank(rank) > (K % 8 == 0 ? 65 : 150) * kb) --want;
   const int64_t slice = (kb + want - 1) / want;
   return int(std::max<int64_t>(1, (kb + slice - 1) / std::max<int64_t>(slice, 1)));
 }

@@ -75,6 +75,19 @@ def test_many_adapters(M, adapters):
     check(operands(M, 128, 136, 8, adapters, M))
 
 
+@pytest.mark.parametrize("r", [8, 12, 64, 100, 129, 192, 250])
+@pytest.mark.parametrize("N", [12000, 12002, 12003])
+def test_many_steps_of_a_cta(r, N):
+    """More column steps than a CTA has buffers, for every form of B's, y's and out's loads; tiles that end within a CTA's
+    run."""
+    d = operands(530, 72, N, r, 3, r)
+    check(d)
+    one = {k: v.to(DEV) for k, v in d.items()}
+    y = one["y"].clone()  # in place: rows without an adapter take no part
+    assert torch.equal(F.fp8_lora_add(y, *list(one.values())[1:], out=y), run(d))
+    assert F.fp8_last_device_status() == F.FP8_OK
+
+
 def test_ids_outside_and_all_bare():
     M = 603
     wild = torch.tensor([-1, 3, -2 ** 31, 2 ** 31 - 1, 2, 0, 4, 511, 512], dtype=torch.int32)
