@@ -100,6 +100,43 @@ __device__ __forceinline__ void store8_run(uint16_t* row, int64_t c, int64_t col
     store_some(first - at, piece, joined ? 0 : at, at + n < 8 ? at + n : 8);
   if (!handed_on) store_some(first, v, 8 - at, n);
 }
+// The same for sixteen values a lane, lo and hi.
+__device__ __forceinline__ void store16_run(uint16_t* row, int64_t c, int64_t cols, uint4 lo, uint4 hi, bool live, bool joined,
+                                            bool handed_on) {
+  uint4 before;
+  before.x = __shfl_up_sync(0xffffffffu, hi.x, 1);
+  before.y = __shfl_up_sync(0xffffffffu, hi.y, 1);
+  before.z = __shfl_up_sync(0xffffffffu, hi.z, 1);
+  before.w = __shfl_up_sync(0xffffffffu, hi.w, 1);
+  if (!live) return;
+  uint16_t* first = row + c;
+  const int at = off_piece(first);
+  const int n = int(cols - c < 16 ? cols - c : 16);
+  if (at != 0) {
+    const uint4 piece = eight_from(before, lo, 8 - at);
+    if (joined && at + n >= 8)
+      *reinterpret_cast<uint4*>(first - at) = piece;
+    else
+      store_some(first - at, piece, joined ? 0 : at, at + n < 8 ? at + n : 8);
+    lo = eight_from(lo, hi, 8 - at);
+    first += 8 - at;
+  }
+  // now lo holds the values from `first` on; the last `at` of hi go to the next lane
+  const int left = n - (at != 0 ? 8 - at : 0);
+  if (left >= 8)
+    *reinterpret_cast<uint4*>(first) = lo;
+  else
+    store_some(first, lo, 0, left);
+  if (at == 0) {
+    if (n == 16)
+      *reinterpret_cast<uint4*>(first + 8) = hi;
+    else
+      store_some(first + 8, hi, 0, n - 8);
+  } else if (!handed_on) {
+    store_some(row + c + 8, hi, 8 - at, n - 8);
+  }
+}
+
 // Lanes with consecutive eights of rows, one row after the other.
 __device__ __forceinline__ void store8_any(uint16_t* row, int64_t c, int64_t cols, uint4 v, bool live) {
   const int lane = threadIdx.x & 31;

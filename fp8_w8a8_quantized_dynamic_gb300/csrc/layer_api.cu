@@ -56,6 +56,7 @@ fp8_status launch_norm_any(const norm::Params& p, int sms, cudaStream_t st) {
   if (!p.vec) {
     if (units <= 32) return launch_norm<32, 1, false>(p, sms, st);
     if (units <= 128) return launch_norm<128, 1, false>(p, sms, st);
+    if (units <= 256) return launch_norm<256, 1, false>(p, sms, st);
     if (units <= 512) return launch_norm<512, 1, false>(p, sms, st);
     if (units <= 1024) return launch_norm<1024, 1, false>(p, sms, st);
     return launch_norm<1024, 2, false>(p, sms, st);

@@ -10,6 +10,7 @@
 
 #include <algorithm>
 
+#include "any_rows.cuh"
 #include "block_gemm.h"
 #include "device_common.cuh"
 #include "tcgen05.cuh"
@@ -100,19 +101,24 @@ __device__ __forceinline__ Held load_unit_any(const uint16_t* row, int c, int co
   uint32_t w[12];
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const uint4 v = 8 * i - shift < n ? load_16(piece + i) : make_uint4(0, 0, 0, 0);
+    const uint4 v = 8 * i - shift < n ? load_piece(piece + i) : make_uint4(0, 0, 0, 0);
     w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
   }
+  if (shift != 0) {
 #pragma unroll
-  for (int i = 0; i < 10; ++i) w[i] = shift & 4 ? w[i + 2] : w[i];
+    for (int i = 0; i < 10; ++i) w[i] = shift & 4 ? w[i + 2] : w[i];
 #pragma unroll
-  for (int i = 0; i < 9; ++i) w[i] = shift & 2 ? w[i + 1] : w[i];
+    for (int i = 0; i < 9; ++i) w[i] = shift & 2 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], shift & 1 ? 16 : 0);
+  }
+  if (n < kUnit) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xFFFFu : 0u;
+  }
   Held h;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    h.w[i] = __funnelshift_r(w[i], w[i + 1], shift & 1 ? 16 : 0);
-    if (n < kUnit) h.w[i] = 2 * i + 1 < n ? h.w[i] : 2 * i < n ? h.w[i] & 0xFFFFu : 0u;
-  }
+  for (int i = 0; i < 8; ++i) h.w[i] = w[i];
   return h;
 }
 
@@ -140,24 +146,16 @@ __device__ __forceinline__ Held load_weights(const uint16_t* w, int c, int cols)
   put8(h, 4, c + 8 < cols ? __ldg(reinterpret_cast<const uint4*>(w + c + 8)) : make_uint4(0, 0, 0, 0));
   return h;
 }
-// The units of a warp's lanes, from column c on, as bf16. Rows that start and end anywhere pass through the warp's kilobyte of
-// shared memory, so that its lanes store neighbouring columns (777 x 1001: 6.4 us; a unit a lane at a time 15.7).
+// The units of a warp's lanes as bf16, each from its column c on; rows that start and end anywhere by whole warps.
 template <bool kVec>
-__device__ __forceinline__ void store_unit(uint16_t* row, int c, int cols, int wide, const Values& v, uint32_t* stage) {
+__device__ __forceinline__ void store_unit(uint16_t* row, int c, int cols, int wide, const Values& v) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = cvt_bf16x2(v.p[i]);
   if constexpr (!kVec) {
-    const int lane = threadIdx.x & 31, c0 = c - lane * kUnit;
-    if (c0 >= cols) return;  // (the whole warp)
-    *reinterpret_cast<uint4*>(stage + lane * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(stage + lane * 8 + 4) = make_uint4(w[4], w[5], w[6], w[7]);
-    __syncwarp();
-    const uint16_t* from = reinterpret_cast<const uint16_t*>(stage);
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i)
-      if (c0 + i * 32 + lane < cols) row[c0 + i * 32 + lane] = from[i * 32 + lane];
-    __syncwarp();
+    const int lane = threadIdx.x & 31;
+    store16_run(row, c, cols, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]), c < cols, lane > 0,
+                lane < 31 && c + kUnit < cols);
   } else if (c >= cols) {
     return;
   } else if (wide) {
@@ -283,7 +281,6 @@ template <int kThreads, int kUnits, bool kPost, bool kGate, bool kVec>
 __global__ void __launch_bounds__(kThreads, ctas_of(kThreads, kUnits))
 residual_norm_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) float red[2][kThreads / 32];
-  __shared__ __align__(16) uint32_t stage[kVec ? 1 : kThreads / 32][kVec ? 4 : 32 * kUnit / 2];
   pdl_trigger();
   const int cols = p.cols;
   auto col_of = [&](int i) { return (i * kThreads + int(threadIdx.x)) * kUnit; };
@@ -328,7 +325,7 @@ residual_norm_kernel(const __grid_constant__ Params p) {
     if (p.r) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i)
-        store_unit<kVec>(p.r + row * p.ldro, col_of(i), cols, p.wide, v[i], stage[kVec ? 0 : threadIdx.x >> 5]);
+        store_unit<kVec>(p.r + row * p.ldro, col_of(i), cols, p.wide, v[i]);
     }
     if (!p.pre) continue;
     const float inv = inverse_rms<kThreads, kUnits>(v, p, red, turn);
@@ -341,7 +338,7 @@ residual_norm_kernel(const __grid_constant__ Params p) {
         for (int j = 0; j < 8; ++j)
           v[i].p[j] = pack_f32x2(c + 2 * j < cols ? lo_of(v[i].p[j]) : 0.0f, c + 2 * j + 1 < cols ? hi_of(v[i].p[j]) : 0.0f);
       }
-      if (p.n) store_unit<kVec>(p.n + row * p.ldn, c, cols, p.wide, v[i], stage[kVec ? 0 : threadIdx.x >> 5]);
+      if (p.n) store_unit<kVec>(p.n + row * p.ldn, c, cols, p.wide, v[i]);
       if (p.q) {
         const float s = block_scale(v[i]);
         const uint4 q = codes_of(v[i], s);
