@@ -780,7 +780,8 @@ def fp8_moe_combine(ys, pos, weights=None, out=None):
 
 def fp8_moe_combine_grad(dy, ys, pos, weights, out=None):
     """The gradient of fp8_moe_combine: (dys [R, H] with dys[pos[t, j]] = weights[t, j] dy[t], dw fp32 [T, k] with
-    <dy[t], ys[pos[t, j]]>). Rows of dys that no pair has are not written; out may be ys."""
+    <dy[t], ys[pos[t, j]]>). No two pairs may have the same row (those of fp8_moe_dispatch do not). Rows of dys that no
+    pair has are not written; out may be ys."""
     torch = _torch_module or _torch()
     f32, T, H, lddy = _check_rows_in(dy, "dy")
     index = dy.get_device()

@@ -119,6 +119,11 @@ inline fp8_status check_bf16_mat(const void* p, int64_t rows, int64_t cols, int6
   return FP8_OK;
 }
 
+// Whether an output is written over an input with another row stride, so that rows fall on other rows.
+inline bool crosses(const void* out, int64_t ldo, const void* in, int64_t ldi, int64_t rows) {
+  return out != nullptr && out == in && rows > 1 && ldo != ldi;
+}
+
 inline fp8_status check_fp8_mat(const void* p, int64_t rows, int64_t cols, int64_t ld) {
   if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return FP8_ERR_INVALID_ARG;
   if (ld < std::max<int64_t>(round_up16(cols), 16)) return FP8_ERR_INVALID_ARG;

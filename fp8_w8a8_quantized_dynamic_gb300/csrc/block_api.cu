@@ -648,7 +648,8 @@ FP8_API fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H
   // the widest pieces that every row of both consists of
   const int64_t any = int64_t(reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(xs)) | H * size |
                       (T > 1 ? ldx * size : 0) | (T * k > 1 ? ldxs * size : 0);
-  if (few_pairs(T, k)) {
+  // (a grid has up to 65535 CTAs a token)
+  if (few_pairs(T, k) && H <= int64_t(65535) * moe::kRowThreads) {
     auto go = [&](auto piece) {
       return launch_few_rows_out<decltype(piece)>(x, H * size, ldx * size, T, ids, k, E, pos, offsets, xs, ldxs * size,
                                                   st);
@@ -704,6 +705,7 @@ FP8_API fp8_status fp8_moe_combine_grad(const void* dy, int f32, int64_t T, int6
   FP8_TRY(check_rows(dy, f32, T, H, lddy));
   FP8_TRY(check_rows(ys, f32, R, H, ldys));
   FP8_TRY(check_rows(dys, f32, R, H, lddys));
+  if (crosses(dys, lddys, ys, ldys, R)) return FP8_ERR_INVALID_ARG;
   if (!aligned(pos, 4) || !aligned(weights, 4) || !aligned(dw, 4)) return FP8_ERR_MISALIGNED;
   if (T == 0) return FP8_OK;
   if (pos == nullptr || weights == nullptr || dw == nullptr) return FP8_ERR_INVALID_ARG;

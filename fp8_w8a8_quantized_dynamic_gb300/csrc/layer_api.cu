@@ -81,6 +81,7 @@ fp8_status fill_norm(norm::Params& p, const void* y, int64_t M, int64_t H, int64
   if (gate != nullptr && ldg != 0) FP8_TRY(check_bf16_mat(gate, M, H, ldg));
   if (residual != nullptr) FP8_TRY(check_bf16_mat(residual, M, H, ldr));
   if (r != nullptr) FP8_TRY(check_bf16_mat(r, M, H, ldro));
+  if (crosses(r, ldro, y, ldy, M) || crosses(r, ldro, residual, ldr, M)) return FP8_ERR_INVALID_ARG;
   FP8_TRY(check_row_vector(post_w));
   FP8_TRY(check_row_vector(gate));
   FP8_TRY(check_row_vector(w));
@@ -160,6 +161,7 @@ FP8_API fp8_status fp8_residual_norm(const void* y_bf16, int64_t M, int64_t H, i
   FP8_TRY(fill_norm(p, y_bf16, M, H, ldy, post_w_bf16, gate_bf16, ldg, scale, residual_bf16, ldr, w_bf16, eps,
                     plus_one, r_bf16, ldro));
   if (n_bf16 != nullptr) FP8_TRY(check_bf16_mat(n_bf16, M, H, ldn));
+  if (crosses(n_bf16, ldn, y_bf16, ldy, M) || crosses(n_bf16, ldn, residual_bf16, ldr, M)) return FP8_ERR_INVALID_ARG;
   if (M == 0 || H == 0) return FP8_OK;
   if ((w_bf16 == nullptr) != (n_bf16 == nullptr)) return FP8_ERR_INVALID_ARG;
   if (n_bf16 == nullptr && r_bf16 == nullptr) return FP8_ERR_INVALID_ARG;
@@ -211,7 +213,7 @@ FP8_API fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_
   FP8_TRY(check_bf16_mat(out_bf16, M, N, ldo));
   if (!aligned(a_bf16, 2) || !aligned(b_bf16, 2) || !aligned(ids, 4) || !aligned(scales, 4)) return FP8_ERR_MISALIGNED;
   if (M == 0 || N == 0) return FP8_OK;
-  if (out_bf16 == y_bf16 && M > 1 && ldo != ldy) return FP8_ERR_INVALID_ARG;
+  if (crosses(out_bf16, ldo, y_bf16, ldy, M)) return FP8_ERR_INVALID_ARG;
   const bool none = K == 0 || L == 0;
   if (!none && (a_bf16 == nullptr || b_bf16 == nullptr || ids == nullptr)) return FP8_ERR_INVALID_ARG;
   FP8_TRY(check_ws(ws, ws_bytes, fp8_lora_workspace_bytes(M, K, N, L, r)));

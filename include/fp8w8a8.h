@@ -411,7 +411,8 @@ fp8_status fp8_moe_experts(const void* x_bf16, int64_t T, int64_t H, int64_t ldx
  *
  * fp8_moe_dispatch: pair (t, j) with ids[t, j] in [0, E) gets row pos[t, j] of xs, rows sorted by expert and, within one,
  * by t and j; any other id gets pos -1 and no row. offsets[e] is expert e's first row, offsets[E] the number
- * of rows; xs[pos[t, j]] = x[t]. xs has T * k rows and may not overlap x; those from offsets[E] on are left as they were. ids and pos int32
+ * of rows; xs[pos[t, j]] = x[t]. xs has T * k rows; those from offsets[E] on are left as they were. What is written
+ * may not overlap what is read. ids and pos int32
  * [T, k], offsets int32 [E + 1], in device memory. ws: >= fp8_moe_dispatch_workspace_bytes, 256-byte aligned.
  */
 size_t fp8_moe_dispatch_workspace_bytes(int64_t T, int64_t k, int64_t E);
@@ -425,7 +426,8 @@ fp8_status fp8_moe_combine(const void* ys, int f32, int64_t R, int64_t H, int64_
                            const float* weights, int64_t T, int64_t k, void* y, int64_t ldy, fp8_stream_t stream);
 
 /* The gradient of fp8_moe_combine: dys[pos[t, j]] = weights[t, j] dy[t] (rows of no pair are left as they were) and
- * dw[t, j] = <dy[t], ys[pos[t, j]]>, fp32 [T, k], 0 for a pair without a row. dys may be ys. */
+ * dw[t, j] = <dy[t], ys[pos[t, j]]>, fp32 [T, k], 0 for a pair without a row. No two pairs may have the same row (those
+ * of fp8_moe_dispatch do not). dys may be ys, with the same stride. */
 fp8_status fp8_moe_combine_grad(const void* dy, int f32, int64_t T, int64_t H, int64_t lddy, const void* ys, int64_t R,
                                 int64_t ldys, const int32_t* pos, const float* weights, int64_t k, void* dys,
                                 int64_t lddys, float* dw, fp8_stream_t stream);
@@ -471,7 +473,7 @@ fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_t ldy, c
  * y, residual bf16 [M, H]; post_w, w bf16 [H], with plus_one 1 both stand for
  * 1 + their values; gate bf16 [M, H] with row stride ldg, or [H] with ldg 0.
  * Writes r and n as bf16 [M, H]; either may be NULL (w NULL with n). r may be y
- * or residual itself, and so may n where r is not. The mean is over H columns;
+ * or residual itself (with the same stride), and so may n where r is not. The mean is over H columns;
  * rows whose squares pass fp32's range are normalised as the formula has it. A
  * NaN or an infinity in a row makes NaN of what it multiplies in that row and
  * of no other row. eps > 0, scale finite, H <= 32768

@@ -64,6 +64,14 @@ def test_dispatch_widths(H, dtype):
     check_dispatch(50, 3, 9, H, dtype, 0.3)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_dispatch_of_one_very_wide_row(dtype):
+    H = 65535 * 256 + 3
+    x = torch.arange(H, device="cuda").remainder(251).to(dtype)[None]
+    xs, pos, offsets = F.fp8_moe_dispatch(x, torch.tensor([[2]], dtype=torch.int32, device="cuda"), 3)
+    assert torch.equal(xs, x) and pos.tolist() == [[0]] and offsets.tolist() == [0, 0, 0, 1]
+
+
 def test_dispatch_all_dropped_and_empty():
     ids = torch.full((9, 4), -1, dtype=torch.int32, device=DEV)
     out = torch.full((36, 40), 3.0, device=DEV)

@@ -55,6 +55,17 @@ def test_norm_refusals_of_outputs():
     assert status("fp8_residual_norm_quantize", QUANT, s=P + 2) == F.FP8_ERR_MISALIGNED
 
 
+@pytest.mark.parametrize("out,ld", [("r", "ldro"), ("n", "ldn")])
+@pytest.mark.parametrize("over", ["y", "residual"])
+def test_norm_over_its_input_with_another_stride(out, ld, over):
+    apart = {**NORM, "y": Q, "residual": Q, "r": P + 4096, "n": P + 8192, over: P, out: P}
+    assert status("fp8_residual_norm", apart, **{ld: 264}) == F.FP8_ERR_INVALID_ARG
+    assert status("fp8_residual_norm", apart, **{ld: 264, "M": 0}) == F.FP8_OK
+    if out == "r":
+        quant = {**QUANT, "y": Q, "residual": Q, over: P}
+        assert status("fp8_residual_norm_quantize", quant, ldro=264) == F.FP8_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("name", ["y", "post", "gate", "residual", "w", "r"])
 def test_norm_misaligned(name):
     assert status("fp8_residual_norm", NORM, **{name: P + 1}) == F.FP8_ERR_MISALIGNED
@@ -140,6 +151,7 @@ def test_more_refusals_on_the_way_back():
         assert status("fp8_moe_combine", COMBINE, **change) == F.FP8_ERR_INVALID_ARG
     for change in (dict(lddy=63), dict(lddys=63), dict(dy=None), dict(dys=None), dict(dw=None), dict(weights=None)):
         assert status("fp8_moe_combine_grad", GRAD, **change) == F.FP8_ERR_INVALID_ARG
+    assert status("fp8_moe_combine_grad", GRAD, lddys=72) == F.FP8_ERR_INVALID_ARG  # over ys with another stride
     assert status("fp8_moe_combine", COMBINE, T=0) == F.FP8_OK and status("fp8_moe_combine", COMBINE, H=0) == F.FP8_OK
     assert status("fp8_moe_combine_grad", GRAD, T=0) == F.FP8_OK
     assert status("fp8_moe_combine_grad", GRAD, dw=P + 2) == F.FP8_ERR_MISALIGNED
