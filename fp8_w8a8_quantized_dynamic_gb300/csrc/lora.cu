@@ -324,6 +324,10 @@ __device__ __forceinline__ void copy8_async(uint32_t dst, const uint16_t* row, b
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                :: "r"(dst), "l"(live ? row + k : row), "r"(live ? 16u : 0u) : "memory");
 }
+// Four bytes, or zeros where bytes is 0.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const uint16_t* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 // What this thread wrote to shared memory becomes visible to the tensor core (after the barrier that follows).
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -409,8 +413,9 @@ __device__ __forceinline__ void tile_end(TileCtl* ctl, uint32_t cols) {
 // tokens: eight threads a 128-byte piece of a row, asynchronous 16-byte copies) and, by TMA, A's into a ring of stages, whose
 // barrier counts the copies' completion; warp 8 issues the MMAs. (With a fence for the tensor core in the copying
 // threads, which waits for their copies in flight, a step took a load's latency: 27 us for 8192 x 4096 at rank 64.)
-// kVec: the rows of x and A start on 16-byte boundaries and K is whole eights.
-template <bool kVec>
+// kPiece: the bytes of a copy, as many as all rows of x and A start and end on. 4: a warp copies 128 bytes of a row. 2: whole
+// pieces are loaded and shifted into place.
+template <int kPiece>
 __global__ void __launch_bounds__(kShrinkThreads, 2)
 shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ TileParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -421,8 +426,14 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
   const int tile = blockIdx.x;
   const Args& g = p.a;
   const int K = int(g.K), r = g.rank;
+  [[maybe_unused]] __shared__ const uint16_t* x_row[kPiece == 4 ? kTileRows : 1];
   if (tile < *p.s.n_tiles) {
     const block::RowTile t = p.s.tiles[tile];
+    if constexpr (kPiece == 4) {
+      const int row = t.row0 + int(threadIdx.x);
+      if (threadIdx.x < kTileRows && row < t.row_end) x_row[threadIdx.x] = g.x + int64_t(p.s.order[row]) * g.ldx;
+      __syncthreads();
+    }
     const int kb0 = int(blockIdx.y) * p.kb_slice, steps = min(p.kb, kb0 + p.kb_slice) - kb0;
     if (t.expert < g.adapters && steps > 0) {
       const int rows = min(kTileRows, t.row_end - t.row0);
@@ -459,7 +470,25 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
         }
         const uint16_t* A = g.a + int64_t(t.expert) * r * K;
         auto a_row = [&](int i) { return A + int64_t(min(first + 32 * i, r - 1)) * K; };
-        if constexpr (kVec) {
+        if constexpr (kPiece == 4) {
+          // (rows of x past the tile's leave nothing in others' sums: they are not copied)
+          for (; filled < steps; ++filled) {
+            if (filled >= p.stages && !(ok = wait(ctl.done, filled - p.stages))) break;
+            const uint32_t st = base + uint32_t(filled % p.stages) * stage_bytes;
+            const uint32_t bar = smem_u32(&ctl.loaded[filled % p.stages]);
+            const int k = (kb0 + filled) * kBk + 2 * lane, bytes = k < K ? 4 : 0, k_in = k < K ? k : 0;
+            const uint32_t word = uint32_t(lane & 3) * 4u;
+#pragma unroll 4
+            for (int row = warp; row < rows; row += kTileThreads / 32)
+              copy4_async(st + swizzled(row, lane >> 2) + word, x_row[row] + k_in, bytes);
+#pragma unroll 4
+            for (int row = warp; row < p.rp; row += kTileThreads / 32)
+              copy4_async(st + kXBytes + swizzled(row, lane >> 2) + word, A + int64_t(min(row, r - 1)) * K + k_in,
+                          row < r ? bytes : 0);
+            if (threadIdx.x == 0) mbar_arrive(bar);  // (in place of the arrival that announces A's bytes)
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
+          }
+        } else if constexpr (kPiece == 16) {
           for (; filled < steps; ++filled) {
             if (filled >= p.stages && !(ok = wait(ctl.done, filled - p.stages))) break;
             const uint32_t st = base + uint32_t(filled % p.stages) * stage_bytes;
@@ -938,7 +967,8 @@ bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st)
   p.kb_slice = (p.kb + s.splits - 1) / s.splits;
   p.vec = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0) && aligned(a.a, 16) && a.K % 8 == 0;
   p.vec_b = aligned(a.b, 16) && a.rank % 8 == 0;
-  auto shrink = p.vec ? shrink_kernel<true> : shrink_kernel<false>;
+  const bool words = aligned(a.x, 4) && (a.M <= 1 || a.ldx % 2 == 0) && aligned(a.a, 4) && a.K % 2 == 0;
+  auto shrink = p.vec ? shrink_kernel<16> : words ? shrink_kernel<4> : shrink_kernel<2>;
   if (!allow_smem(reinterpret_cast<const void*>(shrink))) return false;
   const int stage_bytes = int(kXBytes) + p.rp * 128;
   p.stages = std::max(3, std::min(kShrinkMaxStages, 108 * 1024 / stage_bytes));

@@ -75,6 +75,18 @@ def test_many_adapters(M, adapters):
     check(operands(M, 128, 136, 8, adapters, M))
 
 
+@pytest.mark.parametrize("K", [2, 62, 66, 1002, 5142])
+@pytest.mark.parametrize("r", [7, 16, 76, 130, 256])
+def test_rows_of_whole_words(K, r):
+    """Rows of x and A that start on 4-byte boundaries and no wider ones; more steps of K than stages; x in wider rows."""
+    d = operands(530, K, 72, r, 3, r + K)
+    want = check(d)
+    x = torch.full((530, K + 6), float("nan"), dtype=BF16, device=DEV)
+    x[:, 2:K + 2] = d["x"].to(DEV)
+    rest = {k: v.to(DEV) for k, v in d.items()}
+    assert torch.equal(F.fp8_lora_add(**{**rest, "x": x[:, 2:K + 2]}), want)
+
+
 @pytest.mark.parametrize("r", [8, 12, 64, 100, 129, 192, 250])
 @pytest.mark.parametrize("N", [12000, 12002, 12003])
 def test_many_steps_of_a_cta(r, N):
