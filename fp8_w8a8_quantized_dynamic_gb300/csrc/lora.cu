@@ -700,17 +700,18 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       }
     }
   } else if (warp > kJoinWarps) {
-    // ---------------- copies of y and out: kCopyRows rows a warp, lane l knows the token of the l-th ----------------
+    // ---------------- copies of y and out: a warp has every eighth row, lane l knows the token of the l-th ----------------
+    // (so that the few rows of a short tile are shared out)
     constexpr int kCols = kPiece == 2 ? 8 : kPiece / 2;                     // of a lane
     constexpr int kLanes = kBn / kCols < 32 ? kBn / kCols : 32;             // of a row
     constexpr int kRowsAt = 32 / kLanes, kParts = kBn / kCols / kLanes;     // rows at a time, parts of a row
     constexpr int kTimes = kCopyRows / kRowsAt * kParts;
     constexpr int kBatch = kPiece == 4 ? (kTimes < 16 ? kTimes : 16) : (kTimes < 4 ? kTimes : 4);
-    const int first = (warp - kJoinWarps - 1) * kCopyRows, at_row = lane / kLanes, at_col = (lane % kLanes) * kCols;
+    const int first = warp - kJoinWarps - 1, at_row = lane / kLanes, at_col = (lane % kLanes) * kCols;
     struct Walk {
       int64_t u;      // the step after this part of a tile
       int s, s1;      // columns of the next step, and where the part ends
-      int token;
+      int token, rows;  // .. of the warp, behind which there is nothing to copy
     };
     auto enter = [&](Walk& w) {  // the next part of a tile with something to do; false behind the last
       while (w.u < end) {
@@ -720,12 +721,14 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         w.u += w.s1 - w.s;
         const block::RowTile t = p.s.tiles[tile];
         if (t.expert >= g.adapters && g.out == g.y) continue;
-        w.token = lane < kCopyRows && first + lane < min(kTileRows, t.row_end - t.row0) ? p.s.order[t.row0 + first + lane] : -1;
+        w.rows = (min(kTileRows, t.row_end - t.row0) - first + kCopyWarps - 1) / kCopyWarps;
+        w.token = lane < w.rows ? p.s.order[t.row0 + first + lane * kCopyWarps] : -1;
         return true;
       }
       return false;
     };
-    const uint32_t mine = slots_at + uint32_t(first + at_row) * kPitch + at_col * 2u;
+    constexpr uint32_t kRowPitch = kCopyWarps * kPitch;  // from a warp's row to its next
+    const uint32_t mine = slots_at + uint32_t(first) * kPitch + uint32_t(at_row) * kRowPitch + at_col * 2u;
     // the i-th access of a lane: a row of the warp's, a part of it
     auto row_of = [&](int i) { return i / kParts * kRowsAt; };
     auto part_of = [&](int i) { return i % kParts * kLanes * kCols; };
@@ -741,13 +744,13 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
 #pragma unroll
           for (int i = 0; i < kTimes; ++i) {
             const int token = __shfl_sync(0xffffffffu, in.token, row_of(i) + at_row), n = col + part_of(i);
-            if (token >= 0 && n < N) copy_async<kPiece>(to + uint32_t(row_of(i)) * kPitch + part_of(i) * 2u, g.y + token * g.ldy + n);
+            if (token >= 0 && n < N) copy_async<kPiece>(to + uint32_t(row_of(i)) * kRowPitch + part_of(i) * 2u, g.y + token * g.ldy + n);
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" :: "r"(bar) : "memory");
         } else {
           // rows that start off 4-byte boundaries: whole pieces, shifted into place
 #pragma unroll 1
-          for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
+          for (int i0 = 0; i0 < kTimes && row_of(i0) < in.rows; i0 += kBatch) {
             Raw8 v[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
@@ -759,7 +762,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
             for (int i = 0; i < kBatch; ++i) {
               const int token = __shfl_sync(0xffffffffu, in.token, row_of(i0 + i) + at_row);
               const uint16_t* row = g.y + (token >= 0 ? token * g.ldy : 0);
-              sts128(to + uint32_t(row_of(i0 + i)) * kPitch, values8(v[i], off_piece(row), col, token >= 0 ? N : 0));
+              sts128(to + uint32_t(row_of(i0 + i)) * kRowPitch, values8(v[i], off_piece(row), col, token >= 0 ? N : 0));
             }
           }
           mbar_arrive(bar);
@@ -771,11 +774,11 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       const int col = out.s * kBn + at_col;
       using Piece = typename PieceOf<kPiece == 2 ? 16 : kPiece>::type;
 #pragma unroll 1
-      for (int i0 = 0; i0 < kTimes; i0 += kBatch) {
+      for (int i0 = 0; i0 < kTimes && row_of(i0) < out.rows; i0 += kBatch) {
         Piece v[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-          ld_shared_piece(v[i], from + uint32_t(row_of(i0 + i)) * kPitch + part_of(i0 + i) * 2u);
+          ld_shared_piece(v[i], from + uint32_t(row_of(i0 + i)) * kRowPitch + part_of(i0 + i) * 2u);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           const int token = __shfl_sync(0xffffffffu, out.token, row_of(i0 + i) + at_row), n = col + part_of(i0 + i);
