@@ -1,4 +1,5 @@
-// C ABI of the norms around a block and of the adapters beside a projection (declared in include/fp8w8a8.h): argument validation, launches.
+// C ABI of the norms around a block and of the adapters beside a projection (declared in include/fp8w8a8.h): argument
+// validation, launches.
 
 #include <cuda_runtime.h>
 

@@ -98,6 +98,9 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // kLpr lanes share a row of B (eight values of the rank each). Cluster rank c sums K slice c of v = A x
 // and sends it to all of the cluster; then every CTA adds the slices in order and computes its columns.
+// Bounds: latency for one token (4096 to 6144 at rank 16, 2.8 us); the L2 for more, which hands out an adapter's matrices to each
+// of its tokens (64 tokens, 51 of them with one of 32 adapters, 4096 to 4096 at rank 64: 11.2 us, 54 MB at 4.8 TB/s, 29 MB of them
+// from HBM).
 // kVec: all rows start on 16-byte boundaries and are whole eights. Values beyond `end` are zeros.
 template <bool kVec>
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int end) {
@@ -413,6 +416,8 @@ __device__ __forceinline__ void tile_end(TileCtl* ctl, uint32_t cols) {
 // tokens: eight threads a 128-byte piece of a row, asynchronous 16-byte copies) and, by TMA, A's into a ring of stages, whose
 // barrier counts the copies' completion; warp 8 issues the MMAs. (With a fence for the tensor core in the copying
 // threads, which waits for their copies in flight, a step took a load's latency: 27 us for 8192 x 4096 at rank 64.)
+// Bounds: the first wave's fill and the stream of x (8192 x 4096 at rank 64: 19 us, 3.8 TB/s; the tensor cores are busy for 9
+// percent). A tile of 128 rows is an MMA's; K splits fill the SMs (splits_of).
 // kPiece: the bytes of a copy, as many as all rows of x and A start and end on. 4: a warp copies 128 bytes of a row. 2: whole
 // pieces are loaded and shifted into place.
 template <int kPiece>
@@ -617,11 +622,15 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
 //                  a slot of shared memory and writes the result over y there.
 //   issuing warp   loads B by TMA, two or three steps ahead, and issues the MMAs. Where the rows of B do not start on 16-byte
 //                  boundaries (a rank that is no multiple of eight), four warps more load it in whole pieces.
-//   copying warps  y into the slots, by asynchronous copies of kPiece bytes (2: any rows, by loads) as far ahead as there are slots, and out from them: 16
-//                  rows each, whole lines at a time (the rows of a tile may be any tokens).
+//   copying warps  y into the slots, by asynchronous copies of kPiece bytes (2: rows of any alignment, by loads) as far ahead as
+//                  there are slots, and out from them: every eighth row each, whole lines at a time (the rows of a tile may be
+//                  any tokens).
 // What was measured for 8192 x 14336: rows loaded and stored by the joining threads, 32 bytes of a row at a time, 111 us
 // (each asks the L2 for a single sector); a bulk copy of 256 bytes a row each way 470 us (some 60 cycles a copy).
 // Slot rows lie 16 bytes further apart than they are long, so that eight lanes' accesses down the rows take all banks.
+// Bounds: the stream of y in and out (8192 x 14336 at rank 64 in 16 adapters: 94 us, 5.1 TB/s; the tensor cores are busy for 14
+// percent of it); one CTA an SM, whose copying warps are its loads in flight (two CTAs of 64 columns: 138 us for the call
+// against 128, then).
 constexpr int join_threads(int bn) { return bn * 4; }
 constexpr int kBThreads = 128;
 constexpr int expand_threads(int bn, bool tma) { return join_threads(bn) + 32 + kCopyThreads + (tma ? 0 : kBThreads); }
@@ -929,8 +938,8 @@ bool allow_smem(const void* kfn) {
 }  // namespace
 
 // K splits of the first product: CTAs for the SMs, each with at least four blocks of K (two where rows are shifted into place),
-// and no more than pay for themselves: a block takes 0.65 us (1.5 to 2.2 so), and each split of a tile's sums about 0.01 us a
-// rank to read in the second product.
+// and no more than pay for themselves: a block takes 0.65 us (where rows start anywhere 1.5 to 2.2), and each split of a tile's
+// sums about 0.01 us a rank to read in the second product.
 int splits_of(int64_t M, int64_t K, int64_t adapters, int64_t rank) {
   const int64_t tiles = (M + kTileRows - 1) / kTileRows + std::min(M, adapters) / 2;
   const int64_t kb = (K + kBk - 1) / kBk;

@@ -22,12 +22,12 @@ def _inverse_rms(x: np.ndarray, err: np.ndarray, eps: float):
 
     The kernel's sum of squares: two chains of at most eight fmas of packed pairs in a thread, their sum and the pair's, five
     halvings over its warp's lanes, and at most 32 warps' by fours (two and eight): 25 roundings of positive sums; then the
-    rounded 1 / count, and one fma with it and eps: 27. The root halves what came before it, and is itself off by at most two
-    units in the last place (two halves each).
+    rounded 1 / count, and one fma with it and eps: 27. The root halves what came before it and is
+    itself correctly rounded.
     """
     mean = np.mean(x * x, axis=1, keepdims=True) + eps
     inv = 1.0 / np.sqrt(mean)
-    rel = (27 / 2 + 4) * U + np.mean(np.abs(x) * err + err * err, axis=1, keepdims=True) * inv * inv
+    rel = (27 / 2 + 1) * U + np.mean(np.abs(x) * err + err * err, axis=1, keepdims=True) * inv * inv
     return inv, rel
 
 
