@@ -64,11 +64,29 @@ __device__ __forceinline__ uint4 values8(const Raw8& v, int at, int c, int cols)
   return e;
 }
 
-__device__ __forceinline__ void store_some(uint16_t* p, uint4 v, int from, int to) {  // values [from, to) of eight
+// Values [from, to) of eight to their places in a piece. Those of a piece's end or start take three stores of 8, 4 and 2 bytes
+// at most: by values, a warp's two ends took most of its stores' time (TIMES).
+__device__ __forceinline__ void store_some(uint16_t* piece, uint4 v, int from, int to) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  auto word = [&](int i) { return i & 2 ? (i & 1 ? v.w : v.z) : (i & 1 ? v.y : v.x); };
+  if (from == 0) {
+    if (to & 8) *reinterpret_cast<uint4*>(piece) = v;
+    if (to & 4) *reinterpret_cast<uint2*>(piece) = make_uint2(v.x, v.y);
+    if (to & 2) *reinterpret_cast<uint32_t*>(piece + (to & 4)) = word((to & 4) >> 1);
+    if (to & 1) piece[to - 1] = uint16_t(word(to >> 1));
+  } else if (to == 8) {
+    if (from & 1) piece[from] = uint16_t(word(from >> 1) >> 16);
+    if ((8 - from) & 2) *reinterpret_cast<uint32_t*>(piece + (from < 4 ? 2 : 6)) = from < 4 ? v.y : v.w;
+    if (from <= 4) *reinterpret_cast<uint2*>(piece + 4) = make_uint2(v.z, v.w);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i >= from && i < to) p[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+    for (int i = 0; i < 8; ++i)
+      if (i >= from && i < to) piece[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+// The last values of eight, from the from-th on, to the start of a piece: n of them at most.
+__device__ __forceinline__ void store_rest(uint16_t* piece, uint4 v, int from, int n) {
+  if (n > 0) store_some(piece, eight_from(v, make_uint4(0, 0, 0, 0), from), 0, n);
 }
 
 // Stores values c .. c + 7 of a row (those before cols): all lanes of the warp come here, `live` ones have some. Where a lane is
@@ -98,7 +116,7 @@ __device__ __forceinline__ void store8_run(uint16_t* row, int64_t c, int64_t col
     *reinterpret_cast<uint4*>(first - at) = piece;
   else
     store_some(first - at, piece, joined ? 0 : at, at + n < 8 ? at + n : 8);
-  if (!handed_on) store_some(first, v, 8 - at, n);
+  if (!handed_on) store_rest(first - at + 8, v, 8 - at, at + n - 8);
 }
 // The same for sixteen values a lane, lo and hi.
 __device__ __forceinline__ void store16_run(uint16_t* row, int64_t c, int64_t cols, uint4 lo, uint4 hi, bool live, bool joined,
@@ -126,14 +144,14 @@ __device__ __forceinline__ void store16_run(uint16_t* row, int64_t c, int64_t co
   if (left >= 8)
     *reinterpret_cast<uint4*>(first) = lo;
   else
-    store_some(first, lo, 0, left);
+    store_some(first, lo, 0, left > 0 ? left : 0);
   if (at == 0) {
     if (n == 16)
       *reinterpret_cast<uint4*>(first + 8) = hi;
     else
-      store_some(first + 8, hi, 0, n - 8);
+      store_some(first + 8, hi, 0, n > 8 ? n - 8 : 0);
   } else if (!handed_on) {
-    store_some(row + c + 8, hi, 8 - at, n - 8);
+    store_rest(row + c - at + 16, hi, 8 - at, at + n - 16);
   }
 }
 

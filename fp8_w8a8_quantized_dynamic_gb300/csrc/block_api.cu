@@ -326,7 +326,7 @@ template <typename T, int kPiece, typename... Args>
 fp8_status launch_rows_back_grad(int64_t k, Args... args) {
   if (k == 1) return launch_rows_back_grad_of<T, kPiece, 1>(args...);
   if (k == 2) return launch_rows_back_grad_of<T, kPiece, 2>(args...);
-  if (k <= 4) return launch_rows_back_grad_of<T, kPiece, 4>(args...);
+  if (k <= 4 || kPiece == 2) return launch_rows_back_grad_of<T, kPiece, 4>(args...);
   return launch_rows_back_grad_of<T, kPiece, 8>(args...);
 }
 

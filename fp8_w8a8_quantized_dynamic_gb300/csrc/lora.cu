@@ -232,11 +232,13 @@ bool launch_tokens(const Args& a, int num_sms, cudaStream_t st) {
   TokenParams p = {};
   p.a = a;
   p.k_slice = int(((a.K + 7) / 8 + kCluster - 1) / kCluster * 8);
-  // few tokens: several clusters a token, each with all of v and a share of the columns
-  const int64_t groups = std::max<int64_t>(1, std::min<int64_t>({4, 2 * num_sms / (kCluster * a.M), a.N / (kCluster * 128)}));
-  p.n_slice = int((a.N + kCluster * groups - 1) / (kCluster * groups));
   const bool vec = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0) && aligned(a.a, 16) && a.K % 8 == 0 &&
                    aligned(a.b, 16) && a.rank % 8 == 0;
+  // few tokens: several clusters a token, each with all of v and a share of the columns, for as many CTAs as the SMs hold (of the
+  // deep form; of that for rows of any alignment)
+  const int64_t ctas = (vec ? 2 : 3) * int64_t(num_sms);
+  const int64_t groups = std::max<int64_t>(1, std::min<int64_t>({4, ctas / (kCluster * a.M), a.N / (kCluster * 128)}));
+  p.n_slice = int((a.N + kCluster * groups - 1) / (kCluster * groups));
   if (!vec) return launch_tokens_by_rank<4, false>(p, groups, st);
   // two CTAs of the deep form fit an SM, four of the other
   return a.M * kCluster <= 2 * num_sms ? launch_tokens_by_rank<8, true>(p, groups, st) : launch_tokens_by_rank<4, true>(p, groups, st);

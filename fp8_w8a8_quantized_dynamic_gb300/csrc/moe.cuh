@@ -720,10 +720,10 @@ rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int
 // The gradient of rows_back: dys[pos[t, j]] = w[t, j] dy[t], dw[t, j] = <dy[t], ys[pos[t, j]]> (0 for a pair without a
 // row), fp32 sums in a fixed order. dys may be ys. blockDim.x threads a token (a power of two from 32), blockDim.y tokens a
 // CTA. kB: pairs at a time; where there are few, as many columns more. Bounds: HBM's reads and writes in turn (8192 tokens of
-// eight rows of 2048 bf16, 101 us, 5.6 TB/s). CTAs that stay, with the pairs held by lanes, took 197 us for both gradients against
-// 171, then; five or six CTAs an SM spill.
+// eight rows of 2048 bf16, 90 us, 6.3 TB/s; 101 at four CTAs an SM, with spills). CTAs that stay, with the pairs held by lanes, took
+// 197 us for both gradients against 171, then.
 template <typename T, int kPiece, int kB>
-__global__ void __launch_bounds__(kRowThreads, 4)
+__global__ void __launch_bounds__(kRowThreads, kB == 8 ? 3 : 4)
 rows_back_grad_kernel(const T* __restrict__ dy, int64_t lddy, const T* ys, int64_t ldys, int64_t rows,
                       const int* __restrict__ pos, const float* __restrict__ weights, int k, int64_t tokens, int64_t cols,
                       T* dys, int64_t lddys, float* __restrict__ dw) {
