@@ -296,7 +296,7 @@ fp8_status launch_rows_back_of(const void* ys, int64_t ldys, int64_t R, const in
   constexpr int kCols = moe::kColsOf<T, kPiece>;
   const int64_t units = tokens * ((H + kCols - 1) / kCols);
   return launch(moe::rows_back_kernel<T, kPiece, kB>,
-                dim3(elementwise_grid(units, moe::kRowThreads * moe::kRowBatch / kB, sms, 1024)), dim3(moe::kRowThreads), 0,
+                dim3(elementwise_grid(units, moe::kRowThreads * moe::kRowBatch<kPiece> / kB, sms, 1024)), dim3(moe::kRowThreads), 0,
                 st, true, dim3(1, 1, 1), static_cast<const T*>(ys), ldys, R, pos, weights, int(k), tokens, H,
                 static_cast<T*>(y), ldy);
 }
@@ -306,8 +306,9 @@ fp8_status launch_rows_back(int64_t k, int64_t tokens, int64_t H, int sms, Args.
   const bool many = tokens * (H / moe::kColsOf<T, kPiece>) >= int64_t(sms) * 2048;
   if (k == 1 && many) return launch_rows_back_of<T, kPiece, 1>(args...);
   if (k == 2 && many) return launch_rows_back_of<T, kPiece, 2>(args...);
-  if (k <= 4) return launch_rows_back_of<T, kPiece, 4>(args...);
-  return launch_rows_back_of<T, kPiece, 8>(args...);
+  if constexpr (moe::kRowBatch<kPiece> == 8)
+    if (k > 4) return launch_rows_back_of<T, kPiece, 8>(args...);
+  return launch_rows_back_of<T, kPiece, 4>(args...);
 }
 
 template <typename T, int kPiece, int kB>
@@ -326,8 +327,9 @@ template <typename T, int kPiece, typename... Args>
 fp8_status launch_rows_back_grad(int64_t k, Args... args) {
   if (k == 1) return launch_rows_back_grad_of<T, kPiece, 1>(args...);
   if (k == 2) return launch_rows_back_grad_of<T, kPiece, 2>(args...);
-  if (k <= 4 || kPiece == 2) return launch_rows_back_grad_of<T, kPiece, 4>(args...);
-  return launch_rows_back_grad_of<T, kPiece, 8>(args...);
+  if constexpr (moe::kRowBatch<kPiece> == 8)
+    if (k > 4) return launch_rows_back_grad_of<T, kPiece, 8>(args...);
+  return launch_rows_back_grad_of<T, kPiece, 4>(args...);
 }
 
 }  // namespace

@@ -101,14 +101,29 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // Bounds: latency for one token (4096 to 6144 at rank 16, 2.8 us); the L2 for more, which hands out an adapter's matrices to each
 // of its tokens (64 tokens, 51 of them with one of 32 adapters, 4096 to 4096 at rank 64: 11.2 us, 54 MB at 4.8 TB/s, 29 MB of them
 // from HBM).
-// kVec: all rows start on 16-byte boundaries and are whole eights. Values beyond `end` are zeros.
+// kVec: all rows start on 16-byte boundaries and are whole eights. Values beyond `end` are zeros. (What was loaded is shifted into
+// place where it is used: until then more loads go out. 26 tokens, 128 to 12544 at rank 47: 28.5 us when each was shifted at once,
+// 20.2
+// so.)
 template <bool kVec>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int end) {
-  return kVec ? ld_nc_v4(row + c) : load8_any(row, c, end);
-}
+struct Eight {
+  Raw8 v;
+  __device__ __forceinline__ void load(const uint16_t* row, int c, int end, bool live) {
+    v = load8_raw(row, off_piece(row), c, live ? end : 0);
+  }
+  __device__ __forceinline__ uint4 get(int at, int c, int end) const { return values8(v, at, c, end); }
+};
+template <>
+struct Eight<true> {
+  uint4 v;
+  __device__ __forceinline__ void load(const uint16_t* row, int c, int, bool live) {
+    v = live ? ld_nc_v4(row + c) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ uint4 get(int, int, int) const { return v; }
+};
 
 template <int kLpr, int kLoads, bool kVec>
-__global__ void __launch_bounds__(kTokenThreads, kLoads == 8 ? 2 : kVec ? 4 : 3)
+__global__ void __launch_bounds__(kTokenThreads, kLoads == 8 || !kVec ? 2 : 4)
 tokens_kernel(const __grid_constant__ TokenParams p) {
   constexpr int kU = kLpr < kLoads ? kLpr : kLoads;  // loads of a batch; a lane ends with one column of it
   constexpr int kBatches = kLoads / kU;              // batches in flight
@@ -140,16 +155,16 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   const uint16_t* B = g.b + int64_t(e) * N * r;
   const int sub = lane % kLpr, row_in_load = lane / kLpr;
   // the first loads of B and y are under way while v is summed
-  uint4 bv[kLoads];
+  Eight<kVec> bv[kLoads];
   uint16_t yv[kBatches];
   const int my_u = halving_index<kLpr, kU>(lane);
   auto col_of = [&](int base, int b) { return base + b * kBatchCols + my_u * kRowsPerLoad + row_in_load; };
+  auto row_of = [&](int base, int q) { return base + (q / kU) * kBatchCols + (q % kU) * kRowsPerLoad + row_in_load; };
   auto load_b = [&](int base) {
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
-      const int n = base + (q / kU) * kBatchCols + (q % kU) * kRowsPerLoad + row_in_load;
-      bv[q] = make_uint4(0, 0, 0, 0);
-      if (n < n1 && sub * 8 < r) bv[q] = load8<kVec>(B + int64_t(n) * r, sub * 8, r);
+      const int n = row_of(base, q);
+      bv[q].load(B + int64_t(n) * r, sub * 8, r, n < n1 && sub * 8 < r);
     }
 #pragma unroll
     for (int b = 0; b < kBatches; ++b) yv[b] = col_of(base, b) < n1 ? y[col_of(base, b)] : uint16_t(0);
@@ -164,21 +179,22 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   for (int i0 = warp * per_warp; i0 < i_end; i0 += 4) {
     float acc[4] = {};
     for (int k = k0 + lane * 8; k < k1; k += 256 * kHalves) {  // four rows at a time
-      uint4 xv[kHalves], av[kHalves][4];
+      Eight<kVec> xv[kHalves], av[kHalves][4];
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         const int kh = k + 256 * h;
-        xv[h] = kh < k1 ? load8<kVec>(x, kh, k1) : make_uint4(0, 0, 0, 0);
+        xv[h].load(x, kh, k1, kh < k1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          av[h][i] = kh < k1 && i0 + i < i_end ? load8<kVec>(A + int64_t(i0 + i) * K, kh, k1) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 4; ++i) av[h][i].load(A + int64_t(i0 + i) * K, kh, k1, kh < k1 && i0 + i < i_end);
       }
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
+        const int kh = k + 256 * h;
         float f[8];
-        unpack8(xv[h], f);
+        unpack8(xv[h].get(off_piece(x), kh, k1), f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = dot8(av[h][i], f, acc[i]);
+        for (int i = 0; i < 4; ++i)
+          acc[i] = dot8(av[h][i].get(off_piece(A + int64_t(i0 + i) * K), kh, i0 + i < i_end ? k1 : 0), f, acc[i]);
       }
     }
     // eight lanes end with the sum of a row: each sends it to one of the cluster's CTAs
@@ -200,7 +216,10 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
   for (int base = n0 + warp * kStepCols; base < n1; base += kTokenWarps * kStepCols) {
     float sum[kBatches][kU], was[kBatches];
 #pragma unroll
-    for (int q = 0; q < kLoads; ++q) sum[q / kU][q % kU] = dot8(bv[q], f, 0.0f);
+    for (int q = 0; q < kLoads; ++q) {
+      const int n = row_of(base, q);
+      sum[q / kU][q % kU] = dot8(bv[q].get(off_piece(B + int64_t(n) * r), sub * 8, n < n1 ? r : 0), f, 0.0f);
+    }
 #pragma unroll
     for (int b = 0; b < kBatches; ++b) was[b] = bf16_bits_to_float(yv[b]);
     if (base + kTokenWarps * kStepCols < n1) load_b(base + kTokenWarps * kStepCols);
@@ -234,10 +253,8 @@ bool launch_tokens(const Args& a, int num_sms, cudaStream_t st) {
   p.k_slice = int(((a.K + 7) / 8 + kCluster - 1) / kCluster * 8);
   const bool vec = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0) && aligned(a.a, 16) && a.K % 8 == 0 &&
                    aligned(a.b, 16) && a.rank % 8 == 0;
-  // few tokens: several clusters a token, each with all of v and a share of the columns, for as many CTAs as the SMs hold (of the
-  // deep form; of that for rows of any alignment)
-  const int64_t ctas = (vec ? 2 : 3) * int64_t(num_sms);
-  const int64_t groups = std::max<int64_t>(1, std::min<int64_t>({4, ctas / (kCluster * a.M), a.N / (kCluster * 128)}));
+  // few tokens: several clusters a token, each with all of v and a share of the columns, for as many CTAs as the SMs hold
+  const int64_t groups = std::max<int64_t>(1, std::min<int64_t>({4, 2 * num_sms / (kCluster * a.M), a.N / (kCluster * 128)}));
   p.n_slice = int((a.N + kCluster * groups - 1) / (kCluster * groups));
   if (!vec) return launch_tokens_by_rank<4, false>(p, groups, st);
   // two CTAs of the deep form fit an SM, four of the other

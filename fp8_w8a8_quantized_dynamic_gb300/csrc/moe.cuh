@@ -630,6 +630,7 @@ __device__ __forceinline__ uint4 held(const float (&f)[4]) {
 __device__ __forceinline__ uint32_t held(const float (&f)[2]) { return pack_bf16x2(f[0], f[1]); }
 __device__ __forceinline__ uint32_t held(const float (&f)[1]) { return __float_as_uint(f[0]); }
 
+// (kPiece 2: as loaded, shifted into place where they are used: until then more loads go out)
 template <int kPiece>
 struct HeldAs {
   using type = uint4;
@@ -640,32 +641,50 @@ struct HeldAs<4> {
   using type = uint32_t;
   static __device__ __forceinline__ uint32_t zero() { return 0u; }
 };
+template <>
+struct HeldAs<2> {
+  using type = Raw8;
+  static __device__ __forceinline__ Raw8 zero() { return Raw8{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)}; }
+};
+// Where the values of a row start in their pieces.
+template <int kPiece, typename T>
+__device__ __forceinline__ int start_of(const T* row) {
+  return kPiece == 2 ? off_piece(reinterpret_cast<const uint16_t*>(row)) : 0;
+}
 template <int kPiece, typename T>
 __device__ __forceinline__ typename HeldAs<kPiece>::type load_cols(const T* row, int64_t c, int64_t cols) {
   if constexpr (kPiece == 2)
-    return load8_any(reinterpret_cast<const uint16_t*>(row), c, cols);
+    return load8_raw(reinterpret_cast<const uint16_t*>(row), start_of<kPiece>(row), int(c), int(cols));
   else
     return __ldcs(reinterpret_cast<const typename HeldAs<kPiece>::type*>(row + c));
 }
-template <int kPiece, typename T>
-__device__ __forceinline__ void store_cols(T* row, int64_t c, int64_t cols, typename HeldAs<kPiece>::type v, bool live) {
+template <int kPiece, int kN>
+__device__ __forceinline__ void values_at(const typename HeldAs<kPiece>::type& v, int start, int64_t c, int64_t cols, float (&f)[kN]) {
+  if constexpr (kPiece == 2)
+    values_of(values8(v, start, int(c), int(cols)), f);
+  else
+    values_of(v, f);
+}
+template <int kPiece, typename T, typename U>
+__device__ __forceinline__ void store_cols(T* row, int64_t c, int64_t cols, U v, bool live) {
   if constexpr (kPiece == 2)
     store8_any(reinterpret_cast<uint16_t*>(row), c, cols, v, live);
   else if (live)
-    __stcs(reinterpret_cast<typename HeldAs<kPiece>::type*>(row + c), v);
+    __stcs(reinterpret_cast<U*>(row + c), v);
 }
 
-constexpr int kRowBatch = 8;  // loads that a thread has under way
+template <int kPiece>
+constexpr int kRowBatch = kPiece == 2 ? 4 : 8;  // rows' pieces that a thread has under way
 
 // y[t] = sum_j w[t, j] ys[pos[t, j]] (weights null: 1) over the pairs that have a row, in the order of j, in fp32, the columns
 // of a piece a thread. kB: rows at a time, one to eight; where k <= kB < 8, as many columns more: a thread has eight loads
 // under way (one at a time: 251 us for the two gradients below, eight 171, then). Bounds: HBM (8192 tokens of eight rows of 2048
 // bf16, 47 us, 6.4 TB/s).
 template <typename T, int kPiece, int kB>
-__global__ void __launch_bounds__(kRowThreads, 4)
+__global__ void __launch_bounds__(kRowThreads, kPiece == 2 ? 3 : 4)
 rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int* __restrict__ pos,
                  const float* __restrict__ weights, int k, int64_t tokens, int64_t cols, T* __restrict__ y, int64_t ldy) {
-  constexpr int kN = kColsOf<T, kPiece>, kP = kRowBatch / kB;
+  constexpr int kN = kColsOf<T, kPiece>, kP = kRowBatch<kPiece> / kB;
   using Held = typename HeldAs<kPiece>::type;
   pdl_trigger();
   pdl_wait();
@@ -675,6 +694,7 @@ rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int
     int64_t t[kP], c[kP];
     bool live[kP];
     Held v[kP][kB];
+    int start[kP][kB];
     float w[kP][kB], acc[kN];
     auto load = [&](int p, int j0) {
 #pragma unroll
@@ -682,6 +702,7 @@ rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int
         const int d = live[p] && j0 + j < k ? pos[t[p] * k + j0 + j] : -1;
         const bool in = d >= 0 && d < rows;
         w[p][j] = in ? (weights ? weights[t[p] * k + j0 + j] : 1.0f) : 0.0f;
+        start[p][j] = start_of<kPiece>(ys + (in ? int64_t(d) * ldys : 0));
         v[p][j] = in ? load_cols<kPiece>(ys + int64_t(d) * ldys, c[p], cols) : HeldAs<kPiece>::zero();
       }
     };
@@ -689,7 +710,7 @@ rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int
 #pragma unroll
       for (int j = 0; j < kB; ++j) {
         float f[kN];
-        values_of(v[p][j], f);
+        values_at<kPiece>(v[p][j], start[p][j], c[p], cols, f);
 #pragma unroll
         for (int i = 0; i < kN; ++i) acc[i] = fmaf(w[p][j], f[i], acc[i]);
       }
@@ -723,7 +744,7 @@ rows_back_kernel(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int
 // eight rows of 2048 bf16, 90 us, 6.3 TB/s; 101 at four CTAs an SM, with spills). CTAs that stay, with the pairs held by lanes, took
 // 197 us for both gradients against 171, then.
 template <typename T, int kPiece, int kB>
-__global__ void __launch_bounds__(kRowThreads, kB == 8 ? 3 : 4)
+__global__ void __launch_bounds__(kRowThreads, kB == 8 || kPiece == 2 ? 3 : 4)
 rows_back_grad_kernel(const T* __restrict__ dy, int64_t lddy, const T* ys, int64_t ldys, int64_t rows,
                       const int* __restrict__ pos, const float* __restrict__ weights, int k, int64_t tokens, int64_t cols,
                       T* dys, int64_t lddys, float* __restrict__ dw) {
@@ -760,18 +781,19 @@ rows_back_grad_kernel(const T* __restrict__ dy, int64_t lddy, const T* ys, int64
 #pragma unroll
           for (int p = 0; p < kP; ++p) {
             float h[kN];
-            values_of(g[p], h);
+            const int64_t c = c0 + p * wide;
+            values_at<kPiece>(g[p], start_of<kPiece>(dy + t * lddy), c, cols, h);
 #pragma unroll
             for (int j = 0; j < kB; ++j) {
               if (d[j] < 0) continue;  // (of the token: the whole warp)
               float f[kN], o[kN];
-              values_of(v[p][j], f);
+              values_at<kPiece>(v[p][j], start_of<kPiece>(ys + int64_t(d[j]) * ldys), c, cols, f);
 #pragma unroll
               for (int i = 0; i < kN; ++i) {
                 sum[j] = fmaf(h[i], f[i], sum[j]);
                 o[i] = w[j] * h[i];
               }
-              store_cols<kPiece>(dys + int64_t(d[j]) * lddys, c0 + p * wide, cols, held(o), c0 + p * wide < cols);
+              store_cols<kPiece>(dys + int64_t(d[j]) * lddys, c, cols, held(o), c < cols);
             }
           }
         }
