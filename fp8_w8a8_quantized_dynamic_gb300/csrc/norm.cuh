@@ -279,7 +279,7 @@ __device__ __forceinline__ uint4 codes_of(const Values& v, float s) {
 // in its registers (16384 x 4096: 129 us without, 110 with, then). Sixteen adjacent columns a thread make 32-byte accesses and a
 // block's scale one of eight lanes (95 us in 16-byte accesses, 75 so).
 // Bounds: HBM for the plain form (16384 x 4096 to r and codes, 75 us, 6.2 TB/s); with both norms and a gate the two sums' barriers
-// and the arithmetic beside it (4096 x 8192, 57 us, 5.3 TB/s, 57 percent of the issue slots); a launch and its chain of loads, two
+// and the arithmetic beside it (4096 x 8192, 57 us, 5.3 TB/s, 59 percent of the issue slots); a launch and its chain of loads, two
 // sums and stores for few rows (one of 4096, 2.3 us). Rows that start anywhere pay for their shifts (5615 x 2997, 53 us, 2.8 TB/s).
 template <int kThreads, int kUnits, bool kPost, bool kGate, bool kVec>
 __global__ void __launch_bounds__(kThreads, ctas_of(kThreads, kUnits))
