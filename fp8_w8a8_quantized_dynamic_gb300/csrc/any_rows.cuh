@@ -92,8 +92,8 @@ __device__ __forceinline__ void store_rest(uint16_t* piece, uint4 v, int from, i
 
 // Stores values c .. c + 7 of a row (those before cols): all lanes of the warp come here, `live` ones have some. Where a lane is
 // joined, the lane before it has the eight before its own; where it hands on, the lane after it is joined. A lane stores the
-// whole piece that ends with its own values, with what it takes from the lane before; the ends of a run of lanes are stored by
-// values.
+// whole piece that ends with its own values, with what it takes from the lane before; the ends of a run of lanes are stored in
+// parts.
 __device__ __forceinline__ void store8_run(uint16_t* row, int64_t c, int64_t cols, uint4 v, bool live, bool joined,
                                            bool handed_on) {
   uint4 before;
