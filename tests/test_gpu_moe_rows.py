@@ -245,3 +245,23 @@ def test_there_and_back_in_a_graph_with_a_kept_workspace():
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     total = w.sum(1, keepdim=True)
     assert torch.allclose(want[0].float(), x.float() * total, rtol=2 ** -6, atol=1e-30)
+
+
+@pytest.mark.parametrize("at", [0, 1])
+def test_rows_of_almost_two_to_the_31_columns(at):
+    """The last piece of the widest rows, from column 2**31 - 8 on: what lies behind a row counts in no sum."""
+    H = 2 ** 31 - 5  # three columns of the last eight
+
+    def row(last):
+        wide = torch.full((H + at + 16,), 8.0, dtype=BF16, device=DEV)
+        wide[at:at + H].zero_()
+        wide[at + H - 3:at + H] = torch.tensor(last, dtype=BF16, device=DEV)
+        return wide, wide[None, at:at + H]
+    dy, ys, (wide, out) = row([1.0, 2.0, 3.0])[1], row([1.0, 2.0, 4.0])[1], row([5.0, 5.0, 5.0])
+    pos, w = torch.zeros((1, 1), dtype=torch.int32, device=DEV), torch.full((1, 1), 0.5, device=DEV)
+    F.fp8_moe_combine(ys, pos, w, out=out)
+    assert out[0, -4:].tolist() == [0.0, 0.5, 1.0, 2.0] and (wide[at + H:] == 8.0).all()
+    _, dw = F.fp8_moe_combine_grad(dy, ys, pos, w, out=out)
+    assert dw.item() == 17.0
+    assert out[0, -4:].tolist() == [0.0, 0.5, 1.0, 1.5] and (wide[at + H:] == 8.0).all()
+    assert not out[0, :-3].any()
