@@ -446,8 +446,8 @@ fp8_status fp8_moe_dispatch_grad(const void* dxs, int f32, int64_t R, int64_t H,
  * [L][N, r], without gaps; ids int32 [M], scales fp32 [L] (NULL: ones). Sums and
  * A x are fp32 (for B's product A x is the sum of two bf16 numbers, off by 2^-16);
  * the only rounding to bf16 is that of out. Results do not depend
- * on timing. A NaN or an infinity stays with the tokens of its row or
- * adapter. out may be y (with the same stride), else may not overlap it, nor
+ * on timing. A NaN or an infinity, in B too, gives what the formula gives in
+ * fp32, and stays with the tokens of its row or adapter. out may be y (with the same stride), else may not overlap it, nor
  * anything else that is read. ws: >= fp8_lora_workspace_bytes, 256-byte aligned (fewer tokens may need more, since K is split
  * further for them: one kept for several M has the largest of theirs). Limits: r 1 to 256, L <= 511, K
  * and N <= 2^30 (FP8_ERR_INVALID_ARG).

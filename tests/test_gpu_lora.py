@@ -252,3 +252,45 @@ def test_offsets_past_32_bits():
         ref, err = L.lora(f32(one["y"]), f32(one["x"]), f32(one["a"]), f32(one["b"]), np.zeros(1, np.int32))
         tol = L.rounded_bf16(ref, err)
         assert np.all(np.abs(f32(out[-1:]) - ref) <= tol) and np.all(np.abs(f32(out[:1]) - ref) <= tol)
+
+
+def formula(d):
+    """The result in float64 by elementwise products, which keep infinities and NaN where the formula has them."""
+    y, x, a, b = (f32(d[k]).astype(np.float64) for k in ("y", "x", "a", "b"))
+    out = y.copy()
+    with np.errstate(all="ignore"):
+        for m, e in enumerate(d["ids"].tolist()):
+            if 0 <= e < a.shape[0]:
+                v = (a[e] * x[m]).sum(1)
+                out[m] += float(d["scales"][e]) * (b[e] * v).sum(1)
+    return out
+
+
+@pytest.mark.parametrize("M,K", [(8, 128), (560, 128), (1100, 128), (600, 2056)])
+@pytest.mark.parametrize("r", [12, 16, 76, 130, 256])
+def test_values_of_b_that_are_not_finite(M, K, r):
+    """An infinity in B gives an infinity of its product's sign, in every form, and only in its column of its adapter."""
+    inf = float("inf")
+    d = operands(M, K, 144, r, 4, 5, torch.arange(M, dtype=torch.int32) % 5 - 1)
+    clean = run(d).cpu()
+    d["b"][2, 5, 3] = inf
+    d["b"][2, 6, 1] = -inf
+    d["b"][1, 7, 0] = float("nan")
+    d["b"][3, 143, :2] = inf       # two that may cancel
+    d["a"][0, 2, 2] = inf          # A x is infinite, and so is what it meets
+    d["b"][0, 9, 2] = -inf
+    out, want = run(d).cpu().double().numpy(), formula(d)
+    odd = ~np.isfinite(want)
+    assert odd[d["ids"].numpy() == 0].all() and odd.sum() > M // 5 * 4
+    assert np.array_equal(np.isnan(out), np.isnan(want))
+    assert np.array_equal(out[odd & ~np.isnan(want)], want[odd & ~np.isnan(want)])
+    assert np.array_equal(out[~odd], clean.double().numpy()[~odd])
+
+
+@pytest.mark.parametrize("M", [3, 600])
+def test_a_x_past_the_range_of_bf16(M):
+    """A x = 2**127 * (2 - 2**-8): a finite fp32 number that rounds to an infinite bf16 one."""
+    d = {"y": torch.zeros((M, 8), dtype=BF16), "x": torch.tensor([[2.0 ** 127, 2.0 ** 119]], dtype=BF16).repeat(M, 1),
+         "a": torch.tensor([[[2 - 2.0 ** -7, 1.0]]], dtype=BF16), "b": torch.full((1, 8, 1), 2.0 ** -100, dtype=BF16),
+         "ids": torch.zeros(M, dtype=torch.int32), "scales": torch.ones(1)}
+    assert (run(d) == 2.0 ** 28).all()  # 2**27 * (2 - 2**-8), a tie, to even
