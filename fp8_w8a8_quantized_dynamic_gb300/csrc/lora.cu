@@ -5,8 +5,8 @@
 // Two forms. Few tokens (tokens_kernel): a cluster of CTAs a token, one launch; the adapter's
 // matrices are read once a token, by wide loads. Many tokens (shrink_kernel, expand_kernel): rows are
 // sorted by adapter and tiles of up to 128 of them pass the tensor cores, first v = A x over all of K, then
-// y + s B v, whose time is the stream of y. v is fp32 between the two; the tensor core takes it as the sum of two bf16
-// numbers (16 bits of its fraction), against B's exact bf16 values.
+// y + s B v, whose time is the stream of y. v is fp32 between the two; the tensor core takes it as the sum of three bf16
+// numbers of eight bits each, all that v has, against B's exact bf16 values.
 //
 // MMAs are issued by one lane of a warp that stays together (elect.sync), never by a lane that runs a loop of its own: that
 // form, with the MMAs of a step in straight code, ended in an illegal instruction.
@@ -284,6 +284,15 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       :: "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
 
+// The same with A in tensor memory: row i in lane i, two values of K a column.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
 // D fp32, A and B bf16, both K-major, M = 128.
 __host__ __device__ constexpr uint32_t idesc_of(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(kTileRows >> 4) << 24);
@@ -379,6 +388,12 @@ struct TileParams {
   int vec, vec_b;           // rows of x and A, of B, on 16-byte boundaries
   uint32_t tmem_cols;
 };
+
+// v between the two kernels: four values at a time of each row, [split][rank / 4][row], so that 32 lanes with a row each pass whole
+// lines (with a row's values side by side the second product's kernel took 11 us more for 8192 x 14336 at rank 64).
+__device__ __forceinline__ float4* four_of_v(const TileParams& p, int split, int four, int64_t row) {
+  return reinterpret_cast<float4*>(p.s.v) + (int64_t(split) * (p.rp / 4) + four) * p.a.M + row;
+}
 
 constexpr int kCopyThreads = 256;  // expand: those that copy y and out
 constexpr int kCopyRows = kTileRows / (kCopyThreads / 32);  // of a warp
@@ -574,7 +589,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
         tmem_fence_after();
         // four warps hold the tile's rows, the other four the second half of the columns
         const int row = (warp & 3) * 32 + lane;
-        float* dst = p.s.v + (int64_t(blockIdx.y) * g.M + t.row0 + row) * p.rp;
+        float4* dst = four_of_v(p, blockIdx.y, 0, t.row0 + row);
         const uint32_t from = ctl.tmem_base + (uint32_t((warp & 3) * 32) << 16);
         for (int c = (warp >> 2) * 32; warp < kTileThreads / 32 && c < p.rp; c += 64) {
           uint32_t f[32];
@@ -584,7 +599,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               if (c + 4 * q < p.rp)
-                *reinterpret_cast<uint4*>(dst + c + 4 * q) = make_uint4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+                *reinterpret_cast<uint4*>(dst + (c / 4 + q) * g.M) = make_uint4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
           }
         }
       } else if (threadIdx.x == 0) {  // nothing of a load may land after the CTA has left
@@ -596,27 +611,25 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
   tile_end(&ctl, p.tmem_cols);
 }
 
-// v of a tile's rows, the sum of the splits in order, as two bf16 numbers in two swizzled tiles, by the block's first
-// `threads` threads.
-__device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile& t, int rows, uint32_t v_hi, uint32_t v_lo,
-                                      int threads) {
-  const Args& g = p.a;
-  const int pieces = p.rp / 8;
-  const float inv_pieces = 1.0f / float(pieces);
-  for (int i = threadIdx.x; i < kTileRows * pieces; i += threads) {
-    const int row = quotient(i, inv_pieces), c = i - row * pieces;
+// v of a tile's rows, the sum of the splits in order, as the sum of three bf16 numbers: eight bits each, so that nothing of v's 24
+// is lost (above 2^-133, the smallest bf16 number). The first two go to swizzled tiles of shared memory, the third to tensor memory
+// (as the operand of the same MMAs: three tiles of rank 256 leave no room for B and y, and at rank 64 one would cost a slot of y).
+// A thread has a row; `groups` of four warps share out the pieces of eight values.
+__device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile& t, int rows, uint32_t v_hi, uint32_t v_mid,
+                                      uint32_t v_lo_tmem, int groups) {
+  const int64_t M = p.a.M;
+  const int row = int(threadIdx.x) & (kTileRows - 1);
+  for (int c = int(threadIdx.x) / kTileRows; c < p.rp / 8; c += groups) {
     float f[8] = {};
     if (row < rows) {
-      const float* from = p.s.v + int64_t(t.row0 + row) * p.rp + c * 8;
-      const int64_t step = g.M * p.rp;
       for (int s0 = 0; s0 < p.s.splits; s0 += 4) {  // four splits' loads at once, added in order
         float4 in[4][2];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const float4* at = reinterpret_cast<const float4*>(from + (s0 + s) * step);
+          const float4* at = four_of_v(p, s0 + s, 2 * c, t.row0 + row);
           const bool have = s0 + s < p.s.splits;
           in[s][0] = have ? at[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-          in[s][1] = have ? at[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+          in[s][1] = have ? at[M] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -625,18 +638,28 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
         }
       }
     }
-    uint32_t h[4], l[4];
+    // the next eight bits of each, and what they leave (an infinity leaves nothing; what the formula has of it is seen to where the
+    // sums are read, as in sums_again)
+    auto next8 = [&](uint32_t (&w)[4]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      h[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-      const float h0 = bf16_lo(h[j]), h1 = bf16_hi(h[j]);
-      // (an infinity has no second part; what the formula has of it is seen to where the sums are read, as in sums_again)
-      l[j] = pack_bf16x2(fabsf(h0) <= 3.39e38f ? f[2 * j] - h0 : 0.0f, fabsf(h1) <= 3.39e38f ? f[2 * j + 1] - h1 : 0.0f);
-    }
+      for (int j = 0; j < 4; ++j) {
+        w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
+        const float a = bf16_lo(w[j]), b = bf16_hi(w[j]);
+        f[2 * j] = fabsf(a) <= FLT_MAX ? f[2 * j] - a : 0.0f;
+        f[2 * j + 1] = fabsf(b) <= FLT_MAX ? f[2 * j + 1] - b : 0.0f;
+      }
+    };
+    uint32_t w[4];
     const uint32_t at = uint32_t(c >> 3) * kXBytes + swizzled(row, c & 7);
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v_hi + at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(v_lo + at), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3]) : "memory");
+    next8(w);
+    sts128(v_hi + at, make_uint4(w[0], w[1], w[2], w[3]));
+    next8(w);
+    sts128(v_mid + at, make_uint4(w[0], w[1], w[2], w[3]));
+    next8(w);
+    __syncwarp();
+    tmem_st4(v_lo_tmem + (uint32_t(row & ~31) << 16) + uint32_t(c) * 4u, w);
   }
+  tmem_wait_st();
 }
 
 // Whether any of a thread's sums is not finite.
@@ -650,10 +673,9 @@ __device__ __forceinline__ bool any_not_finite(const uint32_t (&f)[32]) {
 
 // The parts of v lose what the formula has where a number is not finite: an infinity of B times a part that is 0 or of the other
 // sign, or a v that rounds to an infinite bf16 number. Such sums of a warp's rows and columns are taken once more, from v and B
-// themselves in fp32, and put in their places in tensor memory. `v`: this lane's row, `b`: that of the first column.
-__device__ __forceinline__ void sums_again(const TileParams& p, uint32_t taddr, const float* v, const uint16_t* b, int columns,
+// themselves in fp32, and put in their places in tensor memory. `row`: this lane's row of v, `b`: the first column's of B.
+__device__ __forceinline__ void sums_again(const TileParams& p, uint32_t taddr, int64_t row, const uint16_t* b, int columns,
                                            bool live) {
-  const int64_t split = p.a.M * p.rp;
 #pragma unroll 1
   for (int i = 0; i < columns; ++i, b += p.a.rank) {
     float sum = __uint_as_float(tmem_ld1(taddr + i));
@@ -663,7 +685,7 @@ __device__ __forceinline__ void sums_again(const TileParams& p, uint32_t taddr, 
       for (int j = 0; j < p.a.rank && sum == sum; ++j) {
         float vj = 0.0f;
 #pragma unroll 1
-        for (int s = 0; s < p.s.splits; ++s) vj += v[s * split + j];
+        for (int s = 0; s < p.s.splits; ++s) vj += reinterpret_cast<const float*>(four_of_v(p, s, j >> 2, row))[j & 3];
         sum = fmaf(bf16_bits_to_float(b[j]), vj, sum);
       }
     }
@@ -710,7 +732,8 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
   const int64_t total = int64_t(*p.s.n_tiles) * steps, run = (total + gridDim.x - 1) / gridDim.x;
   const int64_t begin = run * blockIdx.x, end = min(total, run * (blockIdx.x + 1));
   const int rk = (p.rp + kBk - 1) / kBk;  // 128-byte rows that the rank fills
-  const uint32_t v_hi = base, v_lo = base + uint32_t(rk) * kXBytes, b_at = v_lo + uint32_t(rk) * kXBytes;
+  const uint32_t v_hi = base, v_mid = base + uint32_t(rk) * kXBytes, b_at = v_mid + uint32_t(rk) * kXBytes;
+  const uint32_t v_lo_tmem = ctl.tmem_base + 2 * kBn;  // behind two steps' sums
   const uint32_t b_bytes = uint32_t(rk) * (kBn * 128u);
   const uint32_t slots_at = b_at + uint32_t(p.b_bufs) * b_bytes;
   auto wait = [&](uint64_t* bar, uint32_t it) {  // the it-th step's phase of a pair of barriers
@@ -865,7 +888,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
     Place slot, filled, used;  // of all steps that pass the slots; of B, filled and multiplied
     // descriptors of v and of B; K steps of 16 and tiles of 64 lie at fixed distances (in 16-byte units)
     const uint64_t v_desc = make_sdesc(v_hi), b_desc = make_sdesc(b_at);
-    const uint32_t lo_part = uint32_t(rk) * (kXBytes >> 4);
+    const uint32_t mid_part = uint32_t(rk) * (kXBytes >> 4);
     bool ok = true;
     for (int64_t u = begin; u < end;) {
       const int tile = int(u / steps), s0 = int(u - int64_t(tile) * steps), s1 = int(min(int64_t(steps), s0 + (end - u)));
@@ -897,8 +920,9 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         for (int i = 0; ok && i < p.b_bufs - 1 && s0 + i < s1; ++i) fill(s0 + i);
       } else {
         // all of the last tile's MMAs are done: each warp waited for its last step
-        put_v(p, t, rows, v_hi, v_lo, kJoin);
+        put_v(p, t, rows, v_hi, v_mid, v_lo_tmem, kJoin / kTileRows);
         fence_async();
+        tmem_fence_before();
       }
       if (!barrier_all(1, kJoin + 32, ok)) {
         ok = false;
@@ -920,7 +944,8 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
                 const uint64_t a = v_desc + uint32_t((i >> 2) * (kXBytes >> 4) + (i & 3) * 2);
                 const uint64_t bi = b + uint32_t((i >> 2) * (kBn * 128 >> 4) + (i & 3) * 2);
                 mma_bf16(d, a, bi, idesc_of(kBn), i != 0);
-                mma_bf16(d, a + lo_part, bi, idesc_of(kBn), 1);
+                mma_bf16(d, a + mid_part, bi, idesc_of(kBn), 1);
+                mma_bf16_ta(d, v_lo_tmem + uint32_t(i) * 8u, bi, idesc_of(kBn), 1);
               }
             }
             mma_commit<false>(smem_u32(&ctl.done[it & 1u]));
@@ -949,8 +974,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         tmem_ld32(sums, f);
         if (__any_sync(0xffffffffu, row < rows && any_not_finite(f))) {
           const int n = s * kBn + group * 32;
-          sums_again(p, sums, p.s.v + int64_t(t.row0 + row) * p.rp, g.b + (int64_t(t.expert) * N + n) * g.rank, min(32, N - n),
-                     row < rows);
+          sums_again(p, sums, t.row0 + row, g.b + (int64_t(t.expert) * N + n) * g.rank, min(32, N - n), row < rows);
           tmem_ld32(sums, f);
         }
         tmem_fence_before();
@@ -1023,7 +1047,8 @@ bool launch_expand_of(TileParams p, const CUtensorMap& map_b, int num_sms, cudaS
   p.b_bufs = room >= 4 * (buf + slot) ? 4 : 3;
   p.slots = int(std::min<size_t>(4, (room - p.b_bufs * buf) / slot));
   const int64_t units = p.s.max_tiles * ((p.a.N + kBn - 1) / kBn);
-  p.tmem_cols = 2 * kBn;
+  p.tmem_cols = 32;
+  while (int(p.tmem_cols) < 2 * kBn + p.rp / 2) p.tmem_cols *= 2;  // two steps' sums and v's last bits
   return launch(expand_kernel<kBn, kPiece, kTma>, dim3(unsigned(std::min<int64_t>(units, num_sms))), dim3(expand_threads(kBn, kTma)),
                 1024 + v + size_t(p.b_bufs) * buf + size_t(p.slots) * slot, st, true, dim3(1, 1, 1), map_b, p) == FP8_OK;
 }

@@ -32,7 +32,7 @@ struct Args {
 bool launch_tokens(const Args& p, int num_sms, cudaStream_t st);
 
 // Rows sorted by adapter, on tensor cores: tiles (and how many) and the token of each sorted row, in
-// device memory; `adapters` itself stands for no adapter there. v: fp32 [splits][M][rank rounded up to 16].
+// device memory; `adapters` itself stands for no adapter there. v: fp32 [splits][rank rounded up to 16, / 4][M][4].
 struct Sorted {
   const block::RowTile* tiles;
   const int* n_tiles;

@@ -102,8 +102,9 @@ def combine_grad(dy: np.ndarray, ys: np.ndarray, pos: np.ndarray, weights: np.nd
 
 
 def lora(y, x, a, b, ids, scales=None) -> Tuple[np.ndarray, np.ndarray]:
-    """(out, bound) before the rounding to bf16. Sums of K and of 2 r products in fp32 in any order, 2**-23 a step (a
-    tensor core may cut instead of round); v as two bf16 numbers is off by 2**-8 of what 2**-8 of it left; one fma."""
+    """(out, bound) before the rounding to bf16. Sums of K and of 3 r products in fp32 in any order, 2**-23 a step (a
+    tensor core may cut instead of round): v passes it as the sum of three bf16 numbers of eight bits each, which are all
+    24 of it (what is below 2**-133, the smallest bf16 number, is part of TINY); one fma."""
     M, K = x.shape
     L, r, _ = a.shape
     out = y.astype(np.float64)
@@ -117,7 +118,7 @@ def lora(y, x, a, b, ids, scales=None) -> Tuple[np.ndarray, np.ndarray]:
         v = X @ A.T
         dv = (K + 16) * 2 * U * (np.abs(X) @ np.abs(A).T) + TINY
         d = v @ Bm.T
-        dd = (dv + np.abs(v) * HALF_BF16 ** 2) @ np.abs(Bm).T + (2 * r + 8) * 2 * U * ((np.abs(v) + dv) @ np.abs(Bm).T)
+        dd = dv @ np.abs(Bm).T + (3 * r + 8) * 2 * U * ((np.abs(v) + dv) @ np.abs(Bm).T)
         out[t] += s * d
         err[t] = abs(s) * dd
         err[t] += (np.abs(out[t]) + err[t]) * U + TINY

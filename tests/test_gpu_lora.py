@@ -294,3 +294,18 @@ def test_a_x_past_the_range_of_bf16(M):
          "a": torch.tensor([[[2 - 2.0 ** -7, 1.0]]], dtype=BF16), "b": torch.full((1, 8, 1), 2.0 ** -100, dtype=BF16),
          "ids": torch.zeros(M, dtype=torch.int32), "scales": torch.ones(1)}
     assert (run(d) == 2.0 ** 28).all()  # 2**27 * (2 - 2**-8), a tie, to even
+
+
+@pytest.mark.parametrize("M", [3, 600])
+@pytest.mark.parametrize("r", [2, 12, 16, 64, 76, 192, 250, 256])
+def test_all_bits_of_a_x_count(M, r):
+    """Pairs of A x that differ in their last bits and cancel in B's product: 1 + 2**-9 + 2**-18 less 1 + 2**-9, and the same
+    one bit further down, at both ends of the rank. All sums are exact in fp32, so the result is."""
+    d = {"y": torch.zeros((M, 40), dtype=BF16), "x": torch.zeros((M, 24), dtype=BF16), "a": torch.zeros((1, r, 24), dtype=BF16),
+         "b": torch.zeros((1, 40, r), dtype=BF16), "ids": torch.zeros(M, dtype=torch.int32), "scales": torch.ones(1)}
+    for at, bit in ((0, 18), (r - 2, 19)):
+        d["b"].zero_(), d["a"].zero_()
+        d["x"][:, :3] = torch.tensor([1.0, 2.0 ** -9, 2.0 ** -bit], dtype=BF16)
+        d["a"][0, at, :3], d["a"][0, at + 1, :2] = 1.0, 1.0
+        d["b"][0, :, at], d["b"][0, :, at + 1] = 1.0, -1.0
+        assert (run(d) == 2.0 ** -bit).all()
