@@ -856,8 +856,8 @@ def fp8_residual_norm(y, weight=None, residual=None, post_weight=None, gate=None
     """The end of a block and the norm before the next: (n, r) bf16 [M, H] of y bf16 [M, H], with
     t = y (with post_weight: y / sqrt(mean y^2 + eps) * post_weight), r = residual + scale * gate * t and
     n = r / sqrt(mean r^2 + eps) * weight, in fp32 with one rounding of r and of n. Weights bf16 [H] (plus_one: they
-    stand for 1 + weight), gate bf16 [H] or [M, H]. Without a weight n is None; where nothing changes y, r is y.
-    residual_out may be y or residual itself."""
+    stand for 1 + weight), gate bf16 [H] or [M, H]. Without a weight n is None; where nothing changes y, r is y, or None if
+    n took y's place (out is y). residual_out may be y or residual itself."""
     torch = _torch_module or _torch()
     M, H, ldy, index, ldg, ldr, r, ldro = _norm_operands(torch, y, weight, residual, post_weight, gate, scale,
                                                          residual_out)
@@ -873,7 +873,9 @@ def fp8_residual_norm(y, weight=None, residual=None, post_weight=None, gate=None
         1 if plus_one else 0, _ptr(r), ldro, _ptr(n), 0 if n is None else _row_stride(n, M, H), _stream_ptr(y))
     if status:
         raise FP8Error(status, "fp8_residual_norm")
-    return n, y if r is None else r
+    if r is None and (out is None or out.data_ptr() != y.data_ptr() or not M * H):
+        r = y
+    return n, r
 
 
 def fp8_residual_norm_quantize(y, weight, residual=None, post_weight=None, gate=None, scale: float = 1.0,

@@ -266,3 +266,12 @@ def test_graph_replay_and_side_stream():
     graph.replay()
     want = F.fp8_residual_norm_quantize(fresh["y"], fresh["weight"], residual=fresh["residual"], gate=fresh["gate"])
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_norm_over_its_input_has_no_residual_to_give():
+    d = operands(9, 300, 13, residual=False)
+    y, w = d["y"].to(DEV), d["weight"].to(DEV)
+    want, same = F.fp8_residual_norm(y, w)
+    assert same is y
+    n, r = F.fp8_residual_norm(y, w, out=y)
+    assert n is y and r is None and torch.equal(n, want)

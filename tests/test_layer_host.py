@@ -200,6 +200,16 @@ def test_a_gate_a_channel_has_no_row_stride(rec):
     assert rec.calls["fp8_residual_norm"][6] == 256
 
 
+def test_no_residual_where_the_norm_took_its_place(rec):
+    y, w = Fake(zeros(4, 256)), vec(256)
+    other = Fake(zeros(4, 256))
+    assert F.fp8_residual_norm(y, w, out=y)[1] is None
+    assert F.fp8_residual_norm(y, w, out=other) == (other, y)
+    assert F.fp8_residual_norm(y, w, residual=Fake(zeros(4, 256)), out=y, residual_out=other)[1] is other
+    for empty in (Fake(zeros(0, 256)), Fake(zeros(4, 0))):
+        assert F.fp8_residual_norm(empty, vec(empty.shape[1]))[1] is empty
+
+
 def bad_calls():
     y, w = Fake(zeros(4, 256)), vec(256)
     yl, xl, a, b, ids, sc = lora_operands()
