@@ -168,7 +168,7 @@ FP8_API fp8_status fp8_residual_norm(const void* y_bf16, int64_t M, int64_t H, i
   if (crosses(n_bf16, ldn, y_bf16, ldy, M) || crosses(n_bf16, ldn, residual_bf16, ldr, M)) return FP8_ERR_INVALID_ARG;
   if (M == 0 || H == 0) return FP8_OK;
   if ((w_bf16 == nullptr) != (n_bf16 == nullptr)) return FP8_ERR_INVALID_ARG;
-  if (n_bf16 == nullptr && r_bf16 == nullptr) return FP8_ERR_INVALID_ARG;
+  if (n_bf16 == r_bf16) return FP8_ERR_INVALID_ARG;  // nothing to write, or one over the other
   p.pre = n_bf16 != nullptr;
   p.n = static_cast<uint16_t*>(n_bf16);
   p.ldn = ldn;

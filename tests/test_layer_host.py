@@ -66,6 +66,12 @@ def test_norm_over_its_input_with_another_stride(out, ld, over):
         assert status("fp8_residual_norm_quantize", quant, ldro=264) == F.FP8_ERR_INVALID_ARG
 
 
+def test_norm_with_both_outputs_in_one_place():
+    apart = {**NORM, "y": Q, "residual": Q, "gate": Q, "post": Q, "w": Q}
+    assert status("fp8_residual_norm", apart) == F.FP8_ERR_INVALID_ARG  # r and n are the same rows
+    assert status("fp8_residual_norm", apart, M=0) == F.FP8_OK
+
+
 @pytest.mark.parametrize("name", ["y", "post", "gate", "residual", "w", "r"])
 def test_norm_misaligned(name):
     assert status("fp8_residual_norm", NORM, **{name: P + 1}) == F.FP8_ERR_MISALIGNED
