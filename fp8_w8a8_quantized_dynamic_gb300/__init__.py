@@ -781,7 +781,7 @@ def fp8_moe_combine(ys, pos, weights=None, out=None):
 def fp8_moe_combine_grad(dy, ys, pos, weights, out=None):
     """The gradient of fp8_moe_combine: (dys [R, H] with dys[pos[t, j]] = weights[t, j] dy[t], dw fp32 [T, k] with
     <dy[t], ys[pos[t, j]]>). No two pairs may have the same row (those of fp8_moe_dispatch do not). Rows of dys that no
-    pair has are not written; out may be ys."""
+    pair has are zeros; in a given out, which may be ys, they are not written."""
     torch = _torch_module or _torch()
     f32, T, H, lddy = _check_rows_in(dy, "dy")
     index = dy.get_device()
@@ -790,7 +790,8 @@ def fp8_moe_combine_grad(dy, ys, pos, weights, out=None):
     if weights is None or _check_pairs(pos, weights, index)[0] != T:
         raise ValueError("expected pos [T, k] and weights [T, k] for dy [T, H]")
     k = pos.shape[1]
-    dys, lddys = _rows_out(out, R, H, ys)
+    # (the kernel passes rows with a pair only)
+    dys, lddys = _rows_out(torch.zeros((R, H), dtype=ys.dtype, device=ys.device) if out is None else out, R, H, ys)
     dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
     status = (_lib or lib()).fp8_moe_combine_grad(dy.data_ptr(), f32, T, H, lddy, ys.data_ptr(), R, ldys,
                                                   pos.data_ptr(), weights.data_ptr(), k, dys.data_ptr(), lddys,

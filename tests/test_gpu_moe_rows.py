@@ -265,3 +265,17 @@ def test_rows_of_almost_two_to_the_31_columns(at):
     assert dw.item() == 17.0
     assert out[0, -4:].tolist() == [0.0, 0.5, 1.0, 1.5] and (wide[at + H:] == 8.0).all()
     assert not out[0, :-3].any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_gradient_of_rows_without_a_pair_is_zero(dtype):
+    """Into a buffer of the call's own, whatever the allocator's memory held before."""
+    T, k, E, H = 50, 4, 8, 333
+    ids, w = routing(T, k, E, 17, 0.4)
+    pos = torch.from_numpy(L.sort_rows(ids.numpy(), E)[0])
+    ys, dy = rows(T * k, H, 18, dtype).to(DEV), rows(T, H, 19, dtype).to(DEV)
+    want, _ = F.fp8_moe_combine_grad(dy, ys, pos.to(DEV), w.to(DEV), out=torch.zeros_like(ys))
+    old = [torch.full_like(ys, float("nan")) for _ in range(4)]
+    del old
+    dys, _ = F.fp8_moe_combine_grad(dy, ys, pos.to(DEV), w.to(DEV))
+    assert (pos < 0).any() and torch.equal(dys, want)
