@@ -790,8 +790,10 @@ def fp8_moe_combine_grad(dy, ys, pos, weights, out=None):
     if weights is None or _check_pairs(pos, weights, index)[0] != T:
         raise ValueError("expected pos [T, k] and weights [T, k] for dy [T, H]")
     k = pos.shape[1]
-    # (the kernel passes rows with a pair only)
-    dys, lddys = _rows_out(torch.zeros((R, H), dtype=ys.dtype, device=ys.device) if out is None else out, R, H, ys)
+    if out is None:  # (the kernel passes rows with a pair only)
+        dys, lddys = torch.zeros((R, H), dtype=ys.dtype, device=ys.device), H or 1
+    else:
+        dys, lddys = _rows_out(out, R, H, ys)
     dw = torch.empty((T, k), dtype=torch.float32, device=dy.device)
     status = (_lib or lib()).fp8_moe_combine_grad(dy.data_ptr(), f32, T, H, lddy, ys.data_ptr(), R, ldys,
                                                   pos.data_ptr(), weights.data_ptr(), k, dys.data_ptr(), lddys,
