@@ -643,6 +643,7 @@ FP8_API fp8_status fp8_moe_dispatch(const void* x, int f32, int64_t T, int64_t H
   if (!aligned(ids, 4) || !aligned(pos, 4) || !aligned(offsets, 4)) return FP8_ERR_MISALIGNED;
   if (offsets == nullptr || (T > 0 && (ids == nullptr || pos == nullptr))) return FP8_ERR_INVALID_ARG;
   FP8_TRY(check_ws(ws, ws_bytes, fp8_moe_dispatch_workspace_bytes(T, k, E)));
+  if (T > 0 && H > 0 && xs == x) return FP8_ERR_INVALID_ARG;  // rows that other tokens' have still to be read from
   int sms = 0;
   FP8_TRY(current_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -674,7 +675,7 @@ FP8_API fp8_status fp8_moe_combine(const void* ys, int f32, int64_t R, int64_t H
   FP8_TRY(check_rows(y, f32, T, H, ldy));
   if (!aligned(pos, 4) || !aligned(weights, 4)) return FP8_ERR_MISALIGNED;
   if (T == 0 || H == 0) return FP8_OK;
-  if (pos == nullptr) return FP8_ERR_INVALID_ARG;
+  if (pos == nullptr || y == ys) return FP8_ERR_INVALID_ARG;
   int sms = 0;
   FP8_TRY(current_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -711,6 +712,7 @@ FP8_API fp8_status fp8_moe_combine_grad(const void* dy, int f32, int64_t T, int6
   if (!aligned(pos, 4) || !aligned(weights, 4) || !aligned(dw, 4)) return FP8_ERR_MISALIGNED;
   if (T == 0) return FP8_OK;
   if (pos == nullptr || weights == nullptr || dw == nullptr) return FP8_ERR_INVALID_ARG;
+  if (R > 0 && H > 0 && dys == dy) return FP8_ERR_INVALID_ARG;  // rows of dy that other pairs have still to be read from
   int sms = 0;
   FP8_TRY(current_device(&sms));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

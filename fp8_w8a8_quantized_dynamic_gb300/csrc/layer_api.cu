@@ -219,6 +219,7 @@ FP8_API fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_
   if (M == 0 || N == 0) return FP8_OK;
   if (crosses(out_bf16, ldo, y_bf16, ldy, M)) return FP8_ERR_INVALID_ARG;
   const bool none = K == 0 || L == 0;
+  if (!none && out_bf16 == x_bf16) return FP8_ERR_INVALID_ARG;
   if (!none && (a_bf16 == nullptr || b_bf16 == nullptr || ids == nullptr)) return FP8_ERR_INVALID_ARG;
   FP8_TRY(check_ws(ws, ws_bytes, fp8_lora_workspace_bytes(M, K, N, L, r)));
   int sms = 0;

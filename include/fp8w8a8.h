@@ -427,7 +427,7 @@ fp8_status fp8_moe_combine(const void* ys, int f32, int64_t R, int64_t H, int64_
 
 /* The gradient of fp8_moe_combine: dys[pos[t, j]] = weights[t, j] dy[t] (rows of no pair are left as they were) and
  * dw[t, j] = <dy[t], ys[pos[t, j]]>, fp32 [T, k], 0 for a pair without a row. No two pairs may have the same row (those
- * of fp8_moe_dispatch do not). dys may be ys, with the same stride. */
+ * of fp8_moe_dispatch do not). dys may be ys, with the same stride, and may overlap nothing else. */
 fp8_status fp8_moe_combine_grad(const void* dy, int f32, int64_t T, int64_t H, int64_t lddy, const void* ys, int64_t R,
                                 int64_t ldys, const int32_t* pos, const float* weights, int64_t k, void* dys,
                                 int64_t lddys, float* dw, fp8_stream_t stream);

@@ -167,6 +167,19 @@ def test_more_refusals_on_the_way_back():
     assert status("fp8_moe_dispatch_grad", d, T=0) == F.FP8_OK
 
 
+def test_outputs_over_rows_that_others_still_read():
+    bad = F.FP8_ERR_INVALID_ARG
+    assert status("fp8_moe_dispatch", DISPATCH) == bad                               # xs over x
+    assert status("fp8_moe_combine", COMBINE) == bad                                 # y over ys
+    assert status("fp8_moe_combine_grad", GRAD, ys=Q) == bad                         # dys over dy
+    assert status("fp8_lora_add", LORA, out=LORA["x"], y=Q) == bad                   # out over x
+    grad = dict(dxs=P, f32=0, R=32, H=64, lddxs=64, pos=Q, T=4, k=8, dx=P, lddx=64, stream=None)
+    assert status("fp8_moe_dispatch_grad", grad) == bad                              # dx over dxs
+    for name, base in (("fp8_moe_dispatch", DISPATCH), ("fp8_moe_combine", COMBINE), ("fp8_moe_combine_grad", GRAD)):
+        wide = {k: 128 if k.startswith("ld") else v for k, v in base.items()}
+        assert status(name, wide) == bad
+
+
 # ---------------------------------------------------------------------------
 # wrappers
 # ---------------------------------------------------------------------------
