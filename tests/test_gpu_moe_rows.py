@@ -279,3 +279,35 @@ def test_gradient_of_rows_without_a_pair_is_zero(dtype):
     del old
     dys, _ = F.fp8_moe_combine_grad(dy, ys, pos.to(DEV), w.to(DEV))
     assert (pos < 0).any() and torch.equal(dys, want)
+
+
+# pairs that a cluster sorts, and that many CTAs sort after counting; rows off 16-byte boundaries
+@pytest.mark.parametrize("T,k,E", [(300, 4, 9), (1037, 2, 64), (2101, 4, 16)])
+@pytest.mark.parametrize("H", [1, 2, 7, 9, 31, 1001, 2047])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("drop", [0.0, 0.3])
+def test_dispatch_of_many_pairs_and_odd_widths(T, k, E, H, dtype, drop):
+    check_dispatch(T, k, E, H, dtype, drop)
+
+
+@pytest.mark.parametrize("T,k", [(600, 3), (2101, 4)])
+@pytest.mark.parametrize("H", [63, 72])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("shift,out_shift,pad", [(1, 0, 0), (0, 1, 3), (3, 6, 2), (5, 7, 1), (8, 2, 6)])
+def test_dispatch_of_many_pairs_with_strides(T, k, H, dtype, shift, out_shift, pad):
+    """x and out start anywhere and lie in wider rows, whose other columns stay as they were."""
+    ids, _ = routing(T, k, 16, 20, 0.3)
+    x = rows(T, H, 21, dtype)
+    sevens = torch.full((T * k, H), 7.0, dtype=dtype, device=DEV)
+    want, pos, offsets = F.fp8_moe_dispatch(x.to(DEV), ids.to(DEV), 16, out=sevens)
+    pos_ref, _ = L.sort_rows(ids.numpy(), 16)
+    kept = torch.from_numpy(np.argwhere(pos_ref >= 0))
+    at = torch.from_numpy(pos_ref[pos_ref >= 0]).long()
+    assert torch.equal(want.cpu()[at], x[kept[:, 0]]) and (want[int(offsets[-1]):] == 7.0).all()
+    wide_x = torch.full((T, H + shift + pad), 5.0, dtype=dtype, device=DEV)
+    wide_x[:, shift:shift + H] = x.to(DEV)
+    wide = torch.full((T * k, H + out_shift + pad), 7.0, dtype=dtype, device=DEV)
+    out = wide[:, out_shift:out_shift + H]
+    got, pos2, offsets2 = F.fp8_moe_dispatch(wide_x[:, shift:shift + H], ids.to(DEV), 16, out=out)
+    assert got is out and torch.equal(got, want) and torch.equal(pos, pos2) and torch.equal(offsets, offsets2)
+    assert (wide[:, :out_shift] == 7.0).all() and (wide[:, out_shift + H:] == 7.0).all()
