@@ -275,3 +275,41 @@ def test_norm_over_its_input_has_no_residual_to_give():
     assert same is y
     n, r = F.fp8_residual_norm(y, w, out=y)
     assert n is y and r is None and torch.equal(n, want)
+
+
+@pytest.mark.parametrize("H", [2049, 2997, 4097, 7026, 8193, 12001, 16385, 32767])
+@pytest.mark.parametrize("post,gate", [(False, None), (False, "token"), (True, None), (True, "channel"), (True, "token")])
+def test_wide_rows_of_any_alignment(H, post, gate):
+    check(operands(7, H, H, post, gate), scale=0.22)
+
+
+# a row's threads from 32 to 1024, and two units of each; several rows of each CTA
+@pytest.mark.parametrize("M,H", [(20000, 101), (6000, 1001), (2600, 2997), (1300, 7026), (700, 12001), (340, 20001)])
+@pytest.mark.parametrize("post,gate", [(False, None), (True, "token")])
+def test_many_rows_of_any_alignment(M, H, post, gate):
+    check(operands(M, H, M, post, gate))
+
+
+@pytest.mark.parametrize("M,H", [(5300, 101), (1700, 1001), (900, 2997), (400, 7026), (200, 12001), (160, 20001)])
+@pytest.mark.parametrize("gate", [None, "token"])
+def test_in_place_of_any_alignment(M, H, gate):
+    """Rows that share 16-byte pieces with their neighbours, which other threads and CTAs write meanwhile."""
+    d = operands(M, H, 14, post=gate is not None, gate=gate)
+    want_n, want_r, want_q, want_s = check(d)
+
+    def fresh():
+        a = on(DEV, d)
+        return a, {k: v for k, v in a.items() if k not in ("y", "weight")}
+    for name in ("y", "residual"):
+        a, rest = fresh()
+        n, r = F.fp8_residual_norm(a["y"], a["weight"], residual_out=a[name], **rest)
+        assert r is a[name] and torch.equal(r, want_r) and torch.equal(n, want_n)
+        a, rest = fresh()
+        q, s, r = F.fp8_residual_norm_quantize(a["y"], a["weight"], residual_out=a[name], **rest)
+        assert torch.equal(r, want_r) and torch.equal(q, want_q) and torch.equal(s, want_s)
+        a, rest = fresh()
+        n, r = F.fp8_residual_norm(a["y"], a["weight"], out=a[name], **rest)
+        assert n is a[name] and torch.equal(r, want_r) and torch.equal(n, want_n)
+    a, rest = fresh()  # each over the other's input
+    n, r = F.fp8_residual_norm(a["y"], a["weight"], out=a["y"], residual_out=a["residual"], **rest)
+    assert torch.equal(r, want_r) and torch.equal(n, want_n)
