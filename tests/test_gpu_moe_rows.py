@@ -311,3 +311,31 @@ def test_dispatch_of_many_pairs_with_strides(T, k, H, dtype, shift, out_shift, p
     got, pos2, offsets2 = F.fp8_moe_dispatch(wide_x[:, shift:shift + H], ids.to(DEV), 16, out=out)
     assert got is out and torch.equal(got, want) and torch.equal(pos, pos2) and torch.equal(offsets, offsets2)
     assert (wide[:, :out_shift] == 7.0).all() and (wide[:, out_shift + H:] == 7.0).all()
+
+
+# one and two rows a token where there is work for every SM: a thread has several pieces under way
+@pytest.mark.parametrize("k", [1, 2])
+@pytest.mark.parametrize("dtype,H", [(BF16, 1000), (BF16, 250), (BF16, 1001), (FP32, 500), (FP32, 125)])
+@pytest.mark.parametrize("drop", [0.0, 0.3])
+def test_few_rows_a_token_of_many_tokens(k, dtype, H, drop):
+    """125 pieces of 16 bytes a row (16-bit rows that start anywhere), of 4 bytes (250 16-bit columns, 125 of 32 bits)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    T = sms * 2048 // 125 + 118
+    assert T * 125 % 256 and T * 125 >= sms * 2048
+    ids, w = routing(T, k, 7, H + k, drop)
+    pos = torch.from_numpy(L.sort_rows(ids.numpy(), 7)[0])
+    ys = rows(T * k, H, 22, dtype)
+    out = torch.full((T + 1, H), 7.0, dtype=dtype, device=DEV)
+    for weights in (w, None):
+        F.fp8_moe_combine(ys.to(DEV), pos.to(DEV), None if weights is None else weights.to(DEV), out=out[:T])
+        ref, err = L.combine(f32(ys), pos.numpy(), None if weights is None else weights.numpy())
+        tol = L.rounded_bf16(ref, err) if dtype == BF16 else err
+        assert np.all(np.abs(f32(out[:T]) - ref) <= tol) and (out[T] == 7.0).all()
+    assert torch.equal(F.fp8_moe_dispatch_grad(ys.to(DEV), pos.to(DEV)), out[:T])
+
+
+@pytest.mark.parametrize("k", [1, 2, 3])
+@pytest.mark.parametrize("H", [70, 1000, 2050, 2051, 9001])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_gradient_of_few_rows_a_token(k, H, dtype):
+    check_back(61, k, 5, H, dtype, 0.2, seed=23)
