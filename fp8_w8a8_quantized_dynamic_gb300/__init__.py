@@ -107,6 +107,8 @@ _SIGNATURES = {
     "fp8_selftest_timeout": (_int, [_i64, _vp]),
     "fp8_block_selftest_timeout": (_int, [_int, _vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp,
                                           _i64, _vp]),
+    "fp8_lora_selftest_timeout": (_int, [_int, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp,
+                                         _i64, _vp, _sz, _vp]),
     "fp8_status_string": (ctypes.c_char_p, [_int]),
 }
 
@@ -919,6 +921,16 @@ def fp8_block_selftest_timeout(form: int, qa, K: int, s_a, qw, s_w, out, s_out=N
         form, qa.data_ptr(), qa.shape[0], K, qa.stride(0), s_a.data_ptr(), s_a.stride(0), qw.data_ptr(), qw.shape[-2],
         qw.shape[-1], s_w.data_ptr(), out.data_ptr(), out.stride(0), _ptr(s_out),
         0 if s_out is None else s_out.stride(0), stream))
+
+
+def fp8_lora_selftest_timeout(form: int, y, x, a, b, ids, scales, out, ws, stream=None) -> int:
+    """Enqueue fp8_lora_add with one load withheld from its waits (forms: see the C header); returns the status."""
+    if stream is None:
+        stream = _torch().cuda.current_stream().cuda_stream
+    return int(lib().fp8_lora_selftest_timeout(
+        form, y.data_ptr(), y.shape[0], y.shape[1], y.stride(0), x.data_ptr(), x.shape[1], x.stride(0), a.data_ptr(),
+        b.data_ptr(), a.shape[0], a.shape[1], ids.data_ptr(), _ptr(scales), out.data_ptr(), out.stride(0), ws.data_ptr(),
+        ws.numel(), stream))
 
 
 def fp8_last_device_status(stream=None) -> int:

@@ -207,10 +207,10 @@ FP8_API size_t fp8_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t
   return lora_ws(M, K, N, L, r).total;
 }
 
-FP8_API fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_t ldy, const void* x_bf16, int64_t K,
-                                int64_t ldx, const void* a_bf16, const void* b_bf16, int64_t L, int64_t r,
-                                const int32_t* ids, const float* scales, void* out_bf16, int64_t ldo, void* ws,
-                                size_t ws_bytes, fp8_stream_t stream) {
+static fp8_status lora_call(const void* y_bf16, int64_t M, int64_t N, int64_t ldy, const void* x_bf16, int64_t K,
+                            int64_t ldx, const void* a_bf16, const void* b_bf16, int64_t L, int64_t r, const int32_t* ids,
+                            const float* scales, void* out_bf16, int64_t ldo, void* ws, size_t ws_bytes,
+                            fp8_stream_t stream, lora::Withhold withhold) {
   if (!lora_sizes_ok(M, K, N, L, r)) return FP8_ERR_INVALID_ARG;
   FP8_TRY(check_bf16_mat(y_bf16, M, N, ldy));
   FP8_TRY(check_bf16_mat(x_bf16, M, K, ldx));
@@ -266,5 +266,29 @@ FP8_API fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_
   s.order = order;
   s.v = reinterpret_cast<float*>(base + w.v);
   s.splits = w.splits;
-  return lora::launch_sorted(p, s, sms, st) ? FP8_OK : FP8_ERR_CUDA;
+  return lora::launch_sorted(p, s, sms, st, withhold) ? FP8_OK : FP8_ERR_CUDA;
+}
+
+FP8_API fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_t ldy, const void* x_bf16, int64_t K,
+                                int64_t ldx, const void* a_bf16, const void* b_bf16, int64_t L, int64_t r,
+                                const int32_t* ids, const float* scales, void* out_bf16, int64_t ldo, void* ws,
+                                size_t ws_bytes, fp8_stream_t stream) {
+  return lora_call(y_bf16, M, N, ldy, x_bf16, K, ldx, a_bf16, b_bf16, L, r, ids, scales, out_bf16, ldo, ws, ws_bytes, stream,
+                   lora::Withhold::kNone);
+}
+
+FP8_API fp8_status fp8_lora_selftest_timeout(int form, const void* y_bf16, int64_t M, int64_t N, int64_t ldy,
+                                             const void* x_bf16, int64_t K, int64_t ldx, const void* a_bf16,
+                                             const void* b_bf16, int64_t L, int64_t r, const int32_t* ids,
+                                             const float* scales, void* out_bf16, int64_t ldo, void* ws, size_t ws_bytes,
+                                             fp8_stream_t stream) {
+  if (form < 0 || form > 2 || !lora_sizes_ok(M, K, N, L, r) || M < 1 || K < 1 || N < 1 || L < 1) return FP8_ERR_INVALID_ARG;
+  if (lora_by_token(M, K, N, L, r)) return FP8_ERR_INVALID_ARG;  // a token at a time has nothing to wait for
+  if (form == 0 && (K % 8 != 0 || ldx % 8 != 0 || !aligned(x_bf16, 16) || !aligned(a_bf16, 16))) return FP8_ERR_INVALID_ARG;
+  if (form == 1 && (r > 64 || r % 8 != 0 || N % 8 != 0 || ldy % 8 != 0 || ldo % 8 != 0 || !aligned(b_bf16, 16) ||
+                    !aligned(y_bf16, 16) || !aligned(out_bf16, 16)))
+    return FP8_ERR_INVALID_ARG;
+  if (form == 2 && r > 192) return FP8_ERR_INVALID_ARG;
+  return lora_call(y_bf16, M, N, ldy, x_bf16, K, ldx, a_bf16, b_bf16, L, r, ids, scales, out_bf16, ldo, ws, ws_bytes, stream,
+                   lora::Withhold(form));
 }

@@ -276,6 +276,9 @@ constexpr uint32_t kXBytes = kTileRows * 128;
 constexpr int kShrinkMaxStages = 6;
 constexpr int kShrinkThreads = kTileThreads + 32;
 
+// kWithhold (the failure-path self-test): the first CTA does without one load, so the waits for it run out, after kWithheldNs.
+constexpr unsigned long long kWithheldNs = 20000000ull;
+
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
@@ -457,8 +460,9 @@ __device__ __forceinline__ void tile_end(TileCtl* ctl, uint32_t cols) {
 // Bounds: the first wave's fill and the stream of x (8192 x 4096 at rank 64: 19 us, 3.8 TB/s; the tensor cores are busy for 9
 // percent). A tile of 128 rows is an MMA's; K splits fill the SMs (splits_of).
 // kPiece: the bytes of a copy, as many as all rows of x and A start and end on. 4: a warp copies 128 bytes of a row. 2: whole
-// pieces are loaded and shifted into place.
-template <int kPiece>
+// pieces are loaded and shifted into place. A tile whose wait ran out gets NaN for its rows, so that the second product leaves
+// nothing of an earlier call's v.
+template <int kPiece, bool kWithhold>
 __global__ void __launch_bounds__(kShrinkThreads, 2)
 shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ TileParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -483,7 +487,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
       const uint32_t stage_bytes = kXBytes + uint32_t(p.rp) * 128u;
       auto wait = [&](uint64_t* bars, int step) {
         return mbar_wait_short(smem_u32(bars + step % p.stages), uint32_t(step / p.stages) & 1u, &ctl.abort_flag,
-                               &g_lora_error);
+                               &g_lora_error, kWithhold ? kWithheldNs : kWaitLimitNs);
       };
       bool ok = true;
       int filled = 0;
@@ -536,7 +540,7 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
             if (filled >= p.stages && !(ok = wait(ctl.done, filled - p.stages))) break;
             const uint32_t st = base + uint32_t(filled % p.stages) * stage_bytes;
             const uint32_t bar = smem_u32(&ctl.loaded[filled % p.stages]);
-            if (threadIdx.x == 0) {
+            if (threadIdx.x == 0 && !(kWithhold && blockIdx.x == 0 && blockIdx.y == 0 && filled == steps - 1)) {
               mbar_arrive_expect_tx(bar, uint32_t(p.rp) * 128u);
               tma_load_3d(st + kXBytes, &tmap_a, bar, (kb0 + filled) * 128, 0, t.expert);
             }
@@ -602,9 +606,15 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
                 *reinterpret_cast<uint4*>(dst + (c / 4 + q) * g.M) = make_uint4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
           }
         }
-      } else if (threadIdx.x == 0) {  // nothing of a load may land after the CTA has left
-        for (int i = max(0, filled - p.stages); i < filled; ++i)
-          mbar_wait_bounded(smem_u32(&ctl.loaded[i % p.stages]), uint32_t(i / p.stages) & 1u, nullptr, &g_lora_error);
+      } else {
+        if (int(threadIdx.x) < rows) {
+          const float nan = __uint_as_float(0x7FC00000u);
+          *four_of_v(p, blockIdx.y, 0, t.row0 + threadIdx.x) = make_float4(nan, nan, nan, nan);
+        }
+        if (threadIdx.x == 0)  // nothing of a load may land after the CTA has left
+          for (int i = max(0, filled - p.stages); i < filled; ++i)
+            mbar_wait_bounded(smem_u32(&ctl.loaded[i % p.stages]), uint32_t(i / p.stages) & 1u, nullptr, &g_lora_error,
+                              kWithhold ? kWithheldNs : kWaitLimitNs);
       }
     }
   }
@@ -715,12 +725,13 @@ constexpr int join_threads(int bn) { return bn * 4; }
 constexpr int kBThreads = 128;
 constexpr int expand_threads(int bn, bool tma) { return join_threads(bn) + 32 + kCopyThreads + (tma ? 0 : kBThreads); }
 
-template <int kBn, int kPiece, bool kTma>
+template <int kBn, int kPiece, bool kTma, bool kWithhold>
 __global__ void __launch_bounds__(kBn * 4 + 32 + kCopyThreads + (kTma ? 0 : kBThreads), 1)
 expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant__ TileParams p) {
   constexpr int kJoin = kBn * 4, kJoinWarps = kJoin / 32;
   constexpr int kMostK = kBn == 128 ? 4 : kBn == 64 ? 12 : 16;  // K steps of the ranks that take this width (launch_sorted)
   constexpr uint32_t kPitch = kBn * 2 + 16, kSlotBytes = kTileRows * kPitch;
+  constexpr unsigned long long kLimit = kWithhold ? kWithheldNs : kWaitLimitNs;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TileCtl ctl;
   const uint32_t base = align1024(smem_u32(smem_raw));
@@ -737,11 +748,12 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
   const uint32_t b_bytes = uint32_t(rk) * (kBn * 128u);
   const uint32_t slots_at = b_at + uint32_t(p.b_bufs) * b_bytes;
   auto wait = [&](uint64_t* bar, uint32_t it) {  // the it-th step's phase of a pair of barriers
-    return mbar_wait_short(smem_u32(bar + (it & 1u)), (it >> 1) & 1u, &ctl.abort_flag, &g_lora_error);
+    return mbar_wait_short(smem_u32(bar + (it & 1u)), (it >> 1) & 1u, &ctl.abort_flag, &g_lora_error, kLimit);
   };
   auto wait_at = [&](uint64_t* bars, const Place& a) {
-    return mbar_wait_short(smem_u32(bars + a.i), a.parity, &ctl.abort_flag, &g_lora_error);
+    return mbar_wait_short(smem_u32(bars + a.i), a.parity, &ctl.abort_flag, &g_lora_error, kLimit);
   };
+  auto withheld = [&](const Place& b) { return kWithhold && blockIdx.x == 0 && b.i == 1 && b.parity == 0; };  // the second B
 
   constexpr int kCopyWarps = kCopyThreads / 32;
   if (!kTma && warp > kJoinWarps + kCopyWarps) {
@@ -786,7 +798,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
           }
         }
         fence_async();
-        mbar_arrive(smem_u32(&ctl.loaded[at.i]));
+        if (!withheld(at) || me != 0) mbar_arrive(smem_u32(&ctl.loaded[at.i]));
       }
     }
   } else if (warp > kJoinWarps) {
@@ -904,7 +916,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         continue;
       }
       auto fill = [&](int step) {  // by the issuing warp
-        if (kTma && elect_one()) {
+        if (kTma && !withheld(filled) && elect_one()) {
           const uint32_t bar = smem_u32(&ctl.loaded[filled.i]);
           mbar_arrive_expect_tx(bar, b_bytes);
           for (int i = 0; i < rk; ++i)
@@ -999,7 +1011,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
     }
     if (kTma && !ok && threadIdx.x == kJoin)  // nothing of a load may land after the CTA has left
       for (; used.i != filled.i || used.parity != filled.parity; used.next(p.b_bufs))
-        mbar_wait_bounded(smem_u32(&ctl.loaded[used.i]), used.parity, nullptr, &g_lora_error);
+        mbar_wait_bounded(smem_u32(&ctl.loaded[used.i]), used.parity, nullptr, &g_lora_error, kLimit);
   }
   __syncwarp();
   tile_end(&ctl, p.tmem_cols);
@@ -1038,9 +1050,10 @@ int splits_of(int64_t M, int64_t K, int64_t adapters, int64_t rank) {
   return int(std::max<int64_t>(1, (kb + slice - 1) / std::max<int64_t>(slice, 1)));
 }
 
-template <int kBn, int kPiece, bool kTma>
+template <int kBn, int kPiece, bool kTma, bool kWithhold = false>
 bool launch_expand_of(TileParams p, const CUtensorMap& map_b, int num_sms, cudaStream_t st) {
-  if (!allow_smem(reinterpret_cast<const void*>(expand_kernel<kBn, kPiece, kTma>))) return false;
+  auto kernel = expand_kernel<kBn, kPiece, kTma, kWithhold>;
+  if (!allow_smem(reinterpret_cast<const void*>(kernel))) return false;
   const int rk = (p.rp + kBk - 1) / kBk;
   const size_t v = size_t(rk) * 2 * kXBytes, buf = size_t(rk) * kBn * 128, slot = size_t(kTileRows) * (kBn * 2 + 16);
   const size_t room = 232448 - 1024 - 1024 - v;  // (the control block and the alignment)
@@ -1049,7 +1062,7 @@ bool launch_expand_of(TileParams p, const CUtensorMap& map_b, int num_sms, cudaS
   const int64_t units = p.s.max_tiles * ((p.a.N + kBn - 1) / kBn);
   p.tmem_cols = 32;
   while (int(p.tmem_cols) < 2 * kBn + p.rp / 2) p.tmem_cols *= 2;  // two steps' sums and v's last bits
-  return launch(expand_kernel<kBn, kPiece, kTma>, dim3(unsigned(std::min<int64_t>(units, num_sms))), dim3(expand_threads(kBn, kTma)),
+  return launch(kernel, dim3(unsigned(std::min<int64_t>(units, num_sms))), dim3(expand_threads(kBn, kTma)),
                 1024 + v + size_t(p.b_bufs) * buf + size_t(p.slots) * slot, st, true, dim3(1, 1, 1), map_b, p) == FP8_OK;
 }
 
@@ -1060,7 +1073,7 @@ bool launch_expand(const TileParams& p, int piece, const CUtensorMap& map_b, int
                       : launch_expand_of<kBn, 2, kTma>(p, map_b, num_sms, st);
 }
 
-bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st) {
+bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st, Withhold withhold) {
   TileParams p = {};
   p.a = a;
   p.s = s;
@@ -1070,7 +1083,8 @@ bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st)
   p.vec = aligned(a.x, 16) && (a.M <= 1 || a.ldx % 8 == 0) && aligned(a.a, 16) && a.K % 8 == 0;
   p.vec_b = aligned(a.b, 16) && a.rank % 8 == 0;
   const bool words = aligned(a.x, 4) && (a.M <= 1 || a.ldx % 2 == 0) && aligned(a.a, 4) && a.K % 2 == 0;
-  auto shrink = p.vec ? shrink_kernel<16> : words ? shrink_kernel<4> : shrink_kernel<2>;
+  auto shrink = p.vec ? shrink_kernel<16, false> : words ? shrink_kernel<4, false> : shrink_kernel<2, false>;
+  if (withhold == Withhold::kFirst) shrink = shrink_kernel<16, true>;
   if (!allow_smem(reinterpret_cast<const void*>(shrink))) return false;
   const int stage_bytes = int(kXBytes) + p.rp * 128;
   p.stages = std::max(3, std::min(kShrinkMaxStages, 108 * 1024 / stage_bytes));
@@ -1091,6 +1105,8 @@ bool launch_sorted(const Args& a, const Sorted& s, int num_sms, cudaStream_t st)
            (a.M <= 1 || (a.ldy * 2 % bytes == 0 && a.ldo * 2 % bytes == 0));
   };
   const int piece = on(16) ? 16 : on(4) ? 4 : 2;
+  if (withhold == Withhold::kSecond) return launch_expand_of<128, 16, true, true>(p, map_b, num_sms, st);
+  if (withhold == Withhold::kSecondByWarps) return launch_expand_of<64, 2, false, true>(p, map_b, num_sms, st);
   if (p.vec_b) {
     if (p.rp <= kBk) return launch_expand<128, true>(p, piece, map_b, num_sms, st);
     return p.rp <= 3 * kBk ? launch_expand<64, true>(p, piece, map_b, num_sms, st)

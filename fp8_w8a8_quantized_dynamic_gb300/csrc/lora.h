@@ -43,7 +43,11 @@ struct Sorted {
 };
 int splits_of(int64_t M, int64_t K, int64_t adapters, int64_t rank);
 inline int padded_rank(int64_t rank) { return int((rank + 15) / 16 * 16); }
-bool launch_sorted(const Args& p, const Sorted& s, int num_sms, cudaStream_t st);
+
+// The failure-path self-test: a load withheld from the waits of the first product (rows of x and A on 16-byte boundaries), or of
+// the second, whose B comes by TMA (rows on 16-byte boundaries, rank up to 64) or by warps (rank up to 192).
+enum class Withhold : int { kNone = -1, kFirst, kSecond, kSecondByWarps };
+bool launch_sorted(const Args& p, const Sorted& s, int num_sms, cudaStream_t st, Withhold withhold = Withhold::kNone);
 
 unsigned int read_and_clear_error();
 

@@ -576,6 +576,18 @@ fp8_status fp8_block_selftest_timeout(int form, const uint8_t* qa, int64_t M, in
                                       const float* s_w, void* y, int64_t ldy, float* s_y, int64_t lds_y,
                                       fp8_stream_t stream);
 
+/*
+ * The same for the adapters of many tokens (sizes for which fp8_lora_workspace_bytes is not 0): the call with one load
+ * withheld from the waits of its first CTA. form 0: the first product's last load of A for its first tile (rows of x and
+ * A on 16-byte boundaries): the tile's rows get NaN, all others what the call gives. form 1: the second product's second load of B
+ * (rank a multiple of 8 up to 64, rows of y, out and B on 16-byte boundaries); 2: the same by the warps that load B of odd
+ * ranks (up to 192). All that the CTA had to do from there on keeps what out held; all else is what the call gives.
+ */
+fp8_status fp8_lora_selftest_timeout(int form, const void* y_bf16, int64_t M, int64_t N, int64_t ldy, const void* x_bf16,
+                                     int64_t K, int64_t ldx, const void* a_bf16, const void* b_bf16, int64_t L, int64_t r,
+                                     const int32_t* ids, const float* scales, void* out_bf16, int64_t ldo, void* ws,
+                                     size_t ws_bytes, fp8_stream_t stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 const char* fp8_status_string(fp8_status status);
 

@@ -115,6 +115,15 @@ def test_lora_workspace():
     assert F.fp8_lora_workspace_bytes(2 ** 31 - 256, 2 ** 30, 2 ** 30, 511, 256) > 2 ** 40  # 64-bit sizes
 
 
+def test_lora_selftest_refusals():
+    many = dict(form=1, **{**LORA, "M": 4096, "N": 4096, "ldy": 4096, "K": 4096, "ldx": 4096, "L": 8, "r": 64, "ldo": 4096})
+    for change in (dict(form=3), dict(form=-1), dict(M=0), dict(N=0), dict(K=0), dict(L=0), dict(M=4), dict(r=72), dict(r=60),
+                   dict(N=4092), dict(ldy=4100), dict(ldo=4100), dict(y=P + 8), dict(out=Q + 8), dict(b=P + 8), dict(form=0, x=P + 8),
+                   dict(form=0, a=P + 8), dict(form=0, ldx=4100), dict(form=0, K=4092), dict(form=2, r=193), dict(ids=None)):
+        assert status("fp8_lora_selftest_timeout", {**many, **change}) == F.FP8_ERR_INVALID_ARG, change
+    assert status("fp8_lora_selftest_timeout", {**many, "ws": None}) == F.FP8_ERR_WORKSPACE
+
+
 def test_lora_nothing_to_do():
     assert status("fp8_lora_add", LORA, M=0) == F.FP8_OK
     assert status("fp8_lora_add", LORA, N=0) == F.FP8_OK
