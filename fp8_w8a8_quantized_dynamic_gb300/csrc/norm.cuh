@@ -208,13 +208,16 @@ __device__ __forceinline__ float squares(const Values (&v)[kUnits], float factor
 }
 
 // 1 / sqrt(mean v^2 + eps) of the CTA's row, the root correctly rounded (the fast one, two units off, takes no less time here).
-// Squares of bf16's range may pass fp32's: then once more of v 2^-80.
+// Squares of bf16's range may pass fp32's, and where the mean and eps are below 2^-100 they may lose bits that count: then once
+// more of v 2^-80 (eps is nothing beside them) or v 2^60.
 template <int kThreads, int kUnits>
 __device__ __forceinline__ float inverse_rms(const Values (&v)[kUnits], const Params& p, float (&red)[2][kThreads / 32],
                                              int& turn) {
   const float ss = squares<kThreads, kUnits>(v, 1.0f, red, turn);
-  if (ss <= 0x1.fffffep127f) return __frsqrt_rn(fmaf(ss, p.inv_cols, p.eps));
-  return __frsqrt_rn(squares<kThreads, kUnits>(v, 0x1p-80f, red, turn) * p.inv_cols) * 0x1p-80f;
+  const float mean = fmaf(ss, p.inv_cols, p.eps);
+  if (mean >= 0x1p-100f && ss <= 0x1.fffffep127f) return __frsqrt_rn(mean);
+  const float f = mean < 0x1p-100f ? 0x1p60f : 0x1p-80f, eps = mean < 0x1p-100f ? p.eps * 0x1p120f : 0.0f;
+  return __frsqrt_rn(fmaf(squares<kThreads, kUnits>(v, f, red, turn), p.inv_cols, eps)) * f;
 }
 
 // A thread's raw values of one row.

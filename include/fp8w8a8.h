@@ -476,7 +476,7 @@ fp8_status fp8_lora_add(const void* y_bf16, int64_t M, int64_t N, int64_t ldy, c
  * Writes r and n as bf16 [M, H]; either may be NULL (w NULL with n). r may be y
  * or residual itself (with the same stride), and so may n where r is not; r and n are never the same
  * (FP8_ERR_INVALID_ARG). The mean is over H columns;
- * rows whose squares pass fp32's range are normalised as the formula has it. A
+ * rows whose squares pass fp32's range, at either end, are normalised as the formula has it. A
  * NaN or an infinity in a row makes NaN of what it multiplies in that row and
  * of no other row. eps > 0, scale finite, H <= 32768
  * (FP8_ERR_INVALID_ARG).

@@ -313,3 +313,14 @@ def test_in_place_of_any_alignment(M, H, gate):
     a, rest = fresh()  # each over the other's input
     n, r = F.fp8_residual_norm(a["y"], a["weight"], out=a["y"], residual_out=a["residual"], **rest)
     assert torch.equal(r, want_r) and torch.equal(n, want_n)
+
+
+@pytest.mark.parametrize("H", [300, 1024, 4096, 8192, 20000])
+@pytest.mark.parametrize("eps", [1e-45, 1e-44, 1e-40, 1e-36, 1e-30])
+@pytest.mark.parametrize("post", [False, True])
+def test_squares_below_fp32(H, eps, post):
+    """Rows whose squares are subnormal or vanish in fp32, beside an eps as small; zeros, and a row of ordinary values."""
+    d = operands(7, H, 15, post=post)
+    d["y"] *= torch.tensor([2.0 ** -60, 2.0 ** -73, 2.0 ** -76, 2.0 ** -80, 2.0 ** -100, 0.0, 1.0])[:, None]
+    d["residual"].mul_(d["y"].abs().amax(1, keepdim=True) > 1e-3)
+    check(d, eps=eps)
