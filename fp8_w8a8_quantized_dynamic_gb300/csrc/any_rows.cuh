@@ -60,9 +60,8 @@ __device__ __forceinline__ Raw8 load8_raw(const uint16_t* row, int at, int c, in
 __device__ __forceinline__ uint4 values8(const Raw8& v, int at, int c, int cols) {
   uint4 e = v.a;
   if (at != 0) e = eight_from(v.a, v.b, at);
-  // (by the difference: c + 8 passes 31 bits in rows of almost 2^31 columns, and so may c of a step behind them, where v is zeros)
-  const int left = int(uint32_t(cols) - uint32_t(c));
-  if (left < 8) e = first_of(e, left > 0 ? left : 0);
+  // (c + 8 passes 31 bits in rows of almost 2^31 columns; c itself may behind a row, where v is zeros)
+  if (c > cols - 8) e = first_of(e, cols > c ? cols - c : 0);
   return e;
 }
 

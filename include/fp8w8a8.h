@@ -444,7 +444,7 @@ fp8_status fp8_moe_dispatch_grad(const void* dxs, int f32, int64_t R, int64_t H,
  * and out[m] = y[m] for any other id. y bf16 [M, N] is the output of a linear
  * of x bf16 [M, K] (any of the linears here), A bf16 [L][r, K], B bf16
  * [L][N, r], without gaps; ids int32 [M], scales fp32 [L] (NULL: ones). Sums and
- * A x are fp32, in every form (tensor cores take A x as the sum of three bf16 numbers);
+ * A x are fp32, in every form (tensor cores take A x as the sum of three bf16 numbers, all of its bits down to 2^-133);
  * the only rounding to bf16 is that of out. Results do not depend
  * on timing. A NaN or an infinity, in B too, gives what the formula gives in
  * fp32, and stays with the tokens of its row or adapter. out may be y (with the same stride), else may not overlap it, nor
