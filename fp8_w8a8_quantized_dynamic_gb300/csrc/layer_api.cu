@@ -123,10 +123,12 @@ bool lora_sizes_ok(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
 
 // A cluster a token, or rows sorted by adapter: by the estimated time in us. A token takes 0.06 and its adapter's w MB at
 // 8.5 MB/us; the sorted form 16 and its adapters (between one and min(L, M): half) at 2.2. Measured, by token and sorted
-// (tokens of 32 adapters drawn at random; of one): K 4096 N 4096 r 64, 64 tokens 11 and 32; 18, 128 tokens 20 and 33; 23, 256
-// tokens 37 and 32; 23. r 16: 128 tokens 10 and 29; 17, 256 tokens 18 and 30; 17. N 14336 r 64: 64 tokens 22 and 49; 18, 128
-// tokens 41 and 58; 23. K 8192 N 8192 r 128: 64 tokens 39 and 71; 26, 128 tokens 71 and 76; 34. Rows that start off 16-byte
-// boundaries take both longer: K 4098 N 4096 r 64: 64 tokens 20 and 45; 26, K 6014 N 1280 r 105: 64 tokens 35 and 42; 27.
+// (tokens of 32 adapters drawn at random; of one): K 4096 N 4096 r 64, 64 tokens 10 and 25; 17, 128 tokens 18 and 27; 18, 256
+// tokens 33 and 27; 19. r 16: 128 tokens 9 and 29; 17, 256 tokens 17 and 29; 17. N 14336 r 64: 64 tokens 22 and 44; 18, 128
+// tokens 38 and 46; 19. K 8192 N 8192 r 128: 64 tokens 35 and 54; 27, 128 tokens 65 and 60; 27. Rows that start off 16-byte
+// boundaries take both longer: K 4098 N 4096 r 64: 64 tokens 22 and 28; 20, K 6014 N 1280 r 105: 64 tokens 36 and 35; 33.
+// (By sizes alone, since they decide on the workspace, which is asked for before there is an address: views of whole rows
+// that start off a boundary go by the rule of those on one.)
 bool lora_by_token(int64_t M, int64_t K, int64_t N, int64_t L, int64_t r) {
   const double w = 2e-6 * double(r) * double(K + N);
   const double sorted = 16.0 + double(std::min(L, M)) * w / 4.4;

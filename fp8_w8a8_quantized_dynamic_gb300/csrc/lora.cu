@@ -624,22 +624,38 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
 // v of a tile's rows, the sum of the splits in order, as the sum of three bf16 numbers: eight bits each, so that nothing of v's 24
 // is lost (above 2^-133, the smallest bf16 number). The first two go to swizzled tiles of shared memory, the third to tensor memory
 // (as the operand of the same MMAs: three tiles of rank 256 leave no room for B and y, and at rank 64 one would cost a slot of y).
-// A thread has a row; `groups` of four warps share out the pieces of eight values.
+// `groups` of four warps share out the pieces of eight values; in a warp with few rows several lanes share a row's. (Where each
+// lane passed all of its row's pieces, one after the other, 64 tokens of 32 adapters took 67 us at K = N = 8192 and rank 128, 54 so.)
+// kSteps: addresses by steps from the first, for kernels of 72 registers (8192 x 14336 at rank 64: 120 us, 131 otherwise); else each
+// by itself, so that no load waits for another's address (2048 x 4096 at rank 128: 46 us against 49).
+template <bool kSteps>
 __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile& t, int rows, uint32_t v_hi, uint32_t v_mid,
                                       uint32_t v_lo_tmem, int groups) {
-  const int64_t M = p.a.M;
-  const int row = int(threadIdx.x) & (kTileRows - 1);
-  for (int c = int(threadIdx.x) / kTileRows; c < p.rp / 8; c += groups) {
+  const int lane = threadIdx.x & 31, quarter = int(threadIdx.x >> 5) & 3, group = int(threadIdx.x) / kTileRows;
+  const int live = min(32, rows - quarter * 32);  // rows of this warp's 32 places
+  if (live <= 0) return;  // (what lies in places without a row reaches no other row's sums)
+  const int mine = (p.rp / 8 - group + groups - 1) / groups;  // pieces of this group
+  const int shift = live > 1 ? __clz(live - 1) - 27 : 5, share = 1 << shift;  // lanes of a row
+  const int at = lane >> shift;
+  const int64_t M = p.a.M, split = p.rp / 4 * M;
+  const int64_t row = t.row0 + quarter * 32 + at;
+  const float4* from = four_of_v(p, 0, 2 * (group + (lane & (share - 1)) * groups), row);
+  const uint32_t to_row = uint32_t(quarter * 32 + at) * 128u;
+  const uint32_t to_tmem = v_lo_tmem + (uint32_t(quarter * 32) << 16);
+  for (int k0 = 0; k0 < mine; k0 += share, from += int64_t(2 * share * groups) * M) {
+    const int k = k0 + (lane & (share - 1)), c = group + k * groups;
+    const bool have = at < live && k < mine;
     float f[8] = {};
-    if (row < rows) {
-      for (int s0 = 0; s0 < p.s.splits; s0 += 4) {  // four splits' loads at once, added in order
+    if (have) {
+      const float4* next = from;
+      for (int s0 = 0; s0 < p.s.splits; s0 += 4, next += 4 * split) {  // four splits' loads at once, added in order
         float4 in[4][2];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-          const float4* at = four_of_v(p, s0 + s, 2 * c, t.row0 + row);
-          const bool have = s0 + s < p.s.splits;
-          in[s][0] = have ? at[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-          in[s][1] = have ? at[M] : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4* four = kSteps ? next + s * split : four_of_v(p, s0 + s, 2 * c, row);
+          const bool more = s0 + s < p.s.splits;
+          in[s][0] = more ? four[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+          in[s][1] = more ? four[M] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -648,26 +664,32 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
         }
       }
     }
-    // the next eight bits of each, and what they leave (an infinity leaves nothing; what the formula has of it is seen to where the
-    // sums are read, as in sums_again)
-    auto next8 = [&](uint32_t (&w)[4]) {
+    // the next eight bits of each, and what they leave (where that is infinite or NaN the sums are, and are taken again)
+    uint32_t w[4];
+    auto next8 = [&]() {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        w[j] = pack_bf16x2(f[2 * j], f[2 * j + 1]);
-        const float a = bf16_lo(w[j]), b = bf16_hi(w[j]);
-        f[2 * j] = fabsf(a) <= FLT_MAX ? f[2 * j] - a : 0.0f;
-        f[2 * j + 1] = fabsf(b) <= FLT_MAX ? f[2 * j + 1] - b : 0.0f;
+        w[j] = cvt_bf16x2(f[2 * j], f[2 * j + 1]);
+        f[2 * j] -= bf16_lo(w[j]);
+        f[2 * j + 1] -= bf16_hi(w[j]);
       }
     };
-    uint32_t w[4];
-    const uint32_t at = uint32_t(c >> 3) * kXBytes + swizzled(row, c & 7);
-    next8(w);
-    sts128(v_hi + at, make_uint4(w[0], w[1], w[2], w[3]));
-    next8(w);
-    sts128(v_mid + at, make_uint4(w[0], w[1], w[2], w[3]));
-    next8(w);
-    __syncwarp();
-    tmem_st4(v_lo_tmem + (uint32_t(row & ~31) << 16) + uint32_t(c) * 4u, w);
+    const uint32_t to = uint32_t(c >> 3) * kXBytes + to_row + uint32_t(((c & 7) ^ (at & 7)) << 4);
+    next8();
+    if (have) sts128(v_hi + to, make_uint4(w[0], w[1], w[2], w[3]));
+    next8();
+    if (have) sts128(v_mid + to, make_uint4(w[0], w[1], w[2], w[3]));
+    next8();
+    if (share == 1) {
+      tmem_st4(to_tmem + uint32_t(c) * 4u, w);
+      continue;
+    }
+    for (int j = 0; j < share && k0 + j < mine; ++j) {  // a row's third parts to the lane of its place
+      uint32_t l[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[i] = __shfl_sync(0xffffffffu, w[i], (lane << shift) + j);
+      tmem_st4(to_tmem + uint32_t(group + (k0 + j) * groups) * 4u, l);
+    }
   }
   tmem_wait_st();
 }
@@ -932,7 +954,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         for (int i = 0; ok && i < p.b_bufs - 1 && s0 + i < s1; ++i) fill(s0 + i);
       } else {
         // all of the last tile's MMAs are done: each warp waited for its last step
-        put_v(p, t, rows, v_hi, v_mid, v_lo_tmem, kJoin / kTileRows);
+        put_v<kBn == 128>(p, t, rows, v_hi, v_mid, v_lo_tmem, kJoin / kTileRows);
         fence_async();
         tmem_fence_before();
       }
@@ -1040,11 +1062,13 @@ bool allow_smem(const void* kfn) {
 
 // K splits of the first product: CTAs for the SMs, each with at least four blocks of K (two where rows are shifted into place),
 // and no more than pay for themselves: a block takes 0.65 us (where rows start anywhere 1.5 to 2.2), and each split of a tile's
-// sums about 0.01 us a rank to read in the second product.
+// sums about 0.01 us a rank to read in the second product. It goes by sizes alone, and by a GB300's 152 SMs: the
+// workspace, which holds the splits, is asked for before there is an address or a device.
+constexpr int kSms = 152;
 int splits_of(int64_t M, int64_t K, int64_t adapters, int64_t rank) {
   const int64_t tiles = (M + kTileRows - 1) / kTileRows + std::min(M, adapters) / 2;
   const int64_t kb = (K + kBk - 1) / kBk;
-  int64_t want = std::max<int64_t>(1, std::min<int64_t>(K % 8 == 0 ? kb / 4 : kb / 2, 2 * 152 / tiles));
+  int64_t want = std::max<int64_t>(1, std::min<int64_t>(K % 8 == 0 ? kb / 4 : kb / 2, 2 * kSms / tiles));
   while (want > 1 && want * want * padded_rank(rank) > (K % 8 == 0 ? 65 : 150) * kb) --want;
   const int64_t slice = (kb + want - 1) / want;
   return int(std::max<int64_t>(1, (kb + slice - 1) / std::max<int64_t>(slice, 1)));
