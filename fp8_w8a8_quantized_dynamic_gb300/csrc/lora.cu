@@ -393,7 +393,7 @@ struct TileParams {
 };
 
 // v between the two kernels: four values at a time of each row, [split][rank / 4][row], so that 32 lanes with a row each pass whole
-// lines (with a row's values side by side the second product's kernel took 11 us more for 8192 x 14336 at rank 64).
+// lines (with a row's values side by side 8192 x 14336 at rank 64 took 134 us against 124, then).
 __device__ __forceinline__ float4* four_of_v(const TileParams& p, int split, int four, int64_t row) {
   return reinterpret_cast<float4*>(p.s.v) + (int64_t(split) * (p.rp / 4) + four) * p.a.M + row;
 }
@@ -457,7 +457,7 @@ __device__ __forceinline__ void tile_end(TileCtl* ctl, uint32_t cols) {
 // tokens: eight threads a 128-byte piece of a row, asynchronous 16-byte copies) and, by TMA, A's into a ring of stages, whose
 // barrier counts the copies' completion; warp 8 issues the MMAs. (With a fence for the tensor core in the copying
 // threads, which waits for their copies in flight, a step took a load's latency: 27 us for 8192 x 4096 at rank 64.)
-// Bounds: the first wave's fill and the stream of x (8192 x 4096 at rank 64: 19 us, 3.8 TB/s; the tensor cores are busy for 9
+// Bounds: the first wave's fill and the stream of x (8192 x 4096 at rank 64: 19 us, 3.9 TB/s; the tensor cores are busy for 10
 // percent). A tile of 128 rows is an MMA's; K splits fill the SMs (splits_of).
 // kPiece: the bytes of a copy, as many as all rows of x and A start and end on. 4: a warp copies 128 bytes of a row. 2: whole
 // pieces are loaded and shifted into place. A tile whose wait ran out gets NaN for its rows, so that the second product leaves
@@ -740,7 +740,7 @@ __device__ __forceinline__ void sums_again(const TileParams& p, uint32_t taddr, 
 // What was measured for 8192 x 14336: rows loaded and stored by the joining threads, 32 bytes of a row at a time, 111 us
 // (each asks the L2 for a single sector); a bulk copy of 256 bytes a row each way 470 us (some 60 cycles a copy).
 // Slot rows lie 16 bytes further apart than they are long, so that eight lanes' accesses down the rows take all banks.
-// Bounds: the stream of y in and out (8192 x 14336 at rank 64 in 16 adapters: 94 us, 5.1 TB/s; the tensor cores are busy for 14
+// Bounds: the stream of y in and out (8192 x 14336 at rank 64 in 16 adapters: 97 us, 4.8 TB/s; the tensor cores are busy for 21
 // percent of it); one CTA an SM, whose copying warps are its loads in flight (two CTAs of 64 columns: 138 us for the call
 // against 128, then).
 constexpr int join_threads(int bn) { return bn * 4; }
