@@ -347,6 +347,13 @@ __device__ __forceinline__ bool barrier_all(int id, int threads, bool ok) {
   return r != 0;
 }
 
+// The larger; NaN if either is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Two fp32 to bf16, the first in the low half.
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   uint32_t d;
@@ -628,9 +635,10 @@ shrink_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant_
 // lane passed all of its row's pieces, one after the other, 64 tokens of 32 adapters took 67 us at K = N = 8192 and rank 128, 54 so.)
 // kSteps: addresses by steps from the first, for kernels of 72 registers (8192 x 14336 at rank 64: 120 us, 131 otherwise); else each
 // by itself, so that no load waits for another's address (2048 x 4096 at rank 128: 46 us against 49).
+// nan_row gets `tag` for the rows with a NaN.
 template <bool kSteps>
 __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile& t, int rows, uint32_t v_hi, uint32_t v_mid,
-                                      uint32_t v_lo_tmem, int groups) {
+                                      uint32_t v_lo_tmem, int groups, int* nan_row, int tag) {
   const int lane = threadIdx.x & 31, quarter = int(threadIdx.x >> 5) & 3, group = int(threadIdx.x) / kTileRows;
   const int live = min(32, rows - quarter * 32);  // rows of this warp's 32 places
   if (live <= 0) return;  // (what lies in places without a row reaches no other row's sums)
@@ -664,6 +672,14 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
         }
       }
     }
+    if (c * 8 + 8 > p.a.rank) {  // (behind the rank an infinity of x times zero is NaN)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = c * 8 + i < p.a.rank ? f[i] : 0.0f;
+    }
+    float most = f[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) most = max_or_nan(most, f[i]);
+    if (most != most) nan_row[quarter * 32 + at] = tag;  // (more than one lane may say so)
     // the next eight bits of each, and what they leave (where that is infinite or NaN the sums are, and are taken again)
     uint32_t w[4];
     auto next8 = [&]() {
@@ -694,7 +710,7 @@ __device__ __forceinline__ void put_v(const TileParams& p, const block::RowTile&
   tmem_wait_st();
 }
 
-// Whether any of a thread's sums is not finite.
+// Whether any of a thread's sums is not finite, and which.
 __device__ __forceinline__ bool any_not_finite(const uint32_t (&f)[32]) {
   uint64_t z[2] = {0, 0};
 #pragma unroll
@@ -702,29 +718,74 @@ __device__ __forceinline__ bool any_not_finite(const uint32_t (&f)[32]) {
     z[i & 1] = fma_f32x2(pack_f32x2(__uint_as_float(f[2 * i]), __uint_as_float(f[2 * i + 1])), 0, z[i & 1]);
   return !(lo_of(z[0]) + hi_of(z[0]) + lo_of(z[1]) + hi_of(z[1]) == 0.0f);
 }
+__device__ __forceinline__ uint32_t not_finite(const uint32_t (&f)[32]) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) bad |= fabsf(__uint_as_float(f[i])) <= FLT_MAX ? 0u : 1u << i;
+  return bad;
+}
+
+// One sum in fp32, from v's splits as put_v adds them and a row of B; a NaN ends it.
+__device__ __forceinline__ float sum_again(const TileParams& p, int64_t row, const uint16_t* b) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int j = 0; j < p.a.rank && sum == sum; j += 4) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int s = 0; s < p.s.splits; ++s) {
+      const float4 in = *four_of_v(p, s, j >> 2, row);
+      v.x += in.x, v.y += in.y, v.z += in.z, v.w += in.w;
+    }
+    const int n = p.a.rank - j;
+    sum = fmaf(bf16_bits_to_float(b[j]), v.x, sum);
+    if (n > 1) sum = fmaf(bf16_bits_to_float(b[j + 1]), v.y, sum);
+    if (n > 2) sum = fmaf(bf16_bits_to_float(b[j + 2]), v.z, sum);
+    if (n > 3) sum = fmaf(bf16_bits_to_float(b[j + 3]), v.w, sum);
+  }
+  return sum;
+}
 
 // The parts of v lose what the formula has where a number is not finite: an infinity of B times a part that is 0 or of the other
-// sign, or a v that rounds to an infinite bf16 number. Such sums of a warp's rows and columns are taken once more, from v and B
-// themselves in fp32, and put in their places in tensor memory. `row`: this lane's row of v, `b`: the first column's of B.
-__device__ __forceinline__ void sums_again(const TileParams& p, uint32_t taddr, int64_t row, const uint16_t* b, int columns,
-                                           bool live) {
+// sign, or a v that rounds to an infinite bf16 number. Such sums of a warp's rows and columns (`bad`: this lane's row's) are
+// taken once more, from v and B themselves, and put in their places in tensor memory: a lane a column where the rows are far fewer
+// (a token's infinity), else a lane a row (an infinity in B). What is NaN all the same is left: rows with a NaN in v are not
+// among `bad`, and a column whose B starts with a NaN is passed over. `row0`: the warp's first row of v, `b`: the first column's of
+// B. (2048 tokens of four adapters, 4096 to 8192 at rank 64: 36 us when all is finite and with NaN tokens or adapters, 66 with an
+// infinite token, 52 with an infinite value in B, 1.2 ms with an adapter whose B is infinite throughout.)
+__device__ __forceinline__ void sums_again(const TileParams& p, uint32_t taddr, uint32_t bad, int64_t row0, const uint16_t* b) {
+  const int lane = threadIdx.x & 31, rank = p.a.rank;
+  uint32_t columns = __reduce_or_sync(0xffffffffu, bad);
+  const float first = (columns >> lane) & 1u ? bf16_bits_to_float(b[lane * rank]) : 0.0f;
+  columns &= ~__ballot_sync(0xffffffffu, first != first);
+  bad &= columns;
+  const uint32_t rows = __ballot_sync(0xffffffffu, bad != 0);
+  if (__popc(rows) * 4 <= __popc(columns)) {
 #pragma unroll 1
-  for (int i = 0; i < columns; ++i, b += p.a.rank) {
-    float sum = __uint_as_float(tmem_ld1(taddr + i));
-    if (live && !(fabsf(sum) <= FLT_MAX)) {
-      sum = 0.0f;
+    for (uint32_t left = rows; left != 0; left &= left - 1) {
+      const int r = __ffs(left) - 1;
+      const uint32_t of_row = __shfl_sync(0xffffffffu, bad, r);
+      const float sum = (of_row >> lane) & 1u ? sum_again(p, row0 + r, b + lane * rank) : 0.0f;
+      __syncwarp();
 #pragma unroll 1
-      for (int j = 0; j < p.a.rank && sum == sum; ++j) {
-        float vj = 0.0f;
-#pragma unroll 1
-        for (int s = 0; s < p.s.splits; ++s) vj += reinterpret_cast<const float*>(four_of_v(p, s, j >> 2, row))[j & 3];
-        sum = fmaf(bf16_bits_to_float(b[j]), vj, sum);
+      for (uint32_t c = of_row; c != 0; c &= c - 1) {
+        const int column = __ffs(c) - 1;
+        const float mine = __shfl_sync(0xffffffffu, sum, column);
+        const uint32_t was = tmem_ld1(taddr + column);
+        tmem_st1(taddr + column, lane == r ? __float_as_uint(mine) : was);
+        tmem_wait_st();
       }
     }
-    __syncwarp();
-    tmem_st1(taddr + i, __float_as_uint(sum));
+  } else {
+#pragma unroll 1
+    for (uint32_t c = columns; c != 0; c &= c - 1) {
+      const int column = __ffs(c) - 1;
+      uint32_t sum = tmem_ld1(taddr + column);
+      if ((bad >> column) & 1u) sum = __float_as_uint(sum_again(p, row0 + lane, b + column * rank));
+      __syncwarp();
+      tmem_st1(taddr + column, sum);
+    }
+    tmem_wait_st();
   }
-  tmem_wait_st();
 }
 
 // out = y + s B[e] v. The CTAs share out
@@ -756,8 +817,10 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
   constexpr unsigned long long kLimit = kWithhold ? kWithheldNs : kWaitLimitNs;
   extern __shared__ uint8_t smem_raw[];
   __shared__ TileCtl ctl;
+  __shared__ int nan_row[kTileRows];  // the tile, plus one, whose row there has a NaN in v
   const uint32_t base = align1024(smem_u32(smem_raw));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < kTileRows) nan_row[threadIdx.x] = 0;
   tile_begin(&ctl, p.tmem_cols, kTma ? 1 : kBThreads, kJoinWarps);
   const Args& g = p.a;
   const int N = int(g.N);
@@ -954,7 +1017,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         for (int i = 0; ok && i < p.b_bufs - 1 && s0 + i < s1; ++i) fill(s0 + i);
       } else {
         // all of the last tile's MMAs are done: each warp waited for its last step
-        put_v<kBn == 128>(p, t, rows, v_hi, v_mid, v_lo_tmem, kJoin / kTileRows);
+        put_v<kBn == 128>(p, t, rows, v_hi, v_mid, v_lo_tmem, kJoin / kTileRows, nan_row, tile + 1);
         fence_async();
         tmem_fence_before();
       }
@@ -999,6 +1062,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
       }
       const int row = (warp & 3) * 32 + lane, group = warp >> 2;  // columns [32 group, 32 group + 32)
       const float scale = g.scales ? g.scales[t.expert] : 1.0f;
+      const bool watched = row < rows && nan_row[row] != tile + 1;  // (all sums of a row with a NaN are NaN)
       for (int s = s0; s < s1; ++s, ++it, slot.next(p.slots)) {
         ok = ok && wait(ctl.done, it);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -1006,9 +1070,11 @@ expand_kernel(const __grid_constant__ CUtensorMap tmap_b, const __grid_constant_
         uint32_t f[32];
         const uint32_t sums = ctl.tmem_base + (it & 1u) * kBn + (uint32_t((warp & 3) * 32) << 16) + group * 32;
         tmem_ld32(sums, f);
-        if (__any_sync(0xffffffffu, row < rows && any_not_finite(f))) {
-          const int n = s * kBn + group * 32;
-          sums_again(p, sums, t.row0 + row, g.b + (int64_t(t.expert) * N + n) * g.rank, min(32, N - n), row < rows);
+        if (__any_sync(0xffffffffu, watched && any_not_finite(f))) {
+          const int n = s * kBn + group * 32;  // columns past the last are no one's
+          const uint32_t mask = N - n >= 32 ? ~0u : N > n ? (1u << (N - n)) - 1u : 0u;
+          sums_again(p, sums, watched ? not_finite(f) & mask : 0u, t.row0 + (warp & 3) * 32,
+                     g.b + (int64_t(t.expert) * N + n) * g.rank);
           tmem_ld32(sums, f);
         }
         tmem_fence_before();

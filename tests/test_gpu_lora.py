@@ -309,3 +309,23 @@ def test_all_bits_of_a_x_count(M, r):
         d["a"][0, at, :3], d["a"][0, at + 1, :2] = 1.0, 1.0
         d["b"][0, :, at], d["b"][0, :, at + 1] = 1.0, -1.0
         assert (run(d) == 2.0 ** -bit).all()
+
+
+@pytest.mark.parametrize("M", [8, 560, 1100])
+@pytest.mark.parametrize("r", [7, 12, 16, 130, 256])
+def test_tokens_and_adapters_that_are_not_finite(M, r):
+    """Single infinite tokens, NaN late in a row of B, rows of B and a whole B that are infinite, NaN tokens beside them."""
+    inf, nan = float("inf"), float("nan")
+    d = operands(M, 128, 150, r, 5, 6, torch.arange(M, dtype=torch.int32) % 6 - 1)
+    clean = run(d).cpu().double().numpy()
+    d["x"][1, 5], d["x"][2, 3] = inf, -inf      # adapters 0 and 1
+    d["x"][M - 1, 0] = nan
+    d["b"][0, 11, r - 1], d["b"][0, 149, 0] = nan, nan
+    d["b"][1, 33], d["b"][1, 34, r - 1] = inf, -inf
+    d["b"][2] = inf
+    d["b"][3, ::2] = nan
+    out, want = run(d).cpu().double().numpy(), formula(d)
+    odd = ~np.isfinite(want)
+    assert np.array_equal(np.isnan(out), np.isnan(want))
+    assert np.array_equal(out[odd & ~np.isnan(want)], want[odd & ~np.isnan(want)])
+    assert np.array_equal(out[~odd], clean[~odd])
