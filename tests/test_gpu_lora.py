@@ -329,3 +329,14 @@ def test_tokens_and_adapters_that_are_not_finite(M, r):
     assert np.array_equal(np.isnan(out), np.isnan(want))
     assert np.array_equal(out[odd & ~np.isnan(want)], want[odd & ~np.isnan(want)])
     assert np.array_equal(out[~odd], clean[~odd])
+
+
+@pytest.mark.parametrize("r", [3, 8, 16, 40, 64, 128, 200, 256])
+@pytest.mark.parametrize("lengths", [[1, 2, 3, 4, 5, 7, 8, 9], [15, 16, 17, 31, 32, 33], [63, 64, 65, 97]])
+@pytest.mark.parametrize("K", [72, 8192])
+def test_tiles_of_few_rows(K, r, lengths):
+    """Rows that several lanes share, in one and in several quarters of a tile, over one and over many splits of K."""
+    runs = [n for _ in range(-(-530 // sum(lengths))) for n in lengths]
+    ids = torch.cat([torch.full((n,), i % 41, dtype=torch.int32) for i, n in enumerate(runs)])
+    order = torch.randperm(ids.numel(), generator=torch.Generator().manual_seed(r))
+    check(operands(ids.numel(), K, 140, r, 41, r, ids[order].contiguous()))
